@@ -19,6 +19,17 @@
  *   FP8 pools add per-layer scale arrays k_scale[], v_scale[]: one float32 per
  *   physical block (shared by all heads), capacity rounded up to a multiple of 4
  *   floats, 16-byte aligned.  Stored value = e4m3 code * scale.
+ *   KV_INT4 pools hold 4-bit codes and their own scales, 9/16 byte per element: K, V are
+ *   [num_blocks][num_heads][block_size/8][4*d + d/2] bytes, per 8 tokens the codes, then one
+ *   scale byte per token and 16 elements (no scale arrays; the caller sets nothing).
+ *     value = (nibble - 8) * scale; a scale byte is an unsigned float of 5 exponent and 3
+ *     mantissa bits with float16's bias ((byte << 7) is the scale as float16).
+ *     K: codes [token][d/2] (low nibble: the even element), scales [token][d/16].
+ *     V: codes as 16-bit pieces of 4 elements of one token (element i at bits 4i),
+ *        [chunk of d/8 elements][token/2][d/32][token%2]; scales [d/16][token].
+ *   Stored from x, per token, head and 16 elements: scale = min(amax/7, 896) rounded to
+ *   nearest even on the scale's grid, code = x/scale rounded to nearest even, within -7 .. 7
+ *   (scale 0: code 0).  Values beyond 6272 saturate; a group holding a NaN reads as NaN.
  */
 #ifndef KVPAGED_H
 #define KVPAGED_H
@@ -50,7 +61,7 @@ typedef enum {
     KV_ERR_UNSUPPORTED = -6   /* valid request this library version does not implement  */
 } kv_status;
 
-typedef enum { KV_F32 = 0, KV_F16 = 1, KV_FP8_E4M3 = 2 } kv_dtype;
+typedef enum { KV_F32 = 0, KV_F16 = 1, KV_FP8_E4M3 = 2, KV_INT4 = 3 } kv_dtype;
 
 /* Device-side error bits (kv_get_device_error).  Kernels never trap: they set a
  * bit, skip or clamp the offending access, and finish. */
@@ -59,7 +70,8 @@ enum {
     KV_DEVERR_BLOCK_ID = 2,    /* block table / copy pair id outside [0, num_blocks)    */
     KV_DEVERR_CONTEXT = 4,     /* context_len < 0, > max_blocks*block_size or > max_context */
     KV_DEVERR_TIMEOUT = 8,     /* a bounded mbarrier wait ran out (about one second)    */
-    KV_DEVERR_PREFIX = 16      /* a prefix group broke its rules (attended without sharing) */
+    KV_DEVERR_PREFIX = 16,     /* a prefix group broke its rules (attended without sharing) */
+    KV_DEVERR_POSITION = 32    /* kv_append_rope: a position outside the table               */
 };
 
 typedef struct {
@@ -147,6 +159,7 @@ KV_API int kv_selftest_wait_timeout(kv_pool* pool, uint64_t limit_ns, kv_stream_
  *                  e4m3 = round-nearest-even-satfinite(fp32(x) / scale[block]), where
  *                  scale[block] is the value already in the layer's scale array
  *                  (the caller sets a fresh block's scale before appending into it).
+ *                  A 4-bit pool takes F16 or F32 input and scales each 16 elements itself.
  *   slot_mapping   device int64 [num_tokens]; slot < 0 means "skip this token".
  * Token i, head h lands at block slot/B, offset slot%B.  Out-of-range slots set
  * KV_DEVERR_SLOT and are skipped.  Bit-exact copy for F32/F16.
@@ -154,6 +167,83 @@ KV_API int kv_selftest_wait_timeout(kv_pool* pool, uint64_t limit_ns, kv_stream_
  * write_KV_to_block of [PagedAttention] §3.3. */
 KV_API int kv_append(kv_pool* pool, int layer, const void* k, const void* v, kv_dtype in_dtype,
               const int64_t* slot_mapping, int num_tokens, kv_stream_t stream);
+
+/* Rotate new queries and keys by their positions and write keys and values into their slots,
+ * in one launch: the rotary position embedding of the projections, then kv_append.  For every
+ * token i with slot_mapping[i] >= 0, with (x, y) the pairs of the first rot_dim elements of a
+ * head and c, s the cosine and sine of the pair at positions[i]:
+ *     x' = x c - y s,   y' = y c + x s     (float32; elements from rot_dim on are unchanged)
+ * for every query head (into q_out) and key head; keys and values are then stored as kv_append
+ * stores them (F32 bit for bit, F16 rounded once from float32, FP8 and 4-bit codes quantised
+ * from the float32 value; values are not rotated).
+ *   layer          0 .. num_layers-1.
+ *   q, num_q_heads device [num_tokens] rows of num_q_heads*head_dim in_dtype elements; NULL:
+ *                  keys and values only (q_out ignored).  num_q_heads 1 .. 2048.
+ *   q_out          the rotated queries: float32 for F32 pools, else float16 (the type decode
+ *                  attention takes).  May be q itself when type and stride are the same.
+ *   k, v           device [num_tokens] rows of num_heads*head_dim elements.
+ *   in_dtype       element type of q, k and v; rules as kv_append.
+ *   q_stride, k_stride, v_stride, q_out_stride  elements between the rows of two tokens (heads
+ *                  are contiguous in a row), so q, k and v may be views of one packed
+ *                  projection; at least a row, and a multiple of 16 bytes.
+ *   slot_mapping   device int64 [num_tokens].  slot < 0: a padding token, of which nothing is
+ *                  read but its slot and nothing written, q_out included.  A slot outside the
+ *                  pool sets KV_DEVERR_SLOT and the token is skipped the same way.  The slots
+ *                  of a call must be distinct.
+ *   positions      device int32 [num_tokens], 0 .. table_len-1; others set KV_DEVERR_POSITION
+ *                  and the token is skipped.
+ *   cos_sin        device float32 [table_len][rot_dim], 16-byte aligned: each position's
+ *                  rot_dim/2 cosines, then its rot_dim/2 sines (kv_rope_table, or the caller's
+ *                  own for another frequency scheme).
+ *   rot_dim        a multiple of 16, 16 .. head_dim.
+ *   adjacent_pairs 0: pair i is elements (i, i + rot_dim/2); 1: elements (2i, 2i + 1).
+ *   num_tokens     >= 0 (0: nothing is done).
+ *   flags          0, or KV_DECODE_PDL: may be scheduled while the previous kernel on the stream
+ *                  finishes; reads and writes nothing before that kernel has completed.
+ * q, k and v 16-byte aligned.  The pool's device must be the current device.  Asynchronous.
+ * The rotation the pages apply before the cache write: [KV Cache篇] §3.1 (apply_rotary_emb on
+ * xq and xk, then cache_k[:, start_pos] = xk). */
+typedef struct {
+    int layer;
+    const void* q;
+    int num_q_heads;
+    void* q_out;
+    const void* k;
+    const void* v;
+    kv_dtype in_dtype;
+    int64_t q_stride;
+    int64_t k_stride;
+    int64_t v_stride;
+    int64_t q_out_stride;
+    const int64_t* slot_mapping;
+    const int32_t* positions;
+    const float* cos_sin;
+    int table_len;
+    int rot_dim;
+    int adjacent_pairs;
+    int num_tokens;
+    unsigned flags;
+    kv_stream_t stream;
+} kv_rope_args;
+KV_API int kv_append_rope(kv_pool* pool, const kv_rope_args* args);
+
+/* Fill a rotation table for kv_append_rope: table (device float32 [num_positions][rot_dim],
+ * 16-byte aligned) row p holds cos and sin of p * position_scale * base^(-2i/rot_dim),
+ * i < rot_dim/2, computed in 64 bits and rounded once.  num_positions 1 .. 2^24, rot_dim a
+ * multiple of 16 in 16 .. 256, base > 1, position_scale > 0, both finite.  Runs on the current
+ * device; made once per model. */
+KV_API int kv_rope_table(float* table, int num_positions, int rot_dim, double base, double position_scale,
+                         kv_stream_t stream);
+
+/* Read cached tokens back: token i's K and V of every head, from slot slot_mapping[i] of one
+ * layer into row i of k_out and v_out (device [num_tokens][num_heads][head_dim] of out_dtype,
+ * 16-byte aligned): the inverse of kv_append, e.g. a cached prefix for a prefill kernel that
+ * reads contiguous K/V.  out_dtype F32, or F16 (not for F32 pools).  F32 and F16 pools are
+ * widened or copied; FP8: float32(code) * scale, for F16 rounded once; 4-bit: exact in both
+ * types.  slot < 0: the row is left as it was.  Slots outside the pool set KV_DEVERR_SLOT and
+ * are skipped.  The same slot may be read by many rows.  The pool's device must be current. */
+KV_API int kv_gather(kv_pool* pool, int layer, const int64_t* slot_mapping, int num_tokens, void* k_out,
+                     void* v_out, kv_dtype out_dtype, kv_stream_t stream);
 
 /* ---------------------------------------------------------------- copy-on-write */
 
@@ -213,7 +303,7 @@ KV_API size_t paged_decode_workspace_size(const kv_pool* pool, int batch, int ma
  * through block_tables.  One query token per sequence (decode); batch 0 ..
  * KV_MAX_DECODE_BATCH.
  *   q             device [batch][num_heads][head_dim]: float32 for F32 pools, float16
- *                 for F16 and FP8 pools; 16-byte aligned.
+ *                 for F16, FP8 and 4-bit pools; 16-byte aligned.
  *   out           device float32 [batch][num_heads][head_dim] (written, not accumulated).
  *   block_tables  device int32 [batch][max_blocks_per_seq]; entry j of row s is the
  *                 physical block of tokens [j*B, (j+1)*B) of sequence s.
@@ -240,6 +330,10 @@ KV_API size_t paged_decode_workspace_size(const kv_pool* pool, int batch, int ma
  * products as fp16 (relative rounding 2^-11; below 2^8 by the running maximum).  With
  * the FP8 V scale folded into those weights, v_scale values must stay below 255.
  * F32 pools: fp32 operands throughout.
+ * 4-bit pools: K and V values enter as fp16, which holds them exactly; with up to 4 query
+ * heads per KV head the softmax weights enter as two fp16 terms (value and rounding error),
+ * with 8 as one (relative rounding 2^-11).  The pool's device must be the current device.
+ * KV_DECODE_EARLY_POOL is accepted and has no effect.
  * The cached decode step of [KV Cache篇] §3.1 / [KV缓存机制解析] §5.1 over the
  * block-table gather of [PagedAttention] §3.2, with [KV Cache篇] §6.3's tiling. */
 KV_API int paged_decode_attention(kv_pool* pool, int layer, const void* q, float* out,
@@ -271,7 +365,7 @@ KV_API int paged_decode_attention_append(kv_pool* pool, int layer, const void* q
 
 /* Grouped-query (GQA) and multi-query (MQA) decode attention: num_q_heads query heads
  * share the pool's num_heads KV heads; query head j reads KV head j / G with
- * G = num_q_heads / num_heads in {1, 2, 4, 8} (G > 1: fp16 and FP8 pools).  Each K/V tile
+ * G = num_q_heads / num_heads in {1, 2, 4, 8} (G > 1: all but F32 pools).  Each K/V tile
  * is read once for its G query heads.
  *   q    device [batch][num_q_heads][head_dim] (as paged_decode_attention).
  *   out  device float32 [batch][num_q_heads][head_dim].

@@ -15,6 +15,8 @@ pages it follows:
 * ``cache``      the paged pool as plain arrays: slot-mapped append, block copy,
   and a block manager (free list, reference counts, fork, copy-on-write).
 * ``fp8``        OCP FP8-E4M3 encoding/decoding from its bit-level definition.
+* ``int4``       4-bit cached values: scales, codes and the layout of a tile.
+* ``rope``       rotation of queries and keys by position.
 
 Sources (web pages, cited by title and section):
   [KV Cache篇]           "大模型推理加速——KV Cache篇"
@@ -30,4 +32,4 @@ rounding, and the allocator's closed forms from [PagedAttention] §2.2/§5.1.
 No oracle function is "parity unpinned".
 """
 
-from . import attention, cache, fp8  # noqa: F401
+from . import attention, cache, fp8, int4, rope  # noqa: F401

@@ -14,9 +14,9 @@ from . import build as _build
 
 KV_OK, KV_ERR_INVALID_ARG, KV_ERR_NO_BLOCKS, KV_ERR_STATE = 0, -1, -2, -3
 KV_ERR_CUDA, KV_ERR_DEVICE, KV_ERR_UNSUPPORTED = -4, -5, -6
-KV_F32, KV_F16, KV_FP8_E4M3 = 0, 1, 2
+KV_F32, KV_F16, KV_FP8_E4M3, KV_INT4 = 0, 1, 2, 3
 KV_DEVERR_SLOT, KV_DEVERR_BLOCK_ID, KV_DEVERR_CONTEXT, KV_DEVERR_TIMEOUT = 1, 2, 4, 8
-KV_DEVERR_PREFIX = 16
+KV_DEVERR_PREFIX, KV_DEVERR_POSITION = 16, 32
 KV_FEATURE_TENSOR_MAPS = 1
 KV_DECODE_WORKSPACE_ZEROED, KV_DECODE_PDL, KV_DECODE_EARLY_TABLES, KV_DECODE_OUT_F16 = 1, 2, 4, 8
 KV_DECODE_EARLY_POOL = 16
@@ -44,6 +44,15 @@ class kv_decode_args(C.Structure):
                 ("flags", C.c_uint), ("prefix_groups", C.c_void_p), ("num_prefix_groups", C.c_int)]
 
 
+class kv_rope_args(C.Structure):
+    _fields_ = [("layer", C.c_int), ("q", C.c_void_p), ("num_q_heads", C.c_int), ("q_out", C.c_void_p),
+                ("k", C.c_void_p), ("v", C.c_void_p), ("in_dtype", C.c_int), ("q_stride", C.c_int64),
+                ("k_stride", C.c_int64), ("v_stride", C.c_int64), ("q_out_stride", C.c_int64),
+                ("slot_mapping", C.c_void_p), ("positions", C.c_void_p), ("cos_sin", C.c_void_p),
+                ("table_len", C.c_int), ("rot_dim", C.c_int), ("adjacent_pairs", C.c_int),
+                ("num_tokens", C.c_int), ("flags", C.c_uint), ("stream", C.c_void_p)]
+
+
 class kv_alloc_stats_t(C.Structure):
     _fields_ = [("num_blocks", C.c_int), ("free_blocks", C.c_int), ("shared_blocks", C.c_int),
                 ("num_seqs", C.c_int), ("used_slots", C.c_int64), ("wasted_slots", C.c_int64)]
@@ -61,6 +70,9 @@ _SIGS = {
     "kv_get_device_error": (C.c_int, [_VP, _VP, C.c_int, C.POINTER(C.c_int)]),
     "kv_selftest_wait_timeout": (C.c_int, [_VP, C.c_uint64, _VP]),
     "kv_append": (C.c_int, [_VP, C.c_int, _VP, _VP, C.c_int, _VP, C.c_int, _VP]),
+    "kv_append_rope": (C.c_int, [_VP, _VP]),
+    "kv_rope_table": (C.c_int, [_VP, C.c_int, C.c_int, C.c_double, C.c_double, _VP]),
+    "kv_gather": (C.c_int, [_VP, C.c_int, _VP, C.c_int, _VP, _VP, C.c_int, _VP]),
     "kv_copy_blocks": (C.c_int, [_VP, _VP, C.c_int, C.c_int, C.c_int, _VP]),
     "kv_swap_bytes": (C.c_size_t, [_VP, C.c_int, C.c_int, C.c_int]),
     "kv_swap_out": (C.c_int, [_VP, _VP, C.c_int, C.c_int, C.c_int, _VP, _VP]),
@@ -193,6 +205,20 @@ def kv_get_device_error(pool: int, stream: int = 0, clear: bool = True) -> int:
 def kv_append(pool: int, layer: int, k: int, v: int, in_dtype: int, slot_mapping: int,
               num_tokens: int, stream: int = 0) -> None:
     _check("kv_append", load().kv_append(pool, layer, k, v, in_dtype, slot_mapping, num_tokens, stream))
+
+
+def kv_append_rope(pool: int, args: "kv_rope_args") -> None:
+    _check("kv_append_rope", load().kv_append_rope(pool, C.byref(args)))
+
+
+def kv_rope_table(table: int, num_positions: int, rot_dim: int, base: float, position_scale: float = 1.0,
+                  stream: int = 0) -> None:
+    _check("kv_rope_table", load().kv_rope_table(table, num_positions, rot_dim, base, position_scale, stream))
+
+
+def kv_gather(pool: int, layer: int, slot_mapping: int, num_tokens: int, k_out: int, v_out: int,
+              out_dtype: int, stream: int = 0) -> None:
+    _check("kv_gather", load().kv_gather(pool, layer, slot_mapping, num_tokens, k_out, v_out, out_dtype, stream))
 
 
 def kv_copy_blocks(pool: int, pairs: int, num_pairs: int, layer_begin: int, layer_end: int,

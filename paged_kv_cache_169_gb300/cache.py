@@ -11,8 +11,8 @@ import torch
 
 from . import abi
 
-_TORCH_DTYPE = {"f32": torch.float32, "f16": torch.float16, "fp8": torch.uint8}
-_KV_DTYPE = {"f32": abi.KV_F32, "f16": abi.KV_F16, "fp8": abi.KV_FP8_E4M3}
+_TORCH_DTYPE = {"f32": torch.float32, "f16": torch.float16, "fp8": torch.uint8, "int4": torch.uint8}
+_KV_DTYPE = {"f32": abi.KV_F32, "f16": abi.KV_F16, "fp8": abi.KV_FP8_E4M3, "int4": abi.KV_INT4}
 _IN_DTYPE = {torch.float32: abi.KV_F32, torch.float16: abi.KV_F16}
 
 
@@ -29,10 +29,32 @@ def _dev_ptr(t: torch.Tensor, what: str) -> int:
     return t.data_ptr()
 
 
+def _row_stride(t: torch.Tensor, what: str) -> int:
+    """Elements between the token rows of [n, heads, d] (heads and elements contiguous)."""
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{what}: heads and elements of a token must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def rope_table(num_positions: int, rot_dim: int, base: float = 10000.0, position_scale: float = 1.0,
+               device="cuda", stream=None) -> torch.Tensor:
+    """Cosines and sines of ``position * position_scale * base ** (-2i / rot_dim)`` for
+    PagedKVCache.append_rope: float32 [num_positions, rot_dim], cosines first.  Made once per
+    model."""
+    with torch.cuda.device(device):
+        t = torch.empty((num_positions, rot_dim), dtype=torch.float32, device=device)
+        abi.kv_rope_table(t.data_ptr(), num_positions, rot_dim, base, position_scale, _stream(stream))
+    return t
+
+
 class PagedKVCache:
     """A paged K/V pool for ``num_layers`` layers, laid out [num_blocks, H, B, d] per layer.
 
-    ``dtype``: "f32", "f16" or "fp8" (E4M3 codes + per-block float32 scales).
+    ``dtype``: "f32", "f16", "fp8" (E4M3 codes + per-block float32 scales) or "int4" (4-bit codes
+    with a scale byte per 16 elements, uint8 [num_blocks, H, B/8, 4*d + d/2]; the layout is in
+    kvpaged.h).
     """
 
     def __init__(self, num_layers: int, num_blocks: int, block_size: int, num_heads: int,
@@ -42,6 +64,8 @@ class PagedKVCache:
         self.num_layers, self.num_blocks, self.block_size = num_layers, num_blocks, block_size
         self.num_heads, self.head_dim, self.dtype = num_heads, head_dim, dtype
         shape = (num_blocks, num_heads, block_size, head_dim)
+        if dtype == "int4":
+            shape = (num_blocks, num_heads, block_size // 8, 4 * head_dim + head_dim // 2)
         td = _TORCH_DTYPE[dtype]
         self.k = [torch.empty(shape, dtype=td, device=device) for _ in range(num_layers)]
         self.v = [torch.empty(shape, dtype=td, device=device) for _ in range(num_layers)]
@@ -68,6 +92,68 @@ class PagedKVCache:
             raise ValueError("k and v must be [num_tokens, H, d] of one dtype")
         abi.kv_append(self.handle, layer, _dev_ptr(k, "k"), _dev_ptr(v, "v"), _IN_DTYPE[k.dtype],
                       _dev_ptr(slot_mapping, "slot_mapping"), n, _stream(stream))
+
+    def append_rope(self, layer: int, k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor,
+                    positions: torch.Tensor, cos_sin: torch.Tensor, q: torch.Tensor | None = None,
+                    q_out: torch.Tensor | None = None, adjacent_pairs: bool = False, flags: int = 0,
+                    stream=None) -> torch.Tensor | None:
+        """Rotate queries and keys by their positions and write keys and values into their slots.
+
+        k, v: [n, H, d], q: [n, Hq, d] or None (pool dtype; f16/f32 for FP8 and 4-bit pools), each
+        possibly a view into a packed projection (heads of a token contiguous); slot_mapping: int64
+        [n] (< 0: a padding token, nothing of it is written); positions: int32 [n]; cos_sin: float32
+        [positions, rot_dim] (rope_table).  Pairs are elements (i, i + rot_dim/2), or (2i, 2i + 1)
+        with ``adjacent_pairs``.  Returns q_out, the rotated queries [n, Hq, d] in the type the
+        attention calls take (may be q itself)."""
+        if slot_mapping.dtype != torch.int64 or positions.dtype != torch.int32:
+            raise ValueError("slot_mapping must be int64 and positions int32")
+        n, d = slot_mapping.numel(), self.head_dim
+        if k.shape != (n, self.num_heads, d) or v.shape != k.shape or k.dtype != v.dtype:
+            raise ValueError("k and v must be [num_tokens, H, d] of one dtype")
+        if positions.numel() != n:
+            raise ValueError("positions must have one entry per token")
+        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be float32 [positions, rot_dim]")
+        if k.dtype not in _IN_DTYPE:
+            raise ValueError("k, v and q must be float16 or float32")
+        a = abi.kv_rope_args()
+        a.layer, a.in_dtype, a.num_tokens, a.flags = layer, _IN_DTYPE[k.dtype], n, flags
+        if q is not None:
+            if q.dim() != 3 or q.shape[0] != n or q.shape[2] != d or q.dtype != k.dtype:
+                raise ValueError("q must be [num_tokens, Hq, d] of k's dtype")
+            dt = torch.float32 if self.dtype == "f32" else torch.float16
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=dt, device=q.device)
+            if q_out.shape != q.shape or q_out.dtype != dt:
+                raise ValueError(f"q_out must be {dt} of q's shape")
+            a.q, a.num_q_heads, a.q_out = q.data_ptr(), q.shape[1], q_out.data_ptr()
+            a.q_stride, a.q_out_stride = _row_stride(q, "q"), _row_stride(q_out, "q_out")
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        a.k, a.v, a.k_stride, a.v_stride = k.data_ptr(), v.data_ptr(), _row_stride(k, "k"), _row_stride(v, "v")
+        a.slot_mapping, a.positions = _dev_ptr(slot_mapping, "slot_mapping"), _dev_ptr(positions, "positions")
+        a.cos_sin, a.table_len, a.rot_dim = _dev_ptr(cos_sin, "cos_sin"), cos_sin.shape[0], cos_sin.shape[1]
+        a.adjacent_pairs, a.stream = int(adjacent_pairs), _stream(stream)
+        abi.kv_append_rope(self.handle, a)
+        return q_out
+
+    def gather(self, layer: int, slot_mapping: torch.Tensor, out_dtype: torch.dtype = torch.float16,
+               k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None, stream=None):
+        """Cached tokens back as contiguous rows: (k, v), [n, H, d] of ``out_dtype`` (float16, or
+        float32; float32 pools: float32), dequantised.  Rows whose slot is < 0 are left as they were
+        (new tensors: zero)."""
+        if slot_mapping.dtype != torch.int64:
+            raise ValueError("slot_mapping must be int64")
+        if (k_out is None) != (v_out is None):
+            raise ValueError("k_out and v_out come together")
+        shape = (slot_mapping.numel(), self.num_heads, self.head_dim)
+        if k_out is None:
+            k_out, v_out = (torch.zeros(shape, dtype=out_dtype, device=self.k[0].device) for _ in range(2))
+        if k_out.shape != shape or v_out.shape != shape or k_out.dtype != v_out.dtype or k_out.dtype not in _IN_DTYPE:
+            raise ValueError("k_out and v_out must be float16 or float32 [num_tokens, H, d]")
+        abi.kv_gather(self.handle, layer, _dev_ptr(slot_mapping, "slot_mapping"), shape[0], _dev_ptr(k_out, "k_out"),
+                      _dev_ptr(v_out, "v_out"), _IN_DTYPE[k_out.dtype], _stream(stream))
+        return k_out, v_out
 
     def copy_blocks(self, pairs: torch.Tensor, layer_begin: int = 0, layer_end: int | None = None,
                     stream=None) -> None:

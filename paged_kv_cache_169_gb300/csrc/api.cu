@@ -6,7 +6,7 @@
 #include <new>
 #include <vector>
 
-#include "kvp_internal.cuh"
+#include "pool_types.cuh"
 
 namespace {
 
@@ -17,7 +17,8 @@ bool valid_desc(const kv_pool_desc* d) {
     if (d->block_size != 8 && d->block_size != 16 && d->block_size != 32) return false;
     if (d->num_heads < 1 || d->num_heads > 256) return false;
     if (d->head_dim != 64 && d->head_dim != 128) return false;
-    if (d->dtype != KV_F32 && d->dtype != KV_F16 && d->dtype != KV_FP8_E4M3) return false;
+    if (d->dtype != KV_F32 && d->dtype != KV_F16 && d->dtype != KV_FP8_E4M3 && d->dtype != KV_INT4)
+        return false;
     // element offsets of a whole layer must fit the kernels' int64 arithmetic with room
     const long long elems = 1ll * d->num_blocks * d->num_heads * d->block_size * d->head_dim;
     return elems > 0 && elems < (1ll << 40);
@@ -31,6 +32,16 @@ void free_pool(kv_pool* p) {
     std::free(p->k_scales);
     std::free(p->v_scales);
     delete p;
+}
+
+bool on_pool_device(const kv_pool* p) {
+    int dev = -1;
+    return cudaGetDevice(&dev) == cudaSuccess && dev == p->device;
+}
+
+// elements between two tokens' rows: at least a row, 16-byte steps, byte offsets within int64
+bool valid_stride(int64_t stride, int64_t row, int elem_bytes) {
+    return stride >= row && stride < (int64_t{1} << 28) && stride * elem_bytes % 16 == 0;
 }
 
 // Tensor maps of an fp16 or FP8, head_dim 128 pool for the grouped-query tensor-core path.
@@ -211,13 +222,65 @@ int kv_append(kv_pool* pool, int layer, const void* k, const void* v, kv_dtype i
     if (!pool || layer < 0 || layer >= pool->desc.num_layers || num_tokens < 0) return KV_ERR_INVALID_ARG;
     if (num_tokens == 0) return KV_OK;
     if (!k || !v || !slot_mapping || !kvp::aligned16(k) || !kvp::aligned16(v)) return KV_ERR_INVALID_ARG;
-    const kv_dtype pd = pool->desc.dtype;
-    if (pd == KV_FP8_E4M3) {
-        if (in_dtype != KV_F16 && in_dtype != KV_F32) return KV_ERR_INVALID_ARG;
-    } else if (in_dtype != pd) {
-        return KV_ERR_INVALID_ARG;
+    if (!kvp::valid_input(pool->desc.dtype, in_dtype)) return KV_ERR_INVALID_ARG;
+    if (pool->desc.dtype == KV_INT4) {
+        if (!on_pool_device(pool)) return KV_ERR_INVALID_ARG;
+        return kvp::launch_append_int4(pool, layer, k, v, in_dtype, slot_mapping, num_tokens, stream);
     }
     return kvp::launch_append(pool, layer, k, v, in_dtype, slot_mapping, num_tokens, stream);
+}
+
+int kv_append_rope(kv_pool* pool, const kv_rope_args* x) {
+    if (!pool || !x || x->layer < 0 || x->layer >= pool->desc.num_layers || x->num_tokens < 0)
+        return KV_ERR_INVALID_ARG;
+    const kv_pool_desc& d = pool->desc;
+    if (x->flags & ~KV_DECODE_PDL) return KV_ERR_INVALID_ARG;
+    if (x->rot_dim < 16 || x->rot_dim > d.head_dim || x->rot_dim % 16 != 0 || x->table_len < 1 ||
+        (x->adjacent_pairs != 0 && x->adjacent_pairs != 1))
+        return KV_ERR_INVALID_ARG;
+    if (!kvp::valid_input(d.dtype, x->in_dtype)) return KV_ERR_INVALID_ARG;
+    if (x->num_tokens == 0) return KV_OK;
+    if (!x->k || !x->v || !x->slot_mapping || !x->positions || !x->cos_sin || !kvp::aligned16(x->k) ||
+        !kvp::aligned16(x->v) || !kvp::aligned16(x->cos_sin))
+        return KV_ERR_INVALID_ARG;
+    const int es = kvp::elem_bytes(x->in_dtype), qs = d.dtype == KV_F32 ? 4 : 2;
+    const int64_t row = static_cast<int64_t>(d.num_heads) * d.head_dim;
+    if (!valid_stride(x->k_stride, row, es) || !valid_stride(x->v_stride, row, es)) return KV_ERR_INVALID_ARG;
+    if (x->q) {
+        if (x->num_q_heads < 1 || x->num_q_heads > 2048 || !x->q_out || !kvp::aligned16(x->q) ||
+            !kvp::aligned16(x->q_out))
+            return KV_ERR_INVALID_ARG;
+        const int64_t qrow = static_cast<int64_t>(x->num_q_heads) * d.head_dim;
+        if (!valid_stride(x->q_stride, qrow, es) || !valid_stride(x->q_out_stride, qrow, qs))
+            return KV_ERR_INVALID_ARG;
+        // in place only row by row: the same addresses hold the same elements
+        if (x->q == x->q_out && (es != qs || x->q_stride != x->q_out_stride)) return KV_ERR_INVALID_ARG;
+    }
+    if (!on_pool_device(pool)) return KV_ERR_INVALID_ARG;
+    return kvp::launch_append_rope(pool, *x);
+}
+
+int kv_rope_table(float* table, int num_positions, int rot_dim, double base, double position_scale,
+                  kv_stream_t stream) {
+    if (!table || !kvp::aligned16(table) || num_positions < 1 || num_positions > (1 << 24) || rot_dim < 16 ||
+        rot_dim > 256 || rot_dim % 16 != 0)
+        return KV_ERR_INVALID_ARG;
+    if (!(base > 1.0) || !(base < 1e300) || !(position_scale > 0.0) || !(position_scale < 1e300))
+        return KV_ERR_INVALID_ARG;
+    return kvp::launch_rope_table(table, num_positions, rot_dim, base, position_scale,
+                                  static_cast<cudaStream_t>(stream));
+}
+
+int kv_gather(kv_pool* pool, int layer, const int64_t* slot_mapping, int num_tokens, void* k_out, void* v_out,
+              kv_dtype out_dtype, kv_stream_t stream) {
+    if (!pool || layer < 0 || layer >= pool->desc.num_layers || num_tokens < 0) return KV_ERR_INVALID_ARG;
+    if (out_dtype != KV_F32 && (out_dtype != KV_F16 || pool->desc.dtype == KV_F32)) return KV_ERR_INVALID_ARG;
+    if (num_tokens == 0) return KV_OK;
+    if (!slot_mapping || !k_out || !v_out || !kvp::aligned16(k_out) || !kvp::aligned16(v_out))
+        return KV_ERR_INVALID_ARG;
+    if (!on_pool_device(pool)) return KV_ERR_INVALID_ARG;
+    return kvp::launch_gather(pool, layer, slot_mapping, num_tokens, k_out, v_out, out_dtype,
+                              static_cast<cudaStream_t>(stream));
 }
 
 int kv_copy_blocks(kv_pool* pool, const int32_t* pairs, int num_pairs, int layer_begin,
@@ -234,7 +297,7 @@ size_t paged_decode_workspace_size(const kv_pool* pool, int batch, int max_conte
                                    int partition_tokens) {
     if (!pool) return 0;
     kvp::AttnPlan plan;
-    if (kvp::plan_attention(pool, batch, max_context, partition_tokens, &plan) != KV_OK) return 0;
+    if (kvp::plan_decode(pool, batch, max_context, partition_tokens, &plan) != KV_OK) return 0;
     return plan.ws_bytes;
 }
 
@@ -253,11 +316,11 @@ int paged_decode_attention(kv_pool* pool, int layer, const void* q, float* out,
         return KV_ERR_INVALID_ARG;
     if (!(scale > 0.f) || !(scale < 3.0e38f)) return KV_ERR_INVALID_ARG;
     kvp::AttnPlan plan;
-    int rc = kvp::plan_attention(pool, batch, max_context, partition_tokens, &plan);
+    int rc = kvp::plan_decode(pool, batch, max_context, partition_tokens, &plan);
     if (rc != KV_OK) return rc;
     if (workspace_bytes < plan.ws_bytes) return KV_ERR_INVALID_ARG;
-    return kvp::launch_attention(pool, layer, q, out, block_tables, max_blocks_per_seq, context_lens,
-                                 batch, max_context, scale, plan, workspace, stream);
+    return kvp::launch_decode(pool, layer, q, nullptr, nullptr, 0, out, block_tables, max_blocks_per_seq,
+                              context_lens, batch, max_context, scale, plan, workspace, stream);
 }
 
 int paged_decode_attention_append(kv_pool* pool, int layer, const void* q, const void* k_new,
@@ -275,18 +338,13 @@ int paged_decode_attention_append(kv_pool* pool, int layer, const void* q, const
     if (!kvp::aligned16(q) || !kvp::aligned16(out) || !kvp::aligned16(k_new) || !kvp::aligned16(v_new) ||
         (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
         return KV_ERR_INVALID_ARG;
-    const kv_dtype pd = pool->desc.dtype;
-    if (pd == KV_FP8_E4M3) {
-        if (in_dtype != KV_F16 && in_dtype != KV_F32) return KV_ERR_INVALID_ARG;
-    } else if (in_dtype != pd) {
-        return KV_ERR_INVALID_ARG;
-    }
+    if (!kvp::valid_input(pool->desc.dtype, in_dtype)) return KV_ERR_INVALID_ARG;
     if (!(scale > 0.f) || !(scale < 3.0e38f)) return KV_ERR_INVALID_ARG;
     kvp::AttnPlan plan;
-    int rc = kvp::plan_attention(pool, batch, max_context, partition_tokens, &plan);
+    int rc = kvp::plan_decode(pool, batch, max_context, partition_tokens, &plan);
     if (rc != KV_OK) return rc;
     if (workspace_bytes < plan.ws_bytes) return KV_ERR_INVALID_ARG;
-    return kvp::launch_attention_append(pool, layer, q, k_new, v_new, kvp::elem_bytes(in_dtype), out,
+    return kvp::launch_decode(pool, layer, q, k_new, v_new, kvp::elem_bytes(in_dtype), out,
                                         block_tables, max_blocks_per_seq, context_lens, batch,
                                         max_context, scale, plan, workspace, stream);
 }
@@ -295,7 +353,7 @@ size_t paged_decode_workspace_size_gqa(const kv_pool* pool, int batch, int num_q
                                        int partition_tokens) {
     if (!pool || num_q_heads < 1 || num_q_heads % pool->desc.num_heads != 0) return 0;
     kvp::AttnPlan plan;
-    if (kvp::plan_attention(pool, batch, max_context, partition_tokens, &plan,
+    if (kvp::plan_decode(pool, batch, max_context, partition_tokens, &plan,
                             num_q_heads / pool->desc.num_heads) != KV_OK)
         return 0;
     return plan.ws_bytes;
@@ -319,20 +377,13 @@ int paged_decode_attention_gqa(kv_pool* pool, int layer, const void* q, int num_
     if (!kvp::aligned16(q) || !kvp::aligned16(out) || (k_new && (!kvp::aligned16(k_new) || !kvp::aligned16(v_new))) ||
         (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
         return KV_ERR_INVALID_ARG;
-    if (k_new) {
-        const kv_dtype pd = pool->desc.dtype;
-        if (pd == KV_FP8_E4M3) {
-            if (in_dtype != KV_F16 && in_dtype != KV_F32) return KV_ERR_INVALID_ARG;
-        } else if (in_dtype != pd) {
-            return KV_ERR_INVALID_ARG;
-        }
-    }
+    if (k_new && !kvp::valid_input(pool->desc.dtype, in_dtype)) return KV_ERR_INVALID_ARG;
     if (!(scale > 0.f) || !(scale < 3.0e38f)) return KV_ERR_INVALID_ARG;
     kvp::AttnPlan plan;
-    int rc = kvp::plan_attention(pool, batch, max_context, partition_tokens, &plan, group);
+    int rc = kvp::plan_decode(pool, batch, max_context, partition_tokens, &plan, group);
     if (rc != KV_OK) return rc;
     if (workspace_bytes < plan.ws_bytes) return KV_ERR_INVALID_ARG;
-    return kvp::launch_attention_append(pool, layer, q, k_new, v_new, k_new ? kvp::elem_bytes(in_dtype) : 0,
+    return kvp::launch_decode(pool, layer, q, k_new, v_new, k_new ? kvp::elem_bytes(in_dtype) : 0,
                                         out, block_tables, max_blocks_per_seq, context_lens, batch,
                                         max_context, scale, plan, workspace, stream);
 }
@@ -348,7 +399,7 @@ size_t paged_decode_workspace_size_ex(const kv_pool* pool, const kv_decode_args*
             return 0;
         return plan.ws_bytes;
     }
-    if (kvp::plan_attention(pool, x->batch, x->max_context, x->partition_tokens, &plan,
+    if (kvp::plan_decode(pool, x->batch, x->max_context, x->partition_tokens, &plan,
                             hq / pool->desc.num_heads, x->window) != KV_OK)
         return 0;
     return plan.ws_bytes;
@@ -371,14 +422,7 @@ int paged_decode_attention_ex(kv_pool* pool, const kv_decode_args* x) {
         (x->k_new && (!kvp::aligned16(x->k_new) || !kvp::aligned16(x->v_new))) ||
         (reinterpret_cast<uintptr_t>(x->workspace) & 255u) != 0)
         return KV_ERR_INVALID_ARG;
-    if (x->k_new) {
-        const kv_dtype pd = pool->desc.dtype;
-        if (pd == KV_FP8_E4M3) {
-            if (x->in_dtype != KV_F16 && x->in_dtype != KV_F32) return KV_ERR_INVALID_ARG;
-        } else if (x->in_dtype != pd) {
-            return KV_ERR_INVALID_ARG;
-        }
-    }
+    if (x->k_new && !kvp::valid_input(pool->desc.dtype, x->in_dtype)) return KV_ERR_INVALID_ARG;
     if (!(x->scale > 0.f) || !(x->scale < 3.0e38f)) return KV_ERR_INVALID_ARG;
     if (x->flags & ~(KV_DECODE_WORKSPACE_ZEROED | KV_DECODE_PDL | KV_DECODE_EARLY_TABLES | KV_DECODE_OUT_F16 |
                      KV_DECODE_EARLY_POOL))
@@ -394,12 +438,12 @@ int paged_decode_attention_ex(kv_pool* pool, const kv_decode_args* x) {
         plan.groups = x->prefix_groups;
         plan.n_groups = x->num_prefix_groups;
     } else {
-        rc = kvp::plan_attention(pool, x->batch, x->max_context, x->partition_tokens, &plan, group, x->window);
+        rc = kvp::plan_decode(pool, x->batch, x->max_context, x->partition_tokens, &plan, group, x->window);
     }
     if (rc != KV_OK) return rc;
     if (x->workspace_bytes < plan.ws_bytes) return KV_ERR_INVALID_ARG;
     plan.flags = x->flags;
-    return kvp::launch_attention_append(pool, x->layer, x->q, x->k_new, x->v_new,
+    return kvp::launch_decode(pool, x->layer, x->q, x->k_new, x->v_new,
                                         x->k_new ? kvp::elem_bytes(x->in_dtype) : 0, x->out, x->block_tables,
                                         x->max_blocks_per_seq, x->context_lens, x->batch, x->max_context,
                                         x->scale, plan, x->workspace, x->stream);

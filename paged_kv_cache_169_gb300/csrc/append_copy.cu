@@ -8,7 +8,7 @@
 // factor; the stored code is RNE-satfinite(x / scale[block]).
 // Copy: "KV Cache与PagedAttention" §3.3 copy_block — the whole physical block.
 
-#include "kvp_internal.cuh"
+#include "pool_types.cuh"
 
 namespace kvp {
 namespace {
@@ -170,8 +170,7 @@ int launch_copy_blocks(const kv_pool* pool, const int32_t* pairs, int num_pairs,
                        int layer_end, cudaStream_t stream) {
     const kv_pool_desc& d = pool->desc;
     if (num_pairs == 0 || layer_end == layer_begin) return KV_OK;
-    const int64_t block_bytes =
-        static_cast<int64_t>(d.num_heads) * d.block_size * d.head_dim * elem_bytes(d.dtype);
+    const int64_t bytes = block_bytes(d);
     for (int l0 = layer_begin; l0 < layer_end; l0 += kMaxCopyLayers) {
         const int nl = (layer_end - l0) < kMaxCopyLayers ? (layer_end - l0) : kMaxCopyLayers;
         LayerPtrs p{};
@@ -181,8 +180,8 @@ int launch_copy_blocks(const kv_pool* pool, const int32_t* pairs, int num_pairs,
             p.ks[i] = pool->k_scales ? pool->k_scales[l0 + i] : nullptr;
             p.vs[i] = pool->v_scales ? pool->v_scales[l0 + i] : nullptr;
         }
-        copy_blocks_kernel<<<dim3(num_pairs, nl, 2), 256, 0, stream>>>(pairs, p, block_bytes,
-                                                                        d.num_blocks, pool->d_err);
+        copy_blocks_kernel<<<dim3(num_pairs, nl, 2), 256, 0, stream>>>(pairs, p, bytes, d.num_blocks,
+                                                                        pool->d_err);
         if (cudaGetLastError() != cudaSuccess) return KV_ERR_CUDA;
     }
     return KV_OK;
@@ -194,10 +193,8 @@ namespace kvp {
 
 size_t swap_bytes(const kv_pool* pool, int num_blocks, int layer_begin, int layer_end) {
     const kv_pool_desc& d = pool->desc;
-    const int64_t block_bytes =
-        static_cast<int64_t>(d.num_heads) * d.block_size * d.head_dim * elem_bytes(d.dtype);
     const int64_t nl = layer_end - layer_begin;
-    int64_t n = static_cast<int64_t>(num_blocks) * nl * 2 * block_bytes;
+    int64_t n = static_cast<int64_t>(num_blocks) * nl * 2 * block_bytes(d);
     if (d.dtype == KV_FP8_E4M3) n += static_cast<int64_t>(num_blocks) * nl * 2 * sizeof(float);
     return static_cast<size_t>(n);
 }
@@ -214,8 +211,7 @@ int launch_swap(const kv_pool* pool, bool out, const int32_t* blocks, int num_bl
         cudaGetLastError();
         return KV_ERR_INVALID_ARG;
     }
-    const int64_t block_bytes =
-        static_cast<int64_t>(d.num_heads) * d.block_size * d.head_dim * elem_bytes(d.dtype);
+    const int64_t bytes = block_bytes(d);
     const int nl = layer_end - layer_begin;
     LayerPtrs p{};
     for (int i = 0; i < nl; ++i) {
@@ -226,10 +222,10 @@ int launch_swap(const kv_pool* pool, bool out, const int32_t* blocks, int num_bl
     }
     const dim3 grid(num_blocks, nl, 2);
     if (out)
-        swap_kernel<true><<<grid, 256, 0, stream>>>(blocks, p, static_cast<char*>(dev), block_bytes, num_blocks,
+        swap_kernel<true><<<grid, 256, 0, stream>>>(blocks, p, static_cast<char*>(dev), bytes, num_blocks,
                                                     nl, d.num_blocks, pool->d_err);
     else
-        swap_kernel<false><<<grid, 256, 0, stream>>>(blocks, p, static_cast<char*>(dev), block_bytes, num_blocks,
+        swap_kernel<false><<<grid, 256, 0, stream>>>(blocks, p, static_cast<char*>(dev), bytes, num_blocks,
                                                      nl, d.num_blocks, pool->d_err);
     return cudaGetLastError() == cudaSuccess ? KV_OK : KV_ERR_CUDA;
 }

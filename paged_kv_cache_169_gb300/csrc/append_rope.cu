@@ -1,0 +1,532 @@
+// kv_append_rope: new tokens' queries and keys rotated by their positions, keys and values written
+// into their slots, in one launch; kv_append into 4-bit pools (the same kernel without rotation);
+// kv_gather, its inverse (cached tokens back as contiguous rows); kv_rope_table.
+//
+// Rotation (rotary position embedding): with angle a = position * frequency_i, elements (x, y) of
+// pair i become (x cos a - y sin a, y cos a + x sin a).  Products and sums are float32, rounded
+// separately (no contraction), from a float32 table of cosines and sines; the only rounding to
+// fewer bits is the store (float16; FP8 and 4-bit codes are quantised from the float32 value).
+//
+// Layout of the work: a half-warp holds whole head rows, 8 elements (a unit) per lane, so a unit's
+// partner under either pairing and the other half of its quantisation group are a shuffle away
+// and every input is read once.  The two half-warps take two consecutive tokens: where their slots
+// share a 32-bit word of a 4-bit V tile (slot 2m and 2m + 1), the pair of lanes writes whole words.
+// A warp walks over the head rows (queries, then keys, then values) with its token's table values
+// in registers and several rows' loads in flight.  Bound: HBM.
+
+#include "int4.cuh"
+#include "pool_types.cuh"
+
+namespace kvp {
+namespace {
+
+constexpr unsigned FULL = 0xffffffffu;
+constexpr int kThreads = 256, kWarpsPerCta = kThreads / 32;
+
+struct RopeArgs {
+    const char *q, *k, *v;
+    char* q_out;
+    int64_t q_stride, k_stride, v_stride, qo_stride;   // bytes between tokens
+    const int64_t* slots;
+    const int32_t* positions;
+    const float* table;
+    int table_len, rot, adjacent;
+    char *kpool, *vpool;
+    const float *kscale, *vscale;
+    int n, Hq, H, B;
+    int64_t num_slots;
+    int* err;
+};
+
+// 8 elements of type TIn as float
+template <typename TIn> struct Raw;
+template <> struct Raw<__half> { uint4 a; };
+template <> struct Raw<float> { float4 a, b; };
+
+__device__ __forceinline__ void load_raw(const char* p, Raw<__half>& r) {
+    r.a = __ldcs(reinterpret_cast<const uint4*>(p));
+}
+__device__ __forceinline__ void load_raw(const char* p, Raw<float>& r) {
+    r.a = __ldcs(reinterpret_cast<const float4*>(p));
+    r.b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+}
+__device__ __forceinline__ void widen(const Raw<__half>& r, float (&x)[8]) {
+    const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+    }
+}
+__device__ __forceinline__ void widen(const Raw<float>& r, float (&x)[8]) {
+    x[0] = r.a.x; x[1] = r.a.y; x[2] = r.a.z; x[3] = r.a.w;
+    x[4] = r.b.x; x[5] = r.b.y; x[6] = r.b.z; x[7] = r.b.w;
+}
+
+__device__ __forceinline__ uint4 halves(const float (&x)[8]) {
+    uint4 r;
+    const __half2 h0 = __floats2half2_rn(x[0], x[1]), h1 = __floats2half2_rn(x[2], x[3]);
+    const __half2 h2 = __floats2half2_rn(x[4], x[5]), h3 = __floats2half2_rn(x[6], x[7]);
+    r.x = *reinterpret_cast<const uint32_t*>(&h0);
+    r.y = *reinterpret_cast<const uint32_t*>(&h1);
+    r.z = *reinterpret_cast<const uint32_t*>(&h2);
+    r.w = *reinterpret_cast<const uint32_t*>(&h3);
+    return r;
+}
+
+// The unit's 8 elements into pool row `at` (the block's tile of the head, token off of it).
+// IS_V only matters to 4-bit tiles; paired: lane ^ 16 holds the same unit of the token that
+// shares this one's words.
+template <int D, kv_dtype POOL>
+__device__ __forceinline__ void store_unit(char* tile, int off, int unit, const float (&x)[8], float scale, bool is_v,
+                                           bool paired, bool live, int lane) {
+    if constexpr (POOL == KV_F32) {
+        if (!live) return;
+        float4* p = reinterpret_cast<float4*>(tile + (static_cast<int64_t>(off) * D + unit * 8) * 4);
+        p[0] = make_float4(x[0], x[1], x[2], x[3]);
+        p[1] = make_float4(x[4], x[5], x[6], x[7]);
+    } else if constexpr (POOL == KV_F16) {
+        if (live) *reinterpret_cast<uint4*>(tile + (off * D + unit * 8) * 2) = halves(x);
+    } else if constexpr (POOL == KV_FP8_E4M3) {
+        if (!live) return;
+        uint2 c;
+        c.x = float2_to_e4m3x2(__fdiv_rn(x[0], scale), __fdiv_rn(x[1], scale)) |
+              static_cast<uint32_t>(float2_to_e4m3x2(__fdiv_rn(x[2], scale), __fdiv_rn(x[3], scale))) << 16;
+        c.y = float2_to_e4m3x2(__fdiv_rn(x[4], scale), __fdiv_rn(x[5], scale)) |
+              static_cast<uint32_t>(float2_to_e4m3x2(__fdiv_rn(x[6], scale), __fdiv_rn(x[7], scale))) << 16;
+        *reinterpret_cast<uint2*>(tile + off * D + unit * 8) = c;
+    } else {
+        float amax = 0.f;
+        #pragma unroll
+        for (int i = 0; i < 8; ++i) amax = max_nan(amax, fabsf(x[i]));
+        amax = max_nan(amax, __shfl_xor_sync(FULL, amax, 1));          // the group's other unit
+        const uint32_t sb = int4_scale_byte(amax);
+        const float s = int4_scale_value(sb), inv = int4_inverse(s);
+        uint32_t w = 0;
+        #pragma unroll
+        for (int i = 0; i < 8; ++i) w |= int4_nibble(x[i], s, inv, 7.f * s) << (4 * i);
+        char* oct = tile + (off >> 3) * Int4<D>::OCT;
+        const int token = off & 7, e0 = unit * 8;
+        if (!is_v) {
+            if (!live) return;
+            *reinterpret_cast<uint32_t*>(oct + int4_k_code<D>(token, e0)) = w;
+            if ((unit & 1) == 0) *reinterpret_cast<uint8_t*>(oct + int4_k_scale<D>(token, e0)) = sb;
+            return;
+        }
+        // the unit's two pieces lie in two words, each shared with the token's neighbour
+        const uint32_t other = __shfl_xor_sync(FULL, w, 16);
+        if (!live) return;
+        if (paired) {
+            // the even token writes the first word, the odd token the second
+            const bool odd = token & 1;
+            const uint32_t word = odd ? __byte_perm(other, w, 0x7632) : __byte_perm(w, other, 0x5410);
+            *reinterpret_cast<uint32_t*>(oct + int4_v_piece<D>(token & ~1, e0 + (odd ? 4 : 0))) = word;
+        } else {
+            *reinterpret_cast<uint16_t*>(oct + int4_v_piece<D>(token, e0)) = static_cast<uint16_t>(w);
+            *reinterpret_cast<uint16_t*>(oct + int4_v_piece<D>(token, e0 + 4)) = static_cast<uint16_t>(w >> 16);
+        }
+        if ((unit & 1) == 0) *reinterpret_cast<uint8_t*>(oct + int4_v_scale<D>(token, e0)) = sb;
+    }
+}
+
+template <int D, typename TIn, kv_dtype POOL>
+__global__ void __launch_bounds__(kThreads) append_rope_kernel(const __grid_constant__ RopeArgs a) {
+    constexpr int UPR = D / 8, HPW = 16 / UPR;         // units per row; head rows per half-warp
+    constexpr int ESZ = sizeof(TIn);
+    constexpr int UNROLL = ESZ == 2 ? 4 : 2;
+    constexpr int ROW = POOL == KV_INT4 ? D / 2 + D / 16 : POOL == KV_FP8_E4M3 ? D : POOL == KV_F16 ? 2 * D : 4 * D;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int unit = lane & (UPR - 1), sub = (lane & 15) / UPR;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int64_t tok = static_cast<int64_t>(blockIdx.x) * 2 + (lane >> 4);
+    // ---- the token: its slot, its position, its rotation
+    int64_t slot = tok < a.n ? a.slots[tok] : -1;
+    int pos = 0;
+    bool live = slot >= 0;
+    if (live && slot >= a.num_slots) {
+        atomicOr(a.err, KV_DEVERR_SLOT);
+        live = false;
+    }
+    if (a.rot > 0 && live) {
+        pos = a.positions[tok];
+        if (pos < 0 || pos >= a.table_len) {
+            atomicOr(a.err, KV_DEVERR_POSITION);
+            live = false;
+        }
+    }
+    if (!__any_sync(FULL, live)) return;
+    if (!live) slot = 0;
+    const int64_t blk = slot / a.B;
+    const int off = static_cast<int>(slot - blk * a.B);
+    // both tokens live and in one 32-bit word of a 4-bit V tile
+    const int64_t other_slot = __shfl_xor_sync(FULL, live ? slot : int64_t{-2}, 16);
+    const bool paired = POOL == KV_INT4 && live && other_slot == (slot ^ 1);
+    float ks = 1.f, vs = 1.f;
+    if constexpr (POOL == KV_FP8_E4M3) {
+        ks = a.kscale[blk];
+        vs = a.vscale[blk];
+    }
+    // this unit's cosines and sines: half pairs 8 of each, adjacent pairs 4 of each
+    float c[8], s[8];
+    const bool turned = unit * 8 < a.rot;
+    const int half_units = a.rot >> 4;
+    const bool low = unit < half_units;                // half pairs: the first element of each pair
+    if (a.rot > 0) {
+        const float* row = a.table + static_cast<int64_t>(pos) * a.rot;
+        const int i0 = !turned ? 0 : a.adjacent ? unit * 4 : (low ? unit : unit - half_units) * 8;
+        #pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if (j == 1 && a.adjacent) break;
+            const float4 cv = *reinterpret_cast<const float4*>(row + i0 + 4 * j);
+            const float4 sv = *reinterpret_cast<const float4*>(row + a.rot / 2 + i0 + 4 * j);
+            c[4 * j] = cv.x; c[4 * j + 1] = cv.y; c[4 * j + 2] = cv.z; c[4 * j + 3] = cv.w;
+            s[4 * j] = sv.x; s[4 * j + 1] = sv.y; s[4 * j + 2] = sv.z; s[4 * j + 3] = sv.w;
+        }
+    }
+    const int partner = (lane & ~(UPR - 1)) | (turned ? (low ? unit + half_units : unit - half_units) : unit);
+    auto rotate = [&](float (&x)[8]) {
+        if (a.adjacent) {
+            if (!turned) return;
+            #pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float u = x[2 * i], w = x[2 * i + 1];
+                x[2 * i] = __fsub_rn(__fmul_rn(u, c[i]), __fmul_rn(w, s[i]));
+                x[2 * i + 1] = __fadd_rn(__fmul_rn(w, c[i]), __fmul_rn(u, s[i]));
+            }
+            return;
+        }
+        #pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float y = __shfl_sync(FULL, x[i], partner);
+            const float z = __fmul_rn(y, s[i]);
+            if (turned) x[i] = __fadd_rn(__fmul_rn(x[i], c[i]), low ? -z : z);
+        }
+    };
+    // ---- head rows: queries, keys, values, HPW rows per half-warp and step
+    const int uq = a.Hq ? (a.Hq + HPW - 1) / HPW : 0, uk = (a.H + HPW - 1) / HPW;
+    const int rows = uq + 2 * uk, step = gridDim.y * kWarpsPerCta;
+    const int64_t safe = live ? tok : tok ^ 1;         // a dead half-warp reads the live one's rows
+    for (int r0 = blockIdx.y * kWarpsPerCta + warp; r0 < rows; r0 += step * UNROLL) {
+        Raw<TIn> raw[UNROLL];
+        #pragma unroll
+        for (int j = 0; j < UNROLL; ++j) {
+            const int r = r0 + j * step;
+            if (r >= rows) break;
+            const int which = r < uq ? 0 : r < uq + uk ? 1 : 2;
+            const int h = min((r - (which == 0 ? 0 : which == 1 ? uq : uq + uk)) * HPW + sub, (which ? a.H : a.Hq) - 1);
+            const char* base = which == 0 ? a.q + safe * a.q_stride : which == 1 ? a.k + safe * a.k_stride
+                                                                                 : a.v + safe * a.v_stride;
+            load_raw(base + (h * D + unit * 8) * ESZ, raw[j]);
+        }
+        __syncwarp();                                  // q_out may be q: every row is read first
+        #pragma unroll
+        for (int j = 0; j < UNROLL; ++j) {
+            const int r = r0 + j * step;
+            if (r >= rows) break;
+            const int which = r < uq ? 0 : r < uq + uk ? 1 : 2;
+            const int h = (r - (which == 0 ? 0 : which == 1 ? uq : uq + uk)) * HPW + sub;
+            const bool here = live && h < (which ? a.H : a.Hq);
+            float x[8];
+            widen(raw[j], x);
+            if (which < 2 && a.rot > 0) rotate(x);
+            if (which == 0) {
+                if (!here) continue;
+                char* p = a.q_out + tok * a.qo_stride;
+                if constexpr (POOL == KV_F32) {
+                    float4* o = reinterpret_cast<float4*>(p + (h * D + unit * 8) * 4);
+                    o[0] = make_float4(x[0], x[1], x[2], x[3]);
+                    o[1] = make_float4(x[4], x[5], x[6], x[7]);
+                } else {
+                    *reinterpret_cast<uint4*>(p + (h * D + unit * 8) * 2) = halves(x);
+                }
+            } else {
+                char* tile = (which == 1 ? a.kpool : a.vpool) +
+                             (blk * a.H + (here ? h : 0)) * static_cast<int64_t>(a.B) * ROW;
+                store_unit<D, POOL>(tile, off, unit, x, which == 1 ? ks : vs, which == 2, paired, here, lane);
+            }
+        }
+    }
+}
+
+template <typename TIn, kv_dtype POOL>
+int launch_rope_typed(const kv_pool* pool, const RopeArgs& a, bool pdl, cudaStream_t stream) {
+    const int D = pool->desc.head_dim;
+    const int hpw = 16 / (D / 8);
+    const int uq = a.Hq ? (a.Hq + hpw - 1) / hpw : 0, rows = uq + 2 * ((a.H + hpw - 1) / hpw);
+    const int pairs = (a.n + 1) / 2;
+    // few tokens: the head rows spread over CTAs, one step each; many: one CTA per token pair
+    const int most = (rows + kWarpsPerCta - 1) / kWarpsPerCta;
+    int gy = (8 * pool->num_sms + pairs - 1) / pairs;
+    gy = gy < 1 ? 1 : gy > most ? most : gy;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(pairs), static_cast<unsigned>(gy));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    const cudaError_t rc = D == 128 ? cudaLaunchKernelEx(&cfg, append_rope_kernel<128, TIn, POOL>, a)
+                                    : cudaLaunchKernelEx(&cfg, append_rope_kernel<64, TIn, POOL>, a);
+    if (rc != cudaSuccess) {
+        cudaGetLastError();
+        return KV_ERR_CUDA;
+    }
+    return KV_OK;
+}
+
+int launch_rope_any(const kv_pool* pool, kv_dtype in, const RopeArgs& a, bool pdl, cudaStream_t stream) {
+    switch (pool->desc.dtype) {
+        case KV_F32: return launch_rope_typed<float, KV_F32>(pool, a, pdl, stream);
+        case KV_F16: return launch_rope_typed<__half, KV_F16>(pool, a, pdl, stream);
+        case KV_FP8_E4M3:
+            return in == KV_F16 ? launch_rope_typed<__half, KV_FP8_E4M3>(pool, a, pdl, stream)
+                                : launch_rope_typed<float, KV_FP8_E4M3>(pool, a, pdl, stream);
+        default:
+            return in == KV_F16 ? launch_rope_typed<__half, KV_INT4>(pool, a, pdl, stream)
+                                : launch_rope_typed<float, KV_INT4>(pool, a, pdl, stream);
+    }
+}
+
+RopeArgs pool_side(const kv_pool* pool, int layer) {
+    const kv_pool_desc& d = pool->desc;
+    RopeArgs a{};
+    a.kpool = static_cast<char*>(pool->k_layers[layer]);
+    a.vpool = static_cast<char*>(pool->v_layers[layer]);
+    a.kscale = pool->k_scales ? pool->k_scales[layer] : nullptr;
+    a.vscale = pool->v_scales ? pool->v_scales[layer] : nullptr;
+    a.H = d.num_heads;
+    a.B = d.block_size;
+    a.num_slots = static_cast<int64_t>(d.num_blocks) * d.block_size;
+    a.err = pool->d_err;
+    return a;
+}
+
+}  // namespace
+
+int launch_append_rope(const kv_pool* pool, const kv_rope_args& x) {
+    const int es = elem_bytes(x.in_dtype), qs = pool->desc.dtype == KV_F32 ? 4 : 2;
+    RopeArgs a = pool_side(pool, x.layer);
+    a.q = static_cast<const char*>(x.q);
+    a.k = static_cast<const char*>(x.k);
+    a.v = static_cast<const char*>(x.v);
+    a.q_out = static_cast<char*>(x.q_out);
+    a.q_stride = x.q_stride * es;
+    a.k_stride = x.k_stride * es;
+    a.v_stride = x.v_stride * es;
+    a.qo_stride = x.q_out_stride * qs;
+    a.slots = x.slot_mapping;
+    a.positions = x.positions;
+    a.table = x.cos_sin;
+    a.table_len = x.table_len;
+    a.rot = x.rot_dim;
+    a.adjacent = x.adjacent_pairs ? 1 : 0;
+    a.n = x.num_tokens;
+    a.Hq = x.q ? x.num_q_heads : 0;
+    return launch_rope_any(pool, x.in_dtype, a, (x.flags & KV_DECODE_PDL) != 0, x.stream);
+}
+
+int launch_append_int4(const kv_pool* pool, int layer, const void* k, const void* v, kv_dtype in_dtype,
+                       const int64_t* slot_mapping, int num_tokens, cudaStream_t stream) {
+    RopeArgs a = pool_side(pool, layer);
+    a.k = static_cast<const char*>(k);
+    a.v = static_cast<const char*>(v);
+    a.k_stride = a.v_stride = static_cast<int64_t>(pool->desc.num_heads) * pool->desc.head_dim * elem_bytes(in_dtype);
+    a.slots = slot_mapping;
+    a.n = num_tokens;
+    return launch_rope_any(pool, in_dtype, a, false, stream);
+}
+
+// ---------------------------------------------------------------- gather
+namespace {
+
+struct GatherArgs {
+    const char *kpool, *vpool;
+    const float *kscale, *vscale;
+    const int64_t* slots;
+    char *k, *v;
+    int n, H, B;
+    int64_t num_slots;
+    int* err;
+};
+
+// The unit's 8 stored elements: their bytes in a (and b), a 4-bit unit's scale byte in a.y.
+template <int D, kv_dtype POOL>
+__device__ __forceinline__ void load_stored(const char* tile, int off, int unit, bool is_v, uint4& a, uint4& b) {
+    if constexpr (POOL == KV_F32) {
+        const uint4* p = reinterpret_cast<const uint4*>(tile + (static_cast<int64_t>(off) * D + unit * 8) * 4);
+        a = __ldcs(p);
+        b = __ldcs(p + 1);
+    } else if constexpr (POOL == KV_F16) {
+        a = __ldcs(reinterpret_cast<const uint4*>(tile + (off * D + unit * 8) * 2));
+    } else if constexpr (POOL == KV_FP8_E4M3) {
+        const uint2 x = __ldcs(reinterpret_cast<const uint2*>(tile + off * D + unit * 8));
+        a.x = x.x;
+        a.y = x.y;
+    } else {
+        const char* oct = tile + (off >> 3) * Int4<D>::OCT;
+        const int token = off & 7, e0 = unit * 8;
+        if (!is_v) {
+            a.x = *reinterpret_cast<const uint32_t*>(oct + int4_k_code<D>(token, e0));
+            a.y = *reinterpret_cast<const uint8_t*>(oct + int4_k_scale<D>(token, e0));
+        } else {
+            a.x = *reinterpret_cast<const uint16_t*>(oct + int4_v_piece<D>(token, e0)) |
+                  static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(oct + int4_v_piece<D>(token, e0 + 4))) << 16;
+            a.y = *reinterpret_cast<const uint8_t*>(oct + int4_v_scale<D>(token, e0));
+        }
+    }
+}
+
+// grid (tokens / 2, head splits): half-warps of one token each, as append_rope_kernel
+template <int D, kv_dtype POOL, typename TOut>
+__global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant__ GatherArgs a) {
+    constexpr int UPR = D / 8, HPW = 16 / UPR, UNROLL = 4;
+    constexpr int ROW = POOL == KV_INT4 ? D / 2 + D / 16 : POOL == KV_FP8_E4M3 ? D : POOL == KV_F16 ? 2 * D : 4 * D;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int unit = lane & (UPR - 1), sub = (lane & 15) / UPR;
+    const int64_t tok = static_cast<int64_t>(blockIdx.x) * 2 + (lane >> 4);
+    const int64_t slot = tok < a.n ? a.slots[tok] : -1;
+    if (slot < 0) return;                              // no shuffles below
+    if (slot >= a.num_slots) {
+        atomicOr(a.err, KV_DEVERR_SLOT);
+        return;
+    }
+    const int64_t blk = slot / a.B;
+    const int off = static_cast<int>(slot - blk * a.B);
+    float ks = 1.f, vs = 1.f;
+    if constexpr (POOL == KV_FP8_E4M3) {
+        ks = a.kscale[blk];
+        vs = a.vscale[blk];
+    }
+    const int uk = (a.H + HPW - 1) / HPW, rows = 2 * uk, step = gridDim.y * kWarpsPerCta;
+    for (int r0 = blockIdx.y * kWarpsPerCta + warp; r0 < rows; r0 += step * UNROLL) {
+        uint4 x[UNROLL], y[UNROLL];
+        #pragma unroll
+        for (int j = 0; j < UNROLL; ++j) {
+            const int r = r0 + j * step;
+            const bool is_v = r >= uk;
+            const int h = (is_v ? r - uk : r) * HPW + sub;
+            if (r >= rows || h >= a.H) continue;
+            load_stored<D, POOL>((is_v ? a.vpool : a.kpool) + (blk * a.H + h) * static_cast<int64_t>(a.B) * ROW, off,
+                                 unit, is_v, x[j], y[j]);
+        }
+        #pragma unroll
+        for (int j = 0; j < UNROLL; ++j) {
+            const int r = r0 + j * step;
+            const bool is_v = r >= uk;
+            const int h = (is_v ? r - uk : r) * HPW + sub;
+            if (r >= rows || h >= a.H) continue;
+            char* out = (is_v ? a.v : a.k) + ((tok * a.H + h) * D + unit * 8) * static_cast<int64_t>(sizeof(TOut));
+            float f[8];
+            if constexpr (POOL == KV_F32) {
+                __stcs(reinterpret_cast<uint4*>(out), x[j]);
+                __stcs(reinterpret_cast<uint4*>(out) + 1, y[j]);
+                continue;
+            } else if constexpr (POOL == KV_F16) {
+                if constexpr (sizeof(TOut) == 2) {
+                    __stcs(reinterpret_cast<uint4*>(out), x[j]);
+                    continue;
+                } else {
+                    Raw<__half> raw;
+                    raw.a = x[j];
+                    widen(raw, f);
+                }
+            } else if constexpr (POOL == KV_FP8_E4M3) {
+                const float sc = is_v ? vs : ks;
+                const uint32_t w[2] = {x[j].x, x[j].y};
+                #pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 e = e4m3x2_to_float2(static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1))));
+                    f[2 * i] = e.x * sc;
+                    f[2 * i + 1] = e.y * sc;
+                }
+            } else {
+                const float sc = int4_scale_value(x[j].y);
+                #pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    f[i] = static_cast<float>(static_cast<int>((x[j].x >> (4 * i)) & 15u) - 8) * sc;
+            }
+            if constexpr (sizeof(TOut) == 2) {
+                __stcs(reinterpret_cast<uint4*>(out), halves(f));
+            } else {
+                __stcs(reinterpret_cast<float4*>(out), make_float4(f[0], f[1], f[2], f[3]));
+                __stcs(reinterpret_cast<float4*>(out) + 1, make_float4(f[4], f[5], f[6], f[7]));
+            }
+        }
+    }
+}
+
+template <kv_dtype POOL, typename TOut>
+void gather_typed(const kv_pool* pool, const GatherArgs& a, cudaStream_t stream) {
+    const int D = pool->desc.head_dim;
+    const int hpw = 16 / (D / 8), rows = 2 * ((a.H + hpw - 1) / hpw), pairs = (a.n + 1) / 2;
+    const int most = (rows + kWarpsPerCta - 1) / kWarpsPerCta;
+    int gy = (8 * pool->num_sms + pairs - 1) / pairs;
+    gy = gy < 1 ? 1 : gy > most ? most : gy;
+    const dim3 grid(static_cast<unsigned>(pairs), static_cast<unsigned>(gy));
+    if (D == 128) gather_kernel<128, POOL, TOut><<<grid, kThreads, 0, stream>>>(a);
+    else gather_kernel<64, POOL, TOut><<<grid, kThreads, 0, stream>>>(a);
+}
+
+}  // namespace
+
+int launch_gather(const kv_pool* pool, int layer, const int64_t* slot_mapping, int num_tokens, void* k_out,
+                  void* v_out, kv_dtype out_dtype, cudaStream_t stream) {
+    const RopeArgs p = pool_side(pool, layer);
+    GatherArgs a{};
+    a.kpool = p.kpool;
+    a.vpool = p.vpool;
+    a.kscale = p.kscale;
+    a.vscale = p.vscale;
+    a.slots = slot_mapping;
+    a.k = static_cast<char*>(k_out);
+    a.v = static_cast<char*>(v_out);
+    a.n = num_tokens;
+    a.H = p.H;
+    a.B = p.B;
+    a.num_slots = p.num_slots;
+    a.err = p.err;
+    const bool half = out_dtype == KV_F16;
+    switch (pool->desc.dtype) {
+        case KV_F32: gather_typed<KV_F32, float>(pool, a, stream); break;
+        case KV_F16: half ? gather_typed<KV_F16, __half>(pool, a, stream) : gather_typed<KV_F16, float>(pool, a, stream); break;
+        case KV_FP8_E4M3:
+            half ? gather_typed<KV_FP8_E4M3, __half>(pool, a, stream) : gather_typed<KV_FP8_E4M3, float>(pool, a, stream);
+            break;
+        default: half ? gather_typed<KV_INT4, __half>(pool, a, stream) : gather_typed<KV_INT4, float>(pool, a, stream);
+    }
+    return cudaGetLastError() == cudaSuccess ? KV_OK : KV_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------- rotation table
+namespace {
+
+// One thread per (position, frequency): the angle, its cosine and sine in 64 bits, rounded once.
+// (A float32 angle of position 10^5 would be off by up to 2^-8.)
+__global__ void rope_table_kernel(float* table, int64_t total, int half, double base, double position_scale) {
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+    if (i >= total) return;
+    const int64_t pos = i / half;
+    const int f = static_cast<int>(i - pos * half);
+    const double angle = static_cast<double>(pos) * position_scale * pow(base, -static_cast<double>(f) / half);
+    double sn, cs;
+    sincos(angle, &sn, &cs);
+    float* row = table + pos * 2 * half;
+    row[f] = static_cast<float>(cs);
+    row[half + f] = static_cast<float>(sn);
+}
+
+}  // namespace
+
+int launch_rope_table(float* table, int num_positions, int rot_dim, double base, double position_scale,
+                      cudaStream_t stream) {
+    const int64_t total = static_cast<int64_t>(num_positions) * (rot_dim / 2);
+    rope_table_kernel<<<static_cast<unsigned>((total + 255) / 256), 256, 0, stream>>>(table, total, rot_dim / 2, base,
+                                                                                    position_scale);
+    return cudaGetLastError() == cudaSuccess ? KV_OK : KV_ERR_CUDA;
+}
+
+}  // namespace kvp

@@ -1,0 +1,121 @@
+// 4-bit pools (KV_INT4): layout of a (block, head) tile, quantisation and exact expansion.
+//
+// A tile is block_size / 8 octs (8 consecutive tokens each); an oct is 4*D bytes of codes and
+// then one scale byte per token and 16 elements:
+//   K codes   [token][D/2 bytes], element 2i in the low nibble of byte i
+//   K scales  [token][D/16]
+//   V codes   16-bit pieces of 4 elements of one token, element i of a piece at bits 4i:
+//             [chunk of D/8 elements][token / 2][D/32 pieces of the chunk][token % 2]
+//   V scales  [D/16][token]
+// so that in the attention kernel lane (g, t) = (lane / 4, lane % 4) of a warp reads its tensor-
+// core fragments of 8 tokens as one contiguous load at lane * D/8: of K, token g's elements
+// [t*D/4, (t+1)*D/4); of V, elements [g*D/8, (g+1)*D/8) of tokens 2t and 2t+1, the two tokens'
+// elements side by side as the halves of a 32-bit word.
+//
+// value = code * scale, code = nibble - 8 in -7 .. 7.  The scale byte is an unsigned float of 5
+// exponent and 3 mantissa bits with float16's exponent bias: (byte << 7) is the scale as float16.
+// A scale has 4 significant bits and a code 3, so code * scale is exact in float16; scales stop
+// at 896, which keeps every step of the expansion below in float16's range (|value| <= 6272).
+#pragma once
+
+#include "kvp_internal.cuh"
+
+namespace kvp {
+
+template <int D> struct Int4 {
+    static constexpr int OCT = 4 * D + D / 2;          // bytes of 8 tokens of one head
+    static constexpr int CODES = 4 * D;                // the scales follow the codes
+    static constexpr int WORDS = D / 32;               // 32-bit words per lane and oct
+};
+
+#ifdef __CUDACC__
+
+constexpr float kInt4MaxScale = 896.f;
+constexpr uint32_t kInt4NanScale = 0xFFu;              // 0x7F80 as float16: NaN
+
+// max that returns NaN when either operand is NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// Scale byte of a group whose largest magnitude is amax: min(amax / 7, 896) rounded to nearest
+// even on the byte's grid.  A NaN in the group makes the whole group NaN.
+__device__ __forceinline__ uint32_t int4_scale_byte(float amax) {
+    if (!(amax == amax)) return kInt4NanScale;
+    const float s = fminf(__fdiv_rn(amax, 7.f), kInt4MaxScale);
+    if (s < 6.103515625e-05f) return __float2uint_rn(s * 131072.f);     // below 2^-14: multiples of 2^-17
+    const uint32_t b = __float_as_uint(s);
+    return ((b + 0x7FFFFu + ((b >> 20) & 1u)) >> 20) - ((127u - 15u) << 3);
+}
+
+__device__ __forceinline__ float int4_scale_value(uint32_t byte) {
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(byte << 7)));
+}
+
+// Nibble (code + 8) of x: x / s rounded to nearest even, within -7 .. 7.  inv = 1 / s rounded (0
+// when s is 0: code 0), top = 7 s (exact): larger magnitudes, infinities among them, are that
+// code.  q = x * inv is off by at most two roundings; the residual x - q*s is exact in one fma,
+// and adding residual * inv gives the exact quotient wherever that is a float, so quotients
+// halfway between two codes (common for float16 inputs) round as x / s does.  Residual correction
+// of a quotient by fma: P. Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990.
+__device__ __forceinline__ uint32_t int4_nibble(float x, float s, float inv, float top) {
+    x = fminf(fmaxf(x, -top), top);
+    float q = x * inv;
+    q = fmaf(fmaf(-q, s, x), inv, q);
+    // 1.5 * 2^23 + 8 + q rounds q to an integer (the offset is even) held in the low bits
+    return __float_as_uint(q + 12582920.f) & 15u;
+}
+
+__device__ __forceinline__ float int4_inverse(float s) { return s > 0.f ? __fdiv_rn(1.f, s) : 0.f; }
+
+// Expansion of the 8 nibbles of a word to four float16 pairs, exact: a nibble under the mantissa
+// of 1024.0 is 1024 + u (low nibble) or 1024 + 16 u, and one fma with a16 = scale / 16 and
+// c0 = -1032 a16 or c1 = -1152 a16 gives code * scale / 16 or code * scale (every product and
+// sum has at most 11 significant bits: 1032 = 129 * 8 times a 4-bit scale is at most 129 * 15 < 2^11).
+// p[0] holds nibbles 0 and 4, p[1] nibbles 1 and 5, p[2] nibbles 2 and 6, p[3] nibbles 3 and 7;
+// p[0] and p[2] are a sixteenth of their values, which the callers make up for.
+struct Int4Scale { __half2 a16, c0, c1; };
+
+__device__ __forceinline__ Int4Scale int4_scale_pair(uint32_t half2_bits) {   // the scales as two float16
+    Int4Scale r;
+    r.a16 = __hmul2(*reinterpret_cast<const __half2*>(&half2_bits), __float2half2_rn(0.0625f));
+    r.c0 = __hmul2(r.a16, __float2half2_rn(-1032.f));
+    r.c1 = __hmul2(r.a16, __float2half2_rn(-1152.f));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t int4_pair(uint32_t masked, const __half2 a, const __half2 c) {
+    const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&masked), a, c);
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+__device__ __forceinline__ void int4_expand(uint32_t w, const Int4Scale& s, uint32_t (&p)[4]) {
+    constexpr uint32_t kMagic = 0x64006400u;           // 1024.0 twice
+    p[0] = int4_pair((w & 0x000F000Fu) | kMagic, s.a16, s.c0);
+    p[1] = int4_pair((w & 0x00F000F0u) | kMagic, s.a16, s.c1);
+    w >>= 8;
+    p[2] = int4_pair((w & 0x000F000Fu) | kMagic, s.a16, s.c0);
+    p[3] = int4_pair((w & 0x00F000F0u) | kMagic, s.a16, s.c1);
+}
+
+// Byte offsets inside an oct.
+template <int D> __device__ __forceinline__ int int4_k_code(int token, int element) {      // of a byte of 2
+    return token * (D / 2) + element / 2;
+}
+template <int D> __device__ __forceinline__ int int4_k_scale(int token, int element) {
+    return Int4<D>::CODES + token * (D / 16) + element / 16;
+}
+template <int D> __device__ __forceinline__ int int4_v_piece(int token, int element) {     // of a piece of 4
+    const int chunk = element / (D / 8), w = element % (D / 8) / 4;
+    return (((chunk * 4 + token / 2) * (D / 32) + w) * 2 + (token & 1)) * 2;
+}
+template <int D> __device__ __forceinline__ int int4_v_scale(int token, int element) {
+    return Int4<D>::CODES + (element / 16) * 8 + token;
+}
+
+#endif  // __CUDACC__
+
+}  // namespace kvp

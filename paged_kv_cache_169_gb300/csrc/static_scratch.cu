@@ -16,7 +16,7 @@
 
 #include <mutex>
 
-#include "kvp_internal.cuh"
+#include "pool_types.cuh"
 
 namespace {
 
@@ -97,12 +97,12 @@ extern "C" int paged_decode_attention_static(kv_pool* pool, int layer, const voi
     if (cudaGetDevice(&dev) != cudaSuccess) return KV_ERR_CUDA;
     if (dev != pool->device) return KV_ERR_INVALID_ARG;      // the pool's device must be current
     kvp::AttnPlan plan;
-    int rc = kvp::plan_attention(pool, batch, max_context, partition_tokens, &plan);
+    int rc = kvp::plan_decode(pool, batch, max_context, partition_tokens, &plan);
     if (rc != KV_OK) return rc;
     if (plan.ws_bytes > KV_STATIC_SCRATCH_BYTES) return KV_ERR_INVALID_ARG;   // does not fit
     void* scratch = nullptr;
     rc = scratch_address(dev, &scratch);
     if (rc != KV_OK) return rc;
-    return kvp::launch_attention(pool, layer, q, out, block_tables, max_blocks_per_seq, context_lens,
-                                 batch, max_context, scale, plan, scratch, stream);
+    return kvp::launch_decode(pool, layer, q, nullptr, nullptr, 0, out, block_tables, max_blocks_per_seq,
+                              context_lens, batch, max_context, scale, plan, scratch, stream);
 }
