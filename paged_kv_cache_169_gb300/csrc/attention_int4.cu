@@ -3,7 +3,7 @@
 //
 // Per 16 tokens and K/V head, with the tokens (and the output's elements) as the M side of
 // mma.m16n8k16 and the query heads as its N side:
-//   S^T  = K Q^T        A = K expanded in registers, B = the query rows (fragments kept per item)
+//   S^T  = K Q^T        A = K expanded in registers, B = the query rows
 //   softmax             fp32, log2 domain, running maximum raised only when exceeded by 8
 //   O^T += V^T P^T      A = V^T expanded in registers, B = P^T from the S accumulators
 //                       (movmatrix)
@@ -12,14 +12,20 @@
 // weights at no further mma; 8 query heads fill all columns and p is rounded to float16 once
 // (relative 2^-11, as in the other pools' tensor-core consumer).  All sums are float32.
 //
-// The pool's tile layout (int4.cuh) makes a lane's fragments of 8 tokens one 16-byte load, so the
-// data goes from global memory straight to registers: no shared-memory ring, barriers or copies
-// (a 16-token tile of one head is 1152 bytes, and every bulk copy costs the SM 80-100 cycles
-// whatever its size).  The K words of the next 32 tokens are loaded as soon as those of this
-// chunk are multiplied, the V words likewise, so one of the two is always in flight.
+// Every warp works alone: it claims items, copies its own chunks with cp.async into two stages of
+// its own in shared memory and multiplies them, with no producer warp and no barrier.  (A 16-token tile of
+// one head is 1152 bytes, and every bulk copy costs the SM 80-100 cycles whatever its size; a
+// 16-byte cp.async per lane moves 512 bytes of a warp's own choosing.)  The tile layout (int4.cuh)
+// makes a lane's fragments of 8 tokens the 16 bytes that the same lane copied.
 //
-// Bound: HBM reads of 9/16 byte per element of K and V; the expansion costs 9 instructions per 8
-// elements and lane.
+// Work: the launch's chunks of 32 tokens, over all (sequence, head) units one after the other (each
+// unit counting kUnitCost chunks more), are cut into equal ranges, one per warp, neighbouring
+// ranges in one CTA, so every warp ends at the same time whatever the lengths.  A range holds the
+// end of one unit, whole units, and the start of another.  A CTA joins the parts of its warps in
+// shared memory; what crosses CTAs goes through (m, l, o) parts in the workspace, merged by the
+// CTA that finishes last, in two levels when there are more than kMergeFan.  (Items of at most P
+// tokens claimed one by one, as in attention_kernel.cuh, cost 2.4 us of a warp each here, against
+// 1.7 us per chunk: a claim's and the queries' round trips, the fence before the ticket.)
 
 #include "attention_kernel.cuh"
 #include "int4.cuh"
@@ -28,37 +34,74 @@
 namespace kvp {
 namespace {
 
-constexpr int kWarps = 8, kCtasPerSm = 2;
+constexpr int kCtasPerSm = 2;
+// 8 query heads hold two columns of state per lane and need more than 128 registers
+template <int G> constexpr int kWarps = G == 8 ? 6 : 8;
+constexpr int kUnitCost = 2;                       // chunks that beginning and ending a unit costs a warp
+constexpr int kChunk = 32, kOcts = kChunk / 8;         // tokens and octs per chunk: one softmax update
+static_assert(32 % kOcts == 0, "a chunk's octs lie in one window of 32 oct ids");
+
+// An item: a unit's part inside a warp's range.
+struct __align__(16) ItemSlot {
+    int s, h, oct0, lo;                                // sequence, head, first oct, rows before the window
+    int first, last, kind, pad;                        // positions of the unit's first and last chunk; its kind
+};
+// whole unit; a part of a unit that began in an earlier range; the start of one that goes on
+enum : int { WHOLE = 0, LATER = 1, START = 2 };
+
+// A part that a warp holds for its CTA: the unit (-1: none) and its first and last chunk.
+struct __align__(16) Held { int u, first, last, pad; };
+
+// One warp's stage: the chunk's K codes, V codes, then their scales, oct by oct.
+template <int D> struct Stage {
+    static constexpr int CODES = Int4<D>::CODES, SCALES = D / 2;       // bytes per oct
+    static constexpr int V = kOcts * CODES, S = 2 * V;
+    static constexpr int BYTES = S + 2 * kOcts * SCALES;
+};
+
+// Dynamic shared memory, per warp: two stages (at the end the START part's rows), the next item's
+// query rows, two item slots (this item, the next), what is held (LATER, START), their (m, l) and
+// the LATER part's rows.
+template <int D, int G> struct Smem {
+    static constexpr int RING = 2 * Stage<D>::BYTES, QBYTES = G * D * 2;
+    static constexpr int Q = RING, SLOTS = Q + QBYTES, HELD = SLOTS + 2 * (int)sizeof(ItemSlot);
+    static constexpr int ML = HELD + 2 * (int)sizeof(Held), ROWS = (ML + 2 * G * 8 + 15) / 16 * 16;
+    static constexpr int WARP = ROWS + G * D * 4;
+    static constexpr int BYTES = kWarps<G> * WARP;
+    static_assert(WARP % 16 == 0 && G * D * 4 <= RING, "16-byte alignment; a part fits the stages");
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const char* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// mma_16816 with a zero accumulator
+__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 
 template <int WORDS> struct Words { uint32_t w[WORDS]; };
-
 template <int WORDS>
-__device__ __forceinline__ void load_words(const char* p, Words<WORDS>& x) {
-    if constexpr (WORDS == 4)
-        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(x.w[0]), "=r"(x.w[1]), "=r"(x.w[2]), "=r"(x.w[3]) : "l"(p) : "memory");
-    else
-        asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
-                     : "=r"(x.w[0]), "=r"(x.w[1]) : "l"(p) : "memory");
-}
-__device__ __forceinline__ uint32_t load_u16(const char* p) {
-    unsigned short v;
-    asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p) : "memory");
-    return v;
-}
-__device__ __forceinline__ uint32_t load_u8(const char* p) {
-    uint32_t v;
-    asm volatile("ld.global.u8 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-    return v;
+__device__ __forceinline__ Words<WORDS> lds_words(const char* p) {
+    Words<WORDS> x;
+    if constexpr (WORDS == 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        x.w[0] = v.x; x.w[1] = v.y; x.w[2] = v.z; x.w[3] = v.w;
+    } else {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        x.w[0] = v.x; x.w[1] = v.y;
+    }
+    return x;
 }
 
 // byte b0 (bits 0-7) and b1 (bits 8-15) of x as the float16 pair (scale b0, scale b1)
 __device__ __forceinline__ uint32_t scales_two(uint32_t x) { return __byte_perm(x, 0, 0x4140) << 7; }
-// byte `which` of x as the float16 pair (scale, scale)
-__device__ __forceinline__ uint32_t scales_same(uint32_t x, int which) {
-    return __byte_perm(x, 0, which ? 0x4141 : 0x4040) << 7;
-}
-
 // The newest token of (sequence, head): quantised by the warp (4 elements per lane) into its slot,
 // before the item's loads.
 template <int D>
@@ -87,14 +130,163 @@ __device__ __forceinline__ void append_row(const char* src, int in_bytes, char* 
     }
 }
 
+// What the kernel needs beside AttnArgs.  A unit u that crosses CTAs b0 .. b1 has its part of CTA b
+// in workspace slot b + u (the next unit's first CTA is at least b1 and its index one more: no two
+// units share a slot).
+struct Int4Args {
+    AttnArgs a;
+    int min_range;         // chunks per range, at least
+    unsigned* group_done;  // [slots] parts finished of the group of kMergeFan that starts at a slot
+};
+
+// Lane `sub`'s elements of one row of D, in float4s LPR apart.
+template <int V> struct RowAcc {
+    float m, l;
+    float4 o[V];
+};
+
+template <int LPR, int V>
+__device__ __forceinline__ void store_out(const AttnArgs& a, int64_t row, int D, const RowAcc<V>& x, int sub) {
+    const float inv = 1.f / x.l;
+    const int64_t at = row * (D / 4) + sub;
+    #pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const float4 v = make_float4(x.o[i].x * inv, x.o[i].y * inv, x.o[i].z * inv, x.o[i].w * inv);
+        if (a.out_f16) {                               // rounded once, from the float32 result
+            const __half2 lo = __floats2half2_rn(v.x, v.y), hi = __floats2half2_rn(v.z, v.w);
+            uint2 w;
+            w.x = *reinterpret_cast<const unsigned*>(&lo);
+            w.y = *reinterpret_cast<const unsigned*>(&hi);
+            static_cast<uint2*>(a.out)[at + i * LPR] = w;
+        } else {
+            static_cast<float4*>(a.out)[at + i * LPR] = v;
+        }
+    }
+}
+
+// The parts of one unit that warps w0, w0 + 1, ... of this CTA hold (w0's of kind `kind`, then
+// LATER ones), joined by one warp, all G rows at once.
 template <int D, int G>
-__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attention_int4_kernel(const __grid_constant__ AttnArgs a) {
+__device__ __forceinline__ void join_parts(const AttnArgs& a, char* smem, int w0, int kind, int n, int u, bool whole,
+                                           int lane) {
+    using Sm = Smem<D, G>;
+    constexpr int LPR = 32 / G < D / 4 ? 32 / G : D / 4, V = D / 4 / LPR;
+    const int sub = lane % LPR, r = lane / LPR < G ? lane / LPR : G - 1;
+    auto ml_of = [&](int k) {
+        const int kd = k == 0 ? kind : LATER;
+        return *reinterpret_cast<const float2*>(smem + (w0 + k) * Sm::WARP + Sm::ML + ((kd - 1) * G + r) * 8);
+    };
+    RowAcc<V> x;
+    x.m = -CUDART_INF_F;
+    x.l = 0.f;
+    for (int k = 0; k < n; ++k) x.m = fmaxf(x.m, ml_of(k).x);
+    #pragma unroll
+    for (int i = 0; i < V; ++i) x.o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < n; ++k) {
+        const float2 v = ml_of(k);
+        const float w = ex2_approx(v.x - x.m);
+        x.l = fmaf(v.y, w, x.l);
+        const char* base = smem + (w0 + k) * Sm::WARP + (k == 0 && kind == START ? 0 : Sm::ROWS) + r * D * 4;
+        #pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float4 o = reinterpret_cast<const float4*>(base)[sub + i * LPR];
+            x.o[i].x = fmaf(w, o.x, x.o[i].x);
+            x.o[i].y = fmaf(w, o.y, x.o[i].y);
+            x.o[i].z = fmaf(w, o.z, x.o[i].z);
+            x.o[i].w = fmaf(w, o.w, x.o[i].w);
+        }
+    }
+    if (lane / LPR >= G) return;
+    if (whole) {
+        store_out<LPR, V>(a, static_cast<int64_t>(u) * G + r, D, x, sub);
+    } else {
+        const int64_t row = (static_cast<int64_t>(blockIdx.x) + u) * G + r;
+        if (sub == 0) reinterpret_cast<float2*>(a.part_ml)[row] = make_float2(x.m, x.l);
+        #pragma unroll
+        for (int i = 0; i < V; ++i) reinterpret_cast<float4*>(a.part_o + row * D)[sub + i * LPR] = x.o[i];
+    }
+}
+
+// Row r of the `count` parts `stride` slots apart from `slot` on, by one warp, read through L2 (they
+// were written by other SMs): into the output (`last`), else into the first part's slot.
+template <int D, int G>
+__device__ __forceinline__ void merge_row(const AttnArgs& a, int64_t slot, int count, int stride, int64_t u, int r, bool last,
+                                          int lane) {
+    constexpr int LPR = D / 4;
+    const int sub = lane % LPR;                        // D 64: both half-warps do the same
+    const int64_t row = slot * G + r, step = static_cast<int64_t>(stride) * G;
+    const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + row;
+    float4* po = reinterpret_cast<float4*>(a.part_o + row * D) + sub;
+    RowAcc<1> x;
+    x.m = -CUDART_INF_F;
+    x.l = 0.f;
+    x.o[0] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = lane; k < count; k += 32) x.m = fmaxf(x.m, __ldcg(ml + k * step).x);
+    x.m = warp_max(x.m);
+    #pragma unroll 8
+    for (int k = 0; k < count; ++k) {
+        const float2 v = __ldcg(ml + k * step);
+        const float4 o = __ldcg(po + k * step * (D / 4));
+        const float w = ex2_approx(v.x - x.m);
+        x.l = fmaf(v.y, w, x.l);
+        x.o[0].x = fmaf(w, o.x, x.o[0].x);
+        x.o[0].y = fmaf(w, o.y, x.o[0].y);
+        x.o[0].z = fmaf(w, o.z, x.o[0].z);
+        x.o[0].w = fmaf(w, o.w, x.o[0].w);
+    }
+    __syncwarp();                                      // every lane has read the first part
+    if (lane >= LPR) return;
+    if (last) {
+        store_out<LPR, 1>(a, u * G + r, D, x, sub);
+    } else {
+        if (sub == 0) reinterpret_cast<float2*>(a.part_ml)[row] = make_float2(x.m, x.l);
+        po[0] = x.o[0];
+    }
+}
+
+// The CTA's part of unit u (CTAs b0 .. b1) is in the workspace: count it, and merge what it
+// completes, a warp per row.  Called by every thread.
+template <int D, int G>
+__device__ __forceinline__ void finish_part(const Int4Args& x, int u, int b0, int b1, unsigned* s_prev) {
+    const AttnArgs& a = x.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int parts = b1 - b0 + 1, part = blockIdx.x - b0;
+    const int64_t slot = static_cast<int64_t>(b0) + u;
+    auto count_one = [&](unsigned* ctr, int of) {      // true in the CTA that finishes the last of `of`
+        __syncthreads();                               // every warp's rows are written
+        if (threadIdx.x == 0) {
+            const unsigned prev = atom_add_acq_rel_gpu(ctr, 1u);
+            if (prev == static_cast<unsigned>(of - 1)) *ctr = 0;       // left zero for the next call
+            *s_prev = prev;
+        }
+        __syncthreads();
+        return *s_prev == static_cast<unsigned>(of - 1);
+    };
+    if (parts > kMergeFan) {
+        const int first = part / kMergeFan * kMergeFan, size = min(kMergeFan, parts - first);
+        if (!count_one(x.group_done + slot + first, size)) return;
+        for (int r = warp; r < G; r += kWarps<G>) merge_row<D, G>(a, slot + first, size, 1, u, r, false, lane);
+    }
+    const int count = parts > kMergeFan ? (parts + kMergeFan - 1) / kMergeFan : parts;
+    if (!count_one(a.arrivals + u, count)) return;
+    for (int r = warp; r < G; r += kWarps<G>)
+        merge_row<D, G>(a, slot, count, parts > kMergeFan ? kMergeFan : 1, u, r, true, lane);
+}
+
+template <int D, int G>
+__global__ void __launch_bounds__(kWarps<G> * 32, kCtasPerSm) attention_int4_kernel(const __grid_constant__ Int4Args args) {
+    const AttnArgs& a = args.a;
     constexpr int WORDS = Int4<D>::WORDS, OCT = Int4<D>::OCT;
-    constexpr int KS = D / 16, MT = D / 16;            // k-steps over the elements; output tiles
+    constexpr int MT = D / 16;                         // output tiles of 16 elements
     constexpr bool SPLIT = G <= 4;                     // odd columns: the weights' rounding errors
     constexpr int NQ = SPLIT ? 1 : 2;                  // query columns per lane
-    constexpr int CT = 32, NO = CT / 8;                // tokens and octs per chunk
-    __shared__ int s_ctx[kMaxBatch], s_end[kMaxBatch], s_P;
+    constexpr int CT = kChunk, NO = kOcts, NW = kWarps<G>;
+    using St = Stage<D>;
+    using Sm = Smem<D, G>;
+    extern __shared__ __align__(128) char smem[];
+    __shared__ int s_ctx[kMaxBatch], s_end[kMaxBatch];
+    __shared__ Held s_cross[2];                        // the CTA's units that cross CTAs, with their CTAs
+    __shared__ unsigned s_prev;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
 
     const bool early = a.early_tables != 0;
@@ -102,8 +294,12 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attention_int4_kernel
         asm volatile("griddepcontrol.wait;" ::: "memory");
         if (tid == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     }
-    // ---- the launch's work list: items per sequence, inclusive prefix (as attention_kernel.cuh)
-    for (int s = tid; s < a.batch; s += kWarps * 32) {
+    // ---- chunks per (sequence, head) and their inclusive prefix over the launch's units
+    auto chunks_of = [&](int ctx) {
+        const int n = ctx - attend_first(ctx, a.window, 8);
+        return n > 0 ? (n + CT - 1) / CT : 1;          // an empty sequence: one chunk without tokens
+    };
+    for (int s = tid; s < a.batch; s += NW * 32) {
         int c = a.lens[s];
         if (c < 0 || c > a.ctx_limit) {
             if (blockIdx.x == 0) atomicOr(a.err, KV_DEVERR_CONTEXT);
@@ -113,20 +309,10 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attention_int4_kernel
     }
     __syncthreads();
     if (warp == 0) {
-        int P = a.P;
-        if (a.P_alt < a.P) {                           // a finer split that still fits one round of items
-            int alt = 0;
-            for (int s = lane; s < a.batch; s += 32)
-                alt += a.H * nparts_of(s_ctx[s] - attend_first(s_ctx[s], a.window, 8), a.P_alt);
-            if (__reduce_add_sync(FULL, alt) <= static_cast<int>(gridDim.x) * kWarps) P = a.P_alt;
-        }
         int carry = 0;
         for (int base = 0; base < a.batch; base += 32) {
             const int s = base + lane;
-            int v = 0;
-            if (s < a.batch)
-                v = a.H * nparts_of(s_ctx[s] - attend_first(s_ctx[s], a.window, 8),
-                                    P == a.P ? part_of(P, a, s) : P);
+            int v = s < a.batch ? a.H * (chunks_of(s_ctx[s]) + kUnitCost) : 0;
             #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int n = __shfl_up_sync(FULL, v, o);
@@ -136,262 +322,302 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attention_int4_kernel
             if (s < a.batch) s_end[s] = v;
             carry = __shfl_sync(FULL, v, 31);
         }
-        if (lane == 0) s_P = P;
     }
     __syncthreads();
-    const int n_items = s_end[a.batch - 1];
-    const int P_eff = s_P;
-    // with the finer split every sequence takes it
-    const int s_fine = P_eff == a.P ? a.s_fine : a.batch;
+    const int total = s_end[a.batch - 1];
+    // ranges: at most one per warp and of min_range chunks at least; k warps of every CTA have one, range
+    // r being chunks [r * total / ranges, (r + 1) * total / ranges)
+    const int grid = static_cast<int>(gridDim.x);
+    const int want = max(total / args.min_range, 1);
+    const int k = min((want + grid - 1) / grid, NW);
+    const int ranges = min(want, k * grid);
+    auto range_of = [&](int chunk) { return static_cast<int>(((chunk + int64_t{1}) * ranges - 1) / total); };
     if (early) {
         asm volatile("griddepcontrol.wait;" ::: "memory");
         if (tid == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     }
 
+    char* const ring = smem + warp * Sm::WARP;
+    char* const s_q = ring + Sm::Q;
+    ItemSlot* const slots = reinterpret_cast<ItemSlot*>(ring + Sm::SLOTS);
+    Held* const held = reinterpret_cast<Held*>(ring + Sm::HELD);
+    if (lane < 2) held[lane].u = -1;
     const int opb = a.B >> 3;                          // octs per (block, head) tile
     const int lg_opb = __ffs(opb) - 1;
-    const unsigned first_claim = gridDim.x * kWarps;
-    unsigned pending = 0;                              // lane 0: the claimed next item (atomic in flight)
-    bool claimed = false;
 
-    // load side: the item whose chunk is loaded next; oct ids of its current and next 32 octs
-    Item L{};
-    int Lc = 0, Lo0 = 0, Lno = 0;
-    int oid = 0, oid_next = 0;
-    const char *kp = nullptr, *vp = nullptr;           // this lane's words of oct 0 of the item's head
-    auto load_oids = [&](int base) -> int {            // global index of oct base + lane of the item
-        const int i = min(base + lane, Lno - 1);
-        if (i < 0) return 0;
-        const int o = Lo0 + i;
-        int id = a.tables[static_cast<int64_t>(L.s) * a.max_blocks + (o >> lg_opb)];
+    // Global ids of octs o0 + lane (of n left) of an item; lanes past the end repeat the last.
+    auto load_oids = [&](int s, int h, int o0, int n) -> int {
+        const int o = o0 + min(lane, n - 1);
+        int id = a.tables[static_cast<int64_t>(s) * a.max_blocks + (o >> lg_opb)];
         if (id < 0 || id >= a.num_blocks) {
             atomicOr(a.err, KV_DEVERR_BLOCK_ID);
             id = 0;
         }
-        return (id * a.H << lg_opb) + (o & (opb - 1));
+        return ((id * a.H + h) << lg_opb) + (o & (opb - 1));
     };
-    auto begin_item = [&](unsigned idx) {
-        L = decode_item<CT>(static_cast<int>(idx), n_items, s_ctx, s_end, a.batch, a.H, P_eff, s_fine, a.P_fine,
-                            a.window, 8);
-        Lc = 0;
-        if (!L.valid) return;
-        Lo0 = L.tok0 >> 3;
-        Lno = (L.ntok + 7) >> 3;
-        const int64_t head = static_cast<int64_t>(L.h) * opb * OCT;
-        kp = a.kpool + head + lane * (4 * WORDS);
-        vp = a.vpool + head + lane * (4 * WORDS);
-        if (a.k_new != nullptr && L.last && L.ntok > 0) {
-            // fused append: the newest token goes to its slot before the item's loads
-            const int tok = s_ctx[L.s] - 1, o = tok >> 3;
-            int id = a.tables[static_cast<int64_t>(L.s) * a.max_blocks + (o >> lg_opb)];
-            if (id < 0 || id >= a.num_blocks) id = 0;  // flagged by load_oids
-            const int64_t at = (((static_cast<int64_t>(id) * a.H + L.h) << lg_opb) + (o & (opb - 1))) * OCT;
-            const int64_t row = (static_cast<int64_t>(L.s) * a.H + L.h) * D * a.in_bytes;
-            append_row<D>(a.k_new + row, a.in_bytes, a.kpool + at, tok & 7, true, lane);
-            append_row<D>(a.v_new + row, a.in_bytes, a.vpool + at, tok & 7, false, lane);
-            __syncwarp();                              // the warp's loads below see the row
+    // Copy nt tokens (octs w .. of the id window) into a stage.  Octs past nt are not copied: what
+    // the stage holds there is masked.
+    constexpr int PPO = St::CODES / 16, SPO = St::SCALES / 16;         // 16-byte pieces of an oct: 32, 4 or 16, 2
+    const char* const kbase = a.kpool + lane % PPO * 16;
+    const char* const vbase = a.vpool + lane % PPO * 16;
+    const char* const sbase = (lane < NO * SPO ? a.kpool : a.vpool) + St::CODES + lane % SPO * 16;
+    const uint32_t ring32 = smem_u32(ring) + lane * 16;
+    auto copy = [&](int stage, int oids, int w, int nt) {
+        const uint32_t dst = ring32 + stage * St::BYTES;
+        #pragma unroll
+        for (int j = 0; j < NO * PPO / 32; ++j) {
+            const int i = j * 32 / PPO + lane / PPO;
+            const int64_t at = static_cast<int64_t>(__shfl_sync(FULL, oids, w + i)) * OCT;
+            if (i * 8 < nt) {
+                cp_async16(dst + j * 512, kbase + at);
+                cp_async16(dst + St::V + j * 512, vbase + at);
+            }
         }
-        oid = load_oids(0);
-        if (Lno > 32) oid_next = load_oids(32);
+        const int i = lane / SPO % NO;
+        const int64_t at = static_cast<int64_t>(__shfl_sync(FULL, oids, w + i)) * OCT;
+        if (lane < 2 * NO * SPO && i * 8 < nt) cp_async16(dst + St::S, sbase + at);
     };
 
-    Words<WORDS> kw[NO], vw[NO];
-    uint32_t ksc[NO], vsc[NO];
-    int oc[NO];                                        // oct indices of the loaded chunk
-    // lane offsets of the scales from the lane's words
-    const int ks_off = OCT - D / 2 - lane * (4 * WORDS) + (D == 128 ? lane * 2 : lane);
-    const int vs_off = OCT - D / 2 - lane * (4 * WORDS) + (D == 128 ? g : g >> 1) * 8 + 2 * t;
-    auto load_k = [&]() {
-        const int w = (Lc * NO) & 31;
-        if (w == 0 && Lc > 0) {                        // the next 32 octs
-            oid = oid_next;
-            if (Lc * NO + 32 < Lno) oid_next = load_oids(Lc * NO + 32);
-        }
-        #pragma unroll
-        for (int j = 0; j < NO; ++j) {
-            oc[j] = __shfl_sync(FULL, oid, w + j);
-            const char* p = kp + static_cast<int64_t>(oc[j]) * OCT;
-            load_words<WORDS>(p, kw[j]);
-            ksc[j] = D == 128 ? load_u16(p + ks_off) : load_u8(p + ks_off);
-        }
-    };
-    auto load_v = [&]() {
-        #pragma unroll
-        for (int j = 0; j < NO; ++j) {
-            const char* p = vp + static_cast<int64_t>(oc[j]) * OCT;
-            load_words<WORDS>(p, vw[j]);
-            vsc[j] = load_u16(p + vs_off);
-        }
-    };
-    // B fragments of Q^T, in the order the K words expand: k-step 2w takes elements (0, 4) and
-    // (1, 5) of word w, k-step 2w+1 elements (2, 6) and (3, 7).  The pairs of the odd elements
-    // meet full K values, those of the even ones a sixteenth: the odd elements' query values are
-    // divided by 16 (exact unless below 2^-10, then off by at most 2^-25) and the score times 16.
-    uint32_t qa[KS][2];
-    auto load_q = [&]() {
-        const int col = SPLIT ? g >> 1 : g;            // query of column g (odd columns: none)
-        const bool real = (SPLIT ? (g & 1) == 0 : true) && col < G && L.ntok > 0;
-        const __half* qrow = static_cast<const __half*>(a.q) +
-                             ((static_cast<int64_t>(L.s) * a.H + L.h) * G + (real ? col : 0)) * D + t * (D / 4);
-        #pragma unroll
-        for (int w = 0; w < WORDS; ++w) {
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (real) x = *reinterpret_cast<const uint4*>(qrow + 8 * w);
-            const uint32_t e04 = __byte_perm(x.x, x.z, 0x5410), e15 = __byte_perm(x.x, x.z, 0x7632);
-            const uint32_t e26 = __byte_perm(x.y, x.w, 0x5410), e37 = __byte_perm(x.y, x.w, 0x7632);
-            const __half2 r = __float2half2_rn(0.0625f);
-            const __half2 b0 = __hmul2(*reinterpret_cast<const __half2*>(&e15), r);
-            const __half2 b1 = __hmul2(*reinterpret_cast<const __half2*>(&e37), r);
-            qa[2 * w][0] = e04;
-            qa[2 * w][1] = *reinterpret_cast<const uint32_t*>(&b0);
-            qa[2 * w + 1][0] = e26;
-            qa[2 * w + 1][1] = *reinterpret_cast<const uint32_t*>(&b1);
-        }
-    };
-
+    const int64_t rng = static_cast<int64_t>(blockIdx.x) * k + warp;
+    const bool works = warp < k && rng < ranges;
+    int pos = works ? static_cast<int>(rng * total / ranges) : 0;      // first chunk not yet taken
+    const int end = works ? static_cast<int>((rng + 1) * total / ranges) : 0;
+    const float xs = a.qscale * 16.f, slack = fminf(8.f / xs, 1e30f);
+    const int col = SPLIT ? g >> 1 : g;                // query of mma column g (odd columns of SPLIT: none)
+    const bool has_q = !(SPLIT && (g & 1)) && col < G;
     float ot[MT][4];
     float m[NQ], l[NQ];
-    Ticket tk{};
-    const float xs = a.qscale * 16.f;
+    uint32_t qa[2 * WORDS][2];                         // B fragments of Q^T
 
-    begin_item(warp * gridDim.x + blockIdx.x);
-    if (L.valid) {
-        load_q();
-        if (L.ntok > 0) {
-            load_k();
-            load_v();
-        }
-    }
-    while (L.valid) {
-        const int c = Lc, nch = L.nchunks;
-        const int nt = min(CT, L.ntok - c * CT), lo = c == 0 ? L.lo : 0;
-        const int is = L.s, ih = L.h, ip = L.p;
-        const bool single = L.single, last = c == nch - 1;
-        if (c == 0) {
+    // The loop runs one chunk ahead of itself: chunk c + 1 of the item (or chunk 0 of the next) is
+    // copied while chunk c is multiplied.  It starts on an item without tokens or result.
+    int ntok = 0, lo = 0, cur = 1, stage = 1;          // this item's tokens, masked rows, slot; the stage in use
+    int oid = 0, oid_next = 0;                         // oct ids of the item's current and next 32 octs
+    for (bool started = false;; started = true) {
+        if (started) {
+            // Query fragments in the order the K words expand: k-step 2w takes elements (0, 4) and
+            // (1, 5) of word w, k-step 2w+1 elements (2, 6) and (3, 7).  The pairs of the odd
+            // elements meet full K values, those of the even ones a sixteenth: the odd elements'
+            // query values are divided by 16 (exact unless below 2^-10, then off by at most
+            // 2^-25) and the score times 16.
+            cp_async_wait();                           // the rows came with the item's first chunk
+            __syncwarp();
+            #pragma unroll
+            for (int w = 0; w < WORDS; ++w) {
+                uint4 x = make_uint4(0, 0, 0, 0);
+                if (has_q) x = *reinterpret_cast<const uint4*>(s_q + (col * D + t * (D / 4) + 8 * w) * 2);
+                const uint32_t e15 = __byte_perm(x.x, x.z, 0x7632), e37 = __byte_perm(x.y, x.w, 0x7632);
+                const __half2 f = __float2half2_rn(0.0625f);
+                const __half2 b0 = __hmul2(*reinterpret_cast<const __half2*>(&e15), f);
+                const __half2 b1 = __hmul2(*reinterpret_cast<const __half2*>(&e37), f);
+                qa[2 * w][0] = __byte_perm(x.x, x.z, 0x5410);
+                qa[2 * w][1] = *reinterpret_cast<const uint32_t*>(&b0);
+                qa[2 * w + 1][0] = __byte_perm(x.y, x.w, 0x5410);
+                qa[2 * w + 1][1] = *reinterpret_cast<const uint32_t*>(&b1);
+            }
+            __syncwarp();                              // the next item's rows may follow now
             #pragma unroll
             for (int q = 0; q < NQ; ++q) { m[q] = -CUDART_INF_F; l[q] = 0.f; }
             #pragma unroll
             for (int i = 0; i < MT; ++i) { ot[i][0] = ot[i][1] = ot[i][2] = ot[i][3] = 0.f; }
         }
-        // ---- S^T = K Q^T for two steps of 16 tokens
-        float x[2][2 * NQ];                            // [step][token g, token g + 8] (x query columns)
-        if (nt > 0) {
-            #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
-                #pragma unroll
-                for (int h = 0; h < 2; ++h) {          // the lane's two scale groups (D 64: one)
-                    if (D == 64 && h == 1) continue;
-                    const Int4Scale s0 = int4_scale_pair(scales_same(ksc[2 * u], h));
-                    const Int4Scale s1 = int4_scale_pair(scales_same(ksc[2 * u + 1], h));
+        int next_tok = -1, next_oid = 0, next_oid2 = 0;
+        bool prepared = false;
+        #pragma unroll 1
+        for (int tok = 0;; tok += CT) {
+            const int nt = ntok - tok;                 // tokens from this chunk on
+            if (nt <= 2 * CT && !prepared) {
+                // the item's last chunk but one: find the next item, fetch its oct ids and queries
+                prepared = true;
+                int s = 0, h = 0, ctx = 0, cps = 0, unit = 0, c0 = 0, n = 0;
+                if (pos < end) {
+                    int hi_s = a.batch - 1;            // first sequence that ends after pos
+                    while (s < hi_s) {
+                        const int mid = (s + hi_s) >> 1;
+                        if (s_end[mid] > pos) hi_s = mid; else s = mid + 1;
+                    }
+                    ctx = s_ctx[s];
+                    cps = chunks_of(ctx);
+                    const int start = s ? s_end[s - 1] : 0;
+                    h = (pos - start) / (cps + kUnitCost);
+                    unit = start + h * (cps + kUnitCost) + kUnitCost;  // the unit's first chunk
+                    c0 = max(pos - unit, 0);
+                    n = min(cps - c0, end - unit - c0);                // <= 0: the range ends before that
+                    pos = n > 0 ? unit + c0 + n : end;
+                }
+                if (n > 0) {
+                    const int tok0 = attend_first(ctx, a.window, 8) + c0 * CT;
+                    next_tok = max(min(n * CT, ctx - tok0), 0);
+                    if (lane == 0) {
+                        ItemSlot* it = slots + (cur ^ 1);
+                        *reinterpret_cast<int4*>(&it->s) =
+                            make_int4(s, h, tok0 >> 3, c0 == 0 ? attend_start(ctx, a.window) - tok0 : 0);
+                        *reinterpret_cast<int4*>(&it->first) =
+                            make_int4(unit, unit + cps - 1, c0 > 0 ? LATER : n < cps ? START : WHOLE, 0);
+                    }
+                    if (a.k_new != nullptr && c0 + n == cps && ctx > 0) {
+                        // fused append: the newest token goes to its slot before the item's copies
+                        const int last = ctx - 1, o = last >> 3;
+                        int id = a.tables[static_cast<int64_t>(s) * a.max_blocks + (o >> lg_opb)];
+                        if (id < 0 || id >= a.num_blocks) id = 0;      // flagged by load_oids
+                        const int64_t to = (((static_cast<int64_t>(id) * a.H + h) << lg_opb) + (o & (opb - 1))) * OCT;
+                        const int64_t row = (static_cast<int64_t>(s) * a.H + h) * D * a.in_bytes;
+                        append_row<D>(a.k_new + row, a.in_bytes, a.kpool + to, last & 7, true, lane);
+                        append_row<D>(a.v_new + row, a.in_bytes, a.vpool + to, last & 7, false, lane);
+                        __syncwarp();                  // the copies below read the row
+                    }
+                    const char* q = static_cast<const char*>(a.q) + (static_cast<int64_t>(s) * a.H + h) * G * D * 2;
                     #pragma unroll
-                    for (int v = 0; v < 2; ++v) {
-                        const int w = 2 * h + v;
+                    for (int i = 0; i < (Sm::QBYTES / 16 + 31) / 32; ++i)
+                        if (i * 32 + lane < Sm::QBYTES / 16)
+                            cp_async16(smem_u32(s_q) + (i * 32 + lane) * 16, q + (i * 32 + lane) * 16);
+                    const int no = (next_tok + 7) >> 3;
+                    if (no > 0) next_oid = load_oids(s, h, tok0 >> 3, no);
+                    if (no > 32) next_oid2 = load_oids(s, h, (tok0 >> 3) + 32, no - 32);
+                }
+            }
+            cp_async_wait();
+            __syncwarp();                              // every lane's copies of this chunk have landed, and
+                                                       // every lane is done with the other stage
+            if (nt > CT) {
+                const int w = (tok / CT + 1) * NO & 31;
+                if (w == 0) {                          // the next 32 octs
+                    oid = oid_next;
+                    const int ahead = (tok + CT) / 8 + 32, no = (ntok + 7) >> 3;
+                    if (ahead < no) oid_next = load_oids(slots[cur].s, slots[cur].h, slots[cur].oct0 + ahead, no - ahead);
+                }
+                copy(stage ^ 1, oid, w, nt - CT);
+            } else if (next_tok > 0) {
+                copy(stage ^ 1, next_oid, 0, next_tok);
+            }
+            if (nt > 0) {
+                // this lane's words and scales of the stage
+                const char* const pc = ring + stage * St::BYTES + lane * (4 * WORDS);
+                const char* const pk = ring + stage * St::BYTES + St::S + (D == 128 ? lane * 2 : lane);
+                const char* const pv = ring + stage * St::BYTES + St::S + NO * St::SCALES + (D == 128 ? g : g >> 1) * 8 + 2 * t;
+                // ---- S^T = K Q^T, 16 tokens per mma
+                float x[2][2 * NQ];                    // [16 tokens][token g, token g + 8] (x query columns)
+                #pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const Words<WORDS> k0 = lds_words<WORDS>(pc + 2 * u * St::CODES);
+                    const Words<WORDS> k1 = lds_words<WORDS>(pc + (2 * u + 1) * St::CODES);
+                    uint32_t b0, b1;                   // the lane's scales of 16 elements: two, D 64: one
+                    if constexpr (D == 128) {
+                        b0 = *reinterpret_cast<const uint16_t*>(pk + 2 * u * St::SCALES);
+                        b1 = *reinterpret_cast<const uint16_t*>(pk + (2 * u + 1) * St::SCALES);
+                    } else {
+                        b0 = *reinterpret_cast<const uint8_t*>(pk + 2 * u * St::SCALES);
+                        b1 = *reinterpret_cast<const uint8_t*>(pk + (2 * u + 1) * St::SCALES);
+                    }
+                    const Int4Scale f0 = int4_scale_pair(scales_two(b0)), f1 = int4_scale_pair(scales_two(b1));
+                    float acc[4];
+                    #pragma unroll
+                    for (int w = 0; w < WORDS; ++w) {
+                        const Int4Scale s0 = int4_scale_of(f0, w / 2), s1 = int4_scale_of(f1, w / 2);
                         uint32_t p0[4], p1[4];
-                        int4_expand(kw[2 * u].w[w], s0, p0);
-                        int4_expand(kw[2 * u + 1].w[w], s1, p1);
-                        mma_16816(sa, p0[0], p1[0], p0[1], p1[1], qa[2 * w][0], qa[2 * w][1]);
-                        mma_16816(sb, p0[2], p1[2], p0[3], p1[3], qa[2 * w + 1][0], qa[2 * w + 1][1]);
+                        int4_expand(k0.w[w], s0, p0);
+                        int4_expand(k1.w[w], s1, p1);
+                        if (w == 0) mma_first(acc, p0[0], p1[0], p0[1], p1[1], qa[0][0], qa[0][1]);
+                        else mma_16816(acc, p0[0], p1[0], p0[1], p1[1], qa[2 * w][0], qa[2 * w][1]);
+                        mma_16816(acc, p0[2], p1[2], p0[3], p1[3], qa[2 * w + 1][0], qa[2 * w + 1][1]);
+                    }
+                    #pragma unroll
+                    for (int q = 0; q < NQ; ++q) {
+                        x[u][q] = acc[q];
+                        x[u][NQ + q] = acc[2 + q];
                     }
                 }
-                const int t0 = 16 * u + g, t1 = t0 + 8;
-                const bool v0 = t0 >= lo && t0 < nt, v1 = t1 >= lo && t1 < nt;
+                const int first = tok == 0 ? lo : 0;
+                if (nt < CT || first > 0) {            // rows outside [first, nt) may hold anything:
+                    #pragma unroll                     // scores of -inf, and V scales of zero
+                    for (int u = 0; u < 2; ++u) {
+                        const int t0 = 16 * u + g, t1 = t0 + 8;
+                        #pragma unroll
+                        for (int q = 0; q < NQ; ++q) {
+                            if (t0 < first || t0 >= nt) x[u][q] = -CUDART_INF_F;
+                            if (t1 < first || t1 >= nt) x[u][NQ + q] = -CUDART_INF_F;
+                        }
+                    }
+                    if (lane < first || lane >= nt) {  // token `lane` of the chunk: its D/16 scales
+                        char* z = ring + stage * St::BYTES + St::S + (NO + lane / 8) * St::SCALES + lane % 8;
+                        #pragma unroll
+                        for (int i = 0; i < D / 16; ++i) z[8 * i] = 0;
+                    }
+                    __syncwarp();
+                }
+                // ---- softmax over the chunk: m is the running maximum of the raw sums, xs turns
+                // them into log2-domain scores
                 #pragma unroll
                 for (int q = 0; q < NQ; ++q) {
-                    x[u][q] = v0 ? (sa[q] + sb[q]) * xs : -CUDART_INF_F;
-                    x[u][NQ + q] = v1 ? (sa[2 + q] + sb[2 + q]) * xs : -CUDART_INF_F;
+                    float mx = fmaxf(fmaxf(x[0][q], x[0][NQ + q]), fmaxf(x[1][q], x[1][NQ + q]));
+                    if (__any_sync(FULL, mx > m[q] + slack)) {
+                        #pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
+                        const float m_new = fmaxf(m[q], mx), corr = ex2_approx((m[q] - m_new) * xs);
+                        m[q] = m_new;
+                        l[q] *= corr;
+                        #pragma unroll
+                        for (int i = 0; i < MT; ++i) {
+                            ot[i][q] *= corr;
+                            ot[i][2 + q] *= corr;
+                            if (SPLIT) { ot[i][1] *= corr; ot[i][3] *= corr; }
+                        }
+                    }
                 }
-            }
-        }
-        // ---- next chunk: claim, switch items, load K (and the next item's queries)
-        if (nch - 1 - c <= 2 && !claimed) {
-            if (lane == 0) pending = atomicAdd(a.counter, 1u) + first_claim;
-            claimed = true;
-        }
-        if (last) {
-            begin_item(__shfl_sync(FULL, pending, 0));
-            claimed = false;
-            if (L.valid) load_q();
-        } else {
-            ++Lc;
-        }
-        const bool more = L.valid && L.ntok > 0;
-        if (more) {
-            // the V words of this chunk are still needed: their oct indices are not
-            load_k();
-        }
-        if (nt > 0) {
-            // ---- softmax over the chunk
-            #pragma unroll
-            for (int q = 0; q < NQ; ++q) {
-                float mx = fmaxf(fmaxf(x[0][q], x[0][NQ + q]), fmaxf(x[1][q], x[1][NQ + q]));
-                if (__any_sync(FULL, mx > m[q] + 8.f)) {
+                auto weight = [&](float v, int q) { return ex2_approx((v - m[q]) * xs); };
+                #pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    uint32_t pb0, pb1;
+                    if constexpr (SPLIT) {
+                        const float p0 = weight(x[u][0], 0), p1 = weight(x[u][1], 0);
+                        l[0] += p0 + p1;
+                        const float h0 = __half2float(__float2half_rn(p0)), h1 = __half2float(__float2half_rn(p1));
+                        pb0 = movmatrix_t(pack_half2(h0, p0 - h0));
+                        pb1 = movmatrix_t(pack_half2(h1, p1 - h1));
+                    } else {
+                        const float p00 = weight(x[u][0], 0), p01 = weight(x[u][1], NQ - 1);
+                        const float p10 = weight(x[u][NQ], 0), p11 = weight(x[u][2 * NQ - 1], NQ - 1);
+                        l[0] += p00 + p10;
+                        l[NQ - 1] += p01 + p11;
+                        pb0 = movmatrix_t(pack_half2(p00, p01));
+                        pb1 = movmatrix_t(pack_half2(p10, p11));
+                    }
+                    // ---- O^T += V^T P^T
+                    const Words<WORDS> v0 = lds_words<WORDS>(pc + St::V + 2 * u * St::CODES);
+                    const Words<WORDS> v1 = lds_words<WORDS>(pc + St::V + (2 * u + 1) * St::CODES);
+                    const uint32_t b0 = *reinterpret_cast<const uint16_t*>(pv + 2 * u * St::SCALES);
+                    const uint32_t b1 = *reinterpret_cast<const uint16_t*>(pv + (2 * u + 1) * St::SCALES);
+                    const Int4Scale s0 = int4_scale_pair(scales_two(b0)), s1 = int4_scale_pair(scales_two(b1));
                     #pragma unroll
-                    for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
-                    const float m_new = fmaxf(m[q], mx), corr = ex2_approx(m[q] - m_new);
-                    m[q] = m_new;
-                    l[q] *= corr;
-                    #pragma unroll
-                    for (int i = 0; i < MT; ++i) {
-                        ot[i][q] *= corr;
-                        ot[i][2 + q] *= corr;
-                        if (SPLIT) { ot[i][1] *= corr; ot[i][3] *= corr; }
+                    for (int w = 0; w < WORDS; ++w) {
+                        uint32_t e0[4], e1[4];
+                        int4_expand(v0.w[w], s0, e0);
+                        int4_expand(v1.w[w], s1, e1);
+                        mma_16816(ot[2 * w], e0[0], e0[1], e1[0], e1[1], pb0, pb1);
+                        mma_16816(ot[2 * w + 1], e0[2], e0[3], e1[2], e1[3], pb0, pb1);
                     }
                 }
             }
-            const bool part = nt < CT || lo > 0;
-            #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                uint32_t pb0, pb1;
-                if constexpr (SPLIT) {
-                    const float p0 = ex2_approx(x[u][0] - m[0]), p1 = ex2_approx(x[u][1] - m[0]);
-                    l[0] += p0 + p1;
-                    const float h0 = __half2float(__float2half_rn(p0)), h1 = __half2float(__float2half_rn(p1));
-                    pb0 = movmatrix_t(pack_half2(h0, p0 - h0));
-                    pb1 = movmatrix_t(pack_half2(h1, p1 - h1));
-                } else {
-                    const float p00 = ex2_approx(x[u][0] - m[0]), p01 = ex2_approx(x[u][1] - m[NQ - 1]);
-                    const float p10 = ex2_approx(x[u][NQ] - m[0]), p11 = ex2_approx(x[u][2 * NQ - 1] - m[NQ - 1]);
-                    l[0] += p00 + p10;
-                    l[NQ - 1] += p01 + p11;
-                    pb0 = movmatrix_t(pack_half2(p00, p01));
-                    pb1 = movmatrix_t(pack_half2(p10, p11));
-                }
-                // ---- O^T += V^T P^T; rows outside [lo, nt) may hold anything: their scales are zeroed
-                uint32_t b0 = vsc[2 * u], b1 = vsc[2 * u + 1];
-                if (part) {
-                    const int r = 16 * u + 2 * t;
-                    if (r < lo || r >= nt) b0 &= 0xFF00u;
-                    if (r + 1 < lo || r + 1 >= nt) b0 &= 0x00FFu;
-                    if (r + 8 < lo || r + 8 >= nt) b1 &= 0xFF00u;
-                    if (r + 9 < lo || r + 9 >= nt) b1 &= 0x00FFu;
-                }
-                const Int4Scale s0 = int4_scale_pair(scales_two(b0)), s1 = int4_scale_pair(scales_two(b1));
-                #pragma unroll
-                for (int w = 0; w < WORDS; ++w) {
-                    uint32_t e0[4], e1[4];
-                    int4_expand(vw[2 * u].w[w], s0, e0);
-                    int4_expand(vw[2 * u + 1].w[w], s1, e1);
-                    mma_16816(ot[2 * w], e0[0], e0[1], e1[0], e1[1], pb0, pb1);
-                    mma_16816(ot[2 * w + 1], e0[2], e0[3], e1[2], e1[3], pb0, pb1);
-                }
-            }
+            stage ^= 1;
+            if (nt <= CT) break;
         }
-        if (more) load_v();
-        ticket_resolve<D, G>(a, tk, lane);             // the previous item's ticket
-        if (last) {
+        if (started) {
+            const ItemSlot it = slots[cur];
+            const int u = it.s * a.H + it.h;
             #pragma unroll
             for (int q = 0; q < NQ; ++q) {
                 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) l[q] += __shfl_xor_sync(FULL, l[q], o);
             }
-            const int64_t shk = static_cast<int64_t>(is) * a.H + ih;
+            // a LATER part is kept beside the stages; a START part ends the warp's work, so the stages
+            // (nothing is being copied into them) take it
+            char* const keep = it.kind == START ? ring : ring + Sm::ROWS;
+            __syncwarp();                              // every lane has read the last chunk
             #pragma unroll
             for (int q = 0; q < NQ; ++q) {
                 const int query = SPLIT ? t : 2 * t + q;
                 if (query >= G) continue;
-                const int64_t sq = shk * G + query;
-                const float f = single ? (nt > 0 ? 1.f / l[q] : 0.f) : 1.f;
+                const float f = it.kind == WHOLE ? (ntok > 0 ? 1.f / l[q] : 0.f) : 1.f;
                 // this lane: elements g*D/8 .. of its query; tile i holds elements 2i and 2i+1,
                 // the even one as a sixteenth
                 float o[2 * MT];
@@ -400,87 +626,99 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attention_int4_kernel
                     o[2 * i] = (SPLIT ? ot[i][0] + ot[i][1] : ot[i][q]) * 16.f * f;
                     o[2 * i + 1] = (SPLIT ? ot[i][2] + ot[i][3] : ot[i][2 + q]) * f;
                 }
-                if (single && a.out_f16) {             // rounded once, from the float32 result
-                    __half2* dst = reinterpret_cast<__half2*>(static_cast<__half*>(a.out) + sq * D + g * (D / 8));
+                const int64_t row = static_cast<int64_t>(u) * G + query;
+                if (it.kind == WHOLE && a.out_f16) {   // rounded once, from the float32 result
+                    __half2* dst = reinterpret_cast<__half2*>(static_cast<__half*>(a.out) + row * D + g * (D / 8));
                     #pragma unroll
                     for (int i = 0; i < MT; ++i) dst[i] = __floats2half2_rn(o[2 * i], o[2 * i + 1]);
                     continue;
                 }
-                float* dst;
-                if (single) {
-                    dst = static_cast<float*>(a.out) + sq * D;
-                } else {
-                    const int64_t idx = sq * a.max_parts + ip;
-                    if (g == 0) {
-                        a.part_ml[2 * idx] = m[q];
-                        a.part_ml[2 * idx + 1] = l[q];
-                    }
-                    dst = a.part_o + idx * D;
-                }
-                float4* d4 = reinterpret_cast<float4*>(dst + g * (D / 8));
+                if (it.kind != WHOLE && g == 0)
+                    *reinterpret_cast<float2*>(ring + Sm::ML + ((it.kind - 1) * G + query) * 8) = make_float2(m[q] * xs, l[q]);
+                float4* dst = it.kind == WHOLE
+                                  ? reinterpret_cast<float4*>(static_cast<float*>(a.out) + row * D + g * (D / 8))
+                                  : reinterpret_cast<float4*>(keep + query * D * 4 + g * (D / 2));
                 #pragma unroll
                 for (int i = 0; i < MT / 2; ++i)
-                    d4[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
             }
-            if (!single) {
-                const int ctx = s_ctx[is];
-                const int P = is >= s_fine ? a.P_fine : P_eff;
-                ticket_issue(a, tk, shk, ip, nparts_of(ctx - attend_first(ctx, a.window, 8), P), lane);
-            }
+            if (it.kind != WHOLE && lane == 0)
+                *reinterpret_cast<int4*>(held + it.kind - 1) = make_int4(u, it.first, it.last, 0);
         }
+        if (next_tok < 0) break;
+        cur ^= 1;
+        __syncwarp();                                  // lane 0 wrote the slot
+        ntok = next_tok;
+        lo = slots[cur].lo;
+        oid = next_oid;
+        oid_next = next_oid2;
     }
-    ticket_resolve<D, G>(a, tk, lane);
-    // every claim of this CTA is made and read: the last CTA of the launch leaves the work and
-    // exit counters zero for the next call on this workspace
+    // ---- join the CTA's parts: a unit's parts lie with consecutive warps, the first START (or, of a
+    // unit from an earlier CTA, warp 0's LATER), the others LATER
+    if (tid < 2) s_cross[tid].u = -1;
     __syncthreads();
-    if (tid == 0) {
-        __threadfence();
-        if (atomicAdd(a.exit_counter, 1u) == gridDim.x - 1) {
-            *reinterpret_cast<volatile unsigned*>(a.counter) = 0u;
-            *reinterpret_cast<volatile unsigned*>(a.exit_counter) = 0u;
-        }
+    auto held_by = [&](int w, int kind) { return reinterpret_cast<const Held*>(smem + w * Sm::WARP + Sm::HELD) + kind - 1; };
+    for (int kind = START; kind >= LATER; --kind) {
+        if (kind == LATER && warp != 0) break;
+        const Held h = *held_by(warp, kind);
+        if (h.u < 0) continue;
+        int n = 1;
+        while (warp + n < k && held_by(warp + n, LATER)->u == h.u) ++n;
+        const int b0 = range_of(h.first) / k, b1 = range_of(h.last) / k;
+        join_parts<D, G>(a, smem, warp, kind, n, h.u, b0 == b1, lane);
+        // at most one unit comes from an earlier CTA, and one that starts here goes on
+        if (b0 != b1 && lane == 0) s_cross[kind - 1] = Held{h.u, b0, b1, 0};
     }
+    __syncthreads();
+    for (int i = 0; i < 2; ++i)
+        if (s_cross[i].u >= 0) finish_part<D, G>(args, s_cross[i].u, s_cross[i].first, s_cross[i].last, &s_prev);
 }
 
 template <int D, int G>
-int launch_d(const kv_pool* pool, const AttnArgs& args, const AttnPlan& plan, unsigned* counters,
-             cudaStream_t stream) {
-    const int total = args.batch;
-    for (int s0 = 0, sub = 0; s0 < total; s0 += kMaxBatch, ++sub) {
-        AttnArgs sa = args;
-        sa.batch = total - s0 < kMaxBatch ? total - s0 : kMaxBatch;
-        const int64_t rows = static_cast<int64_t>(s0) * args.H;     // (sequence, K/V head) rows before this launch
-        sa.q = static_cast<const char*>(args.q) + rows * G * D * 2;
-        sa.out = static_cast<char*>(args.out) + rows * G * D * (args.out_f16 ? 2 : 4);
-        sa.tables = args.tables + static_cast<int64_t>(s0) * args.max_blocks;
-        sa.lens = args.lens + s0;
-        if (args.k_new) {
-            sa.k_new = args.k_new + rows * D * args.in_bytes;
-            sa.v_new = args.v_new + rows * D * args.in_bytes;
+int launch_d(const kv_pool* pool, const Int4Args& args, const AttnPlan& plan, cudaStream_t stream) {
+    static unsigned long long attr_done = 0;           // the shared-memory opt-in is per device
+    const unsigned long long bit = 1ull << (pool->device & 63);
+    if (!(attr_done & bit)) {
+        if (cudaFuncSetAttribute(attention_int4_kernel<D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 Smem<D, G>::BYTES) != cudaSuccess ||
+            cudaFuncSetAttribute(attention_int4_kernel<D, G>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                 cudaSharedmemCarveoutMaxShared) != cudaSuccess)
+            return KV_ERR_CUDA;
+        attr_done |= bit;
+    }
+    const AttnArgs& all = args.a;
+    for (int s0 = 0; s0 < all.batch; s0 += kMaxBatch) {
+        // launches of one call run one after the other on the stream and share the workspace, whose
+        // counters each leaves zero; under programmatic dependent launch a launch writes nothing
+        // before the one ahead of it has completed
+        Int4Args x = args;
+        AttnArgs& sa = x.a;
+        sa.batch = all.batch - s0 < kMaxBatch ? all.batch - s0 : kMaxBatch;
+        const int64_t rows = static_cast<int64_t>(s0) * all.H;         // units before this launch
+        sa.q = static_cast<const char*>(all.q) + rows * G * D * 2;
+        sa.out = static_cast<char*>(all.out) + rows * G * D * (all.out_f16 ? 2 : 4);
+        sa.tables = all.tables + static_cast<int64_t>(s0) * all.max_blocks;
+        sa.lens = all.lens + s0;
+        if (all.k_new) {
+            sa.k_new = all.k_new + rows * D * all.in_bytes;
+            sa.v_new = all.v_new + rows * D * all.in_bytes;
         }
-        if (args.part_ml) {
-            sa.part_ml = args.part_ml + 2 * rows * G * args.max_parts;
-            sa.part_o = args.part_o + rows * G * args.max_parts * D;
-            sa.arrivals = args.arrivals + rows;
-            if (args.grp_arrivals) sa.grp_arrivals = args.grp_arrivals + rows * args.n_grp;
-        }
-        sa.s_fine = args.s_fine - s0 > 0 ? args.s_fine - s0 : 0;
-        sa.s_base = s0;
-        sa.counter = counters + sub;
-        sa.exit_counter = counters + kMaxSub + sub;
-        const int64_t upper = static_cast<int64_t>(sa.batch) * args.H * args.max_parts;
-        int64_t grid = (upper + kWarps - 1) / kWarps;
-        if (grid > static_cast<int64_t>(pool->num_sms) * kCtasPerSm) grid = static_cast<int64_t>(pool->num_sms) * kCtasPerSm;
+        // no more CTAs than ranges of the longest contexts the call allows
+        const int64_t chunks = static_cast<int64_t>(sa.batch) * all.H * (plan.max_parts + kUnitCost);
+        int64_t grid = chunks / args.min_range;
+        const int64_t fit = static_cast<int64_t>(pool->num_sms) * kCtasPerSm;
+        if (grid > fit) grid = fit;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(static_cast<unsigned>(grid < 1 ? 1 : grid));
-        cfg.blockDim = dim3(kWarps * 32);
+        cfg.blockDim = dim3(kWarps<G> * 32);
+        cfg.dynamicSmemBytes = Smem<D, G>::BYTES;
         cfg.stream = stream;
         cfg.attrs = attr;
         cfg.numAttrs = (plan.flags & KV_DECODE_PDL) ? 1 : 0;
-        if (cudaLaunchKernelEx(&cfg, attention_int4_kernel<D, G>, sa) != cudaSuccess) {
+        if (cudaLaunchKernelEx(&cfg, attention_int4_kernel<D, G>, x) != cudaSuccess) {
             cudaGetLastError();
             return KV_ERR_CUDA;
         }
@@ -489,67 +727,60 @@ int launch_d(const kv_pool* pool, const AttnArgs& args, const AttnPlan& plan, un
 }
 
 template <int D>
-int launch_g(int group, const kv_pool* pool, const AttnArgs& a, const AttnPlan& plan, unsigned* counters,
-             cudaStream_t stream) {
+int launch_g(int group, const kv_pool* pool, const Int4Args& x, const AttnPlan& plan, cudaStream_t stream) {
     switch (group) {
-        case 1: return launch_d<D, 1>(pool, a, plan, counters, stream);
-        case 2: return launch_d<D, 2>(pool, a, plan, counters, stream);
-        case 4: return launch_d<D, 4>(pool, a, plan, counters, stream);
-        case 8: return launch_d<D, 8>(pool, a, plan, counters, stream);
+        case 1: return launch_d<D, 1>(pool, x, plan, stream);
+        case 2: return launch_d<D, 2>(pool, x, plan, stream);
+        case 4: return launch_d<D, 4>(pool, x, plan, stream);
+        case 8: return launch_d<D, 8>(pool, x, plan, stream);
         default: return KV_ERR_INVALID_ARG;
     }
 }
 
 constexpr size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
+// Workspace: the units' counters, the part groups' counters, (m, l), o.
+struct Layout {
+    size_t groups, ml, o, end;
+    Layout(int64_t units, int64_t slots, int group, int head_dim) {
+        groups = align256(static_cast<size_t>(units) * 4);
+        ml = groups + align256(static_cast<size_t>(slots) * 4);
+        o = ml + align256(static_cast<size_t>(slots) * group * 2 * sizeof(float));
+        end = o + static_cast<size_t>(slots) * group * head_dim * sizeof(float) + 256;
+    }
+};
+
+// Units of the largest launch of a call; a slot per CTA and unit.
+int64_t units_of(const kv_pool* pool, int batch) {
+    return static_cast<int64_t>(batch < kMaxBatch ? batch : kMaxBatch) * pool->desc.num_heads;
+}
+int64_t slots_of(const kv_pool* pool, int batch) {
+    return units_of(pool, batch) + static_cast<int64_t>(pool->num_sms) * kCtasPerSm;
+}
+
 }  // namespace
 
+// plan->partition: least chunks of a range; plan->max_parts: chunks of the longest context.
 int plan_attention_int4(const kv_pool* pool, int batch, int max_context, int partition_tokens, AttnPlan* plan,
                         int group, int window) {
     const kv_pool_desc& d = pool->desc;
-    if (batch < 0 || max_context < 0 || window < 0 || batch > kMaxBatch * kMaxSub) return KV_ERR_INVALID_ARG;
+    if (batch < 0 || max_context < 0 || window < 0 || batch > KV_MAX_DECODE_BATCH) return KV_ERR_INVALID_ARG;
     if (!valid_group(d, group)) return KV_ERR_INVALID_ARG;
-    // a sliding window bounds the tokens read per sequence (window + up to 7 masked rows)
-    const int span = (window > 0 && window + 32 < max_context) ? window + 32 : max_context;
-    constexpr int kPartMin = 256, kPartMax = 1024, kPartAlt = 192;
-    const int nc = kWarps * kCtasPerSm;
-    int P;
-    if (partition_tokens > 0) {
-        if (partition_tokens % kPartAlign != 0 || partition_tokens > (1 << 24)) return KV_ERR_INVALID_ARG;
-        P = partition_tokens;
-    } else if (partition_tokens == 0) {
-        const int64_t units = static_cast<int64_t>(batch > 0 ? batch : 1) * d.num_heads;
-        const int64_t warps = static_cast<int64_t>(pool->num_sms) * nc;
-        int64_t parts = group == 1 ? (8 * warps + units - 1) / units : warps / units;
-        if (parts < 1) parts = 1;
-        int64_t p = (static_cast<int64_t>(span) + parts - 1) / parts;
-        p = (p + kPartAlign - 1) / kPartAlign * kPartAlign;
-        P = static_cast<int>(p < kPartMin ? kPartMin : p > kPartMax ? kPartMax : p);
-    } else {
+    if (partition_tokens < 0 || partition_tokens % kPartAlign != 0 || partition_tokens > (1 << 24))
         return KV_ERR_INVALID_ARG;
-    }
-    plan->partition = P;
-    plan->fine_partition = P;
-    plan->fine_from = batch;
-    plan->alt_partition = partition_tokens == 0 && group == 1 && P == kPartMin ? kPartAlt : P;
-    const int pmin = plan->alt_partition;
-    plan->max_parts = span <= pmin ? 1 : (span + pmin - 1) / pmin;
-    const int64_t launch_items =
-        static_cast<int64_t>(batch < kMaxBatch ? batch : kMaxBatch) * d.num_heads * plan->max_parts;
-    if (launch_items > (int64_t{1} << 30)) return KV_ERR_INVALID_ARG;
-    plan->consumers = nc;
+    static_assert(kPartAlign == kChunk, "a partition is whole chunks");
+    // a sliding window bounds the tokens read per sequence (window + up to 7 masked rows)
+    const int64_t span = window > 0 && window + 32 < max_context ? window + 32 : max_context;
+    const int64_t chunks = span > 0 ? (span + kChunk - 1) / kChunk : 1;
+    // the kernel numbers a launch's chunks with an int
+    if (units_of(pool, batch) * (chunks + kUnitCost) >= (int64_t{1} << 31)) return KV_ERR_INVALID_ARG;
+    constexpr int kMinChunks = 4;                       // below 128 tokens a range costs more than it spreads
+    *plan = AttnPlan{};
+    plan->partition = partition_tokens ? partition_tokens / kChunk : kMinChunks;
+    plan->max_parts = static_cast<int>(chunks);
     plan->group = group;
     plan->window = window;
-    plan->flags = 0;
-    plan->pairs = false;
-    size_t ws = kCounterBytes;                          // work and exit counters
-    if (plan->max_parts > 1) {
-        const size_t n = static_cast<size_t>(batch) * d.num_heads * group * plan->max_parts;
-        ws += plan->arrivals_bytes(batch, d.num_heads);
-        ws += align256(n * 2 * sizeof(float));
-        ws += align256(n * d.head_dim * sizeof(float));
-    }
-    plan->ws_bytes = ws;
+    plan->ws_bytes = Layout(units_of(pool, batch), slots_of(pool, batch), group, d.head_dim).end;
     return KV_OK;
 }
 
@@ -563,12 +794,11 @@ int launch_attention_int4(const kv_pool* pool, int layer, const void* q, const v
     if (dev != pool->device) return KV_ERR_INVALID_ARG;
     if (batch == 0) return KV_OK;
     char* ws = static_cast<char*>(workspace);
-    unsigned* counters = reinterpret_cast<unsigned*>(ws);
-    const size_t arrivals_bytes = plan.arrivals_bytes(batch, d.num_heads);
-    if (!(plan.flags & KV_DECODE_WORKSPACE_ZEROED) &&
-        cudaMemsetAsync(counters, 0, kCounterBytes + arrivals_bytes, stream) != cudaSuccess)
+    const Layout lay(units_of(pool, batch), slots_of(pool, batch), plan.group, d.head_dim);
+    if (!(plan.flags & KV_DECODE_WORKSPACE_ZEROED) && cudaMemsetAsync(ws, 0, lay.ml, stream) != cudaSuccess)
         return KV_ERR_CUDA;
-    AttnArgs a{};
+    Int4Args x{};
+    AttnArgs& a = x.a;
     a.kpool = static_cast<char*>(pool->k_layers[layer]);
     a.vpool = static_cast<char*>(pool->v_layers[layer]);
     a.k_new = static_cast<const char*>(k_new);
@@ -578,15 +808,11 @@ int launch_attention_int4(const kv_pool* pool, int layer, const void* q, const v
     a.out = out;
     a.tables = block_tables;
     a.lens = context_lens;
-    if (plan.max_parts > 1) {                           // the workspace of launch_attention_append
-        const size_t n = static_cast<size_t>(batch) * d.num_heads * plan.group * plan.max_parts;
-        a.arrivals = reinterpret_cast<unsigned*>(ws + kCounterBytes);
-        a.grp_arrivals =
-            reinterpret_cast<unsigned*>(ws + kCounterBytes + align256(static_cast<size_t>(batch) * d.num_heads * 4));
-        a.n_grp = merge_groups(plan.max_parts);
-        a.part_ml = reinterpret_cast<float*>(ws + kCounterBytes + arrivals_bytes);
-        a.part_o = reinterpret_cast<float*>(ws + kCounterBytes + arrivals_bytes + align256(n * 2 * sizeof(float)));
-    }
+    a.arrivals = reinterpret_cast<unsigned*>(ws);
+    x.group_done = reinterpret_cast<unsigned*>(ws + lay.groups);
+    a.part_ml = reinterpret_cast<float*>(ws + lay.ml);
+    a.part_o = reinterpret_cast<float*>(ws + lay.o);
+    x.min_range = plan.partition;
     a.err = pool->d_err;
     a.batch = batch;
     a.H = d.num_heads;
@@ -594,19 +820,13 @@ int launch_attention_int4(const kv_pool* pool, int layer, const void* q, const v
     a.max_blocks = max_blocks;
     const int64_t lim_tables = static_cast<int64_t>(max_blocks) * d.block_size;
     a.ctx_limit = static_cast<int>(lim_tables < max_context ? lim_tables : max_context);
-    a.P = plan.partition;
-    a.P_fine = plan.fine_partition;
-    a.P_alt = plan.alt_partition;
-    a.s_fine = plan.fine_from;
-    a.max_parts = plan.max_parts;
     a.num_blocks = d.num_blocks;
     a.early_tables = (plan.flags & KV_DECODE_PDL) && (plan.flags & KV_DECODE_EARLY_TABLES) ? 1 : 0;
     a.out_f16 = (plan.flags & KV_DECODE_OUT_F16) ? 1 : 0;
     a.qscale = scale * 1.4426950408889634f;             // log2(e): softmax evaluated with 2^x
     a.window = plan.window;
-    a.fused = k_new != nullptr ? 1 : 0;
-    return d.head_dim == 128 ? launch_g<128>(plan.group, pool, a, plan, counters, stream)
-                             : launch_g<64>(plan.group, pool, a, plan, counters, stream);
+    return d.head_dim == 128 ? launch_g<128>(plan.group, pool, x, plan, stream)
+                             : launch_g<64>(plan.group, pool, x, plan, stream);
 }
 
 }  // namespace kvp

@@ -86,19 +86,30 @@ __device__ __forceinline__ Int4Scale int4_scale_pair(uint32_t half2_bits) {   //
     r.c1 = __hmul2(r.a16, __float2half2_rn(-1152.f));
     return r;
 }
+// one of the two scales for both halves
+__device__ __forceinline__ Int4Scale int4_scale_of(const Int4Scale& s, int which) {
+    Int4Scale r;
+    r.a16 = which ? __high2half2(s.a16) : __low2half2(s.a16);
+    r.c0 = which ? __high2half2(s.c0) : __low2half2(s.c0);
+    r.c1 = which ? __high2half2(s.c1) : __low2half2(s.c1);
+    return r;
+}
 
-__device__ __forceinline__ uint32_t int4_pair(uint32_t masked, const __half2 a, const __half2 c) {
-    const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&masked), a, c);
+// (w & MASK) | 0x64006400 (1024.0 twice) in one instruction, then the fma
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t int4_pair(uint32_t w, const __half2 a, const __half2 c) {
+    uint32_t u;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(u) : "r"(w), "n"(MASK), "r"(0x64006400u));
+    const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&u), a, c);
     return *reinterpret_cast<const uint32_t*>(&r);
 }
 
 __device__ __forceinline__ void int4_expand(uint32_t w, const Int4Scale& s, uint32_t (&p)[4]) {
-    constexpr uint32_t kMagic = 0x64006400u;           // 1024.0 twice
-    p[0] = int4_pair((w & 0x000F000Fu) | kMagic, s.a16, s.c0);
-    p[1] = int4_pair((w & 0x00F000F0u) | kMagic, s.a16, s.c1);
+    p[0] = int4_pair<0x000F000Fu>(w, s.a16, s.c0);
+    p[1] = int4_pair<0x00F000F0u>(w, s.a16, s.c1);
     w >>= 8;
-    p[2] = int4_pair((w & 0x000F000Fu) | kMagic, s.a16, s.c0);
-    p[3] = int4_pair((w & 0x00F000F0u) | kMagic, s.a16, s.c1);
+    p[2] = int4_pair<0x000F000Fu>(w, s.a16, s.c0);
+    p[3] = int4_pair<0x00F000F0u>(w, s.a16, s.c1);
 }
 
 // Byte offsets inside an oct.
