@@ -34,9 +34,8 @@
 namespace kvp {
 namespace {
 
-constexpr int kCtasPerSm = 2;
-// 8 query heads hold two columns of state per lane and need more than 128 registers
-template <int G> constexpr int kWarps = G == 8 ? 6 : 8;
+// One CTA per SM.  8 query heads hold two columns of state per lane and need more than 128 registers.
+template <int G> constexpr int kWarps = G == 8 ? 12 : 16;
 constexpr int kUnitCost = 2;                       // chunks that beginning and ending a unit costs a warp
 constexpr int kChunk = 32, kOcts = kChunk / 8;         // tokens and octs per chunk: one softmax update
 static_assert(32 % kOcts == 0, "a chunk's octs lie in one window of 32 oct ids");
@@ -244,37 +243,54 @@ __device__ __forceinline__ void merge_row(const AttnArgs& a, int64_t slot, int c
     }
 }
 
-// The CTA's part of unit u (CTAs b0 .. b1) is in the workspace: count it, and merge what it
-// completes, a warp per row.  Called by every thread.
+// The CTA's parts of up to two units that cross CTAs (cross[i]: unit, first and last CTA) are in the
+// workspace: count them, and merge what they complete, a warp per row.  Called by every thread.
 template <int D, int G>
-__device__ __forceinline__ void finish_part(const Int4Args& x, int u, int b0, int b1, unsigned* s_prev) {
+__device__ __forceinline__ void finish_parts(const Int4Args& x, const Held* cross, int* s_go) {
     const AttnArgs& a = x.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int parts = b1 - b0 + 1, part = blockIdx.x - b0;
-    const int64_t slot = static_cast<int64_t>(b0) + u;
-    auto count_one = [&](unsigned* ctr, int of) {      // true in the CTA that finishes the last of `of`
-        __syncthreads();                               // every warp's rows are written
-        if (threadIdx.x == 0) {
-            const unsigned prev = atom_add_acq_rel_gpu(ctr, 1u);
-            if (prev == static_cast<unsigned>(of - 1)) *ctr = 0;       // left zero for the next call
-            *s_prev = prev;
+    auto parts_of = [&](int i) { return cross[i].u < 0 ? 0 : cross[i].last - cross[i].first + 1; };
+    // thread 0 of warp i counts unit i's part in a counter of `of`: s_go[i] says whether it was the last
+    auto count_one = [&](int i, unsigned* ctr, int of) {
+        const unsigned prev = atom_add_acq_rel_gpu(ctr, 1u);
+        s_go[i] = prev == static_cast<unsigned>(of - 1);
+        if (s_go[i]) *ctr = 0;                         // left zero for the next call
+    };
+    const int most = max(parts_of(0), parts_of(1));
+    if (most == 0) return;
+    __syncthreads();                                   // every warp's rows are written
+    if (most > kMergeFan) {
+        if (warp < 2 && lane == 0) {
+            const int parts = parts_of(warp), part = blockIdx.x - cross[warp].first, first = part / kMergeFan * kMergeFan;
+            if (parts > kMergeFan)
+                count_one(warp, x.group_done + cross[warp].first + cross[warp].u + first, min(kMergeFan, parts - first));
+            else
+                s_go[warp] = 1;
         }
         __syncthreads();
-        return *s_prev == static_cast<unsigned>(of - 1);
-    };
-    if (parts > kMergeFan) {
-        const int first = part / kMergeFan * kMergeFan, size = min(kMergeFan, parts - first);
-        if (!count_one(x.group_done + slot + first, size)) return;
-        for (int r = warp; r < G; r += kWarps<G>) merge_row<D, G>(a, slot + first, size, 1, u, r, false, lane);
+        for (int j = warp; j < 2 * G; j += kWarps<G>) {
+            const int i = j / G, parts = parts_of(i), first = (blockIdx.x - cross[i].first) / kMergeFan * kMergeFan;
+            if (parts > kMergeFan && s_go[i])
+                merge_row<D, G>(a, static_cast<int64_t>(cross[i].first) + cross[i].u + first, min(kMergeFan, parts - first),
+                                1, cross[i].u, j % G, false, lane);
+        }
+        __syncthreads();
     }
-    const int count = parts > kMergeFan ? (parts + kMergeFan - 1) / kMergeFan : parts;
-    if (!count_one(a.arrivals + u, count)) return;
-    for (int r = warp; r < G; r += kWarps<G>)
-        merge_row<D, G>(a, slot, count, parts > kMergeFan ? kMergeFan : 1, u, r, true, lane);
+    auto groups = [&](int parts) { return parts > kMergeFan ? (parts + kMergeFan - 1) / kMergeFan : parts; };
+    __syncwarp();
+    if (warp < 2 && lane == 0 && parts_of(warp) > 0 && (most <= kMergeFan || s_go[warp]))
+        count_one(warp, a.arrivals + cross[warp].u, groups(parts_of(warp)));
+    __syncthreads();
+    for (int j = warp; j < 2 * G; j += kWarps<G>) {
+        const int i = j / G, parts = parts_of(i);
+        if (parts > 0 && s_go[i])
+            merge_row<D, G>(a, static_cast<int64_t>(cross[i].first) + cross[i].u, groups(parts),
+                            parts > kMergeFan ? kMergeFan : 1, cross[i].u, j % G, true, lane);
+    }
 }
 
 template <int D, int G>
-__global__ void __launch_bounds__(kWarps<G> * 32, kCtasPerSm) attention_int4_kernel(const __grid_constant__ Int4Args args) {
+__global__ void __launch_bounds__(kWarps<G> * 32, 1) attention_int4_kernel(const __grid_constant__ Int4Args args) {
     const AttnArgs& a = args.a;
     constexpr int WORDS = Int4<D>::WORDS, OCT = Int4<D>::OCT;
     constexpr int MT = D / 16;                         // output tiles of 16 elements
@@ -286,7 +302,7 @@ __global__ void __launch_bounds__(kWarps<G> * 32, kCtasPerSm) attention_int4_ker
     extern __shared__ __align__(128) char smem[];
     __shared__ int s_ctx[kMaxBatch], s_end[kMaxBatch];
     __shared__ Held s_cross[2];                        // the CTA's units that cross CTAs, with their CTAs
-    __shared__ unsigned s_prev;
+    __shared__ int s_go[2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
 
     const bool early = a.early_tables != 0;
@@ -294,6 +310,7 @@ __global__ void __launch_bounds__(kWarps<G> * 32, kCtasPerSm) attention_int4_ker
         asm volatile("griddepcontrol.wait;" ::: "memory");
         if (tid == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     }
+    if (tid < 2) s_cross[tid].u = -1;
     // ---- chunks per (sequence, head) and their inclusive prefix over the launch's units
     auto chunks_of = [&](int ctx) {
         const int n = ctx - attend_first(ctx, a.window, 8);
@@ -332,11 +349,6 @@ __global__ void __launch_bounds__(kWarps<G> * 32, kCtasPerSm) attention_int4_ker
     const int k = min((want + grid - 1) / grid, NW);
     const int ranges = min(want, k * grid);
     auto range_of = [&](int chunk) { return static_cast<int>(((chunk + int64_t{1}) * ranges - 1) / total); };
-    if (early) {
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-        if (tid == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    }
-
     char* const ring = smem + warp * Sm::WARP;
     char* const s_q = ring + Sm::Q;
     ItemSlot* const slots = reinterpret_cast<ItemSlot*>(ring + Sm::SLOTS);
@@ -382,6 +394,9 @@ __global__ void __launch_bounds__(kWarps<G> * 32, kCtasPerSm) attention_int4_ker
     const bool works = warp < k && rng < ranges;
     int pos = works ? static_cast<int>(rng * total / ranges) : 0;      // first chunk not yet taken
     const int end = works ? static_cast<int>((rng + 1) * total / ranges) : 0;
+    const int64_t rng0 = static_cast<int64_t>(blockIdx.x) * k;         // the CTA's ranges: rng0 .. rng0 + k - 1
+    const int cta_begin = static_cast<int>(rng0 * total / ranges);
+    const int cta_end = static_cast<int>(min(rng0 + k, static_cast<int64_t>(ranges)) * total / ranges);
     const float xs = a.qscale * 16.f, slack = fminf(8.f / xs, 1e30f);
     const int col = SPLIT ? g >> 1 : g;                // query of mma column g (odd columns of SPLIT: none)
     const bool has_q = !(SPLIT && (g & 1)) && col < G;
@@ -455,6 +470,15 @@ __global__ void __launch_bounds__(kWarps<G> * 32, kCtasPerSm) attention_int4_ker
                         *reinterpret_cast<int4*>(&it->first) =
                             make_int4(unit, unit + cps - 1, c0 > 0 ? LATER : n < cps ? START : WHOLE, 0);
                     }
+                    const int no = (next_tok + 7) >> 3;
+                    if (no > 0) next_oid = load_oids(s, h, tok0 >> 3, no);
+                    if (no > 32) next_oid2 = load_oids(s, h, (tok0 >> 3) + 32, no - 32);
+                }
+                if (!started && early) {               // lengths and tables came early; nothing else does
+                    asm volatile("griddepcontrol.wait;" ::: "memory");
+                    if (tid == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+                }
+                if (n > 0) {
                     if (a.k_new != nullptr && c0 + n == cps && ctx > 0) {
                         // fused append: the newest token goes to its slot before the item's copies
                         const int last = ctx - 1, o = last >> 3;
@@ -471,9 +495,6 @@ __global__ void __launch_bounds__(kWarps<G> * 32, kCtasPerSm) attention_int4_ker
                     for (int i = 0; i < (Sm::QBYTES / 16 + 31) / 32; ++i)
                         if (i * 32 + lane < Sm::QBYTES / 16)
                             cp_async16(smem_u32(s_q) + (i * 32 + lane) * 16, q + (i * 32 + lane) * 16);
-                    const int no = (next_tok + 7) >> 3;
-                    if (no > 0) next_oid = load_oids(s, h, tok0 >> 3, no);
-                    if (no > 32) next_oid2 = load_oids(s, h, (tok0 >> 3) + 32, no - 32);
                 }
             }
             cp_async_wait();
@@ -655,7 +676,6 @@ __global__ void __launch_bounds__(kWarps<G> * 32, kCtasPerSm) attention_int4_ker
     }
     // ---- join the CTA's parts: a unit's parts lie with consecutive warps, the first START (or, of a
     // unit from an earlier CTA, warp 0's LATER), the others LATER
-    if (tid < 2) s_cross[tid].u = -1;
     __syncthreads();
     auto held_by = [&](int w, int kind) { return reinterpret_cast<const Held*>(smem + w * Sm::WARP + Sm::HELD) + kind - 1; };
     for (int kind = START; kind >= LATER; --kind) {
@@ -664,14 +684,13 @@ __global__ void __launch_bounds__(kWarps<G> * 32, kCtasPerSm) attention_int4_ker
         if (h.u < 0) continue;
         int n = 1;
         while (warp + n < k && held_by(warp + n, LATER)->u == h.u) ++n;
-        const int b0 = range_of(h.first) / k, b1 = range_of(h.last) / k;
-        join_parts<D, G>(a, smem, warp, kind, n, h.u, b0 == b1, lane);
+        const bool whole = h.first >= cta_begin && h.last < cta_end;
         // at most one unit comes from an earlier CTA, and one that starts here goes on
-        if (b0 != b1 && lane == 0) s_cross[kind - 1] = Held{h.u, b0, b1, 0};
+        if (!whole && lane == 0) s_cross[kind - 1] = Held{h.u, range_of(h.first) / k, range_of(h.last) / k, 0};
+        join_parts<D, G>(a, smem, warp, kind, n, h.u, whole, lane);
     }
     __syncthreads();
-    for (int i = 0; i < 2; ++i)
-        if (s_cross[i].u >= 0) finish_part<D, G>(args, s_cross[i].u, s_cross[i].first, s_cross[i].last, &s_prev);
+    finish_parts<D, G>(args, s_cross, s_go);
 }
 
 template <int D, int G>
@@ -706,7 +725,7 @@ int launch_d(const kv_pool* pool, const Int4Args& args, const AttnPlan& plan, cu
         // no more CTAs than ranges of the longest contexts the call allows
         const int64_t chunks = static_cast<int64_t>(sa.batch) * all.H * (plan.max_parts + kUnitCost);
         int64_t grid = chunks / args.min_range;
-        const int64_t fit = static_cast<int64_t>(pool->num_sms) * kCtasPerSm;
+        const int64_t fit = static_cast<int64_t>(pool->num_sms);
         if (grid > fit) grid = fit;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -755,7 +774,7 @@ int64_t units_of(const kv_pool* pool, int batch) {
     return static_cast<int64_t>(batch < kMaxBatch ? batch : kMaxBatch) * pool->desc.num_heads;
 }
 int64_t slots_of(const kv_pool* pool, int batch) {
-    return units_of(pool, batch) + static_cast<int64_t>(pool->num_sms) * kCtasPerSm;
+    return units_of(pool, batch) + static_cast<int64_t>(pool->num_sms);
 }
 
 }  // namespace
