@@ -250,42 +250,40 @@ __device__ __forceinline__ void finish_parts(const Int4Args& x, const Held* cros
     const AttnArgs& a = x.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     auto parts_of = [&](int i) { return cross[i].u < 0 ? 0 : cross[i].last - cross[i].first + 1; };
-    // thread 0 of warp i counts unit i's part in a counter of `of`: s_go[i] says whether it was the last
-    auto count_one = [&](int i, unsigned* ctr, int of) {
-        const unsigned prev = atom_add_acq_rel_gpu(ctr, 1u);
-        s_go[i] = prev == static_cast<unsigned>(of - 1);
-        if (s_go[i]) *ctr = 0;                         // left zero for the next call
-    };
     const int most = max(parts_of(0), parts_of(1));
     if (most == 0) return;
-    __syncthreads();                                   // every warp's rows are written
-    if (most > kMergeFan) {
+    // Level 0 joins groups of kMergeFan parts into the group's first slot (units with more parts than
+    // that), level 1 the unit's parts or groups into the output.
+    #pragma unroll 1
+    for (int level = most > kMergeFan ? 0 : 1; level < 2; ++level) {
+        auto first_of = [&](int i) -> int {                // of the parts this CTA's part is counted with
+            return level == 0 ? (blockIdx.x - cross[i].first) / kMergeFan * kMergeFan : 0;
+        };
+        auto count_of = [&](int i) -> int {
+            const int parts = parts_of(i);
+            if (level == 0) return parts > kMergeFan ? min(kMergeFan, parts - first_of(i)) : 0;
+            return parts > kMergeFan ? (parts + kMergeFan - 1) / kMergeFan : parts;
+        };
+        __syncthreads();                               // every warp's rows are written
         if (warp < 2 && lane == 0) {
-            const int parts = parts_of(warp), part = blockIdx.x - cross[warp].first, first = part / kMergeFan * kMergeFan;
-            if (parts > kMergeFan)
-                count_one(warp, x.group_done + cross[warp].first + cross[warp].u + first, min(kMergeFan, parts - first));
-            else
-                s_go[warp] = 1;
+            const int of = count_of(warp);
+            const bool before = level == 1 && most > kMergeFan ? s_go[warp] != 0 : true;
+            bool go = before;
+            if (of > 0 && before) {
+                const int at = cross[warp].first + cross[warp].u;
+                unsigned* ctr = level == 0 ? x.group_done + at + first_of(warp) : a.arrivals + cross[warp].u;
+                go = atom_add_acq_rel_gpu(ctr, 1u) == static_cast<unsigned>(of - 1);
+                if (go) *ctr = 0;                      // left zero for the next call
+            }
+            s_go[warp] = go;                           // this CTA is the last
         }
         __syncthreads();
         for (int j = warp; j < 2 * G; j += kWarps<G>) {
-            const int i = j / G, parts = parts_of(i), first = (blockIdx.x - cross[i].first) / kMergeFan * kMergeFan;
-            if (parts > kMergeFan && s_go[i])
-                merge_row<D, G>(a, static_cast<int64_t>(cross[i].first) + cross[i].u + first, min(kMergeFan, parts - first),
-                                1, cross[i].u, j % G, false, lane);
+            const int i = j / G, of = count_of(i);
+            if (of > 0 && s_go[i])
+                merge_row<D, G>(a, static_cast<int64_t>(cross[i].first) + cross[i].u + first_of(i), of,
+                                level == 1 && parts_of(i) > kMergeFan ? kMergeFan : 1, cross[i].u, j % G, level == 1, lane);
         }
-        __syncthreads();
-    }
-    auto groups = [&](int parts) { return parts > kMergeFan ? (parts + kMergeFan - 1) / kMergeFan : parts; };
-    __syncwarp();
-    if (warp < 2 && lane == 0 && parts_of(warp) > 0 && (most <= kMergeFan || s_go[warp]))
-        count_one(warp, a.arrivals + cross[warp].u, groups(parts_of(warp)));
-    __syncthreads();
-    for (int j = warp; j < 2 * G; j += kWarps<G>) {
-        const int i = j / G, parts = parts_of(i);
-        if (parts > 0 && s_go[i])
-            merge_row<D, G>(a, static_cast<int64_t>(cross[i].first) + cross[i].u, groups(parts),
-                            parts > kMergeFan ? kMergeFan : 1, cross[i].u, j % G, true, lane);
     }
 }
 
@@ -342,13 +340,19 @@ __global__ void __launch_bounds__(kWarps<G> * 32, 1) attention_int4_kernel(const
     }
     __syncthreads();
     const int total = s_end[a.batch - 1];
-    // ranges: at most one per warp and of min_range chunks at least; k warps of every CTA have one, range
-    // r being chunks [r * total / ranges, (r + 1) * total / ranges)
+    // ranges: at most one per warp and of min_range chunks at least; k warps of every CTA have one.
+    // The first `rem` ranges have q + 1 chunks, the others q.
     const int grid = static_cast<int>(gridDim.x);
     const int want = max(total / args.min_range, 1);
     const int k = min((want + grid - 1) / grid, NW);
     const int ranges = min(want, k * grid);
-    auto range_of = [&](int chunk) { return static_cast<int>(((chunk + int64_t{1}) * ranges - 1) / total); };
+    const int q = total / ranges, rem = total - q * ranges;
+    auto range_begin = [&](int r) { return r * q + min(r, rem); };
+    auto range_of = [&](int chunk) {
+        const int c = chunk - rem * (q + 1);
+        return c < 0 ? chunk / (q + 1) : rem + c / q;
+    };
+
     char* const ring = smem + warp * Sm::WARP;
     char* const s_q = ring + Sm::Q;
     ItemSlot* const slots = reinterpret_cast<ItemSlot*>(ring + Sm::SLOTS);
@@ -390,13 +394,10 @@ __global__ void __launch_bounds__(kWarps<G> * 32, 1) attention_int4_kernel(const
         if (lane < 2 * NO * SPO && i * 8 < nt) cp_async16(dst + St::S, sbase + at);
     };
 
-    const int64_t rng = static_cast<int64_t>(blockIdx.x) * k + warp;
-    const bool works = warp < k && rng < ranges;
-    int pos = works ? static_cast<int>(rng * total / ranges) : 0;      // first chunk not yet taken
-    const int end = works ? static_cast<int>((rng + 1) * total / ranges) : 0;
-    const int64_t rng0 = static_cast<int64_t>(blockIdx.x) * k;         // the CTA's ranges: rng0 .. rng0 + k - 1
-    const int cta_begin = static_cast<int>(rng0 * total / ranges);
-    const int cta_end = static_cast<int>(min(rng0 + k, static_cast<int64_t>(ranges)) * total / ranges);
+    const int rng0 = min(static_cast<int>(blockIdx.x) * k, ranges);    // the CTA's ranges: rng0 .. rng0 + k - 1
+    const int rng = rng0 + (warp < k ? warp : k);
+    int pos = range_begin(min(rng, ranges));           // first chunk not yet taken
+    const int end = warp < k ? range_begin(min(rng + 1, ranges)) : pos;
     const float xs = a.qscale * 16.f, slack = fminf(8.f / xs, 1e30f);
     const int col = SPLIT ? g >> 1 : g;                // query of mma column g (odd columns of SPLIT: none)
     const bool has_q = !(SPLIT && (g & 1)) && col < G;
@@ -678,8 +679,9 @@ __global__ void __launch_bounds__(kWarps<G> * 32, 1) attention_int4_kernel(const
     // unit from an earlier CTA, warp 0's LATER), the others LATER
     __syncthreads();
     auto held_by = [&](int w, int kind) { return reinterpret_cast<const Held*>(smem + w * Sm::WARP + Sm::HELD) + kind - 1; };
-    for (int kind = START; kind >= LATER; --kind) {
-        if (kind == LATER && warp != 0) break;
+    const int cta_begin = range_begin(rng0), cta_end = range_begin(min(rng0 + k, ranges));
+    #pragma unroll 1
+    for (int kind = START; kind >= (warp == 0 ? LATER : START); --kind) {
         const Held h = *held_by(warp, kind);
         if (h.u < 0) continue;
         int n = 1;
