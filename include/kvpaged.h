@@ -187,7 +187,7 @@ KV_API int kv_append(kv_pool* pool, int layer, const void* k, const void* v, kv_
  *                  are contiguous in a row), so q, k and v may be views of one packed
  *                  projection; at least a row, and a multiple of 16 bytes.
  *   slot_mapping   device int64 [num_tokens].  slot < 0: a padding token, of which nothing is
- *                  read but its slot and nothing written, q_out included.  A slot outside the
+ *                  used and nothing written, q_out included (its rows may be read).  A slot outside the
  *                  pool sets KV_DEVERR_SLOT and the token is skipped the same way.  The slots
  *                  of a call must be distinct.
  *   positions      device int32 [num_tokens], 0 .. table_len-1; others set KV_DEVERR_POSITION

@@ -75,11 +75,21 @@ __device__ __forceinline__ uint4 halves(const float (&x)[8]) {
     return r;
 }
 
+template <typename TOut>
+__device__ __forceinline__ void store_eight(char* out, const float (&f)[8]) {
+    if constexpr (sizeof(TOut) == 2) {
+        __stcs(reinterpret_cast<uint4*>(out), halves(f));
+    } else {
+        __stcs(reinterpret_cast<float4*>(out), make_float4(f[0], f[1], f[2], f[3]));
+        __stcs(reinterpret_cast<float4*>(out) + 1, make_float4(f[4], f[5], f[6], f[7]));
+    }
+}
+
 // The unit's 8 elements into pool row `at` (the block's tile of the head, token off of it).
 // IS_V only matters to 4-bit tiles; paired: lane ^ 16 holds the same unit of the token that
 // shares this one's words.
 template <int D, kv_dtype POOL>
-__device__ __forceinline__ void store_unit(char* tile, int off, int unit, const float (&x)[8], float scale, bool is_v,
+__device__ __forceinline__ void store_unit(char* tile, int off, int unit, float (&x)[8], float scale, bool is_v,
                                            bool paired, bool live, int lane) {
     if constexpr (POOL == KV_F32) {
         if (!live) return;
@@ -102,10 +112,7 @@ __device__ __forceinline__ void store_unit(char* tile, int off, int unit, const 
         for (int i = 0; i < 8; ++i) amax = max_nan(amax, fabsf(x[i]));
         amax = max_nan(amax, __shfl_xor_sync(FULL, amax, 1));          // the group's other unit
         const uint32_t sb = int4_scale_byte(amax);
-        const float s = int4_scale_value(sb), inv = int4_inverse(s);
-        uint32_t w = 0;
-        #pragma unroll
-        for (int i = 0; i < 8; ++i) w |= int4_nibble(x[i], s, inv, 7.f * s) << (4 * i);
+        const uint32_t w = int4_nibbles<8>(x, amax, int4_scale_value(sb));
         char* oct = tile + (off >> 3) * Int4<D>::OCT;
         const int token = off & 7, e0 = unit * 8;
         if (!is_v) {
@@ -141,6 +148,22 @@ __global__ void __launch_bounds__(kThreads) append_rope_kernel(const __grid_cons
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int64_t tok = static_cast<int64_t>(blockIdx.x) * 2 + (lane >> 4);
+    // ---- head rows: queries, keys, values, HPW rows per half-warp and step.  The first rows are asked
+    // for before anything is known of the token (one past the end takes the pair's first)
+    const int uq = a.Hq ? (a.Hq + HPW - 1) / HPW : 0, uk = (a.H + HPW - 1) / HPW;
+    const int rows = uq + 2 * uk, step = gridDim.y * kWarpsPerCta;
+    const int64_t from = tok < a.n ? tok : tok - 1;
+    auto load = [&](int r, Raw<TIn>& raw) {
+        const int which = r < uq ? 0 : r < uq + uk ? 1 : 2;
+        const int h = min((r - (which == 0 ? 0 : which == 1 ? uq : uq + uk)) * HPW + sub, (which ? a.H : a.Hq) - 1);
+        const char* base = which == 0 ? a.q + from * a.q_stride : which == 1 ? a.k + from * a.k_stride : a.v + from * a.v_stride;
+        load_raw(base + (h * D + unit * 8) * ESZ, raw);
+    };
+    int r0 = blockIdx.y * kWarpsPerCta + warp;
+    Raw<TIn> next[UNROLL];
+    #pragma unroll
+    for (int j = 0; j < UNROLL; ++j)
+        if (r0 + j * step < rows) load(r0 + j * step, next[j]);
     // ---- the token: its slot, its position, its rotation
     int64_t slot = tok < a.n ? a.slots[tok] : -1;
     int pos = 0;
@@ -184,6 +207,10 @@ __global__ void __launch_bounds__(kThreads) append_rope_kernel(const __grid_cons
             c[4 * j] = cv.x; c[4 * j + 1] = cv.y; c[4 * j + 2] = cv.z; c[4 * j + 3] = cv.w;
             s[4 * j] = sv.x; s[4 * j + 1] = sv.y; s[4 * j + 2] = sv.z; s[4 * j + 3] = sv.w;
         }
+        if (!a.adjacent && low) {                      // x cos - y sin as x cos + y (-sin): the same roundings
+            #pragma unroll
+            for (int i = 0; i < 8; ++i) s[i] = -s[i];
+        }
     }
     const int partner = (lane & ~(UPR - 1)) | (turned ? (low ? unit + half_units : unit - half_units) : unit);
     auto rotate = [&](float (&x)[8]) {
@@ -200,27 +227,19 @@ __global__ void __launch_bounds__(kThreads) append_rope_kernel(const __grid_cons
         #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float y = __shfl_sync(FULL, x[i], partner);
-            const float z = __fmul_rn(y, s[i]);
-            if (turned) x[i] = __fadd_rn(__fmul_rn(x[i], c[i]), low ? -z : z);
+            if (turned) x[i] = __fadd_rn(__fmul_rn(x[i], c[i]), __fmul_rn(y, s[i]));
         }
     };
-    // ---- head rows: queries, keys, values, HPW rows per half-warp and step
-    const int uq = a.Hq ? (a.Hq + HPW - 1) / HPW : 0, uk = (a.H + HPW - 1) / HPW;
-    const int rows = uq + 2 * uk, step = gridDim.y * kWarpsPerCta;
-    const int64_t safe = live ? tok : tok ^ 1;         // a dead half-warp reads the live one's rows
-    for (int r0 = blockIdx.y * kWarpsPerCta + warp; r0 < rows; r0 += step * UNROLL) {
+    // ---- every row is read before any is written by the same lanes' warp: q_out may be q
+    for (; r0 < rows; r0 += step * UNROLL) {
         Raw<TIn> raw[UNROLL];
         #pragma unroll
         for (int j = 0; j < UNROLL; ++j) {
-            const int r = r0 + j * step;
-            if (r >= rows) break;
-            const int which = r < uq ? 0 : r < uq + uk ? 1 : 2;
-            const int h = min((r - (which == 0 ? 0 : which == 1 ? uq : uq + uk)) * HPW + sub, (which ? a.H : a.Hq) - 1);
-            const char* base = which == 0 ? a.q + safe * a.q_stride : which == 1 ? a.k + safe * a.k_stride
-                                                                                 : a.v + safe * a.v_stride;
-            load_raw(base + (h * D + unit * 8) * ESZ, raw[j]);
+            raw[j] = next[j];
+            const int r = r0 + (UNROLL + j) * step;
+            if (r < rows) load(r, next[j]);
         }
-        __syncwarp();                                  // q_out may be q: every row is read first
+        __syncwarp();
         #pragma unroll
         for (int j = 0; j < UNROLL; ++j) {
             const int r = r0 + j * step;
@@ -353,30 +372,19 @@ struct GatherArgs {
     int* err;
 };
 
-// The unit's 8 stored elements: their bytes in a (and b), a 4-bit unit's scale byte in a.y.
+// The unit's 8 stored elements: their bytes in a (and b).
 template <int D, kv_dtype POOL>
-__device__ __forceinline__ void load_stored(const char* tile, int off, int unit, bool is_v, uint4& a, uint4& b) {
+__device__ __forceinline__ void load_stored(const char* tile, int off, int unit, uint4& a, uint4& b) {
     if constexpr (POOL == KV_F32) {
         const uint4* p = reinterpret_cast<const uint4*>(tile + (static_cast<int64_t>(off) * D + unit * 8) * 4);
         a = __ldcs(p);
         b = __ldcs(p + 1);
     } else if constexpr (POOL == KV_F16) {
         a = __ldcs(reinterpret_cast<const uint4*>(tile + (off * D + unit * 8) * 2));
-    } else if constexpr (POOL == KV_FP8_E4M3) {
+    } else {
         const uint2 x = __ldcs(reinterpret_cast<const uint2*>(tile + off * D + unit * 8));
         a.x = x.x;
         a.y = x.y;
-    } else {
-        const char* oct = tile + (off >> 3) * Int4<D>::OCT;
-        const int token = off & 7, e0 = unit * 8;
-        if (!is_v) {
-            a.x = *reinterpret_cast<const uint32_t*>(oct + int4_k_code<D>(token, e0));
-            a.y = *reinterpret_cast<const uint8_t*>(oct + int4_k_scale<D>(token, e0));
-        } else {
-            a.x = *reinterpret_cast<const uint16_t*>(oct + int4_v_piece<D>(token, e0)) |
-                  static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(oct + int4_v_piece<D>(token, e0 + 4))) << 16;
-            a.y = *reinterpret_cast<const uint8_t*>(oct + int4_v_scale<D>(token, e0));
-        }
     }
 }
 
@@ -384,7 +392,7 @@ __device__ __forceinline__ void load_stored(const char* tile, int off, int unit,
 template <int D, kv_dtype POOL, typename TOut>
 __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant__ GatherArgs a) {
     constexpr int UPR = D / 8, HPW = 16 / UPR, UNROLL = 4;
-    constexpr int ROW = POOL == KV_INT4 ? D / 2 + D / 16 : POOL == KV_FP8_E4M3 ? D : POOL == KV_F16 ? 2 * D : 4 * D;
+    constexpr int ROW = POOL == KV_FP8_E4M3 ? D : POOL == KV_F16 ? 2 * D : 4 * D;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int unit = lane & (UPR - 1), sub = (lane & 15) / UPR;
     const int64_t tok = static_cast<int64_t>(blockIdx.x) * 2 + (lane >> 4);
@@ -411,7 +419,7 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant_
             const int h = (is_v ? r - uk : r) * HPW + sub;
             if (r >= rows || h >= a.H) continue;
             load_stored<D, POOL>((is_v ? a.vpool : a.kpool) + (blk * a.H + h) * static_cast<int64_t>(a.B) * ROW, off,
-                                 unit, is_v, x[j], y[j]);
+                                 unit, x[j], y[j]);
         }
         #pragma unroll
         for (int j = 0; j < UNROLL; ++j) {
@@ -420,43 +428,194 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant_
             const int h = (is_v ? r - uk : r) * HPW + sub;
             if (r >= rows || h >= a.H) continue;
             char* out = (is_v ? a.v : a.k) + ((tok * a.H + h) * D + unit * 8) * static_cast<int64_t>(sizeof(TOut));
-            float f[8];
             if constexpr (POOL == KV_F32) {
                 __stcs(reinterpret_cast<uint4*>(out), x[j]);
                 __stcs(reinterpret_cast<uint4*>(out) + 1, y[j]);
-                continue;
-            } else if constexpr (POOL == KV_F16) {
-                if constexpr (sizeof(TOut) == 2) {
-                    __stcs(reinterpret_cast<uint4*>(out), x[j]);
-                    continue;
-                } else {
+            } else if constexpr (POOL == KV_F16 && sizeof(TOut) == 2) {
+                __stcs(reinterpret_cast<uint4*>(out), x[j]);
+            } else {
+                float f[8];
+                if constexpr (POOL == KV_F16) {
                     Raw<__half> raw;
                     raw.a = x[j];
                     widen(raw, f);
+                } else {
+                    const float sc = is_v ? vs : ks;
+                    const uint32_t w[2] = {x[j].x, x[j].y};
+                    #pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 e = e4m3x2_to_float2(static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1))));
+                        f[2 * i] = e.x * sc;
+                        f[2 * i + 1] = e.y * sc;
+                    }
                 }
-            } else if constexpr (POOL == KV_FP8_E4M3) {
-                const float sc = is_v ? vs : ks;
-                const uint32_t w[2] = {x[j].x, x[j].y};
-                #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 e = e4m3x2_to_float2(static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1))));
-                    f[2 * i] = e.x * sc;
-                    f[2 * i + 1] = e.y * sc;
-                }
-            } else {
-                const float sc = int4_scale_value(x[j].y);
-                #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    f[i] = static_cast<float>(static_cast<int>((x[j].x >> (4 * i)) & 15u) - 8) * sc;
-            }
-            if constexpr (sizeof(TOut) == 2) {
-                __stcs(reinterpret_cast<uint4*>(out), halves(f));
-            } else {
-                __stcs(reinterpret_cast<float4*>(out), make_float4(f[0], f[1], f[2], f[3]));
-                __stcs(reinterpret_cast<float4*>(out) + 1, make_float4(f[4], f[5], f[6], f[7]));
+                store_eight<TOut>(out, f);
             }
         }
     }
+}
+
+// The 8 nibbles of a word as float16 pairs times their scales, exact: p[0] holds nibbles 0 and 4 ..
+// p[3] nibbles 3 and 7 (int4.cuh's expansion without the sixteenth, one instruction more).
+__device__ __forceinline__ void expand_full(uint32_t w, uint32_t scales, uint32_t (&p)[4]) {
+    const __half2 s = *reinterpret_cast<const __half2*>(&scales);
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t u = w >> (i < 2 ? 0 : 8);
+        if (i & 1) {
+            u = int4_pair<0x00F000F0u>(u, __float2half2_rn(0.0625f), __float2half2_rn(-72.f));
+        } else {
+            u = int4_pair<0x000F000Fu>(u, __float2half2_rn(1.f), __float2half2_rn(-1032.f));
+        }
+        const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&u), s);
+        p[i] = *reinterpret_cast<const uint32_t*>(&r);
+    }
+}
+
+// 8 float16 values to the output type
+template <typename TOut>
+__device__ __forceinline__ void store_halves(char* out, const uint4 v) {
+    if constexpr (sizeof(TOut) == 2) {
+        __stcs(reinterpret_cast<uint4*>(out), v);
+    } else {
+        Raw<__half> raw;
+        raw.a = v;
+        float f[8];
+        widen(raw, f);
+        store_eight<TOut>(out, f);
+    }
+}
+
+// 4-bit pools: a CTA takes 8 tokens, a warp one head of them at a time.  Where the tokens are the 8 of
+// one oct in order (a cached prefix), K comes as 128-byte pieces that hold whole rows, and V as the
+// attention kernel reads it, 16 (D 64: 8) bytes per lane holding a chunk of two tokens; lanes of
+// neighbouring chunks then swap halves so that a store fills whole 32-byte sectors.  Other tokens go
+// one per half-warp.  Bound: HBM, most of it the output.
+template <int D, typename TOut>
+__global__ void __launch_bounds__(kThreads) gather_int4_kernel(const __grid_constant__ GatherArgs a) {
+    constexpr int OCT = Int4<D>::OCT, CODES = Int4<D>::CODES, WORDS = Int4<D>::WORDS, ES = sizeof(TOut);
+    constexpr int UPR = D / 8;                         // units of 8 elements per row
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * 8;
+    const int opb = a.B >> 3;
+    int64_t slot = tok0 + (lane & 7) < a.n ? a.slots[tok0 + (lane & 7)] : -1;
+    if (slot >= a.num_slots) {
+        atomicOr(a.err, KV_DEVERR_SLOT);
+        slot = -1;
+    }
+    const int64_t first = __shfl_sync(FULL, slot, 0);
+    const bool whole = __all_sync(FULL, first >= 0 && (first & 7) == 0 && slot == first + (lane & 7));
+    const int64_t row = static_cast<int64_t>(a.H) * D * ES;            // bytes between two tokens of the output
+    if (whole) {
+        const int64_t blk = first / a.B;
+        const int o = static_cast<int>(first - blk * a.B) >> 3;
+        #pragma unroll 2
+        for (int h = blockIdx.y * kWarpsPerCta + warp; h < a.H; h += gridDim.y * kWarpsPerCta) {
+            const int64_t at = ((blk * a.H + h) * opb + o) * OCT;
+            const char* k = a.kpool + at;
+            const char* v = a.vpool + at;
+            constexpr int NK = 4 * D / 128, TPK = 8 / NK;              // 128-byte pieces of K, tokens in each
+            uint32_t kw[NK], kb[NK], vw[WORDS];
+            const int unit = lane % UPR, tk = lane / UPR;
+            #pragma unroll
+            for (int j = 0; j < NK; ++j) {
+                kw[j] = __ldcs(reinterpret_cast<const uint32_t*>(k + j * 128) + lane);
+                kb[j] = *reinterpret_cast<const uint8_t*>(k + CODES + (j * TPK + tk) * (D / 16) + unit / 2);
+            }
+            if constexpr (WORDS == 4) {
+                const uint4 x = __ldcs(reinterpret_cast<const uint4*>(v) + lane);
+                vw[0] = x.x; vw[1] = x.y; vw[2] = x.z; vw[3] = x.w;
+            } else {
+                const uint2 x = __ldcs(reinterpret_cast<const uint2*>(v) + lane);
+                vw[0] = x.x; vw[1] = x.y;
+            }
+            const uint32_t vb = *reinterpret_cast<const uint16_t*>(v + CODES + (D == 128 ? g : g >> 1) * 8 + 2 * t);
+            char* ko = a.k + tok0 * row + static_cast<int64_t>(h) * D * ES;
+            char* vo = a.v + tok0 * row + static_cast<int64_t>(h) * D * ES;
+            #pragma unroll
+            for (int j = 0; j < NK; ++j) {
+                uint32_t p[4];
+                expand_full(kw[j], (kb[j] << 7) * 0x00010001u, p);
+                store_halves<TOut>(ko + (j * TPK + tk) * row + unit * 8 * ES,
+                                   make_uint4(__byte_perm(p[0], p[1], 0x5410), __byte_perm(p[2], p[3], 0x5410),
+                                              __byte_perm(p[0], p[1], 0x7632), __byte_perm(p[2], p[3], 0x7632)));
+            }
+            const uint32_t sc = __byte_perm(vb, 0, 0x4140) << 7;
+            uint32_t e[2][2 * WORDS];                  // [token][pairs of the chunk's elements]
+            #pragma unroll
+            for (int w = 0; w < WORDS; ++w) {
+                uint32_t p[4];
+                expand_full(vw[w], sc, p);
+                e[0][2 * w] = __byte_perm(p[0], p[1], 0x5410);
+                e[0][2 * w + 1] = __byte_perm(p[2], p[3], 0x5410);
+                e[1][2 * w] = __byte_perm(p[0], p[1], 0x7632);
+                e[1][2 * w + 1] = __byte_perm(p[2], p[3], 0x7632);
+            }
+            #pragma unroll
+            for (int i = 0; i < 2; ++i) {              // token 2t + i, elements g*D/8 ..
+                char* out = vo + (2 * t + i) * row;
+                if constexpr (D == 64) {
+                    store_halves<TOut>(out + g * 8 * ES, make_uint4(e[i][0], e[i][1], e[i][2], e[i][3]));
+                } else if constexpr (ES == 4) {
+                    store_halves<TOut>(out + g * 16 * ES, make_uint4(e[i][0], e[i][1], e[i][2], e[i][3]));
+                    store_halves<TOut>(out + (g * 16 + 8) * ES, make_uint4(e[i][4], e[i][5], e[i][6], e[i][7]));
+                } else {
+                    const bool odd = g & 1;
+                    uint32_t x[4], own[4];
+                    #pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        x[w] = __shfl_xor_sync(FULL, odd ? e[i][w] : e[i][4 + w], 4);
+                        own[w] = odd ? e[i][4 + w] : e[i][w];
+                    }
+                    const uint4 mine = make_uint4(own[0], own[1], own[2], own[3]), other = make_uint4(x[0], x[1], x[2], x[3]);
+                    char* pair = out + (g & ~1) * 32 + (odd ? 16 : 0);
+                    store_halves<TOut>(pair, odd ? other : mine);
+                    store_halves<TOut>(pair + 32, odd ? mine : other);
+                }
+            }
+        }
+        return;
+    }
+    constexpr int HPW = 16 / UPR;                      // head rows per half-warp
+    const int unit = lane & (UPR - 1), sub = (lane & 15) / UPR;
+    const int uk = (a.H + HPW - 1) / HPW;
+    for (int pair = 0; pair < 4; ++pair) {
+        const int64_t tok = tok0 + pair * 2 + (lane >> 4);
+        const int64_t s = __shfl_sync(FULL, slot, pair * 2 + (lane >> 4));
+        if (s < 0) continue;                           // no shuffles below
+        const int64_t blk = s / a.B;
+        const int off = static_cast<int>(s - blk * a.B), token = off & 7, e0 = unit * 8;
+        #pragma unroll 2
+        for (int r = blockIdx.y * kWarpsPerCta + warp; r < 2 * uk; r += gridDim.y * kWarpsPerCta) {
+            const bool is_v = r >= uk;
+            const int h = (is_v ? r - uk : r) * HPW + sub;
+            if (h >= a.H) continue;
+            const char* oct = (is_v ? a.vpool : a.kpool) + ((blk * a.H + h) * opb + (off >> 3)) * OCT;
+            uint32_t w, b, p[4];
+            if (is_v) {
+                w = *reinterpret_cast<const uint16_t*>(oct + int4_v_piece<D>(token, e0)) |
+                    static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(oct + int4_v_piece<D>(token, e0 + 4))) << 16;
+                b = *reinterpret_cast<const uint8_t*>(oct + int4_v_scale<D>(token, e0));
+            } else {
+                w = *reinterpret_cast<const uint32_t*>(oct + int4_k_code<D>(token, e0));
+                b = *reinterpret_cast<const uint8_t*>(oct + int4_k_scale<D>(token, e0));
+            }
+            expand_full(w, (b << 7) * 0x00010001u, p);
+            store_halves<TOut>((is_v ? a.v : a.k) + tok * row + (static_cast<int64_t>(h) * D + e0) * ES,
+                               make_uint4(__byte_perm(p[0], p[1], 0x5410), __byte_perm(p[2], p[3], 0x5410),
+                                          __byte_perm(p[0], p[1], 0x7632), __byte_perm(p[2], p[3], 0x7632)));
+        }
+    }
+}
+
+template <typename TOut>
+void gather_int4(const kv_pool* pool, const GatherArgs& a, cudaStream_t stream) {
+    const int octs = (a.n + 7) / 8, most = (a.H + kWarpsPerCta - 1) / kWarpsPerCta;
+    int gy = (8 * pool->num_sms + octs - 1) / octs;    // few tokens: the heads spread over CTAs
+    gy = gy < 1 ? 1 : gy > most ? most : gy;
+    const dim3 grid(static_cast<unsigned>(octs), static_cast<unsigned>(gy));
+    if (pool->desc.head_dim == 128) gather_int4_kernel<128, TOut><<<grid, kThreads, 0, stream>>>(a);
+    else gather_int4_kernel<64, TOut><<<grid, kThreads, 0, stream>>>(a);
 }
 
 template <kv_dtype POOL, typename TOut>
@@ -496,7 +655,7 @@ int launch_gather(const kv_pool* pool, int layer, const int64_t* slot_mapping, i
         case KV_FP8_E4M3:
             half ? gather_typed<KV_FP8_E4M3, __half>(pool, a, stream) : gather_typed<KV_FP8_E4M3, float>(pool, a, stream);
             break;
-        default: half ? gather_typed<KV_INT4, __half>(pool, a, stream) : gather_typed<KV_INT4, float>(pool, a, stream);
+        default: half ? gather_int4<__half>(pool, a, stream) : gather_int4<float>(pool, a, stream);
     }
     return cudaGetLastError() == cudaSuccess ? KV_OK : KV_ERR_CUDA;
 }

@@ -116,10 +116,7 @@ __device__ __forceinline__ void append_row(const char* src, int in_bytes, char* 
     amax = max_nan(amax, __shfl_xor_sync(FULL, amax, 1));
     amax = max_nan(amax, __shfl_xor_sync(FULL, amax, 2));          // the 4 lanes of a group of 16
     const uint32_t sb = int4_scale_byte(amax);
-    const float s = int4_scale_value(sb), inv = int4_inverse(s);
-    uint32_t piece = 0;
-    #pragma unroll
-    for (int i = 0; i < 4; ++i) piece |= int4_nibble(x[i], s, inv, 7.f * s) << (4 * i);
+    const uint32_t piece = int4_nibbles<4>(x, amax, int4_scale_value(sb));
     if (act) {
         *reinterpret_cast<uint16_t*>(oct + (is_k ? int4_k_code<D>(token, e0) : int4_v_piece<D>(token, e0))) =
             static_cast<uint16_t>(piece);

@@ -40,36 +40,56 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return d;
 }
 
+// x / y by a reciprocal of y good to an ulp or two: q = x * inv is off by a few roundings, the
+// residual x - q*y is exact in one fma, and adding residual * inv gives the exact quotient wherever
+// that is a float, so a quotient halfway between two codes or scales (common for float16 inputs)
+// stays there.  Residual correction by fma: P. Markstein, "Computation of elementary functions on
+// the IBM RISC System/6000 processor", 1990.
+__device__ __forceinline__ float int4_quotient(float x, float y, float inv) {
+    const float q = x * inv;
+    return fmaf(fmaf(-q, y, x), inv, q);
+}
+
 // Scale byte of a group whose largest magnitude is amax: min(amax / 7, 896) rounded to nearest
 // even on the byte's grid.  A NaN in the group makes the whole group NaN.
 __device__ __forceinline__ uint32_t int4_scale_byte(float amax) {
-    if (!(amax == amax)) return kInt4NanScale;
-    const float s = fminf(__fdiv_rn(amax, 7.f), kInt4MaxScale);
-    if (s < 6.103515625e-05f) return __float2uint_rn(s * 131072.f);     // below 2^-14: multiples of 2^-17
+    const float s = int4_quotient(fminf(amax, 7.f * kInt4MaxScale), 7.f, 1.f / 7.f);
     const uint32_t b = __float_as_uint(s);
-    return ((b + 0x7FFFFu + ((b >> 20) & 1u)) >> 20) - ((127u - 15u) << 3);
+    const uint32_t normal = ((b + 0x7FFFFu + ((b >> 20) & 1u)) >> 20) - ((127u - 15u) << 3);
+    // below 2^-14, multiples of 2^-17: 1.5 * 2^23 + s * 2^17 rounds to one in its low bits
+    const uint32_t small = __float_as_uint(fmaf(s, 131072.f, 12582912.f)) & 15u;
+    return !(amax == amax) ? kInt4NanScale : s < 6.103515625e-05f ? small : normal;
 }
 
 __device__ __forceinline__ float int4_scale_value(uint32_t byte) {
     return __half2float(__ushort_as_half(static_cast<unsigned short>(byte << 7)));
 }
 
-// Nibble (code + 8) of x: x / s rounded to nearest even, within -7 .. 7.  inv = 1 / s rounded (0
-// when s is 0: code 0), top = 7 s (exact): larger magnitudes, infinities among them, are that
-// code.  q = x * inv is off by at most two roundings; the residual x - q*s is exact in one fma,
-// and adding residual * inv gives the exact quotient wherever that is a float, so quotients
-// halfway between two codes (common for float16 inputs) round as x / s does.  Residual correction
-// of a quotient by fma: P. Markstein, "Computation of elementary functions on the IBM RISC
-// System/6000 processor", 1990.
-__device__ __forceinline__ uint32_t int4_nibble(float x, float s, float inv, float top) {
-    x = fminf(fmaxf(x, -top), top);
-    float q = x * inv;
-    q = fmaf(fmaf(-q, s, x), inv, q);
-    // 1.5 * 2^23 + 8 + q rounds q to an integer (the offset is even) held in the low bits
-    return __float_as_uint(q + 12582920.f) & 15u;
+__device__ __forceinline__ float int4_inverse(float s) {         // 0 for a scale of 0: code 0
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(s));
+    return s > 0.f ? r : 0.f;
 }
 
-__device__ __forceinline__ float int4_inverse(float s) { return s > 0.f ? __fdiv_rn(1.f, s) : 0.f; }
+// N nibbles (code + 8, in the low 4 N bits, the first lowest) of x / s rounded to nearest even, within
+// -7 .. 7.  An unclamped quotient is at most 7 (1 + 2^-4), which rounds to 7; only a group beyond
+// the largest scale (amax: its largest magnitude) needs the clamp.
+template <int N>
+__device__ __forceinline__ uint32_t int4_nibbles(float (&x)[N], float amax, float s) {
+    const float inv = int4_inverse(s);
+    if (!(amax <= 7.f * kInt4MaxScale)) {
+        #pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = fminf(fmaxf(x[i], -7.f * kInt4MaxScale), 7.f * kInt4MaxScale);
+    }
+    // 1.5 * 2^23 + 8 + q rounds q to an integer (the offset is even) in its low bits; the constant
+    // above them adds up to a constant, modulo 2^32
+    uint32_t w = 0;
+    constexpr uint32_t kMagic = 0x4B400000u;
+    #pragma unroll
+    for (int i = 0; i < N; ++i)
+        w += (__float_as_uint(int4_quotient(x[i], s, inv) + 12582920.f) - kMagic) << (4 * i);
+    return w;
+}
 
 // Expansion of the 8 nibbles of a word to four float16 pairs, exact: a nibble under the mantissa
 // of 1024.0 is 1024 + u (low nibble) or 1024 + 16 u, and one fma with a16 = scale / 16 and
