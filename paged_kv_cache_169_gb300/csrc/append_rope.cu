@@ -14,6 +14,8 @@
 // A warp walks over the head rows (queries, then keys, then values) with its token's table values
 // in registers and several rows' loads in flight.  Bound: HBM.
 
+#include <type_traits>
+
 #include "int4.cuh"
 #include "pool_types.cuh"
 
@@ -85,62 +87,57 @@ __device__ __forceinline__ void store_eight(char* out, const float (&f)[8]) {
     }
 }
 
-// The unit's 8 elements into pool row `at` (the block's tile of the head, token off of it).
-// IS_V only matters to 4-bit tiles; paired: lane ^ 16 holds the same unit of the token that
-// shares this one's words.
-template <int D, kv_dtype POOL>
-__device__ __forceinline__ void store_unit(char* tile, int off, int unit, float (&x)[8], float scale, bool is_v,
-                                           bool paired, bool live, int lane) {
+// Stores of one unit (8 elements of a row) into a pool, at the lane's address for head 0 (`at`, and for
+// 4-bit tiles `sc`, its group's scale byte); `head` is the byte offset of the row's head.
+// paired: lane ^ 16 holds the same unit of the token that shares this one's words of a 4-bit V tile.
+template <kv_dtype POOL, bool IS_V>
+__device__ __forceinline__ void store_unit(char* at, char* sc, int64_t head, float (&x)[8], float scale, bool paired,
+                                           bool odd, bool live, int lane) {
+    at += head;
     if constexpr (POOL == KV_F32) {
         if (!live) return;
-        float4* p = reinterpret_cast<float4*>(tile + (static_cast<int64_t>(off) * D + unit * 8) * 4);
-        p[0] = make_float4(x[0], x[1], x[2], x[3]);
-        p[1] = make_float4(x[4], x[5], x[6], x[7]);
+        reinterpret_cast<float4*>(at)[0] = make_float4(x[0], x[1], x[2], x[3]);
+        reinterpret_cast<float4*>(at)[1] = make_float4(x[4], x[5], x[6], x[7]);
     } else if constexpr (POOL == KV_F16) {
-        if (live) *reinterpret_cast<uint4*>(tile + (off * D + unit * 8) * 2) = halves(x);
+        if (live) *reinterpret_cast<uint4*>(at) = halves(x);
     } else if constexpr (POOL == KV_FP8_E4M3) {
-        if (!live) return;
         uint2 c;
         c.x = float2_to_e4m3x2(__fdiv_rn(x[0], scale), __fdiv_rn(x[1], scale)) |
               static_cast<uint32_t>(float2_to_e4m3x2(__fdiv_rn(x[2], scale), __fdiv_rn(x[3], scale))) << 16;
         c.y = float2_to_e4m3x2(__fdiv_rn(x[4], scale), __fdiv_rn(x[5], scale)) |
               static_cast<uint32_t>(float2_to_e4m3x2(__fdiv_rn(x[6], scale), __fdiv_rn(x[7], scale))) << 16;
-        *reinterpret_cast<uint2*>(tile + off * D + unit * 8) = c;
+        if (live) *reinterpret_cast<uint2*>(at) = c;
     } else {
-        float amax = 0.f;
-        #pragma unroll
-        for (int i = 0; i < 8; ++i) amax = max_nan(amax, fabsf(x[i]));
+        float amax = max_nan(max_nan(max_nan(fabsf(x[0]), fabsf(x[1])), max_nan(fabsf(x[2]), fabsf(x[3]))),
+                             max_nan(max_nan(fabsf(x[4]), fabsf(x[5])), max_nan(fabsf(x[6]), fabsf(x[7]))));
         amax = max_nan(amax, __shfl_xor_sync(FULL, amax, 1));          // the group's other unit
         const uint32_t sb = int4_scale_byte(amax);
         const uint32_t w = int4_nibbles<8>(x, amax, int4_scale_value(sb));
-        char* oct = tile + (off >> 3) * Int4<D>::OCT;
-        const int token = off & 7, e0 = unit * 8;
-        if (!is_v) {
+        if constexpr (!IS_V) {
             if (!live) return;
-            *reinterpret_cast<uint32_t*>(oct + int4_k_code<D>(token, e0)) = w;
-            if ((unit & 1) == 0) *reinterpret_cast<uint8_t*>(oct + int4_k_scale<D>(token, e0)) = sb;
-            return;
-        }
-        // the unit's two pieces lie in two words, each shared with the token's neighbour
-        const uint32_t other = __shfl_xor_sync(FULL, w, 16);
-        if (!live) return;
-        if (paired) {
-            // the even token writes the first word, the odd token the second
-            const bool odd = token & 1;
-            const uint32_t word = odd ? __byte_perm(other, w, 0x7632) : __byte_perm(w, other, 0x5410);
-            *reinterpret_cast<uint32_t*>(oct + int4_v_piece<D>(token & ~1, e0 + (odd ? 4 : 0))) = word;
+            *reinterpret_cast<uint32_t*>(at) = w;
         } else {
-            *reinterpret_cast<uint16_t*>(oct + int4_v_piece<D>(token, e0)) = static_cast<uint16_t>(w);
-            *reinterpret_cast<uint16_t*>(oct + int4_v_piece<D>(token, e0 + 4)) = static_cast<uint16_t>(w >> 16);
+            // the unit's two pieces lie in two consecutive words, each shared with the token's neighbour:
+            // paired, the even token writes the first word, the odd token the second
+            const uint32_t other = __shfl_xor_sync(FULL, w, 16);
+            if (!live) return;
+            if (paired) {
+                *reinterpret_cast<uint32_t*>(at) = odd ? __byte_perm(other, w, 0x7632) : __byte_perm(w, other, 0x5410);
+            } else {
+                *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>(w);
+                *reinterpret_cast<uint16_t*>(at + 4) = static_cast<uint16_t>(w >> 16);
+            }
         }
-        if ((unit & 1) == 0) *reinterpret_cast<uint8_t*>(oct + int4_v_scale<D>(token, e0)) = sb;
+        if ((lane & 1) == 0) *reinterpret_cast<uint8_t*>(sc + head) = sb;
     }
 }
 
-template <int D, typename TIn, kv_dtype POOL>
+enum : int { NO_ROTATION = 0, HALF_PAIRS = 1, ADJACENT_PAIRS = 2 };
+
+template <int D, typename TIn, kv_dtype POOL, int MODE>
 __global__ void __launch_bounds__(kThreads) append_rope_kernel(const __grid_constant__ RopeArgs a) {
     constexpr int UPR = D / 8, HPW = 16 / UPR;         // units per row; head rows per half-warp
-    constexpr int ESZ = sizeof(TIn);
+    constexpr int ESZ = sizeof(TIn), QSZ = POOL == KV_F32 ? 4 : 2;
     constexpr int UNROLL = ESZ == 2 ? 4 : 2;
     constexpr int ROW = POOL == KV_INT4 ? D / 2 + D / 16 : POOL == KV_FP8_E4M3 ? D : POOL == KV_F16 ? 2 * D : 4 * D;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -148,22 +145,28 @@ __global__ void __launch_bounds__(kThreads) append_rope_kernel(const __grid_cons
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int64_t tok = static_cast<int64_t>(blockIdx.x) * 2 + (lane >> 4);
-    // ---- head rows: queries, keys, values, HPW rows per half-warp and step.  The first rows are asked
-    // for before anything is known of the token (one past the end takes the pair's first)
-    const int uq = a.Hq ? (a.Hq + HPW - 1) / HPW : 0, uk = (a.H + HPW - 1) / HPW;
-    const int rows = uq + 2 * uk, step = gridDim.y * kWarpsPerCta;
+    // ---- The head rows: queries, keys, values, HPW rows per half-warp and step, dealt to the warps in
+    // turn.  The first rows are asked for before anything is known of the token (one past the end takes
+    // its neighbour's).
+    const int uq = (a.Hq + HPW - 1) / HPW, uk = (a.H + HPW - 1) / HPW;
+    const int start = blockIdx.y * kWarpsPerCta + warp, step = gridDim.y * kWarpsPerCta;
     const int64_t from = tok < a.n ? tok : tok - 1;
-    auto load = [&](int r, Raw<TIn>& raw) {
-        const int which = r < uq ? 0 : r < uq + uk ? 1 : 2;
-        const int h = min((r - (which == 0 ? 0 : which == 1 ? uq : uq + uk)) * HPW + sub, (which ? a.H : a.Hq) - 1);
-        const char* base = which == 0 ? a.q + from * a.q_stride : which == 1 ? a.k + from * a.k_stride : a.v + from * a.v_stride;
-        load_raw(base + (h * D + unit * 8) * ESZ, raw);
+    const int lane_at = (sub * D + unit * 8) * ESZ;
+    constexpr int STEP = HPW * D * ESZ;                // bytes between a half-warp's steps
+    // rows r, r + step, ... (< count) of a matrix of `heads` heads; an odd head count's last step has a
+    // row too many, which reads the last one
+    auto load = [&](const char* base, int r, int count, int heads, Raw<TIn> (&raw)[UNROLL]) {
+        #pragma unroll
+        for (int j = 0; j < UNROLL; ++j) {
+            const int i = r + j * step;
+            if (i < count) load_raw(base + i * STEP - (HPW > 1 && i * HPW + sub >= heads ? D * ESZ : 0), raw[j]);
+        }
     };
-    int r0 = blockIdx.y * kWarpsPerCta + warp;
-    Raw<TIn> next[UNROLL];
-    #pragma unroll
-    for (int j = 0; j < UNROLL; ++j)
-        if (r0 + j * step < rows) load(r0 + j * step, next[j]);
+    const char* const qp = a.q + from * a.q_stride + lane_at;
+    const char* const kp = a.k + from * a.k_stride + lane_at;
+    const char* const vp = a.v + from * a.v_stride + lane_at;
+    Raw<TIn> raw[UNROLL];
+    if (start < uq) load(qp, start, uq, a.Hq, raw);
     // ---- the token: its slot, its position, its rotation
     int64_t slot = tok < a.n ? a.slots[tok] : -1;
     int pos = 0;
@@ -172,49 +175,63 @@ __global__ void __launch_bounds__(kThreads) append_rope_kernel(const __grid_cons
         atomicOr(a.err, KV_DEVERR_SLOT);
         live = false;
     }
-    if (a.rot > 0 && live) {
+    if (MODE != NO_ROTATION && tok < a.n) {
         pos = a.positions[tok];
         if (pos < 0 || pos >= a.table_len) {
-            atomicOr(a.err, KV_DEVERR_POSITION);
+            if (live) atomicOr(a.err, KV_DEVERR_POSITION);
             live = false;
+            pos = 0;
         }
     }
     if (!__any_sync(FULL, live)) return;
-    if (!live) slot = 0;
-    const int64_t blk = slot / a.B;
-    const int off = static_cast<int>(slot - blk * a.B);
-    // both tokens live and in one 32-bit word of a 4-bit V tile
-    const int64_t other_slot = __shfl_xor_sync(FULL, live ? slot : int64_t{-2}, 16);
-    const bool paired = POOL == KV_INT4 && live && other_slot == (slot ^ 1);
-    float ks = 1.f, vs = 1.f;
-    if constexpr (POOL == KV_FP8_E4M3) {
-        ks = a.kscale[blk];
-        vs = a.vscale[blk];
-    }
     // this unit's cosines and sines: half pairs 8 of each, adjacent pairs 4 of each
     float c[8], s[8];
     const bool turned = unit * 8 < a.rot;
     const int half_units = a.rot >> 4;
     const bool low = unit < half_units;                // half pairs: the first element of each pair
-    if (a.rot > 0) {
+    if constexpr (MODE != NO_ROTATION) {
         const float* row = a.table + static_cast<int64_t>(pos) * a.rot;
-        const int i0 = !turned ? 0 : a.adjacent ? unit * 4 : (low ? unit : unit - half_units) * 8;
+        const int i0 = !turned ? 0 : MODE == ADJACENT_PAIRS ? unit * 4 : (low ? unit : unit - half_units) * 8;
         #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            if (j == 1 && a.adjacent) break;
+        for (int j = 0; j < (MODE == ADJACENT_PAIRS ? 1 : 2); ++j) {
             const float4 cv = *reinterpret_cast<const float4*>(row + i0 + 4 * j);
             const float4 sv = *reinterpret_cast<const float4*>(row + a.rot / 2 + i0 + 4 * j);
             c[4 * j] = cv.x; c[4 * j + 1] = cv.y; c[4 * j + 2] = cv.z; c[4 * j + 3] = cv.w;
             s[4 * j] = sv.x; s[4 * j + 1] = sv.y; s[4 * j + 2] = sv.z; s[4 * j + 3] = sv.w;
         }
-        if (!a.adjacent && low) {                      // x cos - y sin as x cos + y (-sin): the same roundings
+        if (MODE == HALF_PAIRS && low) {               // x cos - y sin as x cos + y (-sin): the same roundings
             #pragma unroll
             for (int i = 0; i < 8; ++i) s[i] = -s[i];
         }
     }
+    if (!live) slot = 0;
+    const int64_t blk = slot / a.B;
+    const int off = static_cast<int>(slot - blk * a.B);
+    // both tokens live and in one 32-bit word of a 4-bit V tile
+    const int64_t other_slot = __shfl_xor_sync(FULL, live ? slot : int64_t{-2}, 16);
+    const bool paired = POOL == KV_INT4 && live && other_slot == (slot ^ 1), odd = off & 1;
+    float ks = 1.f, vs = 1.f;
+    if constexpr (POOL == KV_FP8_E4M3) {
+        ks = a.kscale[blk];
+        vs = a.vscale[blk];
+    }
+    // this lane's addresses in the token's block, head `sub`
+    const int64_t tile = static_cast<int64_t>(a.B) * ROW, tile0 = (blk * a.H + sub) * tile;
+    const int e0 = unit * 8;
+    char *kat = a.kpool + tile0, *vat = a.vpool + tile0, *ksc = kat, *vsc = vat;
+    if constexpr (POOL == KV_INT4) {
+        const int oct = (off >> 3) * Int4<D>::OCT, token = off & 7;
+        ksc += oct + int4_k_scale<D>(token, e0);
+        vsc += oct + int4_v_scale<D>(token, e0);
+        kat += oct + int4_k_code<D>(token, e0);
+        vat += oct + (paired ? int4_v_piece<D>(token & ~1, e0 + (odd ? 4 : 0)) : int4_v_piece<D>(token, e0));
+    } else {
+        kat += off * ROW + e0 * (ROW / D);
+        vat += off * ROW + e0 * (ROW / D);
+    }
     const int partner = (lane & ~(UPR - 1)) | (turned ? (low ? unit + half_units : unit - half_units) : unit);
     auto rotate = [&](float (&x)[8]) {
-        if (a.adjacent) {
+        if constexpr (MODE == ADJACENT_PAIRS) {
             if (!turned) return;
             #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -222,51 +239,57 @@ __global__ void __launch_bounds__(kThreads) append_rope_kernel(const __grid_cons
                 x[2 * i] = __fsub_rn(__fmul_rn(u, c[i]), __fmul_rn(w, s[i]));
                 x[2 * i + 1] = __fadd_rn(__fmul_rn(w, c[i]), __fmul_rn(u, s[i]));
             }
-            return;
-        }
-        #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float y = __shfl_sync(FULL, x[i], partner);
-            if (turned) x[i] = __fadd_rn(__fmul_rn(x[i], c[i]), __fmul_rn(y, s[i]));
+        } else if constexpr (MODE == HALF_PAIRS) {
+            float y[8];
+            #pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(FULL, x[i], partner);
+            if (!turned) return;
+            #pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = __fadd_rn(__fmul_rn(x[i], c[i]), __fmul_rn(y[i], s[i]));
         }
     };
-    // ---- every row is read before any is written by the same lanes' warp: q_out may be q
-    for (; r0 < rows; r0 += step * UNROLL) {
-        Raw<TIn> raw[UNROLL];
+    // ---- queries
+    char* const qo = a.q_out + tok * a.qo_stride + (sub * D + e0) * QSZ;
+    int r = start;
+    for (bool first = true; r < uq; first = false) {
+        if (!first) load(qp, r, uq, a.Hq, raw);
+        __syncwarp();                                  // q_out may be q: rows are read before they are written
         #pragma unroll
-        for (int j = 0; j < UNROLL; ++j) {
-            raw[j] = next[j];
-            const int r = r0 + (UNROLL + j) * step;
-            if (r < rows) load(r, next[j]);
-        }
-        __syncwarp();
-        #pragma unroll
-        for (int j = 0; j < UNROLL; ++j) {
-            const int r = r0 + j * step;
-            if (r >= rows) break;
-            const int which = r < uq ? 0 : r < uq + uk ? 1 : 2;
-            const int h = (r - (which == 0 ? 0 : which == 1 ? uq : uq + uk)) * HPW + sub;
-            const bool here = live && h < (which ? a.H : a.Hq);
+        for (int j = 0; j < UNROLL; ++j, r += step) {
+            if (r >= uq) break;
             float x[8];
             widen(raw[j], x);
-            if (which < 2 && a.rot > 0) rotate(x);
-            if (which == 0) {
-                if (!here) continue;
-                char* p = a.q_out + tok * a.qo_stride;
-                if constexpr (POOL == KV_F32) {
-                    float4* o = reinterpret_cast<float4*>(p + (h * D + unit * 8) * 4);
-                    o[0] = make_float4(x[0], x[1], x[2], x[3]);
-                    o[1] = make_float4(x[4], x[5], x[6], x[7]);
-                } else {
-                    *reinterpret_cast<uint4*>(p + (h * D + unit * 8) * 2) = halves(x);
-                }
+            rotate(x);
+            if (!live || (HPW > 1 && r * HPW + sub >= a.Hq)) continue;
+            char* p = qo + r * (HPW * D * QSZ);
+            if constexpr (POOL == KV_F32) {
+                reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+                reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
             } else {
-                char* tile = (which == 1 ? a.kpool : a.vpool) +
-                             (blk * a.H + (here ? h : 0)) * static_cast<int64_t>(a.B) * ROW;
-                store_unit<D, POOL>(tile, off, unit, x, which == 1 ? ks : vs, which == 2, paired, here, lane);
+                *reinterpret_cast<uint4*>(p) = halves(x);
             }
         }
     }
+    // ---- keys, then values
+    auto cached = [&](auto is_v, const char* src, char* at, char* sc, float scale) {
+        constexpr bool IS_V = decltype(is_v)::value;
+        while (r < uk) {
+            load(src, r, uk, a.H, raw);
+            #pragma unroll
+            for (int j = 0; j < UNROLL; ++j, r += step) {
+                if (r >= uk) break;
+                float x[8];
+                widen(raw[j], x);
+                if constexpr (!IS_V) rotate(x);
+                const bool here = live && (HPW == 1 || r * HPW + sub < a.H);
+                store_unit<POOL, IS_V>(at, sc, r * HPW * tile, x, scale, paired, odd, here, lane);
+            }
+        }
+        r -= uk;
+    };
+    r -= uq;
+    cached(std::integral_constant<bool, false>{}, kp, kat, ksc, ks);
+    cached(std::integral_constant<bool, true>{}, vp, vat, vsc, vs);
 }
 
 template <typename TIn, kv_dtype POOL>
@@ -288,8 +311,16 @@ int launch_rope_typed(const kv_pool* pool, const RopeArgs& a, bool pdl, cudaStre
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
-    const cudaError_t rc = D == 128 ? cudaLaunchKernelEx(&cfg, append_rope_kernel<128, TIn, POOL>, a)
-                                    : cudaLaunchKernelEx(&cfg, append_rope_kernel<64, TIn, POOL>, a);
+    auto launch = [&](auto d) {
+        constexpr int DIM = decltype(d)::value;
+        if (a.rot == 0) {                              // kv_append, which rotates nothing, into 4-bit pools
+            if constexpr (POOL == KV_INT4) return cudaLaunchKernelEx(&cfg, append_rope_kernel<DIM, TIn, POOL, NO_ROTATION>, a);
+            return cudaErrorInvalidValue;
+        }
+        return a.adjacent ? cudaLaunchKernelEx(&cfg, append_rope_kernel<DIM, TIn, POOL, ADJACENT_PAIRS>, a)
+                          : cudaLaunchKernelEx(&cfg, append_rope_kernel<DIM, TIn, POOL, HALF_PAIRS>, a);
+    };
+    const cudaError_t rc = D == 128 ? launch(std::integral_constant<int, 128>{}) : launch(std::integral_constant<int, 64>{});
     if (rc != cudaSuccess) {
         cudaGetLastError();
         return KV_ERR_CUDA;
