@@ -23,7 +23,8 @@ namespace kvp {
 namespace {
 
 constexpr unsigned FULL = 0xffffffffu;
-constexpr int kThreads = 256, kWarpsPerCta = kThreads / 32;
+constexpr int kThreads = 128, kWarpsPerCta = kThreads / 32;           // append
+constexpr int kGatherThreads = 256, kGatherWarps = kGatherThreads / 32;
 
 struct RopeArgs {
     const char *q, *k, *v;
@@ -135,7 +136,7 @@ __device__ __forceinline__ void store_unit(char* at, char* sc, int64_t head, flo
 enum : int { NO_ROTATION = 0, HALF_PAIRS = 1, ADJACENT_PAIRS = 2 };
 
 template <int D, typename TIn, kv_dtype POOL, int MODE>
-__global__ void __launch_bounds__(kThreads) append_rope_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, 7) append_rope_kernel(const __grid_constant__ RopeArgs a) {
     constexpr int UPR = D / 8, HPW = 16 / UPR;         // units per row; head rows per half-warp
     constexpr int ESZ = sizeof(TIn), QSZ = POOL == KV_F32 ? 4 : 2;
     constexpr int UNROLL = ESZ == 2 ? 4 : 2;
@@ -421,7 +422,7 @@ __device__ __forceinline__ void load_stored(const char* tile, int off, int unit,
 
 // grid (tokens / 2, head splits): half-warps of one token each, as append_rope_kernel
 template <int D, kv_dtype POOL, typename TOut>
-__global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant__ GatherArgs a) {
+__global__ void __launch_bounds__(kGatherThreads) gather_kernel(const __grid_constant__ GatherArgs a) {
     constexpr int UPR = D / 8, HPW = 16 / UPR, UNROLL = 4;
     constexpr int ROW = POOL == KV_FP8_E4M3 ? D : POOL == KV_F16 ? 2 * D : 4 * D;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -440,8 +441,8 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant_
         ks = a.kscale[blk];
         vs = a.vscale[blk];
     }
-    const int uk = (a.H + HPW - 1) / HPW, rows = 2 * uk, step = gridDim.y * kWarpsPerCta;
-    for (int r0 = blockIdx.y * kWarpsPerCta + warp; r0 < rows; r0 += step * UNROLL) {
+    const int uk = (a.H + HPW - 1) / HPW, rows = 2 * uk, step = gridDim.y * kGatherWarps;
+    for (int r0 = blockIdx.y * kGatherWarps + warp; r0 < rows; r0 += step * UNROLL) {
         uint4 x[UNROLL], y[UNROLL];
         #pragma unroll
         for (int j = 0; j < UNROLL; ++j) {
@@ -523,7 +524,7 @@ __device__ __forceinline__ void store_halves(char* out, const uint4 v) {
 // neighbouring chunks then swap halves so that a store fills whole 32-byte sectors.  Other tokens go
 // one per half-warp.  Bound: HBM, most of it the output.
 template <int D, typename TOut>
-__global__ void __launch_bounds__(kThreads) gather_int4_kernel(const __grid_constant__ GatherArgs a) {
+__global__ void __launch_bounds__(kGatherThreads) gather_int4_kernel(const __grid_constant__ GatherArgs a) {
     constexpr int OCT = Int4<D>::OCT, CODES = Int4<D>::CODES, WORDS = Int4<D>::WORDS, ES = sizeof(TOut);
     constexpr int UPR = D / 8;                         // units of 8 elements per row
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
@@ -541,7 +542,7 @@ __global__ void __launch_bounds__(kThreads) gather_int4_kernel(const __grid_cons
         const int64_t blk = first / a.B;
         const int o = static_cast<int>(first - blk * a.B) >> 3;
         #pragma unroll 2
-        for (int h = blockIdx.y * kWarpsPerCta + warp; h < a.H; h += gridDim.y * kWarpsPerCta) {
+        for (int h = blockIdx.y * kGatherWarps + warp; h < a.H; h += gridDim.y * kGatherWarps) {
             const int64_t at = ((blk * a.H + h) * opb + o) * OCT;
             const char* k = a.kpool + at;
             const char* v = a.vpool + at;
@@ -617,7 +618,7 @@ __global__ void __launch_bounds__(kThreads) gather_int4_kernel(const __grid_cons
         const int64_t blk = s / a.B;
         const int off = static_cast<int>(s - blk * a.B), token = off & 7, e0 = unit * 8;
         #pragma unroll 2
-        for (int r = blockIdx.y * kWarpsPerCta + warp; r < 2 * uk; r += gridDim.y * kWarpsPerCta) {
+        for (int r = blockIdx.y * kGatherWarps + warp; r < 2 * uk; r += gridDim.y * kGatherWarps) {
             const bool is_v = r >= uk;
             const int h = (is_v ? r - uk : r) * HPW + sub;
             if (h >= a.H) continue;
@@ -641,24 +642,24 @@ __global__ void __launch_bounds__(kThreads) gather_int4_kernel(const __grid_cons
 
 template <typename TOut>
 void gather_int4(const kv_pool* pool, const GatherArgs& a, cudaStream_t stream) {
-    const int octs = (a.n + 7) / 8, most = (a.H + kWarpsPerCta - 1) / kWarpsPerCta;
+    const int octs = (a.n + 7) / 8, most = (a.H + kGatherWarps - 1) / kGatherWarps;
     int gy = (8 * pool->num_sms + octs - 1) / octs;    // few tokens: the heads spread over CTAs
     gy = gy < 1 ? 1 : gy > most ? most : gy;
     const dim3 grid(static_cast<unsigned>(octs), static_cast<unsigned>(gy));
-    if (pool->desc.head_dim == 128) gather_int4_kernel<128, TOut><<<grid, kThreads, 0, stream>>>(a);
-    else gather_int4_kernel<64, TOut><<<grid, kThreads, 0, stream>>>(a);
+    if (pool->desc.head_dim == 128) gather_int4_kernel<128, TOut><<<grid, kGatherThreads, 0, stream>>>(a);
+    else gather_int4_kernel<64, TOut><<<grid, kGatherThreads, 0, stream>>>(a);
 }
 
 template <kv_dtype POOL, typename TOut>
 void gather_typed(const kv_pool* pool, const GatherArgs& a, cudaStream_t stream) {
     const int D = pool->desc.head_dim;
     const int hpw = 16 / (D / 8), rows = 2 * ((a.H + hpw - 1) / hpw), pairs = (a.n + 1) / 2;
-    const int most = (rows + kWarpsPerCta - 1) / kWarpsPerCta;
+    const int most = (rows + kGatherWarps - 1) / kGatherWarps;
     int gy = (8 * pool->num_sms + pairs - 1) / pairs;
     gy = gy < 1 ? 1 : gy > most ? most : gy;
     const dim3 grid(static_cast<unsigned>(pairs), static_cast<unsigned>(gy));
-    if (D == 128) gather_kernel<128, POOL, TOut><<<grid, kThreads, 0, stream>>>(a);
-    else gather_kernel<64, POOL, TOut><<<grid, kThreads, 0, stream>>>(a);
+    if (D == 128) gather_kernel<128, POOL, TOut><<<grid, kGatherThreads, 0, stream>>>(a);
+    else gather_kernel<64, POOL, TOut><<<grid, kGatherThreads, 0, stream>>>(a);
 }
 
 }  // namespace
