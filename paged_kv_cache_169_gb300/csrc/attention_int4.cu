@@ -37,8 +37,10 @@ namespace {
 // One CTA per SM.  8 query heads hold two columns of state per lane and need more than 128 registers.
 template <int G> constexpr int kWarps = G == 8 ? 12 : 16;
 constexpr int kUnitCost = 2;                       // chunks that beginning and ending a unit costs a warp
-constexpr int kChunk = 32, kOcts = kChunk / 8;         // tokens and octs per chunk: one softmax update
-static_assert(32 % kOcts == 0, "a chunk's octs lie in one window of 32 oct ids");
+// Tokens per chunk, one softmax update: 4608 bytes of K and V whatever the head size.  (Head size 64
+// with 32-token chunks pays the loop's fixed part twice per byte: 0.73 of the copy peak.)
+constexpr int chunk_tokens(int head_dim) { return head_dim == 64 ? 64 : 32; }
+template <int D> constexpr int kOcts = chunk_tokens(D) / 8;
 
 // An item: a unit's part inside a warp's range.
 struct __align__(16) ItemSlot {
@@ -54,8 +56,9 @@ struct __align__(16) Held { int u, first, last, pad; };
 // One warp's stage: the chunk's K codes, V codes, then their scales, oct by oct.
 template <int D> struct Stage {
     static constexpr int CODES = Int4<D>::CODES, SCALES = D / 2;       // bytes per oct
-    static constexpr int V = kOcts * CODES, S = 2 * V;
-    static constexpr int BYTES = S + 2 * kOcts * SCALES;
+    static constexpr int OCTS = kOcts<D>, V = OCTS * CODES, S = 2 * V;
+    static constexpr int BYTES = S + 2 * OCTS * SCALES;
+    static_assert(32 % OCTS == 0, "a chunk's octs lie in one window of 32 oct ids");
 };
 
 // Dynamic shared memory, per warp: two stages (at the end the START part's rows), the next item's
@@ -291,7 +294,7 @@ __global__ void __launch_bounds__(kWarps<G> * 32, 1) attention_int4_kernel(const
     constexpr int MT = D / 16;                         // output tiles of 16 elements
     constexpr bool SPLIT = G <= 4;                     // odd columns: the weights' rounding errors
     constexpr int NQ = SPLIT ? 1 : 2;                  // query columns per lane
-    constexpr int CT = kChunk, NO = kOcts, NW = kWarps<G>;
+    constexpr int CT = chunk_tokens(D), NO = kOcts<D>, NW = kWarps<G>, NU = CT / 16;
     using St = Stage<D>;
     using Sm = Smem<D, G>;
     extern __shared__ __align__(128) char smem[];
@@ -515,9 +518,9 @@ __global__ void __launch_bounds__(kWarps<G> * 32, 1) attention_int4_kernel(const
                 const char* const pk = ring + stage * St::BYTES + St::S + (D == 128 ? lane * 2 : lane);
                 const char* const pv = ring + stage * St::BYTES + St::S + NO * St::SCALES + (D == 128 ? g : g >> 1) * 8 + 2 * t;
                 // ---- S^T = K Q^T, 16 tokens per mma
-                float x[2][2 * NQ];                    // [16 tokens][token g, token g + 8] (x query columns)
+                float x[NU][2 * NQ];                   // [16 tokens][token g, token g + 8] (x query columns)
                 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
+                for (int u = 0; u < NU; ++u) {
                     const Words<WORDS> k0 = lds_words<WORDS>(pc + 2 * u * St::CODES);
                     const Words<WORDS> k1 = lds_words<WORDS>(pc + (2 * u + 1) * St::CODES);
                     uint32_t b0, b1;                   // the lane's scales of 16 elements: two, D 64: one
@@ -549,7 +552,7 @@ __global__ void __launch_bounds__(kWarps<G> * 32, 1) attention_int4_kernel(const
                 const int first = tok == 0 ? lo : 0;
                 if (nt < CT || first > 0) {            // rows outside [first, nt) may hold anything:
                     #pragma unroll                     // scores of -inf, and V scales of zero
-                    for (int u = 0; u < 2; ++u) {
+                    for (int u = 0; u < NU; ++u) {
                         const int t0 = 16 * u + g, t1 = t0 + 8;
                         #pragma unroll
                         for (int q = 0; q < NQ; ++q) {
@@ -557,10 +560,11 @@ __global__ void __launch_bounds__(kWarps<G> * 32, 1) attention_int4_kernel(const
                             if (t1 < first || t1 >= nt) x[u][NQ + q] = -CUDART_INF_F;
                         }
                     }
-                    if (lane < first || lane >= nt) {  // token `lane` of the chunk: its D/16 scales
-                        char* z = ring + stage * St::BYTES + St::S + (NO + lane / 8) * St::SCALES + lane % 8;
+                    for (int r = lane; r < CT; r += 32) {
+                        if (r >= first && r < nt) continue;
+                        char* z = ring + stage * St::BYTES + St::S + (NO + r / 8) * St::SCALES + r % 8;
                         #pragma unroll
-                        for (int i = 0; i < D / 16; ++i) z[8 * i] = 0;
+                        for (int i = 0; i < D / 16; ++i) z[8 * i] = 0;         // the token's D/16 scales
                     }
                     __syncwarp();
                 }
@@ -568,7 +572,9 @@ __global__ void __launch_bounds__(kWarps<G> * 32, 1) attention_int4_kernel(const
                 // them into log2-domain scores
                 #pragma unroll
                 for (int q = 0; q < NQ; ++q) {
-                    float mx = fmaxf(fmaxf(x[0][q], x[0][NQ + q]), fmaxf(x[1][q], x[1][NQ + q]));
+                    float mx = fmaxf(x[0][q], x[0][NQ + q]);
+                    #pragma unroll
+                    for (int u = 1; u < NU; ++u) mx = fmaxf(mx, fmaxf(x[u][q], x[u][NQ + q]));
                     if (__any_sync(FULL, mx > m[q] + slack)) {
                         #pragma unroll
                         for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
@@ -585,7 +591,7 @@ __global__ void __launch_bounds__(kWarps<G> * 32, 1) attention_int4_kernel(const
                 }
                 auto weight = [&](float v, int q) { return ex2_approx((v - m[q]) * xs); };
                 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
+                for (int u = 0; u < NU; ++u) {
                     uint32_t pb0, pb1;
                     if constexpr (SPLIT) {
                         const float p0 = weight(x[u][0], 0), p1 = weight(x[u][1], 0);
@@ -786,15 +792,15 @@ int plan_attention_int4(const kv_pool* pool, int batch, int max_context, int par
     if (!valid_group(d, group)) return KV_ERR_INVALID_ARG;
     if (partition_tokens < 0 || partition_tokens % kPartAlign != 0 || partition_tokens > (1 << 24))
         return KV_ERR_INVALID_ARG;
-    static_assert(kPartAlign == kChunk, "a partition is whole chunks");
+    const int chunk = chunk_tokens(d.head_dim);
     // a sliding window bounds the tokens read per sequence (window + up to 7 masked rows)
     const int64_t span = window > 0 && window + 32 < max_context ? window + 32 : max_context;
-    const int64_t chunks = span > 0 ? (span + kChunk - 1) / kChunk : 1;
+    const int64_t chunks = span > 0 ? (span + chunk - 1) / chunk : 1;
     // the kernel numbers a launch's chunks with an int
     if (units_of(pool, batch) * (chunks + kUnitCost) >= (int64_t{1} << 31)) return KV_ERR_INVALID_ARG;
-    constexpr int kMinChunks = 4;                       // below 128 tokens a range costs more than it spreads
+    constexpr int kMinTokens = 128;                     // below that a range costs more than it spreads
     *plan = AttnPlan{};
-    plan->partition = partition_tokens ? partition_tokens / kChunk : kMinChunks;
+    plan->partition = partition_tokens ? (partition_tokens + chunk - 1) / chunk : kMinTokens / chunk;
     plan->max_parts = static_cast<int>(chunks);
     plan->group = group;
     plan->window = window;
