@@ -4,7 +4,7 @@
 // Per 16 tokens and K/V head, with the tokens (and the output's elements) as the M side of
 // mma.m16n8k16 and the query heads as its N side:
 //   S^T  = K Q^T        A = K expanded in registers, B = the query rows
-//   softmax             fp32, log2 domain, running maximum raised only when exceeded by 8
+//   softmax             fp32, log2 domain, the base raised only when the weights would leave float16
 //   O^T += V^T P^T      A = V^T expanded in registers, B = P^T from the S accumulators
 //                       (movmatrix)
 // Up to 4 query heads per K/V head take the even columns and the odd column beside each holds
@@ -216,22 +216,42 @@ __device__ __forceinline__ void merge_row(const AttnArgs& a, int64_t slot, int c
     const int64_t row = slot * G + r, step = static_cast<int64_t>(stride) * G;
     const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + row;
     float4* po = reinterpret_cast<float4*>(a.part_o + row * D) + sub;
+    // lane j holds part j's (m, l) of each 32, which arrive together with the first parts' rows: a unit
+    // of few parts costs one round trip
+    constexpr int AHEAD = 8;
     RowAcc<1> x;
     x.m = -CUDART_INF_F;
     x.l = 0.f;
     x.o[0] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = lane; k < count; k += 32) x.m = fmaxf(x.m, __ldcg(ml + k * step).x);
-    x.m = warp_max(x.m);
-    #pragma unroll 8
-    for (int k = 0; k < count; ++k) {
-        const float2 v = __ldcg(ml + k * step);
-        const float4 o = __ldcg(po + k * step * (D / 4));
-        const float w = ex2_approx(v.x - x.m);
-        x.l = fmaf(v.y, w, x.l);
-        x.o[0].x = fmaf(w, o.x, x.o[0].x);
-        x.o[0].y = fmaf(w, o.y, x.o[0].y);
-        x.o[0].z = fmaf(w, o.z, x.o[0].z);
-        x.o[0].w = fmaf(w, o.w, x.o[0].w);
+    #pragma unroll 1
+    for (int k0 = 0; k0 < count; k0 += 32) {
+        const int n = min(32, count - k0);
+        const float2 v = lane < n ? __ldcg(ml + (k0 + lane) * step) : make_float2(-CUDART_INF_F, 0.f);
+        float4 rows[AHEAD];
+        auto fetch = [&](int k) {
+            #pragma unroll
+            for (int i = 0; i < AHEAD; ++i)
+                if (k + i < n) rows[i] = __ldcg(po + (k0 + k + i) * step * (D / 4));
+        };
+        fetch(0);
+        const float mx = fmaxf(x.m, warp_max(v.x)), old = ex2_approx(x.m - mx);
+        const float w = ex2_approx(v.x - mx);          // 0 past the end
+        x.m = mx;
+        x.l = fmaf(x.l, old, warp_sum(v.y * w));
+        x.o[0] = make_float4(x.o[0].x * old, x.o[0].y * old, x.o[0].z * old, x.o[0].w * old);
+        #pragma unroll 1
+        for (int k = 0; k < n; k += AHEAD) {
+            #pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                if (k + i >= n) break;
+                const float f = __shfl_sync(FULL, w, k + i);
+                x.o[0].x = fmaf(f, rows[i].x, x.o[0].x);
+                x.o[0].y = fmaf(f, rows[i].y, x.o[0].y);
+                x.o[0].z = fmaf(f, rows[i].z, x.o[0].z);
+                x.o[0].w = fmaf(f, rows[i].w, x.o[0].w);
+            }
+            fetch(k + AHEAD);
+        }
     }
     __syncwarp();                                      // every lane has read the first part
     if (lane >= LPR) return;
@@ -398,7 +418,10 @@ __global__ void __launch_bounds__(kWarps<G> * 32, 1) attention_int4_kernel(const
     const int rng = rng0 + (warp < k ? warp : k);
     int pos = range_begin(min(rng, ranges));           // first chunk not yet taken
     const int end = warp < k ? range_begin(min(rng + 1, ranges)) : pos;
-    const float xs = a.qscale * 16.f, slack = fminf(8.f / xs, 1e30f);
+    const float xs = a.qscale * 16.f;                  // raw sum -> log2-domain score
+    // Weights are 2^(score - base), the base between 7 and 15 below the running maximum: at most 2^15
+    // in float16, and normal there down to 2^-21 of the largest.
+    const float lift = fminf(7.f / xs, 4e29f), slack = fminf(15.f / xs, 1e30f);
     const int col = SPLIT ? g >> 1 : g;                // query of mma column g (odd columns of SPLIT: none)
     const bool has_q = !(SPLIT && (g & 1)) && col < G;
     float ot[MT][4];
@@ -568,8 +591,7 @@ __global__ void __launch_bounds__(kWarps<G> * 32, 1) attention_int4_kernel(const
                     }
                     __syncwarp();
                 }
-                // ---- softmax over the chunk: m is the running maximum of the raw sums, xs turns
-                // them into log2-domain scores
+                // ---- softmax over the chunk: m is the base, in raw sums
                 #pragma unroll
                 for (int q = 0; q < NQ; ++q) {
                     float mx = fmaxf(x[0][q], x[0][NQ + q]);
@@ -578,7 +600,7 @@ __global__ void __launch_bounds__(kWarps<G> * 32, 1) attention_int4_kernel(const
                     if (__any_sync(FULL, mx > m[q] + slack)) {
                         #pragma unroll
                         for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
-                        const float m_new = fmaxf(m[q], mx), corr = ex2_approx((m[q] - m_new) * xs);
+                        const float m_new = fmaxf(m[q], mx - lift), corr = ex2_approx((m[q] - m_new) * xs);
                         m[q] = m_new;
                         l[q] *= corr;
                         #pragma unroll

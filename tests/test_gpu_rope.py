@@ -304,4 +304,8 @@ def test_python_refusals():
         cache.gather(0, slots, out_dtype=torch.bfloat16)
     with pytest.raises(abi.KvError):
         cache.append_rope(0, k, k, slots, pos, rope_table(4, 128))          # more than the head
+    with pytest.raises(abi.KvError):
+        cache.append_rope(0, k[:1].expand(3, -1, -1), k, slots, pos, tab)   # rows of stride 0
+    with pytest.raises(abi.KvError):
+        cache.append_rope(0, k, k, slots, pos, tab, q=k, q_out=torch.empty_like(k[:1]).expand(3, -1, -1))
     cache.close()
