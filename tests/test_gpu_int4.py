@@ -359,3 +359,129 @@ def test_prompt_decode_and_read_back_together(G):
         assert np.array_equal(v.double().cpu().numpy(), model[s][1])
     assert cache.device_error() == 0
     cache.close()
+
+
+def test_decode_step_in_one_call():
+    """kv_decode_step over a 4-bit pool (slot reservation, copy-on-write of a forked block, copies,
+    fused append and attention) against append_rope-free steps made call by call: same bits."""
+    import ctypes
+    H, d, B, prompt, cands, steps = 3, 128, 16, 37, 3, 6
+    runs = []
+    for one_call in (True, False):
+        rng = np.random.default_rng(14)
+        cache = PagedKVCache(1, 32, B, H, d, "int4")
+        for t in cache.k + cache.v:
+            t.fill_(0xFF)
+        alloc = BlockAllocator(32, B, rng.permutation(32))
+        root = alloc.new_seq()
+        slots, _ = alloc.append_slots(root, prompt)
+        pk, pv = (torch.from_numpy(rng.standard_normal((prompt, H, d)).astype(np.float16)).cuda() for _ in range(2))
+        cache.append(0, pk, pv, torch.tensor(slots, device="cuda"))
+        seqs = [root] + [alloc.fork(root) for _ in range(cands - 1)]
+        nb = -(-(prompt + steps) // B)
+        width = cands * nb + 3 * cands
+        meta = torch.empty(width, dtype=torch.int32, device="cuda")
+        x = torch.empty(3, cands, H, d, dtype=torch.float16, device="cuda")
+        out = torch.empty(cands, H, d, device="cuda")
+        ws = cache.zeroed_workspace(cands, prompt + steps)
+        outs = []
+        for _ in range(steps):
+            new = torch.from_numpy(rng.standard_normal((3, cands, H, d)).astype(np.float16)).pin_memory()
+            if one_call:
+                a = abi.kv_decode_args()
+                a.q, a.k_new, a.v_new, a.in_dtype = x[0].data_ptr(), x[1].data_ptr(), x[2].data_ptr(), abi.KV_F16
+                a.out, a.block_tables, a.max_blocks_per_seq = out.data_ptr(), meta.data_ptr(), nb
+                a.context_lens, a.batch, a.max_context = meta.data_ptr() + 4 * cands * nb, cands, prompt + steps
+                a.scale, a.workspace, a.workspace_bytes = 0.1, ws.data_ptr(), ws.numel()
+                a.stream = torch.cuda.current_stream().cuda_stream
+                a.flags = abi.KV_DECODE_WORKSPACE_ZEROED | abi.KV_DECODE_PDL
+                staging = torch.empty(width, dtype=torch.int32).pin_memory()
+                back = torch.empty(cands, H, d).pin_memory()
+                abi.kv_decode_step(alloc.handle, cache.handle, (ctypes.c_int32 * cands)(*seqs), cands, nb,
+                                   staging.data_ptr(), meta.data_ptr(), new.data_ptr(), x.data_ptr(), x.numel() * 2,
+                                   back.data_ptr(), out.numel() * 4, a)
+                torch.cuda.synchronize()
+                outs.append(back.clone())
+            else:
+                slots, pairs = [], []
+                for s in seqs:
+                    sl, cow = alloc.append_slots(s, 1)
+                    slots += sl
+                    pairs += [cow] if cow else []
+                if pairs:
+                    cache.copy_blocks(torch.tensor(pairs, dtype=torch.int32, device="cuda"))
+                q, k, v = new.cuda()
+                cache.append(0, k, v, torch.tensor(slots, device="cuda"))
+                tabs, lens = alloc.build_tables(seqs, nb)
+                outs.append(cache.attention(0, q, torch.tensor(tabs, dtype=torch.int32, device="cuda"),
+                                            torch.tensor(lens, dtype=torch.int32, device="cuda"), prompt + steps, 0.1).cpu())
+        assert cache.device_error() == 0
+        runs.append((torch.stack(outs), cache.k[0].cpu(), cache.v[0].cpu()))
+        cache.close()
+    for a, b in zip(*runs):
+        assert torch.equal(a, b)
+
+
+def test_blocks_beyond_four_gigabytes():
+    """Slots whose byte offset in the pool needs more than 32 bits: append, read back and attend."""
+    B, H, d = 16, 40, 128
+    nb = 100_000                                        # 4.6 GB each of K and V
+    cache = PagedKVCache(1, nb, B, H, d, "int4")
+    rng = np.random.default_rng(15)
+    n = 50
+    tab = np.array([[nb - 1, 3, nb - 5, 93_207]], dtype=np.int32)
+    slots = np.array([tab[0][p // B] * B + p % B for p in range(n)], dtype=np.int64)
+    k, v = (rng.standard_normal((n, H, d)).astype(np.float16) for _ in range(2))
+    cache.append(0, torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(), torch.from_numpy(slots).cuda())
+    kb, vb = cache.gather(0, torch.from_numpy(slots).cuda())
+    kv = [O4.dequantize(*O4.quantize(x)) for x in (k, v)]
+    assert np.array_equal(kb.double().cpu().numpy(), kv[0]) and np.array_equal(vb.double().cpu().numpy(), kv[1])
+    q = rng.standard_normal((1, H, d)).astype(np.float16)
+    out = cache.attention(0, torch.from_numpy(q).cuda(), torch.from_numpy(tab).cuda(),
+                          torch.tensor([n], dtype=torch.int32, device="cuda"), n, 0.1)
+    want = OA.decode_attention(q, [kv[0]], [kv[1]], 0.1)
+    mag = max(np.max(np.abs(kv[0][:, h]) @ np.abs(q[0, h].astype(np.float64))) for h in range(H)) * 0.1
+    e = 136 * 2.0 ** -23 * mag + 2.0 ** -21 + (n / 16 + 40) * 2.0 ** -24 + d * 2.0 ** -25 * np.max(np.abs(kv[0])) * 0.1
+    assert np.max(np.abs(out.double().cpu().numpy() - want)) <= 2 * e * np.max(np.abs(kv[1]))
+    assert cache.device_error() == 0
+    cache.close()
+
+
+@pytest.mark.parametrize("G,d", [(1, 128), (8, 128), (2, 64)])
+def test_one_long_context_over_every_sm(G, d):
+    """A single (sequence, head) cut into more ranges than a merge step joins, with and without
+    whole units beside it, twice: the same bits, within the tolerance of the oracle."""
+    rng = np.random.default_rng(16)
+    lens, H, B = [40_003, 70, 0, 3000], 1, 32
+    cache, tab, pools = build(rng, lens, H, d, B)
+    to_cache(cache, pools)
+    q = rng.standard_normal((len(lens), H * G, d)).astype(np.float16)
+    want, tol = oracle(pools, tab, lens, q, B, d, 0.1)
+    t = [torch.from_numpy(x).cuda() for x in (q, tab, np.array(lens, dtype=np.int32))]
+    ws = cache.zeroed_workspace(len(lens), 50_000, num_q_heads=H * G)
+    outs = [cache.attention_ex(0, *t, 50_000, 0.1, workspace=ws, flags=abi.KV_DECODE_WORKSPACE_ZEROED).clone()
+            for _ in range(2)]
+    assert torch.equal(outs[0], outs[1])
+    assert np.max(np.abs(outs[0].double().cpu().numpy() - want)) <= tol
+    assert cache.device_error() == 0
+    cache.close()
+
+
+def test_refusals():
+    cache = PagedKVCache(1, 8, 16, 2, 128, "int4")
+    q = torch.zeros(1, 6, 128, device="cuda").half()
+    tab, ln = torch.zeros(1, 4, dtype=torch.int32, device="cuda"), torch.ones(1, dtype=torch.int32, device="cuda")
+    with pytest.raises(abi.KvError):                    # 3 query heads per K/V head
+        cache.attention_gqa(0, q, tab, ln, 64, 0.1)
+    for bad in (dict(partition_tokens=33), dict(partition_tokens=-32), dict(window=-1)):
+        with pytest.raises(abi.KvError):
+            cache.attention_ex(0, q[:, :2].contiguous(), tab, ln, 64, 0.1, **bad)
+    groups = torch.tensor([[0, 2, 16]], dtype=torch.int32, device="cuda")
+    with pytest.raises(abi.KvError):                    # prefix groups need an fp16 or FP8 pool
+        cache.attention_ex(0, q[:1, :2].expand(2, 2, 128).contiguous(), tab.expand(2, 4).contiguous(), ln.expand(2).contiguous(),
+                           64, 0.1, prefix_groups=groups)
+    with pytest.raises(ValueError):
+        PagedKVCache(1, 8, 16, 2, 128, "int3")
+    with pytest.raises(abi.KvError):
+        PagedKVCache(1, 8, 16, 2, 96, "int4")
+    cache.close()

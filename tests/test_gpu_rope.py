@@ -309,3 +309,19 @@ def test_python_refusals():
     with pytest.raises(abi.KvError):
         cache.append_rope(0, k, k, slots, pos, tab, q=k, q_out=torch.empty_like(k[:1]).expand(3, -1, -1))
     cache.close()
+
+
+def test_rope_and_gather_beyond_four_gigabytes():
+    """fp16 slots whose byte offset needs more than 32 bits."""
+    B, H, d, nb = 16, 40, 128, 30_000                  # 4.9 GB each of K and V
+    cache = PagedKVCache(1, nb, B, H, d, "f16")
+    slots = torch.tensor([nb * B - 1, 5, 27_001 * B + 3], device="cuda")
+    pos = torch.tensor([0, 7, 19], dtype=torch.int32, device="cuda")
+    k, v = (torch.randn(3, H, d, device="cuda").half() for _ in range(2))
+    tab = rope_table(20, d)
+    cache.append_rope(0, k, v, slots, pos, tab)
+    kb, vb = cache.gather(0, slots)
+    want = OR.rotate(k.cpu().numpy(), tab.cpu().numpy()[pos.cpu().numpy()], d, False, np.float32).astype(np.float16)
+    assert np.array_equal(kb.cpu().numpy(), want) and torch.equal(vb, v)
+    assert cache.device_error() == 0
+    cache.close()
