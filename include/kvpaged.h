@@ -290,7 +290,8 @@ KV_API int kv_swap_in(kv_pool* pool, const void* host_src, const int32_t* blocks
  * (0 on invalid arguments).  partition_tokens as in paged_decode_attention.  Arguments
  * whose split-context work would exceed 2^30 items per launch of 1024 sequences
  * (min(batch, 1024) x num_heads x ceil(max_context / partition)) are invalid here and in
- * every decode entry point. */
+ * every decode entry point (4-bit pools: 2^31 chunks of 32 tokens, 64 with head_dim 64, and
+ * two more per sequence and head). */
 KV_API size_t paged_decode_workspace_size(const kv_pool* pool, int batch, int max_context,
                                    int partition_tokens);
 
@@ -322,6 +323,8 @@ KV_API size_t paged_decode_workspace_size(const kv_pool* pool, int batch, int ma
  *                 split into equal parts of at most that many tokens, attended per
  *                 partition and merged exactly (log-sum-exp) in the same launch by the
  *                 warp that finishes the last partition of that sequence and head.
+ *                 4-bit pools cut the whole call into equal ranges of tokens, one per warp:
+ *                 there partition_tokens is the least tokens of a range (0: 128).
  *   workspace     device, >= paged_decode_workspace_size(...) bytes, 256-byte aligned,
  *                 contents need not be initialised; not shared between concurrent calls.
  * Arithmetic: fp32 scores, fp32 online softmax, fp32 accumulation of V.  For F16 and
