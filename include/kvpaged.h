@@ -185,7 +185,7 @@ KV_API int kv_append(kv_pool* pool, int layer, const void* k, const void* v, kv_
  *   in_dtype       element type of q, k and v; rules as kv_append.
  *   q_stride, k_stride, v_stride, q_out_stride  elements between the rows of two tokens (heads
  *                  are contiguous in a row), so q, k and v may be views of one packed
- *                  projection; at least a row, and a multiple of 16 bytes.
+ *                  projection; at least a row, below 2^28, and a multiple of 16 bytes.
  *   slot_mapping   device int64 [num_tokens].  slot < 0: a padding token, of which nothing is
  *                  used and nothing written, q_out included (its rows may be read).  A slot outside the
  *                  pool sets KV_DEVERR_SLOT and the token is skipped the same way.  The slots
@@ -429,8 +429,8 @@ KV_API int paged_decode_attention_gqa(kv_pool* pool, int layer, const void* q, i
  *                chunks below those rows) are fetched while that kernel is still
  *                finishing.  True in a model's layer loop (the kernel before a layer's
  *                attention does not write its pool) and in a loop of fused decode steps
- *                over one layer; false right after kv_copy_blocks, kv_swap_in or kv_append
- *                into rows this call reads.
+ *                over one layer; false right after kv_copy_blocks, kv_swap_in, kv_append
+ *                or kv_append_rope into other rows this call reads.
  *     KV_DECODE_OUT_F16  out is float16 [batch][num_q_heads][head_dim] instead of float32:
  *                each element is the float32 result rounded to nearest even (beyond the
  *                float16 range: +-inf), as the attention output of [KV Cache篇] §3.1 is cast

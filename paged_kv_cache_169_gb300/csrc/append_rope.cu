@@ -298,10 +298,10 @@ int launch_rope_typed(const kv_pool* pool, const RopeArgs& a, bool pdl, cudaStre
     const int D = pool->desc.head_dim;
     const int hpw = 16 / (D / 8);
     const int uq = a.Hq ? (a.Hq + hpw - 1) / hpw : 0, rows = uq + 2 * ((a.H + hpw - 1) / hpw);
-    const int pairs = (a.n + 1) / 2;
+    const int pairs = a.n / 2 + a.n % 2;
     // few tokens: the head rows spread over CTAs, one step each; many: one CTA per token pair
     const int most = (rows + kWarpsPerCta - 1) / kWarpsPerCta;
-    int gy = (8 * pool->num_sms + pairs - 1) / pairs;
+    int gy = (8 * pool->num_sms - 1) / pairs + 1;
     gy = gy < 1 ? 1 : gy > most ? most : gy;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -642,8 +642,8 @@ __global__ void __launch_bounds__(kGatherThreads) gather_int4_kernel(const __gri
 
 template <typename TOut>
 void gather_int4(const kv_pool* pool, const GatherArgs& a, cudaStream_t stream) {
-    const int octs = (a.n + 7) / 8, most = (a.H + kGatherWarps - 1) / kGatherWarps;
-    int gy = (8 * pool->num_sms + octs - 1) / octs;    // few tokens: the heads spread over CTAs
+    const int octs = a.n / 8 + (a.n % 8 != 0), most = (a.H + kGatherWarps - 1) / kGatherWarps;
+    int gy = (8 * pool->num_sms - 1) / octs + 1;    // few tokens: the heads spread over CTAs
     gy = gy < 1 ? 1 : gy > most ? most : gy;
     const dim3 grid(static_cast<unsigned>(octs), static_cast<unsigned>(gy));
     if (pool->desc.head_dim == 128) gather_int4_kernel<128, TOut><<<grid, kGatherThreads, 0, stream>>>(a);
@@ -653,9 +653,9 @@ void gather_int4(const kv_pool* pool, const GatherArgs& a, cudaStream_t stream) 
 template <kv_dtype POOL, typename TOut>
 void gather_typed(const kv_pool* pool, const GatherArgs& a, cudaStream_t stream) {
     const int D = pool->desc.head_dim;
-    const int hpw = 16 / (D / 8), rows = 2 * ((a.H + hpw - 1) / hpw), pairs = (a.n + 1) / 2;
+    const int hpw = 16 / (D / 8), rows = 2 * ((a.H + hpw - 1) / hpw), pairs = a.n / 2 + a.n % 2;
     const int most = (rows + kGatherWarps - 1) / kGatherWarps;
-    int gy = (8 * pool->num_sms + pairs - 1) / pairs;
+    int gy = (8 * pool->num_sms - 1) / pairs + 1;
     gy = gy < 1 ? 1 : gy > most ? most : gy;
     const dim3 grid(static_cast<unsigned>(pairs), static_cast<unsigned>(gy));
     if (D == 128) gather_kernel<128, POOL, TOut><<<grid, kGatherThreads, 0, stream>>>(a);

@@ -504,14 +504,16 @@ __global__ void __launch_bounds__(kWarps<G> * 32, 1) attention_int4_kernel(const
                 }
                 if (n > 0) {
                     if (a.k_new != nullptr && c0 + n == cps && ctx > 0) {
-                        // fused append: the newest token goes to its slot before the item's copies
+                        // fused append: the newest token goes to its slot before the item's copies (a bad
+                        // block id, flagged by load_oids, takes none)
                         const int last = ctx - 1, o = last >> 3;
-                        int id = a.tables[static_cast<int64_t>(s) * a.max_blocks + (o >> lg_opb)];
-                        if (id < 0 || id >= a.num_blocks) id = 0;      // flagged by load_oids
-                        const int64_t to = (((static_cast<int64_t>(id) * a.H + h) << lg_opb) + (o & (opb - 1))) * OCT;
-                        const int64_t row = (static_cast<int64_t>(s) * a.H + h) * D * a.in_bytes;
-                        append_row<D>(a.k_new + row, a.in_bytes, a.kpool + to, last & 7, true, lane);
-                        append_row<D>(a.v_new + row, a.in_bytes, a.vpool + to, last & 7, false, lane);
+                        const int id = a.tables[static_cast<int64_t>(s) * a.max_blocks + (o >> lg_opb)];
+                        if (id >= 0 && id < a.num_blocks) {
+                            const int64_t to = (((static_cast<int64_t>(id) * a.H + h) << lg_opb) + (o & (opb - 1))) * OCT;
+                            const int64_t row = (static_cast<int64_t>(s) * a.H + h) * D * a.in_bytes;
+                            append_row<D>(a.k_new + row, a.in_bytes, a.kpool + to, last & 7, true, lane);
+                            append_row<D>(a.v_new + row, a.in_bytes, a.vpool + to, last & 7, false, lane);
+                        }
                         __syncwarp();                  // the copies below read the row
                     }
                     const char* q = static_cast<const char*>(a.q) + (static_cast<int64_t>(s) * a.H + h) * G * D * 2;

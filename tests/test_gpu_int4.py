@@ -261,6 +261,17 @@ def test_bad_tables_and_lengths_are_flagged():
     out = cache.attention(0, q, torch.from_numpy(bad).cuda(), ln, 40, 0.1)
     assert cache.device_error() == abi.KV_DEVERR_BLOCK_ID
     assert torch.equal(out[0], good[0]) and torch.isfinite(out).all()
+    # a fused append whose block id is bad stores nothing
+    before = [cache.k[0].clone(), cache.v[0].clone()]
+    bad[1, 1], bad[1, 2] = tab[1, 1], -7
+    kn = torch.ones(2, 1, d, device="cuda").half()
+    cache.attention_append(0, q, kn, kn, torch.from_numpy(bad).cuda(), ln, 40, 0.1)
+    assert cache.device_error() == abi.KV_DEVERR_BLOCK_ID
+    last = int(tab[0, 39 // B])
+    for t, b4 in zip((cache.k[0], cache.v[0]), before):
+        changed = (t != b4).flatten(1).any(1).nonzero().flatten().tolist()
+        assert changed in ([], [last])                 # only the other sequence's block
+        t.copy_(b4)
     long = torch.tensor([41, -1], dtype=torch.int32, device="cuda")
     out = cache.attention(0, q, torch.from_numpy(tab).cuda(), long, 40, 0.1)
     assert cache.device_error() == abi.KV_DEVERR_CONTEXT
