@@ -81,13 +81,16 @@ __device__ __forceinline__ uint32_t int4_nibbles(float (&x)[N], float amax, floa
         #pragma unroll
         for (int i = 0; i < N; ++i) x[i] = fminf(fmaxf(x[i], -7.f * kInt4MaxScale), 7.f * kInt4MaxScale);
     }
-    // 1.5 * 2^23 + 8 + q rounds q to an integer (the offset is even) in its low bits; the constant
-    // above them adds up to a constant, modulo 2^32
-    uint32_t w = 0;
+    // 1.5 * 2^23 + 8 + q rounds q to an integer (the offset is even) in its low bits; what the constant's
+    // high bits add up to, modulo 2^32, is taken off once
     constexpr uint32_t kMagic = 0x4B400000u;
+    uint32_t w = 0, high = 0;
     #pragma unroll
-    for (int i = 0; i < N; ++i)
-        w += (__float_as_uint(int4_quotient(x[i], s, inv) + 12582920.f) - kMagic) << (4 * i);
+    for (int i = 0; i < N; ++i) {
+        w += __float_as_uint(int4_quotient(x[i], s, inv) + 12582920.f) << (4 * i);
+        high += kMagic << (4 * i);
+    }
+    w -= high;
     return w;
 }
 
