@@ -12,7 +12,9 @@
 // and every input is read once.  The two half-warps take two consecutive tokens: where their slots
 // share a 32-bit word of a 4-bit V tile (slot 2m and 2m + 1), the pair of lanes writes whole words.
 // A warp walks over the head rows (queries, then keys, then values) with its token's table values
-// in registers and several rows' loads in flight.  Bound: HBM.
+// in registers and several rows' loads in flight.  Bound: HBM (57.4 us for 8192 tokens of 64 + 8 heads into float16,
+// 0.87 of a copy's rate); with a 4-bit pool, the instructions that quantise (43 us for 4097 tokens of
+// 40 + 40 heads, 0.71).
 
 #include <type_traits>
 

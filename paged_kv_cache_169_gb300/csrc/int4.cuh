@@ -31,6 +31,7 @@ template <int D> struct Int4 {
 #ifdef __CUDACC__
 
 constexpr float kInt4MaxScale = 896.f;
+constexpr float kInt4MinNormal = 6.103515625e-05f;     // 2^-14: below it the scales are multiples of 2^-17
 constexpr uint32_t kInt4NanScale = 0xFFu;              // 0x7F80 as float16: NaN
 
 // max that returns NaN when either operand is NaN
@@ -58,7 +59,7 @@ __device__ __forceinline__ uint32_t int4_scale_byte(float amax) {
     const uint32_t normal = ((b + 0x7FFFFu + ((b >> 20) & 1u)) >> 20) - ((127u - 15u) << 3);
     // below 2^-14, multiples of 2^-17: 1.5 * 2^23 + s * 2^17 rounds to one in its low bits
     const uint32_t small = __float_as_uint(fmaf(s, 131072.f, 12582912.f)) & 15u;
-    return !(amax == amax) ? kInt4NanScale : s < 6.103515625e-05f ? small : normal;
+    return !(amax == amax) ? kInt4NanScale : s < kInt4MinNormal ? small : normal;
 }
 
 __device__ __forceinline__ float int4_scale_value(uint32_t byte) {
@@ -72,14 +73,15 @@ __device__ __forceinline__ float int4_inverse(float s) {         // 0 for a scal
 }
 
 // N nibbles (code + 8, in the low 4 N bits, the first lowest) of x / s rounded to nearest even, within
-// -7 .. 7.  An unclamped quotient is at most 7 (1 + 2^-4), which rounds to 7; only a group beyond
-// the largest scale (amax: its largest magnitude) needs the clamp.
+// -7 .. 7.  With a scale of 4 significant bits a quotient is at most 7 (1 + 2^-4), which rounds to 7;
+// only a group (amax: its largest magnitude) beyond the largest scale, or below the normal ones, where
+// the scale may be rounded down by more, needs the clamp.
 template <int N>
 __device__ __forceinline__ uint32_t int4_nibbles(float (&x)[N], float amax, float s) {
     const float inv = int4_inverse(s);
-    if (!(amax <= 7.f * kInt4MaxScale)) {
+    if (!(amax >= 7.f * kInt4MinNormal && amax <= 7.f * kInt4MaxScale)) {
         #pragma unroll
-        for (int i = 0; i < N; ++i) x[i] = fminf(fmaxf(x[i], -7.f * kInt4MaxScale), 7.f * kInt4MaxScale);
+        for (int i = 0; i < N; ++i) x[i] = fminf(fmaxf(x[i], -7.f * s), 7.f * s);
     }
     // 1.5 * 2^23 + 8 + q rounds q to an integer (the offset is even) in its low bits; what the constant's
     // high bits add up to, modulo 2^32, is taken off once

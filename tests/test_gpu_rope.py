@@ -192,6 +192,39 @@ def test_int4_append_bit_exact_with_specials(in_dtype, d, B):
     cache.close()
 
 
+@pytest.mark.parametrize("in_dtype,d", [("f16", 128), ("f32", 64)])
+def test_int4_small_groups_bit_exact(in_dtype, d):
+    """Groups whose scale lies below 2^-14, where its grid is coarse: amax/7 rounds down by up to a third and
+    the largest quotients have to be held at 7.  By kv_append, kv_append_rope and the fused decode step."""
+    rng = np.random.default_rng(14)
+    B, H, n = 16, 2, 120
+    nb = n // B + 1
+    top = np.linspace(0.2, 9.0, n * H * (d // 16)).reshape(n, H, d // 16, 1) * 7 * 2.0 ** -17
+    k, v = ((np.where(rng.random((n, H, d // 16, 16)) < 0.3, rng.choice([-1.0, 1.0], (n, H, d // 16, 16)),
+                      rng.uniform(-1, 1, (n, H, d // 16, 16))) * top).reshape(n, H, d).astype(NP[in_dtype])
+            for _ in range(2))
+    slots = np.arange(n, dtype=np.int64)
+    tk, tv, ts = (torch.from_numpy(x).cuda() for x in (k, v, slots))
+    caches = [PagedKVCache(1, nb, B, H, d, "int4") for _ in range(3)]
+    for c in caches:
+        c.k[0].zero_()
+        c.v[0].zero_()
+    caches[0].append(0, tk, tv, ts)
+    caches[1].append_rope(0, tk, tv, ts, torch.zeros(n, dtype=torch.int32, device="cuda"), rope_table(4, d))
+    q = torch.zeros(n, H, d, device="cuda").half()     # a sequence per token: lengths 1 .. 16 in its block
+    tab = (ts // B).to(torch.int32).reshape(n, 1)
+    ln = (ts % B + 1).to(torch.int32)
+    caches[2].attention_ex(0, q, tab, ln, B, 0.1, k_new=tk, v_new=tv)
+    for which, x in (("k", k), ("v", v)):
+        zero = np.zeros(caches[0].k[0].shape, dtype=np.uint8)
+        want = expected_pool(zero, which, x.astype(np.float32), slots, B, "int4")
+        for c in caches:
+            assert np.array_equal(getattr(c, which)[0].cpu().numpy(), want), which
+    for c in caches:
+        assert c.device_error() == 0
+        c.close()
+
+
 @pytest.mark.parametrize("pool,out", [("f32", "f32"), ("f16", "f16"), ("f16", "f32"), ("fp8", "f16"), ("fp8", "f32"),
                                       ("int4", "f16"), ("int4", "f32")])
 @pytest.mark.parametrize("n,H,d,B", [(1, 1, 64, 8), (45, 3, 128, 16), (2, 40, 128, 32), (333, 5, 64, 8)])
