@@ -160,6 +160,7 @@ KV_API int kv_selftest_wait_timeout(kv_pool* pool, uint64_t limit_ns, kv_stream_
  *                  scale[block] is the value already in the layer's scale array
  *                  (the caller sets a fresh block's scale before appending into it).
  *                  A 4-bit pool takes F16 or F32 input and scales each 16 elements itself.
+ *                  (its slots must be distinct: a token is several stores).
  *   slot_mapping   device int64 [num_tokens]; slot < 0 means "skip this token".
  * Token i, head h lands at block slot/B, offset slot%B.  Out-of-range slots set
  * KV_DEVERR_SLOT and are skipped.  Bit-exact copy for F32/F16.

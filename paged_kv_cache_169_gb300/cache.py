@@ -7,6 +7,8 @@ addresses, and keep the handles alive.
 
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import abi
@@ -31,10 +33,15 @@ def _dev_ptr(t: torch.Tensor, what: str) -> int:
     return t.data_ptr()
 
 
-def _rows(t: torch.Tensor, n: int, heads: int, d: int, what: str):
+def _alloc_on(stream):
+    """Allocations made inside belong to the stream that will write them, and so does what fills them."""
+    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+
+
+def _rows(t: torch.Tensor, n: int, heads: int, d: int, what: str, dev: int):
     """Address and elements between the token rows of [n, heads, d] (heads and elements contiguous)."""
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{what} must be a CUDA tensor on the pool's device")
     row, head, one = t.stride()
     if one != 1 or (head != d and heads > 1):
         raise ValueError(f"{what}: heads and elements of a token must be contiguous")
@@ -46,7 +53,7 @@ def rope_table(num_positions: int, rot_dim: int, base: float = 10000.0, position
     """Cosines and sines of ``position * position_scale * base ** (-2i / rot_dim)`` for
     PagedKVCache.append_rope: float32 [num_positions, rot_dim], cosines first.  Made once per
     model."""
-    with torch.cuda.device(device):
+    with torch.cuda.device(device), _alloc_on(stream):
         t = torch.empty((num_positions, rot_dim), dtype=torch.float32, device=device)
         abi.kv_rope_table(t.data_ptr(), num_positions, rot_dim, base, position_scale, _stream(stream))
     return t
@@ -120,6 +127,7 @@ class PagedKVCache:
             raise ValueError("positions must have one entry per token")
         if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
             raise ValueError("cos_sin must be float32 [positions, rot_dim]")
+        dev = self.k[0].get_device()
         qp = op = qs = os = hq = 0
         if q is not None:
             shape = q.shape
@@ -127,13 +135,16 @@ class PagedKVCache:
                 raise ValueError("q must be [num_tokens, Hq, d] of k's dtype")
             hq, out_dt = shape[1], torch.float32 if self.dtype == "f32" else torch.float16
             if q_out is None:
-                q_out = torch.empty(shape, dtype=out_dt, device=q.device)
+                with _alloc_on(stream):
+                    q_out = torch.empty(shape, dtype=out_dt, device=q.device)
             elif q_out.shape != shape or q_out.dtype != out_dt:
                 raise ValueError(f"q_out must be {out_dt} of q's shape")
-            (qp, qs), (op, os) = _rows(q, n, hq, d, "q"), _rows(q_out, n, hq, d, "q_out")
+            (qp, qs), (op, os) = _rows(q, n, hq, d, "q", dev), _rows(q_out, n, hq, d, "q_out", dev)
         elif q_out is not None:
             raise ValueError("q_out without q")
-        (kp, ks), (vp, vs) = _rows(k, n, h, d, "k"), _rows(v, n, h, d, "v")
+        (kp, ks), (vp, vs) = _rows(k, n, h, d, "k", dev), _rows(v, n, h, d, "v", dev)
+        if slot_mapping.get_device() != dev or positions.get_device() != dev or cos_sin.get_device() != dev:
+            raise ValueError("slot_mapping, positions and cos_sin must be CUDA tensors on the pool's device")
         table_len, rot = cos_sin.shape
         a = abi.kv_rope_args(layer, qp, hq, op, kp, vp, _IN_DTYPE[dt], qs, ks, vs, os,
                              _dev_ptr(slot_mapping, "slot_mapping"), _dev_ptr(positions, "positions"),
@@ -153,9 +164,13 @@ class PagedKVCache:
             raise ValueError("k_out and v_out come together")
         shape = (slot_mapping.numel(), self.num_heads, self.head_dim)
         if k_out is None:
-            k_out, v_out = (torch.zeros(shape, dtype=out_dtype, device=self.k[0].device) for _ in range(2))
+            with _alloc_on(stream):
+                k_out, v_out = (torch.zeros(shape, dtype=out_dtype, device=self.k[0].device) for _ in range(2))
         if k_out.shape != shape or v_out.shape != shape or k_out.dtype != v_out.dtype or k_out.dtype not in _IN_DTYPE:
             raise ValueError("k_out and v_out must be float16 or float32 [num_tokens, H, d]")
+        dev = self.k[0].get_device()
+        if slot_mapping.get_device() != dev or k_out.get_device() != dev or v_out.get_device() != dev:
+            raise ValueError("slot_mapping, k_out and v_out must be CUDA tensors on the pool's device")
         abi.kv_gather(self.handle, layer, _dev_ptr(slot_mapping, "slot_mapping"), shape[0], _dev_ptr(k_out, "k_out"),
                       _dev_ptr(v_out, "v_out"), _IN_DTYPE[k_out.dtype], _stream(stream))
         return k_out, v_out

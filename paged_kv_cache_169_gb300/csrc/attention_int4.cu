@@ -332,7 +332,8 @@ __global__ void __launch_bounds__(kWarps<G> * 32, 1) attention_int4_kernel(const
     // ---- chunks per (sequence, head) and their inclusive prefix over the launch's units
     auto chunks_of = [&](int ctx) {
         const int n = ctx - attend_first(ctx, a.window, 8);
-        return n > 0 ? (n + CT - 1) / CT : 1;          // an empty sequence: one chunk without tokens
+        // an empty sequence: one chunk without tokens (unsigned: a context may reach 2^31 - 1)
+        return n > 0 ? static_cast<int>((static_cast<unsigned>(n) + CT - 1) / CT) : 1;
     };
     for (int s = tid; s < a.batch; s += NW * 32) {
         int c = a.lens[s];
@@ -730,8 +731,10 @@ int launch_d(const kv_pool* pool, const Int4Args& args, const AttnPlan& plan, cu
         if (cudaFuncSetAttribute(attention_int4_kernel<D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  Smem<D, G>::BYTES) != cudaSuccess ||
             cudaFuncSetAttribute(attention_int4_kernel<D, G>, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                 cudaSharedmemCarveoutMaxShared) != cudaSuccess)
+                                 cudaSharedmemCarveoutMaxShared) != cudaSuccess) {
+            cudaGetLastError();
             return KV_ERR_CUDA;
+        }
         attr_done |= bit;
     }
     const AttnArgs& all = args.a;
@@ -818,7 +821,8 @@ int plan_attention_int4(const kv_pool* pool, int batch, int max_context, int par
         return KV_ERR_INVALID_ARG;
     const int chunk = chunk_tokens(d.head_dim);
     // a sliding window bounds the tokens read per sequence (window + up to 7 masked rows)
-    const int64_t span = window > 0 && window + 32 < max_context ? window + 32 : max_context;
+    const int64_t reach = static_cast<int64_t>(window) + 32;
+    const int64_t span = window > 0 && reach < max_context ? reach : max_context;
     const int64_t chunks = span > 0 ? (span + chunk - 1) / chunk : 1;
     // the kernel numbers a launch's chunks with an int
     if (units_of(pool, batch) * (chunks + kUnitCost) >= (int64_t{1} << 31)) return KV_ERR_INVALID_ARG;

@@ -95,7 +95,7 @@ def check(lens, H, G, d, B, window=0, partition=0, seed=0, flags=0, out_f16=Fals
     scale = 1 / math.sqrt(d)
     want, tol = oracle(pools, tab, lens, q, B, d, scale, window)
     t = [torch.from_numpy(x).cuda() for x in (q, tab, np.array(lens, dtype=np.int32))]
-    got = cache.attention_ex(0, *t, max(max(lens), 1), scale, window=window, partition_tokens=partition,
+    got = cache.attention_ex(0, *t, max(max(lens), 1), scale, window=window, partition_tokens=partition, flags=flags,
                              out_dtype=torch.float16 if out_f16 else torch.float32)
     assert cache.device_error() == 0
     err = np.abs(got.double().cpu().numpy() - want)
@@ -125,6 +125,18 @@ def test_partitions(partition, G, d):
 @pytest.mark.parametrize("G,d,B", [(1, 128, 8), (8, 64, 32), (2, 128, 16)])
 def test_window(window, G, d, B):
     check([0, 1, 6, 99, 100, 101, 777], 2, G, d, B, window=window, partition=64, seed=window)
+
+
+@pytest.mark.parametrize("G,flags", [(1, 0), (8, abi.KV_DECODE_PDL)])
+def test_more_sequences_than_one_launch_takes(G, flags):
+    """1024 sequences go in one launch; the second starts at its own queries, tables, lengths and outputs."""
+    lens = [(7 * s) % 90 for s in range(1030)]
+    lens[3], lens[1027] = 700, 900
+    check(lens, 1, G, 64, 16, flags=flags, seed=G)
+
+
+def test_window_up_to_the_int_range():
+    check([0, 5, 300], 1, 1, 128, 16, window=2 ** 31 - 1)
 
 
 def test_float16_output_and_long_context():

@@ -358,3 +358,46 @@ def test_rope_and_gather_beyond_four_gigabytes():
     assert np.array_equal(kb.cpu().numpy(), want) and torch.equal(vb, v)
     assert cache.device_error() == 0
     cache.close()
+
+
+def test_new_outputs_belong_to_the_stream_of_the_call():
+    """Work queued on the current stream must not reach (as a late zero fill) what another stream gathers."""
+    cache = PagedKVCache(1, 4, 16, 2, 64, "f16")
+    k, v = (torch.randn(48, 2, 64, device="cuda").half() for _ in range(2))
+    slots = torch.arange(48, device="cuda")
+    cache.append(0, k, v, slots)
+    busy = torch.randn(4096, 4096, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        busy = (busy @ busy).clamp_(-1, 1)
+    gk, gv = cache.gather(0, slots, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(gk, k) and torch.equal(gv, v)
+    pos = torch.zeros(48, dtype=torch.int32, device="cuda")
+    tab = rope_table(4, 64, stream=side)
+    out = cache.append_rope(0, k, v, slots, pos, tab, q=k, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(out, k)
+    cache.close()
+
+
+def test_tensors_elsewhere_are_refused():
+    cache = PagedKVCache(1, 4, 16, 2, 64, "int4")
+    k = torch.randn(3, 2, 64, device="cuda").half()
+    slots = torch.arange(3, device="cuda")
+    pos = torch.zeros(3, dtype=torch.int32, device="cuda")
+    tab = rope_table(4, 64)
+    for at in range(6):
+        x = [k, k, slots, pos, tab, k]
+        x[at] = x[at].cpu()
+        with pytest.raises(ValueError):
+            cache.append_rope(0, *x[:5], q=x[5])
+    with pytest.raises(ValueError):
+        cache.append_rope(0, k, k, slots, pos, tab, q=k, q_out=k.cpu())
+    for at in range(3):
+        x = [slots, k.clone(), k.clone()]
+        x[at] = x[at].cpu()
+        with pytest.raises(ValueError):
+            cache.gather(0, x[0], k_out=x[1], v_out=x[2])
+    cache.close()
