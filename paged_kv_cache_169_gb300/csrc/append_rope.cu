@@ -11,10 +11,13 @@
 // partner under either pairing and the other half of its quantisation group are a shuffle away
 // and every input is read once.  The two half-warps take two consecutive tokens: where their slots
 // share a 32-bit word of a 4-bit V tile (slot 2m and 2m + 1), the pair of lanes writes whole words.
-// A warp walks over the head rows (queries, then keys, then values) with its token's table values
-// in registers and several rows' loads in flight.  Bound: HBM (57.4 us for 8192 tokens of 64 + 8 heads into float16,
-// 0.87 of a copy's rate); with a 4-bit pool, the instructions that quantise (43 us for 4097 tokens of
-// 40 + 40 heads, 0.71).
+// A warp walks over its head rows (queries, then keys, then values) with its token's table values in
+// registers.  Rows come through shared memory by cp.async, eight ahead: kept in registers, four at a
+// time, too few bytes were in flight (57.4 us for 8192 tokens of 64 + 8 heads into float16, 60.3 us
+// for the 4-bit prompt below).  A CTA per token pair in launch order keeps the addresses in use
+// together; equal ranges of rows per warp over the whole call, with no tail, took 61.6 us.
+// Bound: HBM (52.4 us for the float16 prompt, 0.95 of a copy's rate); with a 4-bit pool, the
+// instructions that quantise (39 us for 4097 tokens of 40 + 40 heads, 0.72).
 
 #include <type_traits>
 
@@ -135,47 +138,75 @@ __device__ __forceinline__ void store_unit(char* at, char* sc, int64_t head, flo
     }
 }
 
-// A 4-bit pool's rows take long enough to quantise for the next rows to be asked for meanwhile, at five
-// CTAs per SM (61 us for the measured 4-bit prompt, 63 without); the others are faster with seven and
-// no read ahead (57 us for the float16 prompt; 64 the 4-bit way).
-template <kv_dtype POOL> constexpr bool kReadAhead = POOL == KV_INT4;
+// Rows a warp has asked for ahead of the one it works on (4, 8, 16: 54.1, 52.4, 55.2 us for the float16
+// prompt), 16 KB per CTA whatever the type.
+template <typename TIn> constexpr int kRowsAhead = sizeof(TIn) == 2 ? 8 : 4;
+// CTAs per SM: quantising takes more registers (6, 7, 8: 57.7, 59.0, 63.0 us for the 4-bit prompt).
+template <kv_dtype POOL> constexpr int kCtasPerSm = POOL == KV_INT4 ? 6 : 7;
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const char* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 
 enum : int { NO_ROTATION = 0, HALF_PAIRS = 1, ADJACENT_PAIRS = 2 };
 
 template <int D, typename TIn, kv_dtype POOL, int MODE>
-__global__ void __launch_bounds__(kThreads, kReadAhead<POOL> ? 5 : 7)
-append_rope_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm<POOL>) append_rope_kernel(const __grid_constant__ RopeArgs a) {
     constexpr int UPR = D / 8, HPW = 16 / UPR;         // units per row; head rows per half-warp
     constexpr int ESZ = sizeof(TIn), QSZ = POOL == KV_F32 ? 4 : 2;
-    constexpr int UNROLL = ESZ == 2 ? 4 : 2;
     constexpr int ROW = POOL == KV_INT4 ? D / 2 + D / 16 : POOL == KV_FP8_E4M3 ? D : POOL == KV_F16 ? 2 * D : 4 * D;
+    constexpr int AHEAD = kRowsAhead<TIn>, PIECES = ESZ / 2;           // 16-byte pieces of a unit
+    __shared__ uint4 s_ring[kWarpsPerCta][AHEAD][PIECES][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int unit = lane & (UPR - 1), sub = (lane & 15) / UPR;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int64_t tok = static_cast<int64_t>(blockIdx.x) * 2 + (lane >> 4);
     // ---- The head rows: queries, keys, values, HPW rows per half-warp and step, dealt to the warps in
-    // turn.  The first rows are asked for before anything is known of the token (one past the end takes
-    // its neighbour's).
-    const int uq = (a.Hq + HPW - 1) / HPW, uk = (a.H + HPW - 1) / HPW;
+    // turn.  A lane copies its own 16 bytes of each row to shared memory, several rows ahead, and reads
+    // them back itself, so it waits for its own copies only.  The first rows are asked for before anything
+    // is known of the token (one past the end takes its neighbour's).
+    const int uq = (a.Hq + HPW - 1) / HPW, uk = (a.H + HPW - 1) / HPW, rows = uq + 2 * uk;
     const int start = blockIdx.y * kWarpsPerCta + warp, step = gridDim.y * kWarpsPerCta;
     const int64_t from = tok < a.n ? tok : tok - 1;
-    const int lane_at = (sub * D + unit * 8) * ESZ;
     constexpr int STEP = HPW * D * ESZ;                // bytes between a half-warp's steps
-    // rows r, r + step, ... (< count) of a matrix of `heads` heads; an odd head count's last step has a
-    // row too many, which reads the last one
-    auto load = [&](const char* base, int r, int count, int heads, Raw<TIn> (&raw)[UNROLL]) {
-        #pragma unroll
-        for (int j = 0; j < UNROLL; ++j) {
-            const int i = r + j * step;
-            if (i < count) load_raw(base + i * STEP - (HPW > 1 && i * HPW + sub >= heads ? D * ESZ : 0), raw[j]);
+    uint4* const ring = &s_ring[warp][0][0][lane];
+    const uint32_t ring32 = smem_u32(ring);
+    int ask_row = start, ask_end = 0, ask_slot = 0;    // the next row to ask for, its matrix's end, its place
+    const char* ask_at = nullptr;
+    auto ask = [&]() {
+        if (ask_row < rows) {
+            if (ask_row >= ask_end) {                  // another matrix
+                const bool is_q = ask_row < uq, is_k = ask_row < uq + uk;
+                const int first = is_q ? 0 : is_k ? uq : uq + uk;
+                ask_end = is_q ? uq : is_k ? uq + uk : rows;
+                ask_at = (is_q ? a.q : is_k ? a.k : a.v) + from * (is_q ? a.q_stride : is_k ? a.k_stride : a.v_stride) +
+                         (ask_row - first) * STEP + (sub * D + unit * 8) * ESZ;
+            }
+            // an odd head count's last step has a row too many, which reads the last one
+            const int heads = ask_end == uq ? a.Hq : a.H;
+            const char* at = ask_at - (HPW > 1 && ask_row + 1 == ask_end && (heads & 1) && sub ? D * ESZ : 0);
+            #pragma unroll
+            for (int i = 0; i < PIECES; ++i) cp_async16(ring32 + (ask_slot * PIECES + i) * 512, at + 16 * i);
+            ask_row += step;
+            ask_at += step * STEP;
+            ask_slot = (ask_slot + 1) % AHEAD;
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    const char* const qp = a.q + from * a.q_stride + lane_at;
-    const char* const kp = a.k + from * a.k_stride + lane_at;
-    const char* const vp = a.v + from * a.v_stride + lane_at;
-    Raw<TIn> raw[UNROLL];
-    if (start < uq) load(qp, start, uq, a.Hq, raw);
+    #pragma unroll
+    for (int i = 0; i < AHEAD - 1; ++i) ask();
+    int slot_of_row = 0;
+    auto next_row = [&](float (&x)[8]) {               // the next row, and one more asked for
+        asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 2) : "memory");
+        Raw<TIn> raw;
+        uint4* const w = reinterpret_cast<uint4*>(&raw);
+        #pragma unroll
+        for (int i = 0; i < PIECES; ++i) w[i] = ring[(slot_of_row * PIECES + i) * 32];
+        slot_of_row = (slot_of_row + 1) % AHEAD;
+        ask();
+        widen(raw, x);
+    };
     // ---- the token: its slot, its position, its rotation
     int64_t slot = tok < a.n ? a.slots[tok] : -1;
     int pos = 0;
@@ -192,25 +223,36 @@ append_rope_kernel(const __grid_constant__ RopeArgs a) {
             pos = 0;
         }
     }
-    if (!__any_sync(FULL, live)) return;
-    // this unit's cosines and sines: half pairs 8 of each, adjacent pairs 4 of each
-    float c[8], s[8];
+    if (!__any_sync(FULL, live)) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        return;
+    }
+    // this unit's cosines and sines for pairs of elements (half pairs: 8 of each; adjacent pairs: 4 of
+    // each, every one for both elements of its pair)
+    float2 c[4], s[4];
     const bool turned = unit * 8 < a.rot;
     const int half_units = a.rot >> 4;
     const bool low = unit < half_units;                // half pairs: the first element of each pair
     if constexpr (MODE != NO_ROTATION) {
+        // x cos - y sin is taken as x cos + y (-sin): the same roundings
         const float* row = a.table + static_cast<int64_t>(pos) * a.rot;
         const int i0 = !turned ? 0 : MODE == ADJACENT_PAIRS ? unit * 4 : (low ? unit : unit - half_units) * 8;
-        #pragma unroll
-        for (int j = 0; j < (MODE == ADJACENT_PAIRS ? 1 : 2); ++j) {
-            const float4 cv = *reinterpret_cast<const float4*>(row + i0 + 4 * j);
-            const float4 sv = *reinterpret_cast<const float4*>(row + a.rot / 2 + i0 + 4 * j);
-            c[4 * j] = cv.x; c[4 * j + 1] = cv.y; c[4 * j + 2] = cv.z; c[4 * j + 3] = cv.w;
-            s[4 * j] = sv.x; s[4 * j + 1] = sv.y; s[4 * j + 2] = sv.z; s[4 * j + 3] = sv.w;
-        }
-        if (MODE == HALF_PAIRS && low) {               // x cos - y sin as x cos + y (-sin): the same roundings
+        if constexpr (MODE == ADJACENT_PAIRS) {
+            const float4 cv = *reinterpret_cast<const float4*>(row + i0);
+            const float4 sv = *reinterpret_cast<const float4*>(row + a.rot / 2 + i0);
+            c[0] = make_float2(cv.x, cv.x); c[1] = make_float2(cv.y, cv.y);
+            c[2] = make_float2(cv.z, cv.z); c[3] = make_float2(cv.w, cv.w);
+            s[0] = make_float2(-sv.x, sv.x); s[1] = make_float2(-sv.y, sv.y);
+            s[2] = make_float2(-sv.z, sv.z); s[3] = make_float2(-sv.w, sv.w);
+        } else {
             #pragma unroll
-            for (int i = 0; i < 8; ++i) s[i] = -s[i];
+            for (int j = 0; j < 2; ++j) {
+                const float4 cv = *reinterpret_cast<const float4*>(row + i0 + 4 * j);
+                float4 sv = *reinterpret_cast<const float4*>(row + a.rot / 2 + i0 + 4 * j);
+                if (low) sv = make_float4(-sv.x, -sv.y, -sv.z, -sv.w);
+                c[2 * j] = make_float2(cv.x, cv.y); c[2 * j + 1] = make_float2(cv.z, cv.w);
+                s[2 * j] = make_float2(sv.x, sv.y); s[2 * j + 1] = make_float2(sv.z, sv.w);
+            }
         }
     }
     if (!live) slot = 0;
@@ -240,74 +282,53 @@ append_rope_kernel(const __grid_constant__ RopeArgs a) {
     }
     const int partner = (lane & ~(UPR - 1)) | (turned ? (low ? unit + half_units : unit - half_units) : unit);
     auto rotate = [&](float (&x)[8]) {
-        if constexpr (MODE == ADJACENT_PAIRS) {
+        if constexpr (MODE != NO_ROTATION) {
+            float y[8];                                // each element's partner
+            #pragma unroll
+            for (int i = 0; i < 8; ++i)
+                y[i] = MODE == ADJACENT_PAIRS ? x[i ^ 1] : __shfl_sync(FULL, x[i], partner);
             if (!turned) return;
             #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float u = x[2 * i], w = x[2 * i + 1];
-                x[2 * i] = __fsub_rn(__fmul_rn(u, c[i]), __fmul_rn(w, s[i]));
-                x[2 * i + 1] = __fadd_rn(__fmul_rn(w, c[i]), __fmul_rn(u, s[i]));
+            for (int i = 0; i < 4; ++i) {              // two elements at a time, rounded op by op
+                const float2 p = __fmul2_rn(make_float2(x[2 * i], x[2 * i + 1]), c[i]);
+                const float2 r = __fmul2_rn(make_float2(y[2 * i], y[2 * i + 1]), s[i]);
+                x[2 * i] = __fadd_rn(p.x, r.x);        // (a sum of pairs would be contracted)
+                x[2 * i + 1] = __fadd_rn(p.y, r.y);
             }
-        } else if constexpr (MODE == HALF_PAIRS) {
-            float y[8];
-            #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(FULL, x[i], partner);
-            if (!turned) return;
-            #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = __fadd_rn(__fmul_rn(x[i], c[i]), __fmul_rn(y[i], s[i]));
         }
     };
     // ---- queries
+    // q_out may be q: a lane writes only elements that it has read, and has asked for none that another writes
     char* const qo = a.q_out + tok * a.qo_stride + (sub * D + e0) * QSZ;
     int r = start;
-    for (bool first = true; r < uq; first = false) {
-        if (!first && !kReadAhead<POOL>) load(qp, r, uq, a.Hq, raw);
-        Raw<TIn> now[UNROLL];
-        #pragma unroll
-        for (int j = 0; j < UNROLL; ++j) now[j] = raw[j];
-        if (kReadAhead<POOL> && r + UNROLL * step < uq) load(qp, r + UNROLL * step, uq, a.Hq, raw);
-        __syncwarp();                                  // q_out may be q: rows are read before they are written
-        #pragma unroll
-        for (int j = 0; j < UNROLL; ++j, r += step) {
-            if (r >= uq) break;
-            float x[8];
-            widen(now[j], x);
-            rotate(x);
-            if (!live || (HPW > 1 && r * HPW + sub >= a.Hq)) continue;
-            char* p = qo + r * (HPW * D * QSZ);
-            if constexpr (POOL == KV_F32) {
-                reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-                reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-            } else {
-                *reinterpret_cast<uint4*>(p) = halves(x);
-            }
+    #pragma unroll 1
+    for (; r < uq; r += step) {
+        float x[8];
+        next_row(x);
+        rotate(x);
+        if (!live || (HPW > 1 && r * HPW + sub >= a.Hq)) continue;
+        char* p = qo + r * (HPW * D * QSZ);
+        if constexpr (POOL == KV_F32) {
+            reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+            reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+        } else {
+            *reinterpret_cast<uint4*>(p) = halves(x);
         }
     }
     // ---- keys, then values
-    auto cached = [&](auto is_v, const char* src, char* at, char* sc, float scale) {
+    auto cached = [&](auto is_v, char* at, char* sc, float scale) {
         constexpr bool IS_V = decltype(is_v)::value;
-        if (kReadAhead<POOL> && r < uk) load(src, r, uk, a.H, raw);
-        while (r < uk) {
-            if (!kReadAhead<POOL>) load(src, r, uk, a.H, raw);
-            Raw<TIn> now[UNROLL];
-            #pragma unroll
-            for (int j = 0; j < UNROLL; ++j) now[j] = raw[j];
-            if (kReadAhead<POOL> && r + UNROLL * step < uk) load(src, r + UNROLL * step, uk, a.H, raw);
-            #pragma unroll
-            for (int j = 0; j < UNROLL; ++j, r += step) {
-                if (r >= uk) break;
-                float x[8];
-                widen(now[j], x);
-                if constexpr (!IS_V) rotate(x);
-                const bool here = live && (HPW == 1 || r * HPW + sub < a.H);
-                store_unit<POOL, IS_V>(at, sc, r * HPW * tile, x, scale, paired, odd, here, lane);
-            }
+        #pragma unroll 1
+        for (r -= IS_V ? uk : uq; r < uk; r += step) {
+            float x[8];
+            next_row(x);
+            if constexpr (!IS_V) rotate(x);
+            const bool here = live && (HPW == 1 || r * HPW + sub < a.H);
+            store_unit<POOL, IS_V>(at, sc, r * HPW * tile, x, scale, paired, odd, here, lane);
         }
-        r -= uk;
     };
-    r -= uq;
-    cached(std::integral_constant<bool, false>{}, kp, kat, ksc, ks);
-    cached(std::integral_constant<bool, true>{}, vp, vat, vsc, vs);
+    cached(std::integral_constant<bool, false>{}, kat, ksc, ks);
+    cached(std::integral_constant<bool, true>{}, vat, vsc, vs);
 }
 
 template <typename TIn, kv_dtype POOL>
@@ -316,9 +337,9 @@ int launch_rope_typed(const kv_pool* pool, const RopeArgs& a, bool pdl, cudaStre
     const int hpw = 16 / (D / 8);
     const int uq = a.Hq ? (a.Hq + hpw - 1) / hpw : 0, rows = uq + 2 * ((a.H + hpw - 1) / hpw);
     const int pairs = a.n / 2 + a.n % 2;
-    // few tokens: the head rows spread over CTAs, one step each; many: one CTA per token pair
+    // a CTA per token pair, or with few tokens as many as are resident at once, down to one row per warp
     const int most = (rows + kWarpsPerCta - 1) / kWarpsPerCta;
-    int gy = (8 * pool->num_sms - 1) / pairs + 1;
+    int gy = pool->num_sms * kCtasPerSm<POOL> / pairs;
     gy = gy < 1 ? 1 : gy > most ? most : gy;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

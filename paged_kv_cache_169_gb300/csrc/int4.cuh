@@ -87,10 +87,13 @@ __device__ __forceinline__ uint32_t int4_nibbles(float (&x)[N], float amax, floa
     // high bits add up to, modulo 2^32, is taken off once
     constexpr uint32_t kMagic = 0x4B400000u;
     uint32_t w = 0, high = 0;
+    const float2 inv2 = make_float2(inv, inv), neg_s = make_float2(-s, -s), offset = make_float2(12582920.f, 12582920.f);
     #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        w += __float_as_uint(int4_quotient(x[i], s, inv) + 12582920.f) << (4 * i);
-        high += kMagic << (4 * i);
+    for (int i = 0; i < N; i += 2) {                   // int4_quotient of two elements at a time
+        const float2 v = make_float2(x[i], x[i + 1]), q = __fmul2_rn(v, inv2);
+        const float2 r = __fadd2_rn(__ffma2_rn(__ffma2_rn(q, neg_s, v), inv2, q), offset);
+        w += (__float_as_uint(r.x) << (4 * i)) + (__float_as_uint(r.y) << (4 * i + 4));
+        high += (kMagic << (4 * i)) + (kMagic << (4 * i + 4));
     }
     w -= high;
     return w;
