@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<POOL>) append_rope_kernel
         }
     };
     // ---- queries
-    // q_out may be q: a lane writes only elements that it has read, and has asked for none that another writes
+    // q_out may be q: a lane writes only elements that it has read (what lanes past the end ask for is not used)
     char* const qo = a.q_out + tok * a.qo_stride + (sub * D + e0) * QSZ;
     int r = start;
     #pragma unroll 1

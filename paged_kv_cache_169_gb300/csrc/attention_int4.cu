@@ -170,29 +170,46 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, char* smem, int w0
                                            int lane) {
     using Sm = Smem<D, G>;
     constexpr int LPR = 32 / G < D / 4 ? 32 / G : D / 4, V = D / 4 / LPR;
+    constexpr int NM = (kWarps<G> + LPR - 1) / LPR;    // parts' (m, l) per lane: part i * LPR + sub
     const int sub = lane % LPR, r = lane / LPR < G ? lane / LPR : G - 1;
-    auto ml_of = [&](int k) {
-        const int kd = k == 0 ? kind : LATER;
-        return *reinterpret_cast<const float2*>(smem + (w0 + k) * Sm::WARP + Sm::ML + ((kd - 1) * G + r) * 8);
-    };
+    float2 ml[NM];
     RowAcc<V> x;
     x.m = -CUDART_INF_F;
     x.l = 0.f;
-    for (int k = 0; k < n; ++k) x.m = fmaxf(x.m, ml_of(k).x);
+    #pragma unroll
+    for (int i = 0; i < NM; ++i) {
+        const int k = i * LPR + sub, kd = k == 0 ? kind : LATER;
+        ml[i] = k < n ? *reinterpret_cast<const float2*>(smem + (w0 + k) * Sm::WARP + Sm::ML + ((kd - 1) * G + r) * 8)
+                      : make_float2(-CUDART_INF_F, 0.f);
+        x.m = fmaxf(x.m, ml[i].x);
+    }
+    #pragma unroll
+    for (int o = LPR / 2; o; o >>= 1) x.m = fmaxf(x.m, __shfl_xor_sync(FULL, x.m, o));
+    #pragma unroll
+    for (int i = 0; i < NM; ++i) {
+        ml[i].x = ex2_approx(ml[i].x - x.m);           // the part's weight, 0 past the end
+        x.l = fmaf(ml[i].y, ml[i].x, x.l);
+    }
+    #pragma unroll
+    for (int o = LPR / 2; o; o >>= 1) x.l += __shfl_xor_sync(FULL, x.l, o);
     #pragma unroll
     for (int i = 0; i < V; ++i) x.o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < n; ++k) {
-        const float2 v = ml_of(k);
-        const float w = ex2_approx(v.x - x.m);
-        x.l = fmaf(v.y, w, x.l);
-        const char* base = smem + (w0 + k) * Sm::WARP + (k == 0 && kind == START ? 0 : Sm::ROWS) + r * D * 4;
-        #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float4 o = reinterpret_cast<const float4*>(base)[sub + i * LPR];
-            x.o[i].x = fmaf(w, o.x, x.o[i].x);
-            x.o[i].y = fmaf(w, o.y, x.o[i].y);
-            x.o[i].z = fmaf(w, o.z, x.o[i].z);
-            x.o[i].w = fmaf(w, o.w, x.o[i].w);
+    #pragma unroll
+    for (int i = 0; i < NM; ++i) {
+        #pragma unroll 4
+        for (int j = 0; j < LPR; ++j) {
+            const int k = i * LPR + j;
+            if (k >= n) break;
+            const float w = __shfl_sync(FULL, ml[i].x, lane - sub + j);
+            const char* base = smem + (w0 + k) * Sm::WARP + (k == 0 && kind == START ? 0 : Sm::ROWS) + r * D * 4;
+            #pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float4 o = reinterpret_cast<const float4*>(base)[sub + e * LPR];
+                x.o[e].x = fmaf(w, o.x, x.o[e].x);
+                x.o[e].y = fmaf(w, o.y, x.o[e].y);
+                x.o[e].z = fmaf(w, o.z, x.o[e].z);
+                x.o[e].w = fmaf(w, o.w, x.o[e].w);
+            }
         }
     }
     if (lane / LPR >= G) return;
@@ -371,7 +388,7 @@ __global__ void __launch_bounds__(kWarps<G> * 32, 1) attention_int4_kernel(const
     auto range_begin = [&](int r) { return r * q + min(r, rem); };
     auto range_of = [&](int chunk) {
         const int c = chunk - rem * (q + 1);
-        return c < 0 ? chunk / (q + 1) : rem + c / q;
+        return (c < 0 ? chunk : c) / (c < 0 ? q + 1 : q) + (c < 0 ? 0 : rem);
     };
 
     char* const ring = smem + warp * Sm::WARP;
@@ -708,16 +725,25 @@ __global__ void __launch_bounds__(kWarps<G> * 32, 1) attention_int4_kernel(const
     __syncthreads();
     auto held_by = [&](int w, int kind) { return reinterpret_cast<const Held*>(smem + w * Sm::WARP + Sm::HELD) + kind - 1; };
     const int cta_begin = range_begin(rng0), cta_end = range_begin(min(rng0 + k, ranges));
+    // Lane w knows what warp w holds.  A warp joins the unit that starts with it; warp 0's LATER unit goes
+    // to the first other warp without one.
+    const int later = lane < NW ? held_by(lane, LATER)->u : -1, starts = lane < NW ? held_by(lane, START)->u : -1;
+    const unsigned idle = ~__ballot_sync(FULL, starts >= 0) & ((1u << NW) - 2u);
+    const int helper = idle ? __ffs(idle) - 1 : 0;
     #pragma unroll 1
-    for (int kind = START; kind >= (warp == 0 ? LATER : START); --kind) {
-        const Held h = *held_by(warp, kind);
+    for (int kind = START; kind >= (warp == helper ? LATER : START); --kind) {
+        const int w0 = kind == START ? warp : 0;
+        const Held h = *held_by(w0, kind);
         if (h.u < 0) continue;
-        int n = 1;
-        while (warp + n < k && held_by(warp + n, LATER)->u == h.u) ++n;
+        const int n = __ffs(~(__ballot_sync(FULL, later == h.u) >> (w0 + 1)));         // w0's and the LATER parts after it
         const bool whole = h.first >= cta_begin && h.last < cta_end;
         // at most one unit comes from an earlier CTA, and one that starts here goes on
-        if (!whole && lane == 0) s_cross[kind - 1] = Held{h.u, range_of(h.first) / k, range_of(h.last) / k, 0};
-        join_parts<D, G>(a, smem, warp, kind, n, h.u, whole, lane);
+        if (!whole) {
+            const int cta = range_of(lane == 0 ? h.first : h.last) / k;
+            if (lane == 0) { s_cross[kind - 1].u = h.u; s_cross[kind - 1].first = cta; }
+            if (lane == 1) s_cross[kind - 1].last = cta;
+        }
+        join_parts<D, G>(a, smem, w0, kind, n, h.u, whole, lane);
     }
     __syncthreads();
     finish_parts<D, G>(args, s_cross, s_go);
