@@ -34,8 +34,14 @@
 namespace kvp {
 namespace {
 
-// One CTA per SM.  8 query heads hold two columns of state per lane and need more than 128 registers.
-template <int G> constexpr int kWarps = G == 8 ? 12 : 16;
+// Warps of a CTA, one CTA per SM: four for each scheduler.  (8 query heads hold two columns of state per
+// lane and fit 128 registers with 16 bytes spilled; 12 warps with 160: 157 us for 192 sequences where 16
+// take 151; 13 or 14 leave the schedulers uneven: 190, 172 us.)
+constexpr int kWarps = 16;
+// Query rows of the next item staged beside the stages, copied with its first chunk.  With 8 query heads
+// there is no room: the first item's rows use the LATER part's place before it is written, and the
+// others', asked into L2 with the item's block ids, are read from there.
+template <int G> constexpr bool kStageQ = G < 8;
 constexpr int kUnitCost = 2;                       // chunks that beginning and ending a unit costs a warp
 // Tokens per chunk, one softmax update: 4608 bytes of K and V whatever the head size.  (Head size 64
 // with 32-token chunks pays the loop's fixed part twice per byte: 0.73 of the copy peak.)
@@ -62,14 +68,14 @@ template <int D> struct Stage {
 };
 
 // Dynamic shared memory, per warp: two stages (at the end the START part's rows), the next item's
-// query rows, two item slots (this item, the next), what is held (LATER, START), their (m, l) and
+// query rows (kStageQ), two item slots (this item, the next), what is held (LATER, START), their (m, l) and
 // the LATER part's rows.
 template <int D, int G> struct Smem {
-    static constexpr int RING = 2 * Stage<D>::BYTES, QBYTES = G * D * 2;
+    static constexpr int RING = 2 * Stage<D>::BYTES, QBYTES = kStageQ<G> ? G * D * 2 : 0;
     static constexpr int Q = RING, SLOTS = Q + QBYTES, HELD = SLOTS + 2 * (int)sizeof(ItemSlot);
     static constexpr int ML = HELD + 2 * (int)sizeof(Held), ROWS = (ML + 2 * G * 8 + 15) / 16 * 16;
     static constexpr int WARP = ROWS + G * D * 4;
-    static constexpr int BYTES = kWarps<G> * WARP;
+    static constexpr int BYTES = kWarps * WARP;
     static_assert(WARP % 16 == 0 && G * D * 4 <= RING, "16-byte alignment; a part fits the stages");
 };
 
@@ -170,7 +176,7 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, char* smem, int w0
                                            int lane) {
     using Sm = Smem<D, G>;
     constexpr int LPR = 32 / G < D / 4 ? 32 / G : D / 4, V = D / 4 / LPR;
-    constexpr int NM = (kWarps<G> + LPR - 1) / LPR;    // parts' (m, l) per lane: part i * LPR + sub
+    constexpr int NM = (kWarps + LPR - 1) / LPR;    // parts' (m, l) per lane: part i * LPR + sub
     const int sub = lane % LPR, r = lane / LPR < G ? lane / LPR : G - 1;
     float2 ml[NM];
     RowAcc<V> x;
@@ -315,7 +321,7 @@ __device__ __forceinline__ void finish_parts(const Int4Args& x, const Held* cros
             s_go[warp] = go;                           // this CTA is the last
         }
         __syncthreads();
-        for (int j = warp; j < 2 * G; j += kWarps<G>) {
+        for (int j = warp; j < 2 * G; j += kWarps) {
             const int i = j / G, of = count_of(i);
             if (of > 0 && s_go[i])
                 merge_row<D, G>(a, static_cast<int64_t>(cross[i].first) + cross[i].u + first_of(i), of,
@@ -325,13 +331,13 @@ __device__ __forceinline__ void finish_parts(const Int4Args& x, const Held* cros
 }
 
 template <int D, int G>
-__global__ void __launch_bounds__(kWarps<G> * 32, 1) attention_int4_kernel(const __grid_constant__ Int4Args args) {
+__global__ void __launch_bounds__(kWarps * 32, 1) attention_int4_kernel(const __grid_constant__ Int4Args args) {
     const AttnArgs& a = args.a;
     constexpr int WORDS = Int4<D>::WORDS, OCT = Int4<D>::OCT;
     constexpr int MT = D / 16;                         // output tiles of 16 elements
     constexpr bool SPLIT = G <= 4;                     // odd columns: the weights' rounding errors
     constexpr int NQ = SPLIT ? 1 : 2;                  // query columns per lane
-    constexpr int CT = chunk_tokens(D), NO = kOcts<D>, NW = kWarps<G>, NU = CT / 16;
+    constexpr int CT = chunk_tokens(D), NO = kOcts<D>, NW = kWarps, NU = CT / 16;
     using St = Stage<D>;
     using Sm = Smem<D, G>;
     extern __shared__ __align__(128) char smem[];
@@ -382,7 +388,9 @@ __global__ void __launch_bounds__(kWarps<G> * 32, 1) attention_int4_kernel(const
     // The first `rem` ranges have q + 1 chunks, the others q.
     const int grid = static_cast<int>(gridDim.x);
     const int want = max(total / args.min_range, 1);
-    const int k = min((want + grid - 1) / grid, NW);
+    // (a whole number of warps for each of the SM's four schedulers: 14 warps of 4 chunks took 16.9 us where
+    // 12 of 4.6 take 15.7)
+    const int k0 = min((want + grid - 1) / grid, NW), k = k0 > 4 ? k0 & ~3 : k0;
     const int ranges = min(want, k * grid);
     const int q = total / ranges, rem = total - q * ranges;
     auto range_begin = [&](int r) { return r * q + min(r, rem); };
@@ -392,7 +400,7 @@ __global__ void __launch_bounds__(kWarps<G> * 32, 1) attention_int4_kernel(const
     };
 
     char* const ring = smem + warp * Sm::WARP;
-    char* const s_q = ring + Sm::Q;
+    char* const s_q = ring + (kStageQ<G> ? Sm::Q : Sm::ROWS);          // (the first item's, before its rows)
     ItemSlot* const slots = reinterpret_cast<ItemSlot*>(ring + Sm::SLOTS);
     Held* const held = reinterpret_cast<Held*>(ring + Sm::HELD);
     if (lane < 2) held[lane].u = -1;
@@ -450,6 +458,7 @@ __global__ void __launch_bounds__(kWarps<G> * 32, 1) attention_int4_kernel(const
     // copied while chunk c is multiplied.  It starts on an item without tokens or result.
     int ntok = 0, lo = 0, cur = 1, stage = 1;          // this item's tokens, masked rows, slot; the stage in use
     int oid = 0, oid_next = 0;                         // oct ids of the item's current and next 32 octs
+    bool first_item = true;
     for (bool started = false;; started = true) {
         if (started) {
             // Query fragments in the order the K words expand: k-step 2w takes elements (0, 4) and
@@ -457,12 +466,15 @@ __global__ void __launch_bounds__(kWarps<G> * 32, 1) attention_int4_kernel(const
             // elements meet full K values, those of the even ones a sixteenth: the odd elements'
             // query values are divided by 16 (exact unless below 2^-10, then off by at most
             // 2^-25) and the score times 16.
-            cp_async_wait();                           // the rows came with the item's first chunk
+            cp_async_wait();                           // rows in shared memory came with the item's first chunk
             __syncwarp();
+            const char* rows = s_q;
+            if (!kStageQ<G> && !first_item)
+                rows = static_cast<const char*>(a.q) + (static_cast<int64_t>(slots[cur].s) * a.H + slots[cur].h) * G * D * 2;
             #pragma unroll
             for (int w = 0; w < WORDS; ++w) {
                 uint4 x = make_uint4(0, 0, 0, 0);
-                if (has_q) x = *reinterpret_cast<const uint4*>(s_q + (col * D + t * (D / 4) + 8 * w) * 2);
+                if (has_q) x = *reinterpret_cast<const uint4*>(rows + (col * D + t * (D / 4) + 8 * w) * 2);
                 const uint32_t e15 = __byte_perm(x.x, x.z, 0x7632), e37 = __byte_perm(x.y, x.w, 0x7632);
                 const __half2 f = __float2half2_rn(0.0625f);
                 const __half2 b0 = __hmul2(*reinterpret_cast<const __half2*>(&e15), f);
@@ -472,6 +484,7 @@ __global__ void __launch_bounds__(kWarps<G> * 32, 1) attention_int4_kernel(const
                 qa[2 * w + 1][0] = __byte_perm(x.y, x.w, 0x5410);
                 qa[2 * w + 1][1] = *reinterpret_cast<const uint32_t*>(&b1);
             }
+            first_item = false;
             __syncwarp();                              // the next item's rows may follow now
             #pragma unroll
             for (int q = 0; q < NQ; ++q) { m[q] = -CUDART_INF_F; l[q] = 0.f; }
@@ -535,10 +548,14 @@ __global__ void __launch_bounds__(kWarps<G> * 32, 1) attention_int4_kernel(const
                         __syncwarp();                  // the copies below read the row
                     }
                     const char* q = static_cast<const char*>(a.q) + (static_cast<int64_t>(s) * a.H + h) * G * D * 2;
-                    #pragma unroll
-                    for (int i = 0; i < (Sm::QBYTES / 16 + 31) / 32; ++i)
-                        if (i * 32 + lane < Sm::QBYTES / 16)
-                            cp_async16(smem_u32(s_q) + (i * 32 + lane) * 16, q + (i * 32 + lane) * 16);
+                    constexpr int QB = G * D * 2;
+                    if (kStageQ<G> || !started) {
+                        #pragma unroll
+                        for (int i = 0; i < (QB / 16 + 31) / 32; ++i)
+                            if (i * 32 + lane < QB / 16) cp_async16(smem_u32(s_q) + (i * 32 + lane) * 16, q + (i * 32 + lane) * 16);
+                    } else if (lane < QB / 128) {
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(q + lane * 128));
+                    }
                 }
             }
             cp_async_wait();
@@ -790,7 +807,7 @@ int launch_d(const kv_pool* pool, const Int4Args& args, const AttnPlan& plan, cu
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(static_cast<unsigned>(grid < 1 ? 1 : grid));
-        cfg.blockDim = dim3(kWarps<G> * 32);
+        cfg.blockDim = dim3(kWarps * 32);
         cfg.dynamicSmemBytes = Smem<D, G>::BYTES;
         cfg.stream = stream;
         cfg.attrs = attr;
