@@ -12,7 +12,7 @@
 // weights at no further mma; 8 query heads fill all columns and p is rounded to float16 once
 // (relative 2^-11, as in the other pools' tensor-core consumer).  All sums are float32.
 //
-// Every warp works alone: it claims items, copies its own chunks with cp.async into two stages of
+// Every warp works alone: it goes through its own range, copies its chunks with cp.async into two stages of
 // its own in shared memory and multiplies them, with no producer warp and no barrier.  (A 16-token tile of
 // one head is 1152 bytes, and every bulk copy costs the SM 80-100 cycles whatever its size; a
 // 16-byte cp.async per lane moves 512 bytes of a warp's own choosing.)  The tile layout (int4.cuh)
