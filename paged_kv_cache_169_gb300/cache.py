@@ -33,6 +33,14 @@ def _dev_ptr(t: torch.Tensor, what: str) -> int:
     return t.data_ptr()
 
 
+def _ptr_on(t: torch.Tensor, what: str, dev: int) -> int:
+    if t.get_device() != dev:
+        raise ValueError(f"{what} must be a CUDA tensor on the pool's device")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
+
+
 def _alloc_on(stream):
     """Allocations made inside belong to the stream that will write them, and so does what fills them."""
     return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
@@ -143,12 +151,10 @@ class PagedKVCache:
         elif q_out is not None:
             raise ValueError("q_out without q")
         (kp, ks), (vp, vs) = _rows(k, n, h, d, "k", dev), _rows(v, n, h, d, "v", dev)
-        if slot_mapping.get_device() != dev or positions.get_device() != dev or cos_sin.get_device() != dev:
-            raise ValueError("slot_mapping, positions and cos_sin must be CUDA tensors on the pool's device")
         table_len, rot = cos_sin.shape
         a = abi.kv_rope_args(layer, qp, hq, op, kp, vp, _IN_DTYPE[dt], qs, ks, vs, os,
-                             _dev_ptr(slot_mapping, "slot_mapping"), _dev_ptr(positions, "positions"),
-                             _dev_ptr(cos_sin, "cos_sin"), table_len, rot, int(adjacent_pairs), n, flags,
+                             _ptr_on(slot_mapping, "slot_mapping", dev), _ptr_on(positions, "positions", dev),
+                             _ptr_on(cos_sin, "cos_sin", dev), table_len, rot, int(adjacent_pairs), n, flags,
                              _stream(stream))
         abi.kv_append_rope(self.handle, a)
         return q_out
@@ -169,10 +175,8 @@ class PagedKVCache:
         if k_out.shape != shape or v_out.shape != shape or k_out.dtype != v_out.dtype or k_out.dtype not in _IN_DTYPE:
             raise ValueError("k_out and v_out must be float16 or float32 [num_tokens, H, d]")
         dev = self.k[0].get_device()
-        if slot_mapping.get_device() != dev or k_out.get_device() != dev or v_out.get_device() != dev:
-            raise ValueError("slot_mapping, k_out and v_out must be CUDA tensors on the pool's device")
-        abi.kv_gather(self.handle, layer, _dev_ptr(slot_mapping, "slot_mapping"), shape[0], _dev_ptr(k_out, "k_out"),
-                      _dev_ptr(v_out, "v_out"), _IN_DTYPE[k_out.dtype], _stream(stream))
+        abi.kv_gather(self.handle, layer, _ptr_on(slot_mapping, "slot_mapping", dev), shape[0],
+                      _ptr_on(k_out, "k_out", dev), _ptr_on(v_out, "v_out", dev), _IN_DTYPE[k_out.dtype], _stream(stream))
         return k_out, v_out
 
     def copy_blocks(self, pairs: torch.Tensor, layer_begin: int = 0, layer_end: int | None = None,
