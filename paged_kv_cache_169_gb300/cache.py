@@ -102,7 +102,7 @@ class PagedKVCache:
     # -------------------------------------------------------------- device ops
     def append(self, layer: int, k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor,
                stream=None) -> None:
-        """k, v: [n, H, d] (pool dtype; f16/f32 for FP8 pools); slot_mapping: int64 [n]."""
+        """k, v: [n, H, d] (pool dtype; f16/f32 for FP8 and 4-bit pools); slot_mapping: int64 [n]."""
         if slot_mapping.dtype != torch.int64:
             raise ValueError("slot_mapping must be int64")
         n = slot_mapping.numel()
