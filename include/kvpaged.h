@@ -334,9 +334,9 @@ KV_API size_t paged_decode_workspace_size(const kv_pool* pool, int batch, int ma
  * products as fp16 (relative rounding 2^-11; below 2^8 by the running maximum).  With
  * the FP8 V scale folded into those weights, v_scale values must stay below 255.
  * F32 pools: fp32 operands throughout.
- * 4-bit pools: K and V values enter as fp16, which holds them exactly; with up to 4 query
- * heads per KV head the softmax weights enter as two fp16 terms (value and rounding error),
- * with 8 as one (relative rounding 2^-11).  The pool's device must be the current device.
+ * 4-bit pools: K and V values enter as fp16, which holds them exactly; the softmax weights
+ * enter as two fp16 terms (value and rounding error).  The pool's device must be the current
+ * device.
  * KV_DECODE_EARLY_POOL is accepted and has no effect.
  * The cached decode step of [KV Cache篇] §3.1 / [KV缓存机制解析] §5.1 over the
  * block-table gather of [PagedAttention] §3.2, with [KV Cache篇] §6.3's tiling. */
