@@ -142,6 +142,9 @@ __device__ __forceinline__ void append_row(const char* src, int in_bytes, char* 
     }
 }
 
+// Maxima (the m of parts too) are kept in raw sums: only their differences, which are exact where it matters,
+// are multiplied by the scale, so no score overflows.
+
 // What the kernel needs beside AttnArgs.  A unit u that crosses CTAs b0 .. b1 has its part of CTA b
 // in workspace slot b + u (the next unit's first CTA is at least b1 and its index one more: no two
 // units share a slot).
@@ -180,7 +183,7 @@ __device__ __forceinline__ void store_out(const AttnArgs& a, int64_t row, int D,
 // LATER ones), joined by one warp, all G rows at once.
 template <int D, int G>
 __device__ __forceinline__ void join_parts(const AttnArgs& a, char* smem, int w0, int kind, int n, int u, bool whole,
-                                           int lane) {
+                                           float xs, int lane) {
     using Sm = Smem<D, G>;
     constexpr int LPR = 32 / G < D / 4 ? 32 / G : D / 4, V = D / 4 / LPR;
     constexpr int NM = (kWarps + LPR - 1) / LPR;    // parts' (m, l) per lane: part i * LPR + sub
@@ -200,7 +203,7 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, char* smem, int w0
     for (int o = LPR / 2; o; o >>= 1) x.m = fmaxf(x.m, __shfl_xor_sync(FULL, x.m, o));
     #pragma unroll
     for (int i = 0; i < NM; ++i) {
-        ml[i].x = ex2_approx(ml[i].x - x.m);           // the part's weight, 0 past the end
+        ml[i].x = ex2_approx((ml[i].x - x.m) * xs);           // the part's weight, 0 past the end
         x.l = fmaf(ml[i].y, ml[i].x, x.l);
     }
     #pragma unroll
@@ -240,7 +243,7 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, char* smem, int w0
 // were written by other SMs): into the output (`last`), else into the first part's slot.
 template <int D, int G>
 __device__ __forceinline__ void merge_row(const AttnArgs& a, int64_t slot, int count, int stride, int64_t u, int r, bool last,
-                                          int lane) {
+                                          float xs, int lane) {
     constexpr int LPR = D / 4;
     const int sub = lane % LPR;                        // D 64: both half-warps do the same
     const int64_t row = slot * G + r, step = static_cast<int64_t>(stride) * G;
@@ -264,8 +267,8 @@ __device__ __forceinline__ void merge_row(const AttnArgs& a, int64_t slot, int c
                 if (k + i < n) rows[i] = __ldcg(po + (k0 + k + i) * step * (D / 4));
         };
         fetch(0);
-        const float mx = fmaxf(x.m, warp_max(v.x)), old = ex2_approx(x.m - mx);
-        const float w = ex2_approx(v.x - mx);          // 0 past the end
+        const float mx = fmaxf(x.m, warp_max(v.x)), old = ex2_approx((x.m - mx) * xs);
+        const float w = ex2_approx((v.x - mx) * xs);          // 0 past the end
         x.m = mx;
         x.l = fmaf(x.l, old, warp_sum(v.y * w));
         x.o[0] = make_float4(x.o[0].x * old, x.o[0].y * old, x.o[0].z * old, x.o[0].w * old);
@@ -296,7 +299,7 @@ __device__ __forceinline__ void merge_row(const AttnArgs& a, int64_t slot, int c
 // The CTA's parts of up to two units that cross CTAs (cross[i]: unit, first and last CTA) are in the
 // workspace: count them, and merge what they complete, a warp per row.  Called by every thread.
 template <int D, int G>
-__device__ __forceinline__ void finish_parts(const Int4Args& x, const Held* cross, int* s_go) {
+__device__ __forceinline__ void finish_parts(const Int4Args& x, const Held* cross, float xs, int* s_go) {
     const AttnArgs& a = x.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     auto parts_of = [&](int i) { return cross[i].u < 0 ? 0 : cross[i].last - cross[i].first + 1; };
@@ -332,7 +335,8 @@ __device__ __forceinline__ void finish_parts(const Int4Args& x, const Held* cros
             const int i = j / G, of = count_of(i);
             if (of > 0 && s_go[i])
                 merge_row<D, G>(a, static_cast<int64_t>(cross[i].first) + cross[i].u + first_of(i), of,
-                                level == 1 && parts_of(i) > kMergeFan ? kMergeFan : 1, cross[i].u, j % G, level == 1, lane);
+                                level == 1 && parts_of(i) > kMergeFan ? kMergeFan : 1, cross[i].u, j % G, level == 1, xs,
+                                lane);
         }
     }
 }
@@ -641,7 +645,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int4_kernel(const __
                     float mx = fmaxf(x[0][q], x[0][NQ + q]);
                     #pragma unroll
                     for (int u = 1; u < NU; ++u) mx = fmaxf(mx, fmaxf(x[u][q], x[u][NQ + q]));
-                    if (__any_sync(FULL, mx > m[q] + slack)) {
+                    if (__any_sync(FULL, mx - m[q] > slack)) {       // (m + slack may round up to mx)
                         #pragma unroll
                         for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
                         const float m_new = fmaxf(m[q], mx - lift), corr = ex2_approx((m[q] - m_new) * xs);
@@ -735,7 +739,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int4_kernel(const __
                     continue;
                 }
                 if (it.kind != WHOLE && g == 0)
-                    *reinterpret_cast<float2*>(ring + Sm::ML + ((it.kind - 1) * G + query) * 8) = make_float2(m[q] * xs, l[q]);
+                    *reinterpret_cast<float2*>(ring + Sm::ML + ((it.kind - 1) * G + query) * 8) = make_float2(m[q], l[q]);
                 float4* dst = it.kind == WHOLE
                                   ? reinterpret_cast<float4*>(static_cast<float*>(a.out) + row * D + g * (D / 8))
                                   : reinterpret_cast<float4*>(keep + query * D * 4 + g * (D / 2));
@@ -777,10 +781,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int4_kernel(const __
             if (lane == 0) { s_cross[kind - 1].u = h.u; s_cross[kind - 1].first = cta; }
             if (lane == 1) s_cross[kind - 1].last = cta;
         }
-        join_parts<D, G>(a, smem, w0, kind, n, h.u, whole, lane);
+        join_parts<D, G>(a, smem, w0, kind, n, h.u, whole, xs, lane);
     }
     __syncthreads();
-    finish_parts<D, G>(args, s_cross, s_go);
+    finish_parts<D, G>(args, s_cross, xs, s_go);
 }
 
 template <int D, int G>
@@ -935,7 +939,9 @@ int launch_attention_int4(const kv_pool* pool, int layer, const void* q, const v
     a.num_blocks = d.num_blocks;
     a.early_tables = (plan.flags & KV_DECODE_PDL) && (plan.flags & KV_DECODE_EARLY_TABLES) ? 1 : 0;
     a.out_f16 = (plan.flags & KV_DECODE_OUT_F16) ? 1 : 0;
-    a.qscale = scale * 1.4426950408889634f;             // log2(e): softmax evaluated with 2^x
+    // log2(e): softmax evaluated with 2^x.  Held where 16 of it are a float: two sums that differ at all do so by
+    // 2^-45 or more, which times 2e37 leaves nothing of the smaller one's weight already.
+    a.qscale = fminf(scale * 1.4426950408889634f, 2e37f);
     a.window = plan.window;
     return d.head_dim == 128 ? launch_g<128>(plan.group, pool, x, plan, stream)
                              : launch_g<64>(plan.group, pool, x, plan, stream);

@@ -63,3 +63,49 @@ def test_weights_are_not_rounded_to_float16(G, d, n):
     q = (rng.standard_normal((2 * G, d)) * 0.02).astype(np.float16)
     got, want, tol = run(random_tokens(rng, n, 2, d), random_tokens(rng, n, 2, d), q, 16, 1 / math.sqrt(d))
     assert np.all(np.abs(got - want) <= tol), np.max(np.abs(got - want) / tol)
+
+
+def one_hot_tokens(n, d, at, low):
+    """n tokens of one head: `low` (code, scale byte) in element 0, but for tokens in `at`: {token:
+    [(element, code, scale byte)]}."""
+    c, s = np.zeros((n, 1, d), dtype=np.int8), np.zeros((n, 1, d // 16), dtype=np.uint8)
+    for t in range(n):
+        for e, code, byte in at.get(t, [(0, *low)]):
+            c[t, 0, e], s[t, 0, e // 16] = code, byte
+    return c, s
+
+
+@pytest.mark.parametrize("G", [1, 2, 4, 8])
+@pytest.mark.parametrize("d", [64, 128])
+def test_scores_whose_float32_step_is_as_large_as_the_slack(G, d):
+    """Two sums of products, 349440000 and 349440064 (every sum exact in float32, where neighbours are 32
+    apart), in different chunks: weights of 0.0035 and 0.9965 at scale 1/sqrt(128).  The scores' distances
+    are exact, so the sums' error does not enter the tolerance."""
+    rng = np.random.default_rng(d + G)
+    n, byte832, byte16 = 130, O4.encode_scale(832.0), O4.encode_scale(16.0)
+    k = one_hot_tokens(n, d, {3: [(0, 7, byte832)], 100: [(0, 7, byte832), (18, 4, byte16)]}, (-7, byte832))
+    v = random_tokens(rng, n, 1, d)
+    q = np.zeros((G, d), dtype=np.float16)
+    q[:, 0], q[:, 18] = 60000, 1
+    kx = O4.dequantize(*k)[:, 0]
+    assert sorted(set(kx @ q[0].astype(np.float64)))[-2:] == [349440000.0, 349440064.0]
+    for scale in (1 / math.sqrt(128), 0.01, 0.5):
+        got, want, _ = run(k, v, q, 16, scale)
+        tol = 2 * (45 * 2.0 ** -24 + 2.0 ** -21 + 60 * 2.0 ** -24) * np.max(np.abs(O4.dequantize(*v)))
+        assert np.all(np.abs(got - want) <= tol), (scale, np.max(np.abs(got - want)), tol)
+
+
+@pytest.mark.parametrize("partition", [0, 32])
+@pytest.mark.parametrize("G,d", [(1, 128), (8, 128), (4, 64)])
+def test_scales_up_to_the_largest(G, d, partition):
+    """With scores of 10^30 and more apart one token has all the weight: its values, exactly.  In one
+    range and in parts that warps and CTAs join."""
+    rng = np.random.default_rng(d)
+    n = 2000
+    k, v = random_tokens(rng, n, 1, d), random_tokens(rng, n, 1, d)
+    q = rng.integers(-9, 10, (G, d)).astype(np.float16)
+    kx, vx = O4.dequantize(*k)[:, 0], O4.dequantize(*v)[:, 0]
+    best = np.argmax(kx @ q.astype(np.float64).T, axis=0)
+    for scale in (1e20, 1e30, 1e37, 2.9e38):
+        got, _, _ = run(k, v, q, 16, scale, partition_tokens=partition)
+        assert np.array_equal(got, vx[best]), scale
