@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int4_kernel(const __
     const int rng = rng0 + (warp < k ? warp : k);
     int pos = range_begin(min(rng, ranges));           // first chunk not yet taken
     const int end = warp < k ? range_begin(min(rng + 1, ranges)) : pos;
-    const float xs = a.qscale * 16.f;                  // raw sum -> log2-domain score
+    const float xs = a.qscale;                         // raw sum (q . k) -> log2-domain score
     // Weights are 2^(score - base), the base between 7 and 15 below the running maximum: at most 2^15
     // in float16, and normal there down to 2^-21 of the largest.
     const float lift = fminf(7.f / xs, 4e29f), slack = fminf(15.f / xs, 1e30f);
@@ -472,11 +472,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int4_kernel(const __
     bool first_item = true;
     for (bool started = false;; started = true) {
         if (started) {
-            // Query fragments in the order the K words expand: k-step 2w takes elements (0, 4) and
-            // (1, 5) of word w, k-step 2w+1 elements (2, 6) and (3, 7).  The pairs of the odd
-            // elements meet full K values, those of the even ones a sixteenth: the odd elements'
-            // query values are divided by 16 (exact unless below 2^-10, then off by at most
-            // 2^-25) and the score times 16.
+            // Query fragments in the order the K words expand: k-step 2w takes the even elements (0, 4)
+            // and (2, 6) of word w, which meet a sixteenth of K, k-step 2w+1 the odd ones (1, 5) and
+            // (3, 7), which meet K.  Each kind has sums of its own, so the queries stay as they are.
             cp_async_wait();                           // rows in shared memory came with the item's first chunk
             __syncwarp();
             const char* rows = s_q;
@@ -486,14 +484,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int4_kernel(const __
             for (int w = 0; w < WORDS; ++w) {
                 uint4 x = make_uint4(0, 0, 0, 0);
                 if (has_q) x = *reinterpret_cast<const uint4*>(rows + (col * D + t * (D / 4) + 8 * w) * 2);
-                const uint32_t e15 = __byte_perm(x.x, x.z, 0x7632), e37 = __byte_perm(x.y, x.w, 0x7632);
-                const __half2 f = __float2half2_rn(0.0625f);
-                const __half2 b0 = __hmul2(*reinterpret_cast<const __half2*>(&e15), f);
-                const __half2 b1 = __hmul2(*reinterpret_cast<const __half2*>(&e37), f);
                 qa[2 * w][0] = __byte_perm(x.x, x.z, 0x5410);
-                qa[2 * w][1] = *reinterpret_cast<const uint32_t*>(&b0);
-                qa[2 * w + 1][0] = __byte_perm(x.y, x.w, 0x5410);
-                qa[2 * w + 1][1] = *reinterpret_cast<const uint32_t*>(&b1);
+                qa[2 * w][1] = __byte_perm(x.y, x.w, 0x5410);
+                qa[2 * w + 1][0] = __byte_perm(x.x, x.z, 0x7632);
+                qa[2 * w + 1][1] = __byte_perm(x.y, x.w, 0x7632);
             }
             first_item = false;
             __syncwarp();                              // the next item's rows may follow now
@@ -603,21 +597,25 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int4_kernel(const __
                         b1 = *reinterpret_cast<const uint8_t*>(pk + (2 * u + 1) * St::SCALES);
                     }
                     const Int4Scale f0 = int4_scale_pair(scales_two(b0)), f1 = int4_scale_pair(scales_two(b1));
-                    float acc[4];
+                    float even[4], odd[4];
                     #pragma unroll
                     for (int w = 0; w < WORDS; ++w) {
                         const Int4Scale s0 = int4_scale_of(f0, w / 2), s1 = int4_scale_of(f1, w / 2);
                         uint32_t p0[4], p1[4];
                         int4_expand(k0.w[w], s0, p0);
                         int4_expand(k1.w[w], s1, p1);
-                        if (w == 0) mma_first(acc, p0[0], p1[0], p0[1], p1[1], qa[0][0], qa[0][1]);
-                        else mma_16816(acc, p0[0], p1[0], p0[1], p1[1], qa[2 * w][0], qa[2 * w][1]);
-                        mma_16816(acc, p0[2], p1[2], p0[3], p1[3], qa[2 * w + 1][0], qa[2 * w + 1][1]);
+                        if (w == 0) {
+                            mma_first(even, p0[0], p1[0], p0[2], p1[2], qa[0][0], qa[0][1]);
+                            mma_first(odd, p0[1], p1[1], p0[3], p1[3], qa[1][0], qa[1][1]);
+                        } else {
+                            mma_16816(even, p0[0], p1[0], p0[2], p1[2], qa[2 * w][0], qa[2 * w][1]);
+                            mma_16816(odd, p0[1], p1[1], p0[3], p1[3], qa[2 * w + 1][0], qa[2 * w + 1][1]);
+                        }
                     }
                     #pragma unroll
                     for (int q = 0; q < NQ; ++q) {
-                        x[u][q] = acc[q];
-                        x[u][NQ + q] = acc[2 + q];
+                        x[u][q] = fmaf(even[q], 16.f, odd[q]);
+                        x[u][NQ + q] = fmaf(even[2 + q], 16.f, odd[2 + q]);
                     }
                 }
                 const int first = tok == 0 ? lo : 0;
@@ -939,9 +937,9 @@ int launch_attention_int4(const kv_pool* pool, int layer, const void* q, const v
     a.num_blocks = d.num_blocks;
     a.early_tables = (plan.flags & KV_DECODE_PDL) && (plan.flags & KV_DECODE_EARLY_TABLES) ? 1 : 0;
     a.out_f16 = (plan.flags & KV_DECODE_OUT_F16) ? 1 : 0;
-    // log2(e): softmax evaluated with 2^x.  Held where 16 of it are a float: two sums that differ at all do so by
-    // 2^-45 or more, which times 2e37 leaves nothing of the smaller one's weight already.
-    a.qscale = fminf(scale * 1.4426950408889634f, 2e37f);
+    // log2(e): softmax evaluated with 2^x.  Held finite: two sums that differ at all do so by 2^-41 or
+    // more, which times 3e38 leaves nothing of the smaller one's weight already.
+    a.qscale = fminf(scale * 1.4426950408889634f, 3e38f);
     a.window = plan.window;
     return d.head_dim == 128 ? launch_g<128>(plan.group, pool, x, plan, stream)
                              : launch_g<64>(plan.group, pool, x, plan, stream);

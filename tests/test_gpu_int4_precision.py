@@ -109,3 +109,19 @@ def test_scales_up_to_the_largest(G, d, partition):
     for scale in (1e20, 1e30, 1e37, 2.9e38):
         got, _, _ = run(k, v, q, 16, scale, partition_tokens=partition)
         assert np.array_equal(got, vx[best]), scale
+
+
+@pytest.mark.parametrize("G", [1, 4, 8])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("odd", [0, 1])
+def test_small_queries_keep_their_bits(G, d, odd):
+    """Queries down to the smallest float16, in even and in odd elements, beside keys and a scale that
+    make them count."""
+    rng = np.random.default_rng(d + G + odd)
+    n = 90
+    q = np.zeros((G, d), dtype=np.float16)
+    q[:, odd::2] = rng.integers(-40, 41, (G, d // 2)) * 2.0 ** -24
+    k, v = random_tokens(rng, n, 1, d, 184, 199), random_tokens(rng, n, 1, d)
+    got, want, tol = run(k, v, q, 8, 2.0)
+    assert np.ptp(O4.dequantize(*k)[:, 0] @ q[0].astype(np.float64)) * 2 > 0.05          # the scores do differ
+    assert np.all(np.abs(got - want) <= tol), np.max(np.abs(got - want) / tol)
