@@ -541,10 +541,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int4_kernel(const __
                 if (n > 0) {
                     if (a.k_new != nullptr && c0 + n == cps && ctx > 0) {
                         // fused append: the newest token goes to its slot before the item's copies (a bad
-                        // block id, flagged by load_oids, takes none)
+                        // block id, flagged by load_oids, and a length that was clamped take none)
                         const int last = ctx - 1, o = last >> 3;
                         const int id = a.tables[static_cast<int64_t>(s) * a.max_blocks + (o >> lg_opb)];
-                        if (id >= 0 && id < a.num_blocks) {
+                        if (id >= 0 && id < a.num_blocks && a.lens[s] == ctx) {
                             const int64_t to = (((static_cast<int64_t>(id) * a.H + h) << lg_opb) + (o & (opb - 1))) * OCT;
                             const int64_t row = (static_cast<int64_t>(s) * a.H + h) * D * a.in_bytes;
                             append_row<D>(a.k_new + row, a.in_bytes, a.kpool + to, last & 7, true, lane);

@@ -1,0 +1,64 @@
+"""GPU: the fused append at the edges of what it may store."""
+
+import numpy as np
+import pytest
+import torch
+
+from paged_kv_cache_169_gb300 import abi
+from paged_kv_cache_169_gb300.cache import PagedKVCache
+
+pytestmark = pytest.mark.gpu
+
+
+def lengths_too_long(pool, G, d, B, **more):
+    """A sequence whose length is beyond max_context, or beyond its table row, or negative, has no
+    place for a new token: KV_DEVERR_CONTEXT, nothing stored, and the attention over its clamped length
+    is that of the cache as it was.  Its neighbours' tokens are stored."""
+    rng = np.random.default_rng(d + B + G)
+    H, limit, width = 2, 3 * B + 5, 4
+    nb = 5 * width
+    cache = PagedKVCache(1, nb, B, H, d, pool)
+    dt = torch.float32 if pool == "f32" else torch.float16
+    for t in cache.k + cache.v:
+        if pool == "int4":
+            a = rng.integers(0, 256, tuple(t.shape), dtype=np.uint8)
+            a[..., 4 * d:] = rng.integers(80, 110, a[..., 4 * d:].shape)
+            t.copy_(torch.from_numpy(a))
+        elif pool == "fp8":
+            t.copy_(torch.from_numpy(rng.integers(0, 120, tuple(t.shape), dtype=np.uint8)))
+        else:
+            t.copy_(torch.from_numpy(rng.standard_normal(tuple(t.shape)).astype(np.float32)))
+    tab = torch.from_numpy(rng.permutation(nb).astype(np.int32).reshape(5, width)).cuda()
+    q = torch.from_numpy(rng.standard_normal((5, H * G, d)).astype(np.float32)).cuda().to(dt)
+    kn, vn = (torch.from_numpy(rng.standard_normal((5, H, d)).astype(np.float32)).cuda().to(dt) for _ in range(2))
+    full = width * B                                   # what a table row holds
+    for limit in (limit, full, full + 7):
+        most = min(limit, full)
+        lens = torch.tensor([most, most + 1, 9, -3, 2 ** 31 - 1], dtype=torch.int32, device="cuda")
+        clamped = torch.tensor([most, most, 9, 0, most], dtype=torch.int32, device="cuda")
+        good = [0, 2]
+        before = [cache.k[0].clone(), cache.v[0].clone()]
+        plain = cache.attention_ex(0, q, tab, clamped, limit, 0.1, **more).clone()
+        assert cache.device_error() == 0
+        out = cache.attention_ex(0, q, tab, lens, limit, 0.1, k_new=kn, v_new=vn, **more)
+        assert cache.device_error() == abi.KV_DEVERR_CONTEXT
+        after = [cache.k[0].clone(), cache.v[0].clone()]
+        for old, new in zip(before, after):
+            changed = set((old != new).flatten(1).any(1).nonzero().flatten().tolist())
+            assert changed == {int(tab[s, (int(clamped[s]) - 1) // B]) for s in good}
+        for s in (1, 3, 4):
+            assert torch.equal(out[s], plain[s]), s
+        want = cache.attention_ex(0, q, tab, clamped, limit, 0.1, **more)
+        for s in good:                                 # as after a separate append
+            assert torch.equal(out[s], want[s]), s
+        for t, old in zip((cache.k[0], cache.v[0]), before):
+            t.copy_(old)
+    assert cache.device_error() == 0
+    cache.close()
+
+
+@pytest.mark.parametrize("G,d,B", [(1, 128, 16), (4, 64, 8), (8, 128, 32)])
+def test_int4_lengths_too_long_store_nothing(G, d, B):
+    lengths_too_long("int4", G, d, B)
+    lengths_too_long("int4", G, d, B, window=20)
+    lengths_too_long("int4", G, d, B, partition_tokens=32)
