@@ -777,6 +777,17 @@ __device__ __forceinline__ void pfx_ticket_resolve(const AttnArgs& a, PfxTicket&
     }
 }
 
+// Set (s_misc[1]) where a length of the launch was clamped.  Never cleared: a CTA that finds it there
+// without cause only reads the lengths of its appends again.
+constexpr int kClamped = 0x436c6d70;
+
+// Whether sequence s has a slot for its newest token: one whose length was clamped has none.  Asked
+// by the consumers, for the chunks that hold a new token only (in the producer's fill: 0.4 % of a
+// small batch's step).
+__device__ __forceinline__ bool has_slot(const AttnArgs& a, const int* s_ctx, const int* s_misc, int s) {
+    return s_misc[1] != kClamped || a.lens[s] == s_ctx[s];
+}
+
 // Fused append: lane's D/32 elements of one new-token row (src, in_bytes per element)
 // are converted to the pool type (FP8: RNE-satfinite(x / scale)) and written both into
 // the consumer's stage row and into the pool slot, so the attention below sees exactly
@@ -892,6 +903,7 @@ __device__ __forceinline__ void consumer_mma(const AttnArgs& a, char* smem, cons
     Ticket tk{};
     PfxTicket ptk{};
     const int* s_pfx = s_ctx + 2 * kMaxBatch;       // shared prefixes (PFX launches only)
+    const int* s_misc = reinterpret_cast<const int*>(smem + C::MISC_OFF);
 
     for (int j = 0;; ++j) {
         const int st = j % NSW;
@@ -940,7 +952,8 @@ __device__ __forceinline__ void consumer_mma(const AttnArgs& a, char* smem, cons
                 qa[k][1] = real ? qrow[8 * k + 4 + t] : 0u;
             }
         }
-        if (C::FP8 && (flags & F_PATCH)) {
+        const bool patch = (flags & F_PATCH) && has_slot(a, s_ctx, s_misc, ms);
+        if (C::FP8 && patch) {
             // the new token, quantised with its block's scale, into the stage row and the slot
             const int r = mp->patch_row;
             const int64_t sh = static_cast<int64_t>(ms) * a.H + mh;
@@ -952,7 +965,7 @@ __device__ __forceinline__ void consumer_mma(const AttnArgs& a, char* smem, cons
                          a.vpool + grow * C::ROW, __ldg(a.vscale + mp->patch_id), lane, r & 7);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-        } else if (flags & F_PATCH) {
+        } else if (patch) {
             // the new token's row, into the swizzled stage and into the pool slot
             const int r = mp->patch_row;
             const int64_t sh = static_cast<int64_t>(ms) * a.H + mh;
@@ -1284,11 +1297,13 @@ __global__ void __launch_bounds__(C::THREADS, C::CPS) attention_partition_kernel
         if (tid == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     }
     // ---- prologue: clamp lengths, items per sequence, inclusive prefix
+    int* s_misc = reinterpret_cast<int*>(smem + C::MISC_OFF);   // launch-wide: the partition size, kClamped
     for (int s = tid; s < a.batch; s += C::THREADS) {
         int c = a.lens[s];
         if (c < 0 || c > a.ctx_limit) {
             if (blockIdx.x == 0) atomicOr(a.err, KV_DEVERR_CONTEXT);
             c = c < 0 ? 0 : a.ctx_limit;
+            s_misc[1] = kClamped;
         }
         s_ctx[s] = c;
         if constexpr (C::PFX) s_pfx[s] = 0;
@@ -1322,7 +1337,6 @@ __global__ void __launch_bounds__(C::THREADS, C::CPS) attention_partition_kernel
         }
         __syncthreads();
     }
-    int* s_misc = reinterpret_cast<int*>(smem + C::MISC_OFF);
     if (warp == 0) {
         // A launch whose items all fit in one round balances best with the smallest
         // partition that still gives every item a consumer warp: take P_alt when it does.
@@ -1659,7 +1673,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CPS) attention_partition_kernel
                 }
             }
         }
-        if (meta.flags & F_PATCH) {
+        if ((meta.flags & F_PATCH) && has_slot(a, s_ctx, s_misc, meta.s)) {
             // this warp owns the stage now: put the new token into its row and its slot
             const Meta* mp = reinterpret_cast<const Meta*>(mst);
             const int r = mp->patch_row;

@@ -62,3 +62,12 @@ def test_int4_lengths_too_long_store_nothing(G, d, B):
     lengths_too_long("int4", G, d, B)
     lengths_too_long("int4", G, d, B, window=20)
     lengths_too_long("int4", G, d, B, partition_tokens=32)
+
+
+@pytest.mark.parametrize("pool,G,d,B", [("f32", 1, 128, 16), ("f32", 1, 64, 8), ("f16", 1, 128, 16), ("f16", 1, 64, 32),
+                                        ("f16", 4, 128, 16), ("f16", 8, 128, 8), ("f16", 2, 64, 16),
+                                        ("fp8", 1, 128, 16), ("fp8", 1, 64, 8), ("fp8", 8, 128, 32), ("fp8", 4, 64, 16)])
+def test_lengths_too_long_store_nothing(pool, G, d, B):
+    lengths_too_long(pool, G, d, B)
+    lengths_too_long(pool, G, d, B, window=20)
+    lengths_too_long(pool, G, d, B, partition_tokens=32, flags=abi.KV_DECODE_PDL | abi.KV_DECODE_EARLY_TABLES)
