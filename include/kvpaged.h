@@ -356,8 +356,9 @@ KV_API int paged_decode_attention(kv_pool* pool, int layer, const void* q, float
  * paged_decode_attention.  Requirement: the block receiving a sequence's new token must
  * not be shared with another sequence of the batch (copy-on-write already done, as the
  * host allocator guarantees); a sequence with context_len 0 appends nothing, nor does one
- * whose length is clamped (KV_DEVERR_CONTEXT).  All other arguments, the workspace and the
- * errors are those of paged_decode_attention.
+ * whose length is clamped (KV_DEVERR_CONTEXT) or whose block id for it lies outside the pool
+ * (KV_DEVERR_BLOCK_ID).  All other arguments, the workspace and the errors are those of
+ * paged_decode_attention.
  * The write-then-read order of [KV Cache篇] §3.1 and the batched cache update of
  * [KV缓存机制解析] §6.2, done inside the attention kernel by the warp that owns the
  * sequence's last chunk. */

@@ -781,11 +781,12 @@ __device__ __forceinline__ void pfx_ticket_resolve(const AttnArgs& a, PfxTicket&
 // without cause only reads the lengths of its appends again.
 constexpr int kClamped = 0x436c6d70;
 
-// Whether sequence s has a slot for its newest token: one whose length was clamped has none.  Asked
-// by the consumers, for the chunks that hold a new token only (in the producer's fill: 0.4 % of a
-// small batch's step).
-__device__ __forceinline__ bool has_slot(const AttnArgs& a, const int* s_ctx, const int* s_misc, int s) {
-    return s_misc[1] != kClamped || a.lens[s] == s_ctx[s];
+// Whether sequence s has a slot for its newest token: one whose length was clamped has none, nor one
+// whose block id lies outside the pool (which became 0: patch_id).  Asked by the consumers, for the
+// chunks that hold a new token only (in the producer's fill: 0.4 % of a small batch's step).
+__device__ __forceinline__ bool has_slot(const AttnArgs& a, const int* s_ctx, const int* s_misc, int s, int patch_id) {
+    if (s_misc[1] == kClamped && a.lens[s] != s_ctx[s]) return false;
+    return patch_id != 0 || a.tables[static_cast<int64_t>(s) * a.max_blocks + (s_ctx[s] - 1) / a.B] == 0;
 }
 
 // Fused append: lane's D/32 elements of one new-token row (src, in_bytes per element)
@@ -952,7 +953,7 @@ __device__ __forceinline__ void consumer_mma(const AttnArgs& a, char* smem, cons
                 qa[k][1] = real ? qrow[8 * k + 4 + t] : 0u;
             }
         }
-        const bool patch = (flags & F_PATCH) && has_slot(a, s_ctx, s_misc, ms);
+        const bool patch = (flags & F_PATCH) && has_slot(a, s_ctx, s_misc, ms, mp->patch_id);
         if (C::FP8 && patch) {
             // the new token, quantised with its block's scale, into the stage row and the slot
             const int r = mp->patch_row;
@@ -1673,7 +1674,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CPS) attention_partition_kernel
                 }
             }
         }
-        if ((meta.flags & F_PATCH) && has_slot(a, s_ctx, s_misc, meta.s)) {
+        if ((meta.flags & F_PATCH) && has_slot(a, s_ctx, s_misc, meta.s, reinterpret_cast<const Meta*>(mst)->patch_id)) {
             // this warp owns the stage now: put the new token into its row and its slot
             const Meta* mp = reinterpret_cast<const Meta*>(mst);
             const int r = mp->patch_row;

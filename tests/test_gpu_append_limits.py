@@ -71,3 +71,34 @@ def test_lengths_too_long_store_nothing(pool, G, d, B):
     lengths_too_long(pool, G, d, B)
     lengths_too_long(pool, G, d, B, window=20)
     lengths_too_long(pool, G, d, B, partition_tokens=32, flags=abi.KV_DECODE_PDL | abi.KV_DECODE_EARLY_TABLES)
+
+
+@pytest.mark.parametrize("pool,G,d,B", [("f32", 1, 128, 16), ("f16", 1, 128, 16), ("f16", 1, 64, 32), ("f16", 4, 128, 16),
+                                        ("f16", 2, 64, 16), ("fp8", 1, 128, 16), ("fp8", 8, 128, 32), ("fp8", 1, 64, 8),
+                                        ("int4", 1, 128, 16), ("int4", 8, 64, 8)])
+def test_bad_block_ids_store_nothing(pool, G, d, B):
+    """A new token whose block id lies outside the pool is stored nowhere (block 0, which is read in its
+    place, belongs to another sequence); a sequence whose token goes into block 0 has it stored."""
+    rng = np.random.default_rng(d + B + G)
+    H, nb = 2, 9
+    cache = PagedKVCache(1, nb, B, H, d, pool)
+    dt = torch.float32 if pool == "f32" else torch.float16
+    for t in cache.k + cache.v:
+        if t.dtype == torch.uint8:
+            t.copy_(torch.from_numpy(rng.integers(80, 110, tuple(t.shape), dtype=np.uint8)))
+        else:
+            t.copy_(torch.from_numpy(rng.standard_normal(tuple(t.shape)).astype(np.float32)))
+    tab = np.array([[3, 4, -5], [1, nb, -1], [2, 0, -1], [5, 2 ** 31 - 1, 6]], dtype=np.int32)
+    lens = torch.tensor([2 * B + 1, B + 3, 2 * B, B + 1], dtype=torch.int32, device="cuda")
+    q = torch.from_numpy(rng.standard_normal((4, H * G, d)).astype(np.float32)).cuda().to(dt)
+    kn, vn = (torch.from_numpy(rng.standard_normal((4, H, d)).astype(np.float32)).cuda().to(dt) for _ in range(2))
+    before = [cache.k[0].clone(), cache.v[0].clone()]
+    cache.attention_ex(0, q, torch.from_numpy(tab).cuda(), lens, 3 * B, 0.1, k_new=kn, v_new=vn)
+    assert cache.device_error() == abi.KV_DEVERR_BLOCK_ID
+    slots = torch.tensor([-1, -1, B - 1, -1], device="cuda")           # block 0, its last row
+    fused = [cache.k[0].clone(), cache.v[0].clone()]
+    for t, old in zip((cache.k[0], cache.v[0]), before):
+        t.copy_(old)
+    cache.append(0, kn, vn, slots)
+    assert torch.equal(fused[0], cache.k[0]) and torch.equal(fused[1], cache.v[0])
+    cache.close()
