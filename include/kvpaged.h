@@ -29,7 +29,8 @@
  *        [chunk of d/8 elements][token/2][d/32][token%2]; scales [d/16][token].
  *   Stored from x, per token, head and 16 elements: scale = min(amax/7, 896) rounded to
  *   nearest even on the scale's grid, code = x/scale rounded to nearest even, within -7 .. 7
- *   (scale 0: code 0).  Values beyond 6272 saturate; a group holding a NaN reads as NaN.
+ *   (scale 0: code 0).  Values beyond 6272 saturate; a group holding a NaN has the
+ *   scale byte 0xFF and codes 0, and reads as NaN.
  */
 #ifndef KVPAGED_H
 #define KVPAGED_H

@@ -80,6 +80,7 @@ template <int N>
 __device__ __forceinline__ uint32_t int4_nibbles(float (&x)[N], float amax, float s) {
     const float inv = int4_inverse(s);
     if (!(amax >= 7.f * kInt4MinNormal && amax <= 7.f * kInt4MaxScale)) {
+        if (!(amax == amax)) s = 0.f;                  // a NaN in the group: every code 0
         #pragma unroll
         for (int i = 0; i < N; ++i) x[i] = fminf(fmaxf(x[i], -7.f * s), 7.f * s);
     }

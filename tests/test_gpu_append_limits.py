@@ -4,8 +4,10 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import int4 as O4
+from oracle import rope as OR
 from paged_kv_cache_169_gb300 import abi
-from paged_kv_cache_169_gb300.cache import PagedKVCache
+from paged_kv_cache_169_gb300.cache import PagedKVCache, rope_table
 
 pytestmark = pytest.mark.gpu
 
@@ -102,3 +104,47 @@ def test_bad_block_ids_store_nothing(pool, G, d, B):
     cache.append(0, kn, vn, slots)
     assert torch.equal(fused[0], cache.k[0]) and torch.equal(fused[1], cache.v[0])
     cache.close()
+
+
+@pytest.mark.parametrize("in_dtype", [torch.float16, torch.float32])
+@pytest.mark.parametrize("d,B", [(128, 16), (64, 8)])
+def test_a_group_with_a_nan_is_the_same_bytes_from_every_call(in_dtype, d, B):
+    """kv_append, kv_append_rope and the fused decode step, neighbours in one V word or not: the scale
+    byte of a NaN and codes of 0."""
+    rng = np.random.default_rng(d)
+    H, n = 2, 24
+    x = rng.standard_normal((2, n, H, d)).astype(np.float32)
+    x[:, 1, 0, 3] = x[:, 2, 1, 17] = x[:, 3, 0, d - 1] = x[:, 8, 1, 0] = np.nan
+    x[:, 5, 0, 16:32] = np.nan
+    x[:, 6, 0, 4], x[:, 6, 0, 5] = np.nan, np.inf
+    x[:, 11, 1, 9] = np.array([0xFFC01234], dtype=np.uint32).view(np.float32)[0]         # a NaN of another sign
+    k, v = (torch.from_numpy(a).cuda().to(in_dtype) for a in x)
+    # half of the tokens side by side, the others anywhere; the fused call, whose sequences share no
+    # block, puts token i into block i
+    slots = np.concatenate([np.arange(12) + n, rng.permutation(n)[:12]]).astype(np.int64)
+    alone = (np.arange(n) * B + rng.integers(0, B, n)).astype(np.int64)
+    caches = [PagedKVCache(1, n, B, H, d, "int4") for _ in range(3)]
+    for c in caches:
+        c.k[0].zero_()
+        c.v[0].zero_()
+    caches[0].append(0, k, v, torch.from_numpy(slots).cuda())
+    caches[1].append_rope(0, k, v, torch.from_numpy(slots).cuda(), torch.zeros(n, dtype=torch.int32, device="cuda"),
+                          rope_table(1, d))
+    q = torch.zeros(n, H, d, device="cuda").half()
+    t = torch.from_numpy(alone).cuda()
+    caches[2].attention_ex(0, q, (t // B).to(torch.int32).reshape(n, 1), (t % B + 1).to(torch.int32), B, 0.1,
+                           k_new=k, v_new=v)
+    # at position 0 a key's pairs turn by nothing, but a NaN or an infinity times 0 makes its partner a NaN
+    turned = OR.rotate(k.cpu().numpy(), rope_table(1, d).cpu().numpy()[np.zeros(n, dtype=int)], d, False, np.float32)
+    for x, which in ((k, "k"), (v, "v")):
+        for c, at in zip(caches, (slots, slots, alone)):
+            codes, scales = O4.quantize(turned if which == "k" and c is caches[1] else x.float().cpu().numpy())
+            assert (scales == O4.NAN_BYTE).sum() >= 6
+            want = np.zeros(tuple(c.k[0].shape), dtype=np.uint8)
+            for i, s in enumerate(at.tolist()):
+                for h in range(H):
+                    O4.store(want, which, s // B, h, s % B, codes[i, h], scales[i, h])
+            assert np.array_equal(getattr(c, which)[0].cpu().numpy(), want), which
+    for c in caches:
+        assert c.device_error() == 0
+        c.close()
