@@ -145,12 +145,13 @@ __device__ __forceinline__ void append_row(const char* src, int in_bytes, char* 
 // Maxima (the m of parts too) are kept in raw sums: only their differences, which are exact where it matters,
 // are multiplied by the scale, so no score overflows.
 
-// What the kernel needs beside AttnArgs.  A unit u that crosses CTAs b0 .. b1 has its part of CTA b
-// in workspace slot b + u (the next unit's first CTA is at least b1 and its index one more: no two
-// units share a slot).
+// What the kernel needs beside AttnArgs.  A unit that crosses CTAs b0 .. b1 has its part of CTA b in
+// workspace slot b0 + b, slots 2 b0 .. b0 + b1 of its own: the next one that crosses begins in CTA b1 at
+// the earliest, at slot 2 b1.  Its counters go by its first slot.
 struct Int4Args {
     AttnArgs a;
     int min_range;         // chunks per range, at least
+    unsigned* done;        // [slots] parts, or groups of them, finished of the unit that starts at a slot
     unsigned* group_done;  // [slots] parts finished of the group of kMergeFan that starts at a slot
 };
 
@@ -183,7 +184,7 @@ __device__ __forceinline__ void store_out(const AttnArgs& a, int64_t row, int D,
 // LATER ones), joined by one warp, all G rows at once.
 template <int D, int G>
 __device__ __forceinline__ void join_parts(const AttnArgs& a, char* smem, int w0, int kind, int n, int u, bool whole,
-                                           float xs, int lane) {
+                                           int slot, float xs, int lane) {
     using Sm = Smem<D, G>;
     constexpr int LPR = 32 / G < D / 4 ? 32 / G : D / 4, V = D / 4 / LPR;
     constexpr int NM = (kWarps + LPR - 1) / LPR;    // parts' (m, l) per lane: part i * LPR + sub
@@ -232,7 +233,7 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, char* smem, int w0
     if (whole) {
         store_out<LPR, V>(a, static_cast<int64_t>(u) * G + r, D, x, sub);
     } else {
-        const int64_t row = (static_cast<int64_t>(blockIdx.x) + u) * G + r;
+        const int64_t row = static_cast<int64_t>(slot) * G + r;
         if (sub == 0) reinterpret_cast<float2*>(a.part_ml)[row] = make_float2(x.m, x.l);
         #pragma unroll
         for (int i = 0; i < V; ++i) reinterpret_cast<float4*>(a.part_o + row * D)[sub + i * LPR] = x.o[i];
@@ -323,8 +324,8 @@ __device__ __forceinline__ void finish_parts(const Int4Args& x, const Held* cros
             const bool before = level == 1 && most > kMergeFan ? s_go[warp] != 0 : true;
             bool go = before;
             if (of > 0 && before) {
-                const int at = cross[warp].first + cross[warp].u;
-                unsigned* ctr = level == 0 ? x.group_done + at + first_of(warp) : a.arrivals + cross[warp].u;
+                const int at = 2 * cross[warp].first;
+                unsigned* ctr = level == 0 ? x.group_done + at + first_of(warp) : x.done + at;
                 go = atom_add_acq_rel_gpu(ctr, 1u) == static_cast<unsigned>(of - 1);
                 if (go) *ctr = 0;                      // left zero for the next call
             }
@@ -334,7 +335,7 @@ __device__ __forceinline__ void finish_parts(const Int4Args& x, const Held* cros
         for (int j = warp; j < 2 * G; j += kWarps) {
             const int i = j / G, of = count_of(i);
             if (of > 0 && s_go[i])
-                merge_row<D, G>(a, static_cast<int64_t>(cross[i].first) + cross[i].u + first_of(i), of,
+                merge_row<D, G>(a, 2 * cross[i].first + first_of(i), of,
                                 level == 1 && parts_of(i) > kMergeFan ? kMergeFan : 1, cross[i].u, j % G, level == 1, xs,
                                 lane);
         }
@@ -774,12 +775,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int4_kernel(const __
         const int n = __ffs(~(__ballot_sync(FULL, later == h.u) >> (w0 + 1)));         // w0's and the LATER parts after it
         const bool whole = h.first >= cta_begin && h.last < cta_end;
         // at most one unit comes from an earlier CTA, and one that starts here goes on
+        int slot = 0;
         if (!whole) {
             const int cta = range_of(lane == 0 ? h.first : h.last) / k;
             if (lane == 0) { s_cross[kind - 1].u = h.u; s_cross[kind - 1].first = cta; }
             if (lane == 1) s_cross[kind - 1].last = cta;
+            slot = __shfl_sync(FULL, cta, 0) + static_cast<int>(blockIdx.x);
         }
-        join_parts<D, G>(a, smem, w0, kind, n, h.u, whole, xs, lane);
+        join_parts<D, G>(a, smem, w0, kind, n, h.u, whole, slot, xs, lane);
     }
     __syncthreads();
     finish_parts<D, G>(args, s_cross, xs, s_go);
@@ -852,23 +855,22 @@ int launch_g(int group, const kv_pool* pool, const Int4Args& x, const AttnPlan& 
 
 constexpr size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
-// Workspace: the units' counters, the part groups' counters, (m, l), o.
+// Workspace: the units' counters, the part groups' counters, (m, l), o; two slots per CTA, whatever the
+// batch.
 struct Layout {
     size_t groups, ml, o, end;
-    Layout(int64_t units, int64_t slots, int group, int head_dim) {
-        groups = align256(static_cast<size_t>(units) * 4);
-        ml = groups + align256(static_cast<size_t>(slots) * 4);
-        o = ml + align256(static_cast<size_t>(slots) * group * 2 * sizeof(float));
-        end = o + static_cast<size_t>(slots) * group * head_dim * sizeof(float) + 256;
+    Layout(const kv_pool* pool, int group) {
+        const size_t slots = 2 * static_cast<size_t>(pool->num_sms);
+        groups = align256(slots * 4);
+        ml = 2 * groups;
+        o = ml + align256(slots * group * 2 * sizeof(float));
+        end = o + slots * group * pool->desc.head_dim * sizeof(float) + 256;
     }
 };
 
-// Units of the largest launch of a call; a slot per CTA and unit.
+// Units of the largest launch of a call.
 int64_t units_of(const kv_pool* pool, int batch) {
     return static_cast<int64_t>(batch < kMaxBatch ? batch : kMaxBatch) * pool->desc.num_heads;
-}
-int64_t slots_of(const kv_pool* pool, int batch) {
-    return units_of(pool, batch) + static_cast<int64_t>(pool->num_sms);
 }
 
 }  // namespace
@@ -894,7 +896,7 @@ int plan_attention_int4(const kv_pool* pool, int batch, int max_context, int par
     plan->max_parts = static_cast<int>(chunks);
     plan->group = group;
     plan->window = window;
-    plan->ws_bytes = Layout(units_of(pool, batch), slots_of(pool, batch), group, d.head_dim).end;
+    plan->ws_bytes = Layout(pool, group).end;
     return KV_OK;
 }
 
@@ -908,7 +910,7 @@ int launch_attention_int4(const kv_pool* pool, int layer, const void* q, const v
     if (dev != pool->device) return KV_ERR_INVALID_ARG;
     if (batch == 0) return KV_OK;
     char* ws = static_cast<char*>(workspace);
-    const Layout lay(units_of(pool, batch), slots_of(pool, batch), plan.group, d.head_dim);
+    const Layout lay(pool, plan.group);
     if (!(plan.flags & KV_DECODE_WORKSPACE_ZEROED) && cudaMemsetAsync(ws, 0, lay.ml, stream) != cudaSuccess)
         return KV_ERR_CUDA;
     Int4Args x{};
@@ -922,7 +924,7 @@ int launch_attention_int4(const kv_pool* pool, int layer, const void* q, const v
     a.out = out;
     a.tables = block_tables;
     a.lens = context_lens;
-    a.arrivals = reinterpret_cast<unsigned*>(ws);
+    x.done = reinterpret_cast<unsigned*>(ws);
     x.group_done = reinterpret_cast<unsigned*>(ws + lay.groups);
     a.part_ml = reinterpret_cast<float*>(ws + lay.ml);
     a.part_o = reinterpret_cast<float*>(ws + lay.o);
