@@ -1756,7 +1756,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CPS) attention_partition_kernel
                 for (int off = TPL; off < LPR; off <<= 1) x += __shfl_xor_sync(FULL, x, off);
                 x *= xs;
                 x = (tok_l < nt && tok_l >= lo) ? x : -CUDART_INF_F;
-                if (__any_sync(FULL, x > m[g] + 8.f)) {   // raise the running max only when needed
+                if (__any_sync(FULL, x - m[g] > 8.f)) {   // raise the running max only when needed (m + 8 may round up to x)
                     const float m_new = fmaxf(m[g], HP >= 2 ? group_max<LPR>(x) : warp_max(x));
                     const float corr = ex2_approx(m[g] - m_new);
                     lsum[g] *= corr;
