@@ -51,13 +51,6 @@ template <typename TIn> struct Raw;
 template <> struct Raw<__half> { uint4 a; };
 template <> struct Raw<float> { float4 a, b; };
 
-__device__ __forceinline__ void load_raw(const char* p, Raw<__half>& r) {
-    r.a = __ldcs(reinterpret_cast<const uint4*>(p));
-}
-__device__ __forceinline__ void load_raw(const char* p, Raw<float>& r) {
-    r.a = __ldcs(reinterpret_cast<const float4*>(p));
-    r.b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-}
 __device__ __forceinline__ void widen(const Raw<__half>& r, float (&x)[8]) {
     const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
     #pragma unroll
@@ -143,10 +136,6 @@ __device__ __forceinline__ void store_unit(char* at, char* sc, int64_t head, flo
 template <typename TIn> constexpr int kRowsAhead = sizeof(TIn) == 2 ? 8 : 4;
 // CTAs per SM: quantising takes more registers (6, 7, 8: 57.7, 59.0, 63.0 us for the 4-bit prompt).
 template <kv_dtype POOL> constexpr int kCtasPerSm = POOL == KV_INT4 ? 6 : 7;
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const char* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
 
 enum : int { NO_ROTATION = 0, HALF_PAIRS = 1, ADJACENT_PAIRS = 2 };
 

@@ -80,9 +80,6 @@ template <int D, int G> struct Smem {
     static_assert(WARP % 16 == 0 && G * D * 4 <= RING, "16-byte alignment; a part fits the stages");
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const char* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // mma_16816 with a zero accumulator

@@ -264,14 +264,6 @@ int plan_attention_prefix(const kv_pool* pool, int batch, int max_context, int p
     return KV_OK;
 }
 
-int launch_attention(const kv_pool* pool, int layer, const void* q, float* out,
-                     const int32_t* block_tables, int max_blocks, const int32_t* context_lens,
-                     int batch, int max_context, float scale, const AttnPlan& plan,
-                     void* workspace, cudaStream_t stream) {
-    return launch_attention_append(pool, layer, q, nullptr, nullptr, 0, out, block_tables, max_blocks,
-                                   context_lens, batch, max_context, scale, plan, workspace, stream);
-}
-
 int launch_attention_append(const kv_pool* pool, int layer, const void* q, const void* k_new,
                             const void* v_new, int in_bytes, void* out, const int32_t* block_tables,
                             int max_blocks, const int32_t* context_lens, int batch, int max_context,

@@ -85,11 +85,7 @@ int plan_attention(const kv_pool* pool, int batch, int max_context, int partitio
 // KV_ERR_UNSUPPORTED otherwise).  The caller sets plan->groups and n_groups.
 int plan_attention_prefix(const kv_pool* pool, int batch, int max_context, int partition_tokens,
                           AttnPlan* plan);
-int launch_attention(const kv_pool* pool, int layer, const void* q, float* out,
-                     const int32_t* block_tables, int max_blocks, const int32_t* context_lens,
-                     int batch, int max_context, float scale, const AttnPlan& plan,
-                     void* workspace, cudaStream_t stream);
-// Same, with the fused append of each sequence's newest token (k_new/v_new [batch][H][D]).
+// k_new, v_new: the fused append of each sequence's newest token ([batch][H][D] of in_bytes each), or null.
 int launch_attention_append(const kv_pool* pool, int layer, const void* q, const void* k_new,
                             const void* v_new, int in_bytes, void* out, const int32_t* block_tables,
                             int max_blocks, const int32_t* context_lens, int batch, int max_context,
@@ -157,6 +153,11 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
 }
 
 int launch_selftest_wait(const kv_pool* pool, uint64_t limit_ns, cudaStream_t stream);
+
+// 16 bytes global -> shared, asynchronous, through L2; both addresses 16-byte aligned.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const char* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 
 // 1-D bulk copy global -> shared (the issuing CTA's own shared memory), completion
 // counted in bytes on the mbarrier.  dst, src 16-byte aligned, bytes a multiple of 16.
