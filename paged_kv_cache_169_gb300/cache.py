@@ -18,11 +18,17 @@ _KV_DTYPE = {"f32": abi.KV_F32, "f16": abi.KV_F16, "fp8": abi.KV_FP8_E4M3, "int4
 _IN_DTYPE = {torch.float32: abi.KV_F32, torch.float16: abi.KV_F16}
 
 
+# The current stream's handle without making a Stream object (3 us less per call); a torch without it
+# takes the public way.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if stream is not None:
         return int(stream.cuda_stream)
-    # the current stream's handle without making a Stream object (3 us less per call)
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if _raw_stream is None:
+        return int(torch.cuda.current_stream().cuda_stream)
+    return _raw_stream(torch.cuda.current_device())
 
 
 def _dev_ptr(t: torch.Tensor, what: str) -> int:
