@@ -36,8 +36,8 @@ namespace kvp {
 namespace {
 
 // Warps of a CTA, one CTA per SM: four for each scheduler.  (8 query heads hold two columns of state per
-// lane and fit 128 registers with 16 bytes spilled; 12 warps with 160: 157 us for 192 sequences where 16
-// take 151; 13 or 14 leave the schedulers uneven: 190, 172 us.)
+// lane and fit 128 registers with 20 bytes spilled, 8 with head size 64; 12 warps with 160: 178 us for 192
+// sequences of 64 / 8 heads where 16 take 174.)
 constexpr int kWarps = 16;
 // Query rows of the next item staged beside the stages, copied with its first chunk.  With 8 query heads
 // there is no room: the first item's rows use the LATER part's place before it is written, and the
@@ -45,7 +45,7 @@ constexpr int kWarps = 16;
 template <int G> constexpr bool kStageQ = G < 8;
 constexpr int kUnitCost = 2;                       // chunks that beginning and ending a unit costs a warp
 // Tokens per chunk, one softmax update: 4608 bytes of K and V whatever the head size.  (Head size 64
-// with 32-token chunks pays the loop's fixed part twice per byte: 0.73 of the copy peak.)
+// with 32-token chunks pays the loop's fixed part twice per byte: 0.74 of the copy peak where 64 give 0.81.)
 constexpr int chunk_tokens(int head_dim) { return head_dim == 64 ? 64 : 32; }
 template <int D> constexpr int kOcts = chunk_tokens(D) / 8;
 
@@ -397,8 +397,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attention_int4_kernel(const __
     // The first `rem` ranges have q + 1 chunks, the others q.
     const int grid = static_cast<int>(gridDim.x);
     const int want = max(total / args.min_range, 1);
-    // (a whole number of warps for each of the SM's four schedulers: 14 warps of 4 chunks took 16.9 us where
-    // 12 of 4.6 take 15.7)
+    // (a whole number of warps for each of the SM's four schedulers: 8 sequences of 64 / 8 heads take 18.1 us
+    // with 14 warps of 4 chunks, 16.7 with 12 of 4.6)
     const int k0 = min((want + grid - 1) / grid, NW), k = k0 > 4 ? k0 & ~3 : k0;
     const int ranges = min(want, k * grid);
     const int q = total / ranges, rem = total - q * ranges;
@@ -887,7 +887,9 @@ int plan_attention_int4(const kv_pool* pool, int batch, int max_context, int par
     const int64_t chunks = span > 0 ? (span + chunk - 1) / chunk : 1;
     // the kernel numbers a launch's chunks with an int
     if (units_of(pool, batch) * (chunks + kUnitCost) >= (int64_t{1} << 31)) return KV_ERR_INVALID_ARG;
-    constexpr int kMinTokens = 128;                     // below that a range costs more than it spreads
+    // below 128 tokens a range costs more than it spreads (8 sequences of 64 / 8 heads, one context of 131072: 64
+    // tokens 17.4, 18.6 us; 128: 16.7, 17.0; 256: 19.9, 17.4, and 7B-shaped 15.7 where 128 take 14.8)
+    constexpr int kMinTokens = 128;
     *plan = AttnPlan{};
     plan->partition = partition_tokens ? (partition_tokens + chunk - 1) / chunk : kMinTokens / chunk;
     plan->max_parts = static_cast<int>(chunks);
