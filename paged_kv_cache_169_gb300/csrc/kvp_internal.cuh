@@ -72,7 +72,7 @@ struct AttnPlan {
         return ((units * 4 + 255) & ~size_t(255)) + ((units * merge_groups(max_parts) * 4 + 255) & ~size_t(255));
     }
 };
-// group: query heads per KV head (1, or 2/4/8 for fp16 and FP8 pools)
+// group: query heads per KV head (1, or 2/4/8 for all but fp32 pools)
 bool valid_group(const kv_pool_desc& d, int group);
 // whether a tensor-core launch on this pool (prefix: with shared prompt prefixes) uses
 // head-pair stages
