@@ -135,7 +135,8 @@ def test_a_group_with_a_nan_is_the_same_bytes_from_every_call(in_dtype, d, B):
     caches[2].attention_ex(0, q, (t // B).to(torch.int32).reshape(n, 1), (t % B + 1).to(torch.int32), B, 0.1,
                            k_new=k, v_new=v)
     # at position 0 a key's pairs turn by nothing, but a NaN or an infinity times 0 makes its partner a NaN
-    turned = OR.rotate(k.cpu().numpy(), rope_table(1, d).cpu().numpy()[np.zeros(n, dtype=int)], d, False, np.float32)
+    with np.errstate(invalid="ignore"):
+        turned = OR.rotate(k.cpu().numpy(), rope_table(1, d).cpu().numpy()[np.zeros(n, dtype=int)], d, False, np.float32)
     for x, which in ((k, "k"), (v, "v")):
         for c, at in zip(caches, (slots, slots, alone)):
             codes, scales = O4.quantize(turned if which == "k" and c is caches[1] else x.float().cpu().numpy())
