@@ -72,7 +72,9 @@ enum {
     KV_DEVERR_CONTEXT = 4,     /* context_len < 0, > max_blocks*block_size or > max_context */
     KV_DEVERR_TIMEOUT = 8,     /* a bounded mbarrier wait ran out (about one second)    */
     KV_DEVERR_PREFIX = 16,     /* a prefix group broke its rules (attended without sharing) */
-    KV_DEVERR_POSITION = 32    /* kv_append_rope: a position outside the table               */
+    KV_DEVERR_POSITION = 32,   /* kv_append_rope: a position outside the table               */
+    KV_DEVERR_QUERY = 64       /* paged_query_attention: a sequence's rows outside [0, num_tokens),
+                                  out of order or more than max_queries (it is left out)     */
 };
 
 typedef struct {
@@ -228,6 +230,26 @@ typedef struct {
     kv_stream_t stream;
 } kv_rope_args;
 KV_API int kv_append_rope(kv_pool* pool, const kv_rope_args* args);
+
+/* kv_append_rope for positions with several axes (time, height and width of images and video):
+ * pair i of a head turns by its own axis' position, by the table's row of that position.
+ *   args->positions  device int32 rows, one per axis: axis a's position of token i is
+ *                    positions[a*axis_stride + i].  Every axis' position of a token must be in
+ *                    0 .. table_len-1, else KV_DEVERR_POSITION and the token is skipped.
+ *   num_axes         1 .. KV_MAX_ROPE_AXES.
+ *   axis_stride      elements between two axes' rows, at least num_tokens, below 2^31.
+ *   pair_axis        the axis of each of the rot_dim/2 pairs, each below num_axes: sections one
+ *                    after the other, interleaved, or any other layout.  (Frequencies are the
+ *                    table's columns, so an axis that counts its own frequencies from the start
+ *                    has them in its pairs' columns.)
+ * Everything else as kv_append_rope; with one axis the same bits. */
+#define KV_MAX_ROPE_AXES 4
+typedef struct {
+    int num_axes;
+    int64_t axis_stride;
+    uint8_t pair_axis[64];
+} kv_rope_axes;
+KV_API int kv_append_rope_axes(kv_pool* pool, const kv_rope_args* args, const kv_rope_axes* axes);
 
 /* Fill a rotation table for kv_append_rope: table (device float32 [num_positions][rot_dim],
  * 16-byte aligned) row p holds cos and sin of p * position_scale * base^(-2i/rot_dim),
@@ -500,6 +522,89 @@ KV_API size_t paged_decode_workspace_size_ex(const kv_pool* pool, const kv_decod
 
 /* Decode attention with every option of kv_decode_args; errors as paged_decode_attention. */
 KV_API int paged_decode_attention_ex(kv_pool* pool, const kv_decode_args* args);
+
+/* Attention of each sequence's newest tokens over its cached context: a prompt or a chunk of one,
+ * drafted tokens to check, or single tokens, in one ragged batch, with masks, capped scores and a
+ * distance bias.  The tokens' K and V are in the cache already (kv_append, kv_append_rope).
+ * Sequence s has n = query_start[s+1] - query_start[s] rows of q and c = context_lens[s] cached
+ * tokens, the new ones last: its row i stands at position p = c - n + i and sees the positions j
+ *     first <= j < end,   p - j < window (window > 0),   0 <= j < c,
+ * with (first, end) = (0, p + 1), or ranges[row].  With x = scale * q . k_j the score is
+ *     t = score_cap * tanh(x / score_cap)  (x itself with score_cap 0),   less slopes[h] * |p - j|,
+ * and out = sum_j softmax(t)_j v_j, 0 where nothing is seen.  What a row does not see never
+ * reaches it, NaN and infinities included.
+ *   layer          0 .. num_layers-1.
+ *   q              device [num_tokens] rows of num_q_heads*head_dim elements: float32 for F32
+ *                  pools, float16 for the others; 16-byte aligned.
+ *   num_q_heads    G * num_heads, G in {1, 2, 4, 8}; query head j reads KV head j / G.
+ *   out            device [num_tokens] rows of q's type, written, not accumulated; must not
+ *                  overlap q.  Rows of no sequence are left as they were.
+ *   q_stride, out_stride  elements between the rows of two tokens (heads are contiguous in a
+ *                  row): at least a row, below 2^28, a multiple of 16 bytes.
+ *   query_start    device int32 [batch + 1].
+ *   num_tokens     rows of q and out, 0 .. 2^24.
+ *   max_queries    host upper bound of a sequence's rows, 0 .. num_tokens.  A sequence with more, or
+ *                  whose rows lie outside [0, num_tokens) or end before they begin, sets
+ *                  KV_DEVERR_QUERY and is left out (no row of it is written).
+ *   block_tables, max_blocks_per_seq, context_lens, batch  as paged_decode_attention.  Lengths
+ *                  below 0 or above min(max_blocks_per_seq*block_size, max_context) are clamped
+ *                  and set KV_DEVERR_CONTEXT; so does c < n (rows before position 0 see nothing
+ *                  without ranges).  A block id outside the pool that some row's positions
+ *                  reach sets KV_DEVERR_BLOCK_ID and block 0 is read; entries of blocks that no
+ *                  row of the sequence sees are not read (they may be -1: kv_alloc_seq_trim).
+ *   max_context    host upper bound of context_lens, 0 .. 2^24.
+ *   window         0, or the last `window` positions only.
+ *   scale          finite and > 0.   score_cap  0 (none), or finite and > 0.
+ *   slopes         NULL, or device float32 [num_q_heads].
+ *   ranges         NULL, or device int32 [num_tokens][2], 8-byte aligned: the positions
+ *                  [first, end) a row sees, in place of the causal [0, p + 1): prefixes and images
+ *                  seen both ways, packed documents, padding rows (an empty range).  Any values:
+ *                  what lies outside the context is not seen.
+ *   workspace      device, >= paged_query_workspace_size(...) bytes, 256-byte aligned; contents
+ *                  need not be initialised; not shared between calls that may overlap.
+ *   flags          0, or a sum of KV_DECODE_WORKSPACE_ZEROED (the workspace was zero-filled once and
+ *                  used since only by calls of this entry point of one shape: pool, batch,
+ *                  num_tokens, num_q_heads, max_queries, max_context, window, with no device error
+ *                  in between) and KV_DECODE_PDL (may be scheduled while the previous kernel on the
+ *                  stream finishes; reads and writes nothing before that kernel has completed).
+ * Arithmetic: float32 scores, softmax and sums; products of float16 operands (q, K and V; FP8
+ * codes convert exactly and their scales are applied in float32; 4-bit values are exact); the
+ * softmax weights enter the V products as float16 (relative 2^-11; down to 2^-21 of a row's
+ * largest weight).  F32 pools: float32 throughout.  The result is rounded once.
+ * The pool's device must be the current device.  Asynchronous.
+ * The masked attention of a prompt that fills the cache, and the steps after it:
+ * [KV Cache篇] §3.1 (scores over cache[:, :start_pos+seqlen] plus mask), over the block-table
+ * gather of [PagedAttention] §3.2. */
+typedef struct {
+    int layer;
+    const void* q;
+    int num_q_heads;
+    int64_t q_stride;
+    void* out;
+    int64_t out_stride;
+    const int32_t* query_start;
+    int num_tokens;
+    int max_queries;
+    const int32_t* block_tables;
+    int max_blocks_per_seq;
+    const int32_t* context_lens;
+    int batch;
+    int max_context;
+    int window;
+    float scale;
+    float score_cap;
+    const float* slopes;
+    const int32_t* ranges;
+    void* workspace;
+    size_t workspace_bytes;
+    unsigned flags;
+    kv_stream_t stream;
+} kv_query_args;
+
+/* Workspace bytes for paged_query_attention: reads batch, num_tokens, num_q_heads, max_queries,
+ * max_context and window (0 on invalid ones). */
+KV_API size_t paged_query_workspace_size(const kv_pool* pool, const kv_query_args* args);
+KV_API int paged_query_attention(kv_pool* pool, const kv_query_args* args);
 
 /* One decode step of a batch, driven from the host in one call: the write-then-read step of
  * [PagedAttention] §3.3 (allocate or copy-on-write, write the new token, attend) for every

@@ -17,6 +17,7 @@ pages it follows:
 * ``fp8``        OCP FP8-E4M3 encoding/decoding from its bit-level definition.
 * ``int4``       4-bit cached values: scales, codes and the layout of a tile.
 * ``rope``       rotation of queries and keys by position.
+* ``query``      attention of a sequence's newest tokens with masks, capped scores and a distance bias.
 
 Sources (web pages, cited by title and section):
   [KV Cache篇]           "大模型推理加速——KV Cache篇"
@@ -32,4 +33,4 @@ rounding, and the allocator's closed forms from [PagedAttention] §2.2/§5.1.
 No oracle function is "parity unpinned".
 """
 
-from . import attention, cache, fp8, int4, rope  # noqa: F401
+from . import attention, cache, fp8, int4, query, rope  # noqa: F401

@@ -16,11 +16,12 @@ KV_OK, KV_ERR_INVALID_ARG, KV_ERR_NO_BLOCKS, KV_ERR_STATE = 0, -1, -2, -3
 KV_ERR_CUDA, KV_ERR_DEVICE, KV_ERR_UNSUPPORTED = -4, -5, -6
 KV_F32, KV_F16, KV_FP8_E4M3, KV_INT4 = 0, 1, 2, 3
 KV_DEVERR_SLOT, KV_DEVERR_BLOCK_ID, KV_DEVERR_CONTEXT, KV_DEVERR_TIMEOUT = 1, 2, 4, 8
-KV_DEVERR_PREFIX, KV_DEVERR_POSITION = 16, 32
+KV_DEVERR_PREFIX, KV_DEVERR_POSITION, KV_DEVERR_QUERY = 16, 32, 64
 KV_FEATURE_TENSOR_MAPS = 1
 KV_DECODE_WORKSPACE_ZEROED, KV_DECODE_PDL, KV_DECODE_EARLY_TABLES, KV_DECODE_OUT_F16 = 1, 2, 4, 8
 KV_DECODE_EARLY_POOL = 16
 KV_MAX_DECODE_BATCH = 65536
+KV_MAX_ROPE_AXES = 4
 
 
 class KvError(RuntimeError):
@@ -53,6 +54,20 @@ class kv_rope_args(C.Structure):
                 ("num_tokens", C.c_int), ("flags", C.c_uint), ("stream", C.c_void_p)]
 
 
+class kv_rope_axes(C.Structure):
+    _fields_ = [("num_axes", C.c_int), ("axis_stride", C.c_int64), ("pair_axis", C.c_uint8 * 64)]
+
+
+class kv_query_args(C.Structure):
+    _fields_ = [("layer", C.c_int), ("q", C.c_void_p), ("num_q_heads", C.c_int), ("q_stride", C.c_int64),
+                ("out", C.c_void_p), ("out_stride", C.c_int64), ("query_start", C.c_void_p),
+                ("num_tokens", C.c_int), ("max_queries", C.c_int), ("block_tables", C.c_void_p),
+                ("max_blocks_per_seq", C.c_int), ("context_lens", C.c_void_p), ("batch", C.c_int),
+                ("max_context", C.c_int), ("window", C.c_int), ("scale", C.c_float), ("score_cap", C.c_float),
+                ("slopes", C.c_void_p), ("ranges", C.c_void_p), ("workspace", C.c_void_p),
+                ("workspace_bytes", C.c_size_t), ("flags", C.c_uint), ("stream", C.c_void_p)]
+
+
 class kv_alloc_stats_t(C.Structure):
     _fields_ = [("num_blocks", C.c_int), ("free_blocks", C.c_int), ("shared_blocks", C.c_int),
                 ("num_seqs", C.c_int), ("used_slots", C.c_int64), ("wasted_slots", C.c_int64)]
@@ -71,6 +86,7 @@ _SIGS = {
     "kv_selftest_wait_timeout": (C.c_int, [_VP, C.c_uint64, _VP]),
     "kv_append": (C.c_int, [_VP, C.c_int, _VP, _VP, C.c_int, _VP, C.c_int, _VP]),
     "kv_append_rope": (C.c_int, [_VP, _VP]),
+    "kv_append_rope_axes": (C.c_int, [_VP, _VP, _VP]),
     "kv_rope_table": (C.c_int, [_VP, C.c_int, C.c_int, C.c_double, C.c_double, _VP]),
     "kv_gather": (C.c_int, [_VP, C.c_int, _VP, C.c_int, _VP, _VP, C.c_int, _VP]),
     "kv_copy_blocks": (C.c_int, [_VP, _VP, C.c_int, C.c_int, C.c_int, _VP]),
@@ -99,6 +115,8 @@ _SIGS = {
     "kv_alloc_seq_trim": (C.c_int, [_VP, C.c_int, C.c_int64, C.POINTER(C.c_int)]),
     "paged_decode_workspace_size_ex": (C.c_size_t, [_VP, _VP]),
     "paged_decode_attention_ex": (C.c_int, [_VP, _VP]),
+    "paged_query_workspace_size": (C.c_size_t, [_VP, _VP]),
+    "paged_query_attention": (C.c_int, [_VP, _VP]),
     "kv_decode_step": (C.c_int, [_VP, _VP, _I32P, C.c_int, C.c_int, _VP, _VP, _VP, _VP, C.c_size_t, _VP,
                                  C.c_size_t, _VP]),
     "kv_alloc_seq_info": (C.c_int, [_VP, C.c_int, C.POINTER(C.c_int), C.POINTER(C.c_int)]),
@@ -211,6 +229,10 @@ def kv_append_rope(pool: int, args: "kv_rope_args") -> None:
     _check("kv_append_rope", load().kv_append_rope(pool, C.byref(args)))
 
 
+def kv_append_rope_axes(pool: int, args: "kv_rope_args", axes: "kv_rope_axes") -> None:
+    _check("kv_append_rope_axes", load().kv_append_rope_axes(pool, C.byref(args), C.byref(axes)))
+
+
 def kv_rope_table(table: int, num_positions: int, rot_dim: int, base: float, position_scale: float = 1.0,
                   stream: int = 0) -> None:
     _check("kv_rope_table", load().kv_rope_table(table, num_positions, rot_dim, base, position_scale, stream))
@@ -293,6 +315,17 @@ def paged_decode_workspace_size_ex(pool: int, args: "kv_decode_args") -> int:
 
 def paged_decode_attention_ex(pool: int, args: "kv_decode_args") -> None:
     _check("paged_decode_attention_ex", load().paged_decode_attention_ex(pool, C.byref(args)))
+
+
+def paged_query_workspace_size(pool: int, args: "kv_query_args") -> int:
+    n = load().paged_query_workspace_size(pool, C.byref(args))
+    if n == 0:
+        raise KvError("paged_query_workspace_size", KV_ERR_INVALID_ARG)
+    return n
+
+
+def paged_query_attention(pool: int, args: "kv_query_args") -> None:
+    _check("paged_query_attention", load().paged_query_attention(pool, C.byref(args)))
 
 
 def kv_decode_step(alloc: int, pool: int, seqs, n: int, max_blocks: int, staging: int, dev_meta: int,

@@ -73,6 +73,18 @@ def rope_table(num_positions: int, rot_dim: int, base: float = 10000.0, position
     return t
 
 
+def rope_axes(pair_axis) -> abi.kv_rope_axes:
+    """The axis of each rotated pair (rot_dim / 2 of them, 0 .. 3) for PagedKVCache.append_rope_axes,
+    e.g. [0] * 16 + [1] * 24 + [2] * 24 for sections of time, height and width.  Made once per model."""
+    axes = [int(x) for x in pair_axis]
+    if not 0 < len(axes) <= 64 or min(axes) < 0 or max(axes) >= abi.KV_MAX_ROPE_AXES:
+        raise ValueError("pair_axis must be 1 to 64 axes, each 0 to 3")
+    a = abi.kv_rope_axes(max(axes) + 1, 0)
+    a.pair_axis[:len(axes)] = axes
+    a.pairs = len(axes)
+    return a
+
+
 class PagedKVCache:
     """A paged K/V pool for ``num_layers`` layers, laid out [num_blocks, H, B, d] per layer.
 
@@ -129,6 +141,19 @@ class PagedKVCache:
         [positions, rot_dim] (rope_table).  Pairs are elements (i, i + rot_dim/2), or (2i, 2i + 1)
         with ``adjacent_pairs``.  Returns q_out, the rotated queries [n, Hq, d] in the type the
         attention calls take (may be q itself)."""
+        return self._append_rope(layer, k, v, slot_mapping, positions, None, cos_sin, q, q_out, adjacent_pairs, flags,
+                                 stream)
+
+    def append_rope_axes(self, layer: int, k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor,
+                         positions: torch.Tensor, axes: abi.kv_rope_axes, cos_sin: torch.Tensor,
+                         q: torch.Tensor | None = None, q_out: torch.Tensor | None = None,
+                         adjacent_pairs: bool = False, flags: int = 0, stream=None) -> torch.Tensor | None:
+        """append_rope for positions with several axes (time, height, width): positions int32
+        [num_axes, n], axes from rope_axes; pair i turns by its own axis' position."""
+        return self._append_rope(layer, k, v, slot_mapping, positions, axes, cos_sin, q, q_out, adjacent_pairs, flags,
+                                 stream)
+
+    def _append_rope(self, layer, k, v, slot_mapping, positions, axes, cos_sin, q, q_out, adjacent_pairs, flags, stream):
         if slot_mapping.dtype != torch.int64 or positions.dtype != torch.int32:
             raise ValueError("slot_mapping must be int64 and positions int32")
         n, d, h = slot_mapping.numel(), self.head_dim, self.num_heads
@@ -137,8 +162,11 @@ class PagedKVCache:
             raise ValueError("k and v must be [num_tokens, H, d] of one dtype")
         if dt not in _IN_DTYPE:
             raise ValueError("k, v and q must be float16 or float32")
-        if positions.numel() != n:
-            raise ValueError("positions must have one entry per token")
+        if axes is None:
+            if positions.numel() != n:
+                raise ValueError("positions must have one entry per token")
+        elif positions.dim() != 2 or positions.shape[0] != axes.num_axes or positions.shape[1] != n:
+            raise ValueError("positions must be [axes, num_tokens]")
         if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
             raise ValueError("cos_sin must be float32 [positions, rot_dim]")
         dev = self.k[0].get_device()
@@ -158,11 +186,17 @@ class PagedKVCache:
             raise ValueError("q_out without q")
         (kp, ks), (vp, vs) = _rows(k, n, h, d, "k", dev), _rows(v, n, h, d, "v", dev)
         table_len, rot = cos_sin.shape
+        if axes is not None and axes.pairs != rot // 2:
+            raise ValueError("the axes must cover the rot_dim / 2 pairs of cos_sin")
         a = abi.kv_rope_args(layer, qp, hq, op, kp, vp, _IN_DTYPE[dt], qs, ks, vs, os,
                              _ptr_on(slot_mapping, "slot_mapping", dev), _ptr_on(positions, "positions", dev),
                              _ptr_on(cos_sin, "cos_sin", dev), table_len, rot, int(adjacent_pairs), n, flags,
                              _stream(stream))
-        abi.kv_append_rope(self.handle, a)
+        if axes is None:
+            abi.kv_append_rope(self.handle, a)
+        else:                                          # (a copy: the caller's may serve several calls at once)
+            x = abi.kv_rope_axes(axes.num_axes, max(n, 1), axes.pair_axis)
+            abi.kv_append_rope_axes(self.handle, a, x)
         return q_out
 
     def gather(self, layer: int, slot_mapping: torch.Tensor, out_dtype: torch.dtype = torch.float16,
@@ -352,6 +386,74 @@ class PagedKVCache:
         a.num_prefix_groups = 1 if prefix_groups else 0
         n = abi.paged_decode_workspace_size_ex(self.handle, a)
         return torch.zeros(n, dtype=torch.uint8, device=self.k[0].device)
+
+    def query_workspace(self, batch: int, num_q_heads: int, max_queries: int, max_context: int, window: int = 0,
+                        num_tokens: int | None = None) -> torch.Tensor:
+        """A new zero-filled workspace for query_attention, also with KV_DECODE_WORKSPACE_ZEROED for calls
+        of this one shape.  num_tokens: rows of q (default batch * max_queries)."""
+        a = abi.kv_query_args()
+        a.num_q_heads, a.batch, a.max_queries, a.max_context, a.window = num_q_heads, batch, max_queries, max_context, window
+        a.num_tokens = batch * max_queries if num_tokens is None else num_tokens
+        n = abi.paged_query_workspace_size(self.handle, a)
+        return torch.zeros(n, dtype=torch.uint8, device=self.k[0].device)
+
+    def query_attention(self, layer: int, q: torch.Tensor, query_start: torch.Tensor, block_tables: torch.Tensor,
+                        context_lens: torch.Tensor, max_queries: int, max_context: int, scale: float, window: int = 0,
+                        score_cap: float = 0.0, slopes: torch.Tensor | None = None,
+                        ranges: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                        workspace: torch.Tensor | None = None, flags: int = 0, stream=None) -> torch.Tensor:
+        """Attention of each sequence's newest tokens over its cached context (their K and V are appended
+        already): prompts, chunks of one, drafted tokens or single tokens in one ragged batch.
+
+        q: [n, Hq, d] in the type the attention calls take (possibly a view: heads of a token contiguous);
+        query_start: int32 [batch + 1], sequence s has rows query_start[s] .. query_start[s+1]-1;
+        block_tables: int32 [batch, max_blocks]; context_lens: int32 [batch], the new tokens included;
+        max_queries, max_context: host upper bounds.  A row sees the positions up to its own, or
+        [first, end) of ``ranges`` (int32 [n, 2]): prefixes seen both ways, packed documents, empty rows
+        (0); ``window``: at most that many positions back.  Scores are capped to score_cap * tanh(x /
+        score_cap) and lowered by slopes[head] (float32 [Hq]) times the distance.  Returns out [n, Hq, d]
+        of q's type; rows of no sequence are left as they were (a new tensor: zero).  flags:
+        abi.KV_DECODE_WORKSPACE_ZEROED (with a workspace from query_workspace), abi.KV_DECODE_PDL."""
+        dev, d = self.k[0].get_device(), self.head_dim
+        dt = torch.float32 if self.dtype == "f32" else torch.float16
+        if q.dim() != 3 or q.shape[2] != d or q.dtype != dt:
+            raise ValueError(f"q must be {dt} [num_tokens, Hq, {d}]")
+        n, hq = q.shape[0], q.shape[1]
+        if query_start.dtype != torch.int32 or block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+            raise ValueError("query_start, block_tables and context_lens must be int32")
+        batch = context_lens.numel()
+        if query_start.numel() != batch + 1 or block_tables.dim() != 2 or block_tables.shape[0] != batch:
+            raise ValueError("query_start must have batch + 1 entries and block_tables batch rows")
+        if out is None:
+            with _alloc_on(stream):
+                out = torch.zeros((n, hq, d), dtype=dt, device=q.device)
+        elif out.shape != q.shape or out.dtype != dt:
+            raise ValueError(f"out must be {dt} of q's shape")
+        a = abi.kv_query_args()
+        a.layer, a.num_q_heads = layer, hq
+        (a.q, a.q_stride), (a.out, a.out_stride) = _rows(q, n, hq, d, "q", dev), _rows(out, n, hq, d, "out", dev)
+        a.query_start, a.num_tokens, a.max_queries = _ptr_on(query_start, "query_start", dev), n, max_queries
+        a.block_tables, a.max_blocks_per_seq = _ptr_on(block_tables, "block_tables", dev), block_tables.shape[1]
+        a.context_lens, a.batch, a.max_context = _ptr_on(context_lens, "context_lens", dev), batch, max_context
+        a.window, a.scale, a.score_cap = window, float(scale), float(score_cap)
+        if slopes is not None:
+            if slopes.dtype != torch.float32 or slopes.numel() != hq:
+                raise ValueError("slopes must be float32 [Hq]")
+            a.slopes = _ptr_on(slopes, "slopes", dev)
+        if ranges is not None:
+            if ranges.dtype != torch.int32 or ranges.shape != (n, 2):
+                raise ValueError("ranges must be int32 [num_tokens, 2]")
+            a.ranges = _ptr_on(ranges, "ranges", dev)
+        if workspace is None:
+            if flags & abi.KV_DECODE_WORKSPACE_ZEROED:
+                raise ValueError("KV_DECODE_WORKSPACE_ZEROED needs a workspace of the caller's")
+            need = abi.paged_query_workspace_size(self.handle, a)
+            with _alloc_on(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        a.workspace, a.workspace_bytes = _ptr_on(workspace, "workspace", dev), workspace.numel() * workspace.element_size()
+        a.flags, a.stream = flags, _stream(stream)
+        abi.paged_query_attention(self.handle, a)
+        return out
 
     def device_error(self, clear: bool = True, stream=None) -> int:
         return abi.kv_get_device_error(self.handle, _stream(stream), clear)

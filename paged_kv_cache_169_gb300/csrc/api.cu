@@ -230,7 +230,7 @@ int kv_append(kv_pool* pool, int layer, const void* k, const void* v, kv_dtype i
     return kvp::launch_append(pool, layer, k, v, in_dtype, slot_mapping, num_tokens, stream);
 }
 
-int kv_append_rope(kv_pool* pool, const kv_rope_args* x) {
+static int append_rope(kv_pool* pool, const kv_rope_args* x, const kv_rope_axes* axes) {
     if (!pool || !x || x->layer < 0 || x->layer >= pool->desc.num_layers || x->num_tokens < 0)
         return KV_ERR_INVALID_ARG;
     const kv_pool_desc& d = pool->desc;
@@ -239,6 +239,13 @@ int kv_append_rope(kv_pool* pool, const kv_rope_args* x) {
         (x->adjacent_pairs != 0 && x->adjacent_pairs != 1))
         return KV_ERR_INVALID_ARG;
     if (!kvp::valid_input(d.dtype, x->in_dtype)) return KV_ERR_INVALID_ARG;
+    if (axes) {
+        if (axes->num_axes < 1 || axes->num_axes > KV_MAX_ROPE_AXES || axes->axis_stride < x->num_tokens ||
+            axes->axis_stride >= (int64_t{1} << 31))
+            return KV_ERR_INVALID_ARG;
+        for (int i = 0; i < x->rot_dim / 2; ++i)
+            if (axes->pair_axis[i] >= axes->num_axes) return KV_ERR_INVALID_ARG;
+    }
     if (x->num_tokens == 0) return KV_OK;
     if (!x->k || !x->v || !x->slot_mapping || !x->positions || !x->cos_sin || !kvp::aligned16(x->k) ||
         !kvp::aligned16(x->v) || !kvp::aligned16(x->cos_sin))
@@ -257,7 +264,13 @@ int kv_append_rope(kv_pool* pool, const kv_rope_args* x) {
         if (x->q == x->q_out && (es != qs || x->q_stride != x->q_out_stride)) return KV_ERR_INVALID_ARG;
     }
     if (!on_pool_device(pool)) return KV_ERR_INVALID_ARG;
-    return kvp::launch_append_rope(pool, *x);
+    return kvp::launch_append_rope(pool, *x, axes);
+}
+
+int kv_append_rope(kv_pool* pool, const kv_rope_args* x) { return append_rope(pool, x, nullptr); }
+
+int kv_append_rope_axes(kv_pool* pool, const kv_rope_args* x, const kv_rope_axes* axes) {
+    return axes ? append_rope(pool, x, axes) : KV_ERR_INVALID_ARG;
 }
 
 int kv_rope_table(float* table, int num_positions, int rot_dim, double base, double position_scale,
@@ -447,6 +460,35 @@ int paged_decode_attention_ex(kv_pool* pool, const kv_decode_args* x) {
                                         x->k_new ? kvp::elem_bytes(x->in_dtype) : 0, x->out, x->block_tables,
                                         x->max_blocks_per_seq, x->context_lens, x->batch, x->max_context,
                                         x->scale, plan, x->workspace, x->stream);
+}
+
+size_t paged_query_workspace_size(const kv_pool* pool, const kv_query_args* x) {
+    kvp::QueryPlan plan;
+    if (!pool || !x || kvp::plan_query(pool, *x, &plan) != KV_OK) return 0;
+    return plan.ws_bytes;
+}
+
+int paged_query_attention(kv_pool* pool, const kv_query_args* x) {
+    if (!pool || !x || x->layer < 0 || x->layer >= pool->desc.num_layers) return KV_ERR_INVALID_ARG;
+    kvp::QueryPlan plan;
+    const int rc = kvp::plan_query(pool, *x, &plan);
+    if (rc != KV_OK) return rc;
+    if (!(x->scale > 0.f) || !(x->scale < 3.0e38f) || !(x->score_cap >= 0.f) || !(x->score_cap < 3.0e38f) ||
+        (x->flags & ~(KV_DECODE_WORKSPACE_ZEROED | KV_DECODE_PDL)))
+        return KV_ERR_INVALID_ARG;
+    if (x->batch == 0 || x->max_queries == 0) return KV_OK;
+    if (!x->q || !x->out || !x->query_start || !x->block_tables || !x->context_lens || !x->workspace ||
+        x->max_blocks_per_seq < 1)
+        return KV_ERR_INVALID_ARG;
+    if (!kvp::aligned16(x->q) || !kvp::aligned16(x->out) || (reinterpret_cast<uintptr_t>(x->workspace) & 255u) != 0 ||
+        (reinterpret_cast<uintptr_t>(x->ranges) & 7u) != 0 || (reinterpret_cast<uintptr_t>(x->slopes) & 3u) != 0)
+        return KV_ERR_INVALID_ARG;
+    const int es = pool->desc.dtype == KV_F32 ? 4 : 2;
+    const int64_t row = static_cast<int64_t>(x->num_q_heads) * pool->desc.head_dim;
+    if (!valid_stride(x->q_stride, row, es) || !valid_stride(x->out_stride, row, es)) return KV_ERR_INVALID_ARG;
+    if (x->workspace_bytes < plan.ws_bytes) return KV_ERR_INVALID_ARG;
+    if (!on_pool_device(pool)) return KV_ERR_INVALID_ARG;
+    return kvp::launch_query(pool, *x, plan);
 }
 
 int kv_decode_step(kv_alloc* alloc, kv_pool* pool, const int32_t* seqs, int n, int max_blocks,

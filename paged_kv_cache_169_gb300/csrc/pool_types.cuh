@@ -47,10 +47,18 @@ inline int launch_decode(const kv_pool* pool, int layer, const void* q, const vo
         scale, plan, workspace, stream);
 }
 
+// paged_query_attention (query_attention.cu)
+struct QueryPlan {
+    size_t ws_bytes;     // workspace bytes
+};
+int plan_query(const kv_pool* pool, const kv_query_args& args, QueryPlan* plan);
+int launch_query(const kv_pool* pool, const kv_query_args& args, const QueryPlan& plan);
+
 // kv_append into a 4-bit pool, kv_append_rope, kv_gather, kv_rope_table (append_rope.cu)
 int launch_append_int4(const kv_pool* pool, int layer, const void* k, const void* v, kv_dtype in_dtype,
                        const int64_t* slot_mapping, int num_tokens, cudaStream_t stream);
-int launch_append_rope(const kv_pool* pool, const kv_rope_args& args);
+// axes: several position axes (kv_append_rope_axes), or null
+int launch_append_rope(const kv_pool* pool, const kv_rope_args& args, const kv_rope_axes* axes);
 int launch_gather(const kv_pool* pool, int layer, const int64_t* slot_mapping, int num_tokens, void* k_out,
                   void* v_out, kv_dtype out_dtype, cudaStream_t stream);
 int launch_rope_table(float* table, int num_positions, int rot_dim, double base, double position_scale,
