@@ -27,6 +27,7 @@ bool valid_desc(const kv_pool_desc* d) {
 void free_pool(kv_pool* p) {
     if (!p) return;
     std::free(p->tmaps_raw);
+    std::free(p->rmaps_raw);
     std::free(p->k_layers);
     std::free(p->v_layers);
     std::free(p->k_scales);
@@ -44,6 +45,45 @@ bool valid_stride(int64_t stride, int64_t row, int elem_bytes) {
     return stride >= row && stride < (int64_t{1} << 28) && stride * elem_bytes % 16 == 0;
 }
 
+using TensorMapEncode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                     const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                     CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's tensor-map encoder, or null.
+TensorMapEncode tensor_map_encoder() {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess || !fn) {
+        cudaGetLastError();
+        return nullptr;
+    }
+    return reinterpret_cast<TensorMapEncode>(fn);
+}
+
+// Row maps of an fp16 pool (kv_pool::rmaps); left null where the encoder is missing or refuses.
+void make_row_maps(kv_pool* p) {
+    const kv_pool_desc& d = p->desc;
+    const TensorMapEncode encode = d.dtype == KV_F16 ? tensor_map_encoder() : nullptr;
+    if (!encode) return;
+    void* raw = std::malloc(2 * d.num_layers * sizeof(CUtensorMap) + 64);
+    if (!raw) return;
+    CUtensorMap* maps = reinterpret_cast<CUtensorMap*>((reinterpret_cast<uintptr_t>(raw) + 63) & ~uintptr_t(63));
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(d.head_dim),
+                                static_cast<cuuint64_t>(d.num_blocks) * d.num_heads * d.block_size};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(d.head_dim) * 2};
+    const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(d.block_size)}, estr[2] = {1, 1};
+    for (int i = 0; i < 2 * d.num_layers; ++i)
+        if (encode(&maps[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, (i & 1 ? p->v_layers : p->k_layers)[i / 2], dims, strides,
+                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS) {
+            std::free(raw);
+            return;
+        }
+    p->rmaps = maps;
+    p->rmaps_raw = raw;
+}
+
 // Tensor maps of an fp16 or FP8, head_dim 128 pool for the grouped-query tensor-core path.
 // fp16: each layer's K and V viewed as [rows][2][64] fp16 (rows = num_blocks*H*B, a row
 // being one token of one head), box {64, 2, min(B, 16)}, 128-byte swizzle.  FP8: K and V
@@ -54,17 +94,8 @@ void make_tensor_maps(kv_pool* p) {
     const kv_pool_desc& d = p->desc;
     const bool fp8 = d.dtype == KV_FP8_E4M3;
     if (d.head_dim != 128 || (d.dtype != KV_F16 && !fp8)) return;
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess || !fn) {
-        cudaGetLastError();
-        return;
-    }
-    using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-    Encode encode = reinterpret_cast<Encode>(fn);
+    const TensorMapEncode encode = tensor_map_encoder();
+    if (!encode) return;
     const int L = d.num_layers;
     void* raw = std::malloc(4 * L * sizeof(CUtensorMap) + 64);
     if (!raw) return;
@@ -178,6 +209,7 @@ int kv_pool_create(const kv_pool_desc* desc, void* const* k_layers, void* const*
         return KV_ERR_CUDA;
     }
     make_tensor_maps(p);
+    make_row_maps(p);
     *out = p;
     return KV_OK;
 }

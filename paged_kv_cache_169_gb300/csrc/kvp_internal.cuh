@@ -25,6 +25,10 @@ struct kv_pool {
     // head-pair stages: fp16 pools with B <= 16 and FP8 pools; nullptr otherwise
     CUtensorMap* pmaps;  // [2 * num_layers]
     void* tmaps_raw;
+    // fp16 pools: per layer K and V viewed as [num_blocks*H*B][head_dim] with boxes of 64 elements
+    // by a block's B rows of one head, 128-byte swizzle (paged_query_attention)
+    CUtensorMap* rmaps;  // [2 * num_layers], 64-byte aligned
+    void* rmaps_raw;
 };
 
 namespace kvp {

@@ -49,6 +49,7 @@ inline int launch_decode(const kv_pool* pool, int layer, const void* q, const vo
 
 // paged_query_attention (query_attention.cu)
 struct QueryPlan {
+    bool prompt;         // the tensor-core kernel
     size_t ws_bytes;     // workspace bytes
 };
 int plan_query(const kv_pool* pool, const kv_query_args& args, QueryPlan* plan);

@@ -66,12 +66,15 @@ int plan_query(const kv_pool* pool, const kv_query_args& x, QueryPlan* plan) {
         return KV_ERR_INVALID_ARG;
     const int g = x.num_q_heads / d.num_heads;
     if (g != 1 && g != 2 && g != 4 && g != 8) return KV_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(x.batch) * d.num_heads * prompt_tiles(x.max_queries, g) > (int64_t{1} << 30))
+        return KV_ERR_INVALID_ARG;
+    // the tensor-core kernel for float16 pools and more rows of a K/V head than one matrix product takes
+    plan->prompt = d.dtype == KV_F16 && static_cast<int64_t>(x.max_queries) * g > 16;
     plan->ws_bytes = 256;
     return KV_OK;
 }
 
 int launch_query(const kv_pool* pool, const kv_query_args& x, const QueryPlan& plan) {
-    (void)plan;
     const kv_pool_desc& d = pool->desc;
     const int es = d.dtype == KV_F32 ? 4 : 2;
     QueryArgs a{};
@@ -103,7 +106,10 @@ int launch_query(const kv_pool* pool, const kv_query_args& x, const QueryPlan& p
     a.scale = x.scale;
     a.cap = x.score_cap;
     a.err = pool->d_err;
-    return launch_query_rows(pool, a, (x.flags & KV_DECODE_PDL) != 0, static_cast<cudaStream_t>(x.stream));
+    const bool pdl = (x.flags & KV_DECODE_PDL) != 0;
+    const cudaStream_t stream = static_cast<cudaStream_t>(x.stream);
+    if (plan.prompt) return launch_query_prompt_f16(pool, x.layer, a, pdl, stream);
+    return launch_query_rows(pool, a, pdl, stream);
 }
 
 }  // namespace kvp

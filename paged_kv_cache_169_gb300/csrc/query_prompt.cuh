@@ -1,0 +1,464 @@
+// paged_query_attention for many rows: the tensor-core kernel.
+#pragma once
+
+#include "query_attention.cuh"
+#include "tcgen05.cuh"
+
+namespace kvp {
+
+struct PromptArgs {
+    CUtensorMap kmap, vmap;            // float16 pools: the layer as [rows][D], boxes of 64 elements by a block
+    QueryArgs a;
+    int tiles;                         // row tiles per (sequence, K/V head)
+};
+
+namespace {
+
+constexpr int kTile = 128;             // rows of a row tile and keys of a key tile
+constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kLoadWarp = 9;
+
+template <int D_, kv_dtype POOL_>
+struct PromptCfg {
+    static constexpr int D = D_;
+    static constexpr kv_dtype POOL = POOL_;
+    static constexpr int HALVES = D / 64;                      // 64-element (128-byte) columns of a tile
+    static constexpr int TILE = HALVES * kTile * 128;          // bytes of 128 rows as float16
+    static constexpr int SLOTS = D == 128 ? 5 : 8;             // key and value tiles in flight
+    static constexpr int WARPS = 10;
+    static constexpr int Q_OFF = 0, KV_OFF = 2 * TILE;
+    static constexpr int BAR_OFF = KV_OFF + SLOTS * TILE;
+    // full, empty per slot; per row tile: queries there, scores there, weights there, product there; edge; done
+    static constexpr int BARS = 2 * SLOTS + 4 * 2 + 2;
+    static constexpr int MISC_OFF = BAR_OFF + BARS * 8;
+    static constexpr int SMEM = MISC_OFF + 64 + 1024;          // and up to 1024 bytes of alignment
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+// A bounded wait by a whole warp: all of its lanes go on, or none.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* err) {
+    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, err));
+}
+
+// What the CTA's roles share: visible range, its first position, key tiles per row tile.
+struct PromptMisc {
+    uint32_t tmem;
+    int lo[2], hi[2];
+};
+
+// Key tiles [a, b) of each row tile, numbered from position `base`.
+struct KeyTiles {
+    int base, end, a[2], b[2], n;
+    __device__ __forceinline__ bool on(int t, int j) const { return j >= a[t] && j < b[t]; }
+    __device__ __forceinline__ int next(int j) const {         // the first tile from j on that a row tile needs
+        while (j < n && !on(0, j) && !on(1, j)) ++j;
+        return j;
+    }
+};
+__device__ __forceinline__ KeyTiles key_tiles(const PromptMisc* m, int block) {
+    KeyTiles k;
+    k.base = min(m->lo[0], m->lo[1]) & -block;
+    k.end = max(m->hi[0], m->hi[1]);
+    #pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const bool some = m->lo[t] < m->hi[t];
+        k.a[t] = some ? (m->lo[t] - k.base) / kTile : 0;
+        k.b[t] = some ? (m->hi[t] - k.base + kTile - 1) / kTile : 0;
+    }
+    k.n = max(k.b[0], k.b[1]);
+    return k;
+}
+
+// t = cap tanh(x) in log2 units for x = s kx: 1 - 2 / (e^2x + 1), exact to a few 2^-24 of the cap
+__device__ __forceinline__ float capped(float s, float k2, float capl) {
+    const float e = ex2_approx(s * k2);
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e + 1.f));
+    return fmaf(-2.f * capl, r, capl);
+}
+
+// Weights are kept 2^7 above their softmax value relative to the base, which may lag the maximum by up to 2^8:
+// at most 2^15 in float16, and normal ones down to 2^-21 of the largest.
+constexpr float kRaise = 8.f, kLift = 7.f;
+
+template <int D, kv_dtype POOL>
+__global__ void __launch_bounds__(PromptCfg<D, POOL>::WARPS * 32, 1)
+query_prompt_kernel(const __grid_constant__ PromptArgs p) {
+    using C = PromptCfg<D, POOL>;
+    extern __shared__ char smem_raw[];
+    char* const smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t{1023});
+    const uint32_t base32 = smem_u32(smem);
+    PromptMisc* const misc = reinterpret_cast<PromptMisc*>(smem + C::MISC_OFF);
+    const QueryArgs& a = p.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    auto bar = [&](int i) { return base32 + C::BAR_OFF + 8 * i; };
+    auto full = [&](int slot) { return bar(slot); };
+    auto empty = [&](int slot) { return bar(C::SLOTS + slot); };
+    auto q_there = [&](int t) { return bar(2 * C::SLOTS + t); };
+    auto s_there = [&](int t) { return bar(2 * C::SLOTS + 2 + t); };
+    auto w_there = [&](int t) { return bar(2 * C::SLOTS + 4 + t); };
+    auto o_there = [&](int t) { return bar(2 * C::SLOTS + 6 + t); };
+    const uint32_t edge = bar(2 * C::SLOTS + 8), done = bar(2 * C::SLOTS + 9);
+
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    // the work item: later row tiles, which see more keys, first
+    const int item = blockIdx.x;
+    const int tile = p.tiles - 1 - item % p.tiles, head = item / p.tiles % a.H, s = item / p.tiles / a.H;
+    const QuerySeq seq = query_seq(a, s, threadIdx.x == 0 && tile == 0 && head == 0);
+    const int per_tile = kTile / a.G;                          // tokens of a row tile
+    if (tile * 2 * per_tile >= seq.n) return;
+
+    // ---- set-up: barriers, tensor memory, what the rows see
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::SLOTS; ++i) {
+            mbar_init(full(i), 1);
+            mbar_init(empty(i), 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(q_there(t), 4);
+            mbar_init(s_there(t), 1);
+            mbar_init(w_there(t), 4);
+            mbar_init(o_there(t), 1);
+        }
+        mbar_init(edge, 1);
+        mbar_init(done, 1);
+        fence_mbar_init();
+    }
+    if (threadIdx.x < 2) {
+        misc->lo[threadIdx.x] = 1 << 30;
+        misc->hi[threadIdx.x] = 0;
+    }
+    if (warp == kMmaWarp) tmem_alloc(smem_u32(&misc->tmem));
+    __syncthreads();
+    const int rt = warp >> 2;                                  // softmax warps: the row tile
+    const int row = (warp & 3) * 32 + lane;                    // and the thread's row of it
+    const int token = (tile * 2 + rt) * per_tile + row / a.G;
+    int2 sees = make_int2(0, 0);
+    if (warp < kSoftmaxWarps) {
+        if (token < seq.n) sees = row_range(a, seq, token);
+        const bool some = sees.x < sees.y;
+        const int lo = __reduce_min_sync(0xffffffffu, some ? sees.x : 1 << 30);
+        const int hi = __reduce_max_sync(0xffffffffu, some ? sees.y : 0);
+        if (lane == 0 && lo < hi) {
+            atomicMin(&misc->lo[rt], lo);
+            atomicMax(&misc->hi[rt], hi);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = misc->tmem;
+    const KeyTiles keys = key_tiles(misc, a.B);
+    const int first_tile = keys.next(0);
+
+    if (warp < kSoftmaxWarps) {
+        // ======== queries in, softmax, result out: a thread per row
+        constexpr int CHUNKS = D / 8;                          // 16-byte pieces of a row
+        char* const qt = smem + C::Q_OFF + rt * C::TILE;
+        const int64_t q0 = static_cast<int64_t>(seq.first) * a.q_stride + static_cast<int64_t>(head) * a.G * D * 2;
+        #pragma unroll 4
+        for (int it = 0; it < CHUNKS; ++it) {                  // the warp's 32 rows, neighbouring pieces side by side
+            const int u = it * 32 + lane, r = (warp & 3) * 32 + u / CHUNKS, c = u % CHUNKS;
+            const int tok = (tile * 2 + rt) * per_tile + r / a.G;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (tok < seq.n)
+                v = *reinterpret_cast<const uint4*>(a.q + q0 + tok * a.q_stride + (r % a.G) * (D * 2) + c * 16);
+            *reinterpret_cast<uint4*>(qt + (c >> 3) * (kTile * 128) + r * 128 + ((c & 7) ^ (r & 7)) * 16) = v;
+        }
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_there(rt));
+
+        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;       // the warp's 32 lanes
+        const uint32_t st = tmem + lanes + rt * kTile, ot = tmem + lanes + 2 * kTile + rt * D;
+        const int hq = head * a.G + row % a.G;
+        const bool bias = a.slopes != nullptr, cap = a.cap > 0.f;
+        const float slope = bias ? a.slopes[hq] * kLog2e : 0.f;
+        const float qscale = a.scale * kLog2e;
+        const float k2 = cap ? 2.f * kLog2e * (a.scale / a.cap) : 0.f, capl = a.cap * kLog2e;
+        const float c = cap || bias ? 1.f : qscale;            // scores to log2 units
+        const int pos = seq.ctx - seq.n + token;
+        float m = -CUDART_INF_F, l = 0.f;
+        int i = 0;                                             // this row tile's key tiles so far
+        bool fine = true;
+        #pragma unroll 1
+        for (int j = keys.a[rt]; j < keys.b[rt]; ++j, ++i) {
+            if (!warp_wait(s_there(rt), i & 1, a.err)) {
+                fine = false;
+                break;
+            }
+            tc_fence_after();
+            float x[kTile];
+            uint32_t* const xr = reinterpret_cast<uint32_t*>(x);
+            #pragma unroll
+            for (int k = 0; k < 4; ++k) tmem_load32(st + 32 * k, xr + 32 * k);
+            #pragma unroll
+            for (int k = 0; k < 4; ++k) tmem_wait_load32(xr + 32 * k);
+            const int j0 = keys.base + j * kTile;
+            if (cap) {
+                #pragma unroll
+                for (int k = 0; k < kTile; ++k) x[k] = capped(x[k], k2, capl);
+            }
+            if (bias) {
+                const float from = static_cast<float>(pos - j0), mul = cap ? 1.f : qscale;
+                #pragma unroll
+                for (int k = 0; k < kTile; ++k) x[k] = fmaf(-slope, fabsf(from - static_cast<float>(k)), x[k] * mul);
+            }
+            if (__any_sync(0xffffffffu, sees.x > j0 || sees.y < j0 + kTile)) {
+                const int from = sees.x - j0;
+                const unsigned len = sees.y - sees.x;
+                #pragma unroll
+                for (int k = 0; k < kTile; ++k)
+                    if (static_cast<unsigned>(k - from) >= len) x[k] = -CUDART_INF_F;
+            }
+            float top = fmaxf(x[0], x[1]);
+            #pragma unroll
+            for (int k = 2; k < kTile; k += 2) top = fmaxf(fmaxf(x[k], x[k + 1]), top);
+            // the base follows the maximum only when it is left behind by more than 2^8
+            const bool raise = (top - m) * c > kRaise;         // (m -inf: yes, but for a row that sees nothing yet)
+            float keep = 1.f;
+            if (raise) {
+                keep = m == -CUDART_INF_F ? 0.f : ex2_approx((m - top) * c);
+                m = top;
+                l *= keep;
+            }
+            if (i > 0 && __any_sync(0xffffffffu, raise)) {
+                if (!warp_wait(o_there(rt), (i - 1) & 1, a.err)) {
+                    fine = false;
+                    break;
+                }
+                tc_fence_after();
+                #pragma unroll 1
+                for (int k = 0; k < D; k += 32) {
+                    uint32_t o[32];
+                    tmem_load32(ot + k, o);
+                    tmem_wait_load32(o);
+                    #pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+                    tmem_store32(ot + k, o);
+                }
+            }
+            const float off = kLift - (m == -CUDART_INF_F ? 0.f : m * c);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            const float2 c2 = make_float2(c, c), off2 = make_float2(off, off);
+            #pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t w[32];
+                #pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    float2 y = __ffma2_rn(make_float2(x[64 * h + 2 * k], x[64 * h + 2 * k + 1]), c2, off2);
+                    y.x = ex2_approx(y.x);
+                    y.y = ex2_approx(y.y);
+                    sum[k & 1] = __fadd2_rn(sum[k & 1], y);
+                    const __half2 hv = __floats2half2_rn(y.x, y.y);
+                    w[k] = *reinterpret_cast<const uint32_t*>(&hv);
+                }
+                tmem_store32(st + 32 * h, w);
+            }
+            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            tmem_wait_store();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(w_there(rt));
+        }
+        // ---- the result: through the queries' place in shared memory, a warp its own 32 rows
+        if (fine && i > 0 && !warp_wait(o_there(rt), (i - 1) & 1, a.err)) fine = false;
+        if (fine && i > 0) tc_fence_after();
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        bool odd = false;                                      // something is not finite: from the definition below
+        #pragma unroll 1
+        for (int k = 0; k < D; k += 32) {
+            uint32_t o[32];
+            if (fine && i > 0) {
+                tmem_load32(ot + k, o);
+                tmem_wait_load32(o);
+            }
+            #pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+                uint32_t w[4];
+                #pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    float2 f = make_float2(0.f, 0.f);
+                    if (fine && i > 0 && l != 0.f)
+                        f = make_float2(__uint_as_float(o[e + 2 * y]) * inv, __uint_as_float(o[e + 2 * y + 1]) * inv);
+                    odd |= !(fabsf(f.x) < CUDART_INF_F) || !(fabsf(f.y) < CUDART_INF_F);
+                    const __half2 hv = __floats2half2_rn(f.x, f.y);
+                    w[y] = *reinterpret_cast<const uint32_t*>(&hv);
+                }
+                const int ch = (k + e) >> 3;
+                *reinterpret_cast<uint4*>(qt + (ch >> 3) * (kTile * 128) + row * 128 + ((ch & 7) ^ (row & 7)) * 16) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+        __syncwarp();
+        if (fine) {
+            const int64_t o0 = static_cast<int64_t>(seq.first) * a.out_stride + static_cast<int64_t>(head) * a.G * D * 2;
+            #pragma unroll 4
+            for (int it = 0; it < CHUNKS; ++it) {
+                const int u = it * 32 + lane, r = (warp & 3) * 32 + u / CHUNKS, ch = u % CHUNKS;
+                const int tok = (tile * 2 + rt) * per_tile + r / a.G;
+                if (tok >= seq.n) continue;
+                *reinterpret_cast<uint4*>(a.out + o0 + tok * a.out_stride + (r % a.G) * (D * 2) + ch * 16) =
+                    *reinterpret_cast<const uint4*>(qt + (ch >> 3) * (kTile * 128) + r * 128 + ((ch & 7) ^ (r & 7)) * 16);
+            }
+            // A key or value that is not finite reaches, as 0 * NaN, rows that do not see it: a row that came out
+            // so is worked out again from the definition, which reads only what it sees.
+            unsigned again = __ballot_sync(0xffffffffu, odd && token < seq.n);
+            __syncwarp();
+            #pragma unroll 1
+            while (again) {
+                const int r = (warp & 3) * 32 + __ffs(again) - 1;
+                again &= again - 1;
+                attend_row<D, POOL>(a, s, seq, (tile * 2 + rt) * per_tile + r / a.G, head * a.G + r % a.G);
+            }
+        }
+    } else if (warp == kMmaWarp) {
+        // ======== matrix products: one thread
+        if (lane == 0) {
+            constexpr uint32_t s_shape = tc_idesc(kTile, false), o_shape = tc_idesc(D, true);
+            int n[2] = {0, 0}, ring = 0;                       // products issued per row tile; tiles taken
+            bool fine = true;
+            auto wait = [&](uint32_t b, uint32_t parity) { fine = fine && mbar_wait_bounded(b, parity, a.err); };
+            auto scores = [&](int t, uint32_t slot) {          // S = Q K^T
+                #pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t at = (k >> 2) * (kTile * 128) + (k & 3) * 32;
+                    tc_mma_ss(tmem + t * kTile, tc_desc(base32 + C::Q_OFF + t * C::TILE + at, 0, 1024),
+                              tc_desc(slot + at, 0, 1024), s_shape, k > 0);
+                }
+                tc_commit(s_there(t));
+            };
+            auto slot_at = [&](int r) { return base32 + C::KV_OFF + (r % C::SLOTS) * C::TILE; };
+            int j = first_tile;
+            if (j < keys.n) {
+                wait(full(0), 0);
+                for (int t = 0; t < 2; ++t) {
+                    if (!keys.on(t, j)) continue;
+                    wait(q_there(t), 0);
+                    if (fine) scores(t, slot_at(0));
+                }
+                if (fine) tc_commit(empty(0));
+                ring = 1;
+            }
+            bool asked[2] = {keys.on(0, j), keys.on(1, j)};    // the queries were waited for
+            #pragma unroll 1
+            while (fine && j < keys.n) {
+                const int jn = keys.next(j + 1);
+                const int v = ring, kn = ring + 1;             // places of this tile's values, of the next one's keys
+                wait(full(v % C::SLOTS), v / C::SLOTS & 1);
+                bool have_keys = false;
+                #pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (keys.on(t, j)) {
+                        wait(w_there(t), n[t] & 1);
+                        if (!fine) break;
+                        tc_fence_after();
+                        #pragma unroll
+                        for (int k = 0; k < kTile / 16; ++k)   // O += W V
+                            tc_mma_ts(tmem + 2 * kTile + t * D, tmem + t * kTile + k * 8,
+                                      tc_desc(slot_at(v) + k * 2048, kTile * 128, 1024), o_shape, n[t] > 0 || k > 0);
+                        tc_commit(o_there(t));
+                        ++n[t];
+                    }
+                    if (t == 1) tc_commit(empty(v % C::SLOTS));
+                    if (jn < keys.n && keys.on(t, jn)) {
+                        if (!have_keys) wait(full(kn % C::SLOTS), kn / C::SLOTS & 1);
+                        have_keys = true;
+                        if (!asked[t]) wait(q_there(t), 0);
+                        asked[t] = true;
+                        if (!fine) break;
+                        scores(t, slot_at(kn));
+                    }
+                }
+                if (fine && jn < keys.n) tc_commit(empty(kn % C::SLOTS));
+                ring += 2;
+                j = jn;
+            }
+            tc_commit(done);                                   // nothing of this thread's is in flight at the end
+            mbar_wait_bounded(done, 0, a.err);
+        }
+        __syncwarp();
+    } else if (warp == kLoadWarp) {
+        // ======== keys and values: a lane per (block, 64 elements) of a tile
+        const int log_b = a.log_b, blocks = kTile >> log_b;
+        const int blk = lane / C::HALVES, half = lane % C::HALVES;
+        int ring = 0, edges = 0;
+        bool fine = true;
+        int issued = 0;
+        #pragma unroll 1
+        for (int j = first_tile; fine && j < keys.n; j = keys.next(j + 1)) {
+            const int j0 = keys.base + j * kTile, rows = min(kTile, keys.end - j0);
+            const bool mine = blk < blocks && (blk << log_b) < rows;
+            const int id = mine ? query_block(a, s, j0 + (blk << log_b)) : 0;
+            const int y = (id * a.H + head) << log_b;
+            const uint32_t bytes = ((rows + a.B - 1) >> log_b) * C::HALVES * a.B * 128;
+            #pragma unroll
+            for (int kv = 0; kv < 2; ++kv, ++ring) {
+                const int slot = ring % C::SLOTS;
+                if (ring >= C::SLOTS && !warp_wait(empty(slot), (ring / C::SLOTS - 1) & 1, a.err)) {
+                    fine = false;
+                    break;
+                }
+                const uint32_t at = base32 + C::KV_OFF + slot * C::TILE;
+                const bool tail = kv == 1 && rows < kTile;     // values past the end: zero, they meet weights of zero
+                const uint32_t b = tail ? edge : full(slot);
+                if (lane == 0) mbar_arrive_expect_tx(b, bytes);
+                __syncwarp();
+                if (mine) tma_load_2d(at + half * (kTile * 128) + (blk << log_b) * 128, kv ? &p.vmap : &p.kmap, half * 64, y, b);
+                if (tail) {
+                    fine = warp_wait(edge, edges++ & 1, a.err);
+                    #pragma unroll 1
+                    for (int u = rows * 8 + lane; u < kTile * 8; u += 32)
+                        #pragma unroll
+                        for (int h = 0; h < C::HALVES; ++h)
+                            *reinterpret_cast<uint4*>(smem + C::KV_OFF + slot * C::TILE + h * (kTile * 128) + u * 16) =
+                                make_uint4(0, 0, 0, 0);
+                    fence_async_shared();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(full(slot));
+                }
+                issued = ring + 1;
+            }
+        }
+        // before the CTA ends: every copy that was asked for has landed
+        for (int r = max(0, issued - C::SLOTS); r < issued; ++r)
+            mbar_wait_bounded(full(r % C::SLOTS), r / C::SLOTS & 1, a.err);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_free(tmem);
+    }
+}
+
+template <typename C>
+int launch_prompt_typed(const kv_pool* pool, const PromptArgs& p, bool pdl, cudaStream_t stream) {
+    static unsigned long long attr_done = 0;               // the shared-memory opt-in is a per-device attribute
+    const unsigned long long bit = 1ull << (pool->device & 63);
+    if (!(attr_done & bit)) {
+        if (cudaFuncSetAttribute(query_prompt_kernel<C::D, C::POOL>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
+            cudaSuccess)
+            return KV_ERR_CUDA;
+        attr_done |= bit;
+    }
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.a.batch * p.a.H * p.tiles));
+    cfg.blockDim = dim3(C::WARPS * 32);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, query_prompt_kernel<C::D, C::POOL>, p) != cudaSuccess) {
+        cudaGetLastError();
+        return KV_ERR_CUDA;
+    }
+    return KV_OK;
+}
+
+}  // namespace
+}  // namespace kvp
