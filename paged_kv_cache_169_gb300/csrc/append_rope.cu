@@ -160,23 +160,6 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const __grid_con
     }
 }
 
-// The 8 nibbles of a word as float16 pairs times their scales, exact: p[0] holds nibbles 0 and 4 ..
-// p[3] nibbles 3 and 7 (int4.cuh's expansion without the sixteenth, one instruction more).
-__device__ __forceinline__ void expand_full(uint32_t w, uint32_t scales, uint32_t (&p)[4]) {
-    const __half2 s = *reinterpret_cast<const __half2*>(&scales);
-    #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t u = w >> (i < 2 ? 0 : 8);
-        if (i & 1) {
-            u = int4_pair<0x00F000F0u>(u, __float2half2_rn(0.0625f), __float2half2_rn(-72.f));
-        } else {
-            u = int4_pair<0x000F000Fu>(u, __float2half2_rn(1.f), __float2half2_rn(-1032.f));
-        }
-        const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&u), s);
-        p[i] = *reinterpret_cast<const uint32_t*>(&r);
-    }
-}
-
 // 8 float16 values to the output type
 template <typename TOut>
 __device__ __forceinline__ void store_halves(char* out, const uint4 v) {
@@ -240,7 +223,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_int4_kernel(const __gri
             #pragma unroll
             for (int j = 0; j < NK; ++j) {
                 uint32_t p[4];
-                expand_full(kw[j], (kb[j] << 7) * 0x00010001u, p);
+                int4_expand_full(kw[j], (kb[j] << 7) * 0x00010001u, p);
                 store_halves<TOut>(ko + (j * TPK + tk) * row + unit * 8 * ES,
                                    make_uint4(__byte_perm(p[0], p[1], 0x5410), __byte_perm(p[2], p[3], 0x5410),
                                               __byte_perm(p[0], p[1], 0x7632), __byte_perm(p[2], p[3], 0x7632)));
@@ -250,7 +233,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_int4_kernel(const __gri
             #pragma unroll
             for (int w = 0; w < WORDS; ++w) {
                 uint32_t p[4];
-                expand_full(vw[w], sc, p);
+                int4_expand_full(vw[w], sc, p);
                 e[0][2 * w] = __byte_perm(p[0], p[1], 0x5410);
                 e[0][2 * w + 1] = __byte_perm(p[2], p[3], 0x5410);
                 e[1][2 * w] = __byte_perm(p[0], p[1], 0x7632);
@@ -305,7 +288,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_int4_kernel(const __gri
                 w = *reinterpret_cast<const uint32_t*>(oct + int4_k_code<D>(token, e0));
                 b = *reinterpret_cast<const uint8_t*>(oct + int4_k_scale<D>(token, e0));
             }
-            expand_full(w, (b << 7) * 0x00010001u, p);
+            int4_expand_full(w, (b << 7) * 0x00010001u, p);
             store_halves<TOut>((is_v ? a.v : a.k) + tok * row + (static_cast<int64_t>(h) * D + e0) * ES,
                                make_uint4(__byte_perm(p[0], p[1], 0x5410), __byte_perm(p[2], p[3], 0x5410),
                                           __byte_perm(p[0], p[1], 0x7632), __byte_perm(p[2], p[3], 0x7632)));

@@ -68,8 +68,8 @@ int plan_query(const kv_pool* pool, const kv_query_args& x, QueryPlan* plan) {
     if (g != 1 && g != 2 && g != 4 && g != 8) return KV_ERR_INVALID_ARG;
     if (static_cast<int64_t>(x.batch) * d.num_heads * prompt_tiles(x.max_queries, g) > (int64_t{1} << 30))
         return KV_ERR_INVALID_ARG;
-    // the tensor-core kernel for float16 pools and more rows of a K/V head than one matrix product takes
-    plan->prompt = d.dtype == KV_F16 && static_cast<int64_t>(x.max_queries) * g > 16;
+    // the tensor-core kernel where a K/V head has more than 16 rows
+    plan->prompt = d.dtype != KV_F32 && static_cast<int64_t>(x.max_queries) * g > 16;
     plan->ws_bytes = 256;
     return KV_OK;
 }
@@ -108,7 +108,7 @@ int launch_query(const kv_pool* pool, const kv_query_args& x, const QueryPlan& p
     a.err = pool->d_err;
     const bool pdl = (x.flags & KV_DECODE_PDL) != 0;
     const cudaStream_t stream = static_cast<cudaStream_t>(x.stream);
-    if (plan.prompt) return launch_query_prompt_f16(pool, x.layer, a, pdl, stream);
+    if (plan.prompt) return launch_query_prompt(pool, x.layer, a, pdl, stream);
     return launch_query_rows(pool, a, pdl, stream);
 }
 

@@ -204,7 +204,7 @@ __device__ __noinline__ void attend_row(const QueryArgs& a, int s, QuerySeq seq,
 inline int prompt_tiles(int max_queries, int group) { return static_cast<int>((static_cast<int64_t>(max_queries) * group + 255) / 256); }
 
 // The kernels' launchers.
-int launch_query_prompt_f16(const kv_pool* pool, int layer, const QueryArgs& a, bool pdl, cudaStream_t stream);
+int launch_query_prompt(const kv_pool* pool, int layer, const QueryArgs& a, bool pdl, cudaStream_t stream);
 int launch_query_rows(const kv_pool* pool, const QueryArgs& a, bool pdl, cudaStream_t stream);
 
 }  // namespace kvp

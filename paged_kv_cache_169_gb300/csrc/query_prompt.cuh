@@ -9,30 +9,52 @@ namespace kvp {
 struct PromptArgs {
     CUtensorMap kmap, vmap;            // float16 pools: the layer as [rows][D], boxes of 64 elements by a block
     QueryArgs a;
-    int tiles;                         // row tiles per (sequence, K/V head)
+    int tiles;                         // pairs of row tiles per (sequence, K/V head)
 };
+
+int launch_query_prompt_fp8(const kv_pool* pool, const PromptArgs& p, bool pdl, cudaStream_t stream);
+int launch_query_prompt_int4(const kv_pool* pool, const PromptArgs& p, bool pdl, cudaStream_t stream);
 
 namespace {
 
 constexpr int kTile = 128;             // rows of a row tile and keys of a key tile
-constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kWidenWarp = 12;
+constexpr int kFactorTiles = 8;        // key tiles whose FP8 scales are kept (more than are in flight)
 
 template <int D_, kv_dtype POOL_>
 struct PromptCfg {
     static constexpr int D = D_;
     static constexpr kv_dtype POOL = POOL_;
+    static constexpr bool WIDEN = POOL != KV_F16;              // tiles are widened to float16 on their way
     static constexpr int HALVES = D / 64;                      // 64-element (128-byte) columns of a tile
     static constexpr int TILE = HALVES * kTile * 128;          // bytes of 128 rows as float16
-    static constexpr int SLOTS = D == 128 ? 5 : 8;             // key and value tiles in flight
-    static constexpr int WARPS = 10;
-    static constexpr int Q_OFF = 0, KV_OFF = 2 * TILE;
-    static constexpr int BAR_OFF = KV_OFF + SLOTS * TILE;
-    // full, empty per slot; per row tile: queries there, scores there, weights there, product there; edge; done
-    static constexpr int BARS = 2 * SLOTS + 4 * 2 + 2;
+    // key and value tiles in flight as float16, and as stored
+    static constexpr int SLOTS = D == 128 ? (WIDEN ? 4 : 5) : 8;
+    static constexpr int RAWS = WIDEN ? (D == 128 ? 2 : 4) : 0;
+    static constexpr int RAW = WIDEN ? kTile * kRowBytes<D, POOL> : 0;
+    // Registers: 168 (12 warps) or 128 (16 warps) per thread at launch, shared out by fours of warps
+    static constexpr int WARPS = WIDEN ? 16 : 12;
+    static constexpr int REGS_SOFTMAX = WIDEN ? 200 : 208, REGS_ISSUE = WIDEN ? 48 : 88, REGS_WIDEN = 64;
+    static_assert(WIDEN ? 2 * REGS_SOFTMAX + REGS_ISSUE + REGS_WIDEN <= 512 : 2 * REGS_SOFTMAX + REGS_ISSUE <= 504, "registers");
+    static constexpr int Q_OFF = 0, KV_OFF = 2 * TILE, RAW_OFF = KV_OFF + SLOTS * TILE;
+    static constexpr int FACTOR_OFF = RAW_OFF + RAWS * RAW;
+    static constexpr int FACTORS = POOL == KV_FP8_E4M3 ? kFactorTiles * 2 * 16 * 4 : 0;
+    static constexpr int BAR_OFF = FACTOR_OFF + FACTORS;
+    // full, empty per slot; per row tile: queries there, scores there, weights there, product there; edge; done;
+    // full, empty per raw tile
+    static constexpr int BARS = 2 * SLOTS + 4 * 2 + 2 + 2 * RAWS;
     static constexpr int MISC_OFF = BAR_OFF + BARS * 8;
     static constexpr int SMEM = MISC_OFF + 64 + 1024;          // and up to 1024 bytes of alignment
     static_assert(SMEM <= 227 * 1024, "shared memory");
+    static_assert(BAR_OFF % 16 == 0 && RAW % 16 == 0, "alignment");
 };
+
+template <int N> __device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 // A bounded wait by a whole warp: all of its lanes go on, or none.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* err) {
@@ -43,6 +65,7 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* er
 struct PromptMisc {
     uint32_t tmem;
     int lo[2], hi[2];
+    int vmax;                          // FP8: the largest value scale, as the bits of its magnitude
 };
 
 // Key tiles [a, b) of each row tile, numbered from position `base`.
@@ -80,6 +103,59 @@ __device__ __forceinline__ float capped(float s, float k2, float capl) {
 // at most 2^15 in float16, and normal ones down to 2^-21 of the largest.
 constexpr float kRaise = 8.f, kLift = 7.f;
 
+// Widen a raw tile (whole blocks of one head, as the pool holds them) to swizzled float16 rows, by 128 threads.
+// Values: rows from `rows` on are zero (they meet weights of zero).  Every conversion is exact.
+template <int D, kv_dtype POOL, bool IS_V>
+__device__ __forceinline__ void widen_tile(const char* raw, char* slot, int rows, int tid) {
+    auto place = [&](int r, int ch) {                          // 16 bytes: 8 elements of a row
+        return reinterpret_cast<uint4*>(slot + (ch >> 3) * (kTile * 128) + r * 128 + ((ch & 7) ^ (r & 7)) * 16);
+    };
+    const uint4 none = make_uint4(0, 0, 0, 0);
+    if constexpr (POOL == KV_FP8_E4M3) {
+        constexpr int PER = D / 16;                            // 16-code pieces of a row
+        #pragma unroll 4
+        for (int u = tid; u < kTile * PER; u += 128) {
+            const int r = u / PER, ch = u % PER * 2;
+            const uint4 v = *reinterpret_cast<const uint4*>(raw + u * 16);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            uint32_t h[8];
+            #pragma unroll
+            for (int k = 0; k < 8; ++k) h[k] = e4m3x2_to_half2_bits(static_cast<uint16_t>(w[k >> 1] >> (16 * (k & 1))));
+            const bool live = !IS_V || r < rows;
+            *place(r, ch) = live ? make_uint4(h[0], h[1], h[2], h[3]) : none;
+            *place(r, ch + 1) = live ? make_uint4(h[4], h[5], h[6], h[7]) : none;
+        }
+    } else if constexpr (!IS_V) {
+        #pragma unroll 4
+        for (int u = tid; u < kTile * (D / 8); u += 128) {
+            const int r = u / (D / 8), ch = u % (D / 8);
+            const char* oct = raw + (r >> 3) * Int4<D>::OCT;
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(oct + int4_k_code<D>(r & 7, ch * 8));
+            const uint32_t sc = *reinterpret_cast<const uint8_t*>(oct + int4_k_scale<D>(r & 7, ch * 8));
+            uint32_t x[4];
+            int4_expand_full(w, (sc << 7) | (sc << 23), x);
+            *place(r, ch) = make_uint4(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410),
+                                       __byte_perm(x[0], x[1], 0x7632), __byte_perm(x[2], x[3], 0x7632));
+        }
+    } else {
+        #pragma unroll 2
+        for (int u = tid; u < kTile / 2 * (D / 8); u += 128) { // 8 elements of two tokens
+            const int r = u / (D / 8) * 2, ch = u % (D / 8);
+            const char* oct = raw + (r >> 3) * Int4<D>::OCT;
+            const uint2 w = *reinterpret_cast<const uint2*>(oct + int4_v_piece<D>(r & 7, ch * 8));
+            const uint32_t sc = *reinterpret_cast<const uint16_t*>(oct + int4_v_scale<D>(r & 7, ch * 8));
+            const uint32_t scales = (sc & 0xFFu) << 7 | (sc & 0xFF00u) << 15;
+            uint32_t x[4], y[4];
+            int4_expand_full(w.x, scales, x);
+            int4_expand_full(w.y, scales, y);
+            *place(r, ch) = r < rows ? make_uint4(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410),
+                                                  __byte_perm(y[0], y[1], 0x5410), __byte_perm(y[2], y[3], 0x5410)) : none;
+            *place(r + 1, ch) = r + 1 < rows ? make_uint4(__byte_perm(x[0], x[1], 0x7632), __byte_perm(x[2], x[3], 0x7632),
+                                                          __byte_perm(y[0], y[1], 0x7632), __byte_perm(y[2], y[3], 0x7632)) : none;
+        }
+    }
+}
+
 template <int D, kv_dtype POOL>
 __global__ void __launch_bounds__(PromptCfg<D, POOL>::WARPS * 32, 1)
 query_prompt_kernel(const __grid_constant__ PromptArgs p) {
@@ -98,6 +174,9 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
     auto w_there = [&](int t) { return bar(2 * C::SLOTS + 4 + t); };
     auto o_there = [&](int t) { return bar(2 * C::SLOTS + 6 + t); };
     const uint32_t edge = bar(2 * C::SLOTS + 8), done = bar(2 * C::SLOTS + 9);
+    auto raw_full = [&](int i) { return bar(2 * C::SLOTS + 10 + i); };
+    auto raw_empty = [&](int i) { return bar(2 * C::SLOTS + 10 + C::RAWS + i); };
+    float* const factors = reinterpret_cast<float*>(smem + C::FACTOR_OFF);     // FP8: [tile][keys, values][block]
 
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -112,7 +191,7 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
     // ---- set-up: barriers, tensor memory, what the rows see
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::SLOTS; ++i) {
-            mbar_init(full(i), 1);
+            mbar_init(full(i), C::WIDEN ? 4 : 1);
             mbar_init(empty(i), 1);
         }
         for (int t = 0; t < 2; ++t) {
@@ -123,6 +202,11 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
         }
         mbar_init(edge, 1);
         mbar_init(done, 1);
+        for (int i = 0; i < C::RAWS; ++i) {
+            mbar_init(raw_full(i), 1);
+            mbar_init(raw_empty(i), 4);
+        }
+        misc->vmax = 0;
         fence_mbar_init();
     }
     if (threadIdx.x < 2) {
@@ -154,6 +238,7 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
 
     if (warp < kSoftmaxWarps) {
         // ======== queries in, softmax, result out: a thread per row
+        more_registers<C::REGS_SOFTMAX>();
         constexpr int CHUNKS = D / 8;                          // 16-byte pieces of a row
         char* const qt = smem + C::Q_OFF + rt * C::TILE;
         const int64_t q0 = static_cast<int64_t>(seq.first) * a.q_stride + static_cast<int64_t>(head) * a.G * D * 2;
@@ -169,6 +254,20 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
         fence_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_there(rt));
+
+        // FP8: value scales enter the weights relative to the largest one, which multiplies the result
+        float vref = 1.f;
+        if constexpr (POOL == KV_FP8_E4M3) {
+            float top = 0.f;
+            for (int at = keys.base + static_cast<int>(threadIdx.x) * a.B; at < keys.end; at += kSoftmaxWarps * 32 * a.B)
+                top = max_nan(top, fabsf(a.vscale[query_block(a, s, at)]));
+            // (bits of magnitudes, NaN among them, are ordered as integers)
+            const int bits = __reduce_max_sync(0xffffffffu, __float_as_int(top) & 0x7FFFFFFF);
+            if (lane == 0) atomicMax(&misc->vmax, bits);
+            asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxWarps * 32) : "memory");
+            vref = max_nan(__int_as_float(misc->vmax), 1.17549435e-38f);
+        }
+        const float inv_vref = 1.f / vref;
 
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;       // the warp's 32 lanes
         const uint32_t st = tmem + lanes + rt * kTile, ot = tmem + lanes + 2 * kTile + rt * D;
@@ -196,6 +295,15 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
             #pragma unroll
             for (int k = 0; k < 4; ++k) tmem_wait_load32(xr + 32 * k);
             const int j0 = keys.base + j * kTile;
+            const float* const scales = factors + (j % kFactorTiles) * 32;
+            if constexpr (POOL == KV_FP8_E4M3) {
+                #pragma unroll
+                for (int k = 0; k < kTile; k += 8) {
+                    const float f = scales[k >> a.log_b];
+                    #pragma unroll
+                    for (int e = 0; e < 8; ++e) x[k + e] *= f;
+                }
+            }
             if (cap) {
                 #pragma unroll
                 for (int k = 0; k < kTile; ++k) x[k] = capped(x[k], k2, capl);
@@ -251,6 +359,10 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                     y.x = ex2_approx(y.x);
                     y.y = ex2_approx(y.y);
                     sum[k & 1] = __fadd2_rn(sum[k & 1], y);
+                    if constexpr (POOL == KV_FP8_E4M3) {
+                        const float f = scales[16 + ((64 * h + 2 * k) >> a.log_b)] * inv_vref;
+                        y = __fmul2_rn(y, make_float2(f, f));
+                    }
                     const __half2 hv = __floats2half2_rn(y.x, y.y);
                     w[k] = *reinterpret_cast<const uint32_t*>(&hv);
                 }
@@ -265,7 +377,7 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
         // ---- the result: through the queries' place in shared memory, a warp its own 32 rows
         if (fine && i > 0 && !warp_wait(o_there(rt), (i - 1) & 1, a.err)) fine = false;
         if (fine && i > 0) tc_fence_after();
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float inv = l == 0.f ? 0.f : vref / l;
         bool odd = false;                                      // something is not finite: from the definition below
         #pragma unroll 1
         for (int k = 0; k < D; k += 32) {
@@ -313,7 +425,41 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                 attend_row<D, POOL>(a, s, seq, (tile * 2 + rt) * per_tile + r / a.G, head * a.G + r % a.G);
             }
         }
-    } else if (warp == kMmaWarp) {
+    } else if (C::WIDEN && warp >= kWidenWarp) {
+        // ======== stored tiles to float16
+        if constexpr (C::WIDEN) {
+            fewer_registers<C::REGS_WIDEN>();
+            const int tid = static_cast<int>(threadIdx.x) - kWidenWarp * 32;
+            int ring = 0;
+            bool fine = true;
+            #pragma unroll 1
+            for (int j = first_tile; fine && j < keys.n; j = keys.next(j + 1)) {
+                const int rows = min(kTile, keys.end - (keys.base + j * kTile));
+                #pragma unroll
+                for (int kv = 0; kv < 2; ++kv, ++ring) {
+                    const int slot = ring % C::SLOTS, raw = ring % C::RAWS;
+                    if (!warp_wait(raw_full(raw), ring / C::RAWS & 1, a.err) ||
+                        (ring >= C::SLOTS && !warp_wait(empty(slot), (ring / C::SLOTS - 1) & 1, a.err))) {
+                        fine = false;
+                        break;
+                    }
+                    const char* from = smem + C::RAW_OFF + raw * C::RAW;
+                    char* to = smem + C::KV_OFF + slot * C::TILE;
+                    if (kv == 0) widen_tile<D, POOL, false>(from, to, rows, tid);
+                    else widen_tile<D, POOL, true>(from, to, rows, tid);
+                    fence_async_shared();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(full(slot));
+                        mbar_arrive(raw_empty(raw));
+                    }
+                }
+            }
+        }
+    } else {
+        fewer_registers<C::REGS_ISSUE>();
+    }
+    if (warp == kMmaWarp) {
         // ======== matrix products: one thread
         if (lane == 0) {
             constexpr uint32_t s_shape = tc_idesc(kTile, false), o_shape = tc_idesc(D, true);
@@ -380,32 +526,50 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
         }
         __syncwarp();
     } else if (warp == kLoadWarp) {
-        // ======== keys and values: a lane per (block, 64 elements) of a tile
-        const int log_b = a.log_b, blocks = kTile >> log_b;
-        const int blk = lane / C::HALVES, half = lane % C::HALVES;
+        // ======== keys and values in: float16 straight to their place, a lane per (block, 64 elements) of a tile;
+        // others as stored, a lane per block
+        constexpr int LPB = C::WIDEN ? 1 : C::HALVES;
+        constexpr int DEPTH = C::WIDEN ? C::RAWS : C::SLOTS;
+        auto there = [&](int i) { return C::WIDEN ? raw_full(i) : full(i); };
+        auto gone = [&](int i) { return C::WIDEN ? raw_empty(i) : empty(i); };
+        const int log_b = a.log_b, blk = lane / LPB, half = lane % LPB;
         int ring = 0, edges = 0;
         bool fine = true;
-        int issued = 0;
         #pragma unroll 1
         for (int j = first_tile; fine && j < keys.n; j = keys.next(j + 1)) {
             const int j0 = keys.base + j * kTile, rows = min(kTile, keys.end - j0);
-            const bool mine = blk < blocks && (blk << log_b) < rows;
+            const bool mine = (blk << log_b) < rows;
             const int id = mine ? query_block(a, s, j0 + (blk << log_b)) : 0;
-            const int y = (id * a.H + head) << log_b;
-            const uint32_t bytes = ((rows + a.B - 1) >> log_b) * C::HALVES * a.B * 128;
+            const uint32_t block_bytes = C::WIDEN ? a.B * kRowBytes<D, POOL> : a.B * 128;
+            const uint32_t bytes = ((rows + a.B - 1) >> log_b) * LPB * block_bytes;
+            if constexpr (POOL == KV_FP8_E4M3) {
+                if (blk < 16) {
+                    factors[(j % kFactorTiles) * 32 + blk] = mine ? a.kscale[id] : 0.f;
+                    factors[(j % kFactorTiles) * 32 + 16 + blk] = mine ? a.vscale[id] : 0.f;
+                }
+                __syncwarp();
+            }
             #pragma unroll
-            for (int kv = 0; kv < 2; ++kv, ++ring) {
-                const int slot = ring % C::SLOTS;
-                if (ring >= C::SLOTS && !warp_wait(empty(slot), (ring / C::SLOTS - 1) & 1, a.err)) {
+            for (int kv = 0; kv < 2; ++kv) {
+                const int slot = ring % DEPTH;
+                if (ring >= DEPTH && !warp_wait(gone(slot), (ring / DEPTH - 1) & 1, a.err)) {
                     fine = false;
                     break;
                 }
-                const uint32_t at = base32 + C::KV_OFF + slot * C::TILE;
-                const bool tail = kv == 1 && rows < kTile;     // values past the end: zero, they meet weights of zero
-                const uint32_t b = tail ? edge : full(slot);
+                const bool tail = !C::WIDEN && kv == 1 && rows < kTile;   // values past the end: zero, they meet weights of zero
+                const uint32_t b = tail ? edge : there(slot);
                 if (lane == 0) mbar_arrive_expect_tx(b, bytes);
                 __syncwarp();
-                if (mine) tma_load_2d(at + half * (kTile * 128) + (blk << log_b) * 128, kv ? &p.vmap : &p.kmap, half * 64, y, b);
+                if (mine) {
+                    if constexpr (C::WIDEN) {
+                        const int64_t from = (static_cast<int64_t>(id) * a.H + head) * block_bytes;
+                        bulk_g2s(base32 + C::RAW_OFF + slot * C::RAW + blk * block_bytes, (kv ? a.vpool : a.kpool) + from,
+                                 block_bytes, b);
+                    } else {
+                        tma_load_2d(base32 + C::KV_OFF + slot * C::TILE + half * (kTile * 128) + (blk << log_b) * 128,
+                                    kv ? &p.vmap : &p.kmap, half * 64, (id * a.H + head) << log_b, b);
+                    }
+                }
                 if (tail) {
                     fine = warp_wait(edge, edges++ & 1, a.err);
                     #pragma unroll 1
@@ -418,12 +582,11 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(full(slot));
                 }
-                issued = ring + 1;
+                ++ring;
             }
         }
         // before the CTA ends: every copy that was asked for has landed
-        for (int r = max(0, issued - C::SLOTS); r < issued; ++r)
-            mbar_wait_bounded(full(r % C::SLOTS), r / C::SLOTS & 1, a.err);
+        for (int r = max(0, ring - DEPTH); r < ring; ++r) mbar_wait_bounded(there(r % DEPTH), r / DEPTH & 1, a.err);
     }
     tc_fence_before();
     __syncthreads();
@@ -458,6 +621,12 @@ int launch_prompt_typed(const kv_pool* pool, const PromptArgs& p, bool pdl, cuda
         return KV_ERR_CUDA;
     }
     return KV_OK;
+}
+
+template <kv_dtype POOL>
+int launch_prompt_pool(const kv_pool* pool, const PromptArgs& p, bool pdl, cudaStream_t stream) {
+    return pool->desc.head_dim == 128 ? launch_prompt_typed<PromptCfg<128, POOL>>(pool, p, pdl, stream)
+                                      : launch_prompt_typed<PromptCfg<64, POOL>>(pool, p, pdl, stream);
 }
 
 }  // namespace
