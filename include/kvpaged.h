@@ -552,7 +552,8 @@ KV_API int paged_decode_attention_ex(kv_pool* pool, const kv_decode_args* args);
  *                  without ranges).  A block id outside the pool that some row's positions
  *                  reach sets KV_DEVERR_BLOCK_ID and block 0 is read; entries of blocks that no
  *                  row of the sequence sees are not read (they may be -1: kv_alloc_seq_trim).
- *   max_context    host upper bound of context_lens, 0 .. 2^24.
+ *   max_context    host upper bound of context_lens, 0 .. 2^24.  (Calls of more than 2^30 row tiles or,
+ *                  with at most 16 rows of a KV head, 16-token chunks in 1024 sequences are refused.)
  *   window         0, or the last `window` positions only.
  *   scale          finite and > 0.   score_cap  0 (none), or finite and > 0.
  *   slopes         NULL, or device float32 [num_q_heads].

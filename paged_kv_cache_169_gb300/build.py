@@ -24,7 +24,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",
               "-Xcompiler", "-fvisibility=hidden", "-DKVPAGED_BUILD"]
 SOURCES = ["api.cu", "append_copy.cu", "append_rope.cu", "append_rope_axes.cu", "attention_int4.cu", "decode_attention.cu",
-           "decode_attention_gqa.cu", "query_attention.cu", "query_prompt_f16.cu",
+           "decode_attention_gqa.cu", "query_attention.cu", "query_few.cu", "query_prompt_f16.cu",
            "query_prompt_fp8.cu", "query_prompt_int4.cu", "static_scratch.cu", "allocator.cpp"]
 
 

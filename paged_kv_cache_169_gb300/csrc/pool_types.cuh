@@ -49,8 +49,9 @@ inline int launch_decode(const kv_pool* pool, int layer, const void* q, const vo
 
 // paged_query_attention (query_attention.cu)
 struct QueryPlan {
-    bool prompt;         // the tensor-core kernel
-    size_t ws_bytes;     // workspace bytes
+    enum Kind { ROWS, FEW, PROMPT } kind;
+    size_t ws_bytes;         // workspace bytes
+    size_t counter_bytes;    // of them, counters at its start, zero between calls
 };
 int plan_query(const kv_pool* pool, const kv_query_args& args, QueryPlan* plan);
 int launch_query(const kv_pool* pool, const kv_query_args& args, const QueryPlan& plan);

@@ -68,9 +68,17 @@ int plan_query(const kv_pool* pool, const kv_query_args& x, QueryPlan* plan) {
     if (g != 1 && g != 2 && g != 4 && g != 8) return KV_ERR_INVALID_ARG;
     if (static_cast<int64_t>(x.batch) * d.num_heads * prompt_tiles(x.max_queries, g) > (int64_t{1} << 30))
         return KV_ERR_INVALID_ARG;
-    // the tensor-core kernel where a K/V head has more than 16 rows
-    plan->prompt = d.dtype != KV_F32 && static_cast<int64_t>(x.max_queries) * g > 16;
+    // float32 pools: a warp per row and head; the others by what a K/V head's rows fill: one 16-row matrix
+    // product over keys that are read once, or 128-row tiles of the tensor cores
+    const int64_t rows = static_cast<int64_t>(x.max_queries) * g;
+    plan->kind = d.dtype == KV_F32 ? QueryPlan::ROWS : rows <= kFewRows ? QueryPlan::FEW : QueryPlan::PROMPT;
     plan->ws_bytes = 256;
+    plan->counter_bytes = 0;
+    if (plan->kind == QueryPlan::FEW) {
+        const int64_t seqs = x.batch < kFewSeqs ? x.batch : kFewSeqs;
+        if (seqs * d.num_heads * (x.max_context / 16 + 2) > (int64_t{1} << 30)) return KV_ERR_INVALID_ARG;
+        plan->ws_bytes = few_space(pool, &plan->counter_bytes);
+    }
     return KV_OK;
 }
 
@@ -108,8 +116,15 @@ int launch_query(const kv_pool* pool, const kv_query_args& x, const QueryPlan& p
     a.err = pool->d_err;
     const bool pdl = (x.flags & KV_DECODE_PDL) != 0;
     const cudaStream_t stream = static_cast<cudaStream_t>(x.stream);
-    if (plan.prompt) return launch_query_prompt(pool, x.layer, a, pdl, stream);
-    return launch_query_rows(pool, a, pdl, stream);
+    // (every launch leaves its counters zero)
+    if (plan.counter_bytes && !(x.flags & KV_DECODE_WORKSPACE_ZEROED) &&
+        cudaMemsetAsync(x.workspace, 0, plan.counter_bytes, stream) != cudaSuccess)
+        return KV_ERR_CUDA;
+    switch (plan.kind) {
+        case QueryPlan::ROWS: return launch_query_rows(pool, a, pdl, stream);
+        case QueryPlan::FEW: return launch_query_few(pool, a, x.workspace, pdl, stream);
+        default: return launch_query_prompt(pool, x.layer, a, pdl, stream);
+    }
 }
 
 }  // namespace kvp

@@ -70,6 +70,18 @@ __device__ __forceinline__ int query_block(const QueryArgs& a, int s, int j) {
     return 0;
 }
 
+// t = cap tanh(x) in log2 units for x = s kx: 1 - 2 / (e^2x + 1), exact to a few 2^-24 of the cap
+__device__ __forceinline__ float capped(float s, float k2, float capl) {
+    const float e = ex2_approx(s * k2);
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e + 1.f));
+    return fmaf(-2.f * capl, r, capl);
+}
+
+// Weights are kept 2^7 above their softmax value relative to the base, which may lag the maximum by up to 2^8:
+// at most 2^15 in float16, and normal ones down to 2^-21 of the largest.
+constexpr float kRaise = 8.f, kLift = 7.f;
+
 template <int D, kv_dtype POOL>
 constexpr int kRowBytes = POOL == KV_INT4 ? D / 2 + D / 16 : POOL == KV_FP8_E4M3 ? D : POOL == KV_F16 ? 2 * D : 4 * D;
 
@@ -200,11 +212,17 @@ __device__ __noinline__ void attend_row(const QueryArgs& a, int s, QuerySeq seq,
 
 #endif  // __CUDACC__
 
+// Rows of a unit (sequence, K/V head) that one 16-row matrix product holds: the few-row kernel's.
+constexpr int kFewRows = 16;
+constexpr int kFewSeqs = 1024;         // sequences per launch of it
+
 // Row tiles (pairs of 128 rows) of a sequence's K/V head in the tensor-core kernel.
 inline int prompt_tiles(int max_queries, int group) { return static_cast<int>((static_cast<int64_t>(max_queries) * group + 255) / 256); }
 
 // The kernels' launchers.
 int launch_query_prompt(const kv_pool* pool, int layer, const QueryArgs& a, bool pdl, cudaStream_t stream);
+size_t few_space(const kv_pool* pool, size_t* counters);       // workspace bytes, those of its counters (at its start)
+int launch_query_few(const kv_pool* pool, const QueryArgs& a, void* workspace, bool pdl, cudaStream_t stream);
 int launch_query_rows(const kv_pool* pool, const QueryArgs& a, bool pdl, cudaStream_t stream);
 
 }  // namespace kvp

@@ -1,0 +1,627 @@
+// paged_query_attention for few rows: at most 16 rows (tokens times query heads) of a K/V head, so the keys and
+// values are read once for little work and the memory is what counts.
+//
+// The rows are the 16 rows of mma.m16n8k16 (empty ones are zero).  Every (sequence, K/V head) is a unit of
+// 16-token chunks; the chunks of all units, one after the other, are cut into equal ranges, one per CTA and SM, so
+// every SM reads as much whatever the lengths.  A CTA's eight warps take its chunks in turn, each through a ring
+// of its own filled by cp.async (tokens that no row sees are filled with zeros and not read); the part of a unit
+// in a CTA is joined in shared memory, and what crosses CTAs through the workspace by the CTA that finishes last,
+// in two levels where there are more than kFan parts.  Softmax as in the tensor-core kernel.
+//   float16   mma operands straight from the ring
+//   FP8, 4-bit  widened to float16 in a tile of the warp's own first
+#pragma once
+
+#include "query_attention.cuh"
+#include "widen.cuh"
+
+namespace kvp {
+
+struct FewArgs {
+    QueryArgs a;
+    float2* part_ml;       // [2 * CTAs][16] of a part's rows: base in log2 units, sum of weights
+    float* part_o;         // [2 * CTAs][16][D]
+    unsigned *done, *group_done;       // [2 * CTAs] each: parts, or groups of them, finished; zero between calls
+};
+
+// Workspace of a launch with `ctas` CTAs.
+struct FewSpace {
+    size_t ml, o, bytes;
+    FewSpace(int ctas, int d) {
+        ml = (static_cast<size_t>(ctas) * 4 * sizeof(unsigned) + 255) / 256 * 256;
+        o = ml + static_cast<size_t>(ctas) * 2 * kFewRows * sizeof(float2);
+        bytes = o + static_cast<size_t>(ctas) * 2 * kFewRows * d * sizeof(float);
+    }
+};
+
+namespace {
+
+constexpr unsigned FULL = 0xffffffffu;
+constexpr int kWarps = 8, kChunk = 16, kFan = 16;
+constexpr int kLeastChunks = 16;       // of a CTA's range: two per warp
+
+template <int D_, kv_dtype POOL_>
+struct FewCfg {
+    static constexpr int D = D_;
+    static constexpr kv_dtype POOL = POOL_;
+    static constexpr bool WIDEN = POOL != KV_F16;
+    static constexpr int ROW = kRowBytes<D, POOL>;
+    static constexpr int RAW = kChunk * ROW;                   // bytes of a chunk's keys (or values) as stored
+    static constexpr int META = POOL == KV_FP8_E4M3 ? 16 : 0;  // two blocks' key and value scales
+    static constexpr int STAGE = 2 * RAW + META;
+    static constexpr int PART = kFewRows * D * 4;              // a warp's part of a unit
+    static constexpr int TILE = WIDEN ? PART : 0;              // widened keys and values: as many bytes
+    static_assert(!WIDEN || TILE == 2 * kChunk * D * 2, "a part fits where the widened chunk was");
+    static_assert(WIDEN || STAGE == PART, "a part fits in a stage");
+    static constexpr int TABLES = 3 * kFewSeqs * 4 + kWarps * kFewRows * 8;
+    static constexpr int FIT = (226 * 1024 - 1024 - TABLES) / kWarps;
+    static constexpr int STAGES_FIT = (FIT - TILE) / STAGE;
+    static constexpr int STAGES = STAGES_FIT > 8 ? 8 : STAGES_FIT;
+    static constexpr int WARP = STAGES * STAGE + TILE;
+    static constexpr int ML_OFF = kWarps * WARP, SEQ_OFF = ML_OFF + kWarps * kFewRows * 8;
+    static constexpr int SMEM = SEQ_OFF + 3 * kFewSeqs * 4;
+    static_assert(STAGES >= 2 && STAGE % 16 == 0 && WARP % 16 == 0, "ring");
+};
+
+// 16 bytes global -> shared, or zeros (nothing is read)
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const char* src, bool read) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(read ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async4_or_zero(uint32_t dst, const void* src, bool read) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(read ? 4 : 0) : "memory");
+}
+
+// Positions [lo, hi) that some row of the sequence sees.
+struct Span { int lo, hi; };
+__device__ __forceinline__ Span seq_span(const QueryArgs& a, const QuerySeq& q) {
+    Span r{1 << 30, 0};
+    if (!a.ranges) {                                           // the first row's start, the last row's end
+        const int2 first = row_range(a, q, 0), last = row_range(a, q, q.n - 1);
+        if (last.x < last.y) {
+            r.lo = first.x;                                    // (0 where the first rows lie before position 0)
+            r.hi = last.y;
+        }
+        return r;
+    }
+    for (int i = 0; i < q.n; ++i) {
+        const int2 x = row_range(a, q, i);
+        if (x.x < x.y) {
+            r.lo = min(r.lo, x.x);
+            r.hi = max(r.hi, x.y);
+        }
+    }
+    return r;
+}
+
+// Four elements of a row's result; whether they are finite.
+template <int D>
+__device__ __forceinline__ bool store_quarter(const QueryArgs& a, const QuerySeq& seq, int h, int row, int c4, float4 o, float l) {
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (l == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
+    o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    const __half2 lo = __floats2half2_rn(o.x, o.y), hi = __floats2half2_rn(o.z, o.w);
+    uint2 w;
+    w.x = *reinterpret_cast<const uint32_t*>(&lo);
+    w.y = *reinterpret_cast<const uint32_t*>(&hi);
+    *reinterpret_cast<uint2*>(a.out + static_cast<int64_t>(seq.first + row / a.G) * a.out_stride +
+                              (h * a.G + row % a.G) * (D * 2) + c4 * 8) = w;
+    return fabsf(o.x) < CUDART_INF_F && fabsf(o.y) < CUDART_INF_F && fabsf(o.z) < CUDART_INF_F && fabsf(o.w) < CUDART_INF_F;
+}
+
+// Rows that came out not finite, by the whole CTA: a key or value that is not finite reaches, as 0 * NaN, rows that
+// do not see it, so such a row is worked out again from the definition, which reads only what it sees.
+template <int D, kv_dtype POOL>
+__device__ __forceinline__ void redo_rows(const QueryArgs& a, int s, const QuerySeq& seq, int h, unsigned* s_odd) {
+    const unsigned odd = *s_odd;
+    __syncthreads();
+    if (threadIdx.x == 0) *s_odd = 0;
+    #pragma unroll 1
+    for (int row = threadIdx.x >> 5; row < kFewRows; row += kWarps)
+        if (odd >> row & 1) attend_row<D, POOL>(a, s, seq, row / a.G, h * a.G + row % a.G);
+    __syncthreads();
+}
+
+template <int D, kv_dtype POOL>
+__global__ void __launch_bounds__(kWarps * 32, 1) query_few_kernel(const __grid_constant__ FewArgs x) {
+    using C = FewCfg<D, POOL>;
+    extern __shared__ __align__(128) char smem[];
+    __shared__ int s_part[kWarps];                             // bytes to a warp's part in shared memory, -1: none
+    __shared__ int s_warp_sum[kWarps];
+    __shared__ int s_go[2];
+    __shared__ unsigned s_odd;                                 // rows that came out not finite
+    const QueryArgs& a = x.a;
+    int* const s_lo = reinterpret_cast<int*>(smem + C::SEQ_OFF);               // what the sequence's rows see
+    int* const s_hi = s_lo + kFewSeqs;
+    int* const s_end = s_hi + kFewSeqs;                                        // inclusive prefix of chunks over all units
+    // chunks of a unit of the sequence (lo > hi: no rows; lo == hi: rows that see nothing, one chunk)
+    auto chunks_of = [&](int s) {
+        return s_lo[s] > s_hi[s] ? 0 : max(1, (s_hi[s] - (s_lo[s] & -kChunk) + kChunk - 1) / kChunk);
+    };
+    float2* const s_ml = reinterpret_cast<float2*>(smem + C::ML_OFF);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    // ---- chunks of every sequence and their prefix over the launch's units
+    {
+        const int per = (a.batch + kWarps * 32 - 1) / (kWarps * 32);
+        int sum = 0;
+        for (int s = tid * per; s < min(a.batch, (tid + 1) * per); ++s) {
+            const QuerySeq q = query_seq(a, s, blockIdx.x == 0);
+            s_lo[s] = q.n > 0 ? 0 : 1;
+            s_hi[s] = 0;
+            if (q.n > 0) {
+                const Span sp = seq_span(a, q);
+                if (sp.lo < sp.hi) {
+                    s_lo[s] = sp.lo;
+                    s_hi[s] = sp.hi;
+                }
+            }
+            sum += chunks_of(s) * a.H;
+        }
+        int upto = sum;
+        #pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const int v = __shfl_up_sync(FULL, upto, o);
+            if (lane >= o) upto += v;
+        }
+        if (lane == 31) s_warp_sum[warp] = upto;
+        if (tid == 0) s_odd = 0;
+        __syncthreads();
+        int before = upto - sum;
+        for (int w = 0; w < warp; ++w) before += s_warp_sum[w];
+        for (int s = tid * per; s < min(a.batch, (tid + 1) * per); ++s) {
+            before += chunks_of(s) * a.H;
+            s_end[s] = before;
+        }
+        __syncthreads();
+    }
+    const int total = s_end[a.batch - 1];
+    const int ctas = min(static_cast<int>(gridDim.x), (total + kLeastChunks - 1) / kLeastChunks);
+    const int cta = blockIdx.x;
+    if (cta >= ctas) return;
+    auto range_at = [&](int b) { return static_cast<int>(static_cast<int64_t>(total) * b / ctas); };
+    const int g0 = range_at(cta), g1 = range_at(cta + 1);
+    // the CTA whose range holds chunk k
+    auto cta_of = [&](int k) {
+        int b = static_cast<int>(static_cast<int64_t>(k) * ctas / total);
+        while (range_at(b + 1) <= k) ++b;
+        while (range_at(b) > k) --b;
+        return b;
+    };
+
+    // A place in the chunks of the launch.
+    struct Place { int s, h, c, n; };                          // sequence, head, chunk of the unit, the unit's chunks
+    auto place_of = [&](int k) {
+        int lo = 0, hi = a.batch - 1;                          // the first sequence that ends after k
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (s_end[mid] > k) hi = mid; else lo = mid + 1;
+        }
+        Place r;
+        r.s = lo;
+        r.n = chunks_of(lo);
+        const int at = k - (s_end[lo] - r.n * a.H);
+        r.h = at / r.n;
+        r.c = at - r.h * r.n;
+        return r;
+    };
+    auto next_unit = [&](Place& r) {                           // (only while a further unit exists)
+        if (++r.h == a.H) {
+            r.h = 0;
+            do r.n = chunks_of(++r.s); while (r.n == 0);
+        }
+    };
+
+    // ---- filling the ring
+    char* const ring = smem + warp * C::WARP;
+    const uint32_t ring32 = smem_u32(ring);
+    int fill_k = g0 + warp, fill_slot = 0;                     // the next chunk to ask for and its stage
+    Place fill = place_of(fill_k < g1 ? fill_k : g0);
+    int ids[2];                                                // its (up to two) physical blocks, -1: not read
+    // blocks of the chunk's 8-token halves; loaded one chunk ahead
+    auto look_up = [&]() {
+        ids[0] = ids[1] = -1;
+        if (fill_k >= g1) return;
+        const int lo = s_lo[fill.s], hi = s_hi[fill.s], j0 = (lo & -kChunk) + fill.c * kChunk;
+        #pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int first = max(j0 + 8 * i, lo);
+            if (first < min(j0 + 8 * i + 8, hi)) ids[i] = query_block(a, fill.s, first);
+        }
+    };
+    auto ask = [&]() {
+        if (fill_k < g1) {
+            const int lo = s_lo[fill.s], hi = s_hi[fill.s], j0 = (lo & -kChunk) + fill.c * kChunk;
+            const uint32_t st = ring32 + fill_slot * C::STAGE;
+            if constexpr (POOL == KV_INT4) {
+                constexpr int PIECES = Int4<D>::OCT / 16;      // of an oct: 8 tokens
+                #pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int64_t from = ((static_cast<int64_t>(max(ids[i], 0)) * a.H + fill.h) * (a.B >> 3) +
+                                          ((j0 + 8 * i) & (a.B - 1)) / 8) * Int4<D>::OCT;
+                    for (int u = lane; u < 2 * PIECES; u += 32) {
+                        const bool v = u >= PIECES;
+                        const int e = v ? u - PIECES : u;
+                        cp_async16_or_zero(st + (v ? C::RAW : 0) + i * Int4<D>::OCT + e * 16, (v ? a.vpool : a.kpool) + from + e * 16,
+                                           ids[i] >= 0);
+                    }
+                }
+            } else {
+                constexpr int PIECES = C::ROW / 16, STEP = 32 / PIECES;        // of a token; tokens per instruction
+                const int e = lane % PIECES;
+                #pragma unroll
+                for (int r0 = 0; r0 < kChunk; r0 += STEP) {
+                    const int r = r0 + lane / PIECES, j = j0 + r;
+                    const int id = r < 8 ? ids[0] : ids[1];
+                    const bool read = id >= 0 && j >= lo && j < hi;
+                    const int64_t from = ((static_cast<int64_t>(max(id, 0)) * a.H + fill.h) * a.B + (j & (a.B - 1))) * C::ROW + e * 16;
+                    // float16 rows in swizzled pieces (ldmatrix), others as they are
+                    const uint32_t to = st + r * C::ROW + (C::WIDEN ? e : (e ^ (r & 7))) * 16;
+                    cp_async16_or_zero(to, a.kpool + (read ? from : 0), read);
+                    cp_async16_or_zero(to + C::RAW, a.vpool + (read ? from : 0), read);
+                }
+                if constexpr (POOL == KV_FP8_E4M3) {
+                    if (lane < 4) {                            // key scales of the halves, then value scales
+                        const int id = lane & 1 ? ids[1] : ids[0];
+                        cp_async4_or_zero(st + 2 * C::RAW + lane * 4, (lane < 2 ? a.kscale : a.vscale) + max(id, 0), id >= 0);
+                    }
+                }
+            }
+            fill_k += kWarps;
+            fill_slot = fill_slot + 1 == C::STAGES ? 0 : fill_slot + 1;
+            if (fill_k < g1) {
+                fill.c += kWarps;
+                while (fill.c >= fill.n) {
+                    fill.c -= fill.n;
+                    next_unit(fill);
+                }
+            }
+            look_up();
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    look_up();
+    #pragma unroll 1
+    for (int i = 0; i < C::STAGES; ++i) ask();
+
+    // ---- the CTA's units
+    const bool bias = a.slopes != nullptr, cap = a.cap > 0.f;
+    const float qscale = a.scale * kLog2e, c = cap || bias ? 1.f : qscale;
+    const float k2 = cap ? 2.f * kLog2e * (a.scale / a.cap) : 0.f, capl = a.cap * kLog2e;
+    struct Cross { int s, h, first, last; };                   // a unit that crosses CTAs: its first and last CTA
+    Cross cross[2] = {{-1, 0, 0, 0}, {-1, 0, 0, 0}};           // one that began before this CTA, one that goes on after
+    int slot = 0;                                              // the ring's stage to read next
+    Place unit = place_of(g0);
+    int at = g0;
+    #pragma unroll 1
+    while (true) {
+        const int u0 = at - unit.c, u1 = u0 + unit.n;          // the unit's chunks; unit.c: the first of them here
+        const int to = min(g1, u1);
+        const QuerySeq seq = query_seq(a, unit.s, false);
+        const int lo = s_lo[unit.s], hi = s_hi[unit.s], base = lo & -kChunk;
+        const int rows = seq.n * a.G;
+        int2 sees[2];
+        int pos[2];
+        float slope[2], m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};
+        uint32_t q[D / 16][4];
+        #pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int row = g + 8 * r, i = row / a.G, hq = unit.h * a.G + row % a.G;
+            sees[r] = make_int2(0, 0);
+            pos[r] = seq.ctx - seq.n + i;
+            slope[r] = 0.f;
+            const bool some = row < rows;
+            if (some) {
+                sees[r] = row_range(a, seq, i);
+                if (bias) slope[r] = a.slopes[hq] * kLog2e;
+            }
+            const char* qr = a.q + static_cast<int64_t>(seq.first + (some ? i : 0)) * a.q_stride + hq * (D * 2) + t * 4;
+            #pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                q[k][r] = some ? *reinterpret_cast<const uint32_t*>(qr + k * 32) : 0u;
+                q[k][r + 2] = some ? *reinterpret_cast<const uint32_t*>(qr + k * 32 + 16) : 0u;
+            }
+        }
+        float o[D / 8][4];
+        #pragma unroll
+        for (int n = 0; n < D / 8; ++n)
+            #pragma unroll
+            for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+        float vref = 0x1p-126f, inv_vref = 0x1p126f;           // FP8: a power of two above the value scales so far
+        int held = -1;                                         // the stage of this warp's last chunk here, not yet filled again
+        #pragma unroll 1
+        for (int k = at + ((warp - (at - g0)) & (kWarps - 1)); k < to; k += kWarps) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(C::STAGES - 1) : "memory");
+            __syncwarp();
+            const char* st = ring + slot * C::STAGE;
+            const int j0 = base + (k - u0) * kChunk;
+            uint32_t kt = ring32 + slot * C::STAGE, vt = kt + C::RAW;
+            float ks[2] = {1.f, 1.f}, vs[2] = {1.f, 1.f};
+            if constexpr (C::WIDEN) {
+                char* const tile = ring + C::STAGES * C::STAGE;
+                widen_rows<D, POOL, false, kChunk, 32>(st, lo - j0, hi - j0, lane, [&](int r, int ch) {
+                    return reinterpret_cast<uint4*>(tile + r * (D * 2) + ((ch ^ (r & 7)) << 4));
+                });
+                widen_rows<D, POOL, true, kChunk, 32>(st + C::RAW, lo - j0, hi - j0, lane, [&](int r, int ch) {
+                    return reinterpret_cast<uint4*>(tile + kChunk * D * 2 + r * (D * 2) + ((ch ^ (r & 7)) << 4));
+                });
+                kt = ring32 + C::STAGES * C::STAGE;
+                vt = kt + kChunk * D * 2;
+                if constexpr (POOL == KV_FP8_E4M3) {
+                    const float4 f = *reinterpret_cast<const float4*>(st + 2 * C::RAW);
+                    ks[0] = f.x; ks[1] = f.y; vs[0] = f.z; vs[1] = f.w;
+                }
+                __syncwarp();
+            }
+            // ---- scores: 16 rows by two times 8 keys
+            float sc[2][4];
+            #pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                #pragma unroll
+                for (int e = 0; e < 4; ++e) sc[n][e] = 0.f;
+                const int r = n * 8 + (lane & 7);
+                #pragma unroll
+                for (int k4 = 0; k4 < D / 32; ++k4) {
+                    uint32_t b[4];
+                    ldsm_x4(kt + r * (D * 2) + (((k4 * 4 + (lane >> 3)) ^ (r & 7)) << 4), b);
+                    mma_16816(sc[n], q[2 * k4][0], q[2 * k4][1], q[2 * k4][2], q[2 * k4][3], b[0], b[1]);
+                    mma_16816(sc[n], q[2 * k4 + 1][0], q[2 * k4 + 1][1], q[2 * k4 + 1][2], q[2 * k4 + 1][3], b[2], b[3]);
+                }
+            }
+            #pragma unroll
+            for (int n = 0; n < 2; ++n)
+                #pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int r = e >> 1, j = j0 + n * 8 + 2 * t + (e & 1);
+                    float v = sc[n][e];
+                    if constexpr (POOL == KV_FP8_E4M3) v *= ks[n];
+                    if (cap) v = capped(v, k2, capl);
+                    if (bias) v = fmaf(-slope[r], fabsf(static_cast<float>(pos[r] - j)), cap ? v : v * qscale);
+                    v *= c;
+                    sc[n][e] = j >= sees[r].x && j < sees[r].y ? v : -CUDART_INF_F;
+                }
+            // ---- the base follows the maximum only when it is left behind by more than 2^8
+            float top[2];
+            #pragma unroll
+            for (int r = 0; r < 2; ++r)
+                top[r] = fmaxf(fmaxf(sc[0][2 * r], sc[0][2 * r + 1]), fmaxf(sc[1][2 * r], sc[1][2 * r + 1]));
+            if (__any_sync(FULL, top[0] - m[0] > kRaise || top[1] - m[1] > kRaise)) {
+                #pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    top[r] = fmaxf(top[r], __shfl_xor_sync(FULL, top[r], 1));
+                    top[r] = fmaxf(top[r], __shfl_xor_sync(FULL, top[r], 2));
+                    if (top[r] - m[r] > kRaise) {
+                        const float keep = ex2_approx(m[r] - top[r]);
+                        m[r] = top[r];
+                        l[r] *= keep;
+                        #pragma unroll
+                        for (int n = 0; n < D / 8; ++n) {
+                            o[n][2 * r] *= keep;
+                            o[n][2 * r + 1] *= keep;
+                        }
+                    }
+                }
+            }
+            if constexpr (POOL == KV_FP8_E4M3) {
+                const float big = fmaxf(fabsf(vs[0]), fabsf(vs[1]));
+                if (big > vref) {                              // (the same in every lane)
+                    const float to_ref = __int_as_float(min((__float_as_int(big) >> 23) + 1, 253) << 23);
+                    const float keep = vref / to_ref;
+                    #pragma unroll
+                    for (int n = 0; n < D / 8; ++n)
+                        #pragma unroll
+                        for (int e = 0; e < 4; ++e) o[n][e] *= keep;
+                    vref = to_ref;
+                    inv_vref = 1.f / to_ref;
+                }
+            }
+            // ---- weights, their sums and the values
+            uint32_t w[4];
+            #pragma unroll
+            for (int n = 0; n < 2; ++n)
+                #pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float off = kLift - (m[r] == -CUDART_INF_F ? 0.f : m[r]);
+                    float y0 = ex2_approx(sc[n][2 * r] + off), y1 = ex2_approx(sc[n][2 * r + 1] + off);
+                    l[r] += y0 + y1;
+                    if constexpr (POOL == KV_FP8_E4M3) {
+                        const float f = vs[n] * inv_vref;
+                        y0 *= f;
+                        y1 *= f;
+                    }
+                    const __half2 hv = __floats2half2_rn(y0, y1);
+                    w[2 * n + r] = *reinterpret_cast<const uint32_t*>(&hv);
+                }
+            const int vr = lane & 15;
+            #pragma unroll
+            for (int n = 0; n < D / 16; ++n) {
+                uint32_t b[4];
+                ldsm_x4_t(vt + vr * (D * 2) + (((2 * n + (lane >> 4)) ^ (vr & 7)) << 4), b);
+                mma_16816(o[2 * n], w[0], w[1], w[2], w[3], b[0], b[1]);
+                mma_16816(o[2 * n + 1], w[0], w[1], w[2], w[3], b[2], b[3]);
+            }
+            held = slot;
+            slot = slot + 1 == C::STAGES ? 0 : slot + 1;
+            __syncwarp();                                      // every lane has read the stage
+            if (k + kWarps < to) ask();
+        }
+        // ---- this warp's part, where its last chunk was
+        const int part_at = warp * C::WARP + (C::WIDEN ? C::STAGES : held) * C::STAGE;
+        if (held >= 0) {
+            char* const part = smem + part_at;
+            #pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                l[r] += __shfl_xor_sync(FULL, l[r], 1);
+                l[r] += __shfl_xor_sync(FULL, l[r], 2);
+                const int row = g + 8 * r;
+                if (row >= rows) continue;
+                if (t == 0) s_ml[warp * kFewRows + row] = make_float2(m[r], l[r]);
+                #pragma unroll
+                for (int n = 0; n < D / 8; ++n)
+                    *reinterpret_cast<float2*>(part + row * (D * 4) + (((2 * n + (t >> 1)) ^ (row & 7)) << 4) + (t & 1) * 8) =
+                        POOL == KV_FP8_E4M3 ? make_float2(o[n][2 * r] * vref, o[n][2 * r + 1] * vref)
+                                            : make_float2(o[n][2 * r], o[n][2 * r + 1]);
+            }
+        }
+        if (lane == 0) s_part[warp] = held >= 0 ? part_at : -1;
+        __syncthreads();
+        // ---- the CTA's part of the unit: to the output, or to the workspace
+        const bool whole = u0 >= g0 && u1 <= g1;
+        const int later = u0 < g0 ? 0 : 1, space = 2 * cta + later;
+        if (!whole) cross[later] = Cross{unit.s, unit.h, cta_of(u0), cta_of(u1 - 1)};
+        for (int e = tid; e < rows * (D / 4); e += kWarps * 32) {
+            const int row = e / (D / 4), c4 = e % (D / 4);
+            float mm = -CUDART_INF_F, ll = 0.f;
+            #pragma unroll
+            for (int v = 0; v < kWarps; ++v)
+                if (s_part[v] >= 0) mm = fmaxf(mm, s_ml[v * kFewRows + row].x);
+            const float off = mm == -CUDART_INF_F ? 0.f : mm;
+            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+            #pragma unroll
+            for (int v = 0; v < kWarps; ++v) {
+                if (s_part[v] < 0) continue;
+                const float2 ml = s_ml[v * kFewRows + row];
+                const float f = ex2_approx(ml.x - off);
+                const float4 p = *reinterpret_cast<const float4*>(smem + s_part[v] + row * (D * 4) + ((c4 ^ (row & 7)) << 4));
+                ll = fmaf(ml.y, f, ll);
+                sum.x = fmaf(p.x, f, sum.x);
+                sum.y = fmaf(p.y, f, sum.y);
+                sum.z = fmaf(p.z, f, sum.z);
+                sum.w = fmaf(p.w, f, sum.w);
+            }
+            if (whole) {
+                if (!store_quarter<D>(a, seq, unit.h, row, c4, sum, ll)) atomicOr(&s_odd, 1u << row);
+            } else {
+                if (c4 == 0) x.part_ml[space * kFewRows + row] = make_float2(mm, ll);
+                reinterpret_cast<float4*>(x.part_o)[(space * kFewRows + row) * (D / 4) + c4] = sum;
+            }
+        }
+        __syncthreads();
+        if (whole && s_odd) redo_rows<D, POOL>(a, unit.s, seq, unit.h, &s_odd);
+        if (held >= 0) ask();                                  // into the held stage
+        at = to;
+        if (at >= g1) break;
+        next_unit(unit);
+        unit.c = 0;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+
+    // ---- units that cross CTAs: counted, and joined by the CTA that completes them
+    auto parts_of = [&](int i) { return cross[i].s < 0 ? 0 : cross[i].last - cross[i].first + 1; };
+    auto space_of = [&](int i, int b) { return 2 * b + (b == cross[i].first ? 1 : 0); };
+    const int most = max(parts_of(0), parts_of(1));
+    if (most == 0) return;
+    #pragma unroll 1
+    for (int level = most > kFan ? 0 : 1; level < 2; ++level) {
+        // level 0: groups of kFan parts into the group's first place; level 1: the parts, or groups, into the output
+        auto first_of = [&](int i) { return level == 0 ? cross[i].first + (cta - cross[i].first) / kFan * kFan : cross[i].first; };
+        auto count_of = [&](int i) {
+            const int parts = parts_of(i);
+            if (level == 0) return parts > kFan ? min(kFan, cross[i].last + 1 - first_of(i)) : 0;
+            return parts > kFan ? (parts + kFan - 1) / kFan : parts;
+        };
+        __threadfence();
+        __syncthreads();                                       // every row of the CTA's parts is written
+        if (warp < 2 && lane == 0) {
+            const int n = count_of(warp);
+            bool go = n > 0 && (level == 0 || parts_of(warp) <= kFan || s_go[warp]);
+            if (go) {
+                unsigned* ctr = (level == 0 ? x.group_done : x.done) + space_of(warp, first_of(warp));
+                go = atom_add_acq_rel_gpu(ctr, 1u) == static_cast<unsigned>(n - 1);
+                if (go) *ctr = 0;                              // left zero for the next call
+            }
+            s_go[warp] = go;
+        }
+        __syncthreads();
+        #pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+            if (!s_go[i] || count_of(i) == 0) continue;
+            const int n = count_of(i), stride = level == 1 && parts_of(i) > kFan ? kFan : 1, b0 = first_of(i);
+            const QuerySeq seq = query_seq(a, cross[i].s, false);
+            const int rows = seq.n * a.G;
+            for (int e = tid; e < rows * (D / 4); e += kWarps * 32) {
+                const int row = e / (D / 4), c4 = e % (D / 4);
+                float2 ml[kFan];
+                float4 p[kFan];
+                float mm = -CUDART_INF_F, ll = 0.f;
+                #pragma unroll
+                for (int v = 0; v < kFan; ++v) {
+                    ml[v] = make_float2(-CUDART_INF_F, 0.f);
+                    if (v < n) {
+                        const int at_row = space_of(i, b0 + v * stride) * kFewRows + row;
+                        ml[v] = __ldcg(x.part_ml + at_row);
+                        p[v] = __ldcg(reinterpret_cast<const float4*>(x.part_o) + at_row * (D / 4) + c4);
+                    }
+                }
+                #pragma unroll
+                for (int v = 0; v < kFan; ++v) mm = fmaxf(mm, ml[v].x);
+                const float off = mm == -CUDART_INF_F ? 0.f : mm;
+                float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+                #pragma unroll
+                for (int v = 0; v < kFan; ++v) {
+                    if (v >= n) break;
+                    const float f = ex2_approx(ml[v].x - off);
+                    ll = fmaf(ml[v].y, f, ll);
+                    sum.x = fmaf(p[v].x, f, sum.x);
+                    sum.y = fmaf(p[v].y, f, sum.y);
+                    sum.z = fmaf(p[v].z, f, sum.z);
+                    sum.w = fmaf(p[v].w, f, sum.w);
+                }
+                if (level == 1) {
+                    if (!store_quarter<D>(a, seq, cross[i].h, row, c4, sum, ll)) atomicOr(&s_odd, 1u << row);
+                } else {
+                    // (the group's first place: each thread replaces what it alone has read, but for (m, l))
+                    const int at_row = space_of(i, b0) * kFewRows + row;
+                    reinterpret_cast<float4*>(x.part_o)[at_row * (D / 4) + c4] = sum;
+                    s_ml[i * kFewRows + row] = make_float2(mm, ll);
+                }
+            }
+            __syncthreads();
+            if (level == 0 && tid < rows) x.part_ml[space_of(i, b0) * kFewRows + tid] = s_ml[i * kFewRows + tid];
+            if (level == 1 && s_odd) redo_rows<D, POOL>(a, cross[i].s, seq, cross[i].h, &s_odd);
+        }
+    }
+}
+
+template <typename C>
+int launch_few_typed(const kv_pool* pool, const FewArgs& x, int ctas, bool pdl, cudaStream_t stream) {
+    static unsigned long long attr_done = 0;               // the shared-memory opt-in is a per-device attribute
+    const unsigned long long bit = 1ull << (pool->device & 63);
+    if (!(attr_done & bit)) {
+        if (cudaFuncSetAttribute(query_few_kernel<C::D, C::POOL>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
+            cudaSuccess)
+            return KV_ERR_CUDA;
+        attr_done |= bit;
+    }
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    for (int s0 = 0; s0 < x.a.batch; s0 += kFewSeqs) {
+        FewArgs y = x;                                     // (rows of q and out are found through query_start)
+        y.a.batch = x.a.batch - s0 < kFewSeqs ? x.a.batch - s0 : kFewSeqs;
+        y.a.query_start += s0;
+        y.a.lens += s0;
+        y.a.tables += static_cast<int64_t>(s0) * x.a.max_blocks;
+        cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+        if (cudaLaunchKernelEx(&cfg, query_few_kernel<C::D, C::POOL>, y) != cudaSuccess) {
+            cudaGetLastError();
+            return KV_ERR_CUDA;
+        }
+    }
+    return KV_OK;
+}
+
+template <kv_dtype POOL>
+int launch_few_pool(const kv_pool* pool, const FewArgs& x, int ctas, bool pdl, cudaStream_t stream) {
+    return pool->desc.head_dim == 128 ? launch_few_typed<FewCfg<128, POOL>>(pool, x, ctas, pdl, stream)
+                                      : launch_few_typed<FewCfg<64, POOL>>(pool, x, ctas, pdl, stream);
+}
+
+}  // namespace
+}  // namespace kvp

@@ -3,6 +3,7 @@
 
 #include "query_attention.cuh"
 #include "tcgen05.cuh"
+#include "widen.cuh"
 
 namespace kvp {
 
@@ -89,71 +90,6 @@ __device__ __forceinline__ KeyTiles key_tiles(const PromptMisc* m, int block) {
     }
     k.n = max(k.b[0], k.b[1]);
     return k;
-}
-
-// t = cap tanh(x) in log2 units for x = s kx: 1 - 2 / (e^2x + 1), exact to a few 2^-24 of the cap
-__device__ __forceinline__ float capped(float s, float k2, float capl) {
-    const float e = ex2_approx(s * k2);
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e + 1.f));
-    return fmaf(-2.f * capl, r, capl);
-}
-
-// Weights are kept 2^7 above their softmax value relative to the base, which may lag the maximum by up to 2^8:
-// at most 2^15 in float16, and normal ones down to 2^-21 of the largest.
-constexpr float kRaise = 8.f, kLift = 7.f;
-
-// Widen a raw tile (whole blocks of one head, as the pool holds them) to swizzled float16 rows, by 128 threads.
-// Values: rows from `rows` on are zero (they meet weights of zero).  Every conversion is exact.
-template <int D, kv_dtype POOL, bool IS_V>
-__device__ __forceinline__ void widen_tile(const char* raw, char* slot, int rows, int tid) {
-    auto place = [&](int r, int ch) {                          // 16 bytes: 8 elements of a row
-        return reinterpret_cast<uint4*>(slot + (ch >> 3) * (kTile * 128) + r * 128 + ((ch & 7) ^ (r & 7)) * 16);
-    };
-    const uint4 none = make_uint4(0, 0, 0, 0);
-    if constexpr (POOL == KV_FP8_E4M3) {
-        constexpr int PER = D / 16;                            // 16-code pieces of a row
-        #pragma unroll 4
-        for (int u = tid; u < kTile * PER; u += 128) {
-            const int r = u / PER, ch = u % PER * 2;
-            const uint4 v = *reinterpret_cast<const uint4*>(raw + u * 16);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            uint32_t h[8];
-            #pragma unroll
-            for (int k = 0; k < 8; ++k) h[k] = e4m3x2_to_half2_bits(static_cast<uint16_t>(w[k >> 1] >> (16 * (k & 1))));
-            const bool live = !IS_V || r < rows;
-            *place(r, ch) = live ? make_uint4(h[0], h[1], h[2], h[3]) : none;
-            *place(r, ch + 1) = live ? make_uint4(h[4], h[5], h[6], h[7]) : none;
-        }
-    } else if constexpr (!IS_V) {
-        #pragma unroll 4
-        for (int u = tid; u < kTile * (D / 8); u += 128) {
-            const int r = u / (D / 8), ch = u % (D / 8);
-            const char* oct = raw + (r >> 3) * Int4<D>::OCT;
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(oct + int4_k_code<D>(r & 7, ch * 8));
-            const uint32_t sc = *reinterpret_cast<const uint8_t*>(oct + int4_k_scale<D>(r & 7, ch * 8));
-            uint32_t x[4];
-            int4_expand_full(w, (sc << 7) | (sc << 23), x);
-            *place(r, ch) = make_uint4(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410),
-                                       __byte_perm(x[0], x[1], 0x7632), __byte_perm(x[2], x[3], 0x7632));
-        }
-    } else {
-        #pragma unroll 2
-        for (int u = tid; u < kTile / 2 * (D / 8); u += 128) { // 8 elements of two tokens
-            const int r = u / (D / 8) * 2, ch = u % (D / 8);
-            const char* oct = raw + (r >> 3) * Int4<D>::OCT;
-            const uint2 w = *reinterpret_cast<const uint2*>(oct + int4_v_piece<D>(r & 7, ch * 8));
-            const uint32_t sc = *reinterpret_cast<const uint16_t*>(oct + int4_v_scale<D>(r & 7, ch * 8));
-            const uint32_t scales = (sc & 0xFFu) << 7 | (sc & 0xFF00u) << 15;
-            uint32_t x[4], y[4];
-            int4_expand_full(w.x, scales, x);
-            int4_expand_full(w.y, scales, y);
-            *place(r, ch) = r < rows ? make_uint4(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410),
-                                                  __byte_perm(y[0], y[1], 0x5410), __byte_perm(y[2], y[3], 0x5410)) : none;
-            *place(r + 1, ch) = r + 1 < rows ? make_uint4(__byte_perm(x[0], x[1], 0x7632), __byte_perm(x[2], x[3], 0x7632),
-                                                          __byte_perm(y[0], y[1], 0x7632), __byte_perm(y[2], y[3], 0x7632)) : none;
-        }
-    }
 }
 
 template <int D, kv_dtype POOL>
@@ -278,7 +214,7 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
         const float k2 = cap ? 2.f * kLog2e * (a.scale / a.cap) : 0.f, capl = a.cap * kLog2e;
         const float c = cap || bias ? 1.f : qscale;            // scores to log2 units
         const int pos = seq.ctx - seq.n + token;
-        float m = -CUDART_INF_F, l = 0.f;
+        float m = -CUDART_INF_F, l = 0.f;                      // the base (log2 units) and the sum of weights
         int i = 0;                                             // this row tile's key tiles so far
         bool fine = true;
         #pragma unroll 1
@@ -324,10 +260,11 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
             #pragma unroll
             for (int k = 2; k < kTile; k += 2) top = fmaxf(fmaxf(x[k], x[k + 1]), top);
             // the base follows the maximum only when it is left behind by more than 2^8
-            const bool raise = (top - m) * c > kRaise;         // (m -inf: yes, but for a row that sees nothing yet)
+            top *= c;
+            const bool raise = top - m > kRaise;               // (m -inf: yes, but for a row that sees nothing yet)
             float keep = 1.f;
             if (raise) {
-                keep = m == -CUDART_INF_F ? 0.f : ex2_approx((m - top) * c);
+                keep = ex2_approx(m - top);
                 m = top;
                 l *= keep;
             }
@@ -347,7 +284,7 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                     tmem_store32(ot + k, o);
                 }
             }
-            const float off = kLift - (m == -CUDART_INF_F ? 0.f : m * c);
+            const float off = kLift - (m == -CUDART_INF_F ? 0.f : m);
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             const float2 c2 = make_float2(c, c), off2 = make_float2(off, off);
             #pragma unroll
@@ -445,8 +382,11 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                     }
                     const char* from = smem + C::RAW_OFF + raw * C::RAW;
                     char* to = smem + C::KV_OFF + slot * C::TILE;
-                    if (kv == 0) widen_tile<D, POOL, false>(from, to, rows, tid);
-                    else widen_tile<D, POOL, true>(from, to, rows, tid);
+                    auto place = [&](int r, int ch) {          // swizzled 128-byte lines, 64 elements each
+                        return reinterpret_cast<uint4*>(to + (ch >> 3) * (kTile * 128) + r * 128 + ((ch & 7) ^ (r & 7)) * 16);
+                    };
+                    if (kv == 0) widen_rows<D, POOL, false, kTile, 128>(from, 0, rows, tid, place);
+                    else widen_rows<D, POOL, true, kTile, 128>(from, 0, rows, tid, place);
                     fence_async_shared();
                     __syncwarp();
                     if (lane == 0) {
