@@ -69,12 +69,15 @@ void make_row_maps(kv_pool* p) {
     void* raw = std::malloc(2 * d.num_layers * sizeof(CUtensorMap) + 64);
     if (!raw) return;
     CUtensorMap* maps = reinterpret_cast<CUtensorMap*>((reinterpret_cast<uintptr_t>(raw) + 63) & ~uintptr_t(63));
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(d.head_dim),
-                                static_cast<cuuint64_t>(d.num_blocks) * d.num_heads * d.block_size};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(d.head_dim) * 2};
-    const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(d.block_size)}, estr[2] = {1, 1};
+    // A block of one head in one copy.  Eight rows of 64 elements are a swizzled unit of 1 KB, and its place in shared
+    // memory is [8-row group][64-element half]: a key tile's groups lie at one stride whatever the blocks.
+    const cuuint64_t rows = static_cast<cuuint64_t>(d.num_blocks) * d.num_heads * d.block_size;
+    const cuuint64_t halves = d.head_dim / 64, row = static_cast<cuuint64_t>(d.head_dim) * 2;
+    const cuuint64_t dims[4] = {64, 8, halves, rows / 8}, strides[3] = {row, 128, 8 * row};
+    const cuuint32_t box[4] = {64, 8, static_cast<cuuint32_t>(halves), static_cast<cuuint32_t>(d.block_size / 8)};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
     for (int i = 0; i < 2 * d.num_layers; ++i)
-        if (encode(&maps[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, (i & 1 ? p->v_layers : p->k_layers)[i / 2], dims, strides,
+        if (encode(&maps[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, (i & 1 ? p->v_layers : p->k_layers)[i / 2], dims, strides,
                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS) {
             std::free(raw);

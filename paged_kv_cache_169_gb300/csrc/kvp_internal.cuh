@@ -25,8 +25,8 @@ struct kv_pool {
     // head-pair stages: fp16 pools with B <= 16 and FP8 pools; nullptr otherwise
     CUtensorMap* pmaps;  // [2 * num_layers]
     void* tmaps_raw;
-    // fp16 pools: per layer K and V viewed as [num_blocks*H*B][head_dim] with boxes of 64 elements
-    // by a block's B rows of one head, 128-byte swizzle (paged_query_attention)
+    // fp16 pools: per layer K and V viewed as [num_blocks*H*B / 8][head_dim / 64][8][64] with boxes of a
+    // block of one head, 128-byte swizzle (paged_query_attention)
     CUtensorMap* rmaps;  // [2 * num_layers], 64-byte aligned
     void* rmaps_raw;
 };
@@ -187,6 +187,14 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int 
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%2, %3, %4}], [%5];"
         ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, int x, int y, int z, int w, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
         : "memory");
 }
 

@@ -8,7 +8,7 @@
 namespace kvp {
 
 struct PromptArgs {
-    CUtensorMap kmap, vmap;            // float16 pools: the layer as [rows][D], boxes of 64 elements by a block
+    CUtensorMap kmap, vmap;            // float16 pools: the layer's row maps, a block of one head per copy
     QueryArgs a;
     int tiles;                         // pairs of row tiles per (sequence, K/V head)
 };
@@ -27,7 +27,8 @@ struct PromptCfg {
     static constexpr int D = D_;
     static constexpr kv_dtype POOL = POOL_;
     static constexpr bool WIDEN = POOL != KV_F16;              // tiles are widened to float16 on their way
-    static constexpr int HALVES = D / 64;                      // 64-element (128-byte) columns of a tile
+    static constexpr int HALVES = D / 64;                      // 64-element (128-byte) columns of a tile: a tile
+    // is [16 groups of 8 rows][HALVES][8][128 bytes], 128-byte swizzled
     static constexpr int TILE = HALVES * kTile * 128;          // bytes of 128 rows as float16
     // key and value tiles in flight as float16, and as stored
     static constexpr int SLOTS = D == 128 ? (WIDEN ? 4 : 5) : 8;
@@ -57,6 +58,16 @@ template <int N> __device__ __forceinline__ void fewer_registers() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// Byte offset of 16 bytes (8 elements, the ch-th of a row) in a tile.
+template <int HALVES>
+__device__ __forceinline__ uint32_t tile_at(int r, int ch) {
+    return (((r >> 3) * HALVES + (ch >> 3)) << 10) + ((r & 7) << 7) + (((ch & 7) ^ (r & 7)) << 4);
+}
+
+// The warp's first lane's value.  The compiler knows the result to be the same in every lane, so branches on it
+// keep a warp together and operands made of it may be uniform registers, as the matrix instructions' must be.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // A bounded wait by a whole warp: all of its lanes go on, or none.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* err) {
     return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, err));
@@ -80,13 +91,14 @@ struct KeyTiles {
 };
 __device__ __forceinline__ KeyTiles key_tiles(const PromptMisc* m, int block) {
     KeyTiles k;
-    k.base = min(m->lo[0], m->lo[1]) & -block;
-    k.end = max(m->hi[0], m->hi[1]);
+    const int lo[2] = {uniform(m->lo[0]), uniform(m->lo[1])}, hi[2] = {uniform(m->hi[0]), uniform(m->hi[1])};
+    k.base = min(lo[0], lo[1]) & -block;
+    k.end = max(hi[0], hi[1]);
     #pragma unroll
     for (int t = 0; t < 2; ++t) {
-        const bool some = m->lo[t] < m->hi[t];
-        k.a[t] = some ? (m->lo[t] - k.base) / kTile : 0;
-        k.b[t] = some ? (m->hi[t] - k.base + kTile - 1) / kTile : 0;
+        const bool some = lo[t] < hi[t];
+        k.a[t] = some ? (lo[t] - k.base) / kTile : 0;
+        k.b[t] = some ? (hi[t] - k.base + kTile - 1) / kTile : 0;
     }
     k.n = max(k.b[0], k.b[1]);
     return k;
@@ -101,7 +113,7 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
     const uint32_t base32 = smem_u32(smem);
     PromptMisc* const misc = reinterpret_cast<PromptMisc*>(smem + C::MISC_OFF);
     const QueryArgs& a = p.a;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     auto bar = [&](int i) { return base32 + C::BAR_OFF + 8 * i; };
     auto full = [&](int slot) { return bar(slot); };
     auto empty = [&](int slot) { return bar(C::SLOTS + slot); };
@@ -120,7 +132,8 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
     // the work item: later row tiles, which see more keys, first
     const int item = blockIdx.x;
     const int tile = p.tiles - 1 - item % p.tiles, head = item / p.tiles % a.H, s = item / p.tiles / a.H;
-    const QuerySeq seq = query_seq(a, s, threadIdx.x == 0 && tile == 0 && head == 0);
+    QuerySeq seq = query_seq(a, s, threadIdx.x == 0 && tile == 0 && head == 0);
+    seq = QuerySeq{uniform(seq.first), uniform(seq.n), uniform(seq.ctx)};
     const int per_tile = kTile / a.G;                          // tokens of a row tile
     if (tile * 2 * per_tile >= seq.n) return;
 
@@ -168,7 +181,7 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = misc->tmem;
+    const uint32_t tmem = uniform(misc->tmem);
     const KeyTiles keys = key_tiles(misc, a.B);
     const int first_tile = keys.next(0);
 
@@ -178,14 +191,21 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
         constexpr int CHUNKS = D / 8;                          // 16-byte pieces of a row
         char* const qt = smem + C::Q_OFF + rt * C::TILE;
         const int64_t q0 = static_cast<int64_t>(seq.first) * a.q_stride + static_cast<int64_t>(head) * a.G * D * 2;
-        #pragma unroll 4
-        for (int it = 0; it < CHUNKS; ++it) {                  // the warp's 32 rows, neighbouring pieces side by side
+        // the warp's 32 rows, neighbouring pieces side by side; every load asked for before the first is stored
+        uint4 qv[CHUNKS];
+        const int log_g = __ffs(a.G) - 1;
+        #pragma unroll
+        for (int it = 0; it < CHUNKS; ++it) {
             const int u = it * 32 + lane, r = (warp & 3) * 32 + u / CHUNKS, c = u % CHUNKS;
-            const int tok = (tile * 2 + rt) * per_tile + r / a.G;
-            uint4 v = make_uint4(0, 0, 0, 0);
+            const int tok = (tile * 2 + rt) * per_tile + (r >> log_g);
+            qv[it] = make_uint4(0, 0, 0, 0);
             if (tok < seq.n)
-                v = *reinterpret_cast<const uint4*>(a.q + q0 + tok * a.q_stride + (r % a.G) * (D * 2) + c * 16);
-            *reinterpret_cast<uint4*>(qt + (c >> 3) * (kTile * 128) + r * 128 + ((c & 7) ^ (r & 7)) * 16) = v;
+                qv[it] = *reinterpret_cast<const uint4*>(a.q + q0 + tok * a.q_stride + (r & (a.G - 1)) * (D * 2) + c * 16);
+        }
+        #pragma unroll
+        for (int it = 0; it < CHUNKS; ++it) {
+            const int u = it * 32 + lane, r = (warp & 3) * 32 + u / CHUNKS, c = u % CHUNKS;
+            *reinterpret_cast<uint4*>(qt + tile_at<C::HALVES>(r, c)) = qv[it];
         }
         fence_async_shared();
         __syncwarp();
@@ -336,20 +356,25 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                     w[y] = *reinterpret_cast<const uint32_t*>(&hv);
                 }
                 const int ch = (k + e) >> 3;
-                *reinterpret_cast<uint4*>(qt + (ch >> 3) * (kTile * 128) + row * 128 + ((ch & 7) ^ (row & 7)) * 16) =
+                *reinterpret_cast<uint4*>(qt + tile_at<C::HALVES>(row, ch)) =
                     make_uint4(w[0], w[1], w[2], w[3]);
             }
         }
         __syncwarp();
         if (fine) {
             const int64_t o0 = static_cast<int64_t>(seq.first) * a.out_stride + static_cast<int64_t>(head) * a.G * D * 2;
-            #pragma unroll 4
+            uint4 ov[CHUNKS];
+            #pragma unroll
             for (int it = 0; it < CHUNKS; ++it) {
                 const int u = it * 32 + lane, r = (warp & 3) * 32 + u / CHUNKS, ch = u % CHUNKS;
-                const int tok = (tile * 2 + rt) * per_tile + r / a.G;
-                if (tok >= seq.n) continue;
-                *reinterpret_cast<uint4*>(a.out + o0 + tok * a.out_stride + (r % a.G) * (D * 2) + ch * 16) =
-                    *reinterpret_cast<const uint4*>(qt + (ch >> 3) * (kTile * 128) + r * 128 + ((ch & 7) ^ (r & 7)) * 16);
+                ov[it] = *reinterpret_cast<const uint4*>(qt + tile_at<C::HALVES>(r, ch));
+            }
+            #pragma unroll
+            for (int it = 0; it < CHUNKS; ++it) {
+                const int u = it * 32 + lane, r = (warp & 3) * 32 + u / CHUNKS, ch = u % CHUNKS;
+                const int tok = (tile * 2 + rt) * per_tile + (r >> log_g);
+                if (tok < seq.n)
+                    *reinterpret_cast<uint4*>(a.out + o0 + tok * a.out_stride + (r & (a.G - 1)) * (D * 2) + ch * 16) = ov[it];
             }
             // A key or value that is not finite reaches, as 0 * NaN, rows that do not see it: a row that came out
             // so is worked out again from the definition, which reads only what it sees.
@@ -382,9 +407,7 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                     }
                     const char* from = smem + C::RAW_OFF + raw * C::RAW;
                     char* to = smem + C::KV_OFF + slot * C::TILE;
-                    auto place = [&](int r, int ch) {          // swizzled 128-byte lines, 64 elements each
-                        return reinterpret_cast<uint4*>(to + (ch >> 3) * (kTile * 128) + r * 128 + ((ch & 7) ^ (r & 7)) * 16);
-                    };
+                    auto place = [&](int r, int ch) { return reinterpret_cast<uint4*>(to + tile_at<C::HALVES>(r, ch)); };
                     if (kv == 0) widen_rows<D, POOL, false, kTile, 128>(from, 0, rows, tid, place);
                     else widen_rows<D, POOL, true, kTile, 128>(from, 0, rows, tid, place);
                     fence_async_shared();
@@ -400,79 +423,86 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
         fewer_registers<C::REGS_ISSUE>();
     }
     if (warp == kMmaWarp) {
-        // ======== matrix products: one thread
-        if (lane == 0) {
-            constexpr uint32_t s_shape = tc_idesc(kTile, false), o_shape = tc_idesc(D, true);
-            int n[2] = {0, 0}, ring = 0;                       // products issued per row tile; tiles taken
-            bool fine = true;
-            auto wait = [&](uint32_t b, uint32_t parity) { fine = fine && mbar_wait_bounded(b, parity, a.err); };
-            auto scores = [&](int t, uint32_t slot) {          // S = Q K^T
+        // ======== matrix products: the warp stays together, one lane issues
+        constexpr uint32_t s_shape = tc_idesc(kTile, false), o_shape = tc_idesc(D, true);
+        int n[2] = {0, 0};                                     // products of weights issued per row tile
+        int slot = 0, phase = 0;                               // the ring's next tile
+        bool fine = true;
+        auto wait = [&](uint32_t b, uint32_t parity) { fine = fine && warp_wait(b, parity, a.err); };
+        auto tile_desc = [&](int at, uint32_t lead) { return tc_desc(base32 + C::KV_OFF + at * C::TILE, lead, C::HALVES * 1024); };
+        const uint64_t q_desc = tc_desc(base32 + C::Q_OFF, 0, C::HALVES * 1024);
+        auto scores = [&](int t, uint64_t k_desc, uint32_t then) {     // S = Q K^T; then: the keys' release, or 0
+            if (elect_one()) {
                 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t at = (k >> 2) * (kTile * 128) + (k & 3) * 32;
-                    tc_mma_ss(tmem + t * kTile, tc_desc(base32 + C::Q_OFF + t * C::TILE + at, 0, 1024),
-                              tc_desc(slot + at, 0, 1024), s_shape, k > 0);
+                    const int at = ((k >> 2) * 1024 + (k & 3) * 32) >> 4;
+                    tc_mma_ss(tmem + t * kTile, q_desc + t * (C::TILE >> 4) + at, k_desc + at, s_shape, k > 0);
                 }
                 tc_commit(s_there(t));
-            };
-            auto slot_at = [&](int r) { return base32 + C::KV_OFF + (r % C::SLOTS) * C::TILE; };
-            int j = first_tile;
-            if (j < keys.n) {
-                wait(full(0), 0);
-                for (int t = 0; t < 2; ++t) {
-                    if (!keys.on(t, j)) continue;
-                    wait(q_there(t), 0);
-                    if (fine) scores(t, slot_at(0));
-                }
-                if (fine) tc_commit(empty(0));
-                ring = 1;
+                if (then) tc_commit(then);
             }
-            bool asked[2] = {keys.on(0, j), keys.on(1, j)};    // the queries were waited for
-            #pragma unroll 1
-            while (fine && j < keys.n) {
-                const int jn = keys.next(j + 1);
-                const int v = ring, kn = ring + 1;             // places of this tile's values, of the next one's keys
-                wait(full(v % C::SLOTS), v / C::SLOTS & 1);
-                bool have_keys = false;
-                #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if (keys.on(t, j)) {
-                        wait(w_there(t), n[t] & 1);
-                        if (!fine) break;
-                        tc_fence_after();
+            __syncwarp();
+        };
+        auto take = [&]() {                                    // the ring's next tile: waited for; its place
+            const int at = slot;
+            wait(full(at), phase);
+            if (++slot == C::SLOTS) {
+                slot = 0;
+                phase ^= 1;
+            }
+            return at;
+        };
+        int j = first_tile;
+        if (j < keys.n) {
+            const int at = take();
+            #pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (!keys.on(t, j)) continue;
+                wait(q_there(t), 0);
+                if (fine) scores(t, tile_desc(at, 0), t == 1 || !keys.on(1, j) ? empty(at) : 0);
+            }
+        }
+        #pragma unroll 1
+        while (fine && j < keys.n) {
+            const int jn = keys.next(j + 1);
+            const int v_at = take();
+            int k_at = -1;
+            const uint64_t v_desc = tile_desc(v_at, 1024);
+            #pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (keys.on(t, j)) {
+                    wait(w_there(t), n[t] & 1);
+                    if (!fine) break;
+                    tc_fence_after();
+                    if (elect_one()) {
                         #pragma unroll
                         for (int k = 0; k < kTile / 16; ++k)   // O += W V
-                            tc_mma_ts(tmem + 2 * kTile + t * D, tmem + t * kTile + k * 8,
-                                      tc_desc(slot_at(v) + k * 2048, kTile * 128, 1024), o_shape, n[t] > 0 || k > 0);
+                            tc_mma_ts(tmem + 2 * kTile + t * D, tmem + t * kTile + k * 8, v_desc + k * (C::HALVES * 2048 >> 4),
+                                      o_shape, n[t] > 0 || k > 0);
                         tc_commit(o_there(t));
-                        ++n[t];
+                        if (t == 1 || !keys.on(1, j)) tc_commit(empty(v_at));
                     }
-                    if (t == 1) tc_commit(empty(v % C::SLOTS));
-                    if (jn < keys.n && keys.on(t, jn)) {
-                        if (!have_keys) wait(full(kn % C::SLOTS), kn / C::SLOTS & 1);
-                        have_keys = true;
-                        if (!asked[t]) wait(q_there(t), 0);
-                        asked[t] = true;
-                        if (!fine) break;
-                        scores(t, slot_at(kn));
-                    }
+                    __syncwarp();
+                    ++n[t];
                 }
-                if (fine && jn < keys.n) tc_commit(empty(kn % C::SLOTS));
-                ring += 2;
-                j = jn;
+                if (jn < keys.n && keys.on(t, jn)) {
+                    if (k_at < 0) k_at = take();
+                    wait(q_there(t), 0);
+                    if (!fine) break;
+                    scores(t, tile_desc(k_at, 0), t == 1 || !keys.on(1, jn) ? empty(k_at) : 0);
+                }
             }
-            tc_commit(done);                                   // nothing of this thread's is in flight at the end
-            mbar_wait_bounded(done, 0, a.err);
+            j = jn;
         }
+        if (elect_one()) tc_commit(done);                      // nothing of it is in flight at the end
         __syncwarp();
+        warp_wait(done, 0, a.err);
     } else if (warp == kLoadWarp) {
-        // ======== keys and values in: float16 straight to their place, a lane per (block, 64 elements) of a tile;
-        // others as stored, a lane per block
-        constexpr int LPB = C::WIDEN ? 1 : C::HALVES;
+        // ======== keys and values in: a lane per block; float16 straight to its place, others as stored
         constexpr int DEPTH = C::WIDEN ? C::RAWS : C::SLOTS;
         auto there = [&](int i) { return C::WIDEN ? raw_full(i) : full(i); };
         auto gone = [&](int i) { return C::WIDEN ? raw_empty(i) : empty(i); };
-        const int log_b = a.log_b, blk = lane / LPB, half = lane % LPB;
+        const int log_b = a.log_b, blk = lane;
         int ring = 0, edges = 0;
         bool fine = true;
         #pragma unroll 1
@@ -480,8 +510,8 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
             const int j0 = keys.base + j * kTile, rows = min(kTile, keys.end - j0);
             const bool mine = (blk << log_b) < rows;
             const int id = mine ? query_block(a, s, j0 + (blk << log_b)) : 0;
-            const uint32_t block_bytes = C::WIDEN ? a.B * kRowBytes<D, POOL> : a.B * 128;
-            const uint32_t bytes = ((rows + a.B - 1) >> log_b) * LPB * block_bytes;
+            const uint32_t block_bytes = C::WIDEN ? a.B * kRowBytes<D, POOL> : a.B * D * 2;
+            const uint32_t bytes = ((rows + a.B - 1) >> log_b) * block_bytes;
             if constexpr (POOL == KV_FP8_E4M3) {
                 if (blk < 16) {
                     factors[(j % kFactorTiles) * 32 + blk] = mine ? a.kscale[id] : 0.f;
@@ -506,18 +536,16 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                         bulk_g2s(base32 + C::RAW_OFF + slot * C::RAW + blk * block_bytes, (kv ? a.vpool : a.kpool) + from,
                                  block_bytes, b);
                     } else {
-                        tma_load_2d(base32 + C::KV_OFF + slot * C::TILE + half * (kTile * 128) + (blk << log_b) * 128,
-                                    kv ? &p.vmap : &p.kmap, half * 64, (id * a.H + head) << log_b, b);
+                        tma_load_4d(base32 + C::KV_OFF + slot * C::TILE + blk * block_bytes, kv ? &p.vmap : &p.kmap, 0, 0, 0,
+                                    (id * a.H + head) << (log_b - 3), b);
                     }
                 }
                 if (tail) {
                     fine = warp_wait(edge, edges++ & 1, a.err);
                     #pragma unroll 1
-                    for (int u = rows * 8 + lane; u < kTile * 8; u += 32)
-                        #pragma unroll
-                        for (int h = 0; h < C::HALVES; ++h)
-                            *reinterpret_cast<uint4*>(smem + C::KV_OFF + slot * C::TILE + h * (kTile * 128) + u * 16) =
-                                make_uint4(0, 0, 0, 0);
+                    for (int u = rows * (D / 8) + lane; u < kTile * (D / 8); u += 32)
+                        *reinterpret_cast<uint4*>(smem + C::KV_OFF + slot * C::TILE + tile_at<C::HALVES>(u / (D / 8), u % (D / 8))) =
+                            make_uint4(0, 0, 0, 0);
                     fence_async_shared();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(full(slot));
