@@ -45,12 +45,8 @@ bool valid_stride(int64_t stride, int64_t row, int elem_bytes) {
     return stride >= row && stride < (int64_t{1} << 28) && stride * elem_bytes % 16 == 0;
 }
 
-using TensorMapEncode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                     const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                     CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
 // The driver's tensor-map encoder, or null.
-TensorMapEncode tensor_map_encoder() {
+kvp::TensorMapEncode tensor_map_encoder() {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult q;
     if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
@@ -58,14 +54,14 @@ TensorMapEncode tensor_map_encoder() {
         cudaGetLastError();
         return nullptr;
     }
-    return reinterpret_cast<TensorMapEncode>(fn);
+    return reinterpret_cast<kvp::TensorMapEncode>(fn);
 }
 
 // Row maps of an fp16 pool (kv_pool::rmaps); left null where the encoder is missing or refuses.
 void make_row_maps(kv_pool* p) {
     const kv_pool_desc& d = p->desc;
-    const TensorMapEncode encode = d.dtype == KV_F16 ? tensor_map_encoder() : nullptr;
-    if (!encode) return;
+    const kvp::TensorMapEncode encode = reinterpret_cast<kvp::TensorMapEncode>(p->encode);
+    if (!encode || d.dtype != KV_F16) return;
     void* raw = std::malloc(2 * d.num_layers * sizeof(CUtensorMap) + 64);
     if (!raw) return;
     CUtensorMap* maps = reinterpret_cast<CUtensorMap*>((reinterpret_cast<uintptr_t>(raw) + 63) & ~uintptr_t(63));
@@ -97,7 +93,7 @@ void make_tensor_maps(kv_pool* p) {
     const kv_pool_desc& d = p->desc;
     const bool fp8 = d.dtype == KV_FP8_E4M3;
     if (d.head_dim != 128 || (d.dtype != KV_F16 && !fp8)) return;
-    const TensorMapEncode encode = tensor_map_encoder();
+    const kvp::TensorMapEncode encode = reinterpret_cast<kvp::TensorMapEncode>(p->encode);
     if (!encode) return;
     const int L = d.num_layers;
     void* raw = std::malloc(4 * L * sizeof(CUtensorMap) + 64);
@@ -211,6 +207,7 @@ int kv_pool_create(const kv_pool_desc* desc, void* const* k_layers, void* const*
         free_pool(p);
         return KV_ERR_CUDA;
     }
+    p->encode = reinterpret_cast<void*>(tensor_map_encoder());
     make_tensor_maps(p);
     make_row_maps(p);
     *out = p;

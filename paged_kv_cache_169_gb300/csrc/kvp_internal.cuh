@@ -29,9 +29,14 @@ struct kv_pool {
     // block of one head, 128-byte swizzle (paged_query_attention)
     CUtensorMap* rmaps;  // [2 * num_layers], 64-byte aligned
     void* rmaps_raw;
+    void* encode;        // the driver's tensor-map encoder (TensorMapEncode), or nullptr
 };
 
 namespace kvp {
+
+using TensorMapEncode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                     const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                     CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 inline int elem_bytes(kv_dtype t) { return t == KV_F32 ? 4 : (t == KV_F16 ? 2 : 1); }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

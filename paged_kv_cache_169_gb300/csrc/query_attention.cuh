@@ -32,6 +32,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 #ifdef __CUDACC__
 
+// 16 bytes global -> shared, or zeros (nothing is read)
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const char* src, bool read) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(read ? 16 : 0) : "memory");
+}
+
 // A sequence's rows of q (first, n) and its context; n 0 where it is left out.
 struct QuerySeq { int first, n, ctx; };
 

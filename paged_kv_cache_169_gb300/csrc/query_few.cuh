@@ -62,10 +62,7 @@ struct FewCfg {
     static_assert(STAGES >= 2 && STAGE % 16 == 0 && WARP % 16 == 0, "ring");
 };
 
-// 16 bytes global -> shared, or zeros (nothing is read)
-__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const char* src, bool read) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(read ? 16 : 0) : "memory");
-}
+// 4 bytes global -> shared, or zeros (nothing is read)
 __device__ __forceinline__ void cp_async4_or_zero(uint32_t dst, const void* src, bool read) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(read ? 4 : 0) : "memory");
 }
