@@ -11,7 +11,8 @@ struct PromptArgs {
     CUtensorMap qmap;                  // [num_tokens][heads][D / 64][64], boxes of a row tile's 64-element halves
     CUtensorMap kmap, vmap;            // float16 pools: the layer's row maps, a block of one head per copy
     QueryArgs a;
-    int tiles;                         // pairs of row tiles per (sequence, K/V head)
+    int tiles;                         // pairs of row tiles per unit (sequence, K/V head)
+    int group;                         // units whose items come together
 };
 
 int launch_query_prompt_fp8(const kv_pool* pool, const PromptArgs& p, bool pdl, cudaStream_t stream);
@@ -310,45 +311,19 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                     for (int k = 0; k < kTile; ++k)
                         if (static_cast<unsigned>(k - from) >= len) x[k] = -CUDART_INF_F;
                 }
-                float tops[4];
-                #pragma unroll
-                for (int k = 0; k < 4; ++k) tops[k] = max3(x[3 * k], x[3 * k + 1], x[3 * k + 2]);
-                #pragma unroll
-                for (int k = 12; k < kTile; k += 2) tops[(k >> 1) & 3] = max3(x[k], x[k + 1], tops[(k >> 1) & 3]);
-                const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * c;
-                // the base follows the maximum only when it is left behind by more than 2^8
-                const bool raise = top - m > kRaise;           // (m -inf: yes, but for a row that sees nothing yet)
-                float keep = 1.f;
-                if (raise) {
-                    keep = ex2_approx(m - top);
-                    m = top;
-                    l *= keep;
-                }
-                if (i > i0 && __any_sync(0xffffffffu, raise)) {
-                    if (!wait(o_there(rt), i - 1)) break;
-                    tc_fence_after();
-                    #pragma unroll 1
-                    for (int k = 0; k < D; k += 32) {
-                        uint32_t o[32];
-                        tmem_load32(ot + k, o);
-                        tmem_wait_load32(o);
-                        #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
-                        tmem_store32(ot + k, o);
-                    }
-                }
-                const float off = kLift - (m == -CUDART_INF_F ? 0.f : m);
-                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                const float2 c2 = make_float2(c, c), off2 = make_float2(off, off);
-                #pragma unroll
-                for (int h = 0; h < 2; ++h) {                  // the first half's products begin while the second's are made
-                    uint32_t w[32];
+                // Weights of the h-th half of the keys at the base m, their sums per pair of columns in `sum`.
+                const float2 c2 = make_float2(c, c);
+                float2 sum[2];
+                uint32_t w[32];
+                auto weigh = [&](int h) {
+                    const float off = kLift - (m == -CUDART_INF_F ? 0.f : m);
+                    const float2 off2 = make_float2(off, off);
                     #pragma unroll
                     for (int k = 0; k < 32; ++k) {
                         float2 y = __ffma2_rn(make_float2(x[64 * h + 2 * k], x[64 * h + 2 * k + 1]), c2, off2);
                         y.x = ex2_approx(y.x);
                         y.y = ex2_approx(y.y);
-                        sum[k & 1] = __fadd2_rn(sum[k & 1], y);
+                        sum[k & 1] = h == 0 && k < 2 ? y : __fadd2_rn(sum[k & 1], y);
                         if constexpr (POOL == KV_FP8_E4M3) {
                             const float f = scales[16 + ((64 * h + 2 * k) >> a.log_b)] * inv_vref;
                             y = __fmul2_rn(y, make_float2(f, f));
@@ -356,12 +331,49 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                         const __half2 hv = __floats2half2_rn(y.x, y.y);
                         w[k] = *reinterpret_cast<const uint32_t*>(&hv);
                     }
+                };
+                auto hand_over = [&](int h) {
                     tmem_store32(st + 32 * h, w);
                     tmem_wait_store();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(w_there(rt, h));
+                };
+                // The first half is weighed at the old base while the maximum is found: the base follows it only when
+                // it is left behind by more than 2^8, which is rare after the first tile.
+                weigh(0);
+                float tops[4];
+                #pragma unroll
+                for (int k = 0; k < 4; ++k) tops[k] = max3(x[3 * k], x[3 * k + 1], x[3 * k + 2]);
+                #pragma unroll
+                for (int k = 12; k < kTile; k += 2) tops[(k >> 1) & 3] = max3(x[k], x[k + 1], tops[(k >> 1) & 3]);
+                const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * c;
+                const bool raise = top - m > kRaise;           // (m -inf: yes, but for a row that sees nothing yet)
+                if (__any_sync(0xffffffffu, raise)) {
+                    float keep = 1.f;
+                    if (raise) {
+                        keep = ex2_approx(m - top);
+                        m = top;
+                        l *= keep;
+                    }
+                    if (i > i0) {
+                        if (!wait(o_there(rt), i - 1)) break;
+                        tc_fence_after();
+                        #pragma unroll 1
+                        for (int k = 0; k < D; k += 32) {
+                            uint32_t o[32];
+                            tmem_load32(ot + k, o);
+                            tmem_wait_load32(o);
+                            #pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+                            tmem_store32(ot + k, o);
+                        }
+                    }
+                    weigh(0);
                 }
+                hand_over(0);                                  // its products begin while the second half is weighed
+                weigh(1);
+                hand_over(1);
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             }
             if (!fine || (i > i0 && !wait(o_there(rt), i - 1))) break;
@@ -372,12 +384,15 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
             const QuerySeq seq{it.first, it.n, it.ctx};
             const bool some = i > i0 && l != 0.f, live = token < it.n;
             const float inv = l == 0.f ? 0.f : it.vref / l;
+            const float2 inv2 = make_float2(inv, inv);
             char* const out = smem + C::OUT_OFF + warp * (32 * 128);
-            bool odd = false;                                  // something is not finite
+            char* const to = a.out + static_cast<int64_t>(it.first + it.token + rt * per_tile) * a.out_stride +
+                             it.head * a.G * (D * 2) + (lane & 7) * 16;
+            const int left = it.n - it.token - rt * per_tile;  // tokens of the row tile
+            float2 odd = make_float2(0.f, 0.f);                // NaN: something was not finite
             #pragma unroll 1
             for (int half = 0; half < C::HALVES; ++half) {
-                float top = 0.f;
-                #pragma unroll 1
+                #pragma unroll
                 for (int part = 0; part < 2; ++part) {
                     uint32_t o[32];                            // (without a key tile: whatever is there, not used)
                     tmem_load32(ot + half * 64 + part * 32, o);
@@ -387,17 +402,15 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                         uint32_t w[4];
                         #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            float2 f = make_float2(__uint_as_float(o[8 * ch + 2 * e]) * inv, __uint_as_float(o[8 * ch + 2 * e + 1]) * inv);
-                            if (!some) f = make_float2(0.f, 0.f);
-                            top = max_nan(top, max_nan(fabsf(f.x), fabsf(f.y)));
+                            float2 f = __fmul2_rn(make_float2(__uint_as_float(o[8 * ch + 2 * e]), __uint_as_float(o[8 * ch + 2 * e + 1])), inv2);
+                            odd = __ffma2_rn(f, make_float2(0.f, 0.f), odd);
                             const __half2 hv = __floats2half2_rn(f.x, f.y);
-                            w[e] = *reinterpret_cast<const uint32_t*>(&hv);
+                            w[e] = some ? *reinterpret_cast<const uint32_t*>(&hv) : 0u;
                         }
                         *reinterpret_cast<uint4*>(out + lane * 128 + (((part * 4 + ch) ^ (lane & 7)) << 4)) =
                             make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
-                odd |= !(top < CUDART_INF_F);
                 __syncwarp();
                 uint4 v[8];
                 #pragma unroll
@@ -407,17 +420,16 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                 }
                 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    const int r = (warp & 3) * 32 + k * 4 + (lane >> 3), tok = it.token + rt * per_tile + (r >> log_g);
-                    if (tok < it.n)
-                        *reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(it.first + tok) * a.out_stride +
-                                                  (it.head * a.G + (r & (a.G - 1))) * (D * 2) + half * 128 + (lane & 7) * 16) = v[k];
+                    const int r = (warp & 3) * 32 + k * 4 + (lane >> 3), tok = r >> log_g;
+                    if (tok < left)
+                        *reinterpret_cast<uint4*>(to + tok * a.out_stride + (r & (a.G - 1)) * (D * 2) + half * 128) = v[k];
                 }
                 __syncwarp();
             }
             tc_fence_before();
             // A key or value that is not finite reaches, as 0 * NaN, rows that do not see it: a row that came out so
             // is worked out again from the definition, which reads only what it sees.
-            unsigned again = __ballot_sync(0xffffffffu, odd && live);
+            unsigned again = __ballot_sync(0xffffffffu, some && live && !(odd.x + odd.y == 0.f));
             #pragma unroll 1
             while (again) {
                 const int r = (warp & 3) * 32 + __ffs(again) - 1;
@@ -484,29 +496,34 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                 if (!spin(q_there(t), count++)) break;
                 const int i0 = i;
                 int j = keys.next(0);
-                if (j < keys.n) spin(full(ring.slot), ring.times);
-                #pragma unroll 1
-                while (fine && j < keys.n) {
-                    const bool on = keys.on(t, j);
-                    const int jn = keys.next(j + 1);
-                    if (on) {                                  // S = Q K^T
-                        const uint64_t k_desc = tc_desc(base32 + C::KV_OFF + ring.slot * C::TILE, 0, C::HALVES * 1024);
-                        #pragma unroll
-                        for (int k = 0; k < D / 16; ++k)
-                            tc_mma_ss(st, q_desc + (((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4),
-                                      k_desc + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), s_shape, k > 0);
-                        tc_commit(s_there(t));
+                bool on = keys.on(t, j);
+                auto scores = [&](int at) {                    // S = Q K^T
+                    const uint64_t k_desc = tc_desc(base32 + C::KV_OFF + at * C::TILE, 0, C::HALVES * 1024);
+                    #pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        tc_mma_ss(st, q_desc + (((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4),
+                                  k_desc + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), s_shape, k > 0);
+                    tc_commit(s_there(t));
+                };
+                if (j < keys.n && spin(full(ring.slot), ring.times)) {
+                    if (on) {
+                        scores(ring.slot);
                         tc_commit(empty(ring.slot));
                         if (j + 1 == keys.b(t)) tc_commit(q_free(t));
                     } else {
                         mbar_arrive(empty(ring.slot));
                     }
-                    // this tile's values and the next one's keys are there before the weights
+                }
+                #pragma unroll 1
+                while (fine && j < keys.n) {                   // (this tile's scores are issued)
+                    const int jn = keys.next(j + 1);
+                    const bool more = jn < keys.n, on_next = more && keys.on(t, jn);
+                    // its values and the next one's keys are there before the weights
                     ring.advance();
                     const int v = ring.slot;
                     if (!spin(full(v), ring.times)) break;
                     ring.advance();
-                    if (jn < keys.n && !spin(full(ring.slot), ring.times)) break;
+                    if (more && !spin(full(ring.slot), ring.times)) break;
                     if (on) {                                  // O += W V
                         const uint64_t v_desc = tc_desc(base32 + C::KV_OFF + v * C::TILE, 1024, C::HALVES * 1024);
                         #pragma unroll
@@ -518,13 +535,23 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                                 tc_mma_ts(ot, st + k * 8, v_desc + k * (C::HALVES * 2048 >> 4), o_shape, i > i0 || k > 0);
                         }
                         if (!fine) break;
+                        ++i;
+                    }
+                    if (on_next) scores(ring.slot);            // right behind: the softmax waits for them
+                    if (on) {
                         tc_commit(o_there(t));
                         tc_commit(empty(v));
-                        ++i;
                     } else {
                         mbar_arrive(empty(v));
                     }
+                    if (on_next) {
+                        tc_commit(empty(ring.slot));
+                        if (jn + 1 == keys.b(t)) tc_commit(q_free(t));
+                    } else if (more) {
+                        mbar_arrive(empty(ring.slot));
+                    }
                     j = jn;
+                    on = on_next;
                 }
                 if (!fine) break;
                 if (keys.a(t) == keys.b(t)) mbar_arrive(q_free(t));
@@ -618,8 +645,11 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
         ask();
         #pragma unroll 1
         while (true) {
-            // later row tiles, which see more keys, first
-            const int tile = p.tiles - 1 - index % p.tiles, head = index / p.tiles % a.H, s = index / p.tiles / a.H;
+            // Groups of units, whose keys and values stay in the L2; in a group the later row tiles, which see more
+            // keys, first, so that the call ends with short items.
+            const int units = a.batch * a.H, g0 = index / (p.group * p.tiles) * p.group, of = min(p.group, units - g0);
+            const int at = index - g0 * p.tiles, unit = g0 + at % of;
+            const int tile = p.tiles - 1 - at / of, head = unit % a.H, s = unit / a.H;
             QuerySeq seq{0, 0, 0};
             const int token = tile * 2 * per_tile;
             if (index >= 0) {
