@@ -21,6 +21,7 @@ int launch_query_prompt_int4(const kv_pool* pool, const PromptArgs& p, bool pdl,
 namespace {
 
 constexpr int kTile = 128;             // rows of a row tile and keys of a key tile
+constexpr int kStep = 64;              // keys of a softmax step: the matrix products of one run while the other is weighed
 constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kLoadWarp = 10, kItemWarp = 11, kWidenWarp = 12;
 constexpr int kFactorTiles = 8;        // key tiles whose FP8 scales are kept (more than are in flight)
 
@@ -46,7 +47,7 @@ struct PromptCfg {
     static constexpr int FACTOR_OFF = OUT_OFF + kSoftmaxWarps * 32 * 128;
     static constexpr int FACTORS = POOL == KV_FP8_E4M3 ? kFactorTiles * 2 * 16 * 4 : 0;
     static constexpr int BAR_OFF = FACTOR_OFF + FACTORS;
-    static constexpr int BARS = 2 * SLOTS + 2 * RAWS + 6 * 2 + 2 * 2 + 3;
+    static constexpr int BARS = 2 * SLOTS + 2 * RAWS + 8 * 2 + 2 * 2 + 3;
     static constexpr int MISC_OFF = (BAR_OFF + BARS * 8 + 15) / 16 * 16;
     static constexpr int SMEM = MISC_OFF + 160 + 1024;         // and up to 1024 bytes of alignment
     static_assert(SMEM <= 227 * 1024, "shared memory");
@@ -93,18 +94,21 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* er
     return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, err));
 }
 
-// Key tiles [a, b) of each row tile, numbered from position `base`; the work item's are those of either.
-struct KeyTiles {
-    int base, end, a0, b0, a1, b1, n;
+// Steps [a, b) of each row tile, numbered from position `base`; key tiles are pairs of them, and the work item's those
+// that either row tile needs.
+struct KeySteps {
+    int base, end, a0, b0, a1, b1, n;                          // n: key tiles
     __device__ __forceinline__ int a(int t) const { return t ? a1 : a0; }
     __device__ __forceinline__ int b(int t) const { return t ? b1 : b0; }
-    __device__ __forceinline__ bool on(int t, int j) const { return j >= a(t) && j < b(t); }
-    __device__ __forceinline__ int next(int j) const {         // the first of them from j on
-        while (j < n && !on(0, j) && !on(1, j)) ++j;
+    __device__ __forceinline__ bool on(int t, int step) const { return step >= a(t) && step < b(t); }
+    __device__ __forceinline__ bool tile_on(int j) const { return on(0, 2 * j) || on(0, 2 * j + 1) || on(1, 2 * j) || on(1, 2 * j + 1); }
+    __device__ __forceinline__ int next(int j) const {         // the first of the item's key tiles from j on
+        while (j < n && !tile_on(j)) ++j;
         return j;
     }
     __device__ __forceinline__ int before(int j) const {       // how many of them lie before j
-        return max(0, min(b0, j) - a0) + max(0, min(b1, j) - a1) - max(0, min(min(b0, b1), j) - max(a0, a1));
+        const int p0 = a0 >> 1, q0 = (b0 + 1) >> 1, p1 = a1 >> 1, q1 = (b1 + 1) >> 1;
+        return max(0, min(q0, j) - p0) + max(0, min(q1, j) - p1) - max(0, min(min(q0, q1), j) - max(p0, p1));
     }
 };
 
@@ -122,17 +126,17 @@ struct PromptMisc {
 };
 static_assert(sizeof(PromptMisc) <= 160, "PromptCfg::SMEM");
 
-__device__ __forceinline__ KeyTiles key_tiles(const Item& x, int block) {
-    KeyTiles k;
+__device__ __forceinline__ KeySteps key_steps(const Item& x, int block) {
+    KeySteps k;
     k.base = min(x.lo[0], x.lo[1]) & -block;
     k.end = max(x.hi[0], x.hi[1]);
-    auto from = [&](int t) { return x.lo[t] < x.hi[t] ? (x.lo[t] - k.base) / kTile : 0; };
-    auto to = [&](int t) { return x.lo[t] < x.hi[t] ? (x.hi[t] - k.base + kTile - 1) / kTile : 0; };
+    auto from = [&](int t) { return x.lo[t] < x.hi[t] ? (x.lo[t] - k.base) / kStep : 0; };
+    auto to = [&](int t) { return x.lo[t] < x.hi[t] ? (x.hi[t] - k.base + kStep - 1) / kStep : 0; };
     k.a0 = from(0);
     k.b0 = to(0);
     k.a1 = from(1);
     k.b1 = to(1);
-    k.n = max(k.b0, k.b1);
+    k.n = (max(k.b0, k.b1) + 1) >> 1;
     return k;
 }
 
@@ -173,12 +177,12 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
     constexpr int B0 = 2 * C::SLOTS + 2 * C::RAWS;
     auto q_there = [&](int t) { return bar(B0 + t); };         // a row tile's queries
     auto q_free = [&](int t) { return bar(B0 + 2 + t); };      // and their place
-    auto s_there = [&](int t) { return bar(B0 + 4 + t); };     // its scores
-    auto w_there = [&](int t, int half) { return bar(B0 + 6 + 2 * t + half); };    // its weights of half the keys
-    auto o_there = [&](int t) { return bar(B0 + 10 + t); };    // its sums so far
-    auto item_there = [&](int i) { return bar(B0 + 12 + i); };
-    auto item_free = [&](int i) { return bar(B0 + 14 + i); };
-    const uint32_t edge = bar(B0 + 16), done = bar(B0 + 17), claim = bar(B0 + 18);
+    auto s_there = [&](int t, int h) { return bar(B0 + 4 + 2 * t + h); };      // its scores of a step (even, odd)
+    auto w_there = [&](int t, int h) { return bar(B0 + 8 + 2 * t + h); };      // its weights of a step
+    auto o_there = [&](int t, int h) { return bar(B0 + 12 + 2 * t + h); };     // its sums after a step
+    auto item_there = [&](int i) { return bar(B0 + 16 + i); };
+    auto item_free = [&](int i) { return bar(B0 + 18 + i); };
+    const uint32_t edge = bar(B0 + 20), done = bar(B0 + 21), claim = bar(B0 + 22);
     float* const factors = reinterpret_cast<float*>(smem + C::FACTOR_OFF);     // FP8: [tile][keys, values][block]
 
     if (threadIdx.x == 0) {
@@ -193,10 +197,12 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
         for (int t = 0; t < 2; ++t) {
             mbar_init(q_there(t), 1);
             mbar_init(q_free(t), 1);
-            mbar_init(s_there(t), 1);
+            mbar_init(s_there(t, 0), 1);
+            mbar_init(s_there(t, 1), 1);
             mbar_init(w_there(t, 0), 4);
             mbar_init(w_there(t, 1), 4);
-            mbar_init(o_there(t), 1);
+            mbar_init(o_there(t, 0), 1);
+            mbar_init(o_there(t, 1), 1);
             mbar_init(item_there(t), 1);
             mbar_init(item_free(t), C::WARPS - 1);
         }
@@ -216,7 +222,7 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
     bool fine = true;                                          // no wait of this warp has run out
     int count = 0;                                             // items so far
     Item it;
-    KeyTiles keys;
+    KeySteps keys;
     auto wait = [&](uint32_t b, int times) {                   // for the barrier's times-th completion (from 0)
         fine = fine && warp_wait(b, times & 1, a.err);
         return fine;
@@ -241,7 +247,7 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
         __syncwarp();
         if (lane == 0) mbar_arrive(item_free(i));
         ++count;
-        keys = key_tiles(it, a.B);
+        keys = key_steps(it, a.B);
         return it.s >= 0;
     };
 
@@ -255,14 +261,19 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
         const float qscale = a.scale * kLog2e;
         const float k2 = cap ? 2.f * kLog2e * (a.scale / a.cap) : 0.f, capl = a.cap * kLog2e;
         const float c = cap || bias ? 1.f : qscale;            // scores to log2 units
-        int i = 0, tiles = 0;                                  // this row tile's key tiles so far; the items'
+        int i = 0, even = 0, tiles = 0;                        // this row tile's steps so far, the even ones; the items' tiles
         #pragma unroll 1
         for (; wait(item_there(count & 1), count >> 1); ++count) {
             // (the item stays in shared memory, where it is read again when needed: registers are short here)
             const Item& x0 = misc->item[count & 1];
             if (uniform(x0.s) < 0) break;
-            keys = key_tiles(x0, a.B);
-            const int j_base = uniform(keys.base), j_from = uniform(keys.a(rt)), j_to = uniform(keys.b(rt));
+            int step, to_step, j0;                             // the row tile's steps; a step's first position
+            {
+                const KeySteps k = key_steps(x0, a.B);
+                step = uniform(k.a(rt));
+                to_step = uniform(k.b(rt));
+                j0 = uniform(k.base) + step * kStep;
+            }
             int2 sees = make_int2(0, 0);
             int pos;
             float slope = 0.f, inv_vref = 1.f;
@@ -276,20 +287,23 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
             float m = -CUDART_INF_F, l = 0.f;                  // the base (log2 units) and the sum of weights
             const int i0 = i;
             #pragma unroll 1
-            for (int j = j_from; j < j_to; ++j, ++i) {
-                if (!wait(s_there(rt), i)) break;
+            for (; step < to_step; ++step, ++i, j0 += kStep) {
+                const int h = step & 1;
+                if (!wait(s_there(rt, h), h ? i - even : even)) break;
+                even += 1 - h;
                 tc_fence_after();
-                float x[kTile];
+                const uint32_t at = st + h * kStep;
+                float x[kStep];
                 uint32_t* const xr = reinterpret_cast<uint32_t*>(x);
-                #pragma unroll
-                for (int k = 0; k < 4; ++k) tmem_load32(st + 32 * k, xr + 32 * k);
-                #pragma unroll
-                for (int k = 0; k < 4; ++k) tmem_wait_load32(xr + 32 * k);
-                const int j0 = j_base + j * kTile;
-                const float* const scales = POOL == KV_FP8_E4M3 ? factors + (tiles + key_tiles(x0, a.B).before(j)) % kFactorTiles * 32 : nullptr;
+                tmem_load32(at, xr);
+                tmem_load32(at + 32, xr + 32);
+                tmem_wait_load32(xr);
+                tmem_wait_load32(xr + 32);
+                const float* const scales = POOL == KV_FP8_E4M3
+                    ? factors + (tiles + key_steps(x0, a.B).before(step >> 1)) % kFactorTiles * 32 + (h * kStep >> a.log_b) : nullptr;
                 if constexpr (POOL == KV_FP8_E4M3) {
                     #pragma unroll
-                    for (int k = 0; k < kTile; k += 8) {
+                    for (int k = 0; k < kStep; k += 8) {
                         const float f = scales[k >> a.log_b];
                         #pragma unroll
                         for (int e = 0; e < 8; ++e) x[k + e] *= f;
@@ -297,56 +311,49 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                 }
                 if (cap) {
                     #pragma unroll
-                    for (int k = 0; k < kTile; ++k) x[k] = capped(x[k], k2, capl);
+                    for (int k = 0; k < kStep; ++k) x[k] = capped(x[k], k2, capl);
                 }
                 if (bias) {
                     const float from = static_cast<float>(pos - j0), mul = cap ? 1.f : qscale;
                     #pragma unroll
-                    for (int k = 0; k < kTile; ++k) x[k] = fmaf(-slope, fabsf(from - static_cast<float>(k)), x[k] * mul);
+                    for (int k = 0; k < kStep; ++k) x[k] = fmaf(-slope, fabsf(from - static_cast<float>(k)), x[k] * mul);
                 }
-                if (__any_sync(0xffffffffu, sees.x > j0 || sees.y < j0 + kTile)) {
+                if (__any_sync(0xffffffffu, sees.x > j0 || sees.y < j0 + kStep)) {
                     const int from = sees.x - j0;
                     const unsigned len = sees.y - sees.x;
                     #pragma unroll
-                    for (int k = 0; k < kTile; ++k)
+                    for (int k = 0; k < kStep; ++k)
                         if (static_cast<unsigned>(k - from) >= len) x[k] = -CUDART_INF_F;
                 }
-                // Weights of the h-th half of the keys at the base m, their sums per pair of columns in `sum`.
+                // Weights at the base m, and their sums per pair of columns.
                 const float2 c2 = make_float2(c, c);
                 float2 sum[2];
-                uint32_t w[32];
-                auto weigh = [&](int h) {
+                uint32_t w[kStep / 2];
+                auto weigh = [&]() {
                     const float off = kLift - (m == -CUDART_INF_F ? 0.f : m);
                     const float2 off2 = make_float2(off, off);
                     #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        float2 y = __ffma2_rn(make_float2(x[64 * h + 2 * k], x[64 * h + 2 * k + 1]), c2, off2);
+                    for (int k = 0; k < kStep / 2; ++k) {
+                        float2 y = __ffma2_rn(make_float2(x[2 * k], x[2 * k + 1]), c2, off2);
                         y.x = ex2_approx(y.x);
                         y.y = ex2_approx(y.y);
-                        sum[k & 1] = h == 0 && k < 2 ? y : __fadd2_rn(sum[k & 1], y);
+                        sum[k & 1] = k < 2 ? y : __fadd2_rn(sum[k & 1], y);
                         if constexpr (POOL == KV_FP8_E4M3) {
-                            const float f = scales[16 + ((64 * h + 2 * k) >> a.log_b)] * inv_vref;
+                            const float f = scales[16 + (2 * k >> a.log_b)] * inv_vref;
                             y = __fmul2_rn(y, make_float2(f, f));
                         }
                         const __half2 hv = __floats2half2_rn(y.x, y.y);
                         w[k] = *reinterpret_cast<const uint32_t*>(&hv);
                     }
                 };
-                auto hand_over = [&](int h) {
-                    tmem_store32(st + 32 * h, w);
-                    tmem_wait_store();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(w_there(rt, h));
-                };
-                // The first half is weighed at the old base while the maximum is found: the base follows it only when
-                // it is left behind by more than 2^8, which is rare after the first tile.
-                weigh(0);
+                // They are taken at the old base while the maximum is found: the base follows it only when it is left
+                // behind by more than 2^8, which is rare after the first step.
+                weigh();
                 float tops[4];
                 #pragma unroll
                 for (int k = 0; k < 4; ++k) tops[k] = max3(x[3 * k], x[3 * k + 1], x[3 * k + 2]);
                 #pragma unroll
-                for (int k = 12; k < kTile; k += 2) tops[(k >> 1) & 3] = max3(x[k], x[k + 1], tops[(k >> 1) & 3]);
+                for (int k = 12; k < kStep; k += 2) tops[(k >> 1) & 3] = max3(x[k], x[k + 1], tops[(k >> 1) & 3]);
                 const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * c;
                 const bool raise = top - m > kRaise;           // (m -inf: yes, but for a row that sees nothing yet)
                 if (__any_sync(0xffffffffu, raise)) {
@@ -357,7 +364,8 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                         l *= keep;
                     }
                     if (i > i0) {
-                        if (!wait(o_there(rt), i - 1)) break;
+                        // the step before (the one before that is done: its scores' place holds this one's)
+                        if (!wait(o_there(rt, 1 - h), h ? even - 1 : i - even)) break;
                         tc_fence_after();
                         #pragma unroll 1
                         for (int k = 0; k < D; k += 32) {
@@ -369,14 +377,16 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                             tmem_store32(ot + k, o);
                         }
                     }
-                    weigh(0);
+                    weigh();
                 }
-                hand_over(0);                                  // its products begin while the second half is weighed
-                weigh(1);
-                hand_over(1);
+                tmem_store32(at, w);
+                tmem_wait_store();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(w_there(rt, h));
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             }
-            if (!fine || (i > i0 && !wait(o_there(rt), i - 1))) break;
+            if (!fine || (i > i0 && !wait(o_there(rt, (step - 1) & 1), (step & 1 ? even : i - even) - 1))) break;
             tc_fence_after();
             // the result, 64 elements at a time through shared memory, so that a store writes whole lines
             const Item it = x0;
@@ -436,7 +446,7 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                 again &= again - 1;
                 attend_row<D, POOL>(a, it.s, seq, it.token + rt * per_tile + (r >> log_g), it.head * a.G + (r & (a.G - 1)));
             }
-            if constexpr (POOL == KV_FP8_E4M3) tiles += key_tiles(x0, a.B).before(1 << 30);
+            if constexpr (POOL == KV_FP8_E4M3) tiles += key_steps(x0, a.B).before(1 << 30);
             __syncwarp();
             if (lane == 0) mbar_arrive(item_free(count & 1));
         }
@@ -477,7 +487,7 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
     if (warp == kMmaWarp || warp == kMmaWarp + 1) {
         // ======== matrix products, a thread per row tile: its products wait for its softmax, and the other row tile's
         // run meanwhile
-        constexpr uint32_t s_shape = tc_idesc(kTile, false), o_shape = tc_idesc(D, true);
+        constexpr uint32_t s_shape = tc_idesc(kStep, false), o_shape = tc_idesc(D, true);
         if (elect_one()) {
             const int t = warp - kMmaWarp;
             const uint32_t st = tmem + t * kTile, ot = tmem + 2 * kTile + t * D;
@@ -486,72 +496,73 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                 fine = fine && mbar_wait_bounded(b, times & 1, a.err);
                 return fine;
             };
-            int i = 0;                                         // this row tile's key tiles so far
+            int i = 0, even = 0;                               // this row tile's steps so far, the even ones
             Ring<C::SLOTS> ring;
             while (spin(item_there(count & 1), count >> 1)) {
                 it = misc->item[count & 1];
                 mbar_arrive(item_free(count & 1));
                 if (it.s < 0) break;
-                keys = key_tiles(it, a.B);
+                keys = key_steps(it, a.B);
                 if (!spin(q_there(t), count++)) break;
                 const int i0 = i;
                 int j = keys.next(0);
-                bool on = keys.on(t, j);
-                auto scores = [&](int at) {                    // S = Q K^T
-                    const uint64_t k_desc = tc_desc(base32 + C::KV_OFF + at * C::TILE, 0, C::HALVES * 1024);
+                auto scores = [&](int at, int h) {             // S = Q K^T for a step
+                    const uint64_t k_desc = tc_desc(base32 + C::KV_OFF + at * C::TILE + h * (C::TILE / 2), 0, C::HALVES * 1024);
                     #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
-                        tc_mma_ss(st, q_desc + (((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4),
+                        tc_mma_ss(st + h * kStep, q_desc + (((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4),
                                   k_desc + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), s_shape, k > 0);
-                    tc_commit(s_there(t));
+                    tc_commit(s_there(t, h));
+                };
+                // a key tile that this row tile has no (more) steps of, or whose products are issued, is left to the loader
+                auto leave = [&](int at, bool used) {
+                    if (used) tc_commit(empty(at));
+                    else mbar_arrive(empty(at));
                 };
                 if (j < keys.n && spin(full(ring.slot), ring.times)) {
-                    if (on) {
-                        scores(ring.slot);
-                        tc_commit(empty(ring.slot));
-                        if (j + 1 == keys.b(t)) tc_commit(q_free(t));
-                    } else {
-                        mbar_arrive(empty(ring.slot));
-                    }
+                    const bool on0 = keys.on(t, 2 * j), on1 = keys.on(t, 2 * j + 1);
+                    if (on0) scores(ring.slot, 0);
+                    if (on1) scores(ring.slot, 1);
+                    leave(ring.slot, on0 || on1);
+                    if ((on0 || on1) && keys.b(t) <= 2 * j + 2) tc_commit(q_free(t));
                 }
                 #pragma unroll 1
                 while (fine && j < keys.n) {                   // (this tile's scores are issued)
                     const int jn = keys.next(j + 1);
-                    const bool more = jn < keys.n, on_next = more && keys.on(t, jn);
+                    const bool more = jn < keys.n;
                     // its values and the next one's keys are there before the weights
                     ring.advance();
                     const int v = ring.slot;
                     if (!spin(full(v), ring.times)) break;
                     ring.advance();
                     if (more && !spin(full(ring.slot), ring.times)) break;
-                    if (on) {                                  // O += W V
-                        const uint64_t v_desc = tc_desc(base32 + C::KV_OFF + v * C::TILE, 1024, C::HALVES * 1024);
-                        #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if (!spin(w_there(t, h), i)) break;
+                    bool used = false, used_next = false;
+                    #pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (keys.on(t, 2 * j + h)) {           // O += W V
+                            if (!spin(w_there(t, h), h ? i - even : even)) break;
+                            even += 1 - h;
                             tc_fence_after();
+                            const uint64_t v_desc = tc_desc(base32 + C::KV_OFF + v * C::TILE + h * (C::TILE / 2), 1024, C::HALVES * 1024);
                             #pragma unroll
-                            for (int k = 4 * h; k < 4 * h + 4; ++k)
-                                tc_mma_ts(ot, st + k * 8, v_desc + k * (C::HALVES * 2048 >> 4), o_shape, i > i0 || k > 0);
+                            for (int k = 0; k < kStep / 16; ++k)
+                                tc_mma_ts(ot, st + h * kStep + k * 8, v_desc + k * (C::HALVES * 2048 >> 4), o_shape, i > i0 || k > 0);
+                            tc_commit(o_there(t, h));
+                            used = true;
+                            ++i;
                         }
-                        if (!fine) break;
-                        ++i;
+                        if (more && keys.on(t, 2 * jn + h)) {
+                            scores(ring.slot, h);
+                            used_next = true;
+                        }
                     }
-                    if (on_next) scores(ring.slot);            // right behind: the softmax waits for them
-                    if (on) {
-                        tc_commit(o_there(t));
-                        tc_commit(empty(v));
-                    } else {
-                        mbar_arrive(empty(v));
-                    }
-                    if (on_next) {
-                        tc_commit(empty(ring.slot));
-                        if (jn + 1 == keys.b(t)) tc_commit(q_free(t));
-                    } else if (more) {
-                        mbar_arrive(empty(ring.slot));
+                    if (!fine) break;
+                    leave(v, used);
+                    if (more) {
+                        leave(ring.slot, used_next);
+                        if (used_next && keys.b(t) <= 2 * jn + 2) tc_commit(q_free(t));
                     }
                     j = jn;
-                    on = on_next;
                 }
                 if (!fine) break;
                 if (keys.a(t) == keys.b(t)) mbar_arrive(q_free(t));
