@@ -66,7 +66,7 @@ int plan_query(const kv_pool* pool, const kv_query_args& x, QueryPlan* plan) {
         return KV_ERR_INVALID_ARG;
     const int g = x.num_q_heads / d.num_heads;
     if (g != 1 && g != 2 && g != 4 && g != 8) return KV_ERR_INVALID_ARG;
-    if (static_cast<int64_t>(x.batch) * d.num_heads * prompt_tiles(x.max_queries, g) > (int64_t{1} << 30))
+    if (prompt_items(x.batch, d.num_heads, g, x.num_tokens, x.max_queries) > (int64_t{1} << 30))
         return KV_ERR_INVALID_ARG;
     // float32 pools: a warp per row and head; the others by what a K/V head's rows fill: one 16-row matrix
     // product over keys that are read once, or 128-row tiles of the tensor cores

@@ -221,8 +221,17 @@ __device__ __noinline__ void attend_row(const QueryArgs& a, int s, QuerySeq seq,
 constexpr int kFewRows = 16;
 constexpr int kFewSeqs = 1024;         // sequences per launch of it
 
-// Row tiles (pairs of 128 rows) of a sequence's K/V head in the tensor-core kernel.
-inline int prompt_tiles(int max_queries, int group) { return static_cast<int>((static_cast<int64_t>(max_queries) * group + 255) / 256); }
+// Pairs of 128-row tiles of a sequence's K/V head in the tensor-core kernel.
+__host__ __device__ inline int prompt_tiles(int queries, int group) {
+    return static_cast<int>((static_cast<int64_t>(queries) * group + 255) / 256);
+}
+// Bound of a call's (pair, K/V head): each sequence has at most max_queries rows, all of them num_tokens, and one pair
+// of each sequence is not full.
+inline int64_t prompt_items(int batch, int heads, int group, int num_tokens, int max_queries) {
+    const int64_t each = static_cast<int64_t>(batch) * prompt_tiles(max_queries, group);
+    const int64_t all = static_cast<int64_t>(num_tokens) * group / 256 + batch;
+    return (each < all ? each : all) * heads;
+}
 
 // The kernels' launchers.
 int launch_query_prompt(const kv_pool* pool, int layer, const QueryArgs& a, bool pdl, cudaStream_t stream);

@@ -11,8 +11,7 @@ struct PromptArgs {
     CUtensorMap qmap;                  // [num_tokens][heads][D / 64][64], boxes of a row tile's 64-element halves
     CUtensorMap kmap, vmap;            // float16 pools: the layer's row maps, a block of one head per copy
     QueryArgs a;
-    int tiles;                         // pairs of row tiles per unit (sequence, K/V head)
-    int group;                         // units whose items come together
+    int items;                         // bound of the work items
 };
 
 int launch_query_prompt_fp8(const kv_pool* pool, const PromptArgs& p, bool pdl, cudaStream_t stream);
@@ -262,28 +261,36 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
         const float k2 = cap ? 2.f * kLog2e * (a.scale / a.cap) : 0.f, capl = a.cap * kLog2e;
         const float c = cap || bias ? 1.f : qscale;            // scores to log2 units
         int i = 0, even = 0, tiles = 0;                        // this row tile's steps so far, the even ones; the items' tiles
+        // An item's part of this thread, taken while the last products of the item before are made.  (The rest stays in
+        // shared memory until the result is out: registers are short here.)
+        struct Part {
+            int step, to_step, j0, pos;                        // the row tile's steps; the first one's position; the row's
+            int2 sees;
+            float slope, inv_vref;
+        } next;
+        auto fetch = [&]() {
+            if (!wait(item_there(count & 1), count >> 1)) return false;
+            const Item& x = misc->item[count & 1];
+            if (uniform(x.s) < 0) return false;
+            const KeySteps k = key_steps(x, a.B);
+            next.step = uniform(k.a(rt));
+            next.to_step = uniform(k.b(rt));
+            next.j0 = uniform(k.base) + next.step * kStep;
+            const int token = x.token + rt * per_tile + (row >> log_g);
+            next.sees = token < x.n ? row_range(a, QuerySeq{x.first, x.n, x.ctx}, token) : make_int2(0, 0);
+            next.slope = bias ? a.slopes[x.head * a.G + (row & (a.G - 1))] * kLog2e : 0.f;
+            next.pos = x.ctx - x.n + token;
+            next.inv_vref = POOL == KV_FP8_E4M3 ? 1.f / x.vref : 1.f;
+            return true;
+        };
+        bool some_item = fetch();
         #pragma unroll 1
-        for (; wait(item_there(count & 1), count >> 1); ++count) {
-            // (the item stays in shared memory, where it is read again when needed: registers are short here)
+        while (some_item) {
             const Item& x0 = misc->item[count & 1];
-            if (uniform(x0.s) < 0) break;
-            int step, to_step, j0;                             // the row tile's steps; a step's first position
-            {
-                const KeySteps k = key_steps(x0, a.B);
-                step = uniform(k.a(rt));
-                to_step = uniform(k.b(rt));
-                j0 = uniform(k.base) + step * kStep;
-            }
-            int2 sees = make_int2(0, 0);
-            int pos;
-            float slope = 0.f, inv_vref = 1.f;
-            {
-                const int token = x0.token + rt * per_tile + (row >> log_g);
-                if (token < x0.n) sees = row_range(a, QuerySeq{x0.first, x0.n, x0.ctx}, token);
-                if (bias) slope = a.slopes[x0.head * a.G + (row & (a.G - 1))] * kLog2e;
-                pos = x0.ctx - x0.n + token;
-                if constexpr (POOL == KV_FP8_E4M3) inv_vref = 1.f / x0.vref;
-            }
+            int step = next.step, j0 = next.j0;
+            const int to_step = next.to_step, pos = next.pos;
+            const int2 sees = next.sees;
+            const float slope = next.slope, inv_vref = next.inv_vref;
             float m = -CUDART_INF_F, l = 0.f;                  // the base (log2 units) and the sum of weights
             const int i0 = i;
             #pragma unroll 1
@@ -386,10 +393,16 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                 if (lane == 0) mbar_arrive(w_there(rt, h));
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             }
+            if (!fine) break;
+            const Item it = x0;
+            const int it_tiles = POOL == KV_FP8_E4M3 ? key_steps(x0, a.B).before(1 << 30) : 0;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(item_free(count & 1));
+            ++count;
+            some_item = fetch();
             if (!fine || (i > i0 && !wait(o_there(rt, (step - 1) & 1), (step & 1 ? even : i - even) - 1))) break;
             tc_fence_after();
             // the result, 64 elements at a time through shared memory, so that a store writes whole lines
-            const Item it = x0;
             const int token = it.token + rt * per_tile + (row >> log_g);
             const QuerySeq seq{it.first, it.n, it.ctx};
             const bool some = i > i0 && l != 0.f, live = token < it.n;
@@ -446,9 +459,7 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                 again &= again - 1;
                 attend_row<D, POOL>(a, it.s, seq, it.token + rt * per_tile + (r >> log_g), it.head * a.G + (r & (a.G - 1)));
             }
-            if constexpr (POOL == KV_FP8_E4M3) tiles += key_steps(x0, a.B).before(1 << 30);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(item_free(count & 1));
+            tiles += it_tiles;
         }
     } else if (C::WIDEN && warp >= kWidenWarp) {
         // ======== stored tiles to float16
@@ -485,92 +496,100 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
         fewer_registers<C::REGS_ISSUE>();
     }
     if (warp == kMmaWarp || warp == kMmaWarp + 1) {
-        // ======== matrix products, a thread per row tile: its products wait for its softmax, and the other row tile's
-        // run meanwhile
+        // ======== matrix products, a warp per row tile (they wait for its softmax, and the other row tile's run
+        // meanwhile): it stays together, one lane issues
         constexpr uint32_t s_shape = tc_idesc(kStep, false), o_shape = tc_idesc(D, true);
-        if (elect_one()) {
-            const int t = warp - kMmaWarp;
-            const uint32_t st = tmem + t * kTile, ot = tmem + 2 * kTile + t * D;
-            const uint64_t q_desc = tc_desc(base32 + C::Q_OFF + t * C::TILE, 0, 1024);
-            auto spin = [&](uint32_t b, int times) {
-                fine = fine && mbar_wait_bounded(b, times & 1, a.err);
-                return fine;
+        const int t = warp - kMmaWarp;
+        const uint32_t st = tmem + t * kTile, ot = tmem + 2 * kTile + t * D;
+        const uint64_t q_desc = tc_desc(base32 + C::Q_OFF + t * C::TILE, 0, 1024);
+        // A look at a barrier takes 200 cycles beside the products' reads of shared memory: lanes 0, 1 and 2 look at one each.
+        auto wait3 = [&](uint32_t b0, int n0, uint32_t b1, int n1, uint32_t b2, int n2) {
+            const uint32_t b = lane == 1 ? b1 : lane == 2 ? b2 : b0;
+            const int n = lane == 1 ? n1 : lane == 2 ? n2 : n0;
+            return wait(b, n);
+        };
+        int i = 0, even = 0;                                   // this row tile's steps so far, the even ones
+        Ring<C::SLOTS> ring;
+        while (next_item()) {
+            const int i0 = i;
+            const int a_t = keys.a(t), b_t = keys.b(t);
+            auto on = [&](int step) { return step >= a_t && step < b_t; };
+            auto scores = [&](int at, int h) {                 // S = Q K^T for a step (one lane)
+                const uint64_t k_desc = tc_desc(base32 + C::KV_OFF + at * C::TILE + h * (C::TILE / 2), 0, C::HALVES * 1024);
+                #pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    tc_mma_ss(st + h * kStep, q_desc + (((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4),
+                              k_desc + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), s_shape, k > 0);
+                tc_commit(s_there(t, h));
             };
-            int i = 0, even = 0;                               // this row tile's steps so far, the even ones
-            Ring<C::SLOTS> ring;
-            while (spin(item_there(count & 1), count >> 1)) {
-                it = misc->item[count & 1];
-                mbar_arrive(item_free(count & 1));
-                if (it.s < 0) break;
-                keys = key_steps(it, a.B);
-                if (!spin(q_there(t), count++)) break;
-                const int i0 = i;
-                int j = keys.next(0);
-                auto scores = [&](int at, int h) {             // S = Q K^T for a step
-                    const uint64_t k_desc = tc_desc(base32 + C::KV_OFF + at * C::TILE + h * (C::TILE / 2), 0, C::HALVES * 1024);
-                    #pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
-                        tc_mma_ss(st + h * kStep, q_desc + (((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4),
-                                  k_desc + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), s_shape, k > 0);
-                    tc_commit(s_there(t, h));
-                };
-                // a key tile that this row tile has no (more) steps of, or whose products are issued, is left to the loader
-                auto leave = [&](int at, bool used) {
-                    if (used) tc_commit(empty(at));
-                    else mbar_arrive(empty(at));
-                };
-                if (j < keys.n && spin(full(ring.slot), ring.times)) {
-                    const bool on0 = keys.on(t, 2 * j), on1 = keys.on(t, 2 * j + 1);
+            // a key tile that this row tile has no (more) steps of, or whose products are issued, is left to the loader
+            auto leave = [&](int at, bool used) {
+                if (used) tc_commit(empty(at));
+                else mbar_arrive(empty(at));
+            };
+            int j = keys.next(0);
+            bool on0 = on(2 * j), on1 = on(2 * j + 1);
+            if (j < keys.n) {
+                if (!wait3(full(ring.slot), ring.times, q_there(t), count - 1, full(ring.slot), ring.times)) break;
+                if (elect_one()) {
                     if (on0) scores(ring.slot, 0);
                     if (on1) scores(ring.slot, 1);
                     leave(ring.slot, on0 || on1);
-                    if ((on0 || on1) && keys.b(t) <= 2 * j + 2) tc_commit(q_free(t));
+                    if ((on0 || on1) && b_t <= 2 * j + 2) tc_commit(q_free(t));
                 }
-                #pragma unroll 1
-                while (fine && j < keys.n) {                   // (this tile's scores are issued)
-                    const int jn = keys.next(j + 1);
-                    const bool more = jn < keys.n;
-                    // its values and the next one's keys are there before the weights
-                    ring.advance();
-                    const int v = ring.slot;
-                    if (!spin(full(v), ring.times)) break;
-                    ring.advance();
-                    if (more && !spin(full(ring.slot), ring.times)) break;
-                    bool used = false, used_next = false;
-                    #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (keys.on(t, 2 * j + h)) {           // O += W V
-                            if (!spin(w_there(t, h), h ? i - even : even)) break;
-                            even += 1 - h;
-                            tc_fence_after();
-                            const uint64_t v_desc = tc_desc(base32 + C::KV_OFF + v * C::TILE + h * (C::TILE / 2), 1024, C::HALVES * 1024);
-                            #pragma unroll
-                            for (int k = 0; k < kStep / 16; ++k)
-                                tc_mma_ts(ot, st + h * kStep + k * 8, v_desc + k * (C::HALVES * 2048 >> 4), o_shape, i > i0 || k > 0);
-                            tc_commit(o_there(t, h));
-                            used = true;
-                            ++i;
-                        }
-                        if (more && keys.on(t, 2 * jn + h)) {
-                            scores(ring.slot, h);
-                            used_next = true;
-                        }
-                    }
-                    if (!fine) break;
-                    leave(v, used);
-                    if (more) {
-                        leave(ring.slot, used_next);
-                        if (used_next && keys.b(t) <= 2 * jn + 2) tc_commit(q_free(t));
-                    }
-                    j = jn;
-                }
-                if (!fine) break;
-                if (keys.a(t) == keys.b(t)) mbar_arrive(q_free(t));
+                __syncwarp();
+            } else if (!wait(q_there(t), count - 1)) {
+                break;
             }
-            tc_commit(done);                                   // nothing of it is in flight at the end
-            mbar_wait_bounded(done, 0, a.err);
+            #pragma unroll 1
+            while (j < keys.n) {                               // (this tile's scores are issued)
+                const int jn = keys.next(j + 1);
+                const bool more = jn < keys.n, next0 = more && on(2 * jn), next1 = more && on(2 * jn + 1);
+                ring.advance();
+                const int v = ring.slot, v_times = ring.times;
+                ring.advance();
+                const uint64_t v_desc = tc_desc(base32 + C::KV_OFF + v * C::TILE, 1024, C::HALVES * 1024);
+                auto values = [&](int h) {                     // O += W V for a step (one lane)
+                    #pragma unroll
+                    for (int k = 0; k < kStep / 16; ++k)
+                        tc_mma_ts(ot, st + h * kStep + k * 8, v_desc + (h * (C::TILE / 2) >> 4) + k * (C::HALVES * 2048 >> 4), o_shape,
+                                  i > i0 || k > 0);
+                    tc_commit(o_there(t, h));
+                };
+                // its values, the next tile's keys and the even step's weights; then the odd step's weights
+                if (!wait3(full(v), v_times, more ? full(ring.slot) : full(v), more ? ring.times : v_times,
+                           on0 ? w_there(t, 0) : full(v), on0 ? even : v_times))
+                    break;
+                tc_fence_after();
+                if (elect_one()) {
+                    if (on0) values(0);
+                    if (next0) scores(ring.slot, 0);
+                }
+                __syncwarp();
+                even += on0;
+                i += on0;
+                if (on1 && !wait(w_there(t, 1), i - even)) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    if (on1) values(1);
+                    if (next1) scores(ring.slot, 1);
+                    leave(v, on0 || on1);
+                    if (more) leave(ring.slot, next0 || next1);
+                    if ((next0 || next1) && b_t <= 2 * jn + 2) tc_commit(q_free(t));
+                }
+                __syncwarp();
+                i += on1;
+                j = jn;
+                on0 = next0;
+                on1 = next1;
+            }
+            if (!fine) break;
+            if (a_t == b_t && elect_one()) mbar_arrive(q_free(t));
+            __syncwarp();
         }
+        if (elect_one()) tc_commit(done);                      // nothing of it is in flight at the end
         __syncwarp();
+        warp_wait(done, 0, a.err);
     } else if (warp == kLoadWarp) {
         // ======== keys and values in: a lane per block; float16 straight to its place, others as stored
         constexpr int DEPTH = C::WIDEN ? C::RAWS : C::SLOTS;
@@ -638,6 +657,7 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
         for (int r = max(0, ring - DEPTH); r < ring; ++r) mbar_wait_bounded(there(r % DEPTH), r / DEPTH & 1, a.err);
     } else if (warp == kItemWarp) {
         // ======== work items: what the rows see, and their queries, an item ahead of the others
+        int s32 = -32, before = 0, upto = 0, lane_items = 0, lane_upto = 0;    // the sequences walked now
         int index = blockIdx.x, claims = 0, asked = 0;         // (asked: items whose queries were asked for, in part at least)
         auto ask = [&]() {
             if (lane == 0) {
@@ -656,21 +676,38 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
         ask();
         #pragma unroll 1
         while (true) {
-            // Groups of units, whose keys and values stay in the L2; in a group the later row tiles, which see more
-            // keys, first, so that the call ends with short items.
-            const int units = a.batch * a.H, g0 = index / (p.group * p.tiles) * p.group, of = min(p.group, units - g0);
-            const int at = index - g0 * p.tiles, unit = g0 + at % of;
-            const int tile = p.tiles - 1 - at / of, head = unit % a.H, s = unit / a.H;
+            // The sequences' items one after the other; of a sequence the later row tiles, which see more keys, first,
+            // each for every head.  Indices only grow, so the sequences are walked 32 at a time, a lane each.
+            int s = 0, head = 0, token = 0;
             QuerySeq seq{0, 0, 0};
-            const int token = tile * 2 * per_tile;
-            if (index >= 0) {
-                seq = query_seq(a, s, lane == 0 && tile == 0 && head == 0);
-                seq = QuerySeq{uniform(seq.first), uniform(seq.n), uniform(seq.ctx)};
-                if (token >= seq.n) {                          // no such rows
-                    index = answer();
-                    if (index >= 0) ask();
-                    continue;
+            while (index >= 0 && index >= upto && s32 + 32 < a.batch) {
+                s32 += 32;
+                before = upto;
+                lane_items = 0;
+                if (s32 + lane < a.batch)
+                    lane_items = prompt_tiles(query_seq(a, s32 + lane, true).n, a.G) * a.H;
+                lane_upto = lane_items;
+                #pragma unroll
+                for (int o = 1; o < 32; o *= 2) {
+                    const int v = __shfl_up_sync(0xffffffffu, lane_upto, o);
+                    if (lane >= o) lane_upto += v;
                 }
+                upto = before + __shfl_sync(0xffffffffu, lane_upto, 31);
+            }
+            if (index >= upto) {                               // beyond the last item
+                index = answer();
+                if (index >= 0) ask();
+                continue;
+            }
+            if (index >= 0) {
+                const int of = __ffs(__ballot_sync(0xffffffffu, before + lane_upto > index)) - 1;
+                s = s32 + of;
+                const int at = index - before - __shfl_sync(0xffffffffu, lane_upto - lane_items, of);
+                const int tiles = __shfl_sync(0xffffffffu, lane_items, of) / a.H;
+                head = at % a.H;
+                token = (tiles - 1 - at / a.H) * 2 * per_tile;
+                seq = query_seq(a, s, false);
+                seq = QuerySeq{uniform(seq.first), uniform(seq.n), uniform(seq.ctx)};
             }
             Item x{index < 0 ? -1 : s, head, token, seq.first, seq.n, seq.ctx, {1 << 30, 1 << 30}, {0, 0}, 1.f};
             if (index >= 0) {
@@ -723,9 +760,15 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
             }
             if (!fine) break;
             ++count;
-            index = answer();
+            // (the last index is followed to the end of the sequences, so that all are looked at, and no item is left
+            // where rows out of order make more of them than the grid)
+            if (index >= p.items - 1) {
+                ++index;
+            } else {
+                index = answer();
+                if (index >= 0) ask();
+            }
             if (!fine) break;
-            if (index >= 0) ask();
         }
         // what is in flight after a wait ran out (queries, a claim's answer) lands before the CTA ends
         if (!fine && lane == 0) {
@@ -756,7 +799,7 @@ int launch_prompt_typed(const kv_pool* pool, const PromptArgs& p, bool pdl, cuda
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.a.batch * p.a.H * p.tiles));
+    cfg.gridDim = dim3(static_cast<unsigned>(p.items));
     cfg.blockDim = dim3(C::WARPS * 32);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = stream;

@@ -4,16 +4,10 @@
 
 namespace kvp {
 
-// Keys and values of the units whose items come together: a part of the 129 MB L2.
-constexpr int64_t kGroupBytes = 16 << 20;
-
 int launch_query_prompt(const kv_pool* pool, int layer, const QueryArgs& a, bool pdl, cudaStream_t stream) {
     PromptArgs p{};
     p.a = a;
-    p.tiles = prompt_tiles(a.max_queries, a.G);
-    const int64_t unit_bytes = 2 * static_cast<int64_t>(a.ctx_limit > 0 ? a.ctx_limit : 1) * row_bytes(pool->desc);
-    const int64_t group = kGroupBytes / unit_bytes, units = static_cast<int64_t>(a.batch) * a.H;
-    p.group = static_cast<int>(group < 1 ? 1 : group < units ? group : units);
+    p.items = static_cast<int>(prompt_items(a.batch, a.H, a.G, a.num_tokens, a.max_queries));
     // queries: rows of a token are D-element heads; a box is 64 elements of the G heads of 128 / G tokens
     const kv_pool_desc& d = pool->desc;
     const TensorMapEncode encode = reinterpret_cast<TensorMapEncode>(pool->encode);
