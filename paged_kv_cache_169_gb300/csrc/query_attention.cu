@@ -76,7 +76,7 @@ int plan_query(const kv_pool* pool, const kv_query_args& x, QueryPlan* plan) {
     plan->counter_bytes = 0;
     if (plan->kind == QueryPlan::FEW) {
         const int64_t seqs = x.batch < kFewSeqs ? x.batch : kFewSeqs;
-        if (seqs * d.num_heads * (x.max_context / 16 + 2) > (int64_t{1} << 30)) return KV_ERR_INVALID_ARG;
+        if (seqs * d.num_heads * (x.max_context / 16 + 40) > (int64_t{1} << 30)) return KV_ERR_INVALID_ARG;
         plan->ws_bytes = few_space(pool, &plan->counter_bytes);
     }
     return KV_OK;

@@ -2,11 +2,12 @@
 // values are read once for little work and the memory is what counts.
 //
 // The rows are the 16 rows of mma.m16n8k16 (empty ones are zero).  Every (sequence, K/V head) is a unit of
-// 16-token chunks; the chunks of all units, one after the other, are cut into equal ranges, one per CTA and SM, so
-// every SM reads as much whatever the lengths.  A CTA's eight warps take its chunks in turn, each through a ring
-// of its own filled by cp.async (tokens that no row sees are filled with zeros and not read); the part of a unit
-// in a CTA is joined in shared memory, and what crosses CTAs through the workspace by the CTA that finishes last,
-// in two levels where there are more than kFan parts.  Softmax as in the tensor-core kernel.
+// 16-token chunks; the chunks of all units, one after the other (and what beginning and joining a unit costs), are
+// cut into equal ranges, one per CTA and SM, so every SM works as long whatever the lengths.  A CTA's eight warps take
+// a unit's chunks in turn, each through a ring of its own filled by cp.async (tokens that no row sees are filled with
+// zeros and not read); the part of a unit in a CTA is joined in shared memory, and what crosses CTAs through the
+// workspace by the CTA that finishes last, in two levels where there are more than kFan parts.  A short unit is one
+// warp's, with nothing to join, and the others go on.  Softmax as in the tensor-core kernel.
 //   float16   mma operands straight from the ring
 //   FP8, 4-bit  widened to float16 in a tile of the warp's own first
 #pragma once
@@ -38,6 +39,10 @@ namespace {
 constexpr unsigned FULL = 0xffffffffu;
 constexpr int kWarps = 8, kChunk = 16, kFan = 16;
 constexpr int kLeastChunks = 16;       // of a CTA's range: two per warp
+constexpr int kShort = 8;              // a unit of at most so many chunks is one warp's
+// What a unit costs a CTA beside its chunks, in chunks: 2 us (queries, joining), where 16 tokens take 180 ns (float16).
+template <kv_dtype POOL> constexpr int kUnitCost = POOL == KV_F16 ? 11 : POOL == KV_FP8_E4M3 ? 22 : 30;
+constexpr int kShortCost = 2;
 
 template <int D_, kv_dtype POOL_>
 struct FewCfg {
@@ -128,17 +133,20 @@ __global__ void __launch_bounds__(kWarps * 32, 1) query_few_kernel(const __grid_
     const QueryArgs& a = x.a;
     int* const s_lo = reinterpret_cast<int*>(smem + C::SEQ_OFF);               // what the sequence's rows see
     int* const s_hi = s_lo + kFewSeqs;
-    int* const s_end = s_hi + kFewSeqs;                                        // inclusive prefix of chunks over all units
+    int* const s_end = s_hi + kFewSeqs;                                        // inclusive prefix of the units' weights
     // chunks of a unit of the sequence (lo > hi: no rows; lo == hi: rows that see nothing, one chunk)
     auto chunks_of = [&](int s) {
         return s_lo[s] > s_hi[s] ? 0 : max(1, (s_hi[s] - (s_lo[s] & -kChunk) + kChunk - 1) / kChunk);
     };
     float2* const s_ml = reinterpret_cast<float2*>(smem + C::ML_OFF);
+    // what a unit costs beside its chunks; its weight in the ranges
+    auto cost_of = [](int n) { return n > kShort ? kUnitCost<POOL> : kShortCost; };
+    auto weight_of = [&](int n) { return n > 0 ? n + cost_of(n) : 0; };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    // ---- chunks of every sequence and their prefix over the launch's units
+    // ---- what every sequence's rows see, and the prefix of the weights of the launch's units
     {
         const int per = (a.batch + kWarps * 32 - 1) / (kWarps * 32);
         int sum = 0;
@@ -153,7 +161,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) query_few_kernel(const __grid_
                     s_hi[s] = sp.hi;
                 }
             }
-            sum += chunks_of(s) * a.H;
+            sum += weight_of(chunks_of(s)) * a.H;
         }
         int upto = sum;
         #pragma unroll
@@ -167,7 +175,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) query_few_kernel(const __grid_
         int before = upto - sum;
         for (int w = 0; w < warp; ++w) before += s_warp_sum[w];
         for (int s = tid * per; s < min(a.batch, (tid + 1) * per); ++s) {
-            before += chunks_of(s) * a.H;
+            before += weight_of(chunks_of(s)) * a.H;
             s_end[s] = before;
         }
         __syncthreads();
@@ -178,7 +186,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) query_few_kernel(const __grid_
     if (cta >= ctas) return;
     auto range_at = [&](int b) { return static_cast<int>(static_cast<int64_t>(total) * b / ctas); };
     const int g0 = range_at(cta), g1 = range_at(cta + 1);
-    // the CTA whose range holds chunk k
+    // the CTA whose range holds weight k
     auto cta_of = [&](int k) {
         int b = static_cast<int>(static_cast<int64_t>(k) * ctas / total);
         while (range_at(b + 1) <= k) ++b;
@@ -186,40 +194,62 @@ __global__ void __launch_bounds__(kWarps * 32, 1) query_few_kernel(const __grid_
         return b;
     };
 
-    // A place in the chunks of the launch.
-    struct Place { int s, h, c, n; };                          // sequence, head, chunk of the unit, the unit's chunks
-    auto place_of = [&](int k) {
-        int lo = 0, hi = a.batch - 1;                          // the first sequence that ends after k
+    // A unit: sequence, head, its chunks, its start among the weights; the chunks [c0, c1) of it that are this CTA's.
+    struct Unit { int s, h, n, at, c0, c1; };
+    auto in_range = [&](Unit& u) {
+        const int first = u.at + cost_of(u.n);
+        u.c0 = max(0, g0 - first);
+        u.c1 = min(u.n, g1 - first);
+    };
+    auto first_unit = [&]() {
+        int lo = 0, hi = a.batch - 1;                          // the first sequence that ends after g0
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
-            if (s_end[mid] > k) hi = mid; else lo = mid + 1;
+            if (s_end[mid] > g0) hi = mid; else lo = mid + 1;
         }
-        Place r;
-        r.s = lo;
-        r.n = chunks_of(lo);
-        const int at = k - (s_end[lo] - r.n * a.H);
-        r.h = at / r.n;
-        r.c = at - r.h * r.n;
-        return r;
+        Unit u;
+        u.s = lo;
+        u.n = chunks_of(lo);
+        const int w = weight_of(u.n), start = s_end[lo] - w * a.H;
+        u.h = (g0 - start) / w;
+        u.at = start + u.h * w;
+        in_range(u);
+        return u;
     };
-    auto next_unit = [&](Place& r) {                           // (only while a further unit exists)
-        if (++r.h == a.H) {
-            r.h = 0;
-            do r.n = chunks_of(++r.s); while (r.n == 0);
+    auto next_unit = [&](Unit& u) {                            // false: no chunk of it is this CTA's
+        u.at += weight_of(u.n);
+        if (u.at + kShortCost >= min(g1, total)) return false;
+        if (++u.h == a.H) {
+            u.h = 0;
+            do u.n = chunks_of(++u.s); while (u.n == 0);
         }
+        in_range(u);
+        return u.c0 < u.c1;
     };
+    auto is_short = [&](const Unit& u) { return u.n <= kShort && u.c0 == 0 && u.c1 == u.n; };
 
     // ---- filling the ring
     char* const ring = smem + warp * C::WARP;
     const uint32_t ring32 = smem_u32(ring);
-    int fill_k = g0 + warp, fill_slot = 0;                     // the next chunk to ask for and its stage
-    Place fill = place_of(fill_k < g1 ? fill_k : g0);
+    int fill_slot = 0, fill_no = 0, fill_c = 0;                // the stage to fill; the unit's number in the CTA; its chunk
+    bool filling = true;
+    Unit fill = first_unit();
+    auto first_chunk = [&](const Unit& u, int no) {            // of this warp
+        return is_short(u) ? ((no & (kWarps - 1)) == warp ? 0 : u.c1) : u.c0 + ((warp + no) & (kWarps - 1));
+    };
+    auto to_chunk = [&]() {                                    // on to the next chunk that there is
+        while (filling && fill_c >= fill.c1) {
+            filling = next_unit(fill);
+            ++fill_no;
+            if (filling) fill_c = first_chunk(fill, fill_no);
+        }
+    };
     int ids[2];                                                // its (up to two) physical blocks, -1: not read
     // blocks of the chunk's 8-token halves; loaded one chunk ahead
     auto look_up = [&]() {
         ids[0] = ids[1] = -1;
-        if (fill_k >= g1) return;
-        const int lo = s_lo[fill.s], hi = s_hi[fill.s], j0 = (lo & -kChunk) + fill.c * kChunk;
+        if (!filling) return;
+        const int lo = s_lo[fill.s], hi = s_hi[fill.s], j0 = (lo & -kChunk) + fill_c * kChunk;
         #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int first = max(j0 + 8 * i, lo);
@@ -227,8 +257,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) query_few_kernel(const __grid_
         }
     };
     auto ask = [&]() {
-        if (fill_k < g1) {
-            const int lo = s_lo[fill.s], hi = s_hi[fill.s], j0 = (lo & -kChunk) + fill.c * kChunk;
+        if (filling) {
+            const int lo = s_lo[fill.s], hi = s_hi[fill.s], j0 = (lo & -kChunk) + fill_c * kChunk;
             const uint32_t st = ring32 + fill_slot * C::STAGE;
             if constexpr (POOL == KV_INT4) {
                 constexpr int PIECES = Int4<D>::OCT / 16;      // of an oct: 8 tokens
@@ -264,19 +294,16 @@ __global__ void __launch_bounds__(kWarps * 32, 1) query_few_kernel(const __grid_
                     }
                 }
             }
-            fill_k += kWarps;
             fill_slot = fill_slot + 1 == C::STAGES ? 0 : fill_slot + 1;
-            if (fill_k < g1) {
-                fill.c += kWarps;
-                while (fill.c >= fill.n) {
-                    fill.c -= fill.n;
-                    next_unit(fill);
-                }
-            }
+            fill_c += is_short(fill) ? 1 : kWarps;
+            to_chunk();
             look_up();
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    filling = fill.c0 < fill.c1 || next_unit(fill);
+    if (filling) fill_c = first_chunk(fill, 0);
+    to_chunk();
     look_up();
     #pragma unroll 1
     for (int i = 0; i < C::STAGES; ++i) ask();
@@ -288,15 +315,24 @@ __global__ void __launch_bounds__(kWarps * 32, 1) query_few_kernel(const __grid_
     struct Cross { int s, h, first, last; };                   // a unit that crosses CTAs: its first and last CTA
     Cross cross[2] = {{-1, 0, 0, 0}, {-1, 0, 0, 0}};           // one that began before this CTA, one that goes on after
     int slot = 0;                                              // the ring's stage to read next
-    Place unit = place_of(g0);
-    int at = g0;
+    Unit unit = first_unit();
+    bool some = unit.c0 < unit.c1 || next_unit(unit);
     #pragma unroll 1
-    while (true) {
-        const int u0 = at - unit.c, u1 = u0 + unit.n;          // the unit's chunks; unit.c: the first of them here
-        const int to = min(g1, u1);
+    for (int no = 0; some; ++no, some = next_unit(unit)) {
+        const bool alone = is_short(unit);                     // one warp's
+        int k = first_chunk(unit, no);
+        if (alone && k >= unit.c1) continue;
+        const int to = unit.c1, step = alone ? 1 : kWarps;
         const QuerySeq seq = query_seq(a, unit.s, false);
         const int lo = s_lo[unit.s], hi = s_hi[unit.s], base = lo & -kChunk;
         const int rows = seq.n * a.G;
+        // the next head's queries are on their way to the L2
+        if ((alone || warp == 0) && unit.h + 1 < a.H && lane < rows * (D * 2) / 128) {
+            const int row = lane * 128 / (D * 2);
+            const char* at = a.q + static_cast<int64_t>(seq.first + row / a.G) * a.q_stride + ((unit.h + 1) * a.G + row % a.G) * (D * 2) +
+                             lane * 128 % (D * 2);
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+        }
         int2 sees[2];
         int pos[2];
         float slope[2], m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};
@@ -307,7 +343,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) query_few_kernel(const __grid_
             sees[r] = make_int2(0, 0);
             pos[r] = seq.ctx - seq.n + i;
             slope[r] = 0.f;
-            const bool some = row < rows;
+            const bool some = row < rows && k < to;            // (a warp without a chunk needs none of it)
             if (some) {
                 sees[r] = row_range(a, seq, i);
                 if (bias) slope[r] = a.slopes[hq] * kLog2e;
@@ -327,11 +363,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) query_few_kernel(const __grid_
         float vref = 0x1p-126f, inv_vref = 0x1p126f;           // FP8: a power of two above the value scales so far
         int held = -1;                                         // the stage of this warp's last chunk here, not yet filled again
         #pragma unroll 1
-        for (int k = at + ((warp - (at - g0)) & (kWarps - 1)); k < to; k += kWarps) {
+        for (; k < to; k += step) {
             asm volatile("cp.async.wait_group %0;" ::"n"(C::STAGES - 1) : "memory");
             __syncwarp();
             const char* st = ring + slot * C::STAGE;
-            const int j0 = base + (k - u0) * kChunk;
+            const int j0 = base + k * kChunk;
             uint32_t kt = ring32 + slot * C::STAGE, vt = kt + C::RAW;
             float ks[2] = {1.f, 1.f}, vs[2] = {1.f, 1.f};
             if constexpr (C::WIDEN) {
@@ -440,7 +476,35 @@ __global__ void __launch_bounds__(kWarps * 32, 1) query_few_kernel(const __grid_
             held = slot;
             slot = slot + 1 == C::STAGES ? 0 : slot + 1;
             __syncwarp();                                      // every lane has read the stage
-            if (k + kWarps < to) ask();
+            if (alone || k + kWarps < to) ask();
+        }
+        if (alone) {                                           // to the output
+            unsigned odd = 0;
+            #pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                l[r] += __shfl_xor_sync(FULL, l[r], 1);
+                l[r] += __shfl_xor_sync(FULL, l[r], 2);
+                const int row = g + 8 * r;
+                const float inv = (l[r] == 0.f ? 0.f : 1.f / l[r]) * (POOL == KV_FP8_E4M3 ? vref : 1.f);
+                char* out = a.out + static_cast<int64_t>(seq.first + row / a.G) * a.out_stride + (unit.h * a.G + row % a.G) * (D * 2) + t * 4;
+                bool finite = true;
+                #pragma unroll
+                for (int n = 0; n < D / 8; ++n) {
+                    const float2 f = l[r] == 0.f ? make_float2(0.f, 0.f) : make_float2(o[n][2 * r] * inv, o[n][2 * r + 1] * inv);
+                    finite &= fabsf(f.x) < CUDART_INF_F && fabsf(f.y) < CUDART_INF_F;
+                    if (row < rows) *reinterpret_cast<__half2*>(out + n * 16) = __floats2half2_rn(f.x, f.y);
+                }
+                const unsigned not_finite = __ballot_sync(FULL, row < rows && !finite);
+                #pragma unroll
+                for (int e = 0; e < 8; ++e)                    // (lanes 4 e .. 4 e + 3: row e)
+                    if (not_finite >> (4 * e) & 15u) odd |= 1u << (e + 8 * r);
+            }
+            #pragma unroll 1
+            for (__syncwarp(); odd; odd &= odd - 1) {          // as redo_rows
+                const int row = __ffs(odd) - 1;
+                attend_row<D, POOL>(a, unit.s, seq, row / a.G, unit.h * a.G + row % a.G);
+            }
+            continue;
         }
         // ---- this warp's part, where its last chunk was
         const int part_at = warp * C::WARP + (C::WIDEN ? C::STAGES : held) * C::STAGE;
@@ -463,9 +527,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1) query_few_kernel(const __grid_
         if (lane == 0) s_part[warp] = held >= 0 ? part_at : -1;
         __syncthreads();
         // ---- the CTA's part of the unit: to the output, or to the workspace
-        const bool whole = u0 >= g0 && u1 <= g1;
-        const int later = u0 < g0 ? 0 : 1, space = 2 * cta + later;
-        if (!whole) cross[later] = Cross{unit.s, unit.h, cta_of(u0), cta_of(u1 - 1)};
+        const bool whole = unit.c0 == 0 && unit.c1 == unit.n;
+        const int later = unit.c0 > 0 ? 0 : 1, space = 2 * cta + later;
+        if (!whole) {
+            const int first = unit.at + cost_of(unit.n);
+            cross[later] = Cross{unit.s, unit.h, cta_of(first), cta_of(first + unit.n - 1)};
+        }
         for (int e = tid; e < rows * (D / 4); e += kWarps * 32) {
             const int row = e / (D / 4), c4 = e % (D / 4);
             float mm = -CUDART_INF_F, ll = 0.f;
@@ -496,10 +563,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) query_few_kernel(const __grid_
         __syncthreads();
         if (whole && s_odd) redo_rows<D, POOL>(a, unit.s, seq, unit.h, &s_odd);
         if (held >= 0) ask();                                  // into the held stage
-        at = to;
-        if (at >= g1) break;
-        next_unit(unit);
-        unit.c = 0;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
 
