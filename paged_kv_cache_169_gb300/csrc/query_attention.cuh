@@ -67,12 +67,15 @@ __device__ __forceinline__ int2 row_range(const QueryArgs& a, const QuerySeq& q,
     return r.x < r.y ? r : make_int2(0, 0);
 }
 
-// The physical block of position j of sequence s; one outside the pool is reported and read as block 0.
-__device__ __forceinline__ int query_block(const QueryArgs& a, int s, int j) {
-    const int id = a.tables[static_cast<int64_t>(s) * a.max_blocks + (j >> a.log_b)];
+// A block id of a table; one outside the pool is reported and read as block 0.
+__device__ __forceinline__ int checked_block(const QueryArgs& a, int id) {
     if (static_cast<unsigned>(id) < static_cast<unsigned>(a.num_blocks)) return id;
     atomicOr(a.err, KV_DEVERR_BLOCK_ID);
     return 0;
+}
+// The physical block of position j of sequence s.
+__device__ __forceinline__ int query_block(const QueryArgs& a, int s, int j) {
+    return checked_block(a, a.tables[static_cast<int64_t>(s) * a.max_blocks + (j >> a.log_b)]);
 }
 
 // t = cap tanh(x) in log2 units for x = s kx: 1 - 2 / (e^2x + 1), exact to a few 2^-24 of the cap

@@ -8,12 +8,17 @@
 // zeros and not read); the part of a unit in a CTA is joined in shared memory, and what crosses CTAs through the
 // workspace by the CTA that finishes last, in two levels where there are more than kFan parts.  A short unit is one
 // warp's, with nothing to join, and the others go on.  Softmax as in the tensor-core kernel.
-//   float16   mma operands straight from the ring
-//   FP8, 4-bit  widened to float16 in a tile of the warp's own first
+// A lane's mma operands come straight from the ring as it stores them, in whatever order of elements and tokens that
+// gives (lane 4 g + t; the queries are loaded, and the result stored, in the same order):
+//   float16  ldmatrix; elements and tokens in order
+//   FP8      keys: the lane's D/4 codes from element t D/4 on; values: byte matrices transposed by ldmatrix, tokens 4 t ..
+//            4 t + 3, so column c of the n-th eight keys is token 4 (c / 2) + 2 n + c % 2
+//   4-bit    keys: as FP8, a word's nibbles i and i + 4 side by side; values: elements g D/8 .. of tokens 2 t and
+//            2 t + 1 side by side (the pool's own order), so column c of product n is element c D/8 + n
 #pragma once
 
 #include "query_attention.cuh"
-#include "widen.cuh"
+#include "int4.cuh"
 
 namespace kvp {
 
@@ -48,20 +53,17 @@ template <int D_, kv_dtype POOL_>
 struct FewCfg {
     static constexpr int D = D_;
     static constexpr kv_dtype POOL = POOL_;
-    static constexpr bool WIDEN = POOL != KV_F16;
     static constexpr int ROW = kRowBytes<D, POOL>;
     static constexpr int RAW = kChunk * ROW;                   // bytes of a chunk's keys (or values) as stored
     static constexpr int META = POOL == KV_FP8_E4M3 ? 16 : 0;  // two blocks' key and value scales
     static constexpr int STAGE = 2 * RAW + META;
     static constexpr int PART = kFewRows * D * 4;              // a warp's part of a unit
-    static constexpr int TILE = WIDEN ? PART : 0;              // widened keys and values: as many bytes
-    static_assert(!WIDEN || TILE == 2 * kChunk * D * 2, "a part fits where the widened chunk was");
-    static_assert(WIDEN || STAGE == PART, "a part fits in a stage");
+    static constexpr bool OWN_PART = STAGE < PART;             // beside the ring; else where the last chunk was
     static constexpr int TABLES = 3 * kFewSeqs * 4 + kWarps * kFewRows * 8;
     static constexpr int FIT = (226 * 1024 - 1024 - TABLES) / kWarps;
-    static constexpr int STAGES_FIT = (FIT - TILE) / STAGE;
+    static constexpr int STAGES_FIT = (FIT - (OWN_PART ? PART : 0)) / STAGE;
     static constexpr int STAGES = STAGES_FIT > 8 ? 8 : STAGES_FIT;
-    static constexpr int WARP = STAGES * STAGE + TILE;
+    static constexpr int WARP = STAGES * STAGE + (OWN_PART ? PART : 0);
     static constexpr int ML_OFF = kWarps * WARP, SEQ_OFF = ML_OFF + kWarps * kFewRows * 8;
     static constexpr int SMEM = SEQ_OFF + 3 * kFewSeqs * 4;
     static_assert(STAGES >= 2 && STAGE % 16 == 0 && WARP % 16 == 0, "ring");
@@ -244,22 +246,27 @@ __global__ void __launch_bounds__(kWarps * 32, 1) query_few_kernel(const __grid_
             if (filling) fill_c = first_chunk(fill, fill_no);
         }
     };
-    int ids[2];                                                // its (up to two) physical blocks, -1: not read
-    // blocks of the chunk's 8-token halves; loaded one chunk ahead
+    // the physical blocks of the chunk's 8-token halves, -1: not read; as the table has them, loaded a chunk ahead
+    // and looked at when they are used (at once, every chunk waited 700 cycles for each)
+    int ids[2];
+    bool used[2] = {false, false};
     auto look_up = [&]() {
-        ids[0] = ids[1] = -1;
+        used[0] = used[1] = false;
         if (!filling) return;
         const int lo = s_lo[fill.s], hi = s_hi[fill.s], j0 = (lo & -kChunk) + fill_c * kChunk;
         #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int first = max(j0 + 8 * i, lo);
-            if (first < min(j0 + 8 * i + 8, hi)) ids[i] = query_block(a, fill.s, first);
+            used[i] = first < min(j0 + 8 * i + 8, hi);
+            if (used[i]) ids[i] = a.tables[static_cast<int64_t>(fill.s) * a.max_blocks + (first >> a.log_b)];
         }
     };
     auto ask = [&]() {
         if (filling) {
             const int lo = s_lo[fill.s], hi = s_hi[fill.s], j0 = (lo & -kChunk) + fill_c * kChunk;
             const uint32_t st = ring32 + fill_slot * C::STAGE;
+            #pragma unroll
+            for (int i = 0; i < 2; ++i) ids[i] = used[i] ? checked_block(a, ids[i]) : -1;
             if constexpr (POOL == KV_INT4) {
                 constexpr int PIECES = Int4<D>::OCT / 16;      // of an oct: 8 tokens
                 #pragma unroll
@@ -275,17 +282,33 @@ __global__ void __launch_bounds__(kWarps * 32, 1) query_few_kernel(const __grid_
                 }
             } else {
                 constexpr int PIECES = C::ROW / 16, STEP = 32 / PIECES;        // of a token; tokens per instruction
-                const int e = lane % PIECES;
-                #pragma unroll
-                for (int r0 = 0; r0 < kChunk; r0 += STEP) {
-                    const int r = r0 + lane / PIECES, j = j0 + r;
-                    const int id = r < 8 ? ids[0] : ids[1];
-                    const bool read = id >= 0 && j >= lo && j < hi;
-                    const int64_t from = ((static_cast<int64_t>(max(id, 0)) * a.H + fill.h) * a.B + (j & (a.B - 1))) * C::ROW + e * 16;
-                    // float16 rows in swizzled pieces (ldmatrix), others as they are
-                    const uint32_t to = st + r * C::ROW + (C::WIDEN ? e : (e ^ (r & 7))) * 16;
-                    cp_async16_or_zero(to, a.kpool + (read ? from : 0), read);
-                    cp_async16_or_zero(to + C::RAW, a.vpool + (read ? from : 0), read);
+                const int e = lane % PIECES, r = lane / PIECES;
+                // rows of 128 bytes or more: pieces swizzled by the row; of 64 bytes: by pairs of rows
+                auto place = [&](int row) {
+                    return row * C::ROW + ((C::ROW >= 128 ? e ^ (row & 7) : e ^ (row >> 1 & 3)) << 4);
+                };
+                auto half_at = [&](int i) {                    // this lane's first byte of the i-th 8 tokens in the pool
+                    return ((static_cast<int64_t>(max(ids[i], 0)) * a.H + fill.h) * a.B + ((j0 + 8 * i) & (a.B - 1)) + (r & 7)) * C::ROW + e * 16;
+                };
+                if (ids[0] >= 0 && ids[1] >= 0 && j0 >= lo && j0 + kChunk <= hi) {
+                    int64_t at[2] = {half_at(0), half_at(1)};
+                    #pragma unroll
+                    for (int r0 = 0; r0 < kChunk; r0 += STEP) {
+                        // (STEP rows at a time of one half, or both halves at once: 16 rows)
+                        const int64_t from = STEP == 16 ? (r < 8 ? at[0] : at[1]) : at[r0 >> 3] + (r0 & 7) * C::ROW;
+                        cp_async16(st + place(r0 + r), a.kpool + from);
+                        cp_async16(st + C::RAW + place(r0 + r), a.vpool + from);
+                    }
+                } else {
+                    #pragma unroll 1
+                    for (int r0 = 0; r0 < kChunk; r0 += STEP) {
+                        const int row = r0 + r, j = j0 + row;
+                        const int id = row < 8 ? ids[0] : ids[1];
+                        const bool read = id >= 0 && j >= lo && j < hi;
+                        const int64_t from = read ? ((static_cast<int64_t>(id) * a.H + fill.h) * a.B + (j & (a.B - 1))) * C::ROW + e * 16 : 0;
+                        cp_async16_or_zero(st + place(row), a.kpool + from, read);
+                        cp_async16_or_zero(st + C::RAW + place(row), a.vpool + from, read);
+                    }
                 }
                 if constexpr (POOL == KV_FP8_E4M3) {
                     if (lane < 4) {                            // key scales of the halves, then value scales
@@ -348,13 +371,34 @@ __global__ void __launch_bounds__(kWarps * 32, 1) query_few_kernel(const __grid_
                 sees[r] = row_range(a, seq, i);
                 if (bias) slope[r] = a.slopes[hq] * kLog2e;
             }
-            const char* qr = a.q + static_cast<int64_t>(seq.first + (some ? i : 0)) * a.q_stride + hq * (D * 2) + t * 4;
-            #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                q[k][r] = some ? *reinterpret_cast<const uint32_t*>(qr + k * 32) : 0u;
-                q[k][r + 2] = some ? *reinterpret_cast<const uint32_t*>(qr + k * 32 + 16) : 0u;
+            const char* qr = a.q + static_cast<int64_t>(seq.first + (some ? i : 0)) * a.q_stride + hq * (D * 2);
+            if constexpr (POOL == KV_F16) {
+                #pragma unroll
+                for (int x = 0; x < D / 16; ++x) {
+                    q[x][r] = some ? *reinterpret_cast<const uint32_t*>(qr + x * 32 + t * 4) : 0u;
+                    q[x][r + 2] = some ? *reinterpret_cast<const uint32_t*>(qr + x * 32 + 16 + t * 4) : 0u;
+                }
+            } else {
+                #pragma unroll
+                for (int x = 0; x < D / 32; ++x) {             // 8 elements, two products
+                    const uint4 v = some ? *reinterpret_cast<const uint4*>(qr + t * (D / 2) + x * 16) : make_uint4(0, 0, 0, 0);
+                    if constexpr (POOL == KV_FP8_E4M3) {
+                        q[2 * x][r] = v.x;
+                        q[2 * x][r + 2] = v.y;
+                        q[2 * x + 1][r] = v.z;
+                        q[2 * x + 1][r + 2] = v.w;
+                    } else {                                   // elements i and i + 4
+                        q[2 * x][r] = __byte_perm(v.x, v.z, 0x5410);
+                        q[2 * x][r + 2] = __byte_perm(v.x, v.z, 0x7632);
+                        q[2 * x + 1][r] = __byte_perm(v.y, v.w, 0x5410);
+                        q[2 * x + 1][r + 2] = __byte_perm(v.y, v.w, 0x7632);
+                    }
+                }
             }
         }
+        // between these positions every row sees everything
+        const int all_from = __reduce_max_sync(FULL, max(g < rows ? sees[0].x : 0, g + 8 < rows ? sees[1].x : 0));
+        const int all_to = __reduce_min_sync(FULL, min(g < rows ? sees[0].y : 1 << 30, g + 8 < rows ? sees[1].y : 1 << 30));
         float o[D / 8][4];
         #pragma unroll
         for (int n = 0; n < D / 8; ++n)
@@ -368,23 +412,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) query_few_kernel(const __grid_
             __syncwarp();
             const char* st = ring + slot * C::STAGE;
             const int j0 = base + k * kChunk;
-            uint32_t kt = ring32 + slot * C::STAGE, vt = kt + C::RAW;
+            const uint32_t kt = ring32 + slot * C::STAGE, vt = kt + C::RAW;
             float ks[2] = {1.f, 1.f}, vs[2] = {1.f, 1.f};
-            if constexpr (C::WIDEN) {
-                char* const tile = ring + C::STAGES * C::STAGE;
-                widen_rows<D, POOL, false, kChunk, 32>(st, lo - j0, hi - j0, lane, [&](int r, int ch) {
-                    return reinterpret_cast<uint4*>(tile + r * (D * 2) + ((ch ^ (r & 7)) << 4));
-                });
-                widen_rows<D, POOL, true, kChunk, 32>(st + C::RAW, lo - j0, hi - j0, lane, [&](int r, int ch) {
-                    return reinterpret_cast<uint4*>(tile + kChunk * D * 2 + r * (D * 2) + ((ch ^ (r & 7)) << 4));
-                });
-                kt = ring32 + C::STAGES * C::STAGE;
-                vt = kt + kChunk * D * 2;
-                if constexpr (POOL == KV_FP8_E4M3) {
-                    const float4 f = *reinterpret_cast<const float4*>(st + 2 * C::RAW);
-                    ks[0] = f.x; ks[1] = f.y; vs[0] = f.z; vs[1] = f.w;
-                }
-                __syncwarp();
+            if constexpr (POOL == KV_FP8_E4M3) {
+                const float4 f = *reinterpret_cast<const float4*>(st + 2 * C::RAW);
+                ks[0] = f.x; ks[1] = f.y; vs[0] = f.z; vs[1] = f.w;
             }
             // ---- scores: 16 rows by two times 8 keys
             float sc[2][4];
@@ -392,26 +424,72 @@ __global__ void __launch_bounds__(kWarps * 32, 1) query_few_kernel(const __grid_
             for (int n = 0; n < 2; ++n) {
                 #pragma unroll
                 for (int e = 0; e < 4; ++e) sc[n][e] = 0.f;
-                const int r = n * 8 + (lane & 7);
-                #pragma unroll
-                for (int k4 = 0; k4 < D / 32; ++k4) {
-                    uint32_t b[4];
-                    ldsm_x4(kt + r * (D * 2) + (((k4 * 4 + (lane >> 3)) ^ (r & 7)) << 4), b);
-                    mma_16816(sc[n], q[2 * k4][0], q[2 * k4][1], q[2 * k4][2], q[2 * k4][3], b[0], b[1]);
-                    mma_16816(sc[n], q[2 * k4 + 1][0], q[2 * k4 + 1][1], q[2 * k4 + 1][2], q[2 * k4 + 1][3], b[2], b[3]);
+                if constexpr (POOL == KV_F16) {
+                    const int r = n * 8 + (lane & 7);
+                    #pragma unroll
+                    for (int x = 0; x < D / 32; ++x) {
+                        uint32_t b[4];
+                        ldsm_x4(kt + r * (D * 2) + (((x * 4 + (lane >> 3)) ^ (r & 7)) << 4), b);
+                        mma_16816(sc[n], q[2 * x][0], q[2 * x][1], q[2 * x][2], q[2 * x][3], b[0], b[1]);
+                        mma_16816(sc[n], q[2 * x + 1][0], q[2 * x + 1][1], q[2 * x + 1][2], q[2 * x + 1][3], b[2], b[3]);
+                    }
+                } else {
+                    uint32_t w[D / 32][2];                     // 8 codes (FP8), or two words of 8 nibbles each
+                    if constexpr (POOL == KV_FP8_E4M3) {
+                        const int r = 4 * (g >> 1) + 2 * n + (g & 1);
+                        #pragma unroll
+                        for (int x = 0; x < D / 64; ++x) {
+                            const int piece = t * (D / 64) + x;
+                            const uint4 v = *reinterpret_cast<const uint4*>(
+                                st + r * C::ROW + ((C::ROW >= 128 ? piece ^ (r & 7) : piece ^ (r >> 1 & 3)) << 4));
+                            w[2 * x][0] = v.x; w[2 * x][1] = v.y; w[2 * x + 1][0] = v.z; w[2 * x + 1][1] = v.w;
+                        }
+                    }
+                    if constexpr (POOL == KV_FP8_E4M3) {
+                        #pragma unroll
+                        for (int x = 0; x < D / 32; ++x) {
+                            #pragma unroll
+                            for (int y = 0; y < 2; ++y)
+                                mma_16816(sc[n], q[2 * x + y][0], q[2 * x + y][1], q[2 * x + y][2], q[2 * x + y][3],
+                                          e4m3x2_to_half2_bits(static_cast<uint16_t>(w[x][y])),
+                                          e4m3x2_to_half2_bits(static_cast<uint16_t>(w[x][y] >> 16)));
+                        }
+                    } else {
+                        const char* oct = st + n * Int4<D>::OCT;
+                        uint32_t words[D / 32];
+                        if constexpr (D == 128) {
+                            const uint4 v = *reinterpret_cast<const uint4*>(oct + lane * 16);
+                            words[0] = v.x; words[1] = v.y; words[2] = v.z; words[3] = v.w;
+                        } else {
+                            const uint2 v = *reinterpret_cast<const uint2*>(oct + lane * 8);
+                            words[0] = v.x; words[1] = v.y;
+                        }
+                        // the scales of the lane's D/64 groups of 16
+                        const uint32_t sb = D == 128 ? *reinterpret_cast<const uint16_t*>(oct + Int4<D>::CODES + lane * 2)
+                                                     : *reinterpret_cast<const uint8_t*>(oct + Int4<D>::CODES + lane);
+                        #pragma unroll
+                        for (int x = 0; x < D / 32; ++x) {
+                            const uint32_t s = x < 2 ? sb & 0xFFu : sb >> 8;
+                            uint32_t p[4];
+                            int4_expand_full(words[x], s << 7 | s << 23, p);
+                            mma_16816(sc[n], q[2 * x][0], q[2 * x][1], q[2 * x][2], q[2 * x][3], p[0], p[1]);
+                            mma_16816(sc[n], q[2 * x + 1][0], q[2 * x + 1][1], q[2 * x + 1][2], q[2 * x + 1][3], p[2], p[3]);
+                        }
+                    }
                 }
             }
+            const bool masked = j0 < all_from || j0 + kChunk > all_to;
             #pragma unroll
             for (int n = 0; n < 2; ++n)
                 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int r = e >> 1, j = j0 + n * 8 + 2 * t + (e & 1);
+                    const int r = e >> 1, j = j0 + (POOL == KV_FP8_E4M3 ? 4 * t + 2 * n : n * 8 + 2 * t) + (e & 1);
                     float v = sc[n][e];
-                    if constexpr (POOL == KV_FP8_E4M3) v *= ks[n];
+                    if constexpr (POOL == KV_FP8_E4M3) v *= t < 2 ? ks[0] : ks[1];
                     if (cap) v = capped(v, k2, capl);
                     if (bias) v = fmaf(-slope[r], fabsf(static_cast<float>(pos[r] - j)), cap ? v : v * qscale);
                     v *= c;
-                    sc[n][e] = j >= sees[r].x && j < sees[r].y ? v : -CUDART_INF_F;
+                    sc[n][e] = !masked || (j >= sees[r].x && j < sees[r].y) ? v : -CUDART_INF_F;
                 }
             // ---- the base follows the maximum only when it is left behind by more than 2^8
             float top[2];
@@ -458,20 +536,59 @@ __global__ void __launch_bounds__(kWarps * 32, 1) query_few_kernel(const __grid_
                     float y0 = ex2_approx(sc[n][2 * r] + off), y1 = ex2_approx(sc[n][2 * r + 1] + off);
                     l[r] += y0 + y1;
                     if constexpr (POOL == KV_FP8_E4M3) {
-                        const float f = vs[n] * inv_vref;
+                        const float f = (t < 2 ? vs[0] : vs[1]) * inv_vref;
                         y0 *= f;
                         y1 *= f;
                     }
                     const __half2 hv = __floats2half2_rn(y0, y1);
                     w[2 * n + r] = *reinterpret_cast<const uint32_t*>(&hv);
                 }
-            const int vr = lane & 15;
-            #pragma unroll
-            for (int n = 0; n < D / 16; ++n) {
-                uint32_t b[4];
-                ldsm_x4_t(vt + vr * (D * 2) + (((2 * n + (lane >> 4)) ^ (vr & 7)) << 4), b);
-                mma_16816(o[2 * n], w[0], w[1], w[2], w[3], b[0], b[1]);
-                mma_16816(o[2 * n + 1], w[0], w[1], w[2], w[3], b[2], b[3]);
+            if constexpr (POOL == KV_F16) {
+                const int vr = lane & 15;
+                #pragma unroll
+                for (int n = 0; n < D / 16; ++n) {
+                    uint32_t b[4];
+                    ldsm_x4_t(vt + vr * (D * 2) + (((2 * n + (lane >> 4)) ^ (vr & 7)) << 4), b);
+                    mma_16816(o[2 * n], w[0], w[1], w[2], w[3], b[0], b[1]);
+                    mma_16816(o[2 * n + 1], w[0], w[1], w[2], w[3], b[2], b[3]);
+                }
+            } else if constexpr (POOL == KV_FP8_E4M3) {
+                const int vr = lane & 15;
+                #pragma unroll
+                for (int n = 0; n < D / 32; ++n) {             // two matrices of 16 tokens by 16 elements
+                    uint32_t b[4];
+                    const int piece = 2 * n + (lane >> 4);
+                    ldsm_b8_x2_t(vt + vr * C::ROW + ((C::ROW >= 128 ? piece ^ (vr & 7) : piece ^ (vr >> 1 & 3)) << 4), b);
+                    #pragma unroll
+                    for (int y = 0; y < 4; ++y)
+                        mma_16816(o[4 * n + y], w[0], w[1], w[2], w[3], e4m3x2_to_half2_bits(static_cast<uint16_t>(b[y])),
+                                  e4m3x2_to_half2_bits(static_cast<uint16_t>(b[y] >> 16)));
+                }
+            } else {
+                uint32_t words[2][D / 32], scales[2];
+                #pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const char* oct = st + C::RAW + n * Int4<D>::OCT;
+                    if constexpr (D == 128) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(oct + lane * 16);
+                        words[n][0] = v.x; words[n][1] = v.y; words[n][2] = v.z; words[n][3] = v.w;
+                    } else {
+                        const uint2 v = *reinterpret_cast<const uint2*>(oct + lane * 8);
+                        words[n][0] = v.x; words[n][1] = v.y;
+                    }
+                    // tokens 2 t and 2 t + 1 of the lane's group; 0 where no row sees them (what lies there may be anything)
+                    const uint32_t sb = *reinterpret_cast<const uint16_t*>(oct + Int4<D>::CODES + (D == 128 ? g : g >> 1) * 8 + 2 * t);
+                    const int j = j0 + n * 8 + 2 * t;
+                    scales[n] = (j >= lo && j < hi ? (sb & 0xFFu) << 7 : 0u) | (j + 1 >= lo && j + 1 < hi ? (sb & 0xFF00u) << 15 : 0u);
+                }
+                #pragma unroll
+                for (int x = 0; x < D / 32; ++x) {
+                    uint32_t p0[4], p1[4];
+                    int4_expand_full(words[0][x], scales[0], p0);
+                    int4_expand_full(words[1][x], scales[1], p1);
+                    #pragma unroll
+                    for (int y = 0; y < 4; ++y) mma_16816(o[4 * x + y], w[0], w[1], w[2], w[3], p0[y], p1[y]);
+                }
             }
             held = slot;
             slot = slot + 1 == C::STAGES ? 0 : slot + 1;
@@ -486,13 +603,17 @@ __global__ void __launch_bounds__(kWarps * 32, 1) query_few_kernel(const __grid_
                 l[r] += __shfl_xor_sync(FULL, l[r], 2);
                 const int row = g + 8 * r;
                 const float inv = (l[r] == 0.f ? 0.f : 1.f / l[r]) * (POOL == KV_FP8_E4M3 ? vref : 1.f);
-                char* out = a.out + static_cast<int64_t>(seq.first + row / a.G) * a.out_stride + (unit.h * a.G + row % a.G) * (D * 2) + t * 4;
+                char* out = a.out + static_cast<int64_t>(seq.first + row / a.G) * a.out_stride + (unit.h * a.G + row % a.G) * (D * 2);
                 bool finite = true;
                 #pragma unroll
                 for (int n = 0; n < D / 8; ++n) {
-                    const float2 f = l[r] == 0.f ? make_float2(0.f, 0.f) : make_float2(o[n][2 * r] * inv, o[n][2 * r + 1] * inv);
+                    const int n0 = n & ~1;
+                    float2 f = POOL != KV_INT4 ? make_float2(o[n][2 * r], o[n][2 * r + 1])
+                                               : make_float2(o[n0][2 * r + (n & 1)], o[n0 + 1][2 * r + (n & 1)]);
+                    f = l[r] == 0.f ? make_float2(0.f, 0.f) : make_float2(f.x * inv, f.y * inv);
                     finite &= fabsf(f.x) < CUDART_INF_F && fabsf(f.y) < CUDART_INF_F;
-                    if (row < rows) *reinterpret_cast<__half2*>(out + n * 16) = __floats2half2_rn(f.x, f.y);
+                    const int at = POOL != KV_INT4 ? 8 * n + 2 * t : (2 * t + (n & 1)) * (D / 8) + n0;
+                    if (row < rows) *reinterpret_cast<__half2*>(out + at * 2) = __floats2half2_rn(f.x, f.y);
                 }
                 const unsigned not_finite = __ballot_sync(FULL, row < rows && !finite);
                 #pragma unroll
@@ -507,7 +628,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) query_few_kernel(const __grid_
             continue;
         }
         // ---- this warp's part, where its last chunk was
-        const int part_at = warp * C::WARP + (C::WIDEN ? C::STAGES : held) * C::STAGE;
+        const int part_at = warp * C::WARP + (C::OWN_PART ? C::STAGES : held) * C::STAGE;
         if (held >= 0) {
             char* const part = smem + part_at;
             #pragma unroll
@@ -517,11 +638,21 @@ __global__ void __launch_bounds__(kWarps * 32, 1) query_few_kernel(const __grid_
                 const int row = g + 8 * r;
                 if (row >= rows) continue;
                 if (t == 0) s_ml[warp * kFewRows + row] = make_float2(m[r], l[r]);
+                const float mul = POOL == KV_FP8_E4M3 ? vref : 1.f;
                 #pragma unroll
-                for (int n = 0; n < D / 8; ++n)
-                    *reinterpret_cast<float2*>(part + row * (D * 4) + (((2 * n + (t >> 1)) ^ (row & 7)) << 4) + (t & 1) * 8) =
-                        POOL == KV_FP8_E4M3 ? make_float2(o[n][2 * r] * vref, o[n][2 * r + 1] * vref)
-                                            : make_float2(o[n][2 * r], o[n][2 * r + 1]);
+                for (int n = 0; n < D / 8; n += 2) {
+                    if constexpr (POOL != KV_INT4) {
+                        #pragma unroll
+                        for (int y = n; y < n + 2; ++y)
+                            *reinterpret_cast<float2*>(part + row * (D * 4) + (((2 * y + (t >> 1)) ^ (row & 7)) << 4) + (t & 1) * 8) =
+                                make_float2(o[y][2 * r] * mul, o[y][2 * r + 1] * mul);
+                    } else if (n % 4 == 0) {
+                        #pragma unroll
+                        for (int y = 0; y < 2; ++y)
+                            *reinterpret_cast<float4*>(part + row * (D * 4) + ((((2 * t + y) * (D / 32) + n / 4) ^ (row & 7)) << 4)) =
+                                make_float4(o[n][2 * r + y], o[n + 1][2 * r + y], o[n + 2][2 * r + y], o[n + 3][2 * r + y]);
+                    }
+                }
             }
         }
         if (lane == 0) s_part[warp] = held >= 0 ? part_at : -1;
