@@ -1,6 +1,8 @@
 // paged_query_attention for many rows: the tensor-core kernel.
 #pragma once
 
+#include <type_traits>
+
 #include "query_attention.cuh"
 #include "tcgen05.cuh"
 #include "widen.cuh"
@@ -94,21 +96,30 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* er
 }
 
 // Steps [a, b) of each row tile, numbered from position `base`; key tiles are pairs of them, and the work item's those
-// that either row tile needs.
+// that either row tile needs.  With a distance bias they are taken from the last one down: it lowers the scores on the
+// way, and the softmax's base, once found, stays (upwards, steep heads raise it at every step: 313 us for packed 4-bit
+// documents, 250 downwards).  Without one upwards: a causal tile's rows then find their base in the same step (a 2048-token
+// prompt takes 5% longer downwards).
+template <bool DOWN>
 struct KeySteps {
     int base, end, a0, b0, a1, b1, n;                          // n: key tiles
     __device__ __forceinline__ int a(int t) const { return t ? a1 : a0; }
     __device__ __forceinline__ int b(int t) const { return t ? b1 : b0; }
     __device__ __forceinline__ bool on(int t, int step) const { return step >= a(t) && step < b(t); }
     __device__ __forceinline__ bool tile_on(int j) const { return on(0, 2 * j) || on(0, 2 * j + 1) || on(1, 2 * j) || on(1, 2 * j + 1); }
-    __device__ __forceinline__ int next(int j) const {         // the first of the item's key tiles from j on
-        while (j < n && !tile_on(j)) ++j;
+    __device__ __forceinline__ bool is(int j) const { return j >= 0 && j < n; }
+    __device__ __forceinline__ int from(int j) const {         // j, or the first of the item's key tiles after it
+        while (is(j) && !tile_on(j)) j += DOWN ? -1 : 1;
         return j;
     }
-    __device__ __forceinline__ int before(int j) const {       // how many of them lie before j
+    __device__ __forceinline__ int first() const { return from(DOWN ? n - 1 : 0); }
+    __device__ __forceinline__ int next(int j) const { return from(DOWN ? j - 1 : j + 1); }
+    __device__ __forceinline__ int below(int j) const {        // how many of them are less than j
         const int p0 = a0 >> 1, q0 = (b0 + 1) >> 1, p1 = a1 >> 1, q1 = (b1 + 1) >> 1;
         return max(0, min(q0, j) - p0) + max(0, min(q1, j) - p1) - max(0, min(min(q0, q1), j) - max(p0, p1));
     }
+    __device__ __forceinline__ int tiles() const { return below(n); }
+    __device__ __forceinline__ int before(int j) const { return DOWN ? tiles() - below(j + 1) : below(j); }
 };
 
 // A work item: a pair of row tiles of a (sequence, K/V head).  s < 0: there are no more.
@@ -125,8 +136,9 @@ struct PromptMisc {
 };
 static_assert(sizeof(PromptMisc) <= 160, "PromptCfg::SMEM");
 
-__device__ __forceinline__ KeySteps key_steps(const Item& x, int block) {
-    KeySteps k;
+template <bool DOWN>
+__device__ __forceinline__ KeySteps<DOWN> key_steps(const Item& x, int block) {
+    KeySteps<DOWN> k;
     k.base = min(x.lo[0], x.lo[1]) & -block;
     k.end = max(x.hi[0], x.hi[1]);
     auto from = [&](int t) { return x.lo[t] < x.hi[t] ? (x.lo[t] - k.base) / kStep : 0; };
@@ -158,7 +170,7 @@ __device__ __forceinline__ int claimed_item(const uint4& v) {
     return x;
 }
 
-template <int D, kv_dtype POOL>
+template <int D, kv_dtype POOL, bool BIAS>
 __global__ void __launch_bounds__(PromptCfg<D, POOL>::WARPS * 32, 1)
 query_prompt_kernel(const __grid_constant__ PromptArgs p) {
     using C = PromptCfg<D, POOL>;
@@ -221,7 +233,7 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
     bool fine = true;                                          // no wait of this warp has run out
     int count = 0;                                             // items so far
     Item it;
-    KeySteps keys;
+    KeySteps<BIAS> keys;
     auto wait = [&](uint32_t b, int times) {                   // for the barrier's times-th completion (from 0)
         fine = fine && warp_wait(b, times & 1, a.err);
         return fine;
@@ -246,7 +258,7 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
         __syncwarp();
         if (lane == 0) mbar_arrive(item_free(i));
         ++count;
-        keys = key_steps(it, a.B);
+        keys = key_steps<BIAS>(it, a.B);
         return it.s >= 0;
     };
 
@@ -256,29 +268,32 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
         const int rt = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;          // the warp's 32 lanes
         const uint32_t st = tmem + lanes + rt * kTile, ot = tmem + lanes + 2 * kTile + rt * D;
-        const bool bias = a.slopes != nullptr, cap = a.cap > 0.f;
+        const bool cap = a.cap > 0.f;
+        constexpr int DIR = BIAS ? -1 : 1;                     // of the steps
         const float qscale = a.scale * kLog2e;
         const float k2 = cap ? 2.f * kLog2e * (a.scale / a.cap) : 0.f, capl = a.cap * kLog2e;
-        const float c = cap || bias ? 1.f : qscale;            // scores to log2 units
+        const float c = cap || BIAS ? 1.f : qscale;            // scores to log2 units
         int i = 0, even = 0, tiles = 0;                        // this row tile's steps so far, the even ones; the items' tiles
         // An item's part of this thread, taken while the last products of the item before are made.  (The rest stays in
         // shared memory until the result is out: registers are short here.)
         struct Part {
-            int step, to_step, j0, pos;                        // the row tile's steps; the first one's position; the row's
+            int step, stop, j0, pos;                           // the row tile's steps; the first one's position; the row's
             int2 sees;
             float slope, inv_vref;
+            int tile;                                          // FP8: the number of the item's first tile, less ± its index
         } next;
         auto fetch = [&]() {
             if (!wait(item_there(count & 1), count >> 1)) return false;
             const Item& x = misc->item[count & 1];
             if (uniform(x.s) < 0) return false;
-            const KeySteps k = key_steps(x, a.B);
-            next.step = uniform(k.a(rt));
-            next.to_step = uniform(k.b(rt));
+            const auto k = key_steps<BIAS>(x, a.B);
+            next.step = BIAS ? uniform(k.b(rt)) - 1 : uniform(k.a(rt));
+            next.stop = BIAS ? uniform(k.a(rt)) - 1 : uniform(k.b(rt));
             next.j0 = uniform(k.base) + next.step * kStep;
+            if (POOL == KV_FP8_E4M3) next.tile = k.before(next.step >> 1) - DIR * (next.step >> 1);
             const int token = x.token + rt * per_tile + (row >> log_g);
             next.sees = token < x.n ? row_range(a, QuerySeq{x.first, x.n, x.ctx}, token) : make_int2(0, 0);
-            next.slope = bias ? a.slopes[x.head * a.G + (row & (a.G - 1))] * kLog2e : 0.f;
+            next.slope = BIAS ? a.slopes[x.head * a.G + (row & (a.G - 1))] * kLog2e : 0.f;
             next.pos = x.ctx - x.n + token;
             next.inv_vref = POOL == KV_FP8_E4M3 ? 1.f / x.vref : 1.f;
             return true;
@@ -288,13 +303,15 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
         while (some_item) {
             const Item& x0 = misc->item[count & 1];
             int step = next.step, j0 = next.j0;
-            const int to_step = next.to_step, pos = next.pos;
+            const int stop = next.stop, pos = next.pos;
             const int2 sees = next.sees;
             const float slope = next.slope, inv_vref = next.inv_vref;
             float m = -CUDART_INF_F, l = 0.f;                  // the base (log2 units) and the sum of weights
             const int i0 = i;
+            // (a row tile's key tiles follow one another)
+            const int tile0 = POOL == KV_FP8_E4M3 ? tiles + next.tile : 0;
             #pragma unroll 1
-            for (; step < to_step; ++step, ++i, j0 += kStep) {
+            for (; step != stop; ++i, step += DIR, j0 += DIR * kStep) {
                 const int h = step & 1;
                 if (!wait(s_there(rt, h), h ? i - even : even)) break;
                 even += 1 - h;
@@ -307,7 +324,7 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                 tmem_wait_load32(xr);
                 tmem_wait_load32(xr + 32);
                 const float* const scales = POOL == KV_FP8_E4M3
-                    ? factors + (tiles + key_steps(x0, a.B).before(step >> 1)) % kFactorTiles * 32 + (h * kStep >> a.log_b) : nullptr;
+                    ? factors + (tile0 + DIR * (step >> 1)) % kFactorTiles * 32 + (h * kStep >> a.log_b) : nullptr;
                 if constexpr (POOL == KV_FP8_E4M3) {
                     #pragma unroll
                     for (int k = 0; k < kStep; k += 8) {
@@ -320,7 +337,7 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                     #pragma unroll
                     for (int k = 0; k < kStep; ++k) x[k] = capped(x[k], k2, capl);
                 }
-                if (bias) {
+                if (BIAS) {
                     const float from = static_cast<float>(pos - j0), mul = cap ? 1.f : qscale;
                     #pragma unroll
                     for (int k = 0; k < kStep; ++k) x[k] = fmaf(-slope, fabsf(from - static_cast<float>(k)), x[k] * mul);
@@ -395,12 +412,12 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
             }
             if (!fine) break;
             const Item it = x0;
-            const int it_tiles = POOL == KV_FP8_E4M3 ? key_steps(x0, a.B).before(1 << 30) : 0;
+            const int it_tiles = POOL == KV_FP8_E4M3 ? key_steps<BIAS>(x0, a.B).tiles() : 0;
             __syncwarp();
             if (lane == 0) mbar_arrive(item_free(count & 1));
             ++count;
             some_item = fetch();
-            if (!fine || (i > i0 && !wait(o_there(rt, (step - 1) & 1), (step & 1 ? even : i - even) - 1))) break;
+            if (!fine || (i > i0 && !wait(o_there(rt, (step - DIR) & 1), (step & 1 ? even : i - even) - 1))) break;
             tc_fence_after();
             // the result, 64 elements at a time through shared memory, so that a store writes whole lines
             const int token = it.token + rt * per_tile + (row >> log_g);
@@ -469,7 +486,7 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
             int ring = 0;
             while (next_item()) {
                 #pragma unroll 1
-                for (int j = keys.next(0); fine && j < keys.n; j = keys.next(j + 1)) {
+                for (int j = keys.first(); fine && keys.is(j); j = keys.next(j)) {
                     const int rows = min(kTile, keys.end - (keys.base + j * kTile));
                     #pragma unroll
                     for (int kv = 0; kv < 2; ++kv, ++ring) {
@@ -527,24 +544,27 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                 if (used) tc_commit(empty(at));
                 else mbar_arrive(empty(at));
             };
-            int j = keys.next(0);
-            bool on0 = on(2 * j), on1 = on(2 * j + 1);
-            if (j < keys.n) {
+            constexpr int h0 = BIAS, h1 = 1 - h0;             // a key tile's steps in their order
+            auto nth = [&](int h) { return h ? i - even : even; };             // steps of this parity so far
+            auto is_last = [&](int at) { return BIAS ? a_t >= 2 * at : b_t <= 2 * at + 2; };
+            int j = keys.first();
+            bool on0 = on(2 * j + h0), on1 = on(2 * j + h1);
+            if (keys.is(j)) {
                 if (!wait3(full(ring.slot), ring.times, q_there(t), count - 1, full(ring.slot), ring.times)) break;
                 if (elect_one()) {
-                    if (on0) scores(ring.slot, 0);
-                    if (on1) scores(ring.slot, 1);
+                    if (on0) scores(ring.slot, h0);
+                    if (on1) scores(ring.slot, h1);
                     leave(ring.slot, on0 || on1);
-                    if ((on0 || on1) && b_t <= 2 * j + 2) tc_commit(q_free(t));
+                    if ((on0 || on1) && is_last(j)) tc_commit(q_free(t));
                 }
                 __syncwarp();
             } else if (!wait(q_there(t), count - 1)) {
                 break;
             }
             #pragma unroll 1
-            while (j < keys.n) {                               // (this tile's scores are issued)
-                const int jn = keys.next(j + 1);
-                const bool more = jn < keys.n, next0 = more && on(2 * jn), next1 = more && on(2 * jn + 1);
+            while (keys.is(j)) {                               // (this tile's scores are issued)
+                const int jn = keys.next(j);
+                const bool more = keys.is(jn), next0 = more && on(2 * jn + h0), next1 = more && on(2 * jn + h1);
                 ring.advance();
                 const int v = ring.slot, v_times = ring.times;
                 ring.advance();
@@ -556,29 +576,30 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                                   i > i0 || k > 0);
                     tc_commit(o_there(t, h));
                 };
-                // its values, the next tile's keys and the even step's weights; then the odd step's weights
+                // its values, the next tile's keys and the first step's weights; then the second step's weights
                 if (!wait3(full(v), v_times, more ? full(ring.slot) : full(v), more ? ring.times : v_times,
-                           on0 ? w_there(t, 0) : full(v), on0 ? even : v_times))
+                           on0 ? w_there(t, h0) : full(v), on0 ? nth(h0) : v_times))
                     break;
                 tc_fence_after();
                 if (elect_one()) {
-                    if (on0) values(0);
-                    if (next0) scores(ring.slot, 0);
+                    if (on0) values(h0);
+                    if (next0) scores(ring.slot, h0);
                 }
                 __syncwarp();
-                even += on0;
                 i += on0;
-                if (on1 && !wait(w_there(t, 1), i - even)) break;
+                even += on0 && h0 == 0;
+                if (on1 && !wait(w_there(t, h1), nth(h1))) break;
                 tc_fence_after();
                 if (elect_one()) {
-                    if (on1) values(1);
-                    if (next1) scores(ring.slot, 1);
+                    if (on1) values(h1);
+                    if (next1) scores(ring.slot, h1);
                     leave(v, on0 || on1);
                     if (more) leave(ring.slot, next0 || next1);
-                    if ((next0 || next1) && b_t <= 2 * jn + 2) tc_commit(q_free(t));
+                    if ((next0 || next1) && is_last(jn)) tc_commit(q_free(t));
                 }
                 __syncwarp();
                 i += on1;
+                even += on1 && h1 == 0;
                 j = jn;
                 on0 = next0;
                 on1 = next1;
@@ -599,16 +620,16 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
         const uint32_t block_bytes = C::WIDEN ? a.B * kRowBytes<D, POOL> : a.B * D * 2;
         int ring = 0, edges = 0;
         while (next_item()) {
-            int j = keys.next(0);
+            int j = keys.first();
             // the tile's blocks are looked up a tile ahead
             auto look_up = [&](int at) {
                 const int x = keys.base + at * kTile + (blk << log_b);
-                return at < keys.n && blk << log_b < kTile && x < keys.end ? query_block(a, it.s, x) : -1;
+                return keys.is(at) && blk << log_b < kTile && x < keys.end ? query_block(a, it.s, x) : -1;
             };
             int id = look_up(j);
             #pragma unroll 1
-            while (fine && j < keys.n) {
-                const int rows = min(kTile, keys.end - (keys.base + j * kTile)), jn = keys.next(j + 1);
+            while (fine && keys.is(j)) {
+                const int rows = min(kTile, keys.end - (keys.base + j * kTile)), jn = keys.next(j);
                 const int next_id = look_up(jn);
                 const uint32_t bytes = ((rows + a.B - 1) >> log_b) * block_bytes;
                 if constexpr (POOL == KV_FP8_E4M3) {
@@ -785,12 +806,12 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
     }
 }
 
-template <typename C>
+template <typename C, bool BIAS>
 int launch_prompt_typed(const kv_pool* pool, const PromptArgs& p, bool pdl, cudaStream_t stream) {
     static unsigned long long attr_done = 0;               // the shared-memory opt-in is a per-device attribute
     const unsigned long long bit = 1ull << (pool->device & 63);
     if (!(attr_done & bit)) {
-        if (cudaFuncSetAttribute(query_prompt_kernel<C::D, C::POOL>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
+        if (cudaFuncSetAttribute(query_prompt_kernel<C::D, C::POOL, BIAS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
             cudaSuccess)
             return KV_ERR_CUDA;
         attr_done |= bit;
@@ -805,7 +826,7 @@ int launch_prompt_typed(const kv_pool* pool, const PromptArgs& p, bool pdl, cuda
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
-    if (cudaLaunchKernelEx(&cfg, query_prompt_kernel<C::D, C::POOL>, p) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, query_prompt_kernel<C::D, C::POOL, BIAS>, p) != cudaSuccess) {
         cudaGetLastError();
         return KV_ERR_CUDA;
     }
@@ -814,8 +835,11 @@ int launch_prompt_typed(const kv_pool* pool, const PromptArgs& p, bool pdl, cuda
 
 template <kv_dtype POOL>
 int launch_prompt_pool(const kv_pool* pool, const PromptArgs& p, bool pdl, cudaStream_t stream) {
-    return pool->desc.head_dim == 128 ? launch_prompt_typed<PromptCfg<128, POOL>>(pool, p, pdl, stream)
-                                      : launch_prompt_typed<PromptCfg<64, POOL>>(pool, p, pdl, stream);
+    auto launch = [&](auto bias) {
+        return pool->desc.head_dim == 128 ? launch_prompt_typed<PromptCfg<128, POOL>, bias.value>(pool, p, pdl, stream)
+                                          : launch_prompt_typed<PromptCfg<64, POOL>, bias.value>(pool, p, pdl, stream);
+    };
+    return p.a.slopes ? launch(std::true_type{}) : launch(std::false_type{});
 }
 
 }  // namespace
