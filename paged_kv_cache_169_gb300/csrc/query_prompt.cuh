@@ -22,8 +22,8 @@ int launch_query_prompt_int4(const kv_pool* pool, const PromptArgs& p, bool pdl,
 namespace {
 
 constexpr int kTile = 128;             // rows of a row tile and keys of a key tile
-constexpr int kStep = 64;              // keys of a softmax step: the matrix products of one run while the other is weighed
-constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kLoadWarp = 10, kItemWarp = 11, kWidenWarp = 12;
+constexpr int kHalf = 64;              // keys of a tile that a softmax thread weighs
+constexpr int kSoftmaxWarps = 16, kMmaWarp = 16, kLoadWarp = 17, kItemWarp = 18, kWidenWarp = 20;      // (19: none)
 constexpr int kFactorTiles = 8;        // key tiles whose FP8 scales are kept (more than are in flight)
 
 template <int D_, kv_dtype POOL_>
@@ -39,16 +39,16 @@ struct PromptCfg {
     static constexpr int SLOTS = D == 128 ? (WIDEN ? 3 : 4) : 8;
     static constexpr int RAWS = WIDEN ? (D == 128 ? 2 : 4) : 0;
     static constexpr int RAW = WIDEN ? kTile * kRowBytes<D, POOL> : 0;
-    // Registers: 168 (12 warps) or 128 (16 warps) per thread at launch, shared out by fours of warps
-    static constexpr int WARPS = WIDEN ? 16 : 12;
-    static constexpr int REGS_SOFTMAX = WIDEN ? 200 : 208, REGS_ISSUE = WIDEN ? 56 : 88, REGS_WIDEN = 56;
-    static_assert(WIDEN ? 2 * REGS_SOFTMAX + REGS_ISSUE + REGS_WIDEN <= 512 : 2 * REGS_SOFTMAX + REGS_ISSUE <= 504, "registers");
+    // Registers: 96 (20 warps) or 80 (24 warps) per thread at launch, shared out by fours of warps
+    static constexpr int WARPS = WIDEN ? 24 : 20;
+    static constexpr int REGS_SOFTMAX = WIDEN ? 96 : 104, REGS_ISSUE = WIDEN ? 48 : 64, REGS_WIDEN = 48;
+    static_assert(WIDEN ? 4 * REGS_SOFTMAX + REGS_ISSUE + REGS_WIDEN <= 6 * 80 : 4 * REGS_SOFTMAX + REGS_ISSUE <= 5 * 96, "registers");
     static constexpr int Q_OFF = 0, KV_OFF = 2 * TILE, RAW_OFF = KV_OFF + SLOTS * TILE;
-    static constexpr int OUT_OFF = RAW_OFF + RAWS * RAW;       // 64 elements of a softmax warp's 32 rows on their way out
-    static constexpr int FACTOR_OFF = OUT_OFF + kSoftmaxWarps * 32 * 128;
+    static constexpr int OUT_OFF = RAW_OFF + RAWS * RAW;       // 32 elements of a softmax warp's 32 rows on their way out
+    static constexpr int FACTOR_OFF = OUT_OFF + kSoftmaxWarps * 32 * 64;
     static constexpr int FACTORS = POOL == KV_FP8_E4M3 ? kFactorTiles * 2 * 16 * 4 : 0;
     static constexpr int BAR_OFF = FACTOR_OFF + FACTORS;
-    static constexpr int BARS = 2 * SLOTS + 2 * RAWS + 8 * 2 + 2 * 2 + 3;
+    static constexpr int BARS = 2 * SLOTS + 2 * RAWS + 5 * 2 + 2 * 2 + 3;
     static constexpr int MISC_OFF = (BAR_OFF + BARS * 8 + 15) / 16 * 16;
     static constexpr int SMEM = MISC_OFF + 160 + 1024;         // and up to 1024 bytes of alignment
     static_assert(SMEM <= 227 * 1024, "shared memory");
@@ -95,28 +95,25 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* er
     return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, err));
 }
 
-// Steps [a, b) of each row tile, numbered from position `base`; key tiles are pairs of them, and the work item's those
-// that either row tile needs.  With a distance bias they are taken from the last one down: it lowers the scores on the
-// way, and the softmax's base, once found, stays (upwards, steep heads raise it at every step: 313 us for packed 4-bit
-// documents, 250 downwards).  Without one upwards: a causal tile's rows then find their base in the same step (a 2048-token
-// prompt takes 5% longer downwards).
+// Key tiles [a, b) of each row tile, numbered from position `base`; the work item's are those that either row tile
+// needs.  With a distance bias they are taken from the last one down: it lowers the scores on the way, and the softmax's
+// base, once found, stays (upwards, steep heads raise it at every tile).  Without one upwards: the rows of a causal tile
+// then find their base in the same tile.
 template <bool DOWN>
-struct KeySteps {
-    int base, end, a0, b0, a1, b1, n;                          // n: key tiles
+struct KeyTiles {
+    int base, end, a0, b0, a1, b1, n;
     __device__ __forceinline__ int a(int t) const { return t ? a1 : a0; }
     __device__ __forceinline__ int b(int t) const { return t ? b1 : b0; }
-    __device__ __forceinline__ bool on(int t, int step) const { return step >= a(t) && step < b(t); }
-    __device__ __forceinline__ bool tile_on(int j) const { return on(0, 2 * j) || on(0, 2 * j + 1) || on(1, 2 * j) || on(1, 2 * j + 1); }
+    __device__ __forceinline__ bool on(int t, int j) const { return j >= a(t) && j < b(t); }
     __device__ __forceinline__ bool is(int j) const { return j >= 0 && j < n; }
     __device__ __forceinline__ int from(int j) const {         // j, or the first of the item's key tiles after it
-        while (is(j) && !tile_on(j)) j += DOWN ? -1 : 1;
+        while (is(j) && !on(0, j) && !on(1, j)) j += DOWN ? -1 : 1;
         return j;
     }
     __device__ __forceinline__ int first() const { return from(DOWN ? n - 1 : 0); }
     __device__ __forceinline__ int next(int j) const { return from(DOWN ? j - 1 : j + 1); }
     __device__ __forceinline__ int below(int j) const {        // how many of them are less than j
-        const int p0 = a0 >> 1, q0 = (b0 + 1) >> 1, p1 = a1 >> 1, q1 = (b1 + 1) >> 1;
-        return max(0, min(q0, j) - p0) + max(0, min(q1, j) - p1) - max(0, min(min(q0, q1), j) - max(p0, p1));
+        return max(0, min(b0, j) - a0) + max(0, min(b1, j) - a1) - max(0, min(min(b0, b1), j) - max(a0, a1));
     }
     __device__ __forceinline__ int tiles() const { return below(n); }
     __device__ __forceinline__ int before(int j) const { return DOWN ? tiles() - below(j + 1) : below(j); }
@@ -137,18 +134,29 @@ struct PromptMisc {
 static_assert(sizeof(PromptMisc) <= 160, "PromptCfg::SMEM");
 
 template <bool DOWN>
-__device__ __forceinline__ KeySteps<DOWN> key_steps(const Item& x, int block) {
-    KeySteps<DOWN> k;
+__device__ __forceinline__ KeyTiles<DOWN> key_tiles(const Item& x, int block) {
+    KeyTiles<DOWN> k;
     k.base = min(x.lo[0], x.lo[1]) & -block;
     k.end = max(x.hi[0], x.hi[1]);
-    auto from = [&](int t) { return x.lo[t] < x.hi[t] ? (x.lo[t] - k.base) / kStep : 0; };
-    auto to = [&](int t) { return x.lo[t] < x.hi[t] ? (x.hi[t] - k.base + kStep - 1) / kStep : 0; };
+    auto from = [&](int t) { return x.lo[t] < x.hi[t] ? (x.lo[t] - k.base) / kTile : 0; };
+    auto to = [&](int t) { return x.lo[t] < x.hi[t] ? (x.hi[t] - k.base + kTile - 1) / kTile : 0; };
     k.a0 = from(0);
     k.b0 = to(0);
     k.a1 = from(1);
     k.b1 = to(1);
-    k.n = (max(k.b0, k.b1) + 1) >> 1;
+    k.n = max(k.b0, k.b1);
     return k;
+}
+
+// The two warps that share 32 rows, a half of each key tile each, meet at a named barrier.
+__device__ __forceinline__ void meet(int id) { asm volatile("barrier.cta.sync %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool meet_any(int id, bool x) {     // does any of the 64 threads say so?
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\t"
+        "barrier.cta.red.or.pred q, %1, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r) : "r"(id), "r"(static_cast<uint32_t>(x)) : "memory");
+    return r;
 }
 
 // Take over a CTA of this launch that has not begun: its index arrives in 16 bytes of shared memory.  (PTX ISA:
@@ -188,18 +196,18 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
     constexpr int B0 = 2 * C::SLOTS + 2 * C::RAWS;
     auto q_there = [&](int t) { return bar(B0 + t); };         // a row tile's queries
     auto q_free = [&](int t) { return bar(B0 + 2 + t); };      // and their place
-    auto s_there = [&](int t, int h) { return bar(B0 + 4 + 2 * t + h); };      // its scores of a step (even, odd)
-    auto w_there = [&](int t, int h) { return bar(B0 + 8 + 2 * t + h); };      // its weights of a step
-    auto o_there = [&](int t, int h) { return bar(B0 + 12 + 2 * t + h); };     // its sums after a step
-    auto item_there = [&](int i) { return bar(B0 + 16 + i); };
-    auto item_free = [&](int i) { return bar(B0 + 18 + i); };
-    const uint32_t edge = bar(B0 + 20), done = bar(B0 + 21), claim = bar(B0 + 22);
+    auto s_there = [&](int t) { return bar(B0 + 4 + t); };     // its scores of a key tile
+    auto w_there = [&](int t) { return bar(B0 + 6 + t); };     // its weights
+    auto o_there = [&](int t) { return bar(B0 + 8 + t); };     // its sums after a key tile
+    auto item_there = [&](int i) { return bar(B0 + 10 + i); };
+    auto item_free = [&](int i) { return bar(B0 + 12 + i); };
+    const uint32_t edge = bar(B0 + 14), done = bar(B0 + 15), claim = bar(B0 + 16);
     float* const factors = reinterpret_cast<float*>(smem + C::FACTOR_OFF);     // FP8: [tile][keys, values][block]
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::SLOTS; ++i) {
             mbar_init(full(i), C::WIDEN ? 4 : 1);
-            mbar_init(empty(i), 2);
+            mbar_init(empty(i), 1);
         }
         for (int i = 0; i < C::RAWS; ++i) {
             mbar_init(raw_full(i), 1);
@@ -208,17 +216,14 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
         for (int t = 0; t < 2; ++t) {
             mbar_init(q_there(t), 1);
             mbar_init(q_free(t), 1);
-            mbar_init(s_there(t, 0), 1);
-            mbar_init(s_there(t, 1), 1);
-            mbar_init(w_there(t, 0), 4);
-            mbar_init(w_there(t, 1), 4);
-            mbar_init(o_there(t, 0), 1);
-            mbar_init(o_there(t, 1), 1);
+            mbar_init(s_there(t), 1);
+            mbar_init(w_there(t), 8);
+            mbar_init(o_there(t), 1);
             mbar_init(item_there(t), 1);
-            mbar_init(item_free(t), C::WARPS - 1);
+            mbar_init(item_free(t), C::WARPS - 2);
         }
         mbar_init(edge, 1);
-        mbar_init(done, 2);
+        mbar_init(done, 1);
         mbar_init(claim, 1);
         fence_mbar_init();
     }
@@ -233,7 +238,7 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
     bool fine = true;                                          // no wait of this warp has run out
     int count = 0;                                             // items so far
     Item it;
-    KeySteps<BIAS> keys;
+    KeyTiles<BIAS> keys;
     auto wait = [&](uint32_t b, int times) {                   // for the barrier's times-th completion (from 0)
         fine = fine && warp_wait(b, times & 1, a.err);
         return fine;
@@ -258,39 +263,42 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
         __syncwarp();
         if (lane == 0) mbar_arrive(item_free(i));
         ++count;
-        keys = key_steps<BIAS>(it, a.B);
+        keys = key_tiles<BIAS>(it, a.B);
         return it.s >= 0;
     };
 
     if (warp < kSoftmaxWarps) {
-        // ======== softmax, a thread per row; the result out
+        // ======== softmax, two threads per row, a half of each key tile each; the result out, half of the elements each
         more_registers<C::REGS_SOFTMAX>();
-        const int rt = warp >> 2, row = (warp & 3) * 32 + lane;
-        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;          // the warp's 32 lanes
-        const uint32_t st = tmem + lanes + rt * kTile, ot = tmem + lanes + 2 * kTile + rt * D;
+        const int rt = warp >> 3, half = warp >> 2 & 1, rows0 = (warp & 3) * 32, row = rows0 + lane;
+        const int pair = 1 + rt * 4 + (warp & 3);              // the named barrier of the two
+        const uint32_t lanes = static_cast<uint32_t>(rows0) << 16;             // the warp's 32 lanes
+        const uint32_t st = tmem + lanes + rt * kTile + half * kHalf, ot = tmem + lanes + 2 * kTile + rt * D + half * (D / 2);
+        char* const own = smem + C::OUT_OFF + warp * (32 * 64);
+        const char* const other = smem + C::OUT_OFF + (warp ^ 4) * (32 * 64);
         const bool cap = a.cap > 0.f;
-        constexpr int DIR = BIAS ? -1 : 1;                     // of the steps
+        constexpr int DIR = BIAS ? -1 : 1;                     // of the key tiles
         const float qscale = a.scale * kLog2e;
         const float k2 = cap ? 2.f * kLog2e * (a.scale / a.cap) : 0.f, capl = a.cap * kLog2e;
         const float c = cap || BIAS ? 1.f : qscale;            // scores to log2 units
-        int i = 0, even = 0, tiles = 0;                        // this row tile's steps so far, the even ones; the items' tiles
+        int i = 0, tiles = 0;                                  // this row tile's key tiles so far; the items'
         // An item's part of this thread, taken while the last products of the item before are made.  (The rest stays in
         // shared memory until the result is out: registers are short here.)
         struct Part {
-            int step, stop, j0, pos;                           // the row tile's steps; the first one's position; the row's
+            int steps, j0, pos;                                // key tiles; the first one's position of this half; the row's
             int2 sees;
             float slope, inv_vref;
-            int tile;                                          // FP8: the number of the item's first tile, less ± its index
+            int tile;                                          // FP8: the first one's number
         } next;
         auto fetch = [&]() {
             if (!wait(item_there(count & 1), count >> 1)) return false;
             const Item& x = misc->item[count & 1];
             if (uniform(x.s) < 0) return false;
-            const auto k = key_steps<BIAS>(x, a.B);
-            next.step = BIAS ? uniform(k.b(rt)) - 1 : uniform(k.a(rt));
-            next.stop = BIAS ? uniform(k.a(rt)) - 1 : uniform(k.b(rt));
-            next.j0 = uniform(k.base) + next.step * kStep;
-            if (POOL == KV_FP8_E4M3) next.tile = k.before(next.step >> 1) - DIR * (next.step >> 1);
+            const auto k = key_tiles<BIAS>(x, a.B);
+            next.steps = uniform(k.b(rt) - k.a(rt));
+            const int j = BIAS ? k.b(rt) - 1 : k.a(rt);
+            next.j0 = uniform(k.base + j * kTile) + half * kHalf;
+            if (POOL == KV_FP8_E4M3) next.tile = tiles + uniform(k.before(j));
             const int token = x.token + rt * per_tile + (row >> log_g);
             next.sees = token < x.n ? row_range(a, QuerySeq{x.first, x.n, x.ctx}, token) : make_int2(0, 0);
             next.slope = BIAS ? a.slopes[x.head * a.G + (row & (a.G - 1))] * kLog2e : 0.f;
@@ -298,36 +306,34 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
             next.inv_vref = POOL == KV_FP8_E4M3 ? 1.f / x.vref : 1.f;
             return true;
         };
+        // (a warp whose wait has run out goes on to the next meeting, where both learn of it)
         bool some_item = fetch();
+        if (meet_any(pair, !fine)) some_item = false;
         #pragma unroll 1
         while (some_item) {
             const Item& x0 = misc->item[count & 1];
-            int step = next.step, j0 = next.j0;
-            const int stop = next.stop, pos = next.pos;
+            const int stop = i + next.steps, pos = next.pos;
+            int j0 = next.j0, tile = next.tile;
             const int2 sees = next.sees;
             const float slope = next.slope, inv_vref = next.inv_vref;
-            float m = -CUDART_INF_F, l = 0.f;                  // the base (log2 units) and the sum of weights
+            float m = -CUDART_INF_F, l = 0.f;                  // the base (log2 units) and this half's sum of weights
             const int i0 = i;
-            // (a row tile's key tiles follow one another)
-            const int tile0 = POOL == KV_FP8_E4M3 ? tiles + next.tile : 0;
+            bool failed = false;
             #pragma unroll 1
-            for (; step != stop; ++i, step += DIR, j0 += DIR * kStep) {
-                const int h = step & 1;
-                if (!wait(s_there(rt, h), h ? i - even : even)) break;
-                even += 1 - h;
+            for (; i < stop; ++i, j0 += DIR * kTile) {
+                wait(s_there(rt), i);
                 tc_fence_after();
-                const uint32_t at = st + h * kStep;
-                float x[kStep];
+                float x[kHalf];
                 uint32_t* const xr = reinterpret_cast<uint32_t*>(x);
-                tmem_load32(at, xr);
-                tmem_load32(at + 32, xr + 32);
+                tmem_load32(st, xr);
+                tmem_load32(st + 32, xr + 32);
                 tmem_wait_load32(xr);
                 tmem_wait_load32(xr + 32);
-                const float* const scales = POOL == KV_FP8_E4M3
-                    ? factors + (tile0 + DIR * (step >> 1)) % kFactorTiles * 32 + (h * kStep >> a.log_b) : nullptr;
+                const float* scales = nullptr;
                 if constexpr (POOL == KV_FP8_E4M3) {
+                    scales = factors + tile++ % kFactorTiles * 32 + (half * kHalf >> a.log_b);
                     #pragma unroll
-                    for (int k = 0; k < kStep; k += 8) {
+                    for (int k = 0; k < kHalf; k += 8) {
                         const float f = scales[k >> a.log_b];
                         #pragma unroll
                         for (int e = 0; e < 8; ++e) x[k + e] *= f;
@@ -335,148 +341,147 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                 }
                 if (cap) {
                     #pragma unroll
-                    for (int k = 0; k < kStep; ++k) x[k] = capped(x[k], k2, capl);
+                    for (int k = 0; k < kHalf; ++k) x[k] = capped(x[k], k2, capl);
                 }
                 if (BIAS) {
                     const float from = static_cast<float>(pos - j0), mul = cap ? 1.f : qscale;
                     #pragma unroll
-                    for (int k = 0; k < kStep; ++k) x[k] = fmaf(-slope, fabsf(from - static_cast<float>(k)), x[k] * mul);
+                    for (int k = 0; k < kHalf; ++k) x[k] = fmaf(-slope, fabsf(from - static_cast<float>(k)), x[k] * mul);
                 }
-                if (__any_sync(0xffffffffu, sees.x > j0 || sees.y < j0 + kStep)) {
+                if (__any_sync(0xffffffffu, sees.x > j0 || sees.y < j0 + kHalf)) {
                     const int from = sees.x - j0;
                     const unsigned len = sees.y - sees.x;
                     #pragma unroll
-                    for (int k = 0; k < kStep; ++k)
+                    for (int k = 0; k < kHalf; ++k)
                         if (static_cast<unsigned>(k - from) >= len) x[k] = -CUDART_INF_F;
                 }
-                // Weights at the base m, and their sums per pair of columns.
-                const float2 c2 = make_float2(c, c);
-                float2 sum[2];
-                uint32_t w[kStep / 2];
-                auto weigh = [&]() {
-                    const float off = kLift - (m == -CUDART_INF_F ? 0.f : m);
-                    const float2 off2 = make_float2(off, off);
-                    #pragma unroll
-                    for (int k = 0; k < kStep / 2; ++k) {
-                        float2 y = __ffma2_rn(make_float2(x[2 * k], x[2 * k + 1]), c2, off2);
-                        y.x = ex2_approx(y.x);
-                        y.y = ex2_approx(y.y);
-                        sum[k & 1] = k < 2 ? y : __fadd2_rn(sum[k & 1], y);
-                        if constexpr (POOL == KV_FP8_E4M3) {
-                            const float f = scales[16 + (2 * k >> a.log_b)] * inv_vref;
-                            y = __fmul2_rn(y, make_float2(f, f));
-                        }
-                        const __half2 hv = __floats2half2_rn(y.x, y.y);
-                        w[k] = *reinterpret_cast<const uint32_t*>(&hv);
-                    }
-                };
-                // They are taken at the old base while the maximum is found: the base follows it only when it is left
-                // behind by more than 2^8, which is rare after the first step.
-                weigh();
                 float tops[4];
                 #pragma unroll
                 for (int k = 0; k < 4; ++k) tops[k] = max3(x[3 * k], x[3 * k + 1], x[3 * k + 2]);
                 #pragma unroll
-                for (int k = 12; k < kStep; k += 2) tops[(k >> 1) & 3] = max3(x[k], x[k + 1], tops[(k >> 1) & 3]);
-                const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * c;
-                const bool raise = top - m > kRaise;           // (m -inf: yes, but for a row that sees nothing yet)
-                if (__any_sync(0xffffffffu, raise)) {
+                for (int k = 12; k < kHalf; k += 2) tops[(k >> 1) & 3] = max3(x[k], x[k + 1], tops[(k >> 1) & 3]);
+                float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * c;
+                // The base follows the maximum only when it is left behind by more than 2^8, which is rare after the
+                // first tile.  (m -inf: it is, but for a row that sees nothing yet)
+                if (meet_any(pair, !fine || top - m > kRaise)) {
+                    reinterpret_cast<float*>(own)[lane] = top;
+                    if (meet_any(pair, !fine)) {
+                        failed = true;
+                        break;
+                    }
+                    top = fmaxf(top, reinterpret_cast<const float*>(other)[lane]);
                     float keep = 1.f;
-                    if (raise) {
+                    if (top - m > kRaise) {
                         keep = ex2_approx(m - top);
                         m = top;
                         l *= keep;
                     }
-                    if (i > i0) {
-                        // the step before (the one before that is done: its scores' place holds this one's)
-                        if (!wait(o_there(rt, 1 - h), h ? even - 1 : i - even)) break;
+                    if (i > i0 && wait(o_there(rt), i - 1)) {
                         tc_fence_after();
                         #pragma unroll 1
-                        for (int k = 0; k < D; k += 32) {
-                            uint32_t o[32];
-                            tmem_load32(ot + k, o);
-                            tmem_wait_load32(o);
+                        for (int k = 0; k < D / 2; k += 16) {
+                            uint32_t o[16];
+                            tmem_load16(ot + k, o);
+                            tmem_wait_load16(o);
                             #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
-                            tmem_store32(ot + k, o);
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+                            tmem_store16(ot + k, o);
                         }
                     }
-                    weigh();
                 }
-                tmem_store32(at, w);
+                // weights, and their sums per pair of columns
+                const float off = kLift - (m == -CUDART_INF_F ? 0.f : m);
+                const float2 c2 = make_float2(c, c), off2 = make_float2(off, off);
+                float2 sum[2];
+                uint32_t w[kHalf / 2];
+                #pragma unroll
+                for (int k = 0; k < kHalf / 2; ++k) {
+                    float2 y = __ffma2_rn(make_float2(x[2 * k], x[2 * k + 1]), c2, off2);
+                    y.x = ex2_approx(y.x);
+                    y.y = ex2_approx(y.y);
+                    sum[k & 1] = k < 2 ? y : __fadd2_rn(sum[k & 1], y);
+                    if constexpr (POOL == KV_FP8_E4M3) {
+                        const float f = scales[16 + (2 * k >> a.log_b)] * inv_vref;
+                        y = __fmul2_rn(y, make_float2(f, f));
+                    }
+                    const __half2 hv = __floats2half2_rn(y.x, y.y);
+                    w[k] = *reinterpret_cast<const uint32_t*>(&hv);
+                }
+                tmem_store32(st, w);
                 tmem_wait_store();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(w_there(rt, h));
+                if (lane == 0) mbar_arrive(w_there(rt));
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             }
-            if (!fine) break;
+            if (failed) break;
             const Item it = x0;
-            const int it_tiles = POOL == KV_FP8_E4M3 ? key_steps<BIAS>(x0, a.B).tiles() : 0;
+            if (POOL == KV_FP8_E4M3) tiles += key_tiles<BIAS>(x0, a.B).tiles();
             __syncwarp();
             if (lane == 0) mbar_arrive(item_free(count & 1));
             ++count;
             some_item = fetch();
-            if (!fine || (i > i0 && !wait(o_there(rt, (step - DIR) & 1), (step & 1 ? even : i - even) - 1))) break;
+            if (i > i0) wait(o_there(rt), i - 1);
             tc_fence_after();
-            // the result, 64 elements at a time through shared memory, so that a store writes whole lines
+            reinterpret_cast<float*>(own)[lane] = l;
+            if (meet_any(pair, !fine)) break;
+            l += reinterpret_cast<const float*>(other)[lane];
+            meet(pair);
+            // the result, 32 elements at a time through shared memory, so that a store writes whole sectors
             const int token = it.token + rt * per_tile + (row >> log_g);
             const QuerySeq seq{it.first, it.n, it.ctx};
             const bool some = i > i0 && l != 0.f, live = token < it.n;
             const float inv = l == 0.f ? 0.f : it.vref / l;
             const float2 inv2 = make_float2(inv, inv);
-            char* const out = smem + C::OUT_OFF + warp * (32 * 128);
             char* const to = a.out + static_cast<int64_t>(it.first + it.token + rt * per_tile) * a.out_stride +
-                             it.head * a.G * (D * 2) + (lane & 7) * 16;
+                             it.head * a.G * (D * 2) + half * D + (lane & 3) * 16;
             const int left = it.n - it.token - rt * per_tile;  // tokens of the row tile
             float2 odd = make_float2(0.f, 0.f);                // NaN: something was not finite
             #pragma unroll 1
-            for (int half = 0; half < C::HALVES; ++half) {
+            for (int part = 0; part < D / 2; part += 32) {
+                uint32_t o[32];                                // (without a key tile: whatever is there, not used)
+                tmem_load32(ot + part, o);
+                tmem_wait_load32(o);
                 #pragma unroll
-                for (int part = 0; part < 2; ++part) {
-                    uint32_t o[32];                            // (without a key tile: whatever is there, not used)
-                    tmem_load32(ot + half * 64 + part * 32, o);
-                    tmem_wait_load32(o);
+                for (int ch = 0; ch < 4; ++ch) {
+                    uint32_t w[4];
                     #pragma unroll
-                    for (int ch = 0; ch < 4; ++ch) {
-                        uint32_t w[4];
-                        #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float2 f = __fmul2_rn(make_float2(__uint_as_float(o[8 * ch + 2 * e]), __uint_as_float(o[8 * ch + 2 * e + 1])), inv2);
-                            odd = __ffma2_rn(f, make_float2(0.f, 0.f), odd);
-                            const __half2 hv = __floats2half2_rn(f.x, f.y);
-                            w[e] = some ? *reinterpret_cast<const uint32_t*>(&hv) : 0u;
-                        }
-                        *reinterpret_cast<uint4*>(out + lane * 128 + (((part * 4 + ch) ^ (lane & 7)) << 4)) =
-                            make_uint4(w[0], w[1], w[2], w[3]);
+                    for (int e = 0; e < 4; ++e) {
+                        float2 f = __fmul2_rn(make_float2(__uint_as_float(o[8 * ch + 2 * e]), __uint_as_float(o[8 * ch + 2 * e + 1])), inv2);
+                        odd = __ffma2_rn(f, make_float2(0.f, 0.f), odd);
+                        const __half2 hv = __floats2half2_rn(f.x, f.y);
+                        w[e] = some ? *reinterpret_cast<const uint32_t*>(&hv) : 0u;
                     }
+                    *reinterpret_cast<uint4*>(own + lane * 64 + ((ch ^ (lane >> 1 & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
                 __syncwarp();
-                uint4 v[8];
+                uint4 v[4];
                 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int r = k * 4 + (lane >> 3);
-                    v[k] = *reinterpret_cast<const uint4*>(out + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+                for (int k = 0; k < 4; ++k) {
+                    const int r = k * 8 + (lane >> 2);
+                    v[k] = *reinterpret_cast<const uint4*>(own + r * 64 + (((lane & 3) ^ (r >> 1 & 3)) << 4));
                 }
                 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int r = (warp & 3) * 32 + k * 4 + (lane >> 3), tok = r >> log_g;
+                for (int k = 0; k < 4; ++k) {
+                    const int r = rows0 + k * 8 + (lane >> 2), tok = r >> log_g;
                     if (tok < left)
-                        *reinterpret_cast<uint4*>(to + tok * a.out_stride + (r & (a.G - 1)) * (D * 2) + half * 128) = v[k];
+                        *reinterpret_cast<uint4*>(to + tok * a.out_stride + (r & (a.G - 1)) * (D * 2) + part * 2) = v[k];
                 }
                 __syncwarp();
             }
             tc_fence_before();
             // A key or value that is not finite reaches, as 0 * NaN, rows that do not see it: a row that came out so
-            // is worked out again from the definition, which reads only what it sees.
-            unsigned again = __ballot_sync(0xffffffffu, some && live && !(odd.x + odd.y == 0.f));
-            #pragma unroll 1
-            while (again) {
-                const int r = (warp & 3) * 32 + __ffs(again) - 1;
-                again &= again - 1;
-                attend_row<D, POOL>(a, it.s, seq, it.token + rt * per_tile + (r >> log_g), it.head * a.G + (r & (a.G - 1)));
+            // is worked out again from the definition, which reads only what it sees, when both halves of it are out.
+            const bool bad = some && live && !(odd.x + odd.y == 0.f);
+            if (meet_any(pair, bad)) {
+                unsigned again = __ballot_sync(0xffffffffu, bad);
+                #pragma unroll 1
+                while (again) {
+                    const int r = rows0 + __ffs(again) - 1;
+                    again &= again - 1;
+                    attend_row<D, POOL>(a, it.s, seq, it.token + rt * per_tile + (r >> log_g), it.head * a.G + (r & (a.G - 1)));
+                }
             }
-            tiles += it_tiles;
         }
     } else if (C::WIDEN && warp >= kWidenWarp) {
         // ======== stored tiles to float16
@@ -512,100 +517,91 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
     } else {
         fewer_registers<C::REGS_ISSUE>();
     }
-    if (warp == kMmaWarp || warp == kMmaWarp + 1) {
-        // ======== matrix products, a warp per row tile (they wait for its softmax, and the other row tile's run
-        // meanwhile): it stays together, one lane issues
-        constexpr uint32_t s_shape = tc_idesc(kStep, false), o_shape = tc_idesc(D, true);
-        const int t = warp - kMmaWarp;
-        const uint32_t st = tmem + t * kTile, ot = tmem + 2 * kTile + t * D;
-        const uint64_t q_desc = tc_desc(base32 + C::Q_OFF + t * C::TILE, 0, 1024);
+    if (warp == kMmaWarp) {
+        // ======== matrix products: the warp stays together, one lane issues.  A row tile's products of a key tile and its
+        // next scores go behind one another, then the other row tile's: so the two take turns, one's softmax runs while
+        // the other's products do.
+        constexpr uint32_t s_shape = tc_idesc(kTile, false), o_shape = tc_idesc(D, true);
         // A look at a barrier takes 200 cycles beside the products' reads of shared memory: lanes 0, 1 and 2 look at one each.
         auto wait3 = [&](uint32_t b0, int n0, uint32_t b1, int n1, uint32_t b2, int n2) {
             const uint32_t b = lane == 1 ? b1 : lane == 2 ? b2 : b0;
             const int n = lane == 1 ? n1 : lane == 2 ? n2 : n0;
             return wait(b, n);
         };
-        int i = 0, even = 0;                                   // this row tile's steps so far, the even ones
+        int i0 = 0, i1 = 0;                                    // the row tiles' key tiles so far
         Ring<C::SLOTS> ring;
         while (next_item()) {
-            const int i0 = i;
-            const int a_t = keys.a(t), b_t = keys.b(t);
-            auto on = [&](int step) { return step >= a_t && step < b_t; };
-            auto scores = [&](int at, int h) {                 // S = Q K^T for a step (one lane)
-                const uint64_t k_desc = tc_desc(base32 + C::KV_OFF + at * C::TILE + h * (C::TILE / 2), 0, C::HALVES * 1024);
+            bool some0 = false, some1 = false;                 // a key tile of this item's behind us
+            auto is_last = [&](int t, int j) { return j == (BIAS ? keys.a(t) : keys.b(t) - 1); };
+            auto scores = [&](int t, int at, int j) {          // S = Q K^T (one lane)
+                const uint64_t q_desc = tc_desc(base32 + C::Q_OFF + t * C::TILE, 0, 1024);
+                const uint64_t k_desc = tc_desc(base32 + C::KV_OFF + at * C::TILE, 0, C::HALVES * 1024);
                 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                    tc_mma_ss(st + h * kStep, q_desc + (((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4),
+                    tc_mma_ss(tmem + t * kTile, q_desc + (((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4),
                               k_desc + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), s_shape, k > 0);
-                tc_commit(s_there(t, h));
+                tc_commit(s_there(t));
+                if (is_last(t, j)) tc_commit(q_free(t));
             };
-            // a key tile that this row tile has no (more) steps of, or whose products are issued, is left to the loader
-            auto leave = [&](int at, bool used) {
-                if (used) tc_commit(empty(at));
-                else mbar_arrive(empty(at));
+            auto values = [&](int t, int at, bool add) {       // O += W V (one lane)
+                const uint64_t v_desc = tc_desc(base32 + C::KV_OFF + at * C::TILE, 1024, C::HALVES * 1024);
+                #pragma unroll
+                for (int k = 0; k < kTile / 16; ++k)           // (a half's weights are at its scores' beginning)
+                    tc_mma_ts(tmem + 2 * kTile + t * D, tmem + t * kTile + (k >> 2) * kHalf + (k & 3) * 8,
+                              v_desc + k * (C::HALVES * 2048 >> 4), o_shape, add || k > 0);
+                tc_commit(o_there(t));
             };
-            constexpr int h0 = BIAS, h1 = 1 - h0;             // a key tile's steps in their order
-            auto nth = [&](int h) { return h ? i - even : even; };             // steps of this parity so far
-            auto is_last = [&](int at) { return BIAS ? a_t >= 2 * at : b_t <= 2 * at + 2; };
             int j = keys.first();
-            bool on0 = on(2 * j + h0), on1 = on(2 * j + h1);
-            if (keys.is(j)) {
-                if (!wait3(full(ring.slot), ring.times, q_there(t), count - 1, full(ring.slot), ring.times)) break;
-                if (elect_one()) {
-                    if (on0) scores(ring.slot, h0);
-                    if (on1) scores(ring.slot, h1);
-                    leave(ring.slot, on0 || on1);
-                    if ((on0 || on1) && is_last(j)) tc_commit(q_free(t));
-                }
-                __syncwarp();
-            } else if (!wait(q_there(t), count - 1)) {
+            bool now0 = keys.on(0, j), now1 = keys.on(1, j);
+            if (!wait3(q_there(0), count - 1, q_there(1), count - 1, keys.is(j) ? full(ring.slot) : q_there(0),
+                       keys.is(j) ? ring.times : count - 1))
                 break;
+            if (keys.is(j) && elect_one()) {
+                if (now0) scores(0, ring.slot, j);
+                if (now1) scores(1, ring.slot, j);
+                tc_commit(empty(ring.slot));
             }
+            __syncwarp();
             #pragma unroll 1
             while (keys.is(j)) {                               // (this tile's scores are issued)
                 const int jn = keys.next(j);
-                const bool more = keys.is(jn), next0 = more && on(2 * jn + h0), next1 = more && on(2 * jn + h1);
+                const bool more = keys.is(jn), then0 = more && keys.on(0, jn), then1 = more && keys.on(1, jn);
                 ring.advance();
                 const int v = ring.slot, v_times = ring.times;
                 ring.advance();
-                const uint64_t v_desc = tc_desc(base32 + C::KV_OFF + v * C::TILE, 1024, C::HALVES * 1024);
-                auto values = [&](int h) {                     // O += W V for a step (one lane)
-                    #pragma unroll
-                    for (int k = 0; k < kStep / 16; ++k)
-                        tc_mma_ts(ot, st + h * kStep + k * 8, v_desc + (h * (C::TILE / 2) >> 4) + k * (C::HALVES * 2048 >> 4), o_shape,
-                                  i > i0 || k > 0);
-                    tc_commit(o_there(t, h));
-                };
-                // its values, the next tile's keys and the first step's weights; then the second step's weights
-                if (!wait3(full(v), v_times, more ? full(ring.slot) : full(v), more ? ring.times : v_times,
-                           on0 ? w_there(t, h0) : full(v), on0 ? nth(h0) : v_times))
+                const int k = ring.slot;
+                // its values, the next tile's keys and the weights
+                if (!wait3(full(v), v_times, more ? full(k) : full(v), more ? ring.times : v_times, now0 ? w_there(0) : full(v),
+                           now0 ? i0 : v_times))
                     break;
                 tc_fence_after();
                 if (elect_one()) {
-                    if (on0) values(h0);
-                    if (next0) scores(ring.slot, h0);
+                    if (now0) values(0, v, some0);
+                    if (then0) scores(0, k, jn);
                 }
                 __syncwarp();
-                i += on0;
-                even += on0 && h0 == 0;
-                if (on1 && !wait(w_there(t, h1), nth(h1))) break;
+                if (now1 && !wait(w_there(1), i1)) break;
                 tc_fence_after();
                 if (elect_one()) {
-                    if (on1) values(h1);
-                    if (next1) scores(ring.slot, h1);
-                    leave(v, on0 || on1);
-                    if (more) leave(ring.slot, next0 || next1);
-                    if ((next0 || next1) && is_last(jn)) tc_commit(q_free(t));
+                    if (now1) values(1, v, some1);
+                    tc_commit(empty(v));
+                    if (then1) scores(1, k, jn);
+                    if (more) tc_commit(empty(k));
                 }
                 __syncwarp();
-                i += on1;
-                even += on1 && h1 == 0;
+                i0 += now0;
+                i1 += now1;
+                some0 |= now0;
+                some1 |= now1;
                 j = jn;
-                on0 = next0;
-                on1 = next1;
+                now0 = then0;
+                now1 = then1;
             }
             if (!fine) break;
-            if (a_t == b_t && elect_one()) mbar_arrive(q_free(t));
+            if (elect_one()) {                                 // without a key tile: not asked for by the scores
+                if (keys.a0 == keys.b0) mbar_arrive(q_free(0));
+                if (keys.a1 == keys.b1) mbar_arrive(q_free(1));
+            }
             __syncwarp();
         }
         if (elect_one()) tc_commit(done);                      // nothing of it is in flight at the end
