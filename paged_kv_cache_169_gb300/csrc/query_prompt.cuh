@@ -22,7 +22,6 @@ int launch_query_prompt_int4(const kv_pool* pool, const PromptArgs& p, bool pdl,
 namespace {
 
 constexpr int kTile = 128;             // rows of a row tile and keys of a key tile
-constexpr int kHalf = 64;              // keys of a tile that a softmax thread weighs
 constexpr int kSoftmaxWarps = 16, kMmaWarp = 16, kLoadWarp = 17, kItemWarp = 18, kWidenWarp = 20;      // (19: none)
 constexpr int kFactorTiles = 8;        // key tiles whose FP8 scales are kept (more than are in flight)
 
@@ -44,8 +43,8 @@ struct PromptCfg {
     static constexpr int REGS_SOFTMAX = WIDEN ? 96 : 104, REGS_ISSUE = WIDEN ? 48 : 64, REGS_WIDEN = 48;
     static_assert(WIDEN ? 4 * REGS_SOFTMAX + REGS_ISSUE + REGS_WIDEN <= 6 * 80 : 4 * REGS_SOFTMAX + REGS_ISSUE <= 5 * 96, "registers");
     static constexpr int Q_OFF = 0, KV_OFF = 2 * TILE, RAW_OFF = KV_OFF + SLOTS * TILE;
-    static constexpr int OUT_OFF = RAW_OFF + RAWS * RAW;       // 32 elements of a softmax warp's 32 rows on their way out
-    static constexpr int FACTOR_OFF = OUT_OFF + kSoftmaxWarps * 32 * 64;
+    static constexpr int OUT_OFF = RAW_OFF + RAWS * RAW;       // 64 elements of a softmax warp's 16 rows on their way out
+    static constexpr int FACTOR_OFF = OUT_OFF + kSoftmaxWarps * 16 * 128;
     static constexpr int FACTORS = POOL == KV_FP8_E4M3 ? kFactorTiles * 2 * 16 * 4 : 0;
     static constexpr int BAR_OFF = FACTOR_OFF + FACTORS;
     static constexpr int BARS = 2 * SLOTS + 2 * RAWS + 5 * 2 + 2 * 2 + 3;
@@ -146,17 +145,6 @@ __device__ __forceinline__ KeyTiles<DOWN> key_tiles(const Item& x, int block) {
     k.b1 = to(1);
     k.n = max(k.b0, k.b1);
     return k;
-}
-
-// The two warps that share 32 rows, a half of each key tile each, meet at a named barrier.
-__device__ __forceinline__ void meet(int id) { asm volatile("barrier.cta.sync %0, 64;" ::"r"(id) : "memory"); }
-__device__ __forceinline__ bool meet_any(int id, bool x) {     // does any of the 64 threads say so?
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\t"
-        "barrier.cta.red.or.pred q, %1, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r) : "r"(id), "r"(static_cast<uint32_t>(x)) : "memory");
-    return r;
 }
 
 // Take over a CTA of this launch that has not begun: its index arrives in 16 bytes of shared memory.  (PTX ISA:
@@ -268,26 +256,27 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
     };
 
     if (warp < kSoftmaxWarps) {
-        // ======== softmax, two threads per row, a half of each key tile each; the result out, half of the elements each
+        // ======== softmax, 16 rows a warp; the result out.  Four lanes share two rows, r and r + 8 of the warp's, and have
+        // columns 8 g + 2 (lane & 3) and the next one of each group g of 8: rows need no other warp.
         more_registers<C::REGS_SOFTMAX>();
-        const int rt = warp >> 3, half = warp >> 2 & 1, rows0 = (warp & 3) * 32, row = rows0 + lane;
-        const int pair = 1 + rt * 4 + (warp & 3);              // the named barrier of the two
-        const uint32_t lanes = static_cast<uint32_t>(rows0) << 16;             // the warp's 32 lanes
-        const uint32_t st = tmem + lanes + rt * kTile + half * kHalf, ot = tmem + lanes + 2 * kTile + rt * D + half * (D / 2);
-        char* const own = smem + C::OUT_OFF + warp * (32 * 64);
-        const char* const other = smem + C::OUT_OFF + (warp ^ 4) * (32 * 64);
+        const int rt = warp >> 3, rows0 = (warp & 3) * 32 + (warp & 4) * 4, quad = lane & 3;
+        const uint32_t lanes = static_cast<uint32_t>(rows0) << 16;
+        const uint32_t st = tmem + lanes + rt * kTile, ot = tmem + lanes + 2 * kTile + rt * D;
+        char* const own = smem + C::OUT_OFF + warp * (16 * 128);
         const bool cap = a.cap > 0.f;
         constexpr int DIR = BIAS ? -1 : 1;                     // of the key tiles
         const float qscale = a.scale * kLog2e;
         const float k2 = cap ? 2.f * kLog2e * (a.scale / a.cap) : 0.f, capl = a.cap * kLog2e;
         const float c = cap || BIAS ? 1.f : qscale;            // scores to log2 units
         int i = 0, tiles = 0;                                  // this row tile's key tiles so far; the items'
+        auto row_of = [&](int r) { return rows0 + (lane >> 2) + 8 * r; };
         // An item's part of this thread, taken while the last products of the item before are made.  (The rest stays in
         // shared memory until the result is out: registers are short here.)
         struct Part {
-            int steps, j0, pos;                                // key tiles; the first one's position of this half; the row's
-            int2 sees;
-            float slope, inv_vref;
+            int steps, j0;                                     // key tiles; the first one's position
+            int2 sees[2];
+            float slope[2], inv_vref;
+            int pos0;                                          // the first row's position
             int tile;                                          // FP8: the first one's number
         } next;
         auto fetch = [&]() {
@@ -297,189 +286,208 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
             const auto k = key_tiles<BIAS>(x, a.B);
             next.steps = uniform(k.b(rt) - k.a(rt));
             const int j = BIAS ? k.b(rt) - 1 : k.a(rt);
-            next.j0 = uniform(k.base + j * kTile) + half * kHalf;
+            next.j0 = uniform(k.base + j * kTile);
             if (POOL == KV_FP8_E4M3) next.tile = tiles + uniform(k.before(j));
-            const int token = x.token + rt * per_tile + (row >> log_g);
-            next.sees = token < x.n ? row_range(a, QuerySeq{x.first, x.n, x.ctx}, token) : make_int2(0, 0);
-            next.slope = BIAS ? a.slopes[x.head * a.G + (row & (a.G - 1))] * kLog2e : 0.f;
-            next.pos = x.ctx - x.n + token;
+            #pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int token = x.token + rt * per_tile + (row_of(r) >> log_g);
+                next.sees[r] = token < x.n ? row_range(a, QuerySeq{x.first, x.n, x.ctx}, token) : make_int2(0, 0);
+                next.slope[r] = BIAS ? a.slopes[x.head * a.G + (row_of(r) & (a.G - 1))] * kLog2e : 0.f;
+            }
+            next.pos0 = x.ctx - x.n + x.token + rt * per_tile;
             next.inv_vref = POOL == KV_FP8_E4M3 ? 1.f / x.vref : 1.f;
             return true;
         };
-        // (a warp whose wait has run out goes on to the next meeting, where both learn of it)
         bool some_item = fetch();
-        if (meet_any(pair, !fine)) some_item = false;
         #pragma unroll 1
         while (some_item) {
             const Item& x0 = misc->item[count & 1];
-            const int stop = i + next.steps, pos = next.pos;
+            const int stop = i + next.steps, pos0 = next.pos0;
             int j0 = next.j0, tile = next.tile;
-            const int2 sees = next.sees;
-            const float slope = next.slope, inv_vref = next.inv_vref;
-            float m = -CUDART_INF_F, l = 0.f;                  // the base (log2 units) and this half's sum of weights
+            const int2 sees[2] = {next.sees[0], next.sees[1]};
+            const float slope[2] = {next.slope[0], next.slope[1]}, inv_vref = next.inv_vref;
+            float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};    // the base (log2 units), this thread's sum of weights
             const int i0 = i;
-            bool failed = false;
             #pragma unroll 1
             for (; i < stop; ++i, j0 += DIR * kTile) {
-                wait(s_there(rt), i);
+                if (!wait(s_there(rt), i)) break;
                 tc_fence_after();
-                float x[kHalf];
+                float x[64];                                   // [group of 8 columns][row][2]
                 uint32_t* const xr = reinterpret_cast<uint32_t*>(x);
-                tmem_load32(st, xr);
-                tmem_load32(st + 32, xr + 32);
+                tmem_load_16x64(st, xr);
+                tmem_load_16x64(st + 64, xr + 32);
                 tmem_wait_load32(xr);
                 tmem_wait_load32(xr + 32);
                 const float* scales = nullptr;
                 if constexpr (POOL == KV_FP8_E4M3) {
-                    scales = factors + tile++ % kFactorTiles * 32 + (half * kHalf >> a.log_b);
+                    scales = factors + tile++ % kFactorTiles * 32;
                     #pragma unroll
-                    for (int k = 0; k < kHalf; k += 8) {
-                        const float f = scales[k >> a.log_b];
+                    for (int g = 0; g < 16; ++g) {
+                        const float f = scales[8 * g >> a.log_b];
                         #pragma unroll
-                        for (int e = 0; e < 8; ++e) x[k + e] *= f;
+                        for (int e = 0; e < 4; ++e) x[4 * g + e] *= f;
                     }
                 }
                 if (cap) {
                     #pragma unroll
-                    for (int k = 0; k < kHalf; ++k) x[k] = capped(x[k], k2, capl);
+                    for (int k = 0; k < 64; ++k) x[k] = capped(x[k], k2, capl);
                 }
                 if (BIAS) {
-                    const float from = static_cast<float>(pos - j0), mul = cap ? 1.f : qscale;
+                    const float mul = cap ? 1.f : qscale;
                     #pragma unroll
-                    for (int k = 0; k < kHalf; ++k) x[k] = fmaf(-slope, fabsf(from - static_cast<float>(k)), x[k] * mul);
-                }
-                if (__any_sync(0xffffffffu, sees.x > j0 || sees.y < j0 + kHalf)) {
-                    const int from = sees.x - j0;
-                    const unsigned len = sees.y - sees.x;
-                    #pragma unroll
-                    for (int k = 0; k < kHalf; ++k)
-                        if (static_cast<unsigned>(k - from) >= len) x[k] = -CUDART_INF_F;
-                }
-                float tops[4];
-                #pragma unroll
-                for (int k = 0; k < 4; ++k) tops[k] = max3(x[3 * k], x[3 * k + 1], x[3 * k + 2]);
-                #pragma unroll
-                for (int k = 12; k < kHalf; k += 2) tops[(k >> 1) & 3] = max3(x[k], x[k + 1], tops[(k >> 1) & 3]);
-                float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * c;
-                // The base follows the maximum only when it is left behind by more than 2^8, which is rare after the
-                // first tile.  (m -inf: it is, but for a row that sees nothing yet)
-                if (meet_any(pair, !fine || top - m > kRaise)) {
-                    reinterpret_cast<float*>(own)[lane] = top;
-                    if (meet_any(pair, !fine)) {
-                        failed = true;
-                        break;
-                    }
-                    top = fmaxf(top, reinterpret_cast<const float*>(other)[lane]);
-                    float keep = 1.f;
-                    if (top - m > kRaise) {
-                        keep = ex2_approx(m - top);
-                        m = top;
-                        l *= keep;
-                    }
-                    if (i > i0 && wait(o_there(rt), i - 1)) {
-                        tc_fence_after();
-                        #pragma unroll 1
-                        for (int k = 0; k < D / 2; k += 16) {
-                            uint32_t o[16];
-                            tmem_load16(ot + k, o);
-                            tmem_wait_load16(o);
-                            #pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
-                            tmem_store16(ot + k, o);
+                    for (int r = 0; r < 2; ++r) {
+                        const float from = static_cast<float>(pos0 + (row_of(r) >> log_g) - j0 - 2 * quad);
+                        #pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            float& y = x[(k >> 1) * 4 + 2 * r + (k & 1)];
+                            y = fmaf(-slope[r], fabsf(from - static_cast<float>((k >> 1) * 8 + (k & 1))), y * mul);
                         }
                     }
                 }
-                // weights, and their sums per pair of columns
-                const float off = kLift - (m == -CUDART_INF_F ? 0.f : m);
-                const float2 c2 = make_float2(c, c), off2 = make_float2(off, off);
-                float2 sum[2];
-                uint32_t w[kHalf / 2];
+                if (__any_sync(0xffffffffu, max(sees[0].x, sees[1].x) > j0 || min(sees[0].y, sees[1].y) < j0 + kTile)) {
+                    #pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const int from = sees[r].x - j0 - 2 * quad;
+                        const unsigned len = sees[r].y - sees[r].x;
+                        #pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (static_cast<unsigned>((k >> 1) * 8 + (k & 1) - from) >= len)
+                                x[(k >> 1) * 4 + 2 * r + (k & 1)] = -CUDART_INF_F;
+                    }
+                }
+                float top[2];
                 #pragma unroll
-                for (int k = 0; k < kHalf / 2; ++k) {
-                    float2 y = __ffma2_rn(make_float2(x[2 * k], x[2 * k + 1]), c2, off2);
+                for (int r = 0; r < 2; ++r) {
+                    float t0 = fmaxf(x[2 * r], x[2 * r + 1]), t1 = fmaxf(x[2 * r + 4], x[2 * r + 5]);
+                    #pragma unroll
+                    for (int g = 2; g < 16; g += 2) {
+                        t0 = max3(x[4 * g + 2 * r], x[4 * g + 2 * r + 1], t0);
+                        t1 = max3(x[4 * g + 2 * r + 4], x[4 * g + 2 * r + 5], t1);
+                    }
+                    top[r] = fmaxf(t0, t1);
+                }
+                #pragma unroll
+                for (int k = 1; k < 4; k *= 2) {
+                    top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], k));
+                    top[1] = fmaxf(top[1], __shfl_xor_sync(0xffffffffu, top[1], k));
+                }
+                // The base follows the maximum only when it is left behind by more than 2^8, which is rare after the
+                // first tile.  (m -inf: it is, but for a row that sees nothing yet)
+                if (__any_sync(0xffffffffu, top[0] * c - m[0] > kRaise || top[1] * c - m[1] > kRaise)) {
+                    float keep[2] = {1.f, 1.f};
+                    #pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        if (top[r] * c - m[r] > kRaise) {
+                            keep[r] = ex2_approx(m[r] - top[r] * c);
+                            m[r] = top[r] * c;
+                            l[r] *= keep[r];
+                        }
+                    }
+                    if (i > i0) {
+                        if (!wait(o_there(rt), i - 1)) break;
+                        tc_fence_after();
+                        #pragma unroll 1
+                        for (int k = 0; k < D; k += 16) {
+                            uint32_t o[8];
+                            tmem_load_16x16(ot + k, o);
+                            #pragma unroll
+                            for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep[e >> 1 & 1]);
+                            tmem_store_16x16(ot + k, o);
+                        }
+                    }
+                }
+                // weights, and their sums
+                const float2 c2 = make_float2(c, c);
+                float2 sum[2];
+                uint32_t w[32];
+                #pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    const int r = k & 1;
+                    const float off = kLift - (m[r] == -CUDART_INF_F ? 0.f : m[r]);
+                    float2 y = __ffma2_rn(make_float2(x[2 * k], x[2 * k + 1]), c2, make_float2(off, off));
                     y.x = ex2_approx(y.x);
                     y.y = ex2_approx(y.y);
-                    sum[k & 1] = k < 2 ? y : __fadd2_rn(sum[k & 1], y);
+                    sum[r] = k < 2 ? y : __fadd2_rn(sum[r], y);
                     if constexpr (POOL == KV_FP8_E4M3) {
-                        const float f = scales[16 + (2 * k >> a.log_b)] * inv_vref;
+                        const float f = scales[16 + (4 * (k & ~1) >> a.log_b)] * inv_vref;
                         y = __fmul2_rn(y, make_float2(f, f));
                     }
                     const __half2 hv = __floats2half2_rn(y.x, y.y);
                     w[k] = *reinterpret_cast<const uint32_t*>(&hv);
                 }
-                tmem_store32(st, w);
+                tmem_store_16x64(st, w);
                 tmem_wait_store();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(w_there(rt));
-                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                l[0] += sum[0].x + sum[0].y;
+                l[1] += sum[1].x + sum[1].y;
             }
-            if (failed) break;
+            if (!fine) break;
             const Item it = x0;
             if (POOL == KV_FP8_E4M3) tiles += key_tiles<BIAS>(x0, a.B).tiles();
             __syncwarp();
             if (lane == 0) mbar_arrive(item_free(count & 1));
             ++count;
+            #pragma unroll
+            for (int k = 1; k < 4; k *= 2) {
+                l[0] += __shfl_xor_sync(0xffffffffu, l[0], k);
+                l[1] += __shfl_xor_sync(0xffffffffu, l[1], k);
+            }
             some_item = fetch();
-            if (i > i0) wait(o_there(rt), i - 1);
+            if (!fine || (i > i0 && !wait(o_there(rt), i - 1))) break;
             tc_fence_after();
-            reinterpret_cast<float*>(own)[lane] = l;
-            if (meet_any(pair, !fine)) break;
-            l += reinterpret_cast<const float*>(other)[lane];
-            meet(pair);
-            // the result, 32 elements at a time through shared memory, so that a store writes whole sectors
-            const int token = it.token + rt * per_tile + (row >> log_g);
-            const QuerySeq seq{it.first, it.n, it.ctx};
-            const bool some = i > i0 && l != 0.f, live = token < it.n;
-            const float inv = l == 0.f ? 0.f : it.vref / l;
-            const float2 inv2 = make_float2(inv, inv);
+            // the result, 64 elements at a time through shared memory, so that a store writes whole lines
+            const bool any = i > i0;
+            const float inv[2] = {l[0] == 0.f ? 0.f : it.vref / l[0], l[1] == 0.f ? 0.f : it.vref / l[1]};
             char* const to = a.out + static_cast<int64_t>(it.first + it.token + rt * per_tile) * a.out_stride +
-                             it.head * a.G * (D * 2) + half * D + (lane & 3) * 16;
+                             it.head * a.G * (D * 2) + (lane & 7) * 16;
             const int left = it.n - it.token - rt * per_tile;  // tokens of the row tile
-            float2 odd = make_float2(0.f, 0.f);                // NaN: something was not finite
+            float2 odd[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};    // NaN: something was not finite
             #pragma unroll 1
-            for (int part = 0; part < D / 2; part += 32) {
+            for (int half = 0; half < C::HALVES; ++half) {
                 uint32_t o[32];                                // (without a key tile: whatever is there, not used)
-                tmem_load32(ot + part, o);
+                tmem_load_16x64(ot + half * 64, o);
                 tmem_wait_load32(o);
                 #pragma unroll
-                for (int ch = 0; ch < 4; ++ch) {
-                    uint32_t w[4];
-                    #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float2 f = __fmul2_rn(make_float2(__uint_as_float(o[8 * ch + 2 * e]), __uint_as_float(o[8 * ch + 2 * e + 1])), inv2);
-                        odd = __ffma2_rn(f, make_float2(0.f, 0.f), odd);
-                        const __half2 hv = __floats2half2_rn(f.x, f.y);
-                        w[e] = some ? *reinterpret_cast<const uint32_t*>(&hv) : 0u;
-                    }
-                    *reinterpret_cast<uint4*>(own + lane * 64 + ((ch ^ (lane >> 1 & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                for (int k = 0; k < 16; ++k) {
+                    const int r = k & 1, at = (lane >> 2) + 8 * r;
+                    const float2 f = __fmul2_rn(make_float2(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1])),
+                                                make_float2(inv[r], inv[r]));
+                    odd[r] = __ffma2_rn(f, make_float2(0.f, 0.f), odd[r]);
+                    const __half2 hv = __floats2half2_rn(f.x, f.y);
+                    *reinterpret_cast<uint32_t*>(own + at * 128 + (((k >> 1) ^ (at & 7)) << 4) + quad * 4) =
+                        any && l[r] != 0.f ? *reinterpret_cast<const uint32_t*>(&hv) : 0u;
                 }
                 __syncwarp();
                 uint4 v[4];
                 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const int r = k * 8 + (lane >> 2);
-                    v[k] = *reinterpret_cast<const uint4*>(own + r * 64 + (((lane & 3) ^ (r >> 1 & 3)) << 4));
+                    const int r = k * 4 + (lane >> 3);
+                    v[k] = *reinterpret_cast<const uint4*>(own + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
                 }
                 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const int r = rows0 + k * 8 + (lane >> 2), tok = r >> log_g;
+                    const int r = rows0 + k * 4 + (lane >> 3), tok = r >> log_g;
                     if (tok < left)
-                        *reinterpret_cast<uint4*>(to + tok * a.out_stride + (r & (a.G - 1)) * (D * 2) + part * 2) = v[k];
+                        *reinterpret_cast<uint4*>(to + tok * a.out_stride + (r & (a.G - 1)) * (D * 2) + half * 128) = v[k];
                 }
                 __syncwarp();
             }
             tc_fence_before();
             // A key or value that is not finite reaches, as 0 * NaN, rows that do not see it: a row that came out so
-            // is worked out again from the definition, which reads only what it sees, when both halves of it are out.
-            const bool bad = some && live && !(odd.x + odd.y == 0.f);
-            if (meet_any(pair, bad)) {
-                unsigned again = __ballot_sync(0xffffffffu, bad);
+            // is worked out again from the definition, which reads only what it sees.
+            #pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                unsigned again = __ballot_sync(0xffffffffu, any && l[r] != 0.f && row_of(r) >> log_g < left &&
+                                                                !(odd[r].x + odd[r].y == 0.f));
+                again = (again | again >> 1 | again >> 2 | again >> 3) & 0x11111111u;          // a bit per row
                 #pragma unroll 1
                 while (again) {
-                    const int r = rows0 + __ffs(again) - 1;
+                    const int at = rows0 + ((__ffs(again) - 1) >> 2) + 8 * r;
                     again &= again - 1;
-                    attend_row<D, POOL>(a, it.s, seq, it.token + rt * per_tile + (r >> log_g), it.head * a.G + (r & (a.G - 1)));
+                    attend_row<D, POOL>(a, it.s, QuerySeq{it.first, it.n, it.ctx}, it.token + rt * per_tile + (at >> log_g),
+                                        it.head * a.G + (at & (a.G - 1)));
                 }
             }
         }
@@ -546,8 +554,8 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
             auto values = [&](int t, int at, bool add) {       // O += W V (one lane)
                 const uint64_t v_desc = tc_desc(base32 + C::KV_OFF + at * C::TILE, 1024, C::HALVES * 1024);
                 #pragma unroll
-                for (int k = 0; k < kTile / 16; ++k)           // (a half's weights are at its scores' beginning)
-                    tc_mma_ts(tmem + 2 * kTile + t * D, tmem + t * kTile + (k >> 2) * kHalf + (k & 3) * 8,
+                for (int k = 0; k < kTile / 16; ++k)
+                    tc_mma_ts(tmem + 2 * kTile + t * D, tmem + t * kTile + k * 8,
                               v_desc + k * (C::HALVES * 2048 >> 4), o_shape, add || k > 0);
                 tc_commit(o_there(t));
             };
