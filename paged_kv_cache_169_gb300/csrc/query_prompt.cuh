@@ -550,90 +550,122 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
     }
     if (warp == kMmaWarp) {
         // ======== matrix products: the warp stays together, one lane issues.  A row tile's products of a key tile and its
-        // next scores go behind one another, then the other row tile's: so the two take turns, one's softmax runs while
-        // the other's products do.
+        // next scores, the next item's too, go behind one another, then the other row tile's: so the two take turns, one's
+        // softmax runs while the other's products do.
         constexpr uint32_t s_shape = tc_idesc(kTile, false), o_shape = tc_idesc(D, true);
-        // A look at a barrier takes 200 cycles beside the products' reads of shared memory: lanes 0, 1 and 2 look at one each.
-        auto wait3 = [&](uint32_t b0, int n0, uint32_t b1, int n1, uint32_t b2, int n2) {
-            const uint32_t b = lane == 1 ? b1 : lane == 2 ? b2 : b0;
-            const int n = lane == 1 ? n1 : lane == 2 ? n2 : n0;
+        // A look at a barrier takes 200 cycles beside the products' reads of shared memory: lanes 0 to 3 look at one each.
+        auto wait4 = [&](uint32_t b0, int n0, uint32_t b1, int n1, uint32_t b2, int n2, uint32_t b3, int n3) {
+            const uint32_t b = lane == 1 ? b1 : lane == 2 ? b2 : lane == 3 ? b3 : b0;
+            const int n = lane == 1 ? n1 : lane == 2 ? n2 : lane == 3 ? n3 : n0;
             return wait(b, n);
         };
         int i0 = 0, i1 = 0;                                    // the row tiles' key tiles so far
+        int j = 0;                                             // the key tile whose scores are asked for next
+        bool fresh = true;                                     // it is its item's first
+        // (Four products a turn: instructions are fetched beside the softmax's, and long straight runs of them come late:
+        // 679 us for capped 8192-token prompts where 757 and 689 were measured with eight, asked for apart and together.)
+        auto scores = [&](int t, int at, bool last) {          // S = Q K^T (one lane)
+            const uint64_t q_desc = tc_desc(base32 + C::Q_OFF + t * C::TILE, 0, 1024);
+            const uint64_t k_desc = tc_desc(base32 + C::KV_OFF + at * C::TILE, 0, C::HALVES * 1024);
+            #pragma unroll 4
+            for (int k = 0; k < D / 16; ++k)
+                tc_mma_ss(tmem + t * kTile, q_desc + (((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4),
+                          k_desc + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), s_shape, k > 0);
+            tc_commit(s_there(t));
+            if (last) tc_commit(q_free(t));
+        };
+        auto values = [&](int t, int at, bool add) {           // O += W V (one lane)
+            const uint64_t v_desc = tc_desc(base32 + C::KV_OFF + at * C::TILE, 1024, C::HALVES * 1024);
+            #pragma unroll 4
+            for (int k = 0; k < kTile / 16; ++k)
+                tc_mma_ts(tmem + 2 * kTile + t * D, tmem + t * kTile + k * 8, v_desc + k * (C::HALVES * 2048 >> 4), o_shape,
+                          add || k > 0);
+            tc_commit(o_there(t));
+        };
+        // What the next key tile's scores of row tile t take: the tile is on; it is t's last of the item, or t has none.
+        struct Next { bool on, last, none; };
+        auto next_of = [&](int t, bool more) {
+            const bool on = more && keys.on(t, j);
+            return Next{on, on && j == (BIAS ? keys.a(t) : keys.b(t) - 1), fresh && keys.a(t) == keys.b(t)};
+        };
+        auto ask = [&](int t, int at, const Next& n) {         // (one lane)
+            if (n.on) scores(t, at, n.last);
+            else if (n.none) mbar_arrive(q_free(t));
+        };
         Ring<C::SLOTS> ring;
-        while (next_item()) {
-            bool some0 = false, some1 = false;                 // a key tile of this item's behind us
-            auto is_last = [&](int t, int j) { return j == (BIAS ? keys.a(t) : keys.b(t) - 1); };
-            auto scores = [&](int t, int at, int j) {          // S = Q K^T (one lane)
-                const uint64_t q_desc = tc_desc(base32 + C::Q_OFF + t * C::TILE, 0, 1024);
-                const uint64_t k_desc = tc_desc(base32 + C::KV_OFF + at * C::TILE, 0, C::HALVES * 1024);
-                #pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    tc_mma_ss(tmem + t * kTile, q_desc + (((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4),
-                              k_desc + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), s_shape, k > 0);
-                tc_commit(s_there(t));
-                if (is_last(t, j)) tc_commit(q_free(t));
-            };
-            auto values = [&](int t, int at, bool add) {       // O += W V (one lane)
-                const uint64_t v_desc = tc_desc(base32 + C::KV_OFF + at * C::TILE, 1024, C::HALVES * 1024);
-                #pragma unroll
-                for (int k = 0; k < kTile / 16; ++k)
-                    tc_mma_ts(tmem + 2 * kTile + t * D, tmem + t * kTile + k * 8,
-                              v_desc + k * (C::HALVES * 2048 >> 4), o_shape, add || k > 0);
-                tc_commit(o_there(t));
-            };
-            int j = keys.first();
-            bool now0 = keys.on(0, j), now1 = keys.on(1, j);
-            if (!wait3(q_there(0), count - 1, q_there(1), count - 1, keys.is(j) ? full(ring.slot) : q_there(0),
-                       keys.is(j) ? ring.times : count - 1))
+        bool item = next_item();
+        while (item && fine) {
+            j = keys.first();
+            fresh = true;
+            const bool more0 = keys.is(j);
+            if (!wait4(q_there(0), count - 1, q_there(1), count - 1, more0 ? full(ring.slot) : q_there(0),
+                       more0 ? ring.times : count - 1, q_there(0), count - 1))
                 break;
-            if (keys.is(j) && elect_one()) {
-                if (now0) scores(0, ring.slot, j);
-                if (now1) scores(1, ring.slot, j);
-                tc_commit(empty(ring.slot));
+            const Next first0 = next_of(0, more0), first1 = next_of(1, more0);
+            if (elect_one()) {
+                ask(0, ring.slot, first0);
+                ask(1, ring.slot, first1);
+                if (more0) tc_commit(empty(ring.slot));
             }
             __syncwarp();
+            if (!more0) {
+                item = next_item();
+                continue;
+            }
+            bool more = true, now0 = first0.on, now1 = first1.on, some0 = false, some1 = false;
             #pragma unroll 1
-            while (keys.is(j)) {                               // (this tile's scores are issued)
-                const int jn = keys.next(j);
-                const bool more = keys.is(jn), then0 = more && keys.on(0, jn), then1 = more && keys.on(1, jn);
+            while (more) {                                     // (a key tile's scores are issued: its values, the next one's scores)
                 ring.advance();
                 const int v = ring.slot, v_times = ring.times;
                 ring.advance();
                 const int k = ring.slot;
-                // its values, the next tile's keys and the weights
-                if (!wait3(full(v), v_times, more ? full(k) : full(v), more ? ring.times : v_times, now0 ? w_there(0) : full(v),
-                           now0 ? i0 : v_times))
+                j = keys.next(j);
+                more = keys.is(j);
+                fresh = false;
+                if (!more && (item = next_item())) {           // (one without key tiles waits for these products' end)
+                    j = keys.first();
+                    fresh = more = keys.is(j);
+                }
+                if (!fine) break;
+                const Next n0 = next_of(0, more), n1 = next_of(1, more);
+                // its values and weights, the next tile's keys; of another item, these and its queries by themselves
+                const bool with = more && !fresh;
+                if (!wait4(full(v), v_times, with ? full(k) : full(v), with ? ring.times : v_times, now0 ? w_there(0) : full(v),
+                           now0 ? i0 : v_times, full(v), v_times))
                     break;
                 tc_fence_after();
                 if (elect_one()) {
                     if (now0) values(0, v, some0);
-                    if (then0) scores(0, k, jn);
+                    if (!fresh) ask(0, k, n0);
                 }
+                __syncwarp();
+                if (fresh && !wait4(full(k), ring.times, q_there(0), count - 1, full(k), ring.times, full(k), ring.times)) break;
+                if (fresh && elect_one()) ask(0, k, n0);
                 __syncwarp();
                 if (now1 && !wait(w_there(1), i1)) break;
                 tc_fence_after();
                 if (elect_one()) {
                     if (now1) values(1, v, some1);
                     tc_commit(empty(v));
-                    if (then1) scores(1, k, jn);
-                    if (more) tc_commit(empty(k));
+                    if (!fresh) {
+                        ask(1, k, n1);
+                        if (more) tc_commit(empty(k));
+                    }
+                }
+                __syncwarp();
+                if (fresh && !wait(q_there(1), count - 1)) break;
+                if (fresh && elect_one()) {
+                    ask(1, k, n1);
+                    tc_commit(empty(k));
                 }
                 __syncwarp();
                 i0 += now0;
                 i1 += now1;
-                some0 |= now0;
-                some1 |= now1;
-                j = jn;
-                now0 = then0;
-                now1 = then1;
+                some0 = !fresh && (some0 || now0);             // (the next one's sums are added to its item's)
+                some1 = !fresh && (some1 || now1);
+                now0 = n0.on;
+                now1 = n1.on;
             }
-            if (!fine) break;
-            if (elect_one()) {                                 // without a key tile: not asked for by the scores
-                if (keys.a0 == keys.b0) mbar_arrive(q_free(0));
-                if (keys.a1 == keys.b1) mbar_arrive(q_free(1));
-            }
-            __syncwarp();
         }
         if (elect_one()) tc_commit(done);                      // nothing of it is in flight at the end
         __syncwarp();
