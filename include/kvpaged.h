@@ -564,10 +564,10 @@ KV_API int paged_decode_attention_ex(kv_pool* pool, const kv_decode_args* args);
  *   workspace      device, >= paged_query_workspace_size(...) bytes, 256-byte aligned; contents
  *                  need not be initialised; not shared between calls that may overlap.
  *   flags          0, or a sum of KV_DECODE_WORKSPACE_ZEROED (the workspace was zero-filled once and
- *                  used since only by calls of this entry point of one shape: pool, batch,
- *                  num_tokens, num_q_heads, max_queries, max_context, window, with no device error
- *                  in between) and KV_DECODE_PDL (may be scheduled while the previous kernel on the
- *                  stream finishes; reads and writes nothing before that kernel has completed).
+ *                  used since only by calls of this entry point on this pool, of any shapes it is
+ *                  large enough for, with no device error in between) and KV_DECODE_PDL (may be
+ *                  scheduled while the previous kernel on the stream finishes; reads and writes
+ *                  nothing before that kernel has completed).
  * Arithmetic: float32 scores, softmax and sums; products of float16 operands (q, K and V; FP8
  * codes convert exactly and their scales are applied in float32; 4-bit values are exact); the
  * softmax weights enter the V products as float16 (relative 2^-11; down to 2^-21 of a row's

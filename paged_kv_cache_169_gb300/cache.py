@@ -389,8 +389,8 @@ class PagedKVCache:
 
     def query_workspace(self, batch: int, num_q_heads: int, max_queries: int, max_context: int, window: int = 0,
                         num_tokens: int | None = None) -> torch.Tensor:
-        """A new zero-filled workspace for query_attention, also with KV_DECODE_WORKSPACE_ZEROED for calls
-        of this one shape.  num_tokens: rows of q (default batch * max_queries)."""
+        """A new zero-filled workspace for query_attention, also with KV_DECODE_WORKSPACE_ZEROED: for calls
+        of this shape, or of any that needs no more.  num_tokens: rows of q (default batch * max_queries)."""
         a = abi.kv_query_args()
         a.num_q_heads, a.batch, a.max_queries, a.max_context, a.window = num_q_heads, batch, max_queries, max_context, window
         a.num_tokens = batch * max_queries if num_tokens is None else num_tokens
@@ -415,43 +415,41 @@ class PagedKVCache:
         of q's type; rows of no sequence are left as they were (a new tensor: zero).  flags:
         abi.KV_DECODE_WORKSPACE_ZEROED (with a workspace from query_workspace), abi.KV_DECODE_PDL."""
         dev, d = self.k[0].get_device(), self.head_dim
-        dt = torch.float32 if self.dtype == "f32" else torch.float16
-        if q.dim() != 3 or q.shape[2] != d or q.dtype != dt:
+        dt, shape = torch.float32 if self.dtype == "f32" else torch.float16, q.shape
+        if len(shape) != 3 or shape[2] != d or q.dtype != dt:
             raise ValueError(f"q must be {dt} [num_tokens, Hq, {d}]")
-        n, hq = q.shape[0], q.shape[1]
+        n, hq, _ = shape
         if query_start.dtype != torch.int32 or block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
             raise ValueError("query_start, block_tables and context_lens must be int32")
-        batch = context_lens.numel()
-        if query_start.numel() != batch + 1 or block_tables.dim() != 2 or block_tables.shape[0] != batch:
+        batch, tables = context_lens.numel(), block_tables.shape
+        if query_start.numel() != batch + 1 or len(tables) != 2 or tables[0] != batch:
             raise ValueError("query_start must have batch + 1 entries and block_tables batch rows")
         if out is None:
             with _alloc_on(stream):
-                out = torch.zeros((n, hq, d), dtype=dt, device=q.device)
-        elif out.shape != q.shape or out.dtype != dt:
+                out = torch.zeros(shape, dtype=dt, device=q.device)
+        elif out.shape != shape or out.dtype != dt:
             raise ValueError(f"out must be {dt} of q's shape")
-        a = abi.kv_query_args()
-        a.layer, a.num_q_heads = layer, hq
-        (a.q, a.q_stride), (a.out, a.out_stride) = _rows(q, n, hq, d, "q", dev), _rows(out, n, hq, d, "out", dev)
-        a.query_start, a.num_tokens, a.max_queries = _ptr_on(query_start, "query_start", dev), n, max_queries
-        a.block_tables, a.max_blocks_per_seq = _ptr_on(block_tables, "block_tables", dev), block_tables.shape[1]
-        a.context_lens, a.batch, a.max_context = _ptr_on(context_lens, "context_lens", dev), batch, max_context
-        a.window, a.scale, a.score_cap = window, float(scale), float(score_cap)
+        slopes_p = ranges_p = 0
         if slopes is not None:
             if slopes.dtype != torch.float32 or slopes.numel() != hq:
                 raise ValueError("slopes must be float32 [Hq]")
-            a.slopes = _ptr_on(slopes, "slopes", dev)
+            slopes_p = _ptr_on(slopes, "slopes", dev)
         if ranges is not None:
             if ranges.dtype != torch.int32 or ranges.shape != (n, 2):
                 raise ValueError("ranges must be int32 [num_tokens, 2]")
-            a.ranges = _ptr_on(ranges, "ranges", dev)
+            ranges_p = _ptr_on(ranges, "ranges", dev)
+        (qp, qs), (op, os) = _rows(q, n, hq, d, "q", dev), _rows(out, n, hq, d, "out", dev)
+        a = abi.kv_query_args(layer, qp, hq, qs, op, os, _ptr_on(query_start, "query_start", dev), n, max_queries,
+                              _ptr_on(block_tables, "block_tables", dev), tables[1],
+                              _ptr_on(context_lens, "context_lens", dev), batch, max_context, window, float(scale),
+                              float(score_cap), slopes_p, ranges_p, 0, 0, flags, _stream(stream))
         if workspace is None:
             if flags & abi.KV_DECODE_WORKSPACE_ZEROED:
                 raise ValueError("KV_DECODE_WORKSPACE_ZEROED needs a workspace of the caller's")
             need = abi.paged_query_workspace_size(self.handle, a)
             with _alloc_on(stream):
                 workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        a.workspace, a.workspace_bytes = _ptr_on(workspace, "workspace", dev), workspace.numel() * workspace.element_size()
-        a.flags, a.stream = flags, _stream(stream)
+        a.workspace, a.workspace_bytes = _ptr_on(workspace, "workspace", dev), workspace.nbytes
         abi.paged_query_attention(self.handle, a)
         return out
 
