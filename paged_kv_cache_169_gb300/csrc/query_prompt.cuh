@@ -189,7 +189,7 @@ __device__ __forceinline__ int claimed_item(const uint4& v) {
     return x;
 }
 
-template <int D, kv_dtype POOL, bool BIAS>
+template <int D, kv_dtype POOL, bool BIAS, bool CAP>
 __global__ void __launch_bounds__(PromptCfg<D, POOL>::WARPS * 32, 1)
 query_prompt_kernel(const __grid_constant__ PromptArgs p) {
     using C = PromptCfg<D, POOL>;
@@ -213,7 +213,7 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
     auto item_there = [&](int i) { return bar(B0 + 10 + i); };
     auto item_free = [&](int i) { return bar(B0 + 12 + i); };
     const uint32_t edge = bar(B0 + 14), done = bar(B0 + 15), claim = bar(B0 + 16);
-    float* const factors = reinterpret_cast<float*>(smem + C::FACTOR_OFF);     // FP8: [tile][keys, values][block]
+    float* const factors = reinterpret_cast<float*>(smem + C::FACTOR_OFF);     // FP8: [tile][keys, values][8 tokens]
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::SLOTS; ++i) {
@@ -286,11 +286,10 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
         const uint32_t lanes = static_cast<uint32_t>(rows0) << 16;
         const uint32_t st = tmem + lanes + rt * kTile, ot = tmem + lanes + 2 * kTile + rt * D;
         char* const own = smem + C::OUT_OFF + warp * (16 * 128);
-        const bool cap = a.cap > 0.f;
         constexpr int DIR = BIAS ? -1 : 1;                     // of the key tiles
         const float qscale = a.scale * kLog2e;
-        const float k2 = cap ? 2.f * kLog2e * (a.scale / a.cap) : 0.f, capl = a.cap * kLog2e;
-        const float c = cap || BIAS ? 1.f : qscale;            // scores to log2 units
+        const float k2 = CAP ? 2.f * kLog2e * (a.scale / a.cap) : 0.f, capl = a.cap * kLog2e;
+        const float c = CAP || BIAS ? 1.f : qscale;            // scores to log2 units
         int i = 0, tiles = 0;                                  // this row tile's key tiles so far; the items'
         auto row_of = [&](int r) { return rows0 + (lane >> 2) + 8 * r; };
         // An item's part of this thread, taken while the last products of the item before are made.  (The rest stays in
@@ -298,7 +297,7 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
         struct Part {
             int steps, j0;                                     // key tiles; the first one's position
             int2 sees[2];
-            float slope[2], inv_vref;
+            float slope[2];
             int pos0;                                          // the first row's position
             int tile;                                          // FP8: the first one's number
         } next;
@@ -318,7 +317,6 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                 next.slope[r] = BIAS ? a.slopes[x.head * a.G + (row_of(r) & (a.G - 1))] * kLog2e : 0.f;
             }
             next.pos0 = x.ctx - x.n + x.token + rt * per_tile;
-            next.inv_vref = POOL == KV_FP8_E4M3 ? 1.f / x.vref : 1.f;
             return true;
         };
         bool some_item = fetch();
@@ -328,7 +326,7 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
             const int stop = i + next.steps, pos0 = next.pos0;
             int j0 = next.j0, tile = next.tile;
             const int2 sees[2] = {next.sees[0], next.sees[1]};
-            const float slope[2] = {next.slope[0], next.slope[1]}, inv_vref = next.inv_vref;
+            const float slope[2] = {next.slope[0], next.slope[1]};
             float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};    // the base (log2 units), this thread's sum of weights
             const int i0 = i;
             #pragma unroll 1
@@ -341,22 +339,28 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                 tmem_load_16x64(st + 64, xr + 32);
                 tmem_wait_load32(xr);
                 tmem_wait_load32(xr + 32);
-                const float* scales = nullptr;
+                const float4* scales = nullptr;                // FP8: per 8 keys, then per 8 values
                 if constexpr (POOL == KV_FP8_E4M3) {
-                    scales = factors + tile++ % kFactorTiles * 32;
+                    scales = reinterpret_cast<const float4*>(factors + tile++ % kFactorTiles * 32);
                     #pragma unroll
-                    for (int g = 0; g < 16; ++g) {
-                        const float f = scales[8 * g >> a.log_b];
+                    for (int k = 0; k < 4; ++k) {
+                        const float4 f = scales[k];
+                        const float of[4] = {f.x, f.y, f.z, f.w};
                         #pragma unroll
-                        for (int e = 0; e < 4; ++e) x[4 * g + e] *= f;
+                        for (int e = 0; e < 8; ++e) {
+                            float* const y = x + 16 * k + 2 * e;
+                            const float2 v = __fmul2_rn(make_float2(y[0], y[1]), make_float2(of[e >> 1], of[e >> 1]));
+                            y[0] = v.x;
+                            y[1] = v.y;
+                        }
                     }
                 }
-                if (cap) {
+                if (CAP) {
                     #pragma unroll
                     for (int k = 0; k < 64; k += 4) capped4(x + k, k2, capl);
                 }
                 if (BIAS) {
-                    const float mul = cap ? 1.f : qscale;
+                    const float mul = CAP ? 1.f : qscale;
                     #pragma unroll
                     for (int r = 0; r < 2; ++r) {
                         const float from = static_cast<float>(pos0 + (row_of(r) >> log_g) - j0 - 2 * quad);
@@ -422,6 +426,7 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                 // weights, and their sums
                 const float2 c2 = make_float2(c, c);
                 float2 sum[2];
+                float4 vf;
                 uint32_t w[32];
                 #pragma unroll
                 for (int k = 0; k < 32; ++k) {
@@ -432,7 +437,8 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                     y.y = ex2_approx(y.y);
                     sum[r] = k < 2 ? y : __fadd2_rn(sum[r], y);
                     if constexpr (POOL == KV_FP8_E4M3) {
-                        const float f = scales[16 + (4 * (k & ~1) >> a.log_b)] * inv_vref;
+                        if (k % 8 == 0) vf = scales[4 + k / 8];
+                        const float f = k % 8 < 2 ? vf.x : k % 8 < 4 ? vf.y : k % 8 < 6 ? vf.z : vf.w;
                         y = __fmul2_rn(y, make_float2(f, f));
                     }
                     const __half2 hv = __floats2half2_rn(y.x, y.y);
@@ -563,7 +569,7 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
         int j = 0;                                             // the key tile whose scores are asked for next
         bool fresh = true;                                     // it is its item's first
         // (Four products a turn: instructions are fetched beside the softmax's, and long straight runs of them come late:
-        // 679 us for capped 8192-token prompts where 757 and 689 were measured with eight, asked for apart and together.)
+        // 679 us for 2 x 4096 capped tokens where 757 and 689 were measured with eight, asked for apart and together.)
         auto scores = [&](int t, int at, bool last) {          // S = Q K^T (one lane)
             const uint64_t q_desc = tc_desc(base32 + C::Q_OFF + t * C::TILE, 0, 1024);
             const uint64_t k_desc = tc_desc(base32 + C::KV_OFF + at * C::TILE, 0, C::HALVES * 1024);
@@ -692,9 +698,11 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                 const int next_id = look_up(jn);
                 const uint32_t bytes = ((rows + a.B - 1) >> log_b) * block_bytes;
                 if constexpr (POOL == KV_FP8_E4M3) {
-                    if (blk < 16) {
-                        factors[(ring >> 1) % kFactorTiles * 32 + blk] = id >= 0 ? a.kscale[id] : 0.f;
-                        factors[(ring >> 1) % kFactorTiles * 32 + 16 + blk] = id >= 0 ? a.vscale[id] : 0.f;
+                    const int of = __shfl_sync(0xffffffffu, id, lane < 16 ? 8 * lane >> log_b : 0);
+                    if (lane < 16) {                           // per 8 tokens
+                        float* const f = factors + (ring >> 1) % kFactorTiles * 32 + lane;
+                        f[0] = of >= 0 ? a.kscale[of] : 0.f;
+                        f[16] = of >= 0 ? a.vscale[of] / it.vref : 0.f;
                     }
                     __syncwarp();
                 }
@@ -865,12 +873,12 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
     }
 }
 
-template <typename C, bool BIAS>
+template <typename C, bool BIAS, bool CAP>
 int launch_prompt_typed(const kv_pool* pool, const PromptArgs& p, bool pdl, cudaStream_t stream) {
     static unsigned long long attr_done = 0;               // the shared-memory opt-in is a per-device attribute
     const unsigned long long bit = 1ull << (pool->device & 63);
     if (!(attr_done & bit)) {
-        if (cudaFuncSetAttribute(query_prompt_kernel<C::D, C::POOL, BIAS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
+        if (cudaFuncSetAttribute(query_prompt_kernel<C::D, C::POOL, BIAS, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
             cudaSuccess)
             return KV_ERR_CUDA;
         attr_done |= bit;
@@ -885,7 +893,7 @@ int launch_prompt_typed(const kv_pool* pool, const PromptArgs& p, bool pdl, cuda
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
-    if (cudaLaunchKernelEx(&cfg, query_prompt_kernel<C::D, C::POOL, BIAS>, p) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, query_prompt_kernel<C::D, C::POOL, BIAS, CAP>, p) != cudaSuccess) {
         cudaGetLastError();
         return KV_ERR_CUDA;
     }
@@ -894,11 +902,14 @@ int launch_prompt_typed(const kv_pool* pool, const PromptArgs& p, bool pdl, cuda
 
 template <kv_dtype POOL>
 int launch_prompt_pool(const kv_pool* pool, const PromptArgs& p, bool pdl, cudaStream_t stream) {
-    auto launch = [&](auto bias) {
-        return pool->desc.head_dim == 128 ? launch_prompt_typed<PromptCfg<128, POOL>, bias.value>(pool, p, pdl, stream)
-                                          : launch_prompt_typed<PromptCfg<64, POOL>, bias.value>(pool, p, pdl, stream);
+    auto launch = [&](auto bias, auto cap) {
+        return pool->desc.head_dim == 128 ? launch_prompt_typed<PromptCfg<128, POOL>, bias.value, cap.value>(pool, p, pdl, stream)
+                                          : launch_prompt_typed<PromptCfg<64, POOL>, bias.value, cap.value>(pool, p, pdl, stream);
     };
-    return p.a.slopes ? launch(std::true_type{}) : launch(std::false_type{});
+    const std::true_type yes{};
+    const std::false_type no{};
+    if (p.a.cap > 0.f) return p.a.slopes ? launch(yes, yes) : launch(no, yes);
+    return p.a.slopes ? launch(yes, no) : launch(no, no);
 }
 
 }  // namespace
