@@ -1,4 +1,28 @@
 // paged_query_attention for many rows: the tensor-core kernel.
+//
+// Mathematics.  Rows are (token, query head) of a K/V head.  Over key tiles of 128 a row keeps a base m, the sum l of its
+// weights and O: with t_j the masked scores in log2 units, w_j = 2^(t_j - m + 7) in float16, l += w_j, O += w_j v_j, and
+// where a tile's maximum leaves m behind by more than 2^8 (rare after the first tile) m goes up and l and O by the
+// difference down.  The result is O / l.
+//
+// Bound.  4 D operations per visible pair on the tensor cores; the special function unit makes an exponential a pair (a
+// capped score an exponential and a quarter of a reciprocal more), 512 cycles of 128 x 128 pairs where the matrix products
+// take 1024 (D = 128).
+//
+// Shape.  A work item is two row tiles of 128 rows (a token's G heads side by side) of one K/V head; a CTA per SM takes
+// items from the grid as long as there are any.  Tensor memory holds two score tiles (the float16 weights go over them)
+// and two O: 512 columns at D = 128, so a row tile's products and its softmax follow one another, and the two row tiles
+// take turns.  Warps 0-15 softmax, 8 to a row tile, 16 rows each; 16 matrix products; 17 keys and values (TMA for float16
+// pools, bulk copies and four widening warps for the others); 18 items and queries, an item ahead.
+//
+// Measured (us; D = 128 but for the last): 4 x 2048 tokens of 40 heads 178 (960 TFLOP/s), 2 x 8192 of them 1003 (1370);
+// 2 x 4096 tokens, 64 / 8 heads, capped 671; 512 rows after 16k tokens in FP8, 4 x, 64 / 8 heads 1210 (883); packed
+// documents with a bias, 4-bit, 240; ragged prompts, D = 64, prefixes seen both ways 268 (543).  What it waits for: per key
+// tile 1660 cycles of softmax and 1660 of products and barrier round trips one behind the other; an item's start and end
+// 7000 cycles.  Before: 8 softmax warps with 64-key steps 187, 768, 1540, 313, 267; store warps for the result and 128-key
+// steps 211, 797, 1690, 284, 260; both row tiles' products issued as they came (the softmaxes ran at the same time, then
+// the products) 190, 806, 1664, 236, 266; scores taken 64 columns at a time (more free registers, the base's loop spilt)
+// 264, 1160, 2127, 285, 275.
 #pragma once
 
 #include <type_traits>
@@ -69,8 +93,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 // capped() of four with one reciprocal: 1/a = b (cd) / (ab cd) and so on, each factor below 2^30 + 1 (tanh is 1 long
-// before).  Four multiplications and the reciprocal are off by 7 2^-24 together: t within 2^-20 of the cap.  The scores
-// of capped prompts are bound by the special function unit, which makes two of these four where it made eight.
+// before).  Four multiplications and the reciprocal are off by 7 2^-24 together: t within 2^-20 of the cap.  The special
+// function unit makes 5 values for four scores where it made 8 (2 x 4096 capped tokens: 773 -> 700 us then).
 __device__ __forceinline__ void capped4(float* x, float k2, float capl) {
     float2 y[2], a[2];
     #pragma unroll
@@ -119,8 +143,9 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* er
 
 // Key tiles [a, b) of each row tile, numbered from position `base`; the work item's are those that either row tile
 // needs.  With a distance bias they are taken from the last one down: it lowers the scores on the way, and the softmax's
-// base, once found, stays (upwards, steep heads raise it at every tile).  Without one upwards: the rows of a causal tile
-// then find their base in the same tile.
+// base, once found, stays (upwards, steep heads raise it at every tile: 313 us against 250 for packed 4-bit documents).
+// Without one upwards: the rows of a causal tile then find their base in the same tile (a 2048-token prompt took 5% longer
+// downwards).
 template <bool DOWN>
 struct KeyTiles {
     int base, end, a0, b0, a1, b1, n;
@@ -569,7 +594,7 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
         int j = 0;                                             // the key tile whose scores are asked for next
         bool fresh = true;                                     // it is its item's first
         // (Four products a turn: instructions are fetched beside the softmax's, and long straight runs of them come late:
-        // 679 us for 2 x 4096 capped tokens where 757 and 689 were measured with eight, asked for apart and together.)
+        // 672 and 178 us for the capped and the 2048-token prompts where eight take 684 and 187.)
         auto scores = [&](int t, int at, bool last) {          // S = Q K^T (one lane)
             const uint64_t q_desc = tc_desc(base32 + C::Q_OFF + t * C::TILE, 0, 1024);
             const uint64_t k_desc = tc_desc(base32 + C::KV_OFF + at * C::TILE, 0, C::HALVES * 1024);
