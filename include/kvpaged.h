@@ -537,8 +537,8 @@ KV_API int paged_decode_attention_ex(kv_pool* pool, const kv_decode_args* args);
  *   q              device [num_tokens] rows of num_q_heads*head_dim elements: float32 for F32
  *                  pools, float16 for the others; 16-byte aligned.
  *   num_q_heads    G * num_heads, G in {1, 2, 4, 8}; query head j reads KV head j / G.
- *   out            device [num_tokens] rows of q's type, written, not accumulated; must not
- *                  overlap q.  Rows of no sequence are left as they were.
+ *   out            device [num_tokens] rows of q's type, written, not accumulated; no row may
+ *                  overlap one of q (out == q is refused).  Rows of no sequence are left as they were.
  *   q_stride, out_stride  elements between the rows of two tokens (heads are contiguous in a
  *                  row): at least a row, below 2^28, a multiple of 16 bytes.
  *   query_start    device int32 [batch + 1].
@@ -550,8 +550,9 @@ KV_API int paged_decode_attention_ex(kv_pool* pool, const kv_decode_args* args);
  *                  below 0 or above min(max_blocks_per_seq*block_size, max_context) are clamped
  *                  and set KV_DEVERR_CONTEXT; so does c < n (rows before position 0 see nothing
  *                  without ranges).  A block id outside the pool that some row's positions
- *                  reach sets KV_DEVERR_BLOCK_ID and block 0 is read; entries of blocks that no
- *                  row of the sequence sees are not read (they may be -1: kv_alloc_seq_trim).
+ *                  reach sets KV_DEVERR_BLOCK_ID and block 0 is read; entries of blocks wholly
+ *                  before the first, or behind the last, position that a row of the sequence sees
+ *                  are not read (they may be -1: kv_alloc_seq_trim).
  *   max_context    host upper bound of context_lens, 0 .. 2^24.  (Calls of more than 2^30 row tiles or,
  *                  with at most 16 rows of a KV head, 16-token chunks in 1024 sequences are refused.)
  *   window         0, or the last `window` positions only.

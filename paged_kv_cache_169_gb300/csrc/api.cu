@@ -509,7 +509,7 @@ int paged_query_attention(kv_pool* pool, const kv_query_args* x) {
         (x->flags & ~(KV_DECODE_WORKSPACE_ZEROED | KV_DECODE_PDL)))
         return KV_ERR_INVALID_ARG;
     if (x->batch == 0 || x->max_queries == 0) return KV_OK;
-    if (!x->q || !x->out || !x->query_start || !x->block_tables || !x->context_lens || !x->workspace ||
+    if (!x->q || !x->out || x->q == x->out || !x->query_start || !x->block_tables || !x->context_lens || !x->workspace ||
         x->max_blocks_per_seq < 1)
         return KV_ERR_INVALID_ARG;
     if (!kvp::aligned16(x->q) || !kvp::aligned16(x->out) || (reinterpret_cast<uintptr_t>(x->workspace) & 255u) != 0 ||

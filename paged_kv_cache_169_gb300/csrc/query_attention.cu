@@ -7,27 +7,135 @@ namespace {
 
 constexpr int kRowWarps = 8;
 
-// A warp per (row, query head), in float32 from the definition.
-template <int D, kv_dtype POOL>
-__global__ void __launch_bounds__(kRowWarps * 32) query_rows_kernel(const __grid_constant__ QueryArgs a) {
+// R rows of K/V head h (row r: token r / G, query head h G + r % G) from r0 on, by one warp, in float32 from the
+// definition: only what a row sees is read for it.  Eight lanes share a key (lane t of them has the t-th 16 bytes of every
+// 128), four keys go side by side with a softmax state each, joined at the end.
+template <int D, int R>
+__device__ __forceinline__ void attend_rows(const QueryArgs& a, int s, QuerySeq seq, int h, int r0) {
+    constexpr int N = D / 8;
+    const int lane = threadIdx.x & 31, part = lane & 7, which = lane >> 3;
+    auto load_parts = [&](const char* row, float (&x)[N]) {
+        #pragma unroll
+        for (int e = 0; e < N; e += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(row + part * 16 + e * 32);
+            x[e] = f.x; x[e + 1] = f.y; x[e + 2] = f.z; x[e + 3] = f.w;
+        }
+    };
+    int2 range[R];
+    int lo = 1 << 30, hi = 0, pos[R];
+    float q[R][N], o[R][N], m[R], l[R], slope[R];
+    #pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int i = (r0 + r) / a.G, head = h * a.G + (r0 + r) % a.G;
+        const bool some = i < seq.n;
+        range[r] = some ? row_range(a, seq, i) : make_int2(0, 0);
+        if (range[r].x < range[r].y) {
+            lo = min(lo, range[r].x);
+            hi = max(hi, range[r].y);
+        }
+        pos[r] = seq.ctx - seq.n + i;
+        slope[r] = a.slopes ? a.slopes[head] : 0.f;
+        m[r] = -CUDART_INF_F;
+        l[r] = 0.f;
+        load_parts(a.q + static_cast<int64_t>(seq.first + (some ? i : 0)) * a.q_stride + head * (D * 4), q[r]);
+        #pragma unroll
+        for (int e = 0; e < N; ++e) o[r][e] = 0.f;
+    }
+    auto seen_by = [&](int r, int j) { return j >= range[r].x && j < range[r].y; };
+    auto any_sees = [&](int j) {
+        bool any = false;
+        #pragma unroll
+        for (int r = 0; r < R; ++r) any |= seen_by(r, j);
+        return any;
+    };
+    // (a key's block is looked up an iteration ahead)
+    auto look_up = [&](int j) { return any_sees(j) ? query_block(a, s, j) : -1; };
+    int next = look_up(lo + which);
+    #pragma unroll 1
+    for (int j0 = lo; j0 < hi; j0 += 4) {
+        const int j = j0 + which, id = next;
+        next = look_up(j + 4);
+        float x[N], v[N], dot[R];
+        #pragma unroll
+        for (int r = 0; r < R; ++r) dot[r] = 0.f;
+        if (id >= 0) {
+            const int64_t at = ((static_cast<int64_t>(id) * a.H + h) * a.B + (j & (a.B - 1))) * (D * 4);
+            load_parts(a.kpool + at, x);
+            load_parts(a.vpool + at, v);
+            #pragma unroll
+            for (int r = 0; r < R; ++r)
+                #pragma unroll
+                for (int e = 0; e < N; ++e) dot[r] = fmaf(q[r][e], x[e], dot[r]);
+        }
+        #pragma unroll
+        for (int k = 1; k < 8; k *= 2)
+            #pragma unroll
+            for (int r = 0; r < R; ++r) dot[r] += __shfl_xor_sync(0xffffffffu, dot[r], k);
+        #pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (!seen_by(r, j)) continue;
+            float t = dot[r] * a.scale;
+            if (a.cap > 0.f) t = a.cap * tanhf(t / a.cap);
+            if (a.slopes) t = fmaf(-slope[r], static_cast<float>(abs(pos[r] - j)), t);
+            t *= kLog2e;
+            if (t > m[r]) {                                    // (rare after the first keys; NaN: it reaches the weight)
+                const float keep = ex2_approx(m[r] - t);
+                m[r] = t;
+                l[r] *= keep;
+                #pragma unroll
+                for (int e = 0; e < N; ++e) o[r][e] *= keep;
+            }
+            const float w = ex2_approx(t - (m[r] == -CUDART_INF_F ? 0.f : m[r]));
+            l[r] += w;
+            #pragma unroll
+            for (int e = 0; e < N; ++e) o[r][e] = fmaf(w, v[e], o[r][e]);
+        }
+    }
+    #pragma unroll
+    for (int r = 0; r < R; ++r) {
+        #pragma unroll
+        for (int k = 8; k < 32; k *= 2) {
+            const float other = __shfl_xor_sync(0xffffffffu, m[r], k);
+            const float to = fmaxf(m[r], other), base = to == -CUDART_INF_F ? 0.f : to;
+            const float mine = ex2_approx(m[r] - base), theirs = ex2_approx(other - base);
+            l[r] = l[r] * mine + __shfl_xor_sync(0xffffffffu, l[r], k) * theirs;
+            #pragma unroll
+            for (int e = 0; e < N; ++e) o[r][e] = o[r][e] * mine + __shfl_xor_sync(0xffffffffu, o[r][e], k) * theirs;
+            m[r] = to;
+        }
+        const int i = (r0 + r) / a.G;
+        if (which != 0 || i >= seq.n) continue;
+        const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
+        char* row = a.out + static_cast<int64_t>(seq.first + i) * a.out_stride + (h * a.G + (r0 + r) % a.G) * (D * 4) + part * 16;
+        #pragma unroll
+        for (int e = 0; e < N; e += 4)
+            *reinterpret_cast<float4*>(row + e * 32) = make_float4(o[r][e] * inv, o[r][e + 1] * inv, o[r][e + 2] * inv, o[r][e + 3] * inv);
+    }
+}
+
+// float32 pools: a warp per R rows of a K/V head, in float32 from the definition.  Bound: the FMA pipe, 4 D operations a
+// pair, at 0.15 of its rate for the latency of the loads (4 prompts of 2048 tokens, 40 heads: 14.9 ms; a row per warp
+// 41.9, four rows, whose registers leave one CTA per SM, 19.1).  R: 2, or 1 where a K/V head has a single row.
+template <int D, int R>
+__global__ void __launch_bounds__(kRowWarps * 32, 2) query_rows_kernel(const __grid_constant__ QueryArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int heads = a.H * a.G;
-    const int64_t per_seq = static_cast<int64_t>(a.max_queries) * heads, all = per_seq * a.batch;
+    const int per_head = (a.max_queries * a.G + R - 1) / R;
+    const int64_t per_seq = static_cast<int64_t>(per_head) * a.H, all = per_seq * a.batch;
     const int64_t step = static_cast<int64_t>(gridDim.x) * kRowWarps;
     #pragma unroll 1
     for (int64_t u = static_cast<int64_t>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5); u < all; u += step) {
         const int s = static_cast<int>(u / per_seq);
-        const int r = static_cast<int>(u - s * per_seq);
-        const int i = r / heads, head = r - i * heads;
-        const QuerySeq seq = query_seq(a, s, r == 0 && (threadIdx.x & 31) == 0);
-        if (i < seq.n) attend_row<D, POOL>(a, s, seq, i, head);
+        const int64_t at = u - s * per_seq;
+        const int h = static_cast<int>(at / per_head), r0 = static_cast<int>(at - static_cast<int64_t>(h) * per_head) * R;
+        const QuerySeq seq = query_seq(a, s, at == 0 && (threadIdx.x & 31) == 0);
+        if (r0 < seq.n * a.G) attend_rows<D, R>(a, s, seq, h, r0);
     }
 }
 
-template <kv_dtype POOL>
-int launch_rows_typed(const kv_pool* pool, const QueryArgs& a, bool pdl, cudaStream_t stream) {
-    const int64_t warps = static_cast<int64_t>(a.batch) * a.max_queries * a.H * a.G;
+template <int R>
+int launch_rows(const kv_pool* pool, const QueryArgs& a, bool pdl, cudaStream_t stream) {
+    const int64_t warps = static_cast<int64_t>(a.batch) * a.H * ((static_cast<int64_t>(a.max_queries) * a.G + R - 1) / R);
     const int64_t want = (warps + kRowWarps - 1) / kRowWarps, most = static_cast<int64_t>(pool->num_sms) * 64;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -38,8 +146,8 @@ int launch_rows_typed(const kv_pool* pool, const QueryArgs& a, bool pdl, cudaStr
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
-    const cudaError_t rc = pool->desc.head_dim == 128 ? cudaLaunchKernelEx(&cfg, query_rows_kernel<128, POOL>, a)
-                                                      : cudaLaunchKernelEx(&cfg, query_rows_kernel<64, POOL>, a);
+    const cudaError_t rc = pool->desc.head_dim == 128 ? cudaLaunchKernelEx(&cfg, query_rows_kernel<128, R>, a)
+                                                      : cudaLaunchKernelEx(&cfg, query_rows_kernel<64, R>, a);
     if (rc != cudaSuccess) {
         cudaGetLastError();
         return KV_ERR_CUDA;
@@ -47,16 +155,12 @@ int launch_rows_typed(const kv_pool* pool, const QueryArgs& a, bool pdl, cudaStr
     return KV_OK;
 }
 
-}  // namespace
-
 int launch_query_rows(const kv_pool* pool, const QueryArgs& a, bool pdl, cudaStream_t stream) {
-    switch (pool->desc.dtype) {
-        case KV_F32: return launch_rows_typed<KV_F32>(pool, a, pdl, stream);
-        case KV_F16: return launch_rows_typed<KV_F16>(pool, a, pdl, stream);
-        case KV_FP8_E4M3: return launch_rows_typed<KV_FP8_E4M3>(pool, a, pdl, stream);
-        default: return launch_rows_typed<KV_INT4>(pool, a, pdl, stream);
-    }
+    return static_cast<int64_t>(a.max_queries) * a.G > 1 ? launch_rows<2>(pool, a, pdl, stream)
+                                                         : launch_rows<1>(pool, a, pdl, stream);
 }
+
+}  // namespace
 
 int plan_query(const kv_pool* pool, const kv_query_args& x, QueryPlan* plan) {
     const kv_pool_desc& d = pool->desc;

@@ -91,7 +91,7 @@ __device__ __forceinline__ float capped(float s, float k2, float capl) {
 constexpr float kRaise = 8.f, kLift = 7.f;
 
 template <int D, kv_dtype POOL>
-constexpr int kRowBytes = POOL == KV_INT4 ? D / 2 + D / 16 : POOL == KV_FP8_E4M3 ? D : POOL == KV_F16 ? 2 * D : 4 * D;
+constexpr int kRowBytes = POOL == KV_INT4 ? D / 2 + D / 16 : POOL == KV_FP8_E4M3 ? D : 2 * D;
 
 // Elements [part * D/8, (part + 1) * D/8) of token `off` of a (block, head) tile, as float32 (FP8: codes).
 template <int D, kv_dtype POOL, bool IS_V>
@@ -112,13 +112,7 @@ __device__ __forceinline__ void load_eighth(const char* tile, int off, int part,
         }
     } else {
         const char* row = tile + (static_cast<int64_t>(off) * D + part * N) * (kRowBytes<D, POOL> / D);
-        if constexpr (POOL == KV_F32) {
-            #pragma unroll
-            for (int i = 0; i < N; i += 4) {
-                const float4 v = *reinterpret_cast<const float4*>(row + 4 * i);
-                x[i] = v.x; x[i + 1] = v.y; x[i + 2] = v.z; x[i + 3] = v.w;
-            }
-        } else if constexpr (POOL == KV_F16) {
+        if constexpr (POOL == KV_F16) {
             #pragma unroll
             for (int i = 0; i < N; i += 8) {
                 const uint4 v = *reinterpret_cast<const uint4*>(row + 2 * i);
@@ -150,16 +144,16 @@ __device__ __forceinline__ void load_eighth(const char* tile, int off, int part,
 // Eight lanes share a key, four keys go side by side with a softmax state each, joined at the end.
 template <int D, kv_dtype POOL>
 __device__ __noinline__ void attend_row(const QueryArgs& a, int s, QuerySeq seq, int i, int head) {
-    constexpr int N = D / 8, QS = POOL == KV_F32 ? 4 : 2;
+    constexpr int N = D / 8;
     const int lane = threadIdx.x & 31, part = lane & 7, which = lane >> 3;
     const int p = seq.ctx - seq.n + i;
     const int2 range = row_range(a, seq, i);
     float q[N], o[N];
     {
-        const char* row = a.q + static_cast<int64_t>(seq.first + i) * a.q_stride + (head * D + part * N) * QS;
+        const char* row = a.q + static_cast<int64_t>(seq.first + i) * a.q_stride + (head * D + part * N) * 2;
         #pragma unroll
         for (int e = 0; e < N; ++e) {
-            q[e] = QS == 4 ? reinterpret_cast<const float*>(row)[e] : __half2float(reinterpret_cast<const __half*>(row)[e]);
+            q[e] = __half2float(reinterpret_cast<const __half*>(row)[e]);
             o[e] = 0.f;
         }
     }
@@ -210,12 +204,9 @@ __device__ __noinline__ void attend_row(const QueryArgs& a, int s, QuerySeq seq,
     }
     if (which != 0) return;
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    char* row = a.out + static_cast<int64_t>(seq.first + i) * a.out_stride + (head * D + part * N) * QS;
+    char* row = a.out + static_cast<int64_t>(seq.first + i) * a.out_stride + (head * D + part * N) * 2;
     #pragma unroll
-    for (int e = 0; e < N; ++e) {
-        if constexpr (QS == 4) reinterpret_cast<float*>(row)[e] = o[e] * inv;
-        else reinterpret_cast<__half*>(row)[e] = __float2half_rn(o[e] * inv);
-    }
+    for (int e = 0; e < N; ++e) reinterpret_cast<__half*>(row)[e] = __float2half_rn(o[e] * inv);
 }
 
 #endif  // __CUDACC__
@@ -240,6 +231,5 @@ inline int64_t prompt_items(int batch, int heads, int group, int num_tokens, int
 int launch_query_prompt(const kv_pool* pool, int layer, const QueryArgs& a, bool pdl, cudaStream_t stream);
 size_t few_space(const kv_pool* pool, size_t* counters);       // workspace bytes, those of its counters (at its start)
 int launch_query_few(const kv_pool* pool, const QueryArgs& a, void* workspace, bool pdl, cudaStream_t stream);
-int launch_query_rows(const kv_pool* pool, const QueryArgs& a, bool pdl, cudaStream_t stream);
 
 }  // namespace kvp

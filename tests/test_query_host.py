@@ -42,7 +42,7 @@ BAD = [dict(layer=2), dict(layer=-1), dict(batch=-1), dict(batch=65537), dict(nu
        dict(q=None), dict(out=None), dict(query_start=None), dict(block_tables=None), dict(context_lens=None),
        dict(workspace=None), dict(max_blocks_per_seq=0), dict(q=A + 8), dict(out=2 * A + 2), dict(workspace=6 * A + 128),
        dict(ranges=7 * A + 4), dict(slopes=7 * A + 2), dict(q_stride=1023), dict(q_stride=1020), dict(q_stride=512),
-       dict(out_stride=0), dict(out_stride=1 << 28), dict(workspace_bytes=0)]
+       dict(out_stride=0), dict(out_stride=1 << 28), dict(workspace_bytes=0), dict(out=A)]
 
 
 @pytest.mark.parametrize("bad", BAD, ids=str)
