@@ -165,7 +165,7 @@ class PagedKVCache:
         if axes is None:
             if positions.numel() != n:
                 raise ValueError("positions must have one entry per token")
-        elif positions.dim() != 2 or positions.shape[0] != axes.num_axes or positions.shape[1] != n:
+        elif positions.shape != (axes.num_axes, n):
             raise ValueError("positions must be [axes, num_tokens]")
         if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
             raise ValueError("cos_sin must be float32 [positions, rot_dim]")
@@ -178,7 +178,7 @@ class PagedKVCache:
             hq, out_dt = shape[1], torch.float32 if self.dtype == "f32" else torch.float16
             if q_out is None:
                 with _alloc_on(stream):
-                    q_out = torch.empty(shape, dtype=out_dt, device=q.device)
+                    q_out = q.new_empty(shape, dtype=out_dt)
             elif q_out.shape != shape or q_out.dtype != out_dt:
                 raise ValueError(f"q_out must be {out_dt} of q's shape")
             (qp, qs), (op, os) = _rows(q, n, hq, d, "q", dev), _rows(q_out, n, hq, d, "q_out", dev)
