@@ -770,7 +770,8 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
         for (int r = max(0, ring - DEPTH); r < ring; ++r) mbar_wait_bounded(there(r % DEPTH), r / DEPTH & 1, a.err);
     } else if (warp == kItemWarp) {
         // ======== work items: what the rows see, and their queries, an item ahead of the others
-        int s32 = -32, before = 0, upto = 0, lane_items = 0, lane_upto = 0;    // the sequences walked now
+        int s32 = -32, before = 0, upto = 0, lane_items = 0, lane_upto = 0;    // the sequences walked now, one a lane
+        QuerySeq lane_seq{0, 0, 0};
         int index = blockIdx.x, claims = 0, asked = 0;         // (asked: items whose queries were asked for, in part at least)
         auto ask = [&]() {
             if (lane == 0) {
@@ -796,9 +797,9 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
             while (index >= 0 && index >= upto && s32 + 32 < a.batch) {
                 s32 += 32;
                 before = upto;
-                lane_items = 0;
-                if (s32 + lane < a.batch)
-                    lane_items = prompt_tiles(query_seq(a, s32 + lane, true).n, a.G) * a.H;
+                lane_seq = QuerySeq{0, 0, 0};
+                if (s32 + lane < a.batch) lane_seq = query_seq(a, s32 + lane, true);
+                lane_items = prompt_tiles(lane_seq.n, a.G) * a.H;
                 lane_upto = lane_items;
                 #pragma unroll
                 for (int o = 1; o < 32; o *= 2) {
@@ -819,8 +820,8 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                 const int tiles = __shfl_sync(0xffffffffu, lane_items, of) / a.H;
                 head = at % a.H;
                 token = (tiles - 1 - at / a.H) * 2 * per_tile;
-                seq = query_seq(a, s, false);
-                seq = QuerySeq{uniform(seq.first), uniform(seq.n), uniform(seq.ctx)};
+                seq = QuerySeq{__shfl_sync(0xffffffffu, lane_seq.first, of), __shfl_sync(0xffffffffu, lane_seq.n, of),
+                               __shfl_sync(0xffffffffu, lane_seq.ctx, of)};
             }
             Item x{index < 0 ? -1 : s, head, token, seq.first, seq.n, seq.ctx, {1 << 30, 1 << 30}, {0, 0}, 1.f};
             if (index >= 0) {
