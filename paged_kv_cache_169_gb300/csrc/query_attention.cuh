@@ -22,6 +22,9 @@ struct QueryArgs {
     int num_tokens, max_queries, max_blocks, batch, ctx_limit, window;
     int H, G, B, log_b, num_blocks;    // K/V heads, query heads per K/V head, block size and its logarithm
     float scale, cap;                  // cap 0: none
+    int splits;                        // parts of an item's keys in the tensor-core kernel; above 1, joined afterwards:
+    float2* part_ml;                   // [part][token][query head]: base in log2 units, sum of weights
+    float* part_o;                     // and the weighted sums, [D]
     int* err;
 };
 

@@ -15,6 +15,9 @@
 // take turns.  Warps 0-15 softmax, 8 to a row tile, 16 rows each; 16 matrix products; 17 keys and values (TMA for float16
 // pools, bulk copies and four widening warps for the others); 18 items and queries, an item ahead.
 //
+// Few items over long contexts are cut into parts of the keys (QueryArgs::splits): their sums go to the workspace in
+// float32 and query_join_kernel joins them, in order.
+//
 // Measured (us; D = 128 but for the last): 4 x 2048 tokens of 40 heads 178 (960 TFLOP/s), 2 x 8192 of them 1003 (1370);
 // 2 x 4096 tokens, 64 / 8 heads, capped 671; 512 rows after 16k tokens in FP8, 4 x, 64 / 8 heads 1210 (883); packed
 // documents with a bias, 4-bit, 240; ragged prompts, D = 64, prefixes seen both ways 268 (543).  What it waits for: per key
@@ -171,6 +174,7 @@ struct Item {
     int s, head, token;                // its first token
     int first, n, ctx;                 // the sequence (QuerySeq)
     int lo[2], hi[2];                  // positions that some row of a row tile sees
+    int z, from, to;                   // the part of the keys, and its positions
     float vref;                        // FP8: the largest value scale
 };
 struct PromptMisc {
@@ -338,7 +342,9 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
             #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 const int token = x.token + rt * per_tile + (row_of(r) >> log_g);
-                next.sees[r] = token < x.n ? row_range(a, QuerySeq{x.first, x.n, x.ctx}, token) : make_int2(0, 0);
+                int2 sees = token < x.n ? row_range(a, QuerySeq{x.first, x.n, x.ctx}, token) : make_int2(0, 0);
+                sees = make_int2(max(sees.x, x.from), min(sees.y, x.to));
+                next.sees[r] = sees.x < sees.y ? sees : make_int2(0, 0);
                 next.slope[r] = BIAS ? a.slopes[x.head * a.G + (row_of(r) & (a.G - 1))] * kLog2e : 0.f;
             }
             next.pos0 = x.ctx - x.n + x.token + rt * per_tile;
@@ -491,8 +497,35 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
             some_item = fetch();
             if (!fine || (i > i0 && !wait(o_there(rt), i - 1))) break;
             tc_fence_after();
-            // the result, 64 elements at a time through shared memory, so that a store writes whole lines
             const bool any = i > i0;
+            if (a.splits > 1) {                                // a part of the rows' keys: to the workspace
+                #pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int token = it.token + rt * per_tile + (row_of(r) >> log_g);
+                    const int64_t at = (static_cast<int64_t>(it.z) * a.num_tokens + it.first + token) * (a.H * a.G) + it.head * a.G +
+                                       (row_of(r) & (a.G - 1));
+                    if (token < it.n && quad == 0) a.part_ml[at] = any ? make_float2(m[r], l[r]) : make_float2(-CUDART_INF_F, 0.f);
+                }
+                #pragma unroll 1
+                for (int k = 0; any && k < D; k += 16) {
+                    uint32_t o[8];
+                    tmem_load_16x16(ot + k, o);
+                    #pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const int token = it.token + rt * per_tile + (row_of(r) >> log_g);
+                        const int64_t at = (static_cast<int64_t>(it.z) * a.num_tokens + it.first + token) * (a.H * a.G) + it.head * a.G +
+                                           (row_of(r) & (a.G - 1));
+                        if (token >= it.n) continue;
+                        #pragma unroll
+                        for (int g = 0; g < 2; ++g)
+                            *reinterpret_cast<float2*>(a.part_o + at * D + k + 8 * g + 2 * quad) =
+                                make_float2(__uint_as_float(o[4 * g + 2 * r]) * it.vref, __uint_as_float(o[4 * g + 2 * r + 1]) * it.vref);
+                    }
+                }
+                tc_fence_before();
+                continue;
+            }
+            // the result, 64 elements at a time through shared memory, so that a store writes whole lines
             const float inv[2] = {l[0] == 0.f ? 0.f : it.vref / l[0], l[1] == 0.f ? 0.f : it.vref / l[1]};
             char* const to = a.out + static_cast<int64_t>(it.first + it.token + rt * per_tile) * a.out_stride +
                              it.head * a.G * (D * 2) + (lane & 7) * 16;
@@ -792,14 +825,14 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
         while (true) {
             // The sequences' items one after the other; of a sequence the later row tiles, which see more keys, first,
             // each for every head.  Indices only grow, so the sequences are walked 32 at a time, a lane each.
-            int s = 0, head = 0, token = 0;
+            int s = 0, head = 0, token = 0, z = 0;
             QuerySeq seq{0, 0, 0};
             while (index >= 0 && index >= upto && s32 + 32 < a.batch) {
                 s32 += 32;
                 before = upto;
                 lane_seq = QuerySeq{0, 0, 0};
                 if (s32 + lane < a.batch) lane_seq = query_seq(a, s32 + lane, true);
-                lane_items = prompt_tiles(lane_seq.n, a.G) * a.H;
+                lane_items = prompt_tiles(lane_seq.n, a.G) * a.H * a.splits;
                 lane_upto = lane_items;
                 #pragma unroll
                 for (int o = 1; o < 32; o *= 2) {
@@ -816,14 +849,15 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
             if (index >= 0) {
                 const int of = __ffs(__ballot_sync(0xffffffffu, before + lane_upto > index)) - 1;
                 s = s32 + of;
-                const int at = index - before - __shfl_sync(0xffffffffu, lane_upto - lane_items, of);
-                const int tiles = __shfl_sync(0xffffffffu, lane_items, of) / a.H;
+                const int nth = index - before - __shfl_sync(0xffffffffu, lane_upto - lane_items, of), at = nth / a.splits;
+                const int tiles = __shfl_sync(0xffffffffu, lane_items, of) / (a.H * a.splits);
+                z = nth - at * a.splits;
                 head = at % a.H;
                 token = (tiles - 1 - at / a.H) * 2 * per_tile;
                 seq = QuerySeq{__shfl_sync(0xffffffffu, lane_seq.first, of), __shfl_sync(0xffffffffu, lane_seq.n, of),
                                __shfl_sync(0xffffffffu, lane_seq.ctx, of)};
             }
-            Item x{index < 0 ? -1 : s, head, token, seq.first, seq.n, seq.ctx, {1 << 30, 1 << 30}, {0, 0}, 1.f};
+            Item x{index < 0 ? -1 : s, head, token, seq.first, seq.n, seq.ctx, {1 << 30, 1 << 30}, {0, 0}, z, 0, 1 << 30, 1.f};
             if (index >= 0) {
                 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
@@ -837,6 +871,20 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                     }
                     x.lo[t] = __reduce_min_sync(0xffffffffu, x.lo[t]);
                     x.hi[t] = __reduce_max_sync(0xffffffffu, x.hi[t]);
+                }
+                if (a.splits > 1 && max(x.hi[0], x.hi[1]) > 0) {               // an equal part of the item's key tiles
+                    const int base = min(x.lo[0], x.lo[1]) & -a.B, tiles = (max(x.hi[0], x.hi[1]) - base + kTile - 1) / kTile;
+                    x.from = base + tiles * z / a.splits * kTile;
+                    x.to = base + tiles * (z + 1) / a.splits * kTile;
+                    #pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        x.lo[t] = max(x.lo[t], x.from);
+                        x.hi[t] = min(x.hi[t], x.to);
+                        if (x.lo[t] >= x.hi[t]) {
+                            x.lo[t] = 1 << 30;
+                            x.hi[t] = 0;
+                        }
+                    }
                 }
                 if constexpr (POOL == KV_FP8_E4M3) {
                     // value scales enter the weights relative to the largest one, which multiplies the result
@@ -899,6 +947,53 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
     }
 }
 
+// The parts of a row's keys, joined: a warp per (row, query head).
+template <int D, kv_dtype POOL>
+__global__ void __launch_bounds__(256) query_join_kernel(const __grid_constant__ QueryArgs a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    constexpr int N = D / 32;
+    const int heads = a.H * a.G, lane = threadIdx.x & 31;
+    const int64_t per_seq = static_cast<int64_t>(a.max_queries) * heads, all = per_seq * a.batch;
+    #pragma unroll 1
+    for (int64_t u = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); u < all; u += static_cast<int64_t>(gridDim.x) * 8) {
+        const int s = static_cast<int>(u / per_seq), r = static_cast<int>(u - s * per_seq), i = r / heads, head = r - i * heads;
+        const QuerySeq seq = query_seq(a, s, false);
+        if (i >= seq.n) continue;
+        const int64_t row = static_cast<int64_t>(seq.first + i) * heads + head, step = static_cast<int64_t>(a.num_tokens) * heads;
+        const float2 mine = lane < a.splits ? __ldcg(a.part_ml + lane * step + row) : make_float2(-CUDART_INF_F, 0.f);
+        float top = mine.y != 0.f ? mine.x : -CUDART_INF_F;
+        #pragma unroll
+        for (int k = 1; k < 32; k *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+        const float factor = mine.y != 0.f ? ex2_approx(mine.x - top) : 0.f;
+        float l = 0.f, o[N] = {};
+        #pragma unroll 4
+        for (int z = 0; z < a.splits; ++z) {                   // (in order: the same bits every time)
+            const float f = __shfl_sync(0xffffffffu, factor, z), lz = __shfl_sync(0xffffffffu, mine.y, z);
+            if (lz == 0.f) continue;                           // (nothing was written)
+            l = fmaf(lz, f, l);
+            const float* const from = a.part_o + (z * step + row) * D + lane * N;
+            #pragma unroll
+            for (int e = 0; e < N; e += 2) {
+                const float2 v = __ldcg(reinterpret_cast<const float2*>(from + e));
+                o[e] = fmaf(v.x, f, o[e]);
+                o[e + 1] = fmaf(v.y, f, o[e + 1]);
+            }
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        bool finite = true;
+        char* const to = a.out + static_cast<int64_t>(seq.first + i) * a.out_stride + (head * D + lane * N) * 2;
+        #pragma unroll
+        for (int e = 0; e < N; e += 2) {
+            const float2 v = make_float2(o[e] * inv, o[e + 1] * inv);
+            finite &= fabsf(v.x) < CUDART_INF_F && fabsf(v.y) < CUDART_INF_F;
+            *reinterpret_cast<__half2*>(to + e * 2) = __floats2half2_rn(v.x, v.y);
+        }
+        // (as in the kernel: a row that came out not finite, from the definition)
+        if (__any_sync(0xffffffffu, !finite)) attend_row<D, POOL>(a, s, seq, i, head);
+    }
+}
+
 template <typename C, bool BIAS, bool CAP>
 int launch_prompt_typed(const kv_pool* pool, const PromptArgs& p, bool pdl, cudaStream_t stream) {
     static unsigned long long attr_done = 0;               // the shared-memory opt-in is a per-device attribute
@@ -922,6 +1017,17 @@ int launch_prompt_typed(const kv_pool* pool, const PromptArgs& p, bool pdl, cuda
     if (cudaLaunchKernelEx(&cfg, query_prompt_kernel<C::D, C::POOL, BIAS, CAP>, p) != cudaSuccess) {
         cudaGetLastError();
         return KV_ERR_CUDA;
+    }
+    if (p.a.splits > 1) {
+        const int64_t rows = static_cast<int64_t>(p.a.batch) * p.a.max_queries * p.a.H * p.a.G, most = static_cast<int64_t>(pool->num_sms) * 8;
+        cfg.gridDim = dim3(static_cast<unsigned>((rows + 7) / 8 < most ? (rows + 7) / 8 : most));
+        cfg.blockDim = dim3(256);
+        cfg.dynamicSmemBytes = 0;
+        cfg.numAttrs = 1;                                      // (it waits for the kernel above itself)
+        if (cudaLaunchKernelEx(&cfg, query_join_kernel<C::D, C::POOL>, p.a) != cudaSuccess) {
+            cudaGetLastError();
+            return KV_ERR_CUDA;
+        }
     }
     return KV_OK;
 }

@@ -7,7 +7,7 @@ namespace kvp {
 int launch_query_prompt(const kv_pool* pool, int layer, const QueryArgs& a, bool pdl, cudaStream_t stream) {
     PromptArgs p{};
     p.a = a;
-    p.items = static_cast<int>(prompt_items(a.batch, a.H, a.G, a.num_tokens, a.max_queries));
+    p.items = static_cast<int>(prompt_items(a.batch, a.H, a.G, a.num_tokens, a.max_queries) * a.splits);
     // queries: rows of a token are D-element heads; a box is 64 elements of the G heads of 128 / G tokens
     const kv_pool_desc& d = pool->desc;
     const TensorMapEncode encode = reinterpret_cast<TensorMapEncode>(pool->encode);

@@ -213,3 +213,39 @@ def test_two_calls_at_once(new):
     for o in outs:
         assert np.array_equal(o.cpu().numpy(), want)
     b.cache.close()
+
+
+@pytest.mark.parametrize("pool", ["f16", "fp8", "int4"])
+@pytest.mark.parametrize("d,group", [(128, 8), (64, 1)])
+def test_contexts_cut_into_parts(pool, d, group):
+    """Few rows over long contexts: parts of the keys, joined.  Masks that leave parts, rows and row tiles empty, a
+    window within one part, a short sequence beside a long one, a workspace kept and one that is given zeroed."""
+    new, lens = [40, 300, 20, 1], [3000, 1700, 21, 900]
+    b = G.Batch(pool, d, 1, 16, lens, seed=d + group)
+    want, q, _ = G.run(b, new, group)
+    ws = b.cache.query_workspace(4, group, 300, 3000, num_tokens=sum(new))
+    assert ws.numel() > sum(new) * group * d * 8
+    got, _, _ = G.run(b, new, group, workspace=ws, flags=abi.KV_DECODE_WORKSPACE_ZEROED | abi.KV_DECODE_PDL, check=False, q_in=q)
+    assert np.array_equal(got, want)
+    G.run(b, new, group, cap=20.0, qmul=3.0, gap=4)
+    G.run(b, new, group, slopes=True)
+    G.run(b, new, group, window=100)
+    p = np.concatenate([np.arange(c - n, c) for n, c in zip(new, lens)])
+    r = np.stack((p // 700 * 700, p + 1), 1)
+    r[3::5] = (600, 610)
+    r[4::5] = (9, 9)
+    r[40:168] = (0, 0)                                         # a whole row tile with one head, most of one with eight
+    G.run(b, new, group, ranges=r)
+    G.run(b, new, group, ranges=r, slopes=True)
+    # what one row may not see: NaN within a part that others of its tile see
+    blk = b.tab[0][2990 // 16]
+    if pool == "f16":
+        b.k[blk, :, 2990 % 16], b.v[blk, :, 2990 % 16] = np.nan, np.nan
+        b.upload()
+        got, q, _ = G.run(b, new, group, check=False)
+        k, v = b.values(0, "k")[:2990], b.values(0, "v")[:2990]
+        assert np.isnan(got[30:40]).all()
+        want = OQ.query_attention(q[:30], k, v, 1 / math.sqrt(d))
+        tol = G.tolerance(pool, q[:30].astype(np.float64), k, v, 40.0, 1 / math.sqrt(d), 0.0, want)
+        G.close(got[:30], want, tol, "beside NaN")
+    b.cache.close()
