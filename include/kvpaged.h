@@ -545,7 +545,8 @@ KV_API int paged_decode_attention_ex(kv_pool* pool, const kv_decode_args* args);
  *   num_tokens     rows of q and out, 0 .. 2^24.
  *   max_queries    host upper bound of a sequence's rows, 0 .. num_tokens.  A sequence with more, or
  *                  whose rows lie outside [0, num_tokens) or end before they begin, sets
- *                  KV_DEVERR_QUERY and is left out (no row of it is written).
+ *                  KV_DEVERR_QUERY and is left out (no row of it is written; rows that two other
+ *                  sequences then name may hold anything).
  *   block_tables, max_blocks_per_seq, context_lens, batch  as paged_decode_attention.  Lengths
  *                  below 0 or above min(max_blocks_per_seq*block_size, max_context) are clamped
  *                  and set KV_DEVERR_CONTEXT; so does c < n (rows before position 0 see nothing
