@@ -18,9 +18,9 @@
 // Few items over long contexts are cut into parts of the keys (QueryArgs::splits): their sums go to the workspace in
 // float32 and query_join_kernel joins them, in order.
 //
-// Measured (us; D = 128 but for the last): 4 x 2048 tokens of 40 heads 178 (960 TFLOP/s), 2 x 8192 of them 1003 (1370);
-// 2 x 4096 tokens, 64 / 8 heads, capped 671; 512 rows after 16k tokens in FP8, 4 x, 64 / 8 heads 1210 (883); packed
-// documents with a bias, 4-bit, 240; ragged prompts, D = 64, prefixes seen both ways 268 (543).  What it waits for: per key
+// Measured (us; D = 128 but for the last): 4 x 2048 tokens of 40 heads 180 (955 TFLOP/s), 2 x 8192 of them 1003 (1370);
+// 2 x 4096 tokens, 64 / 8 heads, capped 674; 512 rows after 16k tokens in FP8, 4 x, 64 / 8 heads 1207 (884); packed
+// documents with a bias, 4-bit, 249; ragged prompts, D = 64, prefixes seen both ways 264 (551).  What it waits for: per key
 // tile 1660 cycles of softmax and 1660 of products and barrier round trips one behind the other; an item's start and end
 // 7000 cycles.  Before: 8 softmax warps with 64-key steps 187, 768, 1540, 313, 267; store warps for the result and 128-key
 // steps 211, 797, 1690, 284, 260; both row tiles' products issued as they came (the softmaxes ran at the same time, then
