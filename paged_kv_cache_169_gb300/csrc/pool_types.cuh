@@ -52,7 +52,9 @@ struct QueryPlan {
     enum Kind { ROWS, FEW, PROMPT } kind;
     size_t ws_bytes;         // workspace bytes
     size_t counter_bytes;    // of them, counters at its start, zero between calls
-    int splits;              // PROMPT: parts of an item's keys
+    int splits;              // PROMPT: parts of an item's keys, and their layout (QueryParts)
+    int64_t part_rows;
+    bool part_by_sequence;
 };
 int plan_query(const kv_pool* pool, const kv_query_args& args, QueryPlan* plan);
 int launch_query(const kv_pool* pool, const kv_query_args& args, const QueryPlan& plan);

@@ -179,24 +179,18 @@ int plan_query(const kv_pool* pool, const kv_query_args& x, QueryPlan* plan) {
     plan->ws_bytes = 256;
     plan->counter_bytes = 0;
     plan->splits = 1;
+    plan->part_rows = 0;
+    plan->part_by_sequence = false;
     size_t counters;
     const size_t few_bytes = few_space(pool, &counters);
     if (plan->kind == QueryPlan::PROMPT) {
-        // Few items over long contexts leave most SMs idle: then an item's keys are cut into parts of at least 512, as
-        // many as the SMs take, and joined by a second launch.  (83 rows of 16 / 2 heads of 64 after 8k tokens, FP8, two
-        // sequences: 178 us whole, 32 in parts; 200 rows of 5 heads after 4.4k, float16: 69 and 21.  The join and the
-        // parts' own beginnings are about 10 us, so that shorter contexts stay whole.)
-        const int64_t items = prompt_items(x.batch, d.num_heads, g, x.num_tokens, x.max_queries);
-        const int64_t reach = static_cast<int64_t>(x.window) + x.max_queries;
-        const int64_t keys = x.window > 0 && reach < x.max_context ? reach : x.max_context;
-        const int64_t most = keys / 512 < 32 ? keys / 512 : 32, parts = items > 0 ? pool->num_sms / items : 0;
-        if (most >= 2) {
-            if (parts >= 2) plan->splits = static_cast<int>(parts < most ? parts : most);
-            // What any call of no more sequences, rows and positions needs: a call has num_tokens G H / 256 items at least,
-            // so parts times rows are 256 per SM at most.  (Behind the few-row kernel's counters, which stay zero.)
-            const int64_t all = static_cast<int64_t>(pool->num_sms) * 256, rows = most * x.num_tokens * x.num_q_heads;
-            plan->ws_bytes = counters + static_cast<size_t>(rows < all ? rows : all) * (d.head_dim * 4 + 8);
-        }
+        const QueryParts parts = query_parts(pool->num_sms, x.batch, d.num_heads, g, x.num_tokens, x.max_queries, x.max_context,
+                                             x.window);
+        plan->splits = parts.splits;
+        plan->part_rows = parts.rows;
+        plan->part_by_sequence = parts.by_sequence;
+        // (behind the few-row kernel's counters, which stay zero)
+        if (parts.space > 0) plan->ws_bytes = counters + static_cast<size_t>(parts.space) * (d.head_dim * 4 + 8);
     }
     if (plan->kind == QueryPlan::FEW) {
         const int64_t seqs = x.batch < kFewSeqs ? x.batch : kFewSeqs;
@@ -242,7 +236,9 @@ int launch_query(const kv_pool* pool, const kv_query_args& x, const QueryPlan& p
     size_t counters;
     few_space(pool, &counters);
     a.part_ml = reinterpret_cast<float2*>(static_cast<char*>(x.workspace) + counters);
-    a.part_o = reinterpret_cast<float*>(a.part_ml + static_cast<int64_t>(plan.splits) * x.num_tokens * x.num_q_heads);
+    a.part_o = reinterpret_cast<float*>(a.part_ml + plan.splits * plan.part_rows * x.num_q_heads);
+    a.part_rows = plan.part_rows;
+    a.part_by_sequence = plan.part_by_sequence;
     a.err = pool->d_err;
     const bool pdl = (x.flags & KV_DECODE_PDL) != 0;
     const cudaStream_t stream = static_cast<cudaStream_t>(x.stream);

@@ -7,6 +7,7 @@
 
 #include "int4.cuh"
 #include "pool_types.cuh"
+#include "query_parts.h"
 
 namespace kvp {
 
@@ -23,8 +24,10 @@ struct QueryArgs {
     int H, G, B, log_b, num_blocks;    // K/V heads, query heads per K/V head, block size and its logarithm
     float scale, cap;                  // cap 0: none
     int splits;                        // parts of an item's keys in the tensor-core kernel; above 1, joined afterwards:
-    float2* part_ml;                   // [part][token][query head]: base in log2 units, sum of weights
+    float2* part_ml;                   // [part][row][query head] (QueryParts): base in log2 units, sum of weights
     float* part_o;                     // and the weighted sums, [D]
+    int64_t part_rows;
+    bool part_by_sequence;
     int* err;
 };
 
@@ -217,18 +220,6 @@ __device__ __noinline__ void attend_row(const QueryArgs& a, int s, QuerySeq seq,
 // Rows of a unit (sequence, K/V head) that one 16-row matrix product holds: the few-row kernel's.
 constexpr int kFewRows = 16;
 constexpr int kFewSeqs = 1024;         // sequences per launch of it
-
-// Pairs of 128-row tiles of a sequence's K/V head in the tensor-core kernel.
-__host__ __device__ inline int prompt_tiles(int queries, int group) {
-    return static_cast<int>((static_cast<int64_t>(queries) * group + 255) / 256);
-}
-// Bound of a call's (pair, K/V head): each sequence has at most max_queries rows, all of them num_tokens, and one pair
-// of each sequence is not full.
-inline int64_t prompt_items(int batch, int heads, int group, int num_tokens, int max_queries) {
-    const int64_t each = static_cast<int64_t>(batch) * prompt_tiles(max_queries, group);
-    const int64_t all = static_cast<int64_t>(num_tokens) * group / 256 + batch;
-    return (each < all ? each : all) * heads;
-}
 
 // The kernels' launchers.
 int launch_query_prompt(const kv_pool* pool, int layer, const QueryArgs& a, bool pdl, cudaStream_t stream);

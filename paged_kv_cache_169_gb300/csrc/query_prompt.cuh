@@ -499,11 +499,14 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
             tc_fence_after();
             const bool any = i > i0;
             if (a.splits > 1) {                                // a part of the rows' keys: to the workspace
+                auto place = [&](int r, int token) {
+                    const int64_t row = it.z * a.part_rows + part_row(a.part_by_sequence, a.max_queries, it.s, it.first, token);
+                    return row * (a.H * a.G) + it.head * a.G + (row_of(r) & (a.G - 1));
+                };
                 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const int token = it.token + rt * per_tile + (row_of(r) >> log_g);
-                    const int64_t at = (static_cast<int64_t>(it.z) * a.num_tokens + it.first + token) * (a.H * a.G) + it.head * a.G +
-                                       (row_of(r) & (a.G - 1));
+                    const int64_t at = place(r, token);
                     if (token < it.n && quad == 0) a.part_ml[at] = any ? make_float2(m[r], l[r]) : make_float2(-CUDART_INF_F, 0.f);
                 }
                 #pragma unroll 1
@@ -513,9 +516,8 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                     #pragma unroll
                     for (int r = 0; r < 2; ++r) {
                         const int token = it.token + rt * per_tile + (row_of(r) >> log_g);
-                        const int64_t at = (static_cast<int64_t>(it.z) * a.num_tokens + it.first + token) * (a.H * a.G) + it.head * a.G +
-                                           (row_of(r) & (a.G - 1));
                         if (token >= it.n) continue;
+                        const int64_t at = place(r, token);
                         #pragma unroll
                         for (int g = 0; g < 2; ++g)
                             *reinterpret_cast<float2*>(a.part_o + at * D + k + 8 * g + 2 * quad) =
@@ -960,7 +962,7 @@ __global__ void __launch_bounds__(256) query_join_kernel(const __grid_constant__
         const int s = static_cast<int>(u / per_seq), r = static_cast<int>(u - s * per_seq), i = r / heads, head = r - i * heads;
         const QuerySeq seq = query_seq(a, s, false);
         if (i >= seq.n) continue;
-        const int64_t row = static_cast<int64_t>(seq.first + i) * heads + head, step = static_cast<int64_t>(a.num_tokens) * heads;
+        const int64_t row = part_row(a.part_by_sequence, a.max_queries, s, seq.first, i) * heads + head, step = a.part_rows * heads;
         const float2 mine = lane < a.splits ? __ldcg(a.part_ml + lane * step + row) : make_float2(-CUDART_INF_F, 0.f);
         float top = mine.y != 0.f ? mine.x : -CUDART_INF_F;
         #pragma unroll
