@@ -139,7 +139,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) query_few_kernel(const __grid_
     __shared__ int s_part[kWarps];                             // bytes to a warp's part in shared memory, -1: none
     __shared__ int s_warp_sum[kWarps];
     __shared__ int s_go[2];
-    __shared__ unsigned s_odd;                                 // rows that came out not finite
+    // rows that came out not finite (two words: while a warp still looks at the first of the two units that a CTA joins
+    // at the end, another marks rows of the second)
+    __shared__ unsigned s_odd[2];
     const QueryArgs& a = x.a;
     int* const s_lo = reinterpret_cast<int*>(smem + C::SEQ_OFF);               // what the sequence's rows see
     int* const s_hi = s_lo + kFewSeqs;
@@ -180,7 +182,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) query_few_kernel(const __grid_
             if (lane >= o) upto += v;
         }
         if (lane == 31) s_warp_sum[warp] = upto;
-        if (tid == 0) s_odd = 0;
+        if (tid < 2) s_odd[tid] = 0;
         __syncthreads();
         int before = upto - sum;
         for (int w = 0; w < warp; ++w) before += s_warp_sum[w];
@@ -693,14 +695,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1) query_few_kernel(const __grid_
                 sum.w = fmaf(p.w, f, sum.w);
             }
             if (whole) {
-                if (!store_quarter<D>(a, seq, unit.h, row, c4, sum, ll)) atomicOr(&s_odd, 1u << row);
+                if (!store_quarter<D>(a, seq, unit.h, row, c4, sum, ll)) atomicOr(&s_odd[0], 1u << row);
             } else {
                 if (c4 == 0) x.part_ml[space * kFewRows + row] = make_float2(mm, ll);
                 reinterpret_cast<float4*>(x.part_o)[(space * kFewRows + row) * (D / 4) + c4] = sum;
             }
         }
         __syncthreads();
-        if (whole && s_odd) redo_rows<D, POOL>(a, unit.s, seq, unit.h, &s_odd);
+        if (whole && s_odd[0]) redo_rows<D, POOL>(a, unit.s, seq, unit.h, &s_odd[0]);
         if (held >= 0) ask();                                  // into the held stage
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -767,7 +769,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) query_few_kernel(const __grid_
                     sum.w = fmaf(p[v].w, f, sum.w);
                 }
                 if (level == 1) {
-                    if (!store_quarter<D>(a, seq, cross[i].h, row, c4, sum, ll)) atomicOr(&s_odd, 1u << row);
+                    if (!store_quarter<D>(a, seq, cross[i].h, row, c4, sum, ll)) atomicOr(&s_odd[i], 1u << row);
                 } else {
                     // (the group's first place: each thread replaces what it alone has read, but for (m, l))
                     const int at_row = space_of(i, b0) * kFewRows + row;
@@ -777,7 +779,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) query_few_kernel(const __grid_
             }
             __syncthreads();
             if (level == 0 && tid < rows) x.part_ml[space_of(i, b0) * kFewRows + tid] = s_ml[i * kFewRows + tid];
-            if (level == 1 && s_odd) redo_rows<D, POOL>(a, cross[i].s, seq, cross[i].h, &s_odd);
+            if (level == 1 && s_odd[i]) redo_rows<D, POOL>(a, cross[i].s, seq, cross[i].h, &s_odd[i]);
         }
     }
 }

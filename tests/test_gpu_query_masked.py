@@ -1,0 +1,60 @@
+"""GPU: paged_query_attention where what some rows do not see is not finite, in units of work that several CTAs share: a row
+that came out not finite is worked out again, by the CTA that joins the unit's parts, often two units one after the other.
+Oracle and tolerance: test_gpu_query's."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import test_gpu_query as G
+from oracle import query as OQ
+from paged_kv_cache_169_gb300 import abi
+
+pytestmark = pytest.mark.gpu
+
+
+def up(x, dtype=np.int32):
+    return torch.from_numpy(np.ascontiguousarray(np.asarray(x, dtype=dtype))).cuda()
+
+
+@pytest.mark.parametrize("pool", ["f16", "fp8", "int4"])
+@pytest.mark.parametrize("seqs,H,c", [(37, 4, 700), (19, 8, 1200), (50, 2, 500), (3, 1, 6000)])
+def test_units_of_several_ctas(pool, seqs, H, c):
+    """Two rows a sequence; the last token's key and value are NaN, which the last row alone sees: it is NaN, the one
+    before it is right, in every unit and every time."""
+    d, B, scale = 64, 16, 0.125
+    lens = [c + 16 * (s % 7) + s for s in range(seqs)]
+    b = G.Batch(pool, d, H, B, lens, seed=seqs)
+    blk, off = np.array([b.tab[s][(n - 1) // B] for s, n in enumerate(lens)]), np.array([(n - 1) % B for n in lens])
+    for i, o in zip(blk, off):
+        if pool == "int4":
+            t = o % 8
+            b.k[i, :, o // 8, 4 * d + t * 4:4 * d + t * 4 + 4] = G.O4.NAN_BYTE
+            b.v[i, :, o // 8, 4 * d + t::8] = G.O4.NAN_BYTE
+        else:
+            bad = 0x7F if pool == "fp8" else np.nan
+            b.k[i, :, o], b.v[i, :, o] = bad, bad
+    b.upload()
+    q = b.rng.standard_normal((2 * seqs, H, d)).astype(np.float16)
+    want, tol = [], []
+    for s, n in enumerate(lens):
+        k, v = b.values(s, "k")[:n - 1], b.values(s, "v")[:n - 1]
+        want.append(OQ.query_attention(q[2 * s:2 * s + 1], k, v, scale))
+        t_max = float(np.max(np.linalg.norm(q[2 * s].astype(np.float64), axis=-1)) * np.max(np.linalg.norm(k, axis=-1))) * scale
+        tol.append(G.tolerance(pool, q[2 * s:2 * s + 1].astype(np.float64), k, v, t_max, scale, 0.0, want[-1]))
+    want, tol = np.concatenate(want), np.concatenate(tol)
+    tq, st, tab, ln = torch.from_numpy(q).cuda(), up(np.arange(0, 2 * seqs + 1, 2)), up(b.tab), up(lens)
+    ws = b.cache.query_workspace(seqs, H, 2, max(lens))
+    outs = [torch.zeros_like(tq) for _ in range(30)]
+    for out in outs:
+        b.cache.query_attention(0, tq, st, tab, ln, 2, max(lens), scale, out=out, workspace=ws,
+                                flags=abi.KV_DECODE_WORKSPACE_ZEROED | abi.KV_DECODE_PDL)
+    assert b.cache.device_error() == 0
+    for out in outs:
+        got = out.cpu().numpy()
+        assert np.isnan(got[1::2]).all()
+        G.close(got[0::2], want, tol, pool)
+        assert np.array_equal(got[0::2], outs[0].cpu().numpy()[0::2])
+    b.cache.close()
