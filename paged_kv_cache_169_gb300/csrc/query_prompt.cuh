@@ -991,8 +991,11 @@ __global__ void __launch_bounds__(256) query_join_kernel(const __grid_constant__
             finite &= fabsf(v.x) < CUDART_INF_F && fabsf(v.y) < CUDART_INF_F;
             *reinterpret_cast<__half2*>(to + e * 2) = __floats2half2_rn(v.x, v.y);
         }
-        // (as in the kernel: a row that came out not finite, from the definition)
-        if (__any_sync(0xffffffffu, !finite)) attend_row<D, POOL>(a, s, seq, i, head);
+        // (as in the kernel: a row that came out not finite, from the definition, other lanes' stores over these)
+        if (__any_sync(0xffffffffu, !finite)) {
+            __syncwarp();
+            attend_row<D, POOL>(a, s, seq, i, head);
+        }
     }
 }
 

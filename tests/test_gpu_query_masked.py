@@ -58,3 +58,37 @@ def test_units_of_several_ctas(pool, seqs, H, c):
         G.close(got[0::2], want, tol, pool)
         assert np.array_equal(got[0::2], outs[0].cpu().numpy()[0::2])
     b.cache.close()
+
+
+@pytest.mark.parametrize("pool", ["f16", "fp8", "int4"])
+@pytest.mark.parametrize("d,group", [(128, 8), (64, 1)])
+def test_rows_of_joined_parts(pool, d, group):
+    """Keys cut into parts: NaN at positions that only the last rows see, in the last part and before it.  Every row that
+    does not see them is right where the join works it out again, the same bits every time."""
+    n, c, B, scale = 60, 3000, 16, 1 / math.sqrt(d)
+    b = G.Batch(pool, d, 1, B, [c], seed=d)
+    for p in (c - 1, c - 20):
+        i, o = b.tab[0][p // B], p % B
+        if pool == "int4":
+            b.k[i, :, o // 8, 4 * d + o % 8 * (d // 16):4 * d + (o % 8 + 1) * (d // 16)] = G.O4.NAN_BYTE
+            b.v[i, :, o // 8, 4 * d + o % 8::8] = G.O4.NAN_BYTE
+        else:
+            bad = 0x7F if pool == "fp8" else np.nan
+            b.k[i, :, o], b.v[i, :, o] = bad, bad
+    b.upload()
+    q = b.rng.standard_normal((n, group, d)).astype(np.float16)
+    k, v = b.values(0, "k"), b.values(0, "v")
+    m = n - 20                                                 # rows that see neither
+    args = (up([0, n]), up(b.tab), up([c]), n, c, scale)
+    first = None
+    for _ in range(10):
+        got = b.cache.query_attention(0, torch.from_numpy(q).cuda(), *args).cpu().numpy()
+        assert b.cache.device_error() == 0
+        assert np.isnan(got[m:]).all()
+        first = got if first is None else first
+        assert np.array_equal(got[:m], first[:m])
+    kk, vv = k[:c - 20], v[:c - 20]
+    want = np.concatenate([OQ.query_attention(q[i:i + 1], kk[:c - n + i + 1], vv[:c - n + i + 1], scale) for i in range(m)])
+    t_max = float(np.max(np.linalg.norm(q.astype(np.float64), axis=-1)) * np.max(np.linalg.norm(kk, axis=-1))) * scale
+    G.close(first[:m], want, G.tolerance(pool, q.astype(np.float64), kk, vv, t_max, scale, 0.0, want), pool)
+    b.cache.close()
