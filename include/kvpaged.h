@@ -573,7 +573,8 @@ KV_API int paged_decode_attention_ex(kv_pool* pool, const kv_decode_args* args);
  * Arithmetic: float32 scores, softmax and sums; products of float16 operands (q, K and V; FP8
  * codes convert exactly and their scales are applied in float32; 4-bit values are exact); the
  * softmax weights enter the V products as float16 (relative 2^-11; down to 2^-21 of a row's
- * largest weight).  F32 pools: float32 throughout.  The result is rounded once.
+ * largest weight; with FP8 the weights times their blocks' value scales, down to 2^-21 of the
+ * largest such product that the row sees).  F32 pools: float32 throughout.  The result is rounded once.
  * The pool's device must be the current device.  Asynchronous.
  * The masked attention of a prompt that fills the cache, and the steps after it:
  * [KV Cache篇] §3.1 (scores over cache[:, :start_pos+seqlen] plus mask), over the block-table

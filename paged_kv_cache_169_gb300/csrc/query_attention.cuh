@@ -96,6 +96,17 @@ __device__ __forceinline__ float capped(float s, float k2, float capl) {
 // at most 2^15 in float16, and normal ones down to 2^-21 of the largest.
 constexpr float kRaise = 8.f, kLift = 7.f;
 
+// FP8: a weight enters the products times its block's value scale v, so the base follows the maximum of t + log2 v (the
+// weights' sum has the same base): what counts is a row's own largest product, whatever scales it does not see, or hardly.
+// (With scales relative to the largest of a work item, a row beside a scale 2^32 times its own was 0.)  v below 2^-60 counts
+// as that: values of less than 2^-51, lost in float16's rounding.  What is no scale, or so large that results overflow, is
+// NaN: a row that sees it is worked out again from the definition.  (Base and sums are joined across 2^84 of scales, so that
+// a weight that underflows there is below 2^-42 of the others.)
+constexpr float kLeastScale = -60.f, kMostScale = 24.f;        // log2
+__device__ __forceinline__ float value_log2(float v) {
+    return v >= 0.f && v <= 16777216.f ? fmaxf(log2f(v), kLeastScale) : CUDART_NAN_F;
+}
+
 template <int D, kv_dtype POOL>
 constexpr int kRowBytes = POOL == KV_INT4 ? D / 2 + D / 16 : POOL == KV_FP8_E4M3 ? D : 2 * D;
 

@@ -414,7 +414,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) query_few_kernel(const __grid_
         for (int n = 0; n < D / 8; ++n)
             #pragma unroll
             for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
-        float vref = 0x1p-126f, inv_vref = 0x1p126f;           // FP8: a power of two above the value scales so far
         int held = -1;                                         // the stage of this warp's last chunk here, not yet filled again
         #pragma unroll 1
         for (; k < to; k += step) {
@@ -423,10 +422,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1) query_few_kernel(const __grid_
             const char* st = ring + slot * C::STAGE;
             const int j0 = base + k * kChunk;
             const uint32_t kt = ring32 + slot * C::STAGE, vt = kt + C::RAW;
-            float ks[2] = {1.f, 1.f}, vs[2] = {1.f, 1.f};
+            float ks = 1.f, vs = 1.f, lv = 0.f;                // FP8: the scales of this lane's keys, log2 of the values'
             if constexpr (POOL == KV_FP8_E4M3) {
                 const float4 f = *reinterpret_cast<const float4*>(st + 2 * C::RAW);
-                ks[0] = f.x; ks[1] = f.y; vs[0] = f.z; vs[1] = f.w;
+                ks = t < 2 ? f.x : f.y;
+                vs = t < 2 ? f.z : f.w;
+                // (for the base only, so an approximate one does; see value_log2)
+                lv = fminf(fmaxf(__log2f(fabsf(vs)), kLeastScale), kMostScale);
             }
             // ---- scores: 16 rows by two times 8 keys
             float sc[2][4];
@@ -495,7 +497,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) query_few_kernel(const __grid_
                 for (int e = 0; e < 4; ++e) {
                     const int r = e >> 1, j = j0 + (POOL == KV_FP8_E4M3 ? 4 * t + 2 * n : n * 8 + 2 * t) + (e & 1);
                     float v = sc[n][e];
-                    if constexpr (POOL == KV_FP8_E4M3) v *= t < 2 ? ks[0] : ks[1];
+                    if constexpr (POOL == KV_FP8_E4M3) v *= ks;
                     if (cap) v = capped(v, k2, capl);
                     if (bias) v = fmaf(-slope[r], fabsf(static_cast<float>(pos[r] - j)), cap ? v : v * qscale);
                     v *= c;
@@ -505,7 +507,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) query_few_kernel(const __grid_
             float top[2];
             #pragma unroll
             for (int r = 0; r < 2; ++r)
-                top[r] = fmaxf(fmaxf(sc[0][2 * r], sc[0][2 * r + 1]), fmaxf(sc[1][2 * r], sc[1][2 * r + 1]));
+                top[r] = fmaxf(fmaxf(sc[0][2 * r], sc[0][2 * r + 1]), fmaxf(sc[1][2 * r], sc[1][2 * r + 1])) + lv;
             if (__any_sync(FULL, top[0] - m[0] > kRaise || top[1] - m[1] > kRaise)) {
                 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
@@ -523,19 +525,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) query_few_kernel(const __grid_
                     }
                 }
             }
-            if constexpr (POOL == KV_FP8_E4M3) {
-                const float big = fmaxf(fabsf(vs[0]), fabsf(vs[1]));
-                if (big > vref) {                              // (the same in every lane)
-                    const float to_ref = __int_as_float(min((__float_as_int(big) >> 23) + 1, 253) << 23);
-                    const float keep = vref / to_ref;
-                    #pragma unroll
-                    for (int n = 0; n < D / 8; ++n)
-                        #pragma unroll
-                        for (int e = 0; e < 4; ++e) o[n][e] *= keep;
-                    vref = to_ref;
-                    inv_vref = 1.f / to_ref;
-                }
-            }
             // ---- weights, their sums and the values
             uint32_t w[4];
             #pragma unroll
@@ -546,9 +535,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) query_few_kernel(const __grid_
                     float y0 = ex2_approx(sc[n][2 * r] + off), y1 = ex2_approx(sc[n][2 * r + 1] + off);
                     l[r] += y0 + y1;
                     if constexpr (POOL == KV_FP8_E4M3) {
-                        const float f = (t < 2 ? vs[0] : vs[1]) * inv_vref;
-                        y0 *= f;
-                        y1 *= f;
+                        y0 *= vs;
+                        y1 *= vs;
                     }
                     const __half2 hv = __floats2half2_rn(y0, y1);
                     w[2 * n + r] = *reinterpret_cast<const uint32_t*>(&hv);
@@ -612,7 +600,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) query_few_kernel(const __grid_
                 l[r] += __shfl_xor_sync(FULL, l[r], 1);
                 l[r] += __shfl_xor_sync(FULL, l[r], 2);
                 const int row = g + 8 * r;
-                const float inv = (l[r] == 0.f ? 0.f : 1.f / l[r]) * (POOL == KV_FP8_E4M3 ? vref : 1.f);
+                const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
                 char* out = a.out + static_cast<int64_t>(seq.first + row / a.G) * a.out_stride + (unit.h * a.G + row % a.G) * (D * 2);
                 bool finite = true;
                 #pragma unroll
@@ -648,14 +636,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1) query_few_kernel(const __grid_
                 const int row = g + 8 * r;
                 if (row >= rows) continue;
                 if (t == 0) s_ml[warp * kFewRows + row] = make_float2(m[r], l[r]);
-                const float mul = POOL == KV_FP8_E4M3 ? vref : 1.f;
                 #pragma unroll
                 for (int n = 0; n < D / 8; n += 2) {
                     if constexpr (POOL != KV_INT4) {
                         #pragma unroll
                         for (int y = n; y < n + 2; ++y)
                             *reinterpret_cast<float2*>(part + row * (D * 4) + (((2 * y + (t >> 1)) ^ (row & 7)) << 4) + (t & 1) * 8) =
-                                make_float2(o[y][2 * r] * mul, o[y][2 * r + 1] * mul);
+                                make_float2(o[y][2 * r], o[y][2 * r + 1]);
                     } else if (n % 4 == 0) {
                         #pragma unroll
                         for (int y = 0; y < 2; ++y)

@@ -72,7 +72,7 @@ struct PromptCfg {
     static constexpr int Q_OFF = 0, KV_OFF = 2 * TILE, RAW_OFF = KV_OFF + SLOTS * TILE;
     static constexpr int OUT_OFF = RAW_OFF + RAWS * RAW;       // 64 elements of a softmax warp's 16 rows on their way out
     static constexpr int FACTOR_OFF = OUT_OFF + kSoftmaxWarps * 16 * 128;
-    static constexpr int FACTORS = POOL == KV_FP8_E4M3 ? kFactorTiles * 2 * 16 * 4 : 0;
+    static constexpr int FACTORS = POOL == KV_FP8_E4M3 ? kFactorTiles * 3 * 16 * 4 : 0;
     static constexpr int BAR_OFF = FACTOR_OFF + FACTORS;
     static constexpr int BARS = 2 * SLOTS + 2 * RAWS + 5 * 2 + 2 * 2 + 3;
     static constexpr int MISC_OFF = (BAR_OFF + BARS * 8 + 15) / 16 * 16;
@@ -175,7 +175,6 @@ struct Item {
     int first, n, ctx;                 // the sequence (QuerySeq)
     int lo[2], hi[2];                  // positions that some row of a row tile sees
     int z, from, to;                   // the part of the keys, and its positions
-    float vref;                        // FP8: the largest value scale
 };
 struct PromptMisc {
     uint4 claim;                       // the answer to a claim of the next item
@@ -242,7 +241,8 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
     auto item_there = [&](int i) { return bar(B0 + 10 + i); };
     auto item_free = [&](int i) { return bar(B0 + 12 + i); };
     const uint32_t edge = bar(B0 + 14), done = bar(B0 + 15), claim = bar(B0 + 16);
-    float* const factors = reinterpret_cast<float*>(smem + C::FACTOR_OFF);     // FP8: [tile][keys, values][8 tokens]
+    // FP8, per 8 tokens of a tile: 16 times (factor of the scores, log2 of the value scale), then 16 times 1 / value scale
+    float* const factors = reinterpret_cast<float*>(smem + C::FACTOR_OFF);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::SLOTS; ++i) {
@@ -299,7 +299,6 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
             it.lo[t] = uniform(x.lo[t]);
             it.hi[t] = uniform(x.hi[t]);
         }
-        it.vref = x.vref;
         __syncwarp();
         if (lane == 0) mbar_arrive(item_free(i));
         ++count;
@@ -318,7 +317,7 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
         constexpr int DIR = BIAS ? -1 : 1;                     // of the key tiles
         const float qscale = a.scale * kLog2e;
         const float k2 = CAP ? 2.f * kLog2e * (a.scale / a.cap) : 0.f, capl = a.cap * kLog2e;
-        const float c = CAP || BIAS ? 1.f : qscale;            // scores to log2 units
+        const float c = CAP || BIAS || POOL == KV_FP8_E4M3 ? 1.f : qscale;     // scores to log2 units
         int i = 0, tiles = 0;                                  // this row tile's key tiles so far; the items'
         auto row_of = [&](int r) { return rows0 + (lane >> 2) + 8 * r; };
         // An item's part of this thread, taken while the last products of the item before are made.  (The rest stays in
@@ -366,32 +365,52 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                 tc_fence_after();
                 float x[64];                                   // [group of 8 columns][row][2]
                 uint32_t* const xr = reinterpret_cast<uint32_t*>(x);
+                const float4* scales = nullptr;                // FP8
                 tmem_load_16x64(st, xr);
-                tmem_load_16x64(st + 64, xr + 32);
-                tmem_wait_load32(xr);
-                tmem_wait_load32(xr + 32);
-                const float4* scales = nullptr;                // FP8: per 8 keys, then per 8 values
-                if constexpr (POOL == KV_FP8_E4M3) {
-                    scales = reinterpret_cast<const float4*>(factors + tile++ % kFactorTiles * 32);
+                if constexpr (POOL != KV_FP8_E4M3) {
+                    tmem_load_16x64(st + 64, xr + 32);
+                    tmem_wait_load32(xr);
+                    tmem_wait_load32(xr + 32);
+                } else {
+                    scales = reinterpret_cast<const float4*>(factors + tile++ % kFactorTiles * 48);
                     #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float4 f = scales[k];
-                        const float of[4] = {f.x, f.y, f.z, f.w};
+                    for (int half = 0; half < 2; ++half) {
+                        float4 f[4];
                         #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            float* const y = x + 16 * k + 2 * e;
-                            const float2 v = __fmul2_rn(make_float2(y[0], y[1]), make_float2(of[e >> 1], of[e >> 1]));
-                            y[0] = v.x;
-                            y[1] = v.y;
+                        for (int k = 0; k < 4; ++k) f[k] = scales[4 * half + k];       // (beside the scores' way here)
+                        tmem_wait_load32(xr + 32 * half);
+                        if (half == 0) tmem_load_16x64(st + 64, xr + 32);
+                        #pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            float* const y = x + 32 * half + 2 * e;
+                            const float of = e & 2 ? f[e >> 2].z : f[e >> 2].x, lv = e & 2 ? f[e >> 2].w : f[e >> 2].y;
+                            const float2 at = make_float2(y[0], y[1]), by = make_float2(of, of);
+                            const float2 s = CAP ? __fmul2_rn(at, by) : __ffma2_rn(at, by, make_float2(lv, lv));
+                            y[0] = s.x;
+                            y[1] = s.y;
                         }
                     }
                 }
                 if (CAP) {
                     #pragma unroll
                     for (int k = 0; k < 64; k += 4) capped4(x + k, k2, capl);
+                    if constexpr (POOL == KV_FP8_E4M3) {
+                        #pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float4 v = scales[k];
+                            #pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                float* const y = x + 8 * k + 2 * e;
+                                const float lv = e < 2 ? v.y : v.w;
+                                const float2 s = __fadd2_rn(make_float2(y[0], y[1]), make_float2(lv, lv));
+                                y[0] = s.x;
+                                y[1] = s.y;
+                            }
+                        }
+                    }
                 }
                 if (BIAS) {
-                    const float mul = CAP ? 1.f : qscale;
+                    const float mul = CAP || POOL == KV_FP8_E4M3 ? 1.f : qscale;
                     #pragma unroll
                     for (int r = 0; r < 2; ++r) {
                         const float from = static_cast<float>(pos0 + (row_of(r) >> log_g) - j0 - 2 * quad);
@@ -466,11 +485,12 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                     float2 y = __ffma2_rn(make_float2(x[2 * k], x[2 * k + 1]), c2, make_float2(off, off));
                     y.x = ex2_approx(y.x);
                     y.y = ex2_approx(y.y);
-                    sum[r] = k < 2 ? y : __fadd2_rn(sum[r], y);
-                    if constexpr (POOL == KV_FP8_E4M3) {
-                        if (k % 8 == 0) vf = scales[4 + k / 8];
+                    if constexpr (POOL == KV_FP8_E4M3) {       // (y: the weight times its value scale)
+                        if (k % 8 == 0) vf = scales[8 + k / 8];
                         const float f = k % 8 < 2 ? vf.x : k % 8 < 4 ? vf.y : k % 8 < 6 ? vf.z : vf.w;
-                        y = __fmul2_rn(y, make_float2(f, f));
+                        sum[r] = k < 2 ? __fmul2_rn(y, make_float2(f, f)) : __ffma2_rn(y, make_float2(f, f), sum[r]);
+                    } else {
+                        sum[r] = k < 2 ? y : __fadd2_rn(sum[r], y);
                     }
                     const __half2 hv = __floats2half2_rn(y.x, y.y);
                     w[k] = *reinterpret_cast<const uint32_t*>(&hv);
@@ -521,14 +541,14 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                         #pragma unroll
                         for (int g = 0; g < 2; ++g)
                             *reinterpret_cast<float2*>(a.part_o + at * D + k + 8 * g + 2 * quad) =
-                                make_float2(__uint_as_float(o[4 * g + 2 * r]) * it.vref, __uint_as_float(o[4 * g + 2 * r + 1]) * it.vref);
+                                make_float2(__uint_as_float(o[4 * g + 2 * r]), __uint_as_float(o[4 * g + 2 * r + 1]));
                     }
                 }
                 tc_fence_before();
                 continue;
             }
             // the result, 64 elements at a time through shared memory, so that a store writes whole lines
-            const float inv[2] = {l[0] == 0.f ? 0.f : it.vref / l[0], l[1] == 0.f ? 0.f : it.vref / l[1]};
+            const float inv[2] = {l[0] == 0.f ? 0.f : 1.f / l[0], l[1] == 0.f ? 0.f : 1.f / l[1]};
             char* const to = a.out + static_cast<int64_t>(it.first + it.token + rt * per_tile) * a.out_stride +
                              it.head * a.G * (D * 2) + (lane & 7) * 16;
             const int left = it.n - it.token - rt * per_tile;  // tokens of the row tile
@@ -760,9 +780,11 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                 if constexpr (POOL == KV_FP8_E4M3) {
                     const int of = __shfl_sync(0xffffffffu, id, lane < 16 ? 8 * lane >> log_b : 0);
                     if (lane < 16) {                           // per 8 tokens
-                        float* const f = factors + (ring >> 1) % kFactorTiles * 32 + lane;
-                        f[0] = of >= 0 ? a.kscale[of] : 0.f;
-                        f[16] = of >= 0 ? a.vscale[of] / it.vref : 0.f;
+                        float* const f = factors + (ring >> 1) % kFactorTiles * 48;
+                        const float lv = value_log2(of >= 0 ? a.vscale[of] : 0.f);
+                        f[2 * lane] = of >= 0 ? a.kscale[of] * (CAP ? 1.f : a.scale * kLog2e) : 0.f;
+                        f[32 + lane] = lv == lv ? exp2f(-lv) : 0.f;
+                        f[2 * lane + 1] = lv;
                     }
                     __syncwarp();
                 }
@@ -859,7 +881,7 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                 seq = QuerySeq{__shfl_sync(0xffffffffu, lane_seq.first, of), __shfl_sync(0xffffffffu, lane_seq.n, of),
                                __shfl_sync(0xffffffffu, lane_seq.ctx, of)};
             }
-            Item x{index < 0 ? -1 : s, head, token, seq.first, seq.n, seq.ctx, {1 << 30, 1 << 30}, {0, 0}, z, 0, 1 << 30, 1.f};
+            Item x{index < 0 ? -1 : s, head, token, seq.first, seq.n, seq.ctx, {1 << 30, 1 << 30}, {0, 0}, z, 0, 1 << 30};
             if (index >= 0) {
                 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
@@ -887,17 +909,6 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                             x.hi[t] = 0;
                         }
                     }
-                }
-                if constexpr (POOL == KV_FP8_E4M3) {
-                    // value scales enter the weights relative to the largest one, which multiplies the result
-                    float top = 0.f;
-                    const int end = max(x.hi[0], x.hi[1]);
-                    #pragma unroll 4
-                    for (int at = (min(x.lo[0], x.lo[1]) & -a.B) + lane * a.B; at < end; at += 32 * a.B)
-                        top = max_nan(top, fabsf(a.vscale[query_block(a, s, at)]));
-                    // (bits of magnitudes, NaN among them, are ordered as integers)
-                    top = __int_as_float(__reduce_max_sync(0xffffffffu, __float_as_int(top) & 0x7FFFFFFF));
-                    x.vref = max_nan(top, 1.17549435e-38f);
                 }
             }
             const int i = count & 1;
