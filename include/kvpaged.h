@@ -557,7 +557,10 @@ KV_API int paged_decode_attention_ex(kv_pool* pool, const kv_decode_args* args);
  *   max_context    host upper bound of context_lens, 0 .. 2^24.  (Calls of more than 2^30 row tiles or,
  *                  with at most 16 rows of a KV head, 16-token chunks in 1024 sequences are refused.)
  *   window         0, or the last `window` positions only.
- *   scale          finite and > 0.   score_cap  0 (none), or finite and > 0.
+ *   scale          finite and > 0.
+ *   score_cap      0 (none), or finite and > 0.  tanh is good to 2^-20 of the cap for caps up to 64,
+ *                  above that and over F32 pools to 2^-20 of the score: a cap far above the scores
+ *                  leaves them as they are.
  *   slopes         NULL, or device float32 [num_q_heads].
  *   ranges         NULL, or device int32 [num_tokens][2], 8-byte aligned: the positions
  *                  [first, end) a row sees, in place of the causal [0, p + 1): prefixes and images

@@ -92,6 +92,20 @@ __device__ __forceinline__ float capped(float s, float k2, float capl) {
     return fmaf(-2.f * capl, r, capl);
 }
 
+// That error is a part of the cap, whatever the score: up to a cap of 64 it is below 2^-14, an eighth of what rounding a
+// weight to float16 is.  Above, the score counts: where |x| < cap / 2 the series of tanh about 0 (its next term is below
+// 2^-23), elsewhere as above; 2^-21 of the score in all.  sl: scale in log2 units.
+constexpr float kLargeCap = 64.f;
+__device__ __forceinline__ float capped_large(float s, float sl, float k2, float capl) {
+    const float u = s * k2, z = u * u * 0.12011325f, x = s * sl;               // u = 2 x / cap in log2 units; z = (x / cap)^2
+    float p = fmaf(21844.f / 6081075.f, z, -1382.f / 155925.f);
+    p = fmaf(p, z, 62.f / 2835.f);
+    p = fmaf(p, z, -17.f / 315.f);
+    p = fmaf(p, z, 2.f / 15.f);
+    p = fmaf(p, z, -1.f / 3.f);
+    return fabsf(u) < kLog2e ? fmaf(x * p, z, x) : capped(s, k2, capl);
+}
+
 // Weights are kept 2^7 above their softmax value relative to the base, which may lag the maximum by up to 2^8:
 // at most 2^15 in float16, and normal ones down to 2^-21 of the largest.
 constexpr float kRaise = 8.f, kLift = 7.f;

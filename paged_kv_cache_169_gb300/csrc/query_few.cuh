@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) query_few_kernel(const __grid_
     for (int i = 0; i < C::STAGES; ++i) ask();
 
     // ---- the CTA's units
-    const bool bias = a.slopes != nullptr, cap = a.cap > 0.f;
+    const bool bias = a.slopes != nullptr, cap = a.cap > 0.f, large_cap = a.cap > kLargeCap;
     const float qscale = a.scale * kLog2e, c = cap || bias ? 1.f : qscale;
     const float k2 = cap ? 2.f * kLog2e * (a.scale / a.cap) : 0.f, capl = a.cap * kLog2e;
     struct Cross { int s, h, first, last; };                   // a unit that crosses CTAs: its first and last CTA
@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) query_few_kernel(const __grid_
                     const int r = e >> 1, j = j0 + (POOL == KV_FP8_E4M3 ? 4 * t + 2 * n : n * 8 + 2 * t) + (e & 1);
                     float v = sc[n][e];
                     if constexpr (POOL == KV_FP8_E4M3) v *= ks;
-                    if (cap) v = capped(v, k2, capl);
+                    if (cap) v = large_cap ? capped_large(v, qscale, k2, capl) : capped(v, k2, capl);
                     if (bias) v = fmaf(-slope[r], fabsf(static_cast<float>(pos[r] - j)), cap ? v : v * qscale);
                     v *= c;
                     sc[n][e] = !masked || (j >= sees[r].x && j < sees[r].y) ? v : -CUDART_INF_F;

@@ -96,7 +96,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 // capped() of four with one reciprocal: 1/a = b (cd) / (ab cd) and so on, each factor below 2^30 + 1 (tanh is 1 long
-// before).  Four multiplications and the reciprocal are off by 7 2^-24 together: t within 2^-20 of the cap.  The special
+// before).  Four multiplications and the reciprocal are off by 7 2^-24 together: t within 2^-20 of the cap, of at
+// most kLargeCap.  The special
 // function unit makes 5 values for four scores where it made 8 (2 x 4096 capped tokens: 773 -> 700 us then).
 __device__ __forceinline__ void capped4(float* x, float k2, float capl) {
     float2 y[2], a[2];
@@ -217,7 +218,10 @@ __device__ __forceinline__ int claimed_item(const uint4& v) {
     return x;
 }
 
-template <int D, kv_dtype POOL, bool BIAS, bool CAP>
+// CAP: none, up to kLargeCap, above it.
+enum Cap : int { NO_CAP = 0, SMALL_CAP = 1, LARGE_CAP = 2 };
+
+template <int D, kv_dtype POOL, bool BIAS, int CAP>
 __global__ void __launch_bounds__(PromptCfg<D, POOL>::WARPS * 32, 1)
 query_prompt_kernel(const __grid_constant__ PromptArgs p) {
     using C = PromptCfg<D, POOL>;
@@ -393,7 +397,14 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                 }
                 if (CAP) {
                     #pragma unroll
-                    for (int k = 0; k < 64; k += 4) capped4(x + k, k2, capl);
+                    for (int k = 0; k < 64; k += 4) {
+                        if constexpr (CAP == SMALL_CAP) {
+                            capped4(x + k, k2, capl);
+                        } else {
+                            #pragma unroll
+                            for (int e = k; e < k + 4; ++e) x[e] = capped_large(x[e], qscale, k2, capl);
+                        }
+                    }
                     if constexpr (POOL == KV_FP8_E4M3) {
                         #pragma unroll
                         for (int k = 0; k < 8; ++k) {
@@ -1010,7 +1021,7 @@ __global__ void __launch_bounds__(256) query_join_kernel(const __grid_constant__
     }
 }
 
-template <typename C, bool BIAS, bool CAP>
+template <typename C, bool BIAS, int CAP>
 int launch_prompt_typed(const kv_pool* pool, const PromptArgs& p, bool pdl, cudaStream_t stream) {
     static unsigned long long attr_done = 0;               // the shared-memory opt-in is a per-device attribute
     const unsigned long long bit = 1ull << (pool->device & 63);
@@ -1054,10 +1065,12 @@ int launch_prompt_pool(const kv_pool* pool, const PromptArgs& p, bool pdl, cudaS
         return pool->desc.head_dim == 128 ? launch_prompt_typed<PromptCfg<128, POOL>, bias.value, cap.value>(pool, p, pdl, stream)
                                           : launch_prompt_typed<PromptCfg<64, POOL>, bias.value, cap.value>(pool, p, pdl, stream);
     };
-    const std::true_type yes{};
-    const std::false_type no{};
-    if (p.a.cap > 0.f) return p.a.slopes ? launch(yes, yes) : launch(no, yes);
-    return p.a.slopes ? launch(yes, no) : launch(no, no);
+    auto with_cap = [&](auto bias) {
+        if (p.a.cap > kLargeCap) return launch(bias, std::integral_constant<int, LARGE_CAP>{});
+        if (p.a.cap > 0.f) return launch(bias, std::integral_constant<int, SMALL_CAP>{});
+        return launch(bias, std::integral_constant<int, NO_CAP>{});
+    };
+    return p.a.slopes ? with_cap(std::true_type{}) : with_cap(std::false_type{});
 }
 
 }  // namespace
