@@ -567,7 +567,9 @@ KV_API int paged_decode_attention_ex(kv_pool* pool, const kv_decode_args* args);
  *                  seen both ways, packed documents, padding rows (an empty range).  Any values:
  *                  what lies outside the context is not seen.
  *   workspace      device, >= paged_query_workspace_size(...) bytes, 256-byte aligned; contents
- *                  need not be initialised; not shared between calls that may overlap.
+ *                  need not be initialised; not shared between calls that may overlap.  The size
+ *                  for a shape serves every call of no more sequences, rows, rows per sequence and
+ *                  positions with the same heads and window (any window, if the size's was 0).
  *   flags          0, or a sum of KV_DECODE_WORKSPACE_ZEROED (the workspace was zero-filled once and
  *                  used since only by calls of this entry point on this pool, of any shapes it is
  *                  large enough for, with no device error in between) and KV_DECODE_PDL (may be

@@ -390,7 +390,8 @@ class PagedKVCache:
     def query_workspace(self, batch: int, num_q_heads: int, max_queries: int, max_context: int, window: int = 0,
                         num_tokens: int | None = None) -> torch.Tensor:
         """A new zero-filled workspace for query_attention, also with KV_DECODE_WORKSPACE_ZEROED: for calls
-        of this shape, or of any that needs no more.  num_tokens: rows of q (default batch * max_queries)."""
+        of this shape and of any no larger (fewer sequences, rows or positions: a prompt's serves the single
+        tokens after it).  num_tokens: rows of q (default batch * max_queries)."""
         a = abi.kv_query_args()
         a.num_q_heads, a.batch, a.max_queries, a.max_context, a.window = num_q_heads, batch, max_queries, max_context, window
         a.num_tokens = batch * max_queries if num_tokens is None else num_tokens

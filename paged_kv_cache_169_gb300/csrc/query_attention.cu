@@ -189,8 +189,10 @@ int plan_query(const kv_pool* pool, const kv_query_args& x, QueryPlan* plan) {
         plan->splits = parts.splits;
         plan->part_rows = parts.rows;
         plan->part_by_sequence = parts.by_sequence;
-        // (behind the few-row kernel's counters, which stay zero)
-        if (parts.space > 0) plan->ws_bytes = counters + static_cast<size_t>(parts.space) * (d.head_dim * 4 + 8);
+        // Behind the few-row kernel's counters, which stay zero; and what that kernel needs, so that a workspace for many
+        // rows serves the calls of few that come between.
+        const size_t part_bytes = counters + static_cast<size_t>(parts.space) * (d.head_dim * 4 + 8);
+        plan->ws_bytes = part_bytes > few_bytes ? part_bytes : few_bytes;
     }
     if (plan->kind == QueryPlan::FEW) {
         const int64_t seqs = x.batch < kFewSeqs ? x.batch : kFewSeqs;

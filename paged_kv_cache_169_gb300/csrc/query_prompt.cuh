@@ -96,9 +96,9 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 // capped() of four with one reciprocal: 1/a = b (cd) / (ab cd) and so on, each factor below 2^30 + 1 (tanh is 1 long
-// before).  Four multiplications and the reciprocal are off by 7 2^-24 together: t within 2^-20 of the cap, of at
-// most kLargeCap.  The special
-// function unit makes 5 values for four scores where it made 8 (2 x 4096 capped tokens: 773 -> 700 us then).
+// before).  Four multiplications and the reciprocal are off by 7 2^-24 together: t within 2^-20 of the cap
+// (kLargeCap at most).  The special function unit makes 5 values for four scores where it made 8 (2 x 4096 capped tokens:
+// 773 -> 700 us then).
 __device__ __forceinline__ void capped4(float* x, float k2, float capl) {
     float2 y[2], a[2];
     #pragma unroll

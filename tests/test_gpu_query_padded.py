@@ -69,3 +69,17 @@ def test_rows_named_twice_in_parts():
     G.close(got[:n], want, G.tolerance("f16", q[:n].astype(np.float64), k, v, 40.0, scale, 0.0, want), n)
     assert (got[n:] == 7.5).all()
     b.cache.close()
+
+
+@pytest.mark.parametrize("pool", ["f16", "fp8", "int4"])
+@pytest.mark.parametrize("lens", [[700, 90], [3000, 400]])
+def test_one_workspace_for_prompts_and_tokens(pool, lens):
+    """The workspace of the largest prompt, zeroed once, serves prompts and the single tokens between them."""
+    b = G.Batch(pool, 128, 2, 16, lens, seed=len(pool))
+    ws = b.cache.query_workspace(2, 4, 90, max(lens))
+    flags = abi.KV_DECODE_WORKSPACE_ZEROED | abi.KV_DECODE_PDL
+    for new in ([90, 60], [1, 1], [20, 3], [1, 2], [90, 60]):
+        want, q, _ = G.run(b, new, 2)
+        for _ in range(2):
+            assert np.array_equal(G.run(b, new, 2, workspace=ws, flags=flags, check=False, q_in=q)[0], want)
+    b.cache.close()

@@ -87,3 +87,32 @@ def test_few_rows_of_a_padded_buffer(lib):
         a = H.query_args(num_q_heads=64, batch=batch, max_queries=queries, num_tokens=tokens, max_context=16384)
         assert abi.load().paged_query_workspace_size(C.addressof(pool(abi.KV_F16, 128, 8)), C.byref(a)) >= \
             (out[1] + 1) * (128 * 4 + 8)
+
+
+@pytest.mark.parametrize("dtype", [abi.KV_F32, abi.KV_F16, abi.KV_FP8_E4M3, abi.KV_INT4])
+def test_a_size_serves_every_smaller_call(lib, dtype):
+    """No call of fewer sequences, rows, rows per sequence or positions needs more, whichever kernel it takes."""
+    heads, group = 4, 4
+    h = pool(dtype, 128, heads)
+
+    def size(batch, queries, tokens, context, window):
+        a = H.query_args(num_q_heads=heads * group, batch=batch, max_queries=queries, num_tokens=tokens, max_context=context,
+                         window=window)
+        return abi.load().paged_query_workspace_size(C.addressof(h), C.byref(a))
+
+    batches, rows, contexts = (1, 2, 8, 40), (1, 4, 5, 32, 300, 2000), (16, 600, 1023, 1024, 1600, 9000, 70000)
+    shapes = [(b, q, t, c) for b in batches for q in rows for t in sorted({q, b * q, b * q + 3, 4 * b * q}) for c in contexts]
+    for window in (0, 900):
+        largest = {s: size(*s, window) for s in shapes}
+        assert min(largest.values()) >= 256
+        for s, n in largest.items():
+            for i in range(4):                                 # one argument less, and all of them
+                for less in (1, s[i] // 2, s[i] - 1):
+                    t = s[:i] + (max(less, 1),) + s[i + 1:]
+                    if t[1] <= t[2]:
+                        assert size(*t, window) <= n, (s, t, window)
+            t = tuple(max(x // 3, 1) for x in s)
+            if t[1] <= t[2]:
+                assert size(*t, window) <= n
+            if window == 0:
+                assert size(*s, 500) <= n and size(*s, 5000) <= n
