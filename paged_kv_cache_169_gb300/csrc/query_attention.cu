@@ -226,7 +226,7 @@ int launch_query(const kv_pool* pool, const kv_query_args& x, const QueryPlan& p
     a.batch = x.batch;
     const int64_t table_tokens = static_cast<int64_t>(x.max_blocks_per_seq) * d.block_size;
     a.ctx_limit = static_cast<int>(table_tokens < x.max_context ? table_tokens : x.max_context);
-    a.window = x.window;
+    a.window = x.window < 2 * kMaxQueryTokens ? x.window : 2 * kMaxQueryTokens;            // (a row may stand at -2^24)
     a.H = d.num_heads;
     a.G = x.num_q_heads / d.num_heads;
     a.B = d.block_size;
