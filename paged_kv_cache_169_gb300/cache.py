@@ -148,8 +148,9 @@ class PagedKVCache:
                          positions: torch.Tensor, axes: abi.kv_rope_axes, cos_sin: torch.Tensor,
                          q: torch.Tensor | None = None, q_out: torch.Tensor | None = None,
                          adjacent_pairs: bool = False, flags: int = 0, stream=None) -> torch.Tensor | None:
-        """append_rope for positions with several axes (time, height, width): positions int32
-        [num_axes, n], axes from rope_axes; pair i turns by its own axis' position."""
+        """append_rope for positions with several axes (time, height, width): positions int32 [axes, n]
+        (rows of axes that no pair uses are not looked at), axes from rope_axes or an abi.kv_rope_axes;
+        pair i turns by its own axis' position."""
         return self._append_rope(layer, k, v, slot_mapping, positions, axes, cos_sin, q, q_out, adjacent_pairs, flags,
                                  stream)
 
@@ -165,8 +166,8 @@ class PagedKVCache:
         if axes is None:
             if positions.numel() != n:
                 raise ValueError("positions must have one entry per token")
-        elif positions.shape != (axes.num_axes, n):
-            raise ValueError("positions must be [axes, num_tokens]")
+        elif positions.dim() != 2 or positions.shape[0] < axes.num_axes or positions.shape[1] != n:
+            raise ValueError("positions must be [axes, num_tokens], with every axis of the pairs")
         if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
             raise ValueError("cos_sin must be float32 [positions, rot_dim]")
         dev = self.k[0].get_device()
@@ -186,7 +187,7 @@ class PagedKVCache:
             raise ValueError("q_out without q")
         (kp, ks), (vp, vs) = _rows(k, n, h, d, "k", dev), _rows(v, n, h, d, "v", dev)
         table_len, rot = cos_sin.shape
-        if axes is not None and axes.pairs != rot // 2:
+        if axes is not None and getattr(axes, "pairs", rot // 2) != rot // 2:         # (one made by hand has no count)
             raise ValueError("the axes must cover the rot_dim / 2 pairs of cos_sin")
         a = abi.kv_rope_args(layer, qp, hq, op, kp, vp, _IN_DTYPE[dt], qs, ks, vs, os,
                              _ptr_on(slot_mapping, "slot_mapping", dev), _ptr_on(positions, "positions", dev),
