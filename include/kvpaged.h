@@ -70,7 +70,8 @@ enum {
     KV_DEVERR_SLOT = 1,        /* slot_mapping entry >= num_blocks*block_size           */
     KV_DEVERR_BLOCK_ID = 2,    /* block table / copy pair id outside [0, num_blocks)    */
     KV_DEVERR_CONTEXT = 4,     /* context_len < 0, > max_blocks*block_size or > max_context */
-    KV_DEVERR_TIMEOUT = 8,     /* a bounded mbarrier wait ran out (about one second)    */
+    KV_DEVERR_TIMEOUT = 8,     /* a bounded mbarrier wait ran out (about one second; eight in
+                                  paged_query_attention)                                 */
     KV_DEVERR_PREFIX = 16,     /* a prefix group broke its rules (attended without sharing) */
     KV_DEVERR_POSITION = 32,   /* kv_append_rope: a position outside the table               */
     KV_DEVERR_QUERY = 64       /* paged_query_attention: a sequence's rows outside [0, num_tokens),
@@ -532,7 +533,8 @@ KV_API int paged_decode_attention_ex(kv_pool* pool, const kv_decode_args* args);
  * with (first, end) = (0, p + 1), or ranges[row].  With x = scale * q . k_j the score is
  *     t = score_cap * tanh(x / score_cap)  (x itself with score_cap 0),   less slopes[h] * |p - j|,
  * and out = sum_j softmax(t)_j v_j, 0 where nothing is seen.  What a row does not see never
- * reaches it, NaN and infinities included.
+ * reaches it, NaN and infinities included.  (Rows beside such a value are worked out again, far slower; over
+ * contexts of more than a million positions that may set KV_DEVERR_TIMEOUT.)
  *   layer          0 .. num_layers-1.
  *   q              device [num_tokens] rows of num_q_heads*head_dim elements: float32 for F32
  *                  pools, float16 for the others; 16-byte aligned.

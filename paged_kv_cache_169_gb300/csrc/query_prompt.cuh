@@ -140,9 +140,12 @@ __device__ __forceinline__ uint32_t tile_at(int r, int ch) {
 // keep a warp together and operands made of it may be uniform registers, as the matrix instructions' must be.
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
-// A bounded wait by a whole warp: all of its lanes go on, or none.
+// A bounded wait by a whole warp: all of its lanes go on, or none.  Eight seconds: a warp that works its 16 rows out again
+// (attend_row: 0.36 us a position and row) lets the rest of its CTA wait, over 170 thousand positions for one second, over
+// 1.4 million for eight.  (A limit from the context's length, read from the arguments, cost FP8 chunks 3%.)
+constexpr uint64_t kPromptWaitNs = 8 * kWaitLimitNs;
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* err) {
-    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, err));
+    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, err, kPromptWaitNs));
 }
 
 // Key tiles [a, b) of each row tile, numbered from position `base`; the work item's are those that either row tile

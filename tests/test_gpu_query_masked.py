@@ -92,3 +92,34 @@ def test_rows_of_joined_parts(pool, d, group):
     t_max = float(np.max(np.linalg.norm(q.astype(np.float64), axis=-1)) * np.max(np.linalg.norm(kk, axis=-1))) * scale
     G.close(first[:m], want, G.tolerance(pool, q.astype(np.float64), kk, vv, t_max, scale, 0.0, want), pool)
     b.cache.close()
+
+
+def test_rows_worked_out_again_over_a_long_context():
+    """The last token's key and value are NaN after 250 000 others: the rows of its row tiles that do not see it are worked
+    out again, 16 a warp, for longer than a wait lasts that nothing moves beside.  No wait runs out, and the rows are right."""
+    c, n, H, group, d, B, scale = 250_000, 512, 8, 8, 64, 32, 0.125
+    nb = -(-c // B)
+    cache = G.PagedKVCache(1, nb, B, H, d, "fp8")
+    rng = np.random.default_rng(3)
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    for t in (cache.k[0], cache.v[0]):
+        t.view(torch.uint8).copy_(torch.randint(0, 127, t.shape, dtype=torch.uint8, device="cuda", generator=gen))
+        t.view(torch.uint8).bitwise_or_(torch.randint(0, 2, t.shape, dtype=torch.uint8, device="cuda", generator=gen) << 7)
+        t.view(torch.uint8)[(c - 1) // B, :, (c - 1) % B] = 0x7F
+    cache.k_scale[0].fill_(0.004)
+    cache.v_scale[0].fill_(0.01)
+    q = rng.standard_normal((n, H * group, d)).astype(np.float16)
+    got = cache.query_attention(0, torch.from_numpy(q).cuda(), up([0, n]), up(np.arange(nb)[None]), up([c]), n, c,
+                                scale).cpu().numpy()
+    assert cache.device_error() == 0
+    assert np.isnan(got[-1]).all() and not np.isnan(got[:-1]).any()
+    for head in (0, 29, 63):
+        k, v = (G.OF.decode(t.view(torch.uint8)[:, head // group].reshape(-1, d)[:c - 1].cpu().numpy()) * s
+                for t, s in ((cache.k[0], float(cache.k_scale[0][0])), (cache.v[0], float(cache.v_scale[0][0]))))
+        for i in (0, n - 3, n - 2):
+            seen = c - n + i + 1
+            want = OQ.query_attention(q[i:i + 1, head:head + 1], k[:seen, None], v[:seen, None], scale)     # (its last row)
+            tol = G.tolerance("fp8", q[i:i + 1, head:head + 1].astype(np.float64), k[:seen, None], v[:seen, None], 60.0, scale, 0.0,
+                              want)
+            G.close(got[i:i + 1, head:head + 1], want, tol, (head, i))
+    cache.close()
