@@ -95,14 +95,14 @@ __device__ __forceinline__ float capped(float s, float k2, float capl) {
 // That error is a part of the cap, whatever the score: up to a cap of 64 it is below 2^-14, an eighth of what rounding a
 // weight to float16 is.  Above, the score counts: where |x| < cap / 2 the series of tanh about 0 (its next term is below
 // 2^-23), elsewhere as above; 2^-21 of the score in all.  sl: scale in log2 units.
-constexpr float kLargeCap = 64.f;
+constexpr float kLargeCap = 64.f, kHalfLn2Sq = 0.12011325f;
+// tanh y = y (1 + z (-1/3 + 2/15 z - ...)), z = y^2
+__device__ constexpr float kTanh[6] = {21844.f / 6081075.f, -1382.f / 155925.f, 62.f / 2835.f, -17.f / 315.f, 2.f / 15.f, -1.f / 3.f};
 __device__ __forceinline__ float capped_large(float s, float sl, float k2, float capl) {
-    const float u = s * k2, z = u * u * 0.12011325f, x = s * sl;               // u = 2 x / cap in log2 units; z = (x / cap)^2
-    float p = fmaf(21844.f / 6081075.f, z, -1382.f / 155925.f);
-    p = fmaf(p, z, 62.f / 2835.f);
-    p = fmaf(p, z, -17.f / 315.f);
-    p = fmaf(p, z, 2.f / 15.f);
-    p = fmaf(p, z, -1.f / 3.f);
+    const float u = s * k2, z = u * u * kHalfLn2Sq, x = s * sl;                // u = 2 x / cap in log2 units; z = (x / cap)^2
+    float p = kTanh[0];
+    #pragma unroll
+    for (int i = 1; i < 6; ++i) p = fmaf(p, z, kTanh[i]);
     return fabsf(u) < kLog2e ? fmaf(x * p, z, x) : capped(s, k2, capl);
 }
 

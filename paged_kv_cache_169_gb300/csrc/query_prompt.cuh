@@ -119,6 +119,16 @@ __device__ __forceinline__ void capped4(float* x, float k2, float capl) {
     }
 }
 
+// capped_large() of two scores below half the cap.
+__device__ __forceinline__ float2 tanh_series2(float2 s, float sl, float k2) {
+    auto both = [](float c) { return make_float2(c, c); };
+    const float2 u = __fmul2_rn(s, both(k2)), z = __fmul2_rn(__fmul2_rn(u, u), both(kHalfLn2Sq)), x = __fmul2_rn(s, both(sl));
+    float2 p = both(kTanh[0]);
+    #pragma unroll
+    for (int i = 1; i < 6; ++i) p = __ffma2_rn(p, z, both(kTanh[i]));
+    return __ffma2_rn(__fmul2_rn(x, p), z, x);
+}
+
 // A place in a ring of N: how often it went round, too.
 template <int N> struct Ring {
     int slot = 0, times = 0;
@@ -399,13 +409,24 @@ query_prompt_kernel(const __grid_constant__ PromptArgs p) {
                     }
                 }
                 if (CAP) {
-                    #pragma unroll
-                    for (int k = 0; k < 64; k += 4) {
-                        if constexpr (CAP == SMALL_CAP) {
-                            capped4(x + k, k2, capl);
+                    if constexpr (CAP == SMALL_CAP) {
+                        #pragma unroll
+                        for (int k = 0; k < 64; k += 4) capped4(x + k, k2, capl);
+                    } else {
+                        // scores below half the cap, as most are below a large one, need no exponential
+                        float top = 0.f;
+                        #pragma unroll
+                        for (int k = 0; k < 64; k += 2) top = max3(fabsf(x[k]), fabsf(x[k + 1]), top);
+                        if (__any_sync(0xffffffffu, top * k2 >= kLog2e)) {
+                            #pragma unroll
+                            for (int k = 0; k < 64; ++k) x[k] = capped_large(x[k], qscale, k2, capl);
                         } else {
                             #pragma unroll
-                            for (int e = k; e < k + 4; ++e) x[e] = capped_large(x[e], qscale, k2, capl);
+                            for (int k = 0; k < 64; k += 2) {
+                                const float2 y = tanh_series2(make_float2(x[k], x[k + 1]), qscale, k2);
+                                x[k] = y.x;
+                                x[k + 1] = y.y;
+                            }
                         }
                     }
                     if constexpr (POOL == KV_FP8_E4M3) {
