@@ -139,3 +139,37 @@ def test_parts_of_different_scales(d, group):
         r[1::3] = (512, 1024)
         check(b, new, group, ranges=r, what="ranges")
         b.cache.close()
+
+
+@pytest.mark.parametrize("new", [[150, 60], [1, 3]])
+@pytest.mark.parametrize("odd", [-0.01, -300.0, 2.0 ** 25, 2.0 ** 100, math.inf, -math.inf, math.nan])
+def test_scales_that_are_none(odd, new):
+    """Blocks whose value scale is negative, enormous or not finite: as the definition has them for rows that see them, and
+    nothing to rows that do not."""
+    lens = [200, 90]
+    b = scaled(128, 2, 16, lens, lambda j, nb: odd if j == nb - 3 else 0.01)
+    p = np.concatenate([np.arange(c - n, c) for n, c in zip(new, lens)])
+    first = np.concatenate([np.full(n, (-(-c // 16) - 2) * 16) for n, c in zip(new, lens)])
+    # every other row begins behind those blocks, where it stands behind them itself; rows before them do not reach them
+    r = np.stack((np.where((np.arange(len(p)) % 2 == 0) & (p >= first), first, 0), p + 1), 1)
+    if math.isfinite(odd):
+        check(b, new, 2, ranges=r, what=odd)
+    else:
+        seen = np.concatenate([(r[:new[0], 0] < first[0]) & (p[:new[0]] >= first[0] - 16),
+                               (r[new[0]:, 0] < first[-1]) & (p[new[0]:] >= first[-1] - 16)])
+        Hq, scale = 4, 1 / math.sqrt(128)
+        q = b.rng.standard_normal((sum(new), Hq, 128)).astype(np.float16)
+        start = np.concatenate(([0], np.cumsum(new))).astype(np.int32)
+        up = lambda x, t=np.int32: torch.from_numpy(np.ascontiguousarray(np.asarray(x, dtype=t))).cuda()       # noqa: E731
+        got = b.cache.query_attention(0, torch.from_numpy(q).cuda(), up(start), up(b.tab), up(lens), max(new), max(lens), scale,
+                                      ranges=up(r)).cpu().numpy().astype(np.float64)
+        assert b.cache.device_error() == 0 and seen.any() and not seen.all()
+        for s, n in enumerate(new):
+            b.vs[b.tab[s][-(-lens[s] // 16) - 3]] = 0.01       # (the values of rows that do not see it)
+            for i in range(n):
+                at = start[s] + i
+                if seen[at]:
+                    assert not np.isfinite(got[at]).any(), (s, i)
+                else:
+                    row_close(b, s, q[at], i, n, got[at], None, 0, r[at], scale, odd)
+    b.cache.close()
