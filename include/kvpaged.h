@@ -582,7 +582,8 @@ KV_API int paged_decode_attention_ex(kv_pool* pool, const kv_decode_args* args);
  * softmax weights enter the V products as float16 (relative 2^-11; down to 2^-21 of a row's
  * largest weight; with FP8 the weights times their blocks' value scales, down to 2^-21 of the
  * largest such product that the row sees).  F32 pools: float32 throughout.  The result is rounded once.
- * The pool's device must be the current device.  Asynchronous.
+ * The pool's device must be the current device.  Asynchronous.  KV_ERR_UNSUPPORTED where the CUDA driver
+ * offers no tensor maps and a KV head has more than 16 rows (other than F32 pools).
  * The masked attention of a prompt that fills the cache, and the steps after it:
  * [KV Cache篇] §3.1 (scores over cache[:, :start_pos+seqlen] plus mask), over the block-table
  * gather of [PagedAttention] §3.2. */

@@ -11,10 +11,11 @@
 //
 // Bound.  The keys and values of a unit, read once.  Measured (us): 32 single tokens after 4095 of 64 / 8 heads, capped,
 // float16 101 (5.3 TB/s, 0.78 of the copy rate); 8 single tokens after 512 .. 2047 of 32 heads, biased 33 (3.4 TB/s); 64
-// sequences of five drafted tokens after 16 .. 16384, 16 / 8 heads, FP8 93 (2.6 TB/s).  What they lose: 15 to 20 us of a
-// call's and its units' beginnings and joints (prefix of the weights 1, first chunks 2, a unit's start 2.4, a joint 2 to
-// 2.5 each, the last one 3 to 4), and with FP8 616 instructions per 16 tokens that two warps per scheduler issue in 39%
-// of the cycles.  Twelve warps, 168 registers each, took the same time.
+// sequences of five drafted tokens after 16 .. 16384, 16 / 8 heads, FP8 90 (2.7 TB/s); the 32 single tokens over FP8 91 and
+// over 4-bit pools 102: fewer bytes, but more instructions.  What they lose: 15 to 20 us of a call's and its units' beginnings
+// and joints (prefix of the weights 1, first chunks 2, a unit's start 2.4, a joint 2 to 2.5 each, the last one 3 to 4), and
+// with FP8 about 600 instructions per 16 tokens that two warps per scheduler issue in 39% of the cycles.  Twelve warps, 168
+// registers each, took the same time.
 //
 // A lane's mma operands come straight from the ring as it stores them, in whatever order of elements and tokens that
 // gives (lane 4 g + t; the queries are loaded, and the result stored, in the same order):

@@ -3,7 +3,8 @@
 // Mathematics.  Rows are (token, query head) of a K/V head.  Over key tiles of 128 a row keeps a base m, the sum l of its
 // weights and O: with t_j the masked scores in log2 units, w_j = 2^(t_j - m + 7) in float16, l += w_j, O += w_j v_j, and
 // where a tile's maximum leaves m behind by more than 2^8 (rare after the first tile) m goes up and l and O by the
-// difference down.  The result is O / l.
+// difference down.  The result is O / l.  (FP8: t_j + log2 of v_j's scale s_j in place of t_j, so w_j is the weight times the
+// scale, O += w_j times the codes, l += w_j / s_j.)
 //
 // Bound.  4 D operations per visible pair on the tensor cores; the special function unit makes an exponential a pair (a
 // capped score an exponential and a quarter of a reciprocal more), 512 cycles of 128 x 128 pairs where the matrix products
@@ -19,10 +20,11 @@
 // float32 and query_join_kernel joins them, in order.
 //
 // Measured (us; D = 128 but for the last): 4 x 2048 tokens of 40 heads 180 (955 TFLOP/s), 2 x 8192 of them 1003 (1370);
-// 2 x 4096 tokens, 64 / 8 heads, capped 674; 512 rows after 16k tokens in FP8, 4 x, 64 / 8 heads 1207 (884); packed
-// documents with a bias, 4-bit, 249; ragged prompts, D = 64, prefixes seen both ways 264 (551).  What it waits for: per key
-// tile 1660 cycles of softmax and 1660 of products and barrier round trips one behind the other; an item's start and end
-// 7000 cycles.  Before: 8 softmax warps with 64-key steps 187, 768, 1540, 313, 267; store warps for the result and 128-key
+// 2 x 4096 tokens, 64 / 8 heads, capped 676 (733 with a cap above 64); 512 rows after 16k tokens in FP8, 4 x, 64 / 8 heads
+// 1247 (856; 1210 with value scales relative to the item's largest, which cost other rows their bits); packed documents with
+// a bias, 4-bit, 248; ragged prompts, D = 64, prefixes seen both ways 265 (550).  What it waits for: per key tile 1660 cycles
+// of softmax and 1660 of products and barrier round trips one behind the other; an item's start and end 7000 cycles.
+// Before: 8 softmax warps with 64-key steps 187, 768, 1540, 313, 267; store warps for the result and 128-key
 // steps 211, 797, 1690, 284, 260; both row tiles' products issued as they came (the softmaxes ran at the same time, then
 // the products) 190, 806, 1664, 236, 266; scores taken 64 columns at a time (more free registers, the base's loop spilt)
 // 264, 1160, 2127, 285, 275.
